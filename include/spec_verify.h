@@ -40,9 +40,9 @@
  *   - All arithmetic on the device is fp32 (bf16 inputs are widened exactly);
  *     cumulative sums for the inverse CDF are exact int64 sums of the fp32
  *     weights of 16-byte groups of logits, in units of 2^-52.
- *   - Workspace: every entry point except spec_verify_linear_static and
- *     spec_tree_mask needs a caller-owned device workspace of
- *     spec_workspace_bytes_*() bytes, 16-byte aligned and zero-filled before
+ *   - Workspace: spec_verify_linear, spec_sample_bonus, spec_sample_rows,
+ *     spec_verify_tree and spec_verify_tree_sample need a caller-owned device
+ *     workspace of spec_workspace_bytes_*() bytes (the others need none), 16-byte aligned and zero-filled before
  *     its first use.  Every call leaves it zero-filled again -- also a call
  *     that reports SPEC_DEV_TIMEOUT: its last CTA then clears every byte the
  *     call used -- so one zeroing suffices for any number of calls, but one
@@ -97,6 +97,12 @@ typedef enum spec_dtype {
 #define SPEC_DEV_BAD_TREE     16u  /* parents[] not topological (0 <= parents[c] < c): edge ignored */
 #define SPEC_DEV_BAD_LENGTH   32u  /* spec_sample_bonus: accept_len[b] outside [0, K] (token -1);
                                       spec_mtp_plug: num_emitted[b] outside [0, K+1] */
+#define SPEC_DEV_BAD_PARAM    64u  /* spec_sample_filtered: a row's parameter out of range (token -1) */
+
+/* Limits of the operators on rows of logits (spec_sample_filtered and
+ * spec_top_logits keep a row in shared memory). */
+#define SPEC_MAX_ROW_BYTES (1 << 20) /* V * element size: 262144 fp32 or 524288 bf16 logits */
+#define SPEC_MAX_TOP       1024      /* K of spec_top_logits */
 
 /* Bytes of workspace spec_verify_linear needs for B sequences of K draft
  * tokens over a vocabulary of V logits of `dtype` (0 for invalid sizes). */
@@ -305,6 +311,58 @@ SPEC_API spec_status spec_build_sparse_tree(const double *accuracy, int K, int S
 SPEC_API spec_status spec_mtp_plug(const int32_t *in_tokens, int B, int K, const int32_t *out_tokens,
                                    const int32_t *num_emitted, int32_t pad, int32_t *next_tokens,
                                    int32_t *seq_lens, uint32_t *dev_status, void *stream);
+
+/*
+ * One token per row under the usual serving filters, each row with parameters
+ * of its own (a batch mixes requests): spec_sample_rows with temperature,
+ * top-k, top-p and min-p.  With w_v = exp((l_v - max l) / T) and the tokens in
+ * the order of falling logits (the lower index first among equal ones), the
+ * kept tokens are, one filter after the other:
+ *   top-k   the first k;
+ *   top-p   of those, the shortest prefix whose weight is at least p times
+ *           theirs (at least one token);
+ *   min-p   of those, the ones with w_v >= min_p.
+ * Each leaves a prefix of the order.  The token is the first v, in index order,
+ * whose running sum of kept weights exceeds u * (their sum).
+ *
+ *   logits      [B, V]  fp32 or bf16; -inf masks a token (it is never kept).
+ *   temperature [B] fp32: 0 (the lowest-index argmax; the row's other
+ *               parameters are not used) or in [1e-6, 1e6].
+ *   top_k       [B] int32 or NULL; <= 0 or >= V: no limit.
+ *   top_p       [B] fp32 or NULL, in [0, 1]; 1: no limit.
+ *   min_p       [B] fp32 or NULL, in [0, 1]; 0: no limit.
+ *   u           [B] fp32 in [0, 1).
+ *   tokens      [B] int32 (output).
+ *   dev_status  SPEC_DEV_BAD_PARAM: a row's parameter is out of range or NaN;
+ *               SPEC_DEV_NONFINITE: a row holds NaN or +inf, or every token of
+ *               it is masked.  Such a row's token is -1; the others are drawn.
+ * Weights and their sums are whole numbers in units of at least 2^-52, right to
+ * about 2^-43 of the largest weight, so the token is the definition's unless u
+ * lies that near a border, and a call gives the same token every time.
+ * Rows of at most SPEC_MAX_ROW_BYTES bytes (SPEC_ERR_UNSUPPORTED above).
+ * No workspace; one launch.
+ */
+SPEC_API spec_status spec_sample_filtered(const void *logits, spec_dtype dtype, int B, int V, const float *temperature,
+                                          const int32_t *top_k, const float *top_p, const float *min_p,
+                                          const float *u, int32_t *tokens, uint32_t *dev_status, void *stream);
+
+/*
+ * The K largest logits of each row, in falling order (the lower index first
+ * among equal ones), and optionally the row's log-normaliser: the candidate
+ * tokens of a draft head (spec_build_sparse_tree's rank i is entry i - 1), or
+ * the target's distribution as spec_distill takes it.
+ *   logits [B, V] fp32 or bf16; -inf masks a token.
+ *   1 <= K <= SPEC_MAX_TOP; K may exceed V.
+ *   temperature in [1e-6, 1e6]: the log-normaliser's, not the values'.
+ *   values [B, K] fp32, ids [B, K] int32: entries past the row's last unmasked
+ *          token are (-inf, -1).
+ *   lse    [B] fp32 or NULL: log sum_v exp(l_v / T); -inf for a masked row.
+ *   dev_status  SPEC_DEV_NONFINITE: a row holds NaN or +inf; its values and lse
+ *          are NaN and its ids -1.
+ * Rows of at most SPEC_MAX_ROW_BYTES bytes.  No workspace; one launch.
+ */
+SPEC_API spec_status spec_top_logits(const void *logits, spec_dtype dtype, int B, int V, int K, float temperature,
+                                     float *values, int32_t *ids, float *lse, uint32_t *dev_status, void *stream);
 
 /*
  * spec_verify_linear with the library's own workspace.  The pages describe no

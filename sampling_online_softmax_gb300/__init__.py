@@ -51,6 +51,10 @@ DEV_TIMEOUT = 4
 DEV_ZERO_RESIDUAL = 8
 DEV_BAD_TREE = 16
 DEV_BAD_LENGTH = 32
+DEV_BAD_PARAM = 64
+
+MAX_ROW_BYTES = 1 << 20  # SPEC_MAX_ROW_BYTES
+MAX_TOP = 1024           # SPEC_MAX_TOP
 
 
 class SpecError(RuntimeError):
@@ -102,6 +106,10 @@ def load_library():
         lib.spec_verify_tree.restype = i32
         lib.spec_verify_tree_sample.argtypes = [P, i32, i32, i32, i32, P, P, P, f32, i32, P, P, P, P, P, u64, P]
         lib.spec_verify_tree_sample.restype = i32
+        lib.spec_sample_filtered.argtypes = [P, i32, i32, i32, P, P, P, P, P, P, P, P]
+        lib.spec_sample_filtered.restype = i32
+        lib.spec_top_logits.argtypes = [P, i32, i32, i32, i32, f32, P, P, P, P, P]
+        lib.spec_top_logits.restype = i32
         lib.spec_status_string.argtypes = [i32]
         lib.spec_status_string.restype = ctypes.c_char_p
         lib.spec_last_error.argtypes = []
@@ -459,6 +467,92 @@ def spec_sample_rows(logits, u, temperature, *, status=None, out=None, workspace
         st = lib.spec_sample_rows(_ptr(logits), _dtype_code(logits), B, V, _ptr(u), float(temperature),
                                   _ptr(out["tokens"]), _ptr(status), _ptr(ws), ws.numel(), h)
     _check(st)
+    return out
+
+
+def _allocate(shapes, dev, s, stream):
+    """New outputs, from the memory of the stream that the kernel runs on."""
+    if stream is None:
+        return {n: torch.empty(shape, dtype=dtype, device=dev) for n, (shape, dtype) in shapes.items()}
+    with torch.cuda.stream(s):
+        return {n: torch.empty(shape, dtype=dtype, device=dev) for n, (shape, dtype) in shapes.items()}
+
+
+def _record(tensors, dev, s, stream):
+    """Keep the memory of tensors that another stream owns until `stream` has used it."""
+    if stream is not None and s != torch.cuda.current_stream(dev):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+
+def _per_row(t, name, dtype, B, dev, required=False):
+    if t is None:
+        if required:
+            raise ValueError("%s is required" % name)
+        return
+    _cuda(t, name, dtype, dev)
+    if tuple(t.shape) != (B,):
+        raise ValueError("%s must be [%d], got %s" % (name, B, tuple(t.shape)))
+
+
+def spec_sample_filtered(logits, u, temperature, *, top_k=None, top_p=None, min_p=None, status=None, out=None,
+                         stream=None):
+    """One token per row of logits [B, V] under temperature [B] (float32; 0: the argmax), top_k [B]
+    (int32; <= 0: no limit), top_p [B] and min_p [B] (float32), at u [B] (float32, in [0, 1)); a
+    filter left None does not limit.  Returns dict(tokens [B], status)."""
+    lib = load_library()
+    _cuda(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [B, V]")
+    B, V = logits.shape
+    dev = logits.device
+    code = _dtype_code(logits)
+    _per_row(u, "u", torch.float32, B, dev, True)
+    _per_row(temperature, "temperature", torch.float32, B, dev, True)
+    _per_row(top_k, "top_k", torch.int32, B, dev)
+    _per_row(top_p, "top_p", torch.float32, B, dev)
+    _per_row(min_p, "min_p", torch.float32, B, dev)
+    h, s = _stream_handle(dev, stream)
+    shapes = {"tokens": ((B,), torch.int32)}
+    out = _outputs(_allocate(shapes, dev, s, stream) if out is None else out, shapes, dev)
+    status = _status(status, dev, s)
+    out["status"] = status
+    with torch.cuda.device(dev):
+        st = lib.spec_sample_filtered(_ptr(logits), code, B, V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                                      _ptr(min_p), _ptr(u), _ptr(out["tokens"]), _ptr(status), h)
+    _check(st)
+    _record((logits, u, temperature, top_k, top_p, min_p, out["tokens"], status), dev, s, stream)
+    return out
+
+
+def spec_top_logits(logits, k, *, temperature=1.0, lse=False, status=None, out=None, stream=None):
+    """The k largest logits of each row of logits [B, V], falling, the lower index first among equal
+    ones: returns dict(values [B, k] float32, ids [B, k] int32, status), and with lse=True also
+    lse [B] float32, the log-normaliser log sum exp(l / temperature).  Entries past a row's last
+    unmasked token are (-inf, -1)."""
+    lib = load_library()
+    _cuda(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be [B, V]")
+    B, V = logits.shape
+    dev = logits.device
+    code = _dtype_code(logits)
+    k = int(k)
+    if k < 1:
+        raise ValueError("k must be >= 1")
+    h, s = _stream_handle(dev, stream)
+    shapes = {"values": ((B, k), torch.float32), "ids": ((B, k), torch.int32)}
+    if lse:
+        shapes["lse"] = ((B,), torch.float32)
+    out = _outputs(_allocate(shapes, dev, s, stream) if out is None else out, shapes, dev)
+    status = _status(status, dev, s)
+    out["status"] = status
+    with torch.cuda.device(dev):
+        st = lib.spec_top_logits(_ptr(logits), code, B, V, k, float(temperature), _ptr(out["values"]),
+                                 _ptr(out["ids"]), _ptr(out["lse"]) if lse else None, _ptr(status), h)
+    _check(st)
+    _record((logits, out["values"], out["ids"], out["lse"] if lse else None, status), dev, s, stream)
     return out
 
 

@@ -2,7 +2,7 @@
 
 The kernel's modes live in separate translation units (csrc/kern_*.cu), which
 are compiled in parallel and linked with the host side (csrc/spec_verify.cu,
-csrc/tree_build.cpp).
+csrc/tree_build.cpp); the operators on rows of logits live in csrc/vocab/.
 """
 from __future__ import annotations
 
@@ -17,9 +17,15 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libspecverify.so")
-SOURCES = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
-DEPENDS = SOURCES + sorted(glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))) + \
-    [os.path.join(INCLUDE, "spec_verify.h")]
+VOCAB = os.path.join(CSRC, "vocab")
+
+
+def _files(pattern):
+    return sorted(glob.glob(os.path.join(CSRC, pattern)) + glob.glob(os.path.join(VOCAB, pattern)))
+
+
+SOURCES = _files("*.cu") + _files("*.cpp")
+DEPENDS = SOURCES + _files("*.cuh") + _files("*.h") + [os.path.join(INCLUDE, "spec_verify.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMPILE_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-Xptxas", "-v"]

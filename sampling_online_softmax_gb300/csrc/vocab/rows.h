@@ -1,0 +1,47 @@
+// rows.h -- what the host and the kernels on rows of logits share: launch
+// constants and the parameter block.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../host.h"
+
+namespace spec {
+namespace vocab {
+
+constexpr int kThreads = 512;
+constexpr int kMaxCluster = 8;    // CTAs per row (the portable limit)
+constexpr int kMaxList = 2048;    // entries of a cluster's list
+
+constexpr float kMinTemperature = 1e-6f, kMaxTemperature = 1e6f;
+
+struct RowArgs {
+    const unsigned char *base;  // [B, V] logits
+    const unsigned char *end;   // one past their last byte
+    int B, V;
+    int cluster;                // CTAs per row
+    int part;                   // 16-byte vectors of a row per CTA
+    int U;                      // weights in units of 2^-U
+    uint32_t *status;
+    // filtered sampling, one entry a row
+    const float *temperature, *u;
+    const int32_t *top_k;       // null: no limit
+    const float *top_p, *min_p;
+    int32_t *tokens;
+    // the largest logits
+    int K;
+    float temp;
+    float *values;              // [B, K]
+    int32_t *ids;
+    float *lse;                 // [B] or null
+};
+
+enum RowOp : int { kSampleRows = 0, kTopRows = 1 };
+
+template <int EB, int OP>
+spec_status launch_rows(const RowArgs &a, cudaStream_t stream);
+
+}  // namespace vocab
+}  // namespace spec

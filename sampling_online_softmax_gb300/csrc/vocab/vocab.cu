@@ -1,0 +1,89 @@
+// vocab.cu -- host side of the operators on rows of logits (spec_sample_filtered,
+// spec_top_logits): argument checks and dispatch.
+#include <climits>
+#include <cmath>
+
+#include "rows.h"
+
+namespace spec {
+
+extern thread_local char g_last_error[512];
+
+namespace vocab {
+namespace {
+
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+bool valid_dtype(spec_dtype d) { return d == SPEC_F32 || d == SPEC_BF16; }
+int elt_bytes(spec_dtype d) { return d == SPEC_F32 ? 4 : 2; }
+
+// The checks every operator on [B, V] logits shares, and their fields of the parameter block.
+spec_status rows_args(RowArgs *a, const void *logits, spec_dtype dtype, int B, int V, uint32_t *dev_status) {
+    const int eb = elt_bytes(dtype);
+    if (!logits || !aligned(logits, eb)) return fail(SPEC_ERR_INVALID_ARG, "logits null or misaligned");
+    if (!dev_status || !aligned(dev_status, 4)) return fail(SPEC_ERR_INVALID_ARG, "dev_status null or misaligned");
+    if (V > SPEC_MAX_ROW_BYTES / eb) return fail(SPEC_ERR_UNSUPPORTED, "V = %d: rows of at most %d bytes", V, SPEC_MAX_ROW_BYTES);
+    if (B > INT_MAX / kMaxCluster) return fail(SPEC_ERR_UNSUPPORTED, "B too large");
+    a->base = static_cast<const unsigned char *>(logits);
+    a->end = a->base + static_cast<size_t>(B) * static_cast<size_t>(V) * eb;
+    a->B = B;
+    a->V = V;
+    a->status = dev_status;
+    int bits = 1;
+    while ((1ll << bits) < V) ++bits;
+    a->U = 62 - bits < 52 ? 62 - bits : 52;
+    return SPEC_OK;
+}
+
+}  // namespace
+}  // namespace vocab
+}  // namespace spec
+
+using namespace spec;
+using namespace spec::vocab;
+
+extern "C" spec_status spec_sample_filtered(const void *logits, spec_dtype dtype, int B, int V, const float *temperature,
+                                            const int32_t *top_k, const float *top_p, const float *min_p, const float *u,
+                                            int32_t *tokens, uint32_t *dev_status, void *stream) {
+    g_last_error[0] = '\0';
+    if (!valid_dtype(dtype)) return fail(SPEC_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (B < 0 || V < 1) return fail(SPEC_ERR_INVALID_ARG, "need B >= 0, V >= 1");
+    if (B == 0) return SPEC_OK;
+    RowArgs a = {};
+    spec_status st = rows_args(&a, logits, dtype, B, V, dev_status);
+    if (st != SPEC_OK) return st;
+    if (!temperature || !u || !tokens) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
+    if (!aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(u, 4) ||
+        !aligned(tokens, 4))
+        return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    a.temperature = temperature;
+    a.top_k = top_k;
+    a.top_p = top_p;
+    a.min_p = min_p;
+    a.u = u;
+    a.tokens = tokens;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == SPEC_F32 ? launch_rows<4, kSampleRows>(a, s) : launch_rows<2, kSampleRows>(a, s);
+}
+
+extern "C" spec_status spec_top_logits(const void *logits, spec_dtype dtype, int B, int V, int K, float temperature,
+                                       float *values, int32_t *ids, float *lse, uint32_t *dev_status, void *stream) {
+    g_last_error[0] = '\0';
+    if (!valid_dtype(dtype)) return fail(SPEC_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (B < 0 || V < 1 || K < 1) return fail(SPEC_ERR_INVALID_ARG, "need B >= 0, V >= 1, K >= 1");
+    if (K > SPEC_MAX_TOP) return fail(SPEC_ERR_UNSUPPORTED, "K = %d > %d", K, SPEC_MAX_TOP);
+    if (!(temperature >= kMinTemperature && temperature <= kMaxTemperature))
+        return fail(SPEC_ERR_INVALID_ARG, "temperature must be in [1e-6, 1e6]");
+    if (B == 0) return SPEC_OK;
+    RowArgs a = {};
+    spec_status st = rows_args(&a, logits, dtype, B, V, dev_status);
+    if (st != SPEC_OK) return st;
+    if (!values || !ids) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
+    if (!aligned(values, 4) || !aligned(ids, 4) || !aligned(lse, 4)) return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    a.K = K;
+    a.temp = temperature;
+    a.values = values;
+    a.ids = ids;
+    a.lse = lse;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == SPEC_F32 ? launch_rows<4, kTopRows>(a, s) : launch_rows<2, kTopRows>(a, s);
+}

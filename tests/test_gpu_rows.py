@@ -1,0 +1,234 @@
+"""Filtered sampling and the largest logits on the GPU, against 64 bits.
+
+Tokens, ids and values must be equal: the inputs' draws lie further than
+2^-36 from every border of the distribution (asserted; the kernel's weights
+are right to about 2^-43), so no tolerance is needed.
+"""
+import numpy as np
+import pytest
+import torch
+
+import rows_reference as ref
+import sampling_online_softmax_gb300 as sv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+NEAR = 2.0 ** -36
+
+
+def host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def rows(B, V, dtype, sigma, seed, masked=0.0, offset=0):
+    """Logits whose first element lies `offset` elements into an allocation."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((B, V), generator=g) * sigma
+    if masked:
+        x[torch.rand((B, V), generator=g) < masked] = float("-inf")
+        x[:, V // 2] = 0.5
+    flat = torch.zeros(B * V + offset, dtype=dtype, device=DEV)
+    flat[offset:] = x.to(dtype).reshape(-1).to(DEV)
+    return flat[offset:].view(B, V)
+
+
+def params(B, seed, T=(1.0,), k=(0,), p=(1.0,), mp=(0.0,)):
+    r = np.random.RandomState(seed)
+    pick = lambda v, dt: torch.tensor([v[r.randint(len(v))] for _ in range(B)], dtype=dt, device=DEV)  # noqa: E731
+    return dict(temperature=pick(T, torch.float32), top_k=pick(k, torch.int32), top_p=pick(p, torch.float32),
+                min_p=pick(mp, torch.float32))
+
+
+def check_sample(x, u, q, status=0, **kw):
+    r = sv.spec_sample_filtered(x, u, q["temperature"], top_k=q.get("top_k"), top_p=q.get("top_p"), min_p=q.get("min_p"), **kw)
+    torch.cuda.synchronize()
+    got = r["tokens"].cpu().numpy()
+    assert int(r["status"][0]) == status
+    at = lambda n, b, none: none if q.get(n) is None else float(q[n][b])  # noqa: E731
+    for b in range(x.shape[0]):
+        tok, far = ref.sample_filtered(host(x[b]), float(u[b]), at("temperature", b, 1.0), int(at("top_k", b, 0)), at("top_p", b, 1.0),
+                                       at("min_p", b, 0.0))
+        assert far > NEAR, "the input lies on a border: row %d" % b
+        assert got[b] == tok, (b, got[b], tok, {n: at(n, b, None) for n in q})
+    return got
+
+
+MIXED = dict(T=(0.0, 0.3, 0.7, 1.0, 2.0), k=(0, 1, 2, 50, 300, 5000), p=(1.0, 0.999, 0.9, 0.5, 0.0), mp=(0.0, 0.0, 0.02, 0.5, 1.0))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 31, 257, 1000, 5003, 32000, 50257, 131072])
+def test_mixed_filters(V, dtype):
+    B = 24 if V < 60000 else 8
+    x = rows(B, V, dtype, 3.0, V, masked=0.3 if V % 2 else 0.0, offset=V % 5)
+    u = torch.rand(B, generator=torch.Generator().manual_seed(V + 1)).to(DEV)
+    check_sample(x, u, params(B, V, **MIXED))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("name,q", [
+    ("none", {}), ("k", dict(k=(40,))), ("k_large", dict(k=(3000,))), ("p", dict(p=(0.9,))), ("p_flat", dict(T=(3.0,), p=(0.97,))),
+    ("mp", dict(mp=(0.05,))), ("mp_flat", dict(T=(3.0,), mp=(0.01,))), ("all", dict(T=(0.8,), k=(64,), p=(0.9,), mp=(0.02,))),
+    ("k_p_large", dict(T=(2.0,), k=(4000,), p=(0.8,))), ("cold", dict(T=(1e-6, 1e-3, 0.01))), ("hot", dict(T=(50.0, 1e6), p=(0.5, 1.0)))])
+def test_each_filter(name, q, dtype):
+    B, V = 20, 20011
+    x = rows(B, V, dtype, 2.5, 77)
+    u = torch.rand(B, generator=torch.Generator().manual_seed(5)).to(DEV)
+    check_sample(x, u, params(B, 3, **q))
+
+
+def test_no_filter_arrays():
+    x = rows(9, 4001, torch.float32, 3.0, 2)
+    u = torch.rand(9, generator=torch.Generator().manual_seed(6)).to(DEV)
+    check_sample(x, u, dict(temperature=torch.full((9,), 0.9, device=DEV)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_ties(dtype):
+    """Equal logits in their thousands: the cuts fall inside a tie, which the lower indices win."""
+    V = 30000
+    x = torch.zeros((6, V), dtype=dtype, device=DEV)
+    x[1] = -3.0e38                               # all at (nearly) the type's lowest value
+    x[2, ::3] = 1.0
+    x[3, 100:] = -0.0                            # -0 and +0 are equal
+    x[4, V - 1] = 5.0
+    x[5, 5000:6000] = 2.0
+    u = torch.tensor([0.1, 0.3, 0.77, 0.9, 0.4, 0.61], device=DEV)
+    for k, p, mp in ((7, 1.0, 0.0), (0, 0.37, 0.0), (12345, 1.0, 0.0), (0, 1.0, 1.0), (9000, 0.123, 0.0), (0, 1.0, 0.0), (0, 0.0, 0.0)):
+        check_sample(x, u, params(6, 0, T=(1.0,), k=(k,), p=(p,), mp=(mp,)))
+    check_sample(x, u, params(6, 0, T=(0.0,)))
+
+
+def test_extreme_uniforms_and_magnitudes():
+    V = 9000
+    x = torch.randn((8, V), generator=torch.Generator().manual_seed(9)).to(DEV) * 2
+    x[2] *= 1e37
+    x[3, 17] = 3.4e38
+    x[3, 18] = -3.4e38
+    x[4] *= 1e-40                                # subnormal
+    x[5] = float("-inf")
+    x[5, 8999] = -7.0
+    x[6, :4000] = -200.0                         # weights below a double's smallest at T = 0.1
+    u = torch.tensor([0.0, 1 - 2.0 ** -24, 0.5, 0.5, 0.37, 0.99, 0.0, 2.0 ** -60], device=DEV)
+    T = torch.tensor([1.0, 1.0, 1.0, 1.0, 1.0, 1.0, 0.1, 1.0], device=DEV)
+    r = sv.spec_sample_filtered(x, u, T)
+    torch.cuda.synchronize()
+    for b in range(8):
+        assert int(r["tokens"][b]) == ref.sample_filtered(host(x[b]), float(u[b]), float(T[b]))[0], b
+
+
+def test_bad_rows_leave_the_others():
+    V = 3001
+    x = rows(10, V, torch.float32, 2.0, 4)
+    x[1, 5] = float("nan")
+    x[2, 3000] = float("inf")
+    x[3] = float("-inf")
+    u = torch.full((10,), 0.43, device=DEV)
+    q = params(10, 0, T=(0.8,), k=(30,), p=(0.9,), mp=(0.0,))
+    r = sv.spec_sample_filtered(x, u, q["temperature"], top_k=q["top_k"], top_p=q["top_p"], min_p=q["min_p"])
+    assert int(r["status"][0]) == sv.DEV_NONFINITE
+    q["temperature"][4], q["temperature"][5], q["top_p"][6], q["min_p"][7] = -1.0, float("nan"), 1.5, float("nan")
+    u[8] = 1.0
+    r = sv.spec_sample_filtered(x, u, q["temperature"], top_k=q["top_k"], top_p=q["top_p"], min_p=q["min_p"])
+    got = r["tokens"].cpu().numpy()
+    assert int(r["status"][0]) == sv.DEV_NONFINITE | sv.DEV_BAD_PARAM
+    assert (got[1:9] == -1).all()
+    for b in (0, 9):
+        assert got[b] == ref.sample_filtered(host(x[b]), 0.43, 0.8, 30, 0.9)[0]
+
+
+def test_sampling_is_repeatable_and_captures():
+    B, V = 40, 12289
+    x = rows(B, V, torch.bfloat16, 2.0, 11)
+    u = torch.rand(B, generator=torch.Generator().manual_seed(8)).to(DEV)
+    q = params(B, 5, **MIXED)
+    want = check_sample(x, u, q)
+    out, status = dict(tokens=torch.zeros(B, dtype=torch.int32, device=DEV)), torch.zeros(1, dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            sv.spec_sample_filtered(x, u, out=out, status=status, **q)
+    for _ in range(3):
+        out["tokens"].zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert (out["tokens"].cpu().numpy() == want).all() and int(status[0]) == 0
+    other = sv.spec_sample_filtered(x, u, stream=torch.cuda.Stream(), **q)
+    torch.cuda.synchronize()
+    assert (other["tokens"].cpu().numpy() == want).all()
+
+
+def check_top(x, k, T=1.0, lse=True):
+    r = sv.spec_top_logits(x, k, temperature=T, lse=lse)
+    torch.cuda.synchronize()
+    assert int(r["status"][0]) == 0
+    for b in range(x.shape[0]):
+        v, i, z = ref.top_logits(host(x[b]), k, T)
+        assert np.array_equal(host(r["values"][b]), v), b
+        assert np.array_equal(r["ids"][b].cpu().numpy(), i), b
+        if lse:
+            # fp32: the last rounding and log's (2^-24 |lse| + 2 * 2^-24 |log S|), and S's relative
+            # error: each weight 2^-21 (ex2's 2^-22, its argument's rounding up to |x| 2^-24 where
+            # weights below 2^-8 count little) and sums in trees, together below 2^-20
+            tol = 2.0 ** -20 + 2.0 ** -22 * abs(z) if np.isfinite(z) else 0.0
+            got = float(r["lse"][b])
+            assert got == z or abs(got - z) <= tol, (b, got, z)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1, 2, 7, 9, 64, 1000, 5003, 32000, 50257, 131072])
+def test_top_logits(V, dtype):
+    x = rows(7, V, dtype, 3.0, V + 9, masked=0.4 if V % 2 else 0.0, offset=V % 3)
+    for k in (1, 8, 100, 777, 1024):
+        check_top(x, k, 0.7 if k == 8 else 1.0, lse=k != 100)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_top_logits_ties(dtype):
+    V = 40001
+    x = torch.zeros((5, V), dtype=dtype, device=DEV)
+    x[1] = float("-inf")
+    x[1, 39990:] = 1.5
+    x[2, ::2] = 3.0
+    x[3] = torch.arange(V, device=DEV).to(dtype) / 4096   # rising: the largest are neighbours
+    x[4] = float("-inf")
+    for k in (1, 5, 11, 500, 1024):
+        check_top(x, k)
+
+
+def test_top_logits_nonfinite_rows():
+    x = rows(4, 6000, torch.float32, 2.0, 4)
+    x[1, 5] = float("nan")
+    x[2, 77] = float("inf")
+    r = sv.spec_top_logits(x, 10, lse=True)
+    assert int(r["status"][0]) == sv.DEV_NONFINITE
+    for b in (1, 2):
+        assert torch.isnan(r["values"][b]).all() and (r["ids"][b] == -1).all() and torch.isnan(r["lse"][b])
+    for b in (0, 3):
+        v, i, _ = ref.top_logits(host(x[b]), 10)
+        assert np.array_equal(host(r["values"][b]), v) and np.array_equal(r["ids"][b].cpu().numpy(), i)
+
+
+def test_the_longest_row_and_the_next():
+    for dtype, V in ((torch.float32, 262144), (torch.bfloat16, 524288)):
+        x = rows(2, V, dtype, 3.0, 5)
+        check_top(x, 50)
+        u = torch.tensor([0.3, 0.8], device=DEV)
+        check_sample(x, u, params(2, 0, T=(0.9,), p=(0.95,)))
+        with pytest.raises(sv.SpecError) as e:
+            sv.spec_top_logits(torch.zeros((1, V + 1), dtype=dtype, device=DEV), 4)
+        assert e.value.status == sv.SPEC_ERR_UNSUPPORTED
+
+
+def test_offsets_past_32_bits():
+    B, V = 17000, 131072                           # 4.5 GB of bf16
+    x = torch.zeros((B, V), dtype=torch.bfloat16, device=DEV)
+    x[-1] = rows(1, V, torch.bfloat16, 3.0, 8)[0]
+    x[:, 7] += 1
+    r = sv.spec_top_logits(x, 3)
+    v, i, _ = ref.top_logits(host(x[-1]), 3)
+    assert np.array_equal(host(r["values"][-1]), v) and np.array_equal(r["ids"][-1].cpu().numpy(), i)
+    assert (r["ids"][:-1].cpu() == torch.tensor([7, 0, 1], dtype=torch.int32)).all()
