@@ -90,7 +90,8 @@ typedef enum spec_dtype {
 } spec_dtype;
 
 /* Bits OR-ed into *dev_status by the kernels. */
-#define SPEC_DEV_BAD_TOKEN     1u  /* a draft token outside [0, V): treated as rejected */
+#define SPEC_DEV_BAD_TOKEN     1u  /* a draft token outside [0, V): treated as rejected;
+                                      spec_distill: a teacher's token outside [-1, V): left out */
 #define SPEC_DEV_NONFINITE     2u  /* a row whose max or exp-sum is not finite; outputs unspecified */
 #define SPEC_DEV_TIMEOUT       4u  /* a bounded wait (a copy, or a value another warp publishes) gave up; outputs unspecified, workspace cleared */
 #define SPEC_DEV_ZERO_RESIDUAL 8u  /* residual weight W == 0 at a rejection: drew from p_j instead */
@@ -99,10 +100,10 @@ typedef enum spec_dtype {
                                       spec_mtp_plug: num_emitted[b] outside [0, K+1] */
 #define SPEC_DEV_BAD_PARAM    64u  /* spec_sample_filtered: a row's parameter out of range (token -1) */
 
-/* Limits of the operators on rows of logits (spec_sample_filtered and
- * spec_top_logits keep a row in shared memory). */
+/* Limits of the operators on rows of logits (spec_sample_filtered,
+ * spec_top_logits, spec_distill: a row is kept in shared memory). */
 #define SPEC_MAX_ROW_BYTES (1 << 20) /* V * element size: 262144 fp32 or 524288 bf16 logits */
-#define SPEC_MAX_TOP       1024      /* K of spec_top_logits */
+#define SPEC_MAX_TOP       1024      /* K of spec_top_logits and spec_distill */
 
 /* Bytes of workspace spec_verify_linear needs for B sequences of K draft
  * tokens over a vocabulary of V logits of `dtype` (0 for invalid sizes). */
@@ -363,6 +364,57 @@ SPEC_API spec_status spec_sample_filtered(const void *logits, spec_dtype dtype, 
  */
 SPEC_API spec_status spec_top_logits(const void *logits, spec_dtype dtype, int B, int V, int K, float temperature,
                                      float *values, int32_t *ids, float *lse, uint32_t *dev_status, void *stream);
+
+/*
+ * Distillation from a teacher's largest logits: how far the student's (the
+ * draft's) distribution is from the teacher's (the target's), whose agreement
+ * decides how many draft tokens a verify accepts.  Row by row, with
+ * q = softmax(s / T) and the teacher's K entries (t_k, id_k) as
+ * spec_top_logits gives them:
+ *   p_k  = exp(t_k / T - lse)           with top_lse (taken at the same T), or
+ *          softmax of t / T over the entries without it;  P = sum_k p_k
+ *   loss = w * sum_k p_k (log p_k - log q[id_k])
+ *   d loss / d s_v = (w / T) * (P q_v - sum of p_k over the entries with id_k = v)
+ * The teacher is a constant: it gets no gradient.
+ *
+ *   student_logits [N, V] fp32 or bf16; -inf masks a token (a masked token that
+ *                  the teacher gives weight makes the loss +inf).
+ *   top_ids    [N, K] int32, 1 <= K <= SPEC_MAX_TOP, in any order: -1 is an empty
+ *              slot (its logit is not used); a token named twice counts twice.
+ *   top_logits [N, K] fp32; -inf has no weight.
+ *   top_lse    [N] fp32 or NULL.
+ *   temperature T in [1e-6, 1e6].
+ *   row_weight [N] fp32 or NULL (1): a row of weight 0 is ignored: its logits and
+ *              its teacher are not read, its loss, statistics and gradient are 0.
+ * Outputs:
+ *   loss  [N] fp32;  stats [N, 2] fp32: the row's largest logit and
+ *         sum_v exp((s_v - largest) / T), for spec_distill_backward.
+ *   grad  [N, V] of the logits' type, or NULL: the gradient of the sum of the
+ *         losses, overwritten; it may be student_logits itself (in place).
+ *         With it the logits are read once for both.
+ *   dev_status  SPEC_DEV_BAD_TOKEN; SPEC_DEV_NONFINITE: a row of weight other
+ *         than 0 with NaN or +inf among its logits or its teacher's, or nothing
+ *         but -inf: its loss, statistics and gradient are NaN.
+ * A row without a teacher's token (P = 0) has loss and gradient 0.
+ * Rows of at most SPEC_MAX_ROW_BYTES bytes.  No workspace; one launch; the same
+ * result every time.
+ */
+SPEC_API spec_status spec_distill(const void *student_logits, spec_dtype dtype, int N, int V, const int32_t *top_ids,
+                                  const float *top_logits, int K, const float *top_lse, float temperature,
+                                  const float *row_weight, float *loss, float *stats, void *grad, uint32_t *dev_status,
+                                  void *stream);
+
+/*
+ * The gradient alone, for losses whose upstream gradients are known only later:
+ * grad[n, v] = grad_loss[n] * d loss[n] / d s_v, from spec_distill's stats of the
+ * same logits, teacher, temperature and weights.  Arguments as there; stats and
+ * grad_loss [N] fp32 are inputs.  A row with row_weight * grad_loss = 0 is not
+ * read and its gradient is 0.  grad may be student_logits itself.
+ */
+SPEC_API spec_status spec_distill_backward(const void *student_logits, spec_dtype dtype, int N, int V, const int32_t *top_ids,
+                                           const float *top_logits, int K, const float *top_lse, float temperature,
+                                           const float *row_weight, const float *stats, const float *grad_loss, void *grad,
+                                           uint32_t *dev_status, void *stream);
 
 /*
  * spec_verify_linear with the library's own workspace.  The pages describe no

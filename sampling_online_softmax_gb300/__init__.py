@@ -110,6 +110,10 @@ def load_library():
         lib.spec_sample_filtered.restype = i32
         lib.spec_top_logits.argtypes = [P, i32, i32, i32, i32, f32, P, P, P, P, P]
         lib.spec_top_logits.restype = i32
+        lib.spec_distill.argtypes = [P, i32, i32, i32, P, P, i32, P, f32, P, P, P, P, P, P]
+        lib.spec_distill.restype = i32
+        lib.spec_distill_backward.argtypes = [P, i32, i32, i32, P, P, i32, P, f32, P, P, P, P, P, P]
+        lib.spec_distill_backward.restype = i32
         lib.spec_status_string.argtypes = [i32]
         lib.spec_status_string.restype = ctypes.c_char_p
         lib.spec_last_error.argtypes = []
@@ -554,6 +558,82 @@ def spec_top_logits(logits, k, *, temperature=1.0, lse=False, status=None, out=N
     _check(st)
     _record((logits, out["values"], out["ids"], out["lse"] if lse else None, status), dev, s, stream)
     return out
+
+
+def _distill_inputs(student, top_ids, top_logits, top_lse, row_weight):
+    """Check the inputs of a distillation; returns (N, V, K, device, dtype code)."""
+    _cuda(student, "student")
+    if student.dim() != 2:
+        raise ValueError("student must be [N, V]")
+    N, V = student.shape
+    dev = student.device
+    code = _dtype_code(student)
+    if top_ids is None or top_logits is None:
+        raise ValueError("top_ids and top_logits are required")
+    _cuda(top_ids, "top_ids", torch.int32, dev)
+    _cuda(top_logits, "top_logits", torch.float32, dev)
+    if top_ids.dim() != 2 or top_ids.shape[0] != N or top_ids.shape[1] < 1:
+        raise ValueError("top_ids must be [N, K]")
+    K = top_ids.shape[1]
+    if tuple(top_logits.shape) != (N, K):
+        raise ValueError("top_logits must be [N, K] like top_ids")
+    _per_row(top_lse, "top_lse", torch.float32, N, dev)
+    _per_row(row_weight, "row_weight", torch.float32, N, dev)
+    return N, V, K, dev, code
+
+
+def spec_distill(student, top_ids, top_logits, temperature=1.0, *, top_lse=None, row_weight=None, grad=False,
+                 status=None, out=None, stream=None):
+    """Distillation loss of student logits [N, V] against a teacher's largest logits (top_ids [N, K]
+    int32, top_logits [N, K] float32, and with top_lse [N] float32 its log-normaliser; as
+    spec_top_logits returns them): returns dict(loss [N], stats [N, 2], status), and with grad=True
+    also grad [N, V], the gradient of the summed losses in student's dtype (out["grad"] may be
+    student itself).  row_weight [N] scales each row; a row of weight 0 is not read.
+
+    No autograd graph is recorded: pass the gradient on with student.backward(r["grad"]), or keep
+    stats for spec_distill_backward."""
+    lib = load_library()
+    N, V, K, dev, code = _distill_inputs(student, top_ids, top_logits, top_lse, row_weight)
+    h, s = _stream_handle(dev, stream)
+    shapes = {"loss": ((N,), torch.float32), "stats": ((N, 2), torch.float32)}
+    if grad:
+        shapes["grad"] = ((N, V), student.dtype)
+    out = _outputs(_allocate(shapes, dev, s, stream) if out is None else out, shapes, dev)
+    status = _status(status, dev, s)
+    out["status"] = status
+    g = out["grad"] if grad else None
+    with torch.cuda.device(dev):
+        st = lib.spec_distill(_ptr(student), code, N, V, _ptr(top_ids), _ptr(top_logits), K, _ptr(top_lse),
+                              float(temperature), _ptr(row_weight), _ptr(out["loss"]), _ptr(out["stats"]), _ptr(g),
+                              _ptr(status), h)
+    _check(st)
+    _record((student, top_ids, top_logits, top_lse, row_weight, out["loss"], out["stats"], g, status), dev, s, stream)
+    return out
+
+
+def spec_distill_backward(student, top_ids, top_logits, stats, grad_loss, temperature=1.0, *, top_lse=None,
+                          row_weight=None, status=None, out=None, stream=None):
+    """The gradient of sum(grad_loss * loss) with respect to student, from spec_distill's stats of
+    the same inputs: returns dict(grad [N, V] in student's dtype, status).  out may be student."""
+    lib = load_library()
+    N, V, K, dev, code = _distill_inputs(student, top_ids, top_logits, top_lse, row_weight)
+    if stats is None:
+        raise ValueError("stats is required")
+    _cuda(stats, "stats", torch.float32, dev)
+    if tuple(stats.shape) != (N, 2):
+        raise ValueError("stats must be [N, 2]")
+    _per_row(grad_loss, "grad_loss", torch.float32, N, dev, True)
+    h, s = _stream_handle(dev, stream)
+    shapes = {"grad": ((N, V), student.dtype)}
+    out = _outputs(_allocate(shapes, dev, s, stream) if out is None else dict(grad=out), shapes, dev)
+    status = _status(status, dev, s)
+    with torch.cuda.device(dev):
+        st = lib.spec_distill_backward(_ptr(student), code, N, V, _ptr(top_ids), _ptr(top_logits), K, _ptr(top_lse),
+                                       float(temperature), _ptr(row_weight), _ptr(stats), _ptr(grad_loss),
+                                       _ptr(out["grad"]), _ptr(status), h)
+    _check(st)
+    _record((student, top_ids, top_logits, top_lse, row_weight, stats, grad_loss, out["grad"], status), dev, s, stream)
+    return dict(grad=out["grad"], status=status)
 
 
 def spec_tree_mask(parents, *, status=None, out=None, stream=None):

@@ -1,9 +1,10 @@
 // vocab.cu -- host side of the operators on rows of logits (spec_sample_filtered,
-// spec_top_logits): argument checks and dispatch.
+// spec_top_logits, spec_distill, spec_distill_backward): argument checks and
+// dispatch.
 #include <climits>
 #include <cmath>
 
-#include "rows.h"
+#include "distill.h"
 
 namespace spec {
 
@@ -15,6 +16,35 @@ namespace {
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 bool valid_dtype(spec_dtype d) { return d == SPEC_F32 || d == SPEC_BF16; }
 int elt_bytes(spec_dtype d) { return d == SPEC_F32 ? 4 : 2; }
+
+// The checks the distillation's calls share, and their fields of the parameter block.
+spec_status distill_args(DistillArgs *a, const void *student, spec_dtype dtype, int N, int V, const int32_t *ids, const float *top,
+                         int K, const float *lse, float T, const float *weight, uint32_t *dev_status) {
+    if (!valid_dtype(dtype)) return fail(SPEC_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+    if (N < 0 || V < 1 || K < 1) return fail(SPEC_ERR_INVALID_ARG, "need N >= 0, V >= 1, K >= 1");
+    if (K > SPEC_MAX_TOP) return fail(SPEC_ERR_UNSUPPORTED, "K = %d > %d", K, SPEC_MAX_TOP);
+    if (!(T >= kMinTemperature && T <= kMaxTemperature)) return fail(SPEC_ERR_INVALID_ARG, "temperature must be in [1e-6, 1e6]");
+    a->N = N;
+    if (N == 0) return SPEC_OK;
+    const int eb = elt_bytes(dtype);
+    if (!student || !aligned(student, eb)) return fail(SPEC_ERR_INVALID_ARG, "student logits null or misaligned");
+    if (!ids || !top || !dev_status) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
+    if (!aligned(ids, 4) || !aligned(top, 4) || !aligned(lse, 4) || !aligned(weight, 4) || !aligned(dev_status, 4))
+        return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    if (V > SPEC_MAX_ROW_BYTES / eb) return fail(SPEC_ERR_UNSUPPORTED, "V = %d: rows of at most %d bytes", V, SPEC_MAX_ROW_BYTES);
+    if (N > INT_MAX / 64) return fail(SPEC_ERR_UNSUPPORTED, "N too large");
+    a->student = static_cast<const unsigned char *>(student);
+    a->student_end = a->student + static_cast<size_t>(N) * static_cast<size_t>(V) * eb;
+    a->ids = ids;
+    a->top = top;
+    a->lse = lse;
+    a->weight = weight;
+    a->V = V;
+    a->K = K;
+    a->T = T;
+    a->status = dev_status;
+    return SPEC_OK;
+}
 
 // The checks every operator on [B, V] logits shares, and their fields of the parameter block.
 spec_status rows_args(RowArgs *a, const void *logits, spec_dtype dtype, int B, int V, uint32_t *dev_status) {
@@ -86,4 +116,38 @@ extern "C" spec_status spec_top_logits(const void *logits, spec_dtype dtype, int
     a.lse = lse;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == SPEC_F32 ? launch_rows<4, kTopRows>(a, s) : launch_rows<2, kTopRows>(a, s);
+}
+
+extern "C" spec_status spec_distill(const void *student_logits, spec_dtype dtype, int N, int V, const int32_t *top_ids,
+                                    const float *top_logits, int K, const float *top_lse, float temperature,
+                                    const float *row_weight, float *loss, float *stats, void *grad, uint32_t *dev_status,
+                                    void *stream) {
+    g_last_error[0] = '\0';
+    DistillArgs a = {};
+    spec_status st = distill_args(&a, student_logits, dtype, N, V, top_ids, top_logits, K, top_lse, temperature, row_weight, dev_status);
+    if (st != SPEC_OK || N == 0) return st;
+    if (!loss || !stats) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
+    if (!aligned(loss, 4) || !aligned(stats, 4) || !aligned(grad, elt_bytes(dtype)))
+        return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    a.loss = loss;
+    a.stats = stats;
+    a.grad = static_cast<unsigned char *>(grad);
+    return launch_distill(a, elt_bytes(dtype), grad ? kLossGrad : kLoss, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" spec_status spec_distill_backward(const void *student_logits, spec_dtype dtype, int N, int V, const int32_t *top_ids,
+                                             const float *top_logits, int K, const float *top_lse, float temperature,
+                                             const float *row_weight, const float *stats, const float *grad_loss, void *grad,
+                                             uint32_t *dev_status, void *stream) {
+    g_last_error[0] = '\0';
+    DistillArgs a = {};
+    spec_status st = distill_args(&a, student_logits, dtype, N, V, top_ids, top_logits, K, top_lse, temperature, row_weight, dev_status);
+    if (st != SPEC_OK || N == 0) return st;
+    if (!stats || !grad_loss || !grad) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
+    if (!aligned(stats, 4) || !aligned(grad_loss, 4) || !aligned(grad, elt_bytes(dtype)))
+        return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    a.stats = const_cast<float *>(stats);
+    a.grad_loss = grad_loss;
+    a.grad = static_cast<unsigned char *>(grad);
+    return launch_distill(a, elt_bytes(dtype), kBackward, static_cast<cudaStream_t>(stream));
 }

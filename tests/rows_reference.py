@@ -49,3 +49,27 @@ def top_logits(x, k, T=1.0):
     m = x[order[0]]
     T = float(np.float32(T))
     return values, ids, m / T + np.log(np.exp((x - m) / T).sum())
+
+
+def distill(x, ids, t, lse=None, T=1.0, w=1.0):
+    """(loss, (largest, exp-sum), gradient) of one row, everything in 64 bits."""
+    x, t = np.asarray(x, np.float64), np.asarray(t, np.float64)
+    T, w = float(np.float32(T)), float(np.float32(w))
+    if w == 0:
+        return 0.0, (0.0, 0.0), np.zeros_like(x)
+    live = (ids >= 0) & (ids < len(x)) & (t > -np.inf)
+    ids, t = ids[live], t[live]
+    m = x.max()
+    e = np.exp((x - m) / T)
+    S = e.sum()
+    if not len(ids):
+        return 0.0, (m, S), np.zeros_like(x)
+    if lse is None:
+        logp = (t - t.max()) / T - np.log(np.exp((t - t.max()) / T).sum())
+    else:
+        logp = t / T - float(lse)
+    p = np.exp(logp)
+    loss = w * (p * (logp - ((x[ids] - m) / T - np.log(S)))).sum()
+    grad = p.sum() * e / S
+    np.subtract.at(grad, ids, p)
+    return loss, (m, S), w / T * grad

@@ -135,3 +135,70 @@ def test_the_reference_on_a_worked_row():
     assert [ref.sample_filtered(x, u, 1.0)[0] for u in (0.0, 0.1, 0.2, 0.6, 0.7, 0.99)] == [0, 0, 1, 1, 2, 3]
     assert [ref.sample_filtered(x, u, 1.0, k=2)[0] for u in (0.0, 0.6, 0.7)] == [1, 1, 3]
     assert ref.sample_filtered(x, 0.9, 0.0)[0] == 1
+
+
+def _distill(lib, **kw):
+    a = dict(x=FAKE, dtype=1, N=2, V=100, ids=FAKE, t=FAKE, K=5, lse=None, T=1.0, w=None, loss=FAKE, stats=FAKE, grad=FAKE, st=FAKE)
+    a.update(kw)
+    head = [a[n] for n in ("x", "dtype", "N", "V", "ids", "t", "K", "lse", "T", "w")]
+    return (lib.spec_distill(*head, a["loss"], a["stats"], a["grad"], a["st"], None),
+            lib.spec_distill_backward(*head, a["stats"], a["loss"], a["grad"], a["st"], None))
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(dtype=3), sv.SPEC_ERR_INVALID_ARG), (dict(N=-1), sv.SPEC_ERR_INVALID_ARG), (dict(V=0), sv.SPEC_ERR_INVALID_ARG),
+    (dict(K=0), sv.SPEC_ERR_INVALID_ARG), (dict(K=sv.MAX_TOP + 1), sv.SPEC_ERR_UNSUPPORTED), (dict(T=0.0), sv.SPEC_ERR_INVALID_ARG),
+    (dict(T=float("inf")), sv.SPEC_ERR_INVALID_ARG), (dict(T=float("nan")), sv.SPEC_ERR_INVALID_ARG), (dict(x=None), sv.SPEC_ERR_INVALID_ARG),
+    (dict(x=ODD), sv.SPEC_ERR_INVALID_ARG), (dict(ids=None), sv.SPEC_ERR_INVALID_ARG), (dict(t=None), sv.SPEC_ERR_INVALID_ARG),
+    (dict(lse=ODD), sv.SPEC_ERR_INVALID_ARG), (dict(w=ODD), sv.SPEC_ERR_INVALID_ARG), (dict(loss=None), sv.SPEC_ERR_INVALID_ARG),
+    (dict(stats=None), sv.SPEC_ERR_INVALID_ARG), (dict(grad=ODD), sv.SPEC_ERR_INVALID_ARG), (dict(st=None), sv.SPEC_ERR_INVALID_ARG),
+    (dict(V=sv.MAX_ROW_BYTES // 2 + 1), sv.SPEC_ERR_UNSUPPORTED), (dict(N=0), sv.SPEC_OK)])
+def test_distill_host_validation(lib, kw, expect):
+    assert _distill(lib, **kw) == (expect, expect)
+
+
+def test_distill_backward_needs_a_gradient(lib):
+    assert lib.spec_distill_backward(FAKE, 1, 2, 100, FAKE, FAKE, 5, None, 1.0, None, FAKE, FAKE, None, FAKE, None) == sv.SPEC_ERR_INVALID_ARG
+
+
+def test_distill_binding(fake):
+    N, K = 4, 6
+    x, ids, t, n = torch.zeros((N, V)), torch.zeros((N, K), dtype=i32), torch.zeros((N, K)), torch.zeros(N)
+    r = sv.spec_distill(x, ids, t, top_lse=n, row_weight=n)
+    assert "grad" not in r and r["stats"].shape == (N, 2)
+    assert sv.spec_distill(x.bfloat16(), ids, t, grad=True)["grad"].dtype == torch.bfloat16
+    assert sv.spec_distill_backward(x, ids, t, r["stats"], n)["grad"].shape == (N, V)
+    for bad in (dict(x=x[0]), dict(ids=ids[:2].contiguous()), dict(ids=None), dict(t=t[:, :3].contiguous()), dict(t=None), dict(ids=ids[:, :0], t=t[:, :0]),
+                dict(lse=torch.zeros(N + 1)), dict(w=torch.zeros((N, 1))), dict(x=torch.zeros((V, N)).t())):
+        with pytest.raises(ValueError):
+            sv.spec_distill(bad.get("x", x), bad.get("ids", ids), bad.get("t", t), top_lse=bad.get("lse"), row_weight=bad.get("w"))
+        with pytest.raises(ValueError):
+            sv.spec_distill_backward(bad.get("x", x), bad.get("ids", ids), bad.get("t", t), r["stats"], n, top_lse=bad.get("lse"), row_weight=bad.get("w"))
+    for kw in (dict(stats=None), dict(stats=n), dict(grad_loss=None), dict(grad_loss=torch.zeros(1)), dict(out=torch.zeros((N, V + 1)))):
+        with pytest.raises(ValueError):
+            sv.spec_distill_backward(x, ids, t, kw.get("stats", r["stats"]) if "stats" in kw else r["stats"],
+                                     kw["grad_loss"] if "grad_loss" in kw else n, out=kw.get("out"))
+    with pytest.raises(ValueError):
+        sv.spec_distill(x, ids, t, grad=True, out=dict(loss=n, stats=torch.zeros((N, 2))))
+    with pytest.raises(TypeError):
+        sv.spec_distill(x, ids.long(), t)
+    with pytest.raises(TypeError):
+        sv.spec_distill(x, ids, t.bfloat16())
+    with pytest.raises(TypeError):
+        sv.spec_distill(x, ids, t, grad=True, out=dict(loss=n, stats=torch.zeros((N, 2)), grad=torch.zeros((N, V)).bfloat16()))
+
+
+def test_the_distillation_reference_on_a_worked_row():
+    """Student uniform over 4, teacher all on token 2: loss log 4, gradient 1/4 - [v = 2]; differences agree."""
+    x, ids, t = np.zeros(4), np.array([2, -1], np.int32), np.array([5.0, 9.0])
+    loss, (m, S), g = ref.distill(x, ids, t)
+    assert abs(loss - np.log(4)) < 1e-15 and (m, S) == (0.0, 4.0) and np.allclose(g, [0.25, 0.25, -0.75, 0.25])
+    r = np.random.RandomState(0)
+    x, ids, t = r.randn(9), np.array([3, 7, 3, 0], np.int32), r.randn(4)
+    for lse in (None, 1.7):
+        _, _, g = ref.distill(x, ids, t, lse, 0.5, 2.0)
+        for v in range(9):
+            h = np.zeros(9)
+            h[v] = 1e-6
+            d = (ref.distill(x + h, ids, t, lse, 0.5, 2.0)[0] - ref.distill(x - h, ids, t, lse, 0.5, 2.0)[0]) / 2e-6
+            assert abs(d - g[v]) < 1e-7
