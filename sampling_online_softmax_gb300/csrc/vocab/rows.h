@@ -11,7 +11,7 @@
 namespace spec {
 namespace vocab {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kMaxCluster = 8;    // CTAs per row (the portable limit)
 constexpr int kMaxList = 2048;    // entries of a cluster's list
 
