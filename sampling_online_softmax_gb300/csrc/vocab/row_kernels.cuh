@@ -11,18 +11,35 @@ namespace spec {
 namespace vocab {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-enum Verdict : uint32_t { kDone = 0, kWeighAll = 1, kMore = 2 };
+enum Verdict : uint32_t { kDone = 0, kWeigh = 1, kMore = 2 };
 
 // One row's request, after the checks.
 struct Request {
-    float T, p, low, u;  // low: the least logit that min-p keeps
-    int k;               // 0: no limit
+    float p, min_p, u;
+    unsigned long long least;  // the weight that min-p asks for (0: none)
+    int k;                     // 0: no limit
 };
+
+// The smallest whole number of units that is at least f times W (f in [0, 1]), and at least 1.
+__device__ __forceinline__ unsigned long long share_of(unsigned long long W, float f) {
+    if (f >= 1.f) return W;
+    bool rest;
+    const unsigned long long t = scaled_floor(W, f, &rest);
+    return max(t + (rest ? 1ull : 0ull), 1ull);
+}
+
+// The first kept token, whatever its weight: what u = 0 draws.  A weight that is 0 in 64 bits
+// (below 2^-1074) is not drawn.
+__device__ __forceinline__ bool drawn_at_zero(float l, const Scale &sc, float min_p) {
+    const float x = (l - sc.m) * sc.ch;
+    return x > -1074.f && (min_p == 0.f || x >= log2f(min_p));
+}
 
 // The leader's part of a row whose kept tokens are among the n entries of its list, which holds the
 // row's n largest logits: sorts them, cuts, draws.  W0, W1: bounds of the weight of all tokens that
-// top-p is a share of, in units of 2^-U; 0: the list's own first k.  kWeighAll: the bounds leave the
+// top-p is a share of, in units of 2^-U; 0: the list's own first k.  kWeigh: the bounds leave the
 // cut open; kMore: the cut lies past the list.
 template <int EB>
 __device__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, const Request &q, int n, unsigned long long W0, unsigned long long W1,
@@ -32,6 +49,8 @@ __device__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, const Request &q,
     sort_list(sh->list, n, tid);
     int nk = q.k > 0 ? min(n, q.k) : n;
     auto value = [&](int i) { return key_value(~static_cast<uint32_t>(sh->list[i] >> 32)); };
+    auto index = [&](int i) { return static_cast<uint32_t>(sh->list[i]); };
+    auto weight = [&](int i) { return sh->cum[i] - (i ? sh->cum[i - 1] : 0ull); };
 
     // running sums of the sorted weights, a run of entries per thread
     const int per = (nk + kThreads - 1) / kThreads;
@@ -41,47 +60,34 @@ __device__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, const Request &q,
         mine += fixed_weight(value(i), sc, sh->pow2);
         sh->cum[i] = mine;
     }
-    const unsigned long long incl = warp_scan(mine, lane);
-    if (lane == 31) sh->red[warp] = incl;
-    __syncthreads();
-    unsigned long long before = incl - mine;
-    for (int w = 0; w < warp; ++w) before += sh->red[w];
+    const unsigned long long before = r.sum_before(mine);
     for (int i = i0; i < i1; ++i) sh->cum[i] += before;
     __syncthreads();
 
-    if (q.p < 1.f || q.low > -INFINITY) {
+    if (q.p < 1.f || q.least) {
         const unsigned long long total = sh->cum[nk - 1];
-        unsigned long long t0 = 0, t1 = 0;
-        if (q.p < 1.f) {
-            bool rest;
-            t0 = scaled_floor(W0 ? W0 : total, q.p, &rest);
-            t0 = max(t0 + (rest ? 1ull : 0ull), 1ull);
-            t1 = scaled_floor(W1 ? W1 : total, q.p, &rest);
-            t1 = max(t1 + (rest ? 1ull : 0ull), 1ull);
-        }
+        const unsigned long long t0 = share_of(W0 ? W0 : total, q.p), t1 = share_of(W1 ? W1 : total, q.p);
         unsigned long long c = 0;  // entries below the two cuts of top-p, and entries that min-p keeps
         for (int i = i0; i < i1; ++i)
             c += static_cast<unsigned long long>(sh->cum[i] < t0) | static_cast<unsigned long long>(sh->cum[i] < t1) << 16 |
-                 static_cast<unsigned long long>(value(i) >= q.low) << 32;
+                 static_cast<unsigned long long>(weight(i) >= q.least) << 32;
         c = block_sum(c, sh->red, lane, warp);
         if (q.p < 1.f) {
             const int a = static_cast<int>(c & 0xffff) + 1, b = static_cast<int>((c >> 16) & 0xffff) + 1;
             if (b > nk) return kMore;
-            if (a != b) return kWeighAll;
+            if (a != b) return kWeigh;
             nk = a;
         }
         nk = min(nk, static_cast<int>(c >> 32));
     }
-    const unsigned long long W = sh->cum[nk - 1];
-    auto index = [&](int i) { return static_cast<uint32_t>(sh->list[i]); };
     if (nk == 1) {
         if (tid == 0) *token = static_cast<int32_t>(index(0));
         return kDone;
     }
-    if (q.u == 0.f) {  // the first kept token, however small its weight (a double's least is 2^-1074)
+    if (q.u == 0.f) {
         uint32_t x = kAll;
         for (int i = tid; i < nk; i += kThreads)
-            if ((value(i) - sc.m) * sc.ch > -1074.f) x = min(x, index(i));
+            if (drawn_at_zero(value(i), sc, q.min_p)) x = min(x, index(i));
         x = __reduce_min_sync(kAll, x);
         __syncthreads();
         if (lane == 0) sh->red[warp] = x;
@@ -93,8 +99,7 @@ __device__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, const Request &q,
         return kDone;
     }
     bool rest;
-    const unsigned long long target = scaled_floor(W, q.u, &rest) + 1;
-    auto weight = [&](int i) { return sh->cum[i] - (i ? sh->cum[i - 1] : 0ull); };
+    const unsigned long long target = scaled_floor(sh->cum[nk - 1], q.u, &rest) + 1;
     if (nk <= kThreads / 2) {  // each token's sum up to its own index, 2 to 8 threads a token
         const int each = nk <= kThreads / 8 ? 8 : nk <= kThreads / 4 ? 4 : 2;
         const int i = tid / each;
@@ -115,112 +120,303 @@ __device__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, const Request &q,
     const int pn = (nk + kThreads - 1) / kThreads;
     const int j0 = min(nk, tid * pn), j1 = min(nk, j0 + pn);
     unsigned long long s = 0;
-    for (int j = j0; j < j1; ++j) s += weight(static_cast<int>(static_cast<uint32_t>(sh->list[j])));
-    const unsigned long long upto = warp_scan(s, lane);
-    if (lane == 31) sh->red[warp] = upto;
-    __syncthreads();
-    unsigned long long run = upto - s;
-    for (int w = 0; w < warp; ++w) run += sh->red[w];
+    for (int j = j0; j < j1; ++j) s += weight(static_cast<int>(index(j)));
+    unsigned long long run = r.sum_before(s);
     for (int j = j0; j < j1; ++j) {
-        const unsigned long long w = weight(static_cast<int>(static_cast<uint32_t>(sh->list[j])));
+        const unsigned long long w = weight(static_cast<int>(index(j)));
         if (run < target && run + w >= target) *token = static_cast<int32_t>(sh->list[j] >> 32);
         run += w;
     }
     return kDone;
 }
 
-// The long way: the kept tokens are cut out of the whole row, and the draw runs over it.
-template <int EB>
-__device__ void draw_from_row(const RowArgs &a, Row<EB> &r, const Scale &sc, const Request &q, int32_t *token) {
-    const float2 *pow2 = r.sh->pow2;
-    // the kept tokens: those of a key above ck, and those of key ck up to index ci
-    uint32_t ck = Row<EB>::kLowest;
-    int ci = INT_MAX;
-    const uint32_t top = Row<EB>::key(sc.m);
+// What a row keeps: the keys above `key`, and of that key the indices up to `index`.
+struct Cut {
+    uint32_t key;
+    int index;
+};
+
+// Where the kept tokens, in the order of falling logits, reach COUNT: the k-th; else: p times
+// their weight.  False: fewer than k.
+//   1  a histogram of counts over 2048 equal steps below the maximum.  A bin's weight lies between
+//      its edges', 2 % apart, so its running sums bracket the cut's bin (COUNT: find it).
+//   2  the exact weights above the bracket and in all, and a histogram of the bracket's inside.
+//   3  the weights between, and the tokens of the narrowed bracket: a few, or equal ones, which one
+//      CTA sorts and weighs.
+// Where more than the list holds are left (equal logits in their thousands), or the cut lies below
+// the histogram, reach() finds it by keys.
+template <bool COUNT, int EB>
+__device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
+    SelectShared *sh = r.sh;
+    const float2 *pow2 = sh->pow2;
+    const int tid = r.tid;
+    const Cut had = *cut;
     auto kept = [&](float l, int x) {
         const uint32_t y = Row<EB>::key(l);
-        return y > ck || (y == ck && x <= ci);
+        return y > had.key || (y == had.key && x <= had.index);
     };
-    auto weight = [&](float l, int x) { return kept(l, x) ? fixed_weight(l, sc, pow2) : 0ull; };
-    auto total = [&]() {
-        unsigned long long v = 0;
-        r.each([&](float l, int x) { v += weight(l, x); });
-        return r.sum(v);
+    // 48 steps of two hold every weight that counts; narrower rows get finer bins
+    const float span = fminf(48.f / sc.ch, 2.f * (sc.m - r.least_maximum()));
+    const float scale = (kBins - 1) / fmaxf(span, 1e-30f);
+    auto place = [&](float l) { return fminf((sc.m - l) * scale, 0x1.fffffep10f); };  // in bins below the maximum; < kBins
+    auto clear = [&]() {
+        r.sync();  // the histogram before this one has been read, by the peers too
+        for (int i = tid; i < kBins; i += kThreads) sh->count[i] = 0;
+        if (tid == 0) sh->cross_bin = kAll, sh->cross_last = kBins - 1;
+        __syncthreads();
     };
-    if (q.k > 0) {
-        uint32_t at;
-        unsigned long long above;
-        if (r.template reach<true>(ck, top, q.k, [&](float, int) { return 1ull; }, &at, &above)) {
-            ci = r.tie_index(at, q.k - above, [](float, int) { return true; });
-            ck = at;
+    // weights of a bin whose edges lie `at` bins below the maximum, in units of 2^-40
+    auto edge = [&](float at, float slack) { return static_cast<unsigned long long>(ptx::ex2(-at / scale * sc.ch) * slack * 0x1p40f); };
+
+    clear();
+    r.each([&](float l, int x) {
+        if (kept(l, x)) atomicAdd(&sh->count[static_cast<int>(place(l))], 1u);
+    });
+    r.sync();
+    unsigned long long v[kBinsPerThread], mine = 0, low = 0, high = 0;
+    r.template bins<true>(v);
+    uint32_t b0, b1;               // the cut's bin is in [b0, b1]
+    unsigned long long over = 0;   // COUNT: tokens above b0
+    const int first = tid * kBinsPerThread;
+    if (COUNT) {
+#pragma unroll
+        for (int i = 0; i < kBinsPerThread; ++i) mine += v[i];
+        unsigned long long run = r.sum_before(mine);
+#pragma unroll
+        for (int i = 0; i < kBinsPerThread; ++i) {
+            if (run < k && run + v[i] >= k) {
+                sh->cross_bin = first + i;
+                sh->above = run;
+            }
+            run += v[i];
         }
-    }
-    if (q.p < 1.f) {
-        bool rest;
-        unsigned long long target = scaled_floor(total(), q.p, &rest);
-        target = max(target + (rest ? 1ull : 0ull), 1ull);
-        uint32_t at;
-        unsigned long long above;
-        if (r.template reach<false>(ck, top, target, weight, &at, &above)) {
-            const unsigned long long w = fixed_weight(Row<EB>::value(at), sc, pow2);
-            const int old = ci;
-            const bool same = at == ck;
-            const int x = r.tie_index(at, (target - above + w - 1) / w, [&](float, int y) { return !same || y <= old; });
-            ck = at;
-            ci = x;
+        __syncthreads();
+        b0 = b1 = sh->cross_bin;
+        if (b0 == kAll) return false;
+        over = sh->above;
+    } else {
+        unsigned long long lo[kBinsPerThread], hi[kBinsPerThread];
+#pragma unroll
+        for (int i = 0; i < kBinsPerThread; ++i) {
+            const float at = static_cast<float>(first + i);
+            hi[i] = v[i] ? v[i] * (edge(at, 1.001f) + 1) : 0ull;
+            lo[i] = v[i] && first + i < kBins - 1 ? v[i] * edge(at + 1.f, 0.999f) : 0ull;
+            low += lo[i];
+            high += hi[i];
         }
+        unsigned long long all_l, all_h;
+        unsigned long long run_l = r.sum_before(low, &all_l), run_h = r.sum_before(high, &all_h);
+        const unsigned long long t0 = share_of(all_l, p), t1 = share_of(all_h, p);
+#pragma unroll
+        for (int i = 0; i < kBinsPerThread; ++i) {
+            if (run_h < t0 && run_h + hi[i] >= t0) sh->cross_bin = first + i;
+            if (run_l < t1 && run_l + lo[i] >= t1) sh->cross_last = first + i;
+            run_h += hi[i];
+            run_l += lo[i];
+        }
+        __syncthreads();
+        b0 = sh->cross_bin;
+        b1 = sh->cross_last;
+        if (b0 == kAll) b0 = 0;
     }
-    if (q.low > -INFINITY) {
-        uint32_t y = Row<EB>::key(q.low);
-        if (EB == 2 && Row<EB>::value(y) < q.low) ++y;
-        if (y > ck) ck = y, ci = INT_MAX;
+
+    const float from = static_cast<float>(b0), upto = static_cast<float>(b1 + 1);
+    const float fine = kBins / (upto - from);
+    auto inside = [&](float at) { return at >= from && at < upto; };
+    auto sub = [&](float at) { return min(kBins - 1, static_cast<int>((at - from) * fine)); };
+    unsigned long long W = 0, A = 0, target = static_cast<unsigned long long>(k);
+    clear();
+    r.each([&](float l, int x) {
+        if (!kept(l, x)) return;
+        const float at = place(l);
+        if (!COUNT) {
+            const unsigned long long w = fixed_weight(l, sc, pow2);
+            W += w;
+            if (at < from) A += w;
+        }
+        if (inside(at)) atomicAdd(&sh->count[sub(at)], 1u);
+    });
+    if (!COUNT) {
+        W = r.sum(W);
+        A = r.sum(A);
+        target = share_of(W, p);
+    } else {
+        r.sync();
+        A = over;
     }
-    if (q.u == 0.f) {  // the first kept token, however small its weight (a double's least is 2^-1074)
-        auto any = [&](float l, int x) {
-            return static_cast<unsigned long long>(kept(l, x) && (l - sc.m) * sc.ch > -1074.f);
+    r.template bins<true>(v);
+    uint32_t s0, s1;
+    if (COUNT) {
+        mine = 0;
+#pragma unroll
+        for (int i = 0; i < kBinsPerThread; ++i) mine += v[i];
+        unsigned long long run = A + r.sum_before(mine);
+#pragma unroll
+        for (int i = 0; i < kBinsPerThread; ++i) {
+            if (run < target && run + v[i] >= target) {
+                sh->cross_bin = first + i;
+                sh->above = run;
+            }
+            run += v[i];
+        }
+        __syncthreads();
+        s0 = s1 = sh->cross_bin;
+        A = sh->above;
+    } else {
+        const float step = 1.f / fine;
+        const unsigned long long unit = A >> (sc.U - 40), aim = target >> (sc.U - 40);  // in units of 2^-40
+        unsigned long long lo[kBinsPerThread], hi[kBinsPerThread];
+        low = high = 0;
+#pragma unroll
+        for (int i = 0; i < kBinsPerThread; ++i) {
+            const float at = from + static_cast<float>(first + i) * step;
+            hi[i] = v[i] ? v[i] * (edge(at, 1.00005f) + 1) : 0ull;
+            lo[i] = v[i] && !(b1 == kBins - 1 && first + i == kBins - 1) ? v[i] * edge(at + step, 0.99995f) : 0ull;
+            low += lo[i];
+            high += hi[i];
+        }
+        unsigned long long run_h = unit + 1 + r.sum_before(high);
+        unsigned long long run_l = unit + r.sum_before(low);
+#pragma unroll
+        for (int i = 0; i < kBinsPerThread; ++i) {
+            if (run_h < aim && run_h + hi[i] >= aim) sh->cross_bin = first + i;
+            if (run_l < aim + 1 && run_l + lo[i] >= aim + 1) sh->cross_last = first + i;
+            run_h += hi[i];
+            run_l += lo[i];
+        }
+        __syncthreads();
+        s0 = sh->cross_bin == kAll ? 0u : sh->cross_bin;  // the first bin may be reached from the start
+        s1 = sh->cross_last;
+    }
+    if (tid == 0) sh->list_n[1] = 0, sh->cut[0] = 0;
+    r.sync();
+    uint32_t found = 0;
+    unsigned long long between = 0;
+    r.vectors([&](const uint4 &vec, int i) {
+        auto pass = [&](float l, int x) {
+            if (!kept(l, x)) return false;
+            const float at = place(l);
+            const int y = inside(at) ? sub(at) : -1;
+            return y >= static_cast<int>(s0) && y <= static_cast<int>(s1);
         };
-        r.locate(1ull, any, [&](int x) { *token = x; });
+        if (!COUNT && i >= 0) {
+            float l[Row<EB>::kPer];
+            Row<EB>::unpack(vec, l);
+#pragma unroll
+            for (int q = 0; q < Row<EB>::kPer; ++q) {
+                const float at = place(l[q]);
+                if (inside(at) && sub(at) < static_cast<int>(s0) && kept(l[q], r.index(i, q))) between += fixed_weight(l[q], sc, pow2);
+            }
+        }
+        found += r.append(vec, i, 1, pass);
+    });
+    if (!COUNT) A += r.sum(between);
+    const uint32_t n = r.collected(found, 1);
+    if (n <= kMaxList) {
+        if (r.rank == 0) {
+            sort_list(sh->list, n, tid);
+            const int per = (n + kThreads - 1) / kThreads;
+            const int i0 = min(static_cast<int>(n), tid * per), i1 = min(static_cast<int>(n), i0 + per);
+            auto weigh = [&](int i) {
+                return COUNT ? 1ull : fixed_weight(key_value(~static_cast<uint32_t>(sh->list[i] >> 32)), sc, pow2);
+            };
+            mine = 0;
+            for (int i = i0; i < i1; ++i) mine += weigh(i);
+            unsigned long long run = A + r.sum_before(mine);
+            for (int i = i0; i < i1; ++i) {
+                const unsigned long long w = weigh(i);
+                if (run < target && run + w >= target) {
+                    const uint32_t key = Row<EB>::key(key_value(~static_cast<uint32_t>(sh->list[i] >> 32)));
+                    for (uint32_t c = 0; c < r.cs; ++c) {
+                        st_peer(peer(&sh->cut[0], c), key);
+                        st_peer(peer(&sh->cut[1], c), static_cast<uint32_t>(sh->list[i]));
+                    }
+                }
+                run += w;
+            }
+        }
+        r.sync();
+        const Cut c = {sh->cut[0], static_cast<int>(sh->cut[1])};
+        r.sync();  // read everywhere before it is written again
+        if (c.key) {
+            *cut = c;
+            return true;
+        }
+    }
+    uint32_t at;
+    unsigned long long above;
+    auto weigh = [&](float l, int x) -> unsigned long long { return !kept(l, x) ? 0ull : COUNT ? 1ull : fixed_weight(l, sc, pow2); };
+    if (!r.template reach<COUNT>(had.key, Row<EB>::key(sc.m), target, weigh, &at, &above)) return false;
+    const unsigned long long w = COUNT ? 1ull : fixed_weight(Row<EB>::value(at), sc, pow2);
+    const bool same = at == had.key;
+    cut->index = r.tie_index(at, (target - above + w - 1) / w, [&](float, int y) { return !same || y <= had.index; });
+    cut->key = at;
+    return true;
+}
+
+// The long way: the kept tokens are cut out of the whole row, and the draw runs over it.
+template <int EB>
+__device__ void draw_from_row(Row<EB> &r, const Scale &sc, const Request &q, int32_t *token) {
+    const float2 *pow2 = r.sh->pow2;
+    Cut cut = {Row<EB>::kLowest, INT_MAX};
+    if (q.k > 0) cut_row<true>(r, sc, q.k, 1.f, &cut);
+    if (q.p < 1.f) cut_row<false>(r, sc, 0, q.p, &cut);
+    auto kept = [&](float l, int x) {
+        const uint32_t y = Row<EB>::key(l);
+        return y > cut.key || (y == cut.key && x <= cut.index);
+    };
+    if (q.u == 0.f) {
+        r.locate([&](float l, int x) { return static_cast<unsigned long long>(kept(l, x) && drawn_at_zero(l, sc, q.min_p)); },
+                 [](unsigned long long) { return 1ull; }, [&](int x) { *token = x; });
         return;
     }
-    bool rest;
-    const unsigned long long target = scaled_floor(total(), q.u, &rest) + 1;
-    r.locate(target, weight, [&](int x) { *token = x; });
+    r.locate(
+        [&](float l, int x) {
+            const unsigned long long w = kept(l, x) ? fixed_weight(l, sc, pow2) : 0ull;
+            return w >= q.least ? w : 0ull;
+        },
+        [&](unsigned long long W) {
+            bool rest;
+            return scaled_floor(W, q.u, &rest) + 1;
+        },
+        [&](int x) { *token = x; });
 }
 
 // Filtered sampling of row b.
 template <int EB>
-__device__ void sample_row(const RowArgs &a, Row<EB> &r, int b, uint4 *buf) {
+__device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
     SelectShared *sh = r.sh;
-    r.start_load(a, b, buf);
     Request q;
     q.u = a.u[b];
-    q.T = a.temperature[b];
+    float T = a.temperature[b];
     q.k = a.top_k ? a.top_k[b] : 0;
     q.p = a.top_p ? a.top_p[b] : 1.f;
-    q.low = -INFINITY;
-    const float mp = a.min_p ? a.min_p[b] : 0.f;
-    const bool greedy = q.T == 0.f;
-    const bool bad = !(greedy || (q.T >= kMinTemperature && q.T <= kMaxTemperature)) ||
-                     !(greedy || (q.p >= 0.f && q.p <= 1.f && mp >= 0.f && mp <= 1.f && q.u >= 0.f && q.u < 1.f));
+    q.min_p = a.min_p ? a.min_p[b] : 0.f;
+    q.least = 0;
+    const bool greedy = T == 0.f;
+    const bool bad = !(greedy || (T >= kMinTemperature && T <= kMaxTemperature)) ||
+                     !(greedy || (q.p >= 0.f && q.p <= 1.f && q.min_p >= 0.f && q.min_p <= 1.f && q.u >= 0.f && q.u < 1.f));
     if (bad) {
-        copies_wait<0>();
-        cluster_wait();
         if (r.rank == 0 && r.tid == 0) {
             a.tokens[b] = -1;
             atomicOr(a.status, SPEC_DEV_BAD_PARAM);
         }
+        if (r.cs > 1) cluster_wait();
         return;
     }
     const bool one = greedy || q.k == 1;  // the argmax, whatever the other filters keep
-    if (greedy) q.T = 1.f;
+    if (greedy) T = 1.f;
     if (q.k < 0 || q.k >= a.V) q.k = 0;
-    const double c = 1.4426950408889634074 / static_cast<double>(q.T);
     Scale sc;
-    sc.ch = static_cast<float>(c);
-    sc.cl = static_cast<float>(c - static_cast<double>(sc.ch));
     sc.U = a.U;
-    const double below = mp > 0.f && !one ? static_cast<double>(q.T) * log(static_cast<double>(mp)) : 0.0;
-    sc.m = r.maximum(buf);
+    {   // log2(e) / T as a pair
+        constexpr float kH = 0x1.715476p+0f, kL = 0x1.4ae0c0p-26f;
+        sc.ch = kH / T;
+        sc.cl = (fmaf(-sc.ch, T, kH) + kL) / T;
+    }
+    const bool share = q.p < 1.f && q.k == 0;  // top-p is a share of the whole row
+    const bool sums = share && a.V > kMaxList && !one;
+    sc.m = sums ? r.template stream<true>(sc.ch) : r.template stream<false>(sc.ch);
     if (!(fabsf(sc.m) < INFINITY)) {  // NaN, +inf, or nothing but -inf
         if (r.rank == 0 && r.tid == 0) {
             a.tokens[b] = -1;
@@ -230,10 +426,17 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b, uint4 *buf) {
     }
     if (one) {  // the lowest index of the maximum: each warp's first, to the leader
         uint32_t x = kAll;
-        if (r.own_max == sc.m) r.each([&](float l, int y) { if (l == sc.m) x = min(x, static_cast<uint32_t>(y)); });
+        r.gather(sc.m, [&](const uint4 &v, int i) {
+            if (i < 0) return;
+            float l[Row<EB>::kPer];
+            Row<EB>::unpack(v, l);
+#pragma unroll
+            for (int e = 0; e < Row<EB>::kPer; ++e)
+                if (l[e] == sc.m) x = min(x, static_cast<uint32_t>(r.index(i, e)));
+        });
         x = __reduce_min_sync(kAll, x);
         if (r.lane == 0) st_peer(peer(&sh->hits[0][r.rank * kWarps + r.warp], 0), x);
-        cluster_sync();
+        r.sync();
         if (r.rank == 0 && r.warp == 0) {
             x = kAll;
             for (uint32_t i = r.lane; i < r.cs * kWarps; i += 32) x = min(x, sh->hits[0][i]);
@@ -242,70 +445,76 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b, uint4 *buf) {
         }
         return;
     }
-    // w >= min_p as a bound on the logit: only the least logit at or above the bound matters
-    if (mp > 0.f) q.low = __double2float_ru(static_cast<double>(sc.m) + below);
+    if (q.min_p > 0.f) q.least = share_of(1ull << sc.U, q.min_p);
 
-    // The list holds the logits from `low` on; all: that is every token.
-    const bool share = q.p < 1.f && q.k == 0;  // top-p is a share of the whole row
-    const int attempts = share && a.V > kMaxList ? 2 : 1;
+    // The short way: the list holds the logits from `low` on; all: that is every token.
     float low[2] = {-FLT_MAX, -FLT_MAX};
     bool all[2] = {true, true};
+    unsigned long long W0 = 0, W1 = 0;
     if (a.V > kMaxList) {
-        if (q.k > kMaxGoal || (q.k == 0 && !share && !(mp > 0.f))) {
-            draw_from_row(a, r, sc, q, a.tokens + b);
+        if (sums) {  // bounds of the row's weight, 2^-18 apart to either side
+            float Q, s = r.exp_total(&Q);
+            s *= ptx::ex2(fmaf(-sc.m, sc.ch, Q));
+            const unsigned long long W = __float2ull_rn(fminf(s, 0x1p22f) * 0x1p40f) << (sc.U - 40);
+            const bool sound = s >= 0.5f && s < 0x1p22f;  // not: logits whose products overflow
+            W0 = sound ? W - (W >> 18) : 1ull;
+            W1 = sound ? W + (W >> 18) : 1ull << 62;
+        }
+        if (q.k > kMaxGoal || (q.k == 0 && !share && q.min_p == 0.f)) {
+            draw_from_row(r, sc, q, a.tokens + b);
             return;
         }
-        if (q.k > 0 || share) {  // fewer groups than asked for: few tokens that are not masked
+        if (q.k > 0 || share) {  // too few groups for it: few tokens that are not masked
             all[0] = !r.threshold(sc.m, q.k > 0 ? q.k : kFirstGoal, &low[0]);
             if (share && !all[0]) all[1] = !r.threshold(sc.m, kMaxGoal, &low[1]);
-        } else {
-            low[0] = q.low;
+        } else {  // from a little below what min-p asks for
+            const float x = log2f(q.min_p) / sc.ch;
+            low[0] = sc.m + x - (fabsf(x) + fabsf(sc.m)) * 0x1p-18f;
             all[0] = false;
         }
     }
-    const bool sums = share && !all[0];
-    if (sums) r.exp_sum(sc.m, sc.ch);
-    for (int attempt = 0; attempt < attempts; ++attempt) {
-        r.collect(low[attempt], attempt);
-        cluster_sync();
-        const uint32_t n = r.collected(attempt);
-        if (sums && attempt == 0) {
-            const unsigned long long W = r.exp_total() << (sc.U - 40);
-            sh->W[0] = W - (W >> 16);
-            sh->W[1] = W + (W >> 16);
-        }
+    for (int attempt = 0; attempt < (sums ? 2 : 1); ++attempt) {
+        const uint32_t n = r.collect(low[attempt], attempt);
         if (n > kMaxList) break;
         if (!share || all[attempt]) {
             if (r.rank == 0) draw_from_list(r, sc, q, n, 0ull, 0ull, a.tokens + b);
             return;
         }
-        __syncthreads();
         uint32_t v = kDone;
-        for (int exact = 0; exact < 2; ++exact) {
+        for (int weighed = 0; weighed < 3; ++weighed) {
             if (r.rank == 0) {
-                v = draw_from_list(r, sc, q, n, sh->W[0], sh->W[1], a.tokens + b);
+                v = draw_from_list(r, sc, q, n, W0, W1, a.tokens + b);
                 if (r.tid < static_cast<int>(r.cs)) st_peer(peer(&sh->verdict, r.tid), v);
             }
-            cluster_sync();
+            r.sync();
             v = sh->verdict;
-            if (v != kWeighAll) break;
+            if (v != kWeigh || weighed == 2) break;
             unsigned long long w = 0;
-            r.each([&](float l, int) { w += fixed_weight(l, sc, sh->pow2); });
-            w = r.sum(w);
-            sh->W[0] = sh->W[1] = w;
-            __syncthreads();
+            if (weighed == 0) {  // the list's weights are exact: the error is the rest's alone
+                float rest = 0.f;
+                r.each([&](float l, int) { rest += l >= low[attempt] ? 0.f : ptx::ex2((l - sc.m) * sc.ch); });
+                w = r.sum(__float2ull_rn(rest * 0x1p40f)) << (sc.U - 40);
+                if (r.rank == 0) {  // (the leader alone draws)
+                    const unsigned long long listed = sh->cum[n - 1];
+                    W0 = listed + w - (w >> 17) - 1;
+                    W1 = listed + w + (w >> 17) + (1ull << (sc.U - 30));
+                }
+            } else {
+                r.each([&](float l, int) { w += fixed_weight(l, sc, sh->pow2); });
+                W0 = W1 = r.sum(w);
+            }
         }
         if (v == kDone) return;
     }
-    draw_from_row(a, r, sc, q, a.tokens + b);
+    draw_from_row(r, sc, q, a.tokens + b);
 }
 
 // The K largest logits of row b.
 template <int EB>
-__device__ void top_row(const RowArgs &a, Row<EB> &r, int b, uint4 *buf) {
+__device__ void top_row(const RowArgs &a, Row<EB> &r, int b) {
     SelectShared *sh = r.sh;
-    r.start_load(a, b, buf);
-    const float m = r.maximum(buf);
+    const float c = kLog2e / a.temp;
+    const float m = a.lse ? r.template stream<true>(c) : r.template stream<false>(c);
     const size_t out = static_cast<size_t>(b) * a.K;
     if (!(m < INFINITY)) {  // NaN or +inf
         if (r.rank == 0) {
@@ -321,41 +530,41 @@ __device__ void top_row(const RowArgs &a, Row<EB> &r, int b, uint4 *buf) {
         return;
     }
     const bool empty = m == -INFINITY;  // every token masked: an empty list, no error
-    if (a.lse && !empty) r.exp_sum(m, kLog2e / a.temp);
-    float low = -FLT_MAX;
-    if (!empty && a.V > kMaxList && !r.threshold(m, a.K, &low)) low = -FLT_MAX;  // few tokens that are not masked
-    bool shorter = !empty;
-    if (shorter) r.collect(low, 0);
-    cluster_sync();
     if (a.lse) {
-        const float S = empty ? 0.f : static_cast<float>(r.exp_total()) * 0x1p-40f;
-        if (r.rank == 0 && r.tid == 0) a.lse[b] = empty ? -INFINITY : m / a.temp + logf(S);
+        float Q, z = -INFINITY;
+        const float s = r.exp_total(&Q);
+        if (!empty) {
+            z = fmaf(Q, kLn2, logf(s));
+            if (!(fabsf(z) < INFINITY) || !(s >= 0.25f)) {  // logits whose products with c overflow
+                float d = 0.f;
+                r.each([&](float l, int) { d += ptx::ex2((l - m) * c); });
+                z = m / a.temp + logf(static_cast<float>(r.sum(__float2ull_rn(d * 0x1p40f))) * 0x1p-40f);
+            }
+        }
+        if (r.rank == 0 && r.tid == 0) a.lse[b] = z;
     }
-    int n = 0;
-    if (shorter) {
-        const uint32_t c = r.collected(0);
-        shorter = c <= kMaxList;
-        n = static_cast<int>(c);
+    uint32_t n = 0;
+    if (!empty) {
+        float low = -FLT_MAX;
+        if (a.V > kMaxList && !r.threshold(m, a.K, &low)) low = -FLT_MAX;  // few tokens that are not masked
+        n = r.collect(low, 0);
     }
-    if (!shorter && !empty) {
-        uint32_t ck = Row<EB>::kLowest;
-        int ci = INT_MAX;
+    if (n > kMaxList) {  // equal logits in their thousands
         uint32_t at;
         unsigned long long above;
-        if (r.template reach<true>(ck, Row<EB>::key(m), a.K, [](float, int) { return 1ull; }, &at, &above)) {
-            ci = r.tie_index(at, a.K - above, [](float, int) { return true; });
-            ck = at;
+        Cut cut = {Row<EB>::kLowest, INT_MAX};
+        if (r.template reach<true>(cut.key, Row<EB>::key(m), a.K, [](float, int) { return 1ull; }, &at, &above)) {
+            cut.index = r.tie_index(at, a.K - above, [](float, int) { return true; });
+            cut.key = at;
         }
-        const uint32_t n_at = peer(&sh->list_n[1], 0), list_at = peer(sh->list, 0);
-        r.each([&](float l, int x) {
-            const uint32_t y = Row<EB>::key(l);
-            if (y > ck || (y == ck && x <= ci)) {
-                const uint32_t i = atom_add_peer(n_at, 1);
-                if (i < kMaxList) st_peer(list_at + i * 8, static_cast<unsigned long long>(~order_key(l)) << 32 | static_cast<uint32_t>(x));
-            }
+        uint32_t found = 0;
+        r.vectors([&](const uint4 &v, int i) {
+            found += r.append(v, i, 1, [&](float l, int x) {
+                const uint32_t y = Row<EB>::key(l);
+                return y > cut.key || (y == cut.key && x <= cut.index);
+            });
         });
-        cluster_sync();
-        n = static_cast<int>(sh->list_n[1]);
+        n = r.collected(found, 1);
     }
     if (r.rank != 0) return;
     sort_list(sh->list, n, r.tid);
@@ -367,35 +576,33 @@ __device__ void top_row(const RowArgs &a, Row<EB> &r, int b, uint4 *buf) {
 }
 
 template <int EB, int OP>
-__global__ void __launch_bounds__(kThreads) row_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kThreads, kRowCtas) row_kernel(const RowArgs a) {
     extern __shared__ uint4 dyn[];
     SelectShared *sh = reinterpret_cast<SelectShared *>(dyn);
-    uint4 *buf = dyn + sizeof(SelectShared) / 16;
-    Row<EB> r = row_setup<EB>(a, sh);
-    cluster_arrive();  // the first peer access waits for it
     const int b = blockIdx.x / a.cluster;
-    if (OP == kSampleRows)
-        sample_row<EB>(a, r, b, buf);
+    Row<EB> r = row_setup<EB>(a, sh, b);
+    if (r.cs > 1)
+        cluster_arrive();  // the first peer access waits for it
     else
-        top_row<EB>(a, r, b, buf);
+        __syncthreads();
+    if (OP == kSampleRows)
+        sample_row<EB>(a, r, b);
+    else
+        top_row<EB>(a, r, b);
 }
 
-// CTAs per row and vectors per CTA.
-inline spec_status row_split(RowArgs *a, int EB, size_t fixed, size_t max_dyn) {
+// CTAs per row and vectors per CTA: one CTA a row where that gives every SM two rows, else enough
+// to do so, as long as a CTA has at least two vectors a thread.
+inline void row_split(RowArgs *a, int EB, int sms) {
     const long long vecs = (static_cast<long long>(a->V) * EB + 14) / 16 + 1;  // at the worst alignment
     int cs = 1;
-    while (cs < kMaxCluster && (vecs + cs - 1) / cs * 16 > 40 * 1024) cs *= 2;
-    while (cs < kMaxCluster && static_cast<long long>(a->B) * cs < 152 && vecs / cs > kThreads) cs *= 2;
+    while (cs < kMaxCluster && static_cast<long long>(a->B) * cs < 2 * sms && vecs / cs > 2 * kThreads) cs *= 2;
     a->cluster = cs;
     a->part = static_cast<int>((vecs + cs - 1) / cs);
-    if (fixed + static_cast<size_t>(a->part) * 16 > max_dyn)
-        return fail(SPEC_ERR_UNSUPPORTED, "V = %d: a row does not fit the shared memory of %d SMs", a->V, cs);
-    return SPEC_OK;
 }
 
 template <int EB, int OP>
 spec_status launch_rows(const RowArgs &a0, cudaStream_t stream) {
-    static_assert(sizeof(SelectShared) % 16 == 0, "the row follows in 16-byte vectors");
     RowArgs a = a0;
     DeviceInfo di;
     int dev = 0;
@@ -404,12 +611,11 @@ spec_status launch_rows(const RowArgs &a0, cudaStream_t stream) {
     auto kernel = row_kernel<EB, OP>;
     st = allow_max_dyn_smem(dev, reinterpret_cast<const void *>(kernel), &di);
     if (st != SPEC_OK) return st;
-    st = row_split(&a, EB, sizeof(SelectShared), di.max_dyn);
-    if (st != SPEC_OK) return st;
+    row_split(&a, EB, di.sms);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.cluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = sizeof(SelectShared) + static_cast<size_t>(a.part) * 16;
+    cfg.dynamicSmemBytes = sizeof(SelectShared);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -421,8 +627,7 @@ spec_status launch_rows(const RowArgs &a0, cudaStream_t stream) {
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess)
-        return fail(SPEC_ERR_CUDA, "row kernel launch (B=%d, cluster=%d, smem=%zu): %s", a.B, a.cluster, (size_t)cfg.dynamicSmemBytes,
-                    cudaGetErrorString(e));
+        return fail(SPEC_ERR_CUDA, "row kernel launch (B=%d, cluster=%d): %s", a.B, a.cluster, cudaGetErrorString(e));
     return SPEC_OK;
 }
 

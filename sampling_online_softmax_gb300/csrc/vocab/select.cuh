@@ -1,21 +1,22 @@
 // select.cuh -- rows of logits kept on the chip: filtered sampling and the
 // largest logits.
 //
-// One thread-block cluster per row.  The row's 16-byte vectors are dealt out to the
-// cluster's CTAs in contiguous parts, which stay in shared memory, so HBM is read
-// once however many passes the choice takes; what the CTAs have to know of one
-// another (maxima, sums, histograms) goes through distributed shared memory.
+// A row is read from HBM once: while it streams by, each thread keeps the maxima of
+// the groups that its vectors make (about 2048 groups a row) and, where a share of
+// the whole row's weight or the log-normaliser is wanted, a running exp-sum.
 //
-// The short way (Row::threshold, Row::collect, and the leader's list): the logits
-// are in about 2048 groups, a thread's own vectors, and the k-th largest of the
-// groups' maxima is at or below the k-th largest logit, while few logits more than
-// k lie at or above it (k groups hold them: 1.4 k of random logits at k = 1024, 1.03 k
-// at k = 64).  So two cluster barriers bring every candidate for the k largest into
-// one short list in the leader's shared memory, which sorts and weighs it alone.
-// Only the threads whose own maximum reaches the bound look at their logits again.
+// The short way: the k-th largest of the groups' maxima is at or below the k-th
+// largest logit, while few logits more than k lie at or above it (k groups hold
+// them all: 1.4 k of random logits at k = 1024, 1.03 k at k = 64).  Those k groups are
+// read again, from L2, into one short list of candidates, which one CTA sorts,
+// weighs and cuts alone.
 //
-// The long way (Row::reach, Row::locate), for rows of which thousands of tokens
-// are kept: exact histograms of the whole row.
+// The long way, for rows of which thousands of tokens are kept: passes over the
+// row in L2.  A histogram of counts brackets the cut, a second one narrows it,
+// and the few tokens left are sorted; see cut_row.
+//
+// Many rows: one CTA each, several to an SM, so that some stream while others
+// choose.  Few rows: a cluster shares a row through distributed shared memory.
 #pragma once
 
 #include "../ptx.cuh"
@@ -55,19 +56,21 @@ struct alignas(16) SelectShared {
         unsigned long long list[kMaxList];     // (~key << 32) | index
     };
     union {
-        uint32_t maxima[kGroups];              // keys of the groups' maxima, the whole row's
         unsigned long long cum[kMaxList];      // the leader's: running sums of the sorted list's weights
+        uint16_t hit[kGroups];                 // this CTA's groups that reach a bound
     };
+    uint32_t maxima[kGroups];                  // keys of the groups' maxima, the whole row's
     unsigned long long slot[2][kMaxCluster];
     unsigned long long seg[2][kMaxCluster * kWarps];
     uint32_t hits[2][kMaxCluster * kWarps];    // candidates of each warp of the cluster
     unsigned long long red[kWarps];
     unsigned long long above;                  // a crossing: what lies above its bin,
-    uint32_t cross_bin;                        // and the bin (kAll: none)
+    uint32_t cross_bin, cross_last;            // and the bin (kAll: none), or the last it may be in
     uint32_t list_n[2];
+    uint32_t hit_n;
     uint32_t tie_index;
+    uint32_t cut[2];                           // a cut's key and index
     uint32_t verdict;
-    unsigned long long W[2];                   // bounds of the row's weight
     uint32_t steps[kSteps];
     float2 pow2[kPow2Steps];
 };
@@ -91,18 +94,35 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// Pairs of floats in one instruction each.
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(unsigned long long p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 template <int EB>
 struct Row {
     using P = Part<EB>;
     static constexpr int kPer = P::kPer;
     static constexpr uint32_t kLowest = EB == 2 ? 0x0080u : 0x00800000u;  // the key of the lowest finite logit
     P part;
-    const uint4 *data;  // this CTA's part
-    int n;              // its vectors
+    int n;              // this CTA's vectors
     int tid, lane, warp;
     uint32_t rank, cs;
+    int per;            // groups per thread: a thread's vectors i = tid + r kThreads of equal r mod per
     int turn;           // which half of the exchange buffers comes next
-    float own_max;      // the largest of this thread's vectors (tid, tid + kThreads, ...)
     SelectShared *sh;
 
     static __device__ __forceinline__ uint32_t key(float l) { return EB == 2 ? order_key(l) >> 16 : order_key(l); }
@@ -111,20 +131,20 @@ struct Row {
     }
     static __device__ __forceinline__ void unpack(const uint4 &v, float (&l)[kPer]) { P::unpack(v, l); }
     __device__ __forceinline__ int index(int i, int q) const { return part.index(i, q); }
-
-    __device__ void start_load(const RowArgs &a, int b, uint4 *buf) {
-        part.place(a.base, a.end, a.V, b, rank, a.part);
-        n = part.n;
-        data = buf;
-        for (int i = tid; i < n; i += kThreads) part.copy(buf, i);
-        copies_commit();
+    // A barrier of all threads that work on the row.
+    __device__ __forceinline__ void sync() const {
+        if (cs == 1)
+            __syncthreads();
+        else
+            cluster_sync();
     }
-    // The largest logit of a vector, NaN if it holds one.
+
     static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
         uint32_t r;
         asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
     }
+    // The largest logit of a vector, NaN if it holds one.
     static __device__ __forceinline__ float vector_max(const uint4 &v) {
         if (EB == 2) {
             const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
@@ -132,26 +152,71 @@ struct Row {
         }
         return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
+    static __device__ __forceinline__ unsigned long long exp_pair(float a, float b, unsigned long long c2, unsigned long long q2) {
+        float x, y;
+        split(fma2(pair(a, b), c2, q2), x, y);
+        return pair(ptx::ex2(x), ptx::ex2(y));
+    }
+    static __device__ __forceinline__ unsigned long long vector_exp(const uint4 &v, unsigned long long c2, unsigned long long q2) {
+        float l[kPer];
+        unpack(v, l);
+        unsigned long long s = add2(exp_pair(l[0], l[1], c2, q2), exp_pair(l[2], l[3], c2, q2));
+        if (kPer == 8) s = add2(s, add2(exp_pair(l[4 % kPer], l[5 % kPer], c2, q2), exp_pair(l[6 % kPer], l[7 % kPer], c2, q2)));
+        return s;
+    }
 
-    // Waits for the part; then the largest logit of the row, NaN if there is one, and in
-    // sh->maxima, in every CTA, the keys of the groups' maxima.  A thread's vectors make
-    // kMaxCluster / cs groups, so that a row has kGroups of them.
-    __device__ float maximum(uint4 *buf) {
-        copies_wait<0>();
-        constexpr int kMost = kMaxCluster;
-        const int per = kMost / static_cast<int>(cs);  // groups per thread
-        float g[kMost];
+    // Reads the part; then the largest logit of the row (returned; NaN if there is one), the keys of
+    // the groups' maxima in sh->maxima of every CTA, and with SUM what exp_total() takes: a sum of
+    // 2^(l c - q) and its q for every warp.  q is a rounded maximum times c and counts as exact, so
+    // only l c - q (one fused operation) and ex2 round: a weight of size 2^-x is off by
+    // (x + 4) 2^-24 relative, and a row's sum, whose terms below 2^-16 weigh little each, by 2^-18.
+    template <bool SUM>
+    __device__ float stream(float c) {
+        constexpr int kBatch = 8;
+        static_assert(kBatch == kMaxCluster, "a batch's vectors are one of each group");
+        float g[kBatch];
 #pragma unroll
-        for (int j = 0; j < kMost; ++j) g[j] = -INFINITY;
-        for (int i0 = tid; i0 < n; i0 += kMost * kThreads) {
+        for (int j = 0; j < kBatch; ++j) g[j] = -INFINITY;
+        float top = -INFINITY, q = -INFINITY;
+        unsigned long long s = pair(0.f, 0.f);
+        const unsigned long long c2 = pair(c, c);
+        auto take = [&](const uint4(&v)[kBatch]) {
+            float m = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < kMost; ++j) {
-                const int i = i0 + j * kThreads;
-                if (i < n) {
-                    part.mend(buf, i);
-                    g[j] = max_nan(g[j], vector_max(buf[i]));
+            for (int j = 0; j < kBatch; ++j) {
+                const float x = vector_max(v[j]);
+                g[j] = max_nan(g[j], x);
+                if (SUM) m = fmaxf(m, x);
+            }
+            if (SUM) {
+                if (m > top) {
+                    const float f = ptx::ex2(q - m * c);
+                    s = fma2(s, pair(f, f), pair(0.f, 0.f));
+                    top = m;
+                    q = m * c;
+                }
+                if (top > -INFINITY) {
+                    const unsigned long long q2 = pair(-q, -q);
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) s = add2(s, vector_exp(v[j], c2, q2));
                 }
             }
+        };
+        for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
+            uint4 v[kBatch];
+            if (i0 > 0 && i0 + (kBatch - 1) * kThreads < n - 1) {
+                const uint4 *p = reinterpret_cast<const uint4 *>(part.at(i0));
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) v[j] = __ldg(p + j * kThreads);
+            } else {  // the row's first and last vectors may hold a neighbour's logits
+                const uint32_t none = EB == 2 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int i = i0 + j * kThreads;
+                    v[j] = i < n ? part.fetch(i) : make_uint4(none, none, none, none);
+                }
+            }
+            take(v);
         }
         if (per <= 4) {
 #pragma unroll
@@ -159,17 +224,28 @@ struct Row {
         }
         if (per <= 2) g[0] = max_nan(g[0], g[2]), g[1] = max_nan(g[1], g[3]);
         if (per <= 1) g[0] = max_nan(g[0], g[1]);
-        own_max = -INFINITY;
-        cluster_wait();  // the peers have started
+        unsigned long long warp_sums = 0;
+        if (SUM) {
+            float Q = q;
 #pragma unroll
-        for (int j = 0; j < kMost; ++j) {
+            for (int o = 16; o; o >>= 1) Q = fmaxf(Q, __shfl_xor_sync(kAll, Q, o));
+            float x, y;
+            split(s, x, y);
+            x = q > -INFINITY ? (x + y) * ptx::ex2(q - Q) : 0.f;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+            warp_sums = pair(Q, x);
+        }
+        if (cs > 1) cluster_wait();  // the peers have started
+        if (SUM && lane < static_cast<int>(cs)) st_peer(peer(&sh->seg[turn][rank * kWarps + warp], lane), warp_sums);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
             if (j < per) {
-                own_max = max_nan(own_max, g[j]);
                 const uint32_t k = order_key(g[j]);
                 for (uint32_t p = 0; p < cs; ++p) st_peer(peer(&sh->maxima[(rank * per + j) * kThreads + tid], p), k);
             }
         }
-        cluster_sync();
+        sync();
         uint32_t k = 0;
 #pragma unroll
         for (int j = 0; j < kKeysPerThread; ++j) k = max(k, sh->maxima[j * kThreads + tid]);
@@ -178,6 +254,44 @@ struct Row {
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) k = max(k, static_cast<uint32_t>(sh->red[w]));
+        return key_value(k);
+    }
+    // The row's sum of 2^(l c - *q) and its q, after stream<true>.
+    __device__ float exp_total(float *q) {
+        float Q = -INFINITY, s = 0.f, e[(kMaxCluster * kWarps + 31) / 32][2];
+#pragma unroll
+        for (int i = 0; i < (kMaxCluster * kWarps + 31) / 32; ++i) {
+            const uint32_t g = i * 32 + lane;
+            e[i][0] = -INFINITY;
+            e[i][1] = 0.f;
+            if (g < cs * kWarps) split(sh->seg[turn][g], e[i][0], e[i][1]);
+            Q = fmaxf(Q, e[i][0]);
+        }
+        turn ^= 1;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) Q = fmaxf(Q, __shfl_xor_sync(kAll, Q, o));
+#pragma unroll
+        for (int i = 0; i < (kMaxCluster * kWarps + 31) / 32; ++i)
+            if (e[i][0] > -INFINITY) s += e[i][1] * ptx::ex2(e[i][0] - Q);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+        *q = Q;
+        return s;
+    }
+    // The smallest of the groups' maxima that is finite (the row's largest if there is no other).
+    __device__ float least_maximum() {
+        uint32_t k = kAll;
+#pragma unroll
+        for (int j = 0; j < kKeysPerThread; ++j) {
+            const uint32_t x = sh->maxima[j * kThreads + tid];
+            if (x >= 0x00800000u) k = min(k, x);
+        }
+        k = __reduce_min_sync(kAll, k);
+        __syncthreads();
+        if (lane == 0) sh->red[warp] = k;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) k = min(k, static_cast<uint32_t>(sh->red[w]));
         return key_value(k);
     }
 
@@ -221,129 +335,174 @@ struct Row {
         return false;
     }
 
-    // sum of 2^((l - m) c) over the part, in fp32, posted by warp to every CTA in units of 2^-40;
-    // exp_total() after the caller's cluster barrier.  Off by less than 2^-16 relative: 2^-22 an
-    // ex2, its argument's rounding (3/2 of 2^-24 |x|, and what lies beyond |x| = 48 adds up to
-    // less than 2^-29), and sums of a dozen levels.
-    __device__ void exp_sum(float m, float c) {
-        float s = 0.f;
-        for (int i = tid; i < n; i += kThreads) {
-            float l[kPer];
-            unpack(data[i], l);
+    // f(vector, its number or -1) for every vector of the groups whose maximum reaches `low`, all
+    // threads at once, whole warps together.
+    template <class F>
+    __device__ void gather(float low, F f) {
+        const uint32_t bound = order_key(low);
+        __syncthreads();
+        if (tid == 0) sh->hit_n = 0;
+        __syncthreads();
+        for (int j = 0; j < per; ++j)
+            if (sh->maxima[(rank * per + j) * kThreads + tid] >= bound) sh->hit[atomicAdd(&sh->hit_n, 1u)] = static_cast<uint16_t>(j * kThreads + tid);
+        __syncthreads();
+        const int rounds = ((n + kThreads - 1) / kThreads + per - 1) / per;  // vectors of a group, at most
+        const int total = static_cast<int>(sh->hit_n) * rounds;
+        constexpr int kBatch = 4;
+        const uint32_t none = EB == 2 ? 0xff80ff80u : 0xff800000u;
+        for (int e0 = tid; e0 - lane < total; e0 += kBatch * kThreads) {
+            uint4 v[kBatch];
+            int at[kBatch];
 #pragma unroll
-            for (int q = 0; q < kPer; ++q) l[q] = ptx::ex2((l[q] - m) * c);
-#pragma unroll
-            for (int h = kPer / 2; h; h >>= 1)
-#pragma unroll
-                for (int q = 0; q < h; ++q) l[q] += l[q + h];
-            s += l[0];
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-        const unsigned long long v = __float2ull_rn(s * 0x1p40f);
-        if (lane < static_cast<int>(cs)) st_peer(peer(&sh->seg[turn][rank * kWarps + warp], lane), v);
-    }
-    __device__ unsigned long long exp_total() {
-        unsigned long long v = 0;
-        for (uint32_t i = lane; i < cs * kWarps; i += 32) v += sh->seg[turn][i];
-        turn ^= 1;
-        return warp_sum(v);
-    }
-
-    // Every logit >= low into the leader's list; what each warp found, into sh->hits of every
-    // CTA.  The caller's cluster barrier follows.
-    __device__ void collect(float low, int attempt) {
-        uint32_t c = 0;
-        unsigned long long h[2] = {0, 0};
-        auto entry = [&](float l, int x) {
-            return static_cast<unsigned long long>(~order_key(l)) << 32 | static_cast<uint32_t>(x);
-        };
-        const bool mine = own_max >= low;
-        if (__any_sync(kAll, mine)) {
-            if (mine) {
-                for (int i = tid; i < n; i += kThreads) {
-                    const uint4 v = data[i];
-                    if (!(vector_max(v) >= low)) continue;
-                    float l[kPer];
-                    unpack(v, l);
-#pragma unroll
-                    for (int q = 0; q < kPer; ++q) {
-                        if (l[q] >= low) {
-                            const unsigned long long e = entry(l[q], index(i, q));
-                            if (c == 0) h[0] = e;
-                            if (c == 1) h[1] = e;
-                            ++c;
-                        }
-                    }
+            for (int j = 0; j < kBatch; ++j) {
+                const int e = e0 + j * kThreads;
+                at[j] = -1;
+                v[j] = make_uint4(none, none, none, none);
+                if (e < total) {
+                    const int h = e / rounds, group = sh->hit[h];
+                    const int i = ((e - h * rounds) * per + group / kThreads) * kThreads + group % kThreads;
+                    if (i < n) at[j] = i, v[j] = part.fetch(i);
                 }
             }
-            __syncwarp();
-            uint32_t incl = c;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t x = __shfl_up_sync(kAll, incl, o);
-                if (lane >= o) incl += x;
-            }
-            const uint32_t total = __shfl_sync(kAll, incl, 31);
-            uint32_t base = 0;
-            if (lane == 0) base = atom_add_peer(peer(&sh->list_n[attempt], 0), total);
-            base = __shfl_sync(kAll, base, 0) + incl - c;
+            for (int j = 0; j < kBatch; ++j) f(v[j], at[j]);
+        }
+        __syncwarp();
+    }
+    static __device__ __forceinline__ unsigned long long entry(float l, int x) {
+        return static_cast<unsigned long long>(~order_key(l)) << 32 | static_cast<uint32_t>(x);
+    }
+    // Appends, for a whole warp, the logits of a vector that pass; returns how many the warp had.
+    template <class T>
+    __device__ uint32_t append(const uint4 &v, int at, int attempt, T pass) {
+        float l[kPer];
+        unpack(v, l);
+        uint32_t c = 0;
+        if (at >= 0) {
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) c += pass(l[q], index(at, q));
+        }
+        if (!__any_sync(kAll, c != 0)) return 0;
+        uint32_t incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(kAll, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const uint32_t total = __shfl_sync(kAll, incl, 31);
+        uint32_t base = 0;
+        if (lane == 0) base = cs == 1 ? atomicAdd(&sh->list_n[attempt], total) : atom_add_peer(peer(&sh->list_n[attempt], 0), total);
+        base = __shfl_sync(kAll, base, 0) + incl - c;
+        if (c) {
             const uint32_t list = peer(sh->list, 0);
-            if (c > 0 && base < kMaxList) st_peer(list + base * 8, h[0]);
-            if (c > 1 && base + 1 < kMaxList) st_peer(list + base * 8 + 8, h[1]);
-            if (c > 2) {
-                uint32_t at = 0;
-                for (int i = tid; i < n; i += kThreads) {
-                    const uint4 v = data[i];
-                    if (!(vector_max(v) >= low)) continue;
-                    float l[kPer];
-                    unpack(v, l);
 #pragma unroll
-                    for (int q = 0; q < kPer; ++q) {
-                        if (l[q] >= low) {
-                            if (at >= 2 && base + at < kMaxList) st_peer(list + (base + at) * 8, entry(l[q], index(i, q)));
-                            ++at;
-                        }
-                    }
+            for (int q = 0; q < kPer; ++q) {
+                if (pass(l[q], index(at, q))) {
+                    if (base < kMaxList) st_peer(list + base * 8, entry(l[q], index(at, q)));
+                    ++base;
                 }
             }
-            __syncwarp();
-            c = total;
         }
-        if (lane < static_cast<int>(cs)) st_peer(peer(&sh->hits[attempt][rank * kWarps + warp], lane), c);
+        __syncwarp();
+        return total;
     }
-    // After that barrier: how many there are.
-    __device__ uint32_t collected(int attempt) const {
+    // Every logit >= low into the leader's list; returns, after a barrier of the row, how many there are.
+    __device__ uint32_t collect(float low, int attempt) {
         uint32_t c = 0;
+        gather(low, [&](const uint4 &v, int at) {
+            if (__any_sync(kAll, vector_max(v) >= low)) c += append(v, at, attempt, [&](float l, int) { return l >= low; });
+        });
+        return collected(c, attempt);
+    }
+    __device__ uint32_t collected(uint32_t c, int attempt) {
+        if (lane < static_cast<int>(cs)) st_peer(peer(&sh->hits[attempt][rank * kWarps + warp], lane), c);
+        sync();
+        c = 0;
         for (uint32_t i = lane; i < cs * kWarps; i += 32) c += sh->hits[attempt][i];
         return __reduce_add_sync(kAll, c);
     }
 
-    // f(logit, index) for every logit of the part, a thread's own vectors.
+    // f(vector, its number or -1) for every vector of the part, a thread's own, whole warps together.
+    template <class F>
+    __device__ __forceinline__ void vectors(F f) const {
+        constexpr int kBatch = 4;
+        const uint32_t none = EB == 2 ? 0xff80ff80u : 0xff800000u;
+        for (int i0 = tid; i0 - lane < n; i0 += kBatch * kThreads) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const int i = i0 + j * kThreads;
+                v[j] = i < n ? part.fetch(i) : make_uint4(none, none, none, none);
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) f(v[j], i0 + j * kThreads < n ? i0 + j * kThreads : -1);
+        }
+    }
+    // f(logit, index) for every logit of the part.
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        for (int i = tid; i < n; i += kThreads) {
+        vectors([&](const uint4 &v, int i) {
+            if (i < 0) return;
             float l[kPer];
-            unpack(data[i], l);
+            unpack(v, l);
 #pragma unroll
             for (int q = 0; q < kPer; ++q) f(l[q], index(i, q));
-        }
+        });
     }
 
     // The sum of v over every thread of the cluster.
     __device__ unsigned long long sum(unsigned long long v) {
         v = warp_sum(v);
+        __syncthreads();
         if (lane == 0) sh->red[warp] = v;
         __syncthreads();
         if (warp == 0) {
             v = warp_sum(lane < kWarps ? sh->red[lane] : 0ull);
             if (lane < static_cast<int>(cs)) st_peer(peer(&sh->slot[turn][rank], lane), v);
         }
-        cluster_sync();
+        sync();
         v = 0;
         for (uint32_t r = 0; r < cs; ++r) v += sh->slot[turn][r];
         turn ^= 1;
         return v;
+    }
+
+    // The row's histogram: this thread's kBinsPerThread bins, summed over the CTAs.
+    template <bool COUNT>
+    __device__ __forceinline__ void bins(unsigned long long (&v)[kBinsPerThread]) const {
+#pragma unroll
+        for (int i = 0; i < kBinsPerThread; ++i) v[i] = 0;
+        for (uint32_t r = 0; r < cs; ++r) {
+            if (COUNT) {
+#pragma unroll
+                for (int h = 0; h < kBinsPerThread / 4; ++h) {
+                    const uint4 c = ld_peer4(peer(&sh->count[tid * kBinsPerThread + 4 * h], r));
+                    v[4 * h] += c.x, v[4 * h + 1] += c.y, v[4 * h + 2] += c.z, v[4 * h + 3] += c.w;
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < kBinsPerThread / 2; ++h) {
+                    const uint4 c = ld_peer4(peer(&sh->mass[tid * kBinsPerThread + 2 * h], r));
+                    v[2 * h] += c.x | static_cast<unsigned long long>(c.y) << 32;
+                    v[2 * h + 1] += c.z | static_cast<unsigned long long>(c.w) << 32;
+                }
+            }
+        }
+    }
+    // The block's running sum before this thread's v, and its whole sum.
+    __device__ __forceinline__ unsigned long long sum_before(unsigned long long v, unsigned long long *all = nullptr) const {
+        const unsigned long long incl = warp_scan(v, lane);
+        __syncthreads();
+        if (lane == 31) sh->red[warp] = incl;
+        __syncthreads();
+        unsigned long long run = incl - v, total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) run += sh->red[w];
+            total += sh->red[w];
+        }
+        if (all) *all = total;
+        return run;
     }
 
     // Where, in the order of falling keys, the running sum of weigh(logit, index) over the keys
@@ -374,32 +533,12 @@ struct Row {
                 else
                     atomicAdd(&sh->mass[(hi - k) >> s], w);
             });
-            cluster_sync();
-            unsigned long long v[kBinsPerThread] = {};
-            for (uint32_t r = 0; r < cs; ++r) {
-                if (COUNT) {
-#pragma unroll
-                    for (int h = 0; h < kBinsPerThread / 4; ++h) {
-                        const uint4 c = ld_peer4(peer(&sh->count[tid * kBinsPerThread + 4 * h], r));
-                        v[4 * h] += c.x, v[4 * h + 1] += c.y, v[4 * h + 2] += c.z, v[4 * h + 3] += c.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < kBinsPerThread / 2; ++h) {
-                        const uint4 c = ld_peer4(peer(&sh->mass[tid * kBinsPerThread + 2 * h], r));
-                        v[2 * h] += c.x | static_cast<unsigned long long>(c.y) << 32;
-                        v[2 * h + 1] += c.z | static_cast<unsigned long long>(c.w) << 32;
-                    }
-                }
-            }
-            unsigned long long mine = 0;
+            sync();
+            unsigned long long v[kBinsPerThread], mine = 0;
+            bins<COUNT>(v);
 #pragma unroll
             for (int i = 0; i < kBinsPerThread; ++i) mine += v[i];
-            const unsigned long long incl = warp_scan(mine, lane);
-            if (lane == 31) sh->red[warp] = incl;
-            __syncthreads();
-            unsigned long long run = over + incl - mine;
-            for (int w = 0; w < warp; ++w) run += sh->red[w];
+            unsigned long long run = over + sum_before(mine);
 #pragma unroll
             for (int i = 0; i < kBinsPerThread; ++i) {
                 if (run < target && run + v[i] >= target) {
@@ -408,7 +547,7 @@ struct Row {
                 }
                 run += v[i];
             }
-            cluster_sync();  // the crossing is known, and the peers have read this histogram
+            sync();  // the crossing is known, and the peers have read this histogram
             const uint32_t bin = sh->cross_bin;
             if (bin == kAll) return false;
             over = sh->above;
@@ -424,32 +563,47 @@ struct Row {
     }
 
     // The first index, in index order, at which the running sum of weigh(logit, index) reaches
-    // target: found(index) is called by the one thread of the cluster that holds it.
-    template <class F, class G>
-    __device__ void locate(unsigned long long target, F weigh, G found) {
-        const int per = (n + kWarps - 1) / kWarps;
-        const int s0 = min(n, warp * per), s1 = min(n, s0 + per);
+    // aim(the row's sum): found(index) is called by the one thread of the row that holds it.
+    template <class F, class A, class G>
+    __device__ void locate(F weigh, A aim, G found) {
+        const int run = (n + kWarps - 1) / kWarps;
+        const int s0 = min(n, warp * run), s1 = min(n, s0 + run);
         unsigned long long v = 0;
-        for (int i = s0 + lane; i < s1; i += 32) {
-            float l[kPer];
-            unpack(data[i], l);
+        constexpr int kBatch = 4;
+        for (int i0 = s0 + lane; i0 < s1; i0 += kBatch * 32) {
+            uint4 w[kBatch];
 #pragma unroll
-            for (int q = 0; q < kPer; ++q) v += weigh(l[q], index(i, q));
+            for (int j = 0; j < kBatch; ++j)
+                if (i0 + 32 * j < s1) w[j] = part.fetch(i0 + 32 * j);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (i0 + 32 * j >= s1) break;
+                float l[kPer];
+                unpack(w[j], l);
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) v += weigh(l[q], index(i0 + 32 * j, q));
+            }
         }
+        __syncwarp();
         v = warp_sum(v);
         const uint32_t me = rank * kWarps + warp;
         if (lane < static_cast<int>(cs)) st_peer(peer(&sh->seg[turn][me], lane), v);
-        cluster_sync();
-        unsigned long long before = 0;
-        for (uint32_t g = lane; g < me; g += 32) before += sh->seg[turn][g];
+        sync();
+        unsigned long long before = 0, total = 0;
+        for (uint32_t g = lane; g < cs * kWarps; g += 32) {
+            const unsigned long long x = sh->seg[turn][g];
+            total += x;
+            if (g < me) before += x;
+        }
         before = warp_sum(before);
         turn ^= 1;
+        const unsigned long long target = aim(warp_sum(total));
         if (before >= target || before + v < target) return;  // the whole warp
         for (int base = s0; base < s1; base += 32) {
             const int i = base + lane;
             float l[kPer];
             unsigned long long w[kPer], mine = 0;
-            if (i < s1) unpack(data[i], l);
+            if (i < s1) unpack(part.fetch(i), l);
 #pragma unroll
             for (int q = 0; q < kPer; ++q) {
                 w[q] = i < s1 ? weigh(l[q], index(i, q)) : 0ull;
@@ -459,11 +613,11 @@ struct Row {
             const uint32_t hit = __ballot_sync(kAll, incl >= target);
             if (hit) {
                 if (lane == __ffs(hit) - 1) {
-                    unsigned long long run = incl - mine;
+                    unsigned long long at = incl - mine;
 #pragma unroll
                     for (int q = 0; q < kPer; ++q) {
-                        if (run < target && run + w[q] >= target) found(index(i, q));
-                        run += w[q];
+                        if (at < target && at + w[q] >= target) found(index(i, q));
+                        at += w[q];
                     }
                 }
                 return;
@@ -475,22 +629,24 @@ struct Row {
     // The index of the r-th logit of key k, in index order, for every thread of the cluster.
     template <class P>
     __device__ int tie_index(uint32_t k, unsigned long long r, P also) {
-        locate(r, [&](float l, int x) { return static_cast<unsigned long long>(key(l) == k && also(l, x)); },
+        locate([&](float l, int x) { return static_cast<unsigned long long>(key(l) == k && also(l, x)); },
+               [&](unsigned long long) { return r; },
                [&](int x) {
                    for (uint32_t p = 0; p < cs; ++p) st_peer(peer(&sh->tie_index, p), static_cast<uint32_t>(x));
                });
-        cluster_sync();
+        sync();
         const int x = static_cast<int>(sh->tie_index);
-        cluster_sync();  // read everywhere before it is written again
+        sync();  // read everywhere before it is written again
         return x;
     }
 };
 
 // ---- the leader's list: one CTA, all its threads
 
-// Sum over the block of v; red is free again after the caller's next barrier.
+// Sum over the block of v.
 __device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long *red, int lane, int warp) {
     v = warp_sum(v);
+    __syncthreads();
     if (lane == 0) red[warp] = v;
     __syncthreads();
     v = 0;
@@ -536,21 +692,21 @@ __device__ inline void sort_list(unsigned long long *v, int n, int tid) {
 
 // A row's cluster: one CTA's part of it, and the row.
 template <int EB>
-__device__ __forceinline__ Row<EB> row_setup(const RowArgs &a, SelectShared *sh) {
-    const float2 pow2[kPow2Steps] = SPEC_POW2_TABLE;
+__device__ __forceinline__ Row<EB> row_setup(const RowArgs &a, SelectShared *sh, int b) {
+    static __constant__ const float2 pow2[kPow2Steps] = SPEC_POW2_TABLE;
     Row<EB> r;
     r.tid = threadIdx.x;
     r.lane = threadIdx.x & 31;
     r.warp = threadIdx.x >> 5;
-    r.rank = cluster_rank();
     r.cs = a.cluster;
+    r.rank = r.cs == 1 ? 0u : cluster_rank();
+    r.per = kMaxCluster / static_cast<int>(r.cs);
     r.turn = 0;
     r.sh = sh;
-    if (r.tid == 0) {
-#pragma unroll
-        for (int i = 0; i < kPow2Steps; ++i) sh->pow2[i] = pow2[i];
-        sh->list_n[0] = sh->list_n[1] = 0;
-    }
+    if (r.tid < kPow2Steps) sh->pow2[r.tid] = pow2[r.tid];
+    if (r.tid < 2) sh->list_n[r.tid] = 0;
+    r.part.place(a.base, a.end, a.V, b, static_cast<int>(r.rank), a.part);
+    r.n = r.part.n;
     return r;
 }
 

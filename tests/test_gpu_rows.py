@@ -232,3 +232,43 @@ def test_offsets_past_32_bits():
     v, i, _ = ref.top_logits(host(x[-1]), 3)
     assert np.array_equal(host(r["values"][-1]), v) and np.array_equal(r["ids"][-1].cpu().numpy(), i)
     assert (r["ids"][:-1].cpu() == torch.tensor([7, 0, 1], dtype=torch.int32)).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,V,T,k,p,mp", [
+    (5, 150001, 3.0, 0, 0.9, 0.0), (5, 150001, 3.0, 0, 1.0, 0.0), (3, 150001, 2.0, 20000, 0.6, 0.0), (3, 200000, 1.5, 3000, 1.0, 0.01),
+    (700, 4099, 2.0, 0, 0.95, 0.0), (700, 4099, 1.0, 0, 1.0, 0.02), (400, 9001, 5.0, 2000, 0.9, 0.0), (2, 70000, 1e6, 0, 0.5, 0.0),
+    (4, 60000, 0.05, 0, 0.999, 0.0), (4, 60000, 0.7, 1024, 0.99, 0.0), (4, 60000, 0.7, 1025, 0.99, 0.0)])
+def test_long_rows_of_which_many_tokens_are_kept(B, V, T, k, p, mp, dtype):
+    x = rows(B, V, dtype, 2.0, V + B)
+    u = torch.rand(B, generator=torch.Generator().manual_seed(B)).to(DEV)
+    check_sample(x, u, params(B, 0, T=(T,), k=(k,), p=(p,), mp=(mp,)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_few_unmasked_tokens_of_a_long_row(dtype):
+    B, V = 6, 90001
+    x = torch.full((B, V), float("-inf"), dtype=dtype, device=DEV)
+    g = torch.Generator().manual_seed(1)
+    for b, live in enumerate((1, 2, 40, 300, 1500, 5000)):
+        at = torch.randperm(V, generator=g)[:live].to(DEV)
+        x[b, at] = torch.randn(live, generator=g).to(dtype).to(DEV)
+    u = torch.rand(B, generator=g).to(DEV)
+    for q in (dict(), dict(k=(50,)), dict(p=(0.9,)), dict(mp=(0.3,)), dict(k=(1000,), p=(0.5,)), dict(k=(4000,), p=(0.5,))):
+        check_sample(x, u, params(B, 0, **q))
+    check_top(x, 100)
+    check_top(x, 1024)
+
+
+@pytest.mark.parametrize("scale", [1e30, 3e37, 1e-30])
+def test_magnitudes(scale):
+    """Logits whose products with log2(e) / T overflow, or are all but equal."""
+    x = rows(4, 5003, torch.float32, 1.0, 3) * scale
+    u = torch.tensor([0.1, 0.4, 0.7, 0.95], device=DEV)
+    for q in (dict(p=(0.9,), T=(0.01,)), dict(p=(0.9,), T=(1e-6,)), dict(mp=(0.1,), T=(0.5,)), dict(T=(1e6,)), dict(k=(10,), T=(1e6,), p=(0.7,))):
+        check_sample(x, u, params(4, 0, **q))
+    r = sv.spec_top_logits(x, 20, lse=True)
+    for b in range(4):
+        v, i, z = ref.top_logits(host(x[b]), 20)
+        assert np.array_equal(r["ids"][b].cpu().numpy(), i) and np.array_equal(host(r["values"][b]), v)
+        assert abs(float(r["lse"][b]) - z) <= 2.0 ** -20 + 2.0 ** -22 * abs(z)
