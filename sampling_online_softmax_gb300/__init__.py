@@ -27,6 +27,7 @@ Entry points (same names as the C ABI):
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -474,30 +475,75 @@ def spec_sample_rows(logits, u, temperature, *, status=None, out=None, workspace
     return out
 
 
-def _allocate(shapes, dev, s, stream):
-    """New outputs, from the memory of the stream that the kernel runs on."""
-    if stream is None:
-        return {n: torch.empty(shape, dtype=dtype, device=dev) for n, (shape, dtype) in shapes.items()}
-    with torch.cuda.stream(s):
-        return {n: torch.empty(shape, dtype=dtype, device=dev) for n, (shape, dtype) in shapes.items()}
+# The operators on rows of logits are short calls (a few microseconds on the device), so their checks
+# take the quick way first: one look at each tensor, and the named refusal only where it fails.
+def _need(t, name, dtype, shape, dev, index):
+    """`t` is on the device, contiguous, and of this type and shape; returns its address."""
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+        _cuda(t, name, dtype, dev)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
 
 
-def _record(tensors, dev, s, stream):
-    """Keep the memory of tensors that another stream owns until `stream` has used it."""
-    if stream is not None and s != torch.cuda.current_stream(dev):
+def _may(t, name, dtype, shape, dev, index):
+    return None if t is None else _need(t, name, dtype, shape, dev, index)
+
+
+def _logits_2d(t, name):
+    """Checks a matrix of logits; returns (rows, V, device, its index, dtype code)."""
+    if not (t.is_cuda and t.is_contiguous()):
+        _cuda(t, name)
+    if t.dim() != 2:
+        raise ValueError("%s must be [rows, V]" % name)
+    rows, V = t.shape
+    dev = t.device
+    return rows, V, dev, dev.index, _dtype_code(t)
+
+
+def _results(out, shapes, status, dev, index, stream):
+    """The outputs (new ones, from the memory of the stream that the kernel runs on, where `out` is
+    None) and the status word: returns (out, the addresses by shapes' order, status' address)."""
+    if out is None or status is None:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            if out is None:
+                out = {n: torch.empty(shape, dtype=dtype, device=dev) for n, (shape, dtype) in shapes.items()}
+            if status is None:
+                status = torch.zeros(1, dtype=torch.int32, device=dev)
+    at = []
+    for name, (shape, dtype) in shapes.items():
+        t = out.get(name)
+        if t is None:
+            raise ValueError("out[%r] is missing" % name)
+        at.append(_need(t, "out[%r]" % name, dtype, shape, dev, index))
+    if not (status.is_cuda and status.dtype is torch.int32 and status.get_device() == index and status.is_contiguous()):
+        _cuda(status, "status", torch.int32, dev)
+    if status.numel() < 1:
+        raise ValueError("status must hold at least one int32")
+    out["status"] = status
+    return out, at, status.data_ptr()
+
+
+def _raw_stream(index):
+    """The handle of the device's current stream (torch.cuda.current_stream, without the object: 2 us)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _launch(fn, args, tensors, dev, stream):
+    """Calls the library on `stream` (the device's current one where it is None), with the tensors'
+    device current; a stream that is not the current one keeps the tensors' memory until it is done."""
+    h = _raw_stream(dev.index) if stream is None else stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, h)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, h)
+    if st != SPEC_OK:
+        _check(st)
+    if stream is not None and stream != torch.cuda.current_stream(dev):
         for t in tensors:
             if t is not None:
-                t.record_stream(s)
-
-
-def _per_row(t, name, dtype, B, dev, required=False):
-    if t is None:
-        if required:
-            raise ValueError("%s is required" % name)
-        return
-    _cuda(t, name, dtype, dev)
-    if tuple(t.shape) != (B,):
-        raise ValueError("%s must be [%d], got %s" % (name, B, tuple(t.shape)))
+                t.record_stream(stream)
 
 
 def spec_sample_filtered(logits, u, temperature, *, top_k=None, top_p=None, min_p=None, status=None, out=None,
@@ -506,27 +552,15 @@ def spec_sample_filtered(logits, u, temperature, *, top_k=None, top_p=None, min_
     (int32; <= 0: no limit), top_p [B] and min_p [B] (float32), at u [B] (float32, in [0, 1)); a
     filter left None does not limit.  Returns dict(tokens [B], status)."""
     lib = load_library()
-    _cuda(logits, "logits")
-    if logits.dim() != 2:
-        raise ValueError("logits must be [B, V]")
-    B, V = logits.shape
-    dev = logits.device
-    code = _dtype_code(logits)
-    _per_row(u, "u", torch.float32, B, dev, True)
-    _per_row(temperature, "temperature", torch.float32, B, dev, True)
-    _per_row(top_k, "top_k", torch.int32, B, dev)
-    _per_row(top_p, "top_p", torch.float32, B, dev)
-    _per_row(min_p, "min_p", torch.float32, B, dev)
-    h, s = _stream_handle(dev, stream)
-    shapes = {"tokens": ((B,), torch.int32)}
-    out = _outputs(_allocate(shapes, dev, s, stream) if out is None else out, shapes, dev)
-    status = _status(status, dev, s)
-    out["status"] = status
-    with torch.cuda.device(dev):
-        st = lib.spec_sample_filtered(_ptr(logits), code, B, V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
-                                      _ptr(min_p), _ptr(u), _ptr(out["tokens"]), _ptr(status), h)
-    _check(st)
-    _record((logits, u, temperature, top_k, top_p, min_p, out["tokens"], status), dev, s, stream)
+    B, V, dev, i, code = _logits_2d(logits, "logits")
+    if u is None or temperature is None:
+        raise ValueError("u and temperature are required")
+    f32, row = torch.float32, (B,)
+    args = [_need(temperature, "temperature", f32, row, dev, i), _may(top_k, "top_k", torch.int32, row, dev, i),
+            _may(top_p, "top_p", f32, row, dev, i), _may(min_p, "min_p", f32, row, dev, i), _need(u, "u", f32, row, dev, i)]
+    out, (tokens,), st = _results(out, {"tokens": (row, torch.int32)}, status, dev, i, stream)
+    _launch(lib.spec_sample_filtered, (logits.data_ptr(), code, B, V, *args, tokens, st),
+            (logits, u, temperature, top_k, top_p, min_p, *out.values()), dev, stream)
     return out
 
 
@@ -536,50 +570,31 @@ def spec_top_logits(logits, k, *, temperature=1.0, lse=False, status=None, out=N
     lse [B] float32, the log-normaliser log sum exp(l / temperature).  Entries past a row's last
     unmasked token are (-inf, -1)."""
     lib = load_library()
-    _cuda(logits, "logits")
-    if logits.dim() != 2:
-        raise ValueError("logits must be [B, V]")
-    B, V = logits.shape
-    dev = logits.device
-    code = _dtype_code(logits)
+    B, V, dev, i, code = _logits_2d(logits, "logits")
     k = int(k)
     if k < 1:
         raise ValueError("k must be >= 1")
-    h, s = _stream_handle(dev, stream)
     shapes = {"values": ((B, k), torch.float32), "ids": ((B, k), torch.int32)}
     if lse:
         shapes["lse"] = ((B,), torch.float32)
-    out = _outputs(_allocate(shapes, dev, s, stream) if out is None else out, shapes, dev)
-    status = _status(status, dev, s)
-    out["status"] = status
-    with torch.cuda.device(dev):
-        st = lib.spec_top_logits(_ptr(logits), code, B, V, k, float(temperature), _ptr(out["values"]),
-                                 _ptr(out["ids"]), _ptr(out["lse"]) if lse else None, _ptr(status), h)
-    _check(st)
-    _record((logits, out["values"], out["ids"], out["lse"] if lse else None, status), dev, s, stream)
+    out, at, st = _results(out, shapes, status, dev, i, stream)
+    _launch(lib.spec_top_logits, (logits.data_ptr(), code, B, V, k, float(temperature), at[0], at[1], at[2] if lse else None, st),
+            (logits, *out.values()), dev, stream)
     return out
 
 
-def _distill_inputs(student, top_ids, top_logits, top_lse, row_weight):
-    """Check the inputs of a distillation; returns (N, V, K, device, dtype code)."""
-    _cuda(student, "student")
-    if student.dim() != 2:
-        raise ValueError("student must be [N, V]")
-    N, V = student.shape
-    dev = student.device
-    code = _dtype_code(student)
+def _distill_inputs(student, top_ids, top_logits, top_lse, row_weight, temperature):
+    """Checks the inputs of a distillation; returns (N, V, device, its index, the call's first arguments)."""
+    N, V, dev, i, code = _logits_2d(student, "student")
     if top_ids is None or top_logits is None:
         raise ValueError("top_ids and top_logits are required")
-    _cuda(top_ids, "top_ids", torch.int32, dev)
-    _cuda(top_logits, "top_logits", torch.float32, dev)
-    if top_ids.dim() != 2 or top_ids.shape[0] != N or top_ids.shape[1] < 1:
+    if top_ids.dim() != 2 or top_ids.shape[1] < 1:
         raise ValueError("top_ids must be [N, K]")
     K = top_ids.shape[1]
-    if tuple(top_logits.shape) != (N, K):
-        raise ValueError("top_logits must be [N, K] like top_ids")
-    _per_row(top_lse, "top_lse", torch.float32, N, dev)
-    _per_row(row_weight, "row_weight", torch.float32, N, dev)
-    return N, V, K, dev, code
+    f32 = torch.float32
+    return N, V, dev, i, (student.data_ptr(), code, N, V, _need(top_ids, "top_ids", torch.int32, (N, K), dev, i),
+                          _need(top_logits, "top_logits", f32, (N, K), dev, i), K, _may(top_lse, "top_lse", f32, (N,), dev, i),
+                          float(temperature), _may(row_weight, "row_weight", f32, (N,), dev, i))
 
 
 def spec_distill(student, top_ids, top_logits, temperature=1.0, *, top_lse=None, row_weight=None, grad=False,
@@ -593,21 +608,13 @@ def spec_distill(student, top_ids, top_logits, temperature=1.0, *, top_lse=None,
     No autograd graph is recorded: pass the gradient on with student.backward(r["grad"]), or keep
     stats for spec_distill_backward."""
     lib = load_library()
-    N, V, K, dev, code = _distill_inputs(student, top_ids, top_logits, top_lse, row_weight)
-    h, s = _stream_handle(dev, stream)
+    N, V, dev, i, args = _distill_inputs(student, top_ids, top_logits, top_lse, row_weight, temperature)
     shapes = {"loss": ((N,), torch.float32), "stats": ((N, 2), torch.float32)}
     if grad:
         shapes["grad"] = ((N, V), student.dtype)
-    out = _outputs(_allocate(shapes, dev, s, stream) if out is None else out, shapes, dev)
-    status = _status(status, dev, s)
-    out["status"] = status
-    g = out["grad"] if grad else None
-    with torch.cuda.device(dev):
-        st = lib.spec_distill(_ptr(student), code, N, V, _ptr(top_ids), _ptr(top_logits), K, _ptr(top_lse),
-                              float(temperature), _ptr(row_weight), _ptr(out["loss"]), _ptr(out["stats"]), _ptr(g),
-                              _ptr(status), h)
-    _check(st)
-    _record((student, top_ids, top_logits, top_lse, row_weight, out["loss"], out["stats"], g, status), dev, s, stream)
+    out, at, st = _results(out, shapes, status, dev, i, stream)
+    _launch(lib.spec_distill, (*args, at[0], at[1], at[2] if grad else None, st),
+            (student, top_ids, top_logits, top_lse, row_weight, *out.values()), dev, stream)
     return out
 
 
@@ -616,24 +623,15 @@ def spec_distill_backward(student, top_ids, top_logits, stats, grad_loss, temper
     """The gradient of sum(grad_loss * loss) with respect to student, from spec_distill's stats of
     the same inputs: returns dict(grad [N, V] in student's dtype, status).  out may be student."""
     lib = load_library()
-    N, V, K, dev, code = _distill_inputs(student, top_ids, top_logits, top_lse, row_weight)
-    if stats is None:
-        raise ValueError("stats is required")
-    _cuda(stats, "stats", torch.float32, dev)
-    if tuple(stats.shape) != (N, 2):
-        raise ValueError("stats must be [N, 2]")
-    _per_row(grad_loss, "grad_loss", torch.float32, N, dev, True)
-    h, s = _stream_handle(dev, stream)
-    shapes = {"grad": ((N, V), student.dtype)}
-    out = _outputs(_allocate(shapes, dev, s, stream) if out is None else dict(grad=out), shapes, dev)
-    status = _status(status, dev, s)
-    with torch.cuda.device(dev):
-        st = lib.spec_distill_backward(_ptr(student), code, N, V, _ptr(top_ids), _ptr(top_logits), K, _ptr(top_lse),
-                                       float(temperature), _ptr(row_weight), _ptr(stats), _ptr(grad_loss),
-                                       _ptr(out["grad"]), _ptr(status), h)
-    _check(st)
-    _record((student, top_ids, top_logits, top_lse, row_weight, stats, grad_loss, out["grad"], status), dev, s, stream)
-    return dict(grad=out["grad"], status=status)
+    N, V, dev, i, args = _distill_inputs(student, top_ids, top_logits, top_lse, row_weight, temperature)
+    if stats is None or grad_loss is None:
+        raise ValueError("stats and grad_loss are required")
+    f32 = torch.float32
+    more = (_need(stats, "stats", f32, (N, 2), dev, i), _need(grad_loss, "grad_loss", f32, (N,), dev, i))
+    r, (g,), st = _results(None if out is None else dict(grad=out), {"grad": ((N, V), student.dtype)}, status, dev, i, stream)
+    _launch(lib.spec_distill_backward, (*args, *more, g, st),
+            (student, top_ids, top_logits, top_lse, row_weight, stats, grad_loss, *r.values()), dev, stream)
+    return r
 
 
 def spec_tree_mask(parents, *, status=None, out=None, stream=None):

@@ -46,7 +46,7 @@ __device__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, const Request &q,
                                   int32_t *token) {
     SelectShared *sh = r.sh;
     const int tid = r.tid, lane = r.lane, warp = r.warp;
-    sort_list(sh->list, n, tid);
+    sort_list(sh->list, n, sh->scratch, sh->red, tid);
     int nk = q.k > 0 ? min(n, q.k) : n;
     auto value = [&](int i) { return key_value(~static_cast<uint32_t>(sh->list[i] >> 32)); };
     auto index = [&](int i) { return static_cast<uint32_t>(sh->list[i]); };
@@ -116,7 +116,7 @@ __device__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, const Request &q,
     // by index: (index << 32 | place in the order)
     __syncthreads();
     for (int i = tid; i < nk; i += kThreads) sh->list[i] = static_cast<unsigned long long>(index(i)) << 32 | static_cast<uint32_t>(i);
-    sort_list(sh->list, nk, tid);
+    sort_list(sh->list, nk, sh->maxima, sh->red, tid);  // (cum holds the weights; the maxima have served)
     const int pn = (nk + kThreads - 1) / kThreads;
     const int j0 = min(nk, tid * pn), j1 = min(nk, j0 + pn);
     unsigned long long s = 0;
@@ -292,29 +292,33 @@ __device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
     r.sync();
     uint32_t found = 0;
     unsigned long long between = 0;
-    r.vectors([&](const uint4 &vec, int i) {
-        auto pass = [&](float l, int x) {
-            if (!kept(l, x)) return false;
-            const float at = place(l);
-            const int y = inside(at) ? sub(at) : -1;
-            return y >= static_cast<int>(s0) && y <= static_cast<int>(s1);
-        };
-        if (!COUNT && i >= 0) {
-            float l[Row<EB>::kPer];
-            Row<EB>::unpack(vec, l);
+    r.vectors([&](const uint4(&vec)[Row<EB>::kBatch], int i0) {
+        constexpr int kPer = Row<EB>::kPer;
+        unsigned long long bits = 0;
+#pragma unroll 1
+        for (int j = 0; j < Row<EB>::kBatch; ++j) {
+            const uint4 w = j == 0 ? vec[0] : j == 1 ? vec[1] : j == 2 ? vec[2] : vec[3];
+            float l[kPer];
+            Row<EB>::unpack(w, l);
 #pragma unroll
-            for (int q = 0; q < Row<EB>::kPer; ++q) {
-                const float at = place(l[q]);
-                if (inside(at) && sub(at) < static_cast<int>(s0) && kept(l[q], r.index(i, q))) between += fixed_weight(l[q], sc, pow2);
+            for (int e = 0; e < kPer; ++e) {
+                const float at = place(l[e]);
+                if (!inside(at) || !kept(l[e], r.index(i0 + j * kThreads, e))) continue;
+                const int y = sub(at);
+                if (y < static_cast<int>(s0)) {
+                    if (!COUNT) between += fixed_weight(l[e], sc, pow2);
+                } else if (y <= static_cast<int>(s1)) {
+                    bits |= 1ull << (j * kPer + e);
+                }
             }
         }
-        found += r.append(vec, i, 1, pass);
+        found += r.append(bits, 1, [&](int j) { return i0 + j * kThreads; });
     });
     if (!COUNT) A += r.sum(between);
     const uint32_t n = r.collected(found, 1);
     if (n <= kMaxList) {
         if (r.rank == 0) {
-            sort_list(sh->list, n, tid);
+            sort_list(sh->list, n, sh->scratch, sh->red, tid);
             const int per = (n + kThreads - 1) / kThreads;
             const int i0 = min(static_cast<int>(n), tid * per), i1 = min(static_cast<int>(n), i0 + per);
             auto weigh = [&](int i) {
@@ -415,7 +419,7 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
         sc.cl = (fmaf(-sc.ch, T, kH) + kL) / T;
     }
     const bool share = q.p < 1.f && q.k == 0;  // top-p is a share of the whole row
-    const bool sums = share && a.V > kMaxList && !one;
+    const bool sums = share && a.V > kWhole && !one;
     sc.m = sums ? r.template stream<true>(sc.ch) : r.template stream<false>(sc.ch);
     if (!(fabsf(sc.m) < INFINITY)) {  // NaN, +inf, or nothing but -inf
         if (r.rank == 0 && r.tid == 0) {
@@ -426,13 +430,12 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
     }
     if (one) {  // the lowest index of the maximum: each warp's first, to the leader
         uint32_t x = kAll;
-        r.gather(sc.m, [&](const uint4 &v, int i) {
-            if (i < 0) return;
-            float l[Row<EB>::kPer];
-            Row<EB>::unpack(v, l);
+        r.gather(sc.m, [&](const uint4(&v)[Row<EB>::kGather], auto number) {
 #pragma unroll
-            for (int e = 0; e < Row<EB>::kPer; ++e)
-                if (l[e] == sc.m) x = min(x, static_cast<uint32_t>(r.index(i, e)));
+            for (int j = 0; j < Row<EB>::kGather; ++j) {
+                const uint32_t m = Row<EB>::reaching(v[j], sc.m);
+                if (m) x = min(x, static_cast<uint32_t>(r.index(number(j), __ffs(m) - 1)));
+            }
         });
         x = __reduce_min_sync(kAll, x);
         if (r.lane == 0) st_peer(peer(&sh->hits[0][r.rank * kWarps + r.warp], 0), x);
@@ -448,10 +451,10 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
     if (q.min_p > 0.f) q.least = share_of(1ull << sc.U, q.min_p);
 
     // The short way: the list holds the logits from `low` on; all: that is every token.
-    float low[2] = {-FLT_MAX, -FLT_MAX};
-    bool all[2] = {true, true};
+    float low = -FLT_MAX;
+    bool all = true;
     unsigned long long W0 = 0, W1 = 0;
-    if (a.V > kMaxList) {
+    if (a.V > kWhole) {
         if (sums) {  // bounds of the row's weight, 2^-18 apart to either side
             float Q, s = r.exp_total(&Q);
             s *= ptx::ex2(fmaf(-sc.m, sc.ch, Q));
@@ -465,18 +468,19 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
             return;
         }
         if (q.k > 0 || share) {  // too few groups for it: few tokens that are not masked
-            all[0] = !r.threshold(sc.m, q.k > 0 ? q.k : kFirstGoal, &low[0]);
-            if (share && !all[0]) all[1] = !r.threshold(sc.m, kMaxGoal, &low[1]);
+            all = !r.threshold(sc.m, q.k > 0 ? q.k : kFirstGoal, &low);
         } else {  // from a little below what min-p asks for
             const float x = log2f(q.min_p) / sc.ch;
-            low[0] = sc.m + x - (fabsf(x) + fabsf(sc.m)) * 0x1p-18f;
-            all[0] = false;
+            low = sc.m + x - (fabsf(x) + fabsf(sc.m)) * 0x1p-18f;
+            all = false;
         }
     }
     for (int attempt = 0; attempt < (sums ? 2 : 1); ++attempt) {
-        const uint32_t n = r.collect(low[attempt], attempt);
+        if (attempt == 1) all = !r.threshold(sc.m, kMaxGoal, &low);
+        if (all) low = -FLT_MAX;
+        const uint32_t n = r.collect(low, attempt);
         if (n > kMaxList) break;
-        if (!share || all[attempt]) {
+        if (!share || all) {
             if (r.rank == 0) draw_from_list(r, sc, q, n, 0ull, 0ull, a.tokens + b);
             return;
         }
@@ -492,7 +496,7 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
             unsigned long long w = 0;
             if (weighed == 0) {  // the list's weights are exact: the error is the rest's alone
                 float rest = 0.f;
-                r.each([&](float l, int) { rest += l >= low[attempt] ? 0.f : ptx::ex2((l - sc.m) * sc.ch); });
+                r.each([&](float l, int) { rest += l >= low ? 0.f : ptx::ex2((l - sc.m) * sc.ch); });
                 w = r.sum(__float2ull_rn(rest * 0x1p40f)) << (sc.U - 40);
                 if (r.rank == 0) {  // (the leader alone draws)
                     const unsigned long long listed = sh->cum[n - 1];
@@ -546,7 +550,7 @@ __device__ void top_row(const RowArgs &a, Row<EB> &r, int b) {
     uint32_t n = 0;
     if (!empty) {
         float low = -FLT_MAX;
-        if (a.V > kMaxList && !r.threshold(m, a.K, &low)) low = -FLT_MAX;  // few tokens that are not masked
+        if (a.V > kWhole && !r.threshold(m, a.K, &low)) low = -FLT_MAX;  // few tokens that are not masked
         n = r.collect(low, 0);
     }
     if (n > kMaxList) {  // equal logits in their thousands
@@ -558,16 +562,25 @@ __device__ void top_row(const RowArgs &a, Row<EB> &r, int b) {
             cut.key = at;
         }
         uint32_t found = 0;
-        r.vectors([&](const uint4 &v, int i) {
-            found += r.append(v, i, 1, [&](float l, int x) {
-                const uint32_t y = Row<EB>::key(l);
-                return y > cut.key || (y == cut.key && x <= cut.index);
-            });
+        r.vectors([&](const uint4(&v)[Row<EB>::kBatch], int i0) {
+            constexpr int kPer = Row<EB>::kPer;
+            unsigned long long bits = 0;
+#pragma unroll
+            for (int j = 0; j < Row<EB>::kBatch; ++j) {
+                float l[kPer];
+                Row<EB>::unpack(v[j], l);
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    const uint32_t y = Row<EB>::key(l[e]);
+                    if (y > cut.key || (y == cut.key && r.index(i0 + j * kThreads, e) <= cut.index)) bits |= 1ull << (j * kPer + e);
+                }
+            }
+            found += r.append(bits, 1, [&](int j) { return i0 + j * kThreads; });
         });
         n = r.collected(found, 1);
     }
     if (r.rank != 0) return;
-    sort_list(sh->list, n, r.tid);
+    sort_list(sh->list, n, sh->scratch, sh->red, r.tid);
     for (int i = r.tid; i < a.K; i += kThreads) {
         const unsigned long long e = i < n ? sh->list[i] : 0ull;
         a.values[out + i] = i < n ? key_value(~static_cast<uint32_t>(e >> 32)) : -INFINITY;

@@ -33,7 +33,8 @@ constexpr int kBins = 1 << kBinBits;
 constexpr int kBinsPerThread = kBins / kThreads;
 constexpr int kGroups = kMaxCluster * kThreads;  // groups of a row's logits, whatever the cluster's size
 constexpr int kKeysPerThread = kGroups / kThreads;
-constexpr int kFirstGoal = 128;                  // candidates asked for at first where top-p alone limits,
+constexpr int kWhole = 128;                      // rows up to this long are listed whole
+constexpr int kFirstGoal = 96;                   // candidates asked for at first where top-p alone limits,
 constexpr int kMaxGoal = 1024;                   // and at most
 constexpr int kSteps = kThreads;                 // bins of the groups' maxima
 constexpr uint32_t kAll = 0xffffffffu;
@@ -58,6 +59,7 @@ struct alignas(16) SelectShared {
     union {
         unsigned long long cum[kMaxList];      // the leader's: running sums of the sorted list's weights
         uint16_t hit[kGroups];                 // this CTA's groups that reach a bound
+        uint32_t scratch[kBins];               // sort_list's
     };
     uint32_t maxima[kGroups];                  // keys of the groups' maxima, the whole row's
     unsigned long long slot[2][kMaxCluster];
@@ -123,6 +125,7 @@ struct Row {
     uint32_t rank, cs;
     int per;            // groups per thread: a thread's vectors i = tid + r kThreads of equal r mod per
     int turn;           // which half of the exchange buffers comes next
+    bool used;          // sh->steps has been
     SelectShared *sh;
 
     static __device__ __forceinline__ uint32_t key(float l) { return EB == 2 ? order_key(l) >> 16 : order_key(l); }
@@ -301,10 +304,13 @@ struct Row {
     __device__ bool threshold(float m, uint32_t goal, float *at) {
         const uint32_t top = order_key(m) >> 16;
         for (int s = 0; s <= 8; s += 4) {
-            __syncthreads();
-            sh->steps[tid] = 0;
-            if (tid == 0) sh->cross_bin = kAll;
-            __syncthreads();
+            if (used) {  // (the first time: cleared by row_setup)
+                __syncthreads();
+                sh->steps[tid] = 0;
+                if (tid == 0) sh->cross_bin = kAll;
+                __syncthreads();
+            }
+            used = true;
 #pragma unroll
             for (int j = 0; j < kKeysPerThread; ++j) {
                 const uint32_t k = sh->maxima[j * kThreads + tid];
@@ -335,12 +341,16 @@ struct Row {
         return false;
     }
 
-    // f(vector, its number or -1) for every vector of the groups whose maximum reaches `low`, all
-    // threads at once, whole warps together.
+    static __device__ __forceinline__ uint4 nothing() {
+        const uint32_t w = EB == 2 ? 0xff80ff80u : 0xff800000u;
+        return make_uint4(w, w, w, w);
+    }
+    // f(vectors, number) for the vectors of the groups whose maximum reaches `low`, spread over all
+    // threads, kGather at a time, whole warps together; number(j) is vector j's (-1: none).
+    static constexpr int kGather = 8;
     template <class F>
     __device__ void gather(float low, F f) {
         const uint32_t bound = order_key(low);
-        __syncthreads();
         if (tid == 0) sh->hit_n = 0;
         __syncthreads();
         for (int j = 0; j < per; ++j)
@@ -348,41 +358,44 @@ struct Row {
         __syncthreads();
         const int rounds = ((n + kThreads - 1) / kThreads + per - 1) / per;  // vectors of a group, at most
         const int total = static_cast<int>(sh->hit_n) * rounds;
-        constexpr int kBatch = 4;
-        const uint32_t none = EB == 2 ? 0xff80ff80u : 0xff800000u;
-        for (int e0 = tid; e0 - lane < total; e0 += kBatch * kThreads) {
-            uint4 v[kBatch];
-            int at[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
+        for (int e0 = tid; e0 - lane < total; e0 += kGather * kThreads) {
+            auto number = [&](int j) {
                 const int e = e0 + j * kThreads;
-                at[j] = -1;
-                v[j] = make_uint4(none, none, none, none);
-                if (e < total) {
-                    const int h = e / rounds, group = sh->hit[h];
-                    const int i = ((e - h * rounds) * per + group / kThreads) * kThreads + group % kThreads;
-                    if (i < n) at[j] = i, v[j] = part.fetch(i);
-                }
-            }
+                if (e >= total) return -1;
+                const int h = e / rounds, group = sh->hit[h];
+                const int i = ((e - h * rounds) * per + group / kThreads) * kThreads + group % kThreads;
+                return i < n ? i : -1;
+            };
+            uint4 v[kGather];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) f(v[j], at[j]);
+            for (int j = 0; j < kGather; ++j) {
+                const int i = number(j);
+                v[j] = nothing();
+                if (i >= 0) v[j] = part.fetch(i);
+            }
+            f(v, number);
         }
         __syncwarp();
+    }
+    // One bit for each logit of a vector that is at least `low`.
+    static __device__ __forceinline__ uint32_t reaching(const uint4 &v, float low) {
+        if (!(vector_max(v) >= low)) return 0;
+        float l[kPer];
+        unpack(v, l);
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) m |= static_cast<uint32_t>(l[q] >= low) << q;
+        return m;
     }
     static __device__ __forceinline__ unsigned long long entry(float l, int x) {
         return static_cast<unsigned long long>(~order_key(l)) << 32 | static_cast<uint32_t>(x);
     }
-    // Appends, for a whole warp, the logits of a vector that pass; returns how many the warp had.
-    template <class T>
-    __device__ uint32_t append(const uint4 &v, int at, int attempt, T pass) {
-        float l[kPer];
-        unpack(v, l);
-        uint32_t c = 0;
-        if (at >= 0) {
-#pragma unroll
-            for (int q = 0; q < kPer; ++q) c += pass(l[q], index(at, q));
-        }
-        if (!__any_sync(kAll, c != 0)) return 0;
+    // Appends to the leader's list, for a whole warp, the logits of the bits (bit j * kPer + q: element q
+    // of vector number(j)); returns how many the warp had.
+    template <class N>
+    __device__ uint32_t append(unsigned long long bits, int attempt, N number) {
+        if (!__any_sync(kAll, bits != 0)) return 0;
+        const uint32_t c = __popcll(bits);
         uint32_t incl = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -393,15 +406,10 @@ struct Row {
         uint32_t base = 0;
         if (lane == 0) base = cs == 1 ? atomicAdd(&sh->list_n[attempt], total) : atom_add_peer(peer(&sh->list_n[attempt], 0), total);
         base = __shfl_sync(kAll, base, 0) + incl - c;
-        if (c) {
-            const uint32_t list = peer(sh->list, 0);
-#pragma unroll
-            for (int q = 0; q < kPer; ++q) {
-                if (pass(l[q], index(at, q))) {
-                    if (base < kMaxList) st_peer(list + base * 8, entry(l[q], index(at, q)));
-                    ++base;
-                }
-            }
+        const uint32_t list = peer(sh->list, 0);
+        for (; bits; bits &= bits - 1, ++base) {
+            const int e = __ffsll(bits) - 1, i = number(e / kPer);
+            if (base < kMaxList) st_peer(list + base * 8, entry(P::logit(part.at(i), e % kPer), index(i, e % kPer)));
         }
         __syncwarp();
         return total;
@@ -409,8 +417,11 @@ struct Row {
     // Every logit >= low into the leader's list; returns, after a barrier of the row, how many there are.
     __device__ uint32_t collect(float low, int attempt) {
         uint32_t c = 0;
-        gather(low, [&](const uint4 &v, int at) {
-            if (__any_sync(kAll, vector_max(v) >= low)) c += append(v, at, attempt, [&](float l, int) { return l >= low; });
+        gather(low, [&](const uint4(&v)[kGather], auto number) {
+            unsigned long long bits = 0;
+#pragma unroll
+            for (int j = 0; j < kGather; ++j) bits |= static_cast<unsigned long long>(reaching(v[j], low)) << (j * kPer);
+            c += append(bits, attempt, number);
         });
         return collected(c, attempt);
     }
@@ -422,31 +433,35 @@ struct Row {
         return __reduce_add_sync(kAll, c);
     }
 
-    // f(vector, its number or -1) for every vector of the part, a thread's own, whole warps together.
+    // f(vectors, the first's number) for the vectors of the part, a thread's own (i, i + kThreads,
+    // ...; -inf beyond the last), kBatch at a time, whole warps together.
+    static constexpr int kBatch = 4;
     template <class F>
     __device__ __forceinline__ void vectors(F f) const {
-        constexpr int kBatch = 4;
-        const uint32_t none = EB == 2 ? 0xff80ff80u : 0xff800000u;
         for (int i0 = tid; i0 - lane < n; i0 += kBatch * kThreads) {
             uint4 v[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 const int i = i0 + j * kThreads;
-                v[j] = i < n ? part.fetch(i) : make_uint4(none, none, none, none);
+                v[j] = nothing();
+                if (i < n) v[j] = part.fetch(i);
             }
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) f(v[j], i0 + j * kThreads < n ? i0 + j * kThreads : -1);
+            f(v, i0);
         }
+        __syncwarp();
     }
-    // f(logit, index) for every logit of the part.
+    // f(logit, index) for every logit of the part (and for some -inf of no index).
     template <class F>
     __device__ __forceinline__ void each(F f) const {
-        vectors([&](const uint4 &v, int i) {
-            if (i < 0) return;
-            float l[kPer];
-            unpack(v, l);
+        vectors([&](const uint4(&v)[kBatch], int i0) {
+#pragma unroll 1
+            for (int j = 0; j < kBatch; ++j) {
+                const uint4 w = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
+                float l[kPer];
+                unpack(w, l);
 #pragma unroll
-            for (int q = 0; q < kPer; ++q) f(l[q], index(i, q));
+                for (int q = 0; q < kPer; ++q) f(l[q], index(i0 + j * kThreads, q));
+            }
         });
     }
 
@@ -656,8 +671,10 @@ __device__ __forceinline__ unsigned long long block_sum(unsigned long long v, un
 }
 
 // Sorts n distinct entries ascending.  Up to 128: each entry's rank is counted (2 to 8 threads an
-// entry); above: a bitonic network over the next power of two.  (list holds room for it.)
-__device__ inline void sort_list(unsigned long long *v, int n, int tid) {
+// entry).  Above: by 2048 equal steps of the upper halves' range, each entry then counts its rank in
+// its own bin; a bitonic network where a bin holds too many for that (equal logits in their hundreds).
+// `scratch` holds kBins counts.
+__device__ inline void sort_list(unsigned long long *v, int n, uint32_t *scratch, unsigned long long *red, int tid) {
     __syncthreads();
     if (n <= kThreads / 2) {
         const int each = n <= kThreads / 8 ? 8 : n <= kThreads / 4 ? 4 : 2;
@@ -668,6 +685,83 @@ __device__ inline void sort_list(unsigned long long *v, int n, int tid) {
         for (int o = 1; o < each; o <<= 1) rank += __shfl_xor_sync(kAll, rank, o);
         __syncthreads();
         if (i < n && (tid & (each - 1)) == 0) v[rank] = e;
+        __syncthreads();
+        return;
+    }
+    constexpr int kEach = kMaxList / kThreads;
+    const int lane = tid & 31, warp = tid >> 5;
+    unsigned long long e[kEach];
+    uint32_t least = kAll, most = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int i = tid + j * kThreads;
+        e[j] = i < n ? v[i] : 0ull;
+        if (i < n) {
+            least = min(least, static_cast<uint32_t>(e[j] >> 32));
+            most = max(most, static_cast<uint32_t>(e[j] >> 32));
+        }
+        scratch[i] = 0;
+    }
+    least = __reduce_min_sync(kAll, least);
+    most = __reduce_max_sync(kAll, most);
+    if (lane == 0) red[warp] = static_cast<unsigned long long>(least) << 32 | most;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        least = min(least, static_cast<uint32_t>(red[w] >> 32));
+        most = max(most, static_cast<uint32_t>(red[w]));
+    }
+    const float scale = 2047.f / fmaxf(static_cast<float>(most - least), 1.f);
+    auto bin = [&](unsigned long long x) {
+        return min(kBins - 1, static_cast<int>(static_cast<float>(static_cast<uint32_t>(x >> 32) - least) * scale));
+    };
+    uint32_t at[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+        if (tid + j * kThreads < n) at[j] = atomicAdd(&scratch[bin(e[j])], 1u);
+    __syncthreads();
+    uint32_t own[kBinsPerThread], sum = 0, large = 0;
+#pragma unroll
+    for (int j = 0; j < kBinsPerThread; ++j) {
+        own[j] = scratch[tid * kBinsPerThread + j];
+        sum += own[j];
+        large = max(large, own[j]);
+    }
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += x;
+    }
+    large = __syncthreads_or(large > 192);
+    if (lane == 31) red[warp] = incl;
+    __syncthreads();
+    uint32_t run = incl - sum;
+    for (int w = 0; w < warp; ++w) run += static_cast<uint32_t>(red[w]);
+    if (!large) {
+#pragma unroll
+        for (int j = 0; j < kBinsPerThread; ++j) {
+            scratch[tid * kBinsPerThread + j] = run;
+            run += own[j];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+            if (tid + j * kThreads < n) v[scratch[bin(e[j])] + at[j]] = e[j];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            if (tid + j * kThreads >= n) continue;
+            const int b = bin(e[j]);
+            const uint32_t from = scratch[b], upto = b + 1 < kBins ? scratch[b + 1] : static_cast<uint32_t>(n);
+            uint32_t rank = from;
+            for (uint32_t i = from; i < upto; ++i) rank += v[i] < e[j];
+            at[j] = rank;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+            if (tid + j * kThreads < n) v[at[j]] = e[j];
         __syncthreads();
         return;
     }
@@ -702,7 +796,10 @@ __device__ __forceinline__ Row<EB> row_setup(const RowArgs &a, SelectShared *sh,
     r.rank = r.cs == 1 ? 0u : cluster_rank();
     r.per = kMaxCluster / static_cast<int>(r.cs);
     r.turn = 0;
+    r.used = false;
     r.sh = sh;
+    sh->steps[r.tid] = 0;
+    if (r.tid == 0) sh->cross_bin = kAll;
     if (r.tid < kPow2Steps) sh->pow2[r.tid] = pow2[r.tid];
     if (r.tid < 2) sh->list_n[r.tid] = 0;
     r.part.place(a.base, a.end, a.V, b, static_cast<int>(r.rank), a.part);

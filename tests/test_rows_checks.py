@@ -85,8 +85,8 @@ def fake(monkeypatch):
 
     monkeypatch.setattr(sv, "load_library", lambda: lib)
     monkeypatch.setattr(sv, "_cuda", lambda t, *a: t if t is None or real(OnGpu(t), *a) is None else t)
-    monkeypatch.setattr(sv, "_stream_handle", lambda dev, stream: (ctypes.c_void_p(0), None))
-    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(sv, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)  # a CPU device's index
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     return calls
 
