@@ -151,10 +151,8 @@ __device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
     const float2 *pow2 = sh->pow2;
     const int tid = r.tid;
     const Cut had = *cut;
-    auto kept = [&](float l, int x) {
-        const uint32_t y = Row<EB>::key(l);
-        return y > had.key || (y == had.key && x <= had.index);
-    };
+    const float floor = Row<EB>::value(had.key);
+    auto kept = [&](float l, int x) { return l > floor || (l == floor && x <= had.index); };
     // 48 steps of two hold every weight that counts; narrower rows get finer bins
     const float span = fminf(48.f / sc.ch, 2.f * (sc.m - r.least_maximum()));
     const float scale = (kBins - 1) / fmaxf(span, 1e-30f);
@@ -237,8 +235,7 @@ __device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
         if (inside(at)) atomicAdd(&sh->count[sub(at)], 1u);
     });
     if (!COUNT) {
-        W = r.sum(W);
-        A = r.sum(A);
+        r.sum2(W, A);
         target = share_of(W, p);
     } else {
         r.sync();
@@ -365,10 +362,8 @@ __device__ void draw_from_row(Row<EB> &r, const Scale &sc, const Request &q, int
     Cut cut = {Row<EB>::kLowest, INT_MAX};
     if (q.k > 0) cut_row<true>(r, sc, q.k, 1.f, &cut);
     if (q.p < 1.f) cut_row<false>(r, sc, 0, q.p, &cut);
-    auto kept = [&](float l, int x) {
-        const uint32_t y = Row<EB>::key(l);
-        return y > cut.key || (y == cut.key && x <= cut.index);
-    };
+    const float floor = Row<EB>::value(cut.key);
+    auto kept = [&](float l, int x) { return l > floor || (l == floor && x <= cut.index); };
     if (q.u == 0.f) {
         r.locate([&](float l, int x) { return static_cast<unsigned long long>(kept(l, x) && drawn_at_zero(l, sc, q.min_p)); },
                  [](unsigned long long) { return 1ull; }, [&](int x) { *token = x; });
@@ -476,7 +471,13 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
         }
     }
     for (int attempt = 0; attempt < (sums ? 2 : 1); ++attempt) {
-        if (attempt == 1) all = !r.threshold(sc.m, kMaxGoal, &low);
+        // a list of the largest n logits weighs at most n, and about what its groups' maxima do
+        const float need = sums ? q.p * static_cast<float>(W0) * exp2f(static_cast<float>(-sc.U)) : 0.f;
+        if (sums && need > (attempt ? static_cast<float>(kMaxList) : 2.f * kFirstGoal)) continue;
+        if (attempt == 1) {
+            all = !r.threshold(sc.m, kMaxGoal, &low);
+            if (!all && 2.f * r.weight_of_maxima(sc.m, sc.ch, low) < need) break;
+        }
         if (all) low = -FLT_MAX;
         const uint32_t n = r.collect(low, attempt);
         if (n > kMaxList) break;

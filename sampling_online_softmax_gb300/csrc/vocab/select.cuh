@@ -34,7 +34,7 @@ constexpr int kBinsPerThread = kBins / kThreads;
 constexpr int kGroups = kMaxCluster * kThreads;  // groups of a row's logits, whatever the cluster's size
 constexpr int kKeysPerThread = kGroups / kThreads;
 constexpr int kWhole = 128;                      // rows up to this long are listed whole
-constexpr int kFirstGoal = 96;                   // candidates asked for at first where top-p alone limits,
+constexpr int kFirstGoal = 64;                   // candidates asked for at first where top-p alone limits,
 constexpr int kMaxGoal = 1024;                   // and at most
 constexpr int kSteps = kThreads;                 // bins of the groups' maxima
 constexpr uint32_t kAll = 0xffffffffu;
@@ -62,8 +62,7 @@ struct alignas(16) SelectShared {
         uint32_t scratch[kBins];               // sort_list's
     };
     uint32_t maxima[kGroups];                  // keys of the groups' maxima, the whole row's
-    unsigned long long slot[2][kMaxCluster];
-    unsigned long long seg[2][kMaxCluster * kWarps];
+    unsigned long long seg[2][kMaxCluster * kWarps], seg2[2][kMaxCluster * kWarps];
     uint32_t hits[2][kMaxCluster * kWarps];    // candidates of each warp of the cluster
     unsigned long long red[kWarps];
     unsigned long long above;                  // a crossing: what lies above its bin,
@@ -94,6 +93,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
+}
+
+// Sum over the block of v.
+__device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long *red, int lane, int warp) {
+    v = warp_sum(v);
+    __syncthreads();
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += red[w];
+    return v;
 }
 
 // Pairs of floats in one instruction each.
@@ -356,22 +367,26 @@ struct Row {
         for (int j = 0; j < per; ++j)
             if (sh->maxima[(rank * per + j) * kThreads + tid] >= bound) sh->hit[atomicAdd(&sh->hit_n, 1u)] = static_cast<uint16_t>(j * kThreads + tid);
         __syncthreads();
+        // (group, round) pairs, the rounds padded to a power of two: no division in number()
         const int rounds = ((n + kThreads - 1) / kThreads + per - 1) / per;  // vectors of a group, at most
-        const int total = static_cast<int>(sh->hit_n) * rounds;
+        const int sh2 = 32 - __clz(rounds - 1);
+        const int total = static_cast<int>(sh->hit_n) << sh2;
         for (int e0 = tid; e0 - lane < total; e0 += kGather * kThreads) {
             auto number = [&](int j) {
                 const int e = e0 + j * kThreads;
                 if (e >= total) return -1;
-                const int h = e / rounds, group = sh->hit[h];
-                const int i = ((e - h * rounds) * per + group / kThreads) * kThreads + group % kThreads;
+                const int group = sh->hit[e >> sh2];
+                const int i = ((e & ((1 << sh2) - 1)) * per + group / kThreads) * kThreads + group % kThreads;
                 return i < n ? i : -1;
             };
             uint4 v[kGather];
 #pragma unroll
             for (int j = 0; j < kGather; ++j) {
-                const int i = number(j);
                 v[j] = nothing();
-                if (i >= 0) v[j] = part.fetch(i);
+                if (e0 - lane + j * kThreads < total) {  // the whole warp
+                    const int i = number(j);
+                    if (i >= 0) v[j] = part.fetch(i);
+                }
             }
             f(v, number);
         }
@@ -465,21 +480,39 @@ struct Row {
         });
     }
 
-    // The sum of v over every thread of the cluster.
-    __device__ unsigned long long sum(unsigned long long v) {
+    // The sums of v and w over every thread of the row.
+    __device__ void sum2(unsigned long long &v, unsigned long long &w) {
         v = warp_sum(v);
-        __syncthreads();
-        if (lane == 0) sh->red[warp] = v;
-        __syncthreads();
-        if (warp == 0) {
-            v = warp_sum(lane < kWarps ? sh->red[lane] : 0ull);
-            if (lane < static_cast<int>(cs)) st_peer(peer(&sh->slot[turn][rank], lane), v);
+        w = warp_sum(w);
+        if (lane < static_cast<int>(cs)) {
+            st_peer(peer(&sh->seg[turn][rank * kWarps + warp], lane), v);
+            st_peer(peer(&sh->seg2[turn][rank * kWarps + warp], lane), w);
         }
         sync();
-        v = 0;
-        for (uint32_t r = 0; r < cs; ++r) v += sh->slot[turn][r];
+        v = w = 0;
+        for (uint32_t g = lane; g < cs * kWarps; g += 32) {
+            v += sh->seg[turn][g];
+            w += sh->seg2[turn][g];
+        }
+        v = warp_sum(v);
+        w = warp_sum(w);
         turn ^= 1;
+    }
+    __device__ unsigned long long sum(unsigned long long v) {
+        unsigned long long none = 0;
+        sum2(v, none);
         return v;
+    }
+    // The summed weights 2^((l - m) c) of the groups' maxima that reach `low`, roughly.
+    __device__ float weight_of_maxima(float m, float c, float low) {
+        const uint32_t bound = order_key(low);
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < kKeysPerThread; ++j) {
+            const uint32_t k = sh->maxima[j * kThreads + tid];
+            if (k >= bound) s += ptx::ex2((key_value(k) - m) * c);
+        }
+        return static_cast<float>(block_sum(__float2ull_rn(s * 0x1p24f), sh->red, lane, warp)) * 0x1p-24f;
     }
 
     // The row's histogram: this thread's kBinsPerThread bins, summed over the CTAs.
@@ -487,7 +520,9 @@ struct Row {
     __device__ __forceinline__ void bins(unsigned long long (&v)[kBinsPerThread]) const {
 #pragma unroll
         for (int i = 0; i < kBinsPerThread; ++i) v[i] = 0;
-        for (uint32_t r = 0; r < cs; ++r) {
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) {  // unrolled: the peers' loads overlap
+            if (r >= cs) break;
             if (COUNT) {
 #pragma unroll
                 for (int h = 0; h < kBinsPerThread / 4; ++h) {
@@ -657,18 +692,6 @@ struct Row {
 };
 
 // ---- the leader's list: one CTA, all its threads
-
-// Sum over the block of v.
-__device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long *red, int lane, int warp) {
-    v = warp_sum(v);
-    __syncthreads();
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    v = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w];
-    return v;
-}
 
 // Sorts n distinct entries ascending.  Up to 128: each entry's rank is counted (2 to 8 threads an
 // entry).  Above: by 2048 equal steps of the upper halves' range, each entry then counts its rank in

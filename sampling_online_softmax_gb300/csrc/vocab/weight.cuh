@@ -18,6 +18,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cstring>
 
 namespace spec {
 namespace vocab {
@@ -49,6 +50,16 @@ constexpr int kPow2Steps = 32;
         {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}, \
         {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f} \
     }
+
+SPEC_HD float bits_float(int b) {
+#ifdef __CUDA_ARCH__
+    return __int_as_float(b);
+#else
+    float f;
+    memcpy(&f, &b, 4);
+    return f;
+#endif
+}
 
 // What turns a row's logits into weights: the row maximum m, c = log2(e) / T as a pair, U.
 struct Scale {
@@ -87,13 +98,15 @@ SPEC_HD unsigned long long fixed_weight(float l, const Scale &s, const float2 *p
     const float ql = fmaf(T.x, el, fmaf(T.x, eh, -qh)) + T.y * eh;
     const float wh = T.x + qh;
     const float wl = (qh - (wh - T.x)) + (T.y + ql);
-    // wh in (0.98, 2.02) as a multiple of 2^-24, wl in units of 2^-46
-    const long long v = (static_cast<long long>(static_cast<int>(wh * 16777216.f)) << 22) +
-                        static_cast<int>(rintf(wl * 0x1p46f));
-    const int sft = s.U + (j >> 5) - 46;
-    if (sft >= 0) return static_cast<unsigned long long>(v) << sft;
-    if (sft < -48) return 0ull;
-    return static_cast<unsigned long long>((v + (1ll << (-sft - 1))) >> -sft);
+    // wh + wl in units of 2^-U as (whole multiple of 2^22) + rest: scaled by a power of two, so exactly
+    const int e = (j >> 5) + s.U - 22;                   // 2^e units of 2^(22 - U); e in [-41, 30]
+    if (e < -24) return 0ull;                            // below half a unit
+    const float up = bits_float((e + 127) << 23);
+    const float t = wh * up;
+    const uint32_t hi = static_cast<uint32_t>(t);
+    const float rest = (t - static_cast<float>(hi)) + wl * up;  // exact, then one rounding
+    const int lo = static_cast<int>(rintf(rest * 0x1p22f));
+    return (static_cast<unsigned long long>(hi) << 22) + static_cast<long long>(lo);
 }
 
 // floor(W * f) for f in [0, 1), and whether f * W is no whole number, exactly.
