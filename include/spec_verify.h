@@ -337,8 +337,8 @@ SPEC_API spec_status spec_mtp_plug(const int32_t *in_tokens, int B, int K, const
  *   dev_status  SPEC_DEV_BAD_PARAM: a row's parameter is out of range or NaN;
  *               SPEC_DEV_NONFINITE: a row holds NaN or +inf, or every token of
  *               it is masked.  Such a row's token is -1; the others are drawn.
- * Weights and their sums are whole numbers in units of at least 2^-52, right to
- * about 2^-43 of the largest weight, so the token is the definition's unless u
+ * Weights and their sums are whole numbers in units of at most 2^-42, right to
+ * about 2^-38 relative, so the token is the definition's unless u
  * lies that near a border, and a call gives the same token every time.
  * Rows of at most SPEC_MAX_ROW_BYTES bytes (SPEC_ERR_UNSUPPORTED above).
  * No workspace; one launch.

@@ -42,7 +42,7 @@ __device__ __forceinline__ bool drawn_at_zero(float l, const Scale &sc, float mi
 // top-p is a share of, in units of 2^-U; 0: the list's own first k.  kWeigh: the bounds leave the
 // cut open; kMore: the cut lies past the list.
 template <int EB>
-__device__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, const Request &q, int n, unsigned long long W0, unsigned long long W1,
+__device__ __forceinline__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, const Request &q, int n, unsigned long long W0, unsigned long long W1,
                                   int32_t *token) {
     SelectShared *sh = r.sh;
     const int tid = r.tid, lane = r.lane, warp = r.warp;
@@ -136,23 +136,81 @@ struct Cut {
     int index;
 };
 
+// Weights of a vector's kept tokens.  Near: 2^((l - m) c) by ex2, off by at most
+//   3 2^-24 |x| ln 2 (difference, product and c round) + 2^-22 (ex2) + 3 2^-24 (sums of eight)
+// relative, which bound() adds up; in units of 2^-40.  Exact: fixed_weight, in units of 2^-U.
+template <int EB>
+struct Weigh {
+    static constexpr int kPer = Row<EB>::kPer;
+    static constexpr float kPerBit = 2.1f * 0x1p-24f, kFlat = 7.5f * 0x1p-24f;
+    const Scale &sc;
+    const float2 *pow2;
+    float floor;
+    int last;
+
+    __device__ __forceinline__ Weigh(const Scale &s, const float2 *p, const Cut &cut) : sc(s), pow2(p) {
+        floor = Row<EB>::value(cut.key);
+        last = cut.index;
+    }
+    __device__ __forceinline__ bool kept(float l, int x) const { return l > floor || (l == floor && x <= last); }
+    __device__ __forceinline__ float near(float l, float *b) const {
+        const float x = fmaxf((l - sc.m) * sc.ch, -200.f), w = ptx::ex2(x);  // (bounded: 0 times infinity is no bound)
+        *b = fmaf(w, fmaf(-x, kPerBit, kFlat), *b);
+        return w;
+    }
+    // The kept weights of a vector, and in *b their error's bound.
+    __device__ __forceinline__ unsigned long long near_sum(const Row<EB> &r, const uint4 &v, int i, float *b) const {
+        if (!(Row<EB>::vector_max(v) >= floor)) return 0ull;
+        float l[kPer], s = 0.f;
+        Row<EB>::unpack(v, l);
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) l[q] = kept(l[q], r.index(i, q)) ? near(l[q], b) : 0.f;
+#pragma unroll
+        for (int q = 0; q < kPer; q += 2) s += l[q] + l[q + 1];
+        return __float2ull_rn(s * 0x1p40f);
+    }
+    __device__ __forceinline__ unsigned long long exact(float l, int x) const {
+        const unsigned long long w = fixed_weight(l, sc, pow2);
+        return kept(l, x) ? w : 0ull;
+    }
+    __device__ __forceinline__ unsigned long long exact_sum(const Row<EB> &r, const uint4 &v, int i) const {
+        if (!(Row<EB>::vector_max(v) >= floor)) return 0ull;
+        float l[kPer];
+        Row<EB>::unpack(v, l);
+        unsigned long long s = 0;
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) s += exact(l[q], r.index(i, q));
+        return s;
+    }
+    // A thread's summed bound in units of 2^-40, and half a unit for each rounding to them.
+    static __device__ __forceinline__ unsigned long long bound(float b, int vectors) {
+        return __float2ull_ru(b * (1.001f * 0x1p40f)) + vectors;
+    }
+};
+
+constexpr uint32_t kOpen = 1;  // in place of a cut's key (keys are larger): the near sums leave it open
+
 // Where the kept tokens, in the order of falling logits, reach COUNT: the k-th; else: p times
-// their weight.  False: fewer than k.
+// their weight.  False: fewer than k, or (with near sums) open.
 //   1  a histogram of counts over 2048 equal steps below the maximum.  A bin's weight lies between
 //      its edges', 2 % apart, so its running sums bracket the cut's bin (COUNT: find it).
-//   2  the exact weights above the bracket and in all, and a histogram of the bracket's inside.
+//   2  the weights above the bracket and in all, and a histogram of the bracket's inside.
 //   3  the weights between, and the tokens of the narrowed bracket: a few, or equal ones, which one
 //      CTA sorts and weighs.
-// Where more than the list holds are left (equal logits in their thousands), or the cut lies below
-// the histogram, reach() finds it by keys.
+// The sums are near ones, by ex2 with a bound of the error (about 2^-20 of the whole), at a tenth of
+// the exact weights' time, where the tokens at the cut weigh enough (2^-14 of the whole) for that to
+// decide which comes last in most rows; where it leaves that open the caller comes again with
+// `exact`.  Where more than the list holds are left (equal logits in their thousands), reach() finds
+// the cut by keys.
+// (Always inlined, as all that takes a Row is: a pointer to one would keep it in memory.)
 template <bool COUNT, int EB>
-__device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
+__device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, bool exact, Cut *cut) {
+    using W_ = Weigh<EB>;
+    constexpr int kPer = Row<EB>::kPer;
     SelectShared *sh = r.sh;
-    const float2 *pow2 = sh->pow2;
     const int tid = r.tid;
     const Cut had = *cut;
-    const float floor = Row<EB>::value(had.key);
-    auto kept = [&](float l, int x) { return l > floor || (l == floor && x <= had.index); };
+    const W_ weigh(sc, sh->pow2, had);
     // 48 steps of two hold every weight that counts; narrower rows get finer bins
     const float span = fminf(48.f / sc.ch, 2.f * (sc.m - r.least_maximum()));
     const float scale = (kBins - 1) / fmaxf(span, 1e-30f);
@@ -163,37 +221,59 @@ __device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
         if (tid == 0) sh->cross_bin = kAll, sh->cross_last = kBins - 1;
         __syncthreads();
     };
-    // weights of a bin whose edges lie `at` bins below the maximum, in units of 2^-40
+    // weights of a bin whose edge lies `at` bins below the maximum, in units of 2^-40
     auto edge = [&](float at, float slack) { return static_cast<unsigned long long>(ptx::ex2(-at / scale * sc.ch) * slack * 0x1p40f); };
-
-    clear();
-    r.each([&](float l, int x) {
-        if (kept(l, x)) atomicAdd(&sh->count[static_cast<int>(place(l))], 1u);
-    });
-    r.sync();
-    unsigned long long v[kBinsPerThread], mine = 0, low = 0, high = 0;
-    r.template bins<true>(v);
-    uint32_t b0, b1;               // the cut's bin is in [b0, b1]
-    unsigned long long over = 0;   // COUNT: tokens above b0
+    unsigned long long v[kBinsPerThread];
     const int first = tid * kBinsPerThread;
-    if (COUNT) {
+    // the bin of the histogram in which the count from `over` on reaches `goal`
+    auto counted = [&](unsigned long long over, unsigned long long goal) {
+        unsigned long long mine = 0;
 #pragma unroll
         for (int i = 0; i < kBinsPerThread; ++i) mine += v[i];
-        unsigned long long run = r.sum_before(mine);
+        unsigned long long run = over + r.sum_before(mine);
 #pragma unroll
         for (int i = 0; i < kBinsPerThread; ++i) {
-            if (run < k && run + v[i] >= k) {
+            if (run < goal && run + v[i] >= goal) {
                 sh->cross_bin = first + i;
                 sh->above = run;
             }
             run += v[i];
         }
         __syncthreads();
+    };
+
+    clear();
+    uint32_t deep = 0;  // in the last bin, which may hold most of a cold row
+    r.vectors([&](const uint4(&vec)[Row<EB>::kBatch], int i0) {
+#pragma unroll
+        for (int j = 0; j < Row<EB>::kBatch; ++j) {
+            if (!(Row<EB>::vector_max(vec[j]) >= weigh.floor)) continue;
+            float l[kPer];
+            Row<EB>::unpack(vec[j], l);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+                if (!weigh.kept(l[q], r.index(i0 + j * kThreads, q))) continue;
+                const int y = static_cast<int>(place(l[q]));
+                if (y == kBins - 1)
+                    ++deep;
+                else
+                    atomicAdd(&sh->count[y], 1u);
+            }
+        }
+    });
+    deep = __reduce_add_sync(kAll, deep);
+    if (r.lane == 0 && deep) atomicAdd(&sh->count[kBins - 1], deep);
+    r.sync();
+    r.template bins<true>(v);
+    uint32_t b0, b1;              // the cut's bin is in [b0, b1]
+    unsigned long long A = 0;     // what lies above b0
+    if (COUNT) {
+        counted(0, k);
         b0 = b1 = sh->cross_bin;
         if (b0 == kAll) return false;
-        over = sh->above;
+        A = sh->above;
     } else {
-        unsigned long long lo[kBinsPerThread], hi[kBinsPerThread];
+        unsigned long long lo[kBinsPerThread], hi[kBinsPerThread], low = 0, high = 0, all_l, all_h;
 #pragma unroll
         for (int i = 0; i < kBinsPerThread; ++i) {
             const float at = static_cast<float>(first + i);
@@ -202,7 +282,6 @@ __device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
             low += lo[i];
             high += hi[i];
         }
-        unsigned long long all_l, all_h;
         unsigned long long run_l = r.sum_before(low, &all_l), run_h = r.sum_before(high, &all_h);
         const unsigned long long t0 = share_of(all_l, p), t1 = share_of(all_h, p);
 #pragma unroll
@@ -213,57 +292,70 @@ __device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
             run_l += lo[i];
         }
         __syncthreads();
-        b0 = sh->cross_bin;
+        b0 = sh->cross_bin == kAll ? 0u : sh->cross_bin;
         b1 = sh->cross_last;
-        if (b0 == kAll) b0 = 0;
+        exact |= edge(static_cast<float>(b1), 1.f) < all_l >> 14;
     }
 
     const float from = static_cast<float>(b0), upto = static_cast<float>(b1 + 1);
     const float fine = kBins / (upto - from);
-    auto inside = [&](float at) { return at >= from && at < upto; };
     auto sub = [&](float at) { return min(kBins - 1, static_cast<int>((at - from) * fine)); };
-    unsigned long long W = 0, A = 0, target = static_cast<unsigned long long>(k);
+    // no logit of the bracket lies below (the last bin has no end)
+    const float edge_l = b1 == kBins - 1 ? -FLT_MAX : sc.m - upto / scale - (fabsf(sc.m) + span) * 0x1p-20f;
+    unsigned long long W = 0, B = 0, target = static_cast<unsigned long long>(k);
+    float b = 0.f;
+    int vectors = 0;
     clear();
-    r.each([&](float l, int x) {
-        if (!kept(l, x)) return;
-        const float at = place(l);
-        if (!COUNT) {
-            const unsigned long long w = fixed_weight(l, sc, pow2);
-            W += w;
-            if (at < from) A += w;
+    r.vectors([&](const uint4(&vec)[Row<EB>::kBatch], int i0) {
+#pragma unroll
+        for (int j = 0; j < Row<EB>::kBatch; ++j) {
+            const float top = Row<EB>::vector_max(vec[j]);
+            if (!(top >= (COUNT ? fmaxf(weigh.floor, edge_l) : weigh.floor))) continue;
+            float l[kPer], s = 0.f, a = 0.f;
+            Row<EB>::unpack(vec[j], l);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+                const bool in = weigh.kept(l[q], r.index(i0 + j * kThreads, q));
+                const float at = place(l[q]);
+                if (!COUNT && !exact) {
+                    const float w = in ? weigh.near(l[q], &b) : 0.f;
+                    s += w;
+                    a += at < from ? w : 0.f;
+                }
+                if (in && at >= from && at < upto) atomicAdd(&sh->count[sub(at)], 1u);
+            }
+            if (!COUNT && exact) {
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) {
+                    const unsigned long long w = weigh.exact(l[q], r.index(i0 + j * kThreads, q));
+                    W += w;
+                    A += place(l[q]) < from ? w : 0ull;
+                }
+            } else if (!COUNT) {
+                W += __float2ull_rn(s * 0x1p40f);
+                A += __float2ull_rn(a * 0x1p40f);
+                ++vectors;
+            }
         }
-        if (inside(at)) atomicAdd(&sh->count[sub(at)], 1u);
     });
-    if (!COUNT) {
-        r.sum2(W, A);
-        target = share_of(W, p);
-    } else {
+    if (COUNT) {
         r.sync();
-        A = over;
+    } else {
+        r.sum2(W, A);
+        if (!exact) B = r.sum(W_::bound(b * 2.f, 2 * vectors));  // (sums in a row, not a tree: 7 2^-24 more)
+        target = share_of(W, p);
     }
     r.template bins<true>(v);
     uint32_t s0, s1;
     if (COUNT) {
-        mine = 0;
-#pragma unroll
-        for (int i = 0; i < kBinsPerThread; ++i) mine += v[i];
-        unsigned long long run = A + r.sum_before(mine);
-#pragma unroll
-        for (int i = 0; i < kBinsPerThread; ++i) {
-            if (run < target && run + v[i] >= target) {
-                sh->cross_bin = first + i;
-                sh->above = run;
-            }
-            run += v[i];
-        }
-        __syncthreads();
+        counted(A, target);
         s0 = s1 = sh->cross_bin;
         A = sh->above;
     } else {
         const float step = 1.f / fine;
-        const unsigned long long unit = A >> (sc.U - 40), aim = target >> (sc.U - 40);  // in units of 2^-40
-        unsigned long long lo[kBinsPerThread], hi[kBinsPerThread];
-        low = high = 0;
+        const int drop = exact ? sc.U - 40 : 0;  // from the sums' units to 2^-40
+        const unsigned long long unit = A >> drop, aim = target >> drop, slack = B + 1;
+        unsigned long long lo[kBinsPerThread], hi[kBinsPerThread], low = 0, high = 0;
 #pragma unroll
         for (int i = 0; i < kBinsPerThread; ++i) {
             const float at = from + static_cast<float>(first + i) * step;
@@ -272,12 +364,12 @@ __device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
             low += lo[i];
             high += hi[i];
         }
-        unsigned long long run_h = unit + 1 + r.sum_before(high);
+        unsigned long long run_h = unit + slack + r.sum_before(high);
         unsigned long long run_l = unit + r.sum_before(low);
 #pragma unroll
         for (int i = 0; i < kBinsPerThread; ++i) {
             if (run_h < aim && run_h + hi[i] >= aim) sh->cross_bin = first + i;
-            if (run_l < aim + 1 && run_l + lo[i] >= aim + 1) sh->cross_last = first + i;
+            if (run_l < aim + slack && run_l + lo[i] >= aim + slack) sh->cross_last = first + i;
             run_h += hi[i];
             run_l += lo[i];
         }
@@ -290,24 +382,26 @@ __device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
     uint32_t found = 0;
     unsigned long long between = 0;
     r.vectors([&](const uint4(&vec)[Row<EB>::kBatch], int i0) {
-        constexpr int kPer = Row<EB>::kPer;
         unsigned long long bits = 0;
-#pragma unroll 1
+#pragma unroll
         for (int j = 0; j < Row<EB>::kBatch; ++j) {
-            const uint4 w = j == 0 ? vec[0] : j == 1 ? vec[1] : j == 2 ? vec[2] : vec[3];
-            float l[kPer];
-            Row<EB>::unpack(w, l);
+            const float top = Row<EB>::vector_max(vec[j]);
+            if (!(top >= fmaxf(weigh.floor, edge_l))) continue;
+            float l[kPer], s = 0.f;
+            Row<EB>::unpack(vec[j], l);
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 const float at = place(l[e]);
-                if (!inside(at) || !kept(l[e], r.index(i0 + j * kThreads, e))) continue;
+                if (!(at >= from && at < upto) || !weigh.kept(l[e], r.index(i0 + j * kThreads, e))) continue;
                 const int y = sub(at);
                 if (y < static_cast<int>(s0)) {
-                    if (!COUNT) between += fixed_weight(l[e], sc, pow2);
+                    if (!COUNT && !exact) s += weigh.near(l[e], &b);
+                    if (!COUNT && exact) between += fixed_weight(l[e], sc, weigh.pow2);
                 } else if (y <= static_cast<int>(s1)) {
                     bits |= 1ull << (j * kPer + e);
                 }
             }
+            if (!COUNT && s > 0.f) between += __float2ull_rn(s * 0x1p40f);
         }
         found += r.append(bits, 1, [&](int j) { return i0 + j * kThreads; });
     });
@@ -318,18 +412,22 @@ __device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
             sort_list(sh->list, n, sh->scratch, sh->red, tid);
             const int per = (n + kThreads - 1) / kThreads;
             const int i0 = min(static_cast<int>(n), tid * per), i1 = min(static_cast<int>(n), i0 + per);
-            auto weigh = [&](int i) {
-                return COUNT ? 1ull : fixed_weight(key_value(~static_cast<uint32_t>(sh->list[i] >> 32)), sc, pow2);
+            auto weight = [&](int i) -> unsigned long long {
+                if (COUNT) return 1ull;
+                const unsigned long long w = fixed_weight(key_value(~static_cast<uint32_t>(sh->list[i] >> 32)), sc, weigh.pow2);
+                return exact ? w : w >> (sc.U - 40);
             };
-            mine = 0;
-            for (int i = i0; i < i1; ++i) mine += weigh(i);
+            const unsigned long long slack = !COUNT && !exact ? B + n + 2 : 0ull;
+            unsigned long long mine = 0;
+            for (int i = i0; i < i1; ++i) mine += weight(i);
             unsigned long long run = A + r.sum_before(mine);
             for (int i = i0; i < i1; ++i) {
-                const unsigned long long w = weigh(i);
+                const unsigned long long w = weight(i);
                 if (run < target && run + w >= target) {
+                    const bool sure = run + slack < target && run + w >= target + slack;
                     const uint32_t key = Row<EB>::key(key_value(~static_cast<uint32_t>(sh->list[i] >> 32)));
                     for (uint32_t c = 0; c < r.cs; ++c) {
-                        st_peer(peer(&sh->cut[0], c), key);
+                        st_peer(peer(&sh->cut[0], c), !COUNT && !exact && !sure ? kOpen : key);
                         st_peer(peer(&sh->cut[1], c), static_cast<uint32_t>(sh->list[i]));
                     }
                 }
@@ -339,51 +437,147 @@ __device__ bool cut_row(Row<EB> &r, const Scale &sc, int k, float p, Cut *cut) {
         r.sync();
         const Cut c = {sh->cut[0], static_cast<int>(sh->cut[1])};
         r.sync();  // read everywhere before it is written again
-        if (c.key) {
+        if (c.key > kOpen) {
             *cut = c;
             return true;
         }
     }
+    if (!COUNT && !exact) return false;
     uint32_t at;
     unsigned long long above;
-    auto weigh = [&](float l, int x) -> unsigned long long { return !kept(l, x) ? 0ull : COUNT ? 1ull : fixed_weight(l, sc, pow2); };
-    if (!r.template reach<COUNT>(had.key, Row<EB>::key(sc.m), target, weigh, &at, &above)) return false;
-    const unsigned long long w = COUNT ? 1ull : fixed_weight(Row<EB>::value(at), sc, pow2);
-    const bool same = at == had.key;
-    cut->index = r.tie_index(at, (target - above + w - 1) / w, [&](float, int y) { return !same || y <= had.index; });
+    auto each = [&](float l, int x) -> unsigned long long {
+        return !weigh.kept(l, x) ? 0ull : COUNT ? 1ull : fixed_weight(l, sc, weigh.pow2);
+    };
+    if (!r.template reach<COUNT>(had.key, Row<EB>::key(sc.m), target, each, &at, &above)) return false;
+    const unsigned long long w = COUNT ? 1ull : fixed_weight(Row<EB>::value(at), sc, weigh.pow2);
+    cut->index = r.tie_index(at, (target - above + w - 1) / w, at == had.key ? had.index : INT_MAX);
     cut->key = at;
     return true;
 }
 
+// The key of the least logit whose weight is at least `least`; a warp's lanes try 32 keys at a time.
+template <int EB>
+__device__ __forceinline__ uint32_t least_key(const Row<EB> &r, const Scale &sc, unsigned long long least) {
+    uint32_t lo = Row<EB>::kLowest, hi = Row<EB>::key(sc.m);  // hi's weight suffices; the answer is in [lo, hi]
+    while (lo < hi) {
+        const uint32_t step = (hi - lo) / 32 + 1, k = min(hi, lo + r.lane * step);
+        const uint32_t ok = __ballot_sync(kAll, fixed_weight(Row<EB>::value(k), sc, r.sh->pow2) >= least);
+        if (!ok) {  // above the last key tried
+            lo = min(hi, lo + 31 * step + 1);
+            continue;
+        }
+        const uint32_t j = __ffs(ok) - 1, at = min(hi, lo + j * step);
+        if (j > 0) lo = min(hi, lo + (j - 1) * step + 1);
+        hi = at;
+        if (j == 0) break;
+    }
+    return hi;
+}
+
 // The long way: the kept tokens are cut out of the whole row, and the draw runs over it.
 template <int EB>
-__device__ void draw_from_row(Row<EB> &r, const Scale &sc, const Request &q, int32_t *token) {
-    const float2 *pow2 = r.sh->pow2;
+__device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const Request &q, int32_t *token) {
+    constexpr int kPer = Row<EB>::kPer;
+    SelectShared *sh = r.sh;
     Cut cut = {Row<EB>::kLowest, INT_MAX};
-    if (q.k > 0) cut_row<true>(r, sc, q.k, 1.f, &cut);
-    if (q.p < 1.f) cut_row<false>(r, sc, 0, q.p, &cut);
-    const float floor = Row<EB>::value(cut.key);
-    auto kept = [&](float l, int x) { return l > floor || (l == floor && x <= cut.index); };
+    if (q.k > 0) cut_row<true>(r, sc, q.k, 1.f, false, &cut);
+    if (q.p < 1.f) {
+        for (int again = 0; again < 2; ++again)
+            if (cut_row<false>(r, sc, 0, q.p, again, &cut)) break;
+    }
+    if (q.least) {
+        const uint32_t x = least_key(r, sc, q.least);
+        if (x > cut.key) cut = {x, INT_MAX};
+    }
+    const Weigh<EB> weigh(sc, sh->pow2, cut);
     if (q.u == 0.f) {
-        r.locate([&](float l, int x) { return static_cast<unsigned long long>(kept(l, x) && drawn_at_zero(l, sc, q.min_p)); },
-                 [](unsigned long long) { return 1ull; }, [&](int x) { *token = x; });
+        r.locate(
+            [&](const uint4 &v, int i) {
+                float l[kPer];
+                Row<EB>::unpack(v, l);
+                unsigned long long c = 0;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) c += weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc, q.min_p);
+                return c;
+            },
+            [](unsigned long long) { return 1ull; },
+            [&](const uint4 &v, int i, unsigned long long, unsigned long long) {
+                float l[kPer];
+                Row<EB>::unpack(v, l);
+                int x = -1;
+#pragma unroll
+                for (int e = kPer - 1; e >= 0; --e)
+                    if (weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc, q.min_p)) x = r.index(i, e);
+                *token = x;
+            });
         return;
     }
+    auto aim = [&](unsigned long long W) {
+        bool rest;
+        return scaled_floor(W, q.u, &rest) + 1;
+    };
+    // first by near sums: the draw is sure where u's place is further from the token's ends than the
+    // sums' error (the same 2^-20 of the whole)
+    float b = 0.f;
+    int vectors = 0;
+    if (r.tid == 0) sh->slack = 0;
+    __syncthreads();
+    bool counting = true;
     r.locate(
-        [&](float l, int x) {
-            const unsigned long long w = kept(l, x) ? fixed_weight(l, sc, pow2) : 0ull;
-            return w >= q.least ? w : 0ull;
+        [&](const uint4 &v, int i) {
+            float more = 0.f;
+            const unsigned long long w = weigh.near_sum(r, v, i, &more);
+            if (counting) b += more, ++vectors;
+            return w;
         },
         [&](unsigned long long W) {
-            bool rest;
-            return scaled_floor(W, q.u, &rest) + 1;
+            counting = false;
+            return aim(W);
         },
-        [&](int x) { *token = x; });
+        [&](const uint4 &v, int i, unsigned long long before, unsigned long long target) {
+            float l[kPer], none = 0.f;
+            Row<EB>::unpack(v, l);
+            unsigned long long run = before;
+            uint32_t x = kAll;
+            long long left = 0, right = 0;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                const bool in = weigh.kept(l[e], r.index(i, e));
+                const unsigned long long w = in ? __float2ull_rn(weigh.near(l[e], &none) * 0x1p40f) : 0ull;
+                if (x == kAll && run < target && run + w >= target) {
+                    x = static_cast<uint32_t>(r.index(i, e));
+                    left = static_cast<long long>(target - 1 - run);
+                    right = static_cast<long long>(run + w - target);
+                }
+                run += w;
+            }
+            if (x != kAll)
+                for (uint32_t c = 0; c < r.cs; ++c) {
+                    st_peer(peer(&sh->drawn, c), x);
+                    st_peer(peer(&sh->slack, c), static_cast<unsigned long long>(min(left, right)));
+                }
+        });
+    const unsigned long long B = r.sum(Weigh<EB>::bound(b, vectors)) + kPer + 2;
+    if (sh->slack > B) {
+        if (r.rank == 0 && r.tid == 0) *token = static_cast<int32_t>(sh->drawn);
+        return;
+    }
+    r.locate([&](const uint4 &v, int i) { return weigh.exact_sum(r, v, i); }, aim,
+             [&](const uint4 &v, int i, unsigned long long before, unsigned long long target) {
+                 float l[kPer];
+                 Row<EB>::unpack(v, l);
+#pragma unroll
+                 for (int e = 0; e < kPer; ++e) {
+                     const unsigned long long w = weigh.exact(l[e], r.index(i, e));
+                     if (before < target && before + w >= target) *token = r.index(i, e);
+                     before += w;
+                 }
+             });
 }
 
 // Filtered sampling of row b.
 template <int EB>
-__device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
+__device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
     SelectShared *sh = r.sh;
     Request q;
     q.u = a.u[b];
@@ -415,7 +609,7 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
     }
     const bool share = q.p < 1.f && q.k == 0;  // top-p is a share of the whole row
     const bool sums = share && a.V > kWhole && !one;
-    sc.m = sums ? r.template stream<true>(sc.ch) : r.template stream<false>(sc.ch);
+    sc.m = sums ? r.template stream<Row<EB>::kBounded>(sc.ch) : r.template stream<Row<EB>::kNone>(sc.ch);
     if (!(fabsf(sc.m) < INFINITY)) {  // NaN, +inf, or nothing but -inf
         if (r.rank == 0 && r.tid == 0) {
             a.tokens[b] = -1;
@@ -448,21 +642,23 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
     // The short way: the list holds the logits from `low` on; all: that is every token.
     float low = -FLT_MAX;
     bool all = true;
+    int attempts = sums ? 2 : 1;
     unsigned long long W0 = 0, W1 = 0;
     if (a.V > kWhole) {
-        if (sums) {  // bounds of the row's weight, 2^-18 apart to either side
-            float Q, s = r.exp_total(&Q);
-            s *= ptx::ex2(fmaf(-sc.m, sc.ch, Q));
-            const unsigned long long W = __float2ull_rn(fminf(s, 0x1p22f) * 0x1p40f) << (sc.U - 40);
-            const bool sound = s >= 0.5f && s < 0x1p22f;  // not: logits whose products overflow
-            W0 = sound ? W - (W >> 18) : 1ull;
-            W1 = sound ? W + (W >> 18) : 1ull << 62;
+        if (sums) {  // bounds of the row's weight
+            float Q, off, s = r.exp_total(&Q, &off);
+            const float d = fmaf(-sc.m, sc.ch, Q);
+            s *= ptx::ex2(d);
+            off += (fabsf(d) + 8.f) * 0x1p-24f;
+            const bool sound = s >= 0.5f && s <= static_cast<float>(a.V) * 1.01f && off < 0x1p-10f;  // not: logits whose products overflow
+            const float unit = bits_float((sc.U + 127) << 23);
+            const unsigned long long w = __float2ull_rn(sound ? s * unit : 0.f), e = __float2ull_ru(sound ? s * off * unit : 0.f);
+            W0 = sound ? w - e : 1ull;
+            W1 = sound ? w + e : 1ull << 62;
         }
         if (q.k > kMaxGoal || (q.k == 0 && !share && q.min_p == 0.f)) {
-            draw_from_row(r, sc, q, a.tokens + b);
-            return;
-        }
-        if (q.k > 0 || share) {  // too few groups for it: few tokens that are not masked
+            attempts = 0;
+        } else if (q.k > 0 || share) {  // too few groups for it: few tokens that are not masked
             all = !r.threshold(sc.m, q.k > 0 ? q.k : kFirstGoal, &low);
         } else {  // from a little below what min-p asks for
             const float x = log2f(q.min_p) / sc.ch;
@@ -470,7 +666,7 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
             all = false;
         }
     }
-    for (int attempt = 0; attempt < (sums ? 2 : 1); ++attempt) {
+    for (int attempt = 0; attempt < attempts; ++attempt) {
         // a list of the largest n logits weighs at most n, and about what its groups' maxima do
         const float need = sums ? q.p * static_cast<float>(W0) * exp2f(static_cast<float>(-sc.U)) : 0.f;
         if (sums && need > (attempt ? static_cast<float>(kMaxList) : 2.f * kFirstGoal)) continue;
@@ -481,30 +677,40 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
         if (all) low = -FLT_MAX;
         const uint32_t n = r.collect(low, attempt);
         if (n > kMaxList) break;
-        if (!share || all) {
-            if (r.rank == 0) draw_from_list(r, sc, q, n, 0ull, 0ull, a.tokens + b);
-            return;
-        }
+        const bool part = share && !all;
         uint32_t v = kDone;
         for (int weighed = 0; weighed < 3; ++weighed) {
             if (r.rank == 0) {
-                v = draw_from_list(r, sc, q, n, W0, W1, a.tokens + b);
-                if (r.tid < static_cast<int>(r.cs)) st_peer(peer(&sh->verdict, r.tid), v);
+                v = draw_from_list(r, sc, q, n, part ? W0 : 0ull, part ? W1 : 0ull, a.tokens + b);
+                if (part && r.tid < static_cast<int>(r.cs)) st_peer(peer(&sh->verdict, r.tid), v);
             }
+            if (!part) return;
             r.sync();
             v = sh->verdict;
             if (v != kWeigh || weighed == 2) break;
-            unsigned long long w = 0;
-            if (weighed == 0) {  // the list's weights are exact: the error is the rest's alone
-                float rest = 0.f;
-                r.each([&](float l, int) { rest += l >= low ? 0.f : ptx::ex2((l - sc.m) * sc.ch); });
-                w = r.sum(__float2ull_rn(rest * 0x1p40f)) << (sc.U - 40);
-                if (r.rank == 0) {  // (the leader alone draws)
-                    const unsigned long long listed = sh->cum[n - 1];
-                    W0 = listed + w - (w >> 17) - 1;
-                    W1 = listed + w + (w >> 17) + (1ull << (sc.U - 30));
-                }
+            if (weighed == 0) {  // the list's weights are exact, in the leader's hands: the error is the rest's alone
+                const Weigh<EB> weigh(sc, sh->pow2, Cut{Row<EB>::kLowest, INT_MAX});
+                unsigned long long rest = 0, bound = 0;
+                float e = 0.f;
+                int vectors = 0;
+                r.vectors([&](const uint4(&v)[Row<EB>::kBatch], int) {
+#pragma unroll
+                    for (int j = 0; j < Row<EB>::kBatch; ++j) {
+                        float l[Row<EB>::kPer], s = 0.f;
+                        Row<EB>::unpack(v[j], l);
+#pragma unroll
+                        for (int x = 0; x < Row<EB>::kPer; ++x) s += l[x] >= low || l[x] == -INFINITY ? 0.f : weigh.near(l[x], &e);
+                        rest += __float2ull_rn(s * 0x1p40f);
+                        ++vectors;
+                    }
+                });
+                bound = Weigh<EB>::bound(2.f * e, vectors);  // (in a row, not a tree)
+                r.sum2(rest, bound);
+                const unsigned long long listed = sh->cum[n - 1];
+                W0 = listed + ((rest - min(rest, bound)) << (sc.U - 40));
+                W1 = listed + ((rest + bound) << (sc.U - 40));
             } else {
+                unsigned long long w = 0;
                 r.each([&](float l, int) { w += fixed_weight(l, sc, sh->pow2); });
                 W0 = W1 = r.sum(w);
             }
@@ -516,10 +722,10 @@ __device__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
 
 // The K largest logits of row b.
 template <int EB>
-__device__ void top_row(const RowArgs &a, Row<EB> &r, int b) {
+__device__ __forceinline__ void top_row(const RowArgs &a, Row<EB> &r, int b) {
     SelectShared *sh = r.sh;
     const float c = kLog2e / a.temp;
-    const float m = a.lse ? r.template stream<true>(c) : r.template stream<false>(c);
+    const float m = a.lse ? r.template stream<Row<EB>::kSum>(c) : r.template stream<Row<EB>::kNone>(c);
     const size_t out = static_cast<size_t>(b) * a.K;
     if (!(m < INFINITY)) {  // NaN or +inf
         if (r.rank == 0) {
@@ -536,8 +742,8 @@ __device__ void top_row(const RowArgs &a, Row<EB> &r, int b) {
     }
     const bool empty = m == -INFINITY;  // every token masked: an empty list, no error
     if (a.lse) {
-        float Q, z = -INFINITY;
-        const float s = r.exp_total(&Q);
+        float Q, off, z = -INFINITY;
+        const float s = r.exp_total(&Q, &off);
         if (!empty) {
             z = fmaf(Q, kLn2, logf(s));
             if (!(fabsf(z) < INFINITY) || !(s >= 0.25f)) {  // logits whose products with c overflow
@@ -559,7 +765,7 @@ __device__ void top_row(const RowArgs &a, Row<EB> &r, int b) {
         unsigned long long above;
         Cut cut = {Row<EB>::kLowest, INT_MAX};
         if (r.template reach<true>(cut.key, Row<EB>::key(m), a.K, [](float, int) { return 1ull; }, &at, &above)) {
-            cut.index = r.tie_index(at, a.K - above, [](float, int) { return true; });
+            cut.index = r.tie_index(at, a.K - above, INT_MAX);
             cut.key = at;
         }
         uint32_t found = 0;

@@ -72,6 +72,8 @@ struct alignas(16) SelectShared {
     uint32_t tie_index;
     uint32_t cut[2];                           // a cut's key and index
     uint32_t verdict;
+    uint32_t drawn;                            // a near draw and how far u is from its token's ends
+    unsigned long long slack;
     uint32_t steps[kSteps];
     float2 pow2[kPow2Steps];
 };
@@ -166,33 +168,43 @@ struct Row {
         }
         return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
-    static __device__ __forceinline__ unsigned long long exp_pair(float a, float b, unsigned long long c2, unsigned long long q2) {
-        float x, y;
-        split(fma2(pair(a, b), c2, q2), x, y);
-        return pair(ptx::ex2(x), ptx::ex2(y));
+    // 2^(l c - q) of two logits; adds weight times exponent to `b`.
+    template <bool BOUND>
+    static __device__ __forceinline__ unsigned long long exp_pair(float l0, float l1, unsigned long long c2, unsigned long long q2,
+                                                                  unsigned long long &b) {
+        const unsigned long long x = fma2(pair(l0, l1), c2, q2);
+        float x0, x1;
+        split(x, x0, x1);
+        const unsigned long long w = pair(ptx::ex2(x0), ptx::ex2(x1));
+        if (BOUND) b = fma2(w, pair(fmaxf(x0, -200.f), fmaxf(x1, -200.f)), b);  // (a masked logit's is -inf)
+        return w;
     }
-    static __device__ __forceinline__ unsigned long long vector_exp(const uint4 &v, unsigned long long c2, unsigned long long q2) {
+    template <bool BOUND>
+    static __device__ __forceinline__ unsigned long long vector_exp(const uint4 &v, unsigned long long c2, unsigned long long q2,
+                                                                    unsigned long long &b) {
         float l[kPer];
         unpack(v, l);
-        unsigned long long s = add2(exp_pair(l[0], l[1], c2, q2), exp_pair(l[2], l[3], c2, q2));
-        if (kPer == 8) s = add2(s, add2(exp_pair(l[4 % kPer], l[5 % kPer], c2, q2), exp_pair(l[6 % kPer], l[7 % kPer], c2, q2)));
+        unsigned long long s = add2(exp_pair<BOUND>(l[0], l[1], c2, q2, b), exp_pair<BOUND>(l[2], l[3], c2, q2, b));
+        if (kPer == 8) s = add2(s, add2(exp_pair<BOUND>(l[4 % kPer], l[5 % kPer], c2, q2, b), exp_pair<BOUND>(l[6 % kPer], l[7 % kPer], c2, q2, b)));
         return s;
     }
 
     // Reads the part; then the largest logit of the row (returned; NaN if there is one), the keys of
-    // the groups' maxima in sh->maxima of every CTA, and with SUM what exp_total() takes: a sum of
-    // 2^(l c - q) and its q for every warp.  q is a rounded maximum times c and counts as exact, so
-    // only l c - q (one fused operation) and ex2 round: a weight of size 2^-x is off by
-    // (x + 4) 2^-24 relative, and a row's sum, whose terms below 2^-16 weigh little each, by 2^-18.
-    template <bool SUM>
-    __device__ float stream(float c) {
+    // the groups' maxima in sh->maxima of every CTA, and with kSum what exp_total() takes: a sum s of
+    // 2^x, x = l c - q, for every warp, its q, and (kBounded) b, the sum of 2^x |x|, for the error.  q is a rounded
+    // maximum times c and counts as exact, so a term is off by 2 |x| 2^-24 ln 2 (x and c round) + 2^-22
+    // (ex2) relative; rebasing a sum to a larger q by (6 + |change|) 2^-24, which counts as 4 more of
+    // |x|; and the sums by 2 + 3 (trees), 2 (pairs of floats), 5 + 5 levels of 2^-24.
+    enum Sums : int { kNone = 0, kSum = 1, kBounded = 2 };  // kBounded: b too
+    template <int SUM>
+    __device__ __forceinline__ float stream(float c) {
         constexpr int kBatch = 8;
         static_assert(kBatch == kMaxCluster, "a batch's vectors are one of each group");
         float g[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) g[j] = -INFINITY;
         float top = -INFINITY, q = -INFINITY;
-        unsigned long long s = pair(0.f, 0.f);
+        unsigned long long s = pair(0.f, 0.f), less = s, b = s;  // the sum, its rounding errors, the exponents'
         const unsigned long long c2 = pair(c, c);
         auto take = [&](const uint4(&v)[kBatch]) {
             float m = -INFINITY;
@@ -204,15 +216,27 @@ struct Row {
             }
             if (SUM) {
                 if (m > top) {
-                    const float f = ptx::ex2(q - m * c);
-                    s = fma2(s, pair(f, f), pair(0.f, 0.f));
+                    const float to = m * c, f = top > -INFINITY ? ptx::ex2(q - to) : 0.f, d = top > -INFINITY ? q - to - 4.f : 0.f;
+                    const unsigned long long none = pair(0.f, 0.f), f2 = pair(f, f);
+                    if (SUM == kBounded) b = fma2(fma2(s, pair(d, d), b), f2, none);
+                    s = fma2(s, f2, none);
+                    less = fma2(less, f2, none);
                     top = m;
-                    q = m * c;
+                    q = to;
                 }
                 if (top > -INFINITY) {
                     const unsigned long long q2 = pair(-q, -q);
+                    unsigned long long t[kBatch];
 #pragma unroll
-                    for (int j = 0; j < kBatch; ++j) s = add2(s, vector_exp(v[j], c2, q2));
+                    for (int j = 0; j < kBatch; ++j) t[j] = vector_exp<SUM == kBounded>(v[j], c2, q2, b);
+#pragma unroll
+                    for (int h = kBatch / 2; h; h >>= 1)
+#pragma unroll
+                        for (int j = 0; j < h; ++j) t[j] = add2(t[j], t[j + h]);
+                    const unsigned long long minus = pair(-1.f, -1.f), sum = add2(s, t[0]);  // TwoSum, s or t larger
+                    const unsigned long long bb = fma2(s, minus, sum);
+                    less = add2(less, add2(fma2(fma2(bb, minus, sum), minus, s), fma2(bb, minus, t[0])));
+                    s = sum;
                 }
             }
         };
@@ -239,19 +263,33 @@ struct Row {
         if (per <= 2) g[0] = max_nan(g[0], g[2]), g[1] = max_nan(g[1], g[3]);
         if (per <= 1) g[0] = max_nan(g[0], g[1]);
         unsigned long long warp_sums = 0;
+        float warp_bound = 0.f;
         if (SUM) {
             float Q = q;
 #pragma unroll
             for (int o = 16; o; o >>= 1) Q = fmaxf(Q, __shfl_xor_sync(kAll, Q, o));
             float x, y;
             split(s, x, y);
-            x = q > -INFINITY ? (x + y) * ptx::ex2(q - Q) : 0.f;
+            float e0, e1, b0, b1;
+            split(less, e0, e1);
+            split(b, b0, b1);
+            const float f = q > -INFINITY ? ptx::ex2(q - Q) : 0.f, d = q > -INFINITY ? 4.f + Q - q : 0.f;
+            x = (x + y) + (e0 + e1);
+            y = (x * d - (b0 + b1)) * f;
+            x *= f;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+            for (int o = 16; o; o >>= 1) {
+                x += __shfl_xor_sync(kAll, x, o);
+                y += __shfl_xor_sync(kAll, y, o);
+            }
             warp_sums = pair(Q, x);
+            warp_bound = y;
         }
         if (cs > 1) cluster_wait();  // the peers have started
-        if (SUM && lane < static_cast<int>(cs)) st_peer(peer(&sh->seg[turn][rank * kWarps + warp], lane), warp_sums);
+        if (SUM && lane < static_cast<int>(cs)) {
+            st_peer(peer(&sh->seg[turn][rank * kWarps + warp], lane), warp_sums);
+            st_peer(peer(&sh->seg2[turn][rank * kWarps + warp], lane), static_cast<unsigned long long>(__float_as_uint(warp_bound)));
+        }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             if (j < per) {
@@ -270,30 +308,43 @@ struct Row {
         for (int w = 0; w < kWarps; ++w) k = max(k, static_cast<uint32_t>(sh->red[w]));
         return key_value(k);
     }
-    // The row's sum of 2^(l c - *q) and its q, after stream<true>.
-    __device__ float exp_total(float *q) {
-        float Q = -INFINITY, s = 0.f, e[(kMaxCluster * kWarps + 31) / 32][2];
+    // The row's sum of 2^(l c - *q), its q, and a bound of its error, relative, after stream<kSum or kBounded>
+    // (the bound: kBounded).
+    __device__ __forceinline__ float exp_total(float *q, float *off) {
+        constexpr int kEach = (kMaxCluster * kWarps + 31) / 32;
+        float Q = -INFINITY, s = 0.f, b = 0.f, e[kEach][3];
 #pragma unroll
-        for (int i = 0; i < (kMaxCluster * kWarps + 31) / 32; ++i) {
+        for (int i = 0; i < kEach; ++i) {
             const uint32_t g = i * 32 + lane;
             e[i][0] = -INFINITY;
-            e[i][1] = 0.f;
-            if (g < cs * kWarps) split(sh->seg[turn][g], e[i][0], e[i][1]);
+            e[i][1] = e[i][2] = 0.f;
+            if (g < cs * kWarps) {
+                split(sh->seg[turn][g], e[i][0], e[i][1]);
+                e[i][2] = __uint_as_float(static_cast<uint32_t>(sh->seg2[turn][g]));
+            }
             Q = fmaxf(Q, e[i][0]);
         }
         turn ^= 1;
 #pragma unroll
         for (int o = 16; o; o >>= 1) Q = fmaxf(Q, __shfl_xor_sync(kAll, Q, o));
 #pragma unroll
-        for (int i = 0; i < (kMaxCluster * kWarps + 31) / 32; ++i)
-            if (e[i][0] > -INFINITY) s += e[i][1] * ptx::ex2(e[i][0] - Q);
+        for (int i = 0; i < kEach; ++i) {
+            if (e[i][0] == -INFINITY) continue;
+            const float f = ptx::ex2(e[i][0] - Q);
+            s += e[i][1] * f;
+            b += (e[i][2] + e[i][1] * (4.f + Q - e[i][0])) * f;
+        }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+        for (int o = 16; o; o >>= 1) {
+            s += __shfl_xor_sync(kAll, s, o);
+            b += __shfl_xor_sync(kAll, b, o);
+        }
         *q = Q;
+        *off = (1.5f * (b / s) + 24.f) * (1.01f * 0x1p-24f);
         return s;
     }
     // The smallest of the groups' maxima that is finite (the row's largest if there is no other).
-    __device__ float least_maximum() {
+    __device__ __forceinline__ float least_maximum() {
         uint32_t k = kAll;
 #pragma unroll
         for (int j = 0; j < kKeysPerThread; ++j) {
@@ -312,7 +363,7 @@ struct Row {
     // A logit that at least `goal` groups reach (so at least `goal` logits), near the goal-th largest
     // group's: the maxima are counted by their distance below the row's in steps of the key's upper
     // 16 bits, two powers of two of them first, coarser where that does not reach.  False: too few groups.
-    __device__ bool threshold(float m, uint32_t goal, float *at) {
+    __device__ __forceinline__ bool threshold(float m, uint32_t goal, float *at) {
         const uint32_t top = order_key(m) >> 16;
         for (int s = 0; s <= 8; s += 4) {
             if (used) {  // (the first time: cleared by row_setup)
@@ -360,7 +411,7 @@ struct Row {
     // threads, kGather at a time, whole warps together; number(j) is vector j's (-1: none).
     static constexpr int kGather = 8;
     template <class F>
-    __device__ void gather(float low, F f) {
+    __device__ __forceinline__ void gather(float low, F f) {
         const uint32_t bound = order_key(low);
         if (tid == 0) sh->hit_n = 0;
         __syncthreads();
@@ -408,7 +459,7 @@ struct Row {
     // Appends to the leader's list, for a whole warp, the logits of the bits (bit j * kPer + q: element q
     // of vector number(j)); returns how many the warp had.
     template <class N>
-    __device__ uint32_t append(unsigned long long bits, int attempt, N number) {
+    __device__ __forceinline__ uint32_t append(unsigned long long bits, int attempt, N number) {
         if (!__any_sync(kAll, bits != 0)) return 0;
         const uint32_t c = __popcll(bits);
         uint32_t incl = c;
@@ -430,7 +481,7 @@ struct Row {
         return total;
     }
     // Every logit >= low into the leader's list; returns, after a barrier of the row, how many there are.
-    __device__ uint32_t collect(float low, int attempt) {
+    __device__ __forceinline__ uint32_t collect(float low, int attempt) {
         uint32_t c = 0;
         gather(low, [&](const uint4(&v)[kGather], auto number) {
             unsigned long long bits = 0;
@@ -440,7 +491,7 @@ struct Row {
         });
         return collected(c, attempt);
     }
-    __device__ uint32_t collected(uint32_t c, int attempt) {
+    __device__ __forceinline__ uint32_t collected(uint32_t c, int attempt) {
         if (lane < static_cast<int>(cs)) st_peer(peer(&sh->hits[attempt][rank * kWarps + warp], lane), c);
         sync();
         c = 0;
@@ -481,7 +532,7 @@ struct Row {
     }
 
     // The sums of v and w over every thread of the row.
-    __device__ void sum2(unsigned long long &v, unsigned long long &w) {
+    __device__ __forceinline__ void sum2(unsigned long long &v, unsigned long long &w) {
         v = warp_sum(v);
         w = warp_sum(w);
         if (lane < static_cast<int>(cs)) {
@@ -498,13 +549,13 @@ struct Row {
         w = warp_sum(w);
         turn ^= 1;
     }
-    __device__ unsigned long long sum(unsigned long long v) {
+    __device__ __forceinline__ unsigned long long sum(unsigned long long v) {
         unsigned long long none = 0;
         sum2(v, none);
         return v;
     }
     // The summed weights 2^((l - m) c) of the groups' maxima that reach `low`, roughly.
-    __device__ float weight_of_maxima(float m, float c, float low) {
+    __device__ __forceinline__ float weight_of_maxima(float m, float c, float low) {
         const uint32_t bound = order_key(low);
         float s = 0.f;
 #pragma unroll
@@ -560,7 +611,7 @@ struct Row {
     // never does.  Each step counts the keys left into 2048 equal bins and goes on inside the one
     // that crosses: 3 steps from 32 bits, 2 from 16.  COUNT: weigh gives 0 or 1.
     template <bool COUNT, class F>
-    __device__ bool reach(uint32_t lo, uint32_t hi, unsigned long long target, F weigh, uint32_t *at, unsigned long long *above) {
+    __device__ __forceinline__ bool reach(uint32_t lo, uint32_t hi, unsigned long long target, F weigh, uint32_t *at, unsigned long long *above) {
         unsigned long long over = 0;
         for (;;) {
             const uint32_t range = hi - lo;
@@ -612,78 +663,94 @@ struct Row {
         return true;
     }
 
-    // The first index, in index order, at which the running sum of weigh(logit, index) reaches
-    // aim(the row's sum): found(index) is called by the one thread of the row that holds it.
+    // Where, in index order, the running sum of weigh(vector, number) reaches aim(the row's sum):
+    // found(vector, number, the sum before it, target) is called by the one thread of the row that has
+    // it.  By warps over runs of the row, then by the warps of the CTA that has it over parts of that
+    // run, then by one warp.
     template <class F, class A, class G>
-    __device__ void locate(F weigh, A aim, G found) {
-        const int run = (n + kWarps - 1) / kWarps;
-        const int s0 = min(n, warp * run), s1 = min(n, s0 + run);
-        unsigned long long v = 0;
-        constexpr int kBatch = 4;
-        for (int i0 = s0 + lane; i0 < s1; i0 += kBatch * 32) {
-            uint4 w[kBatch];
+    __device__ __forceinline__ void locate(F weigh, A aim, G found) {
+        auto run_sum = [&](int s0, int s1) {
+            unsigned long long v = 0;
+            for (int i0 = s0 + lane; i0 - lane < s1; i0 += kBatch * 32) {
+                uint4 w[kBatch];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (i0 + 32 * j < s1) w[j] = part.fetch(i0 + 32 * j);
+                for (int j = 0; j < kBatch; ++j) {
+                    w[j] = nothing();
+                    if (i0 + 32 * j < s1) w[j] = part.fetch(i0 + 32 * j);
+                }
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) {
-                if (i0 + 32 * j >= s1) break;
-                float l[kPer];
-                unpack(w[j], l);
-#pragma unroll
-                for (int q = 0; q < kPer; ++q) v += weigh(l[q], index(i0 + 32 * j, q));
+                for (int j = 0; j < kBatch; ++j) v += weigh(w[j], i0 + 32 * j);
             }
-        }
-        __syncwarp();
-        v = warp_sum(v);
-        const uint32_t me = rank * kWarps + warp;
-        if (lane < static_cast<int>(cs)) st_peer(peer(&sh->seg[turn][me], lane), v);
+            return warp_sum(v);
+        };
+        const int run = (n + kWarps - 1) / kWarps;
+        const unsigned long long mine = run_sum(min(n, warp * run), min(n, (warp + 1) * run));
+        if (lane < static_cast<int>(cs)) st_peer(peer(&sh->seg[turn][rank * kWarps + warp], lane), mine);
         sync();
-        unsigned long long before = 0, total = 0;
-        for (uint32_t g = lane; g < cs * kWarps; g += 32) {
-            const unsigned long long x = sh->seg[turn][g];
-            total += x;
-            if (g < me) before += x;
-        }
-        before = warp_sum(before);
-        turn ^= 1;
+        unsigned long long total = 0;
+        for (uint32_t g = lane; g < cs * kWarps; g += 32) total += sh->seg[turn][g];
         const unsigned long long target = aim(warp_sum(total));
-        if (before >= target || before + v < target) return;  // the whole warp
+        unsigned long long before = 0;
+        uint32_t g = 0;
+        for (; g < cs * kWarps; ++g) {
+            const unsigned long long x = sh->seg[turn][g];
+            if (before + x >= target) break;
+            before += x;
+        }
+        turn ^= 1;
+        if (g / kWarps != rank) return;  // the whole CTA
+        int s0 = min(n, static_cast<int>(g % kWarps) * run), s1 = min(n, s0 + run);
+        const int piece = (s1 - s0 + kWarps - 1) / kWarps;
+        const unsigned long long part_sum = run_sum(min(s1, s0 + warp * piece), min(s1, s0 + (warp + 1) * piece));
+        __syncthreads();
+        if (lane == 0) sh->red[warp] = part_sum;
+        __syncthreads();
+        int w = 0;
+        for (; w < kWarps - 1; ++w) {
+            if (before + sh->red[w] >= target) break;
+            before += sh->red[w];
+        }
+        if (w != warp) return;
+        s1 = min(s1, s0 + (w + 1) * piece);
+        s0 = min(s1, s0 + w * piece);
         for (int base = s0; base < s1; base += 32) {
             const int i = base + lane;
-            float l[kPer];
-            unsigned long long w[kPer], mine = 0;
-            if (i < s1) unpack(part.fetch(i), l);
-#pragma unroll
-            for (int q = 0; q < kPer; ++q) {
-                w[q] = i < s1 ? weigh(l[q], index(i, q)) : 0ull;
-                mine += w[q];
-            }
-            const unsigned long long incl = before + warp_scan(mine, lane);
+            uint4 v = nothing();
+            if (i < s1) v = part.fetch(i);
+            const unsigned long long x = weigh(v, i), incl = before + warp_scan(x, lane);
             const uint32_t hit = __ballot_sync(kAll, incl >= target);
             if (hit) {
-                if (lane == __ffs(hit) - 1) {
-                    unsigned long long at = incl - mine;
-#pragma unroll
-                    for (int q = 0; q < kPer; ++q) {
-                        if (at < target && at + w[q] >= target) found(index(i, q));
-                        at += w[q];
-                    }
-                }
+                if (lane == __ffs(hit) - 1) found(v, i, incl - x, target);
                 return;
             }
             before = __shfl_sync(kAll, incl, 31);
         }
     }
 
-    // The index of the r-th logit of key k, in index order, for every thread of the cluster.
-    template <class P>
-    __device__ int tie_index(uint32_t k, unsigned long long r, P also) {
-        locate([&](float l, int x) { return static_cast<unsigned long long>(key(l) == k && also(l, x)); },
-               [&](unsigned long long) { return r; },
-               [&](int x) {
-                   for (uint32_t p = 0; p < cs; ++p) st_peer(peer(&sh->tie_index, p), static_cast<uint32_t>(x));
-               });
+    // The index of the r-th logit of key k, in index order, among those up to `last`, for every thread
+    // of the row.
+    __device__ __forceinline__ int tie_index(uint32_t k, unsigned long long r, int last) {
+        auto is = [&](float l, int x) { return key(l) == k && x <= last; };
+        locate(
+            [&](const uint4 &v, int i) {
+                float l[kPer];
+                unpack(v, l);
+                unsigned long long c = 0;
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) c += is(l[q], index(i, q));
+                return c;
+            },
+            [&](unsigned long long) { return r; },
+            [&](const uint4 &v, int i, unsigned long long before, unsigned long long target) {
+                float l[kPer];
+                unpack(v, l);
+#pragma unroll
+                for (int q = 0; q < kPer; ++q) {
+                    if (!is(l[q], index(i, q))) continue;
+                    if (++before == target)
+                        for (uint32_t p = 0; p < cs; ++p) st_peer(peer(&sh->tie_index, p), static_cast<uint32_t>(index(i, q)));
+                }
+            });
         sync();
         const int x = static_cast<int>(sh->tie_index);
         sync();  // read everywhere before it is written again

@@ -60,7 +60,7 @@ spec_status rows_args(RowArgs *a, const void *logits, spec_dtype dtype, int B, i
     a->status = dev_status;
     int bits = 1;
     while ((1ll << bits) < V) ++bits;
-    a->U = 62 - bits < 52 ? 62 - bits : 52;
+    a->U = 62 - bits < 48 ? 62 - bits : 48;
     return SPEC_OK;
 }
 

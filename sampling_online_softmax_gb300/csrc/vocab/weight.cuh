@@ -1,20 +1,18 @@
 // weight.cuh -- softmax weights as whole numbers: 2^((l - m) c) in units of
-// 2^-U, right to about 45 bits, in fp32 arithmetic alone.
+// 2^-U, right to about 38 bits, in fp32 arithmetic alone.
 //
 // A draw picks the token at a border of a sum over the whole row, and top-p cuts
 // the order at another, so a weight's error moves the choice wherever tokens are
 // small: with 10^4 tokens in play, weights right to 2^-22 (one ex2.approx) would
 // pick another token than the definition for about one row in a hundred.  GB300's
 // FP64 pipe issues two FMAs a clock per SM, so an exp in double costs a row of
-// 150 k logits over a millisecond; the same accuracy from pairs of floats takes
-// about 50 fp32 operations.  Sums of whole numbers do not depend on their order.
+// 150 k logits over a millisecond; pairs of floats take about 60 fp32 operations.  Sums of whole numbers do not depend on their order.
 //
 // x = (l - m) c is kept as a pair (TwoSum of l and -m, products with their FMA
-// remainders), x = n + t/32 + g with |g| <= 1/64, and
-//   2^x = 2^n T[t] (1 + E),  E = e^y - 1,  y = g ln 2,  |y| < 0.0109,
-// T from a table of float pairs, E by its Taylor series: y and y^2/2 as pairs,
-// y^3/6 + y^4/24 + y^5/120 in fp32 (their sum is below 2^-22, so its rounding is
-// below 2^-45; y^6/720 is below 2^-48).
+// remainders), x = n + t/128 + g with |g| <= 1/256, and
+//   2^x = 2^n T[t] (1 + E),  E = e^y - 1,  y = g ln 2,  |y| < 0.0028,
+// T from a table of float pairs, E by its Taylor series: y as a pair, y^2/2 + y^3/6
+// in fp32 (below 2^-18, so its rounding is below 2^-42; y^4/24 is below 2^-38).
 #pragma once
 
 #include <cstdint>
@@ -29,26 +27,53 @@ namespace vocab {
 #define SPEC_HD inline
 #endif
 
-constexpr int kPow2Steps = 32;
-// 2^(t/32) as a float and the remainder.
-#define SPEC_POW2_TABLE                                                                          \
-    {                                                                                            \
-        {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f},    \
-        {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f}, \
-        {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f}, \
-        {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f}, \
-        {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, \
-        {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f}, \
-        {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, \
-        {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}, {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f}, \
-        {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f}, \
-        {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f}, \
-        {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, \
-        {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f}, \
-        {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, \
-        {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}, {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f}, \
-        {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}, \
-        {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f} \
+constexpr int kPow2Steps = 128, kPow2Bits = 7;
+// 2^(t/128) as a float and the remainder.
+#define SPEC_POW2_TABLE                                                                                        \
+    {                                                                                                          \
+        {0x1.0p+0f, 0x0.0p+0f}, {0x1.0163dap+0f, 0x1.3f6666p-25f}, {0x1.02c9a4p+0f, -0x1.887fap-28f},          \
+        {0x1.04315ep+0f, 0x1.0dcffp-25f}, {0x1.059b0ep+0f, -0x1.9d4f52p-25f}, {0x1.0706b2p+0f, 0x1.3bbedcp-25f}, \
+        {0x1.087452p+0f, -0x1.e2990ep-26f}, {0x1.09e3ecp+0f, 0x1.58de7p-25f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f}, \
+        {0x1.0cc922p+0f, 0x1.6e48fep-25f}, {0x1.0e3ec4p+0f, -0x1.a585ccp-25f}, {0x1.0fb66ap+0f, 0x1.ffda64p-25f}, \
+        {0x1.11301ep+0f, -0x1.fdb496p-25f}, {0x1.12abdcp+0f, 0x1.b0c73p-30f}, {0x1.1429aap+0f, 0x1.d525bcp-25f}, \
+        {0x1.15a98cp+0f, 0x1.14b1cap-25f}, {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.18af94p+0f, -0x1.dcdc86p-26f}, \
+        {0x1.1a35bep+0f, 0x1.6df96ep-25f}, {0x1.1bbe08p+0f, 0x1.011734p-26f}, {0x1.1d4874p+0f, -0x1.d2e8cap-25f}, \
+        {0x1.1ed502p+0f, 0x1.7e6c8ep-27f}, {0x1.2063b8p+0f, 0x1.0c519ap-25f}, {0x1.21f49ap+0f, -0x1.d0446ep-25f}, \
+        {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.251ce4p+0f, 0x1.f654c8p-25f}, {0x1.26b456p+0f, 0x1.789f38p-26f}, \
+        {0x1.284dfep+0f, 0x1.f5638p-28f}, {0x1.29e9ep+0f, -0x1.5c0424p-25f}, {0x1.2b87fep+0f, -0x1.e4a4cep-25f}, \
+        {0x1.2d285ap+0f, 0x1.b900c2p-26f}, {0x1.2ecafap+0f, 0x1.27c5eap-25f}, {0x1.306fep+0f, 0x1.4636e2p-25f}, \
+        {0x1.32171p+0f, -0x1.d993e8p-27f}, {0x1.33c08cp+0f, -0x1.b37d2p-25f}, {0x1.356c56p+0f, -0x1.b5803cp-30f}, \
+        {0x1.371a74p+0f, -0x1.18aac6p-25f}, {0x1.38cae6p+0f, 0x1.a0bb0cp-25f}, {0x1.3a7db4p+0f, -0x1.634c02p-25f}, \
+        {0x1.3c32dcp+0f, 0x1.89d472p-27f}, {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.3fa45p+0f, 0x1.2b2006p-26f}, \
+        {0x1.4160a2p+0f, 0x1.f72e2ap-28f}, {0x1.431f5ep+0f, -0x1.abd5dap-26f}, {0x1.44e086p+0f, 0x1.8624b4p-30f}, \
+        {0x1.46a41ep+0f, 0x1.a3a00ap-25f}, {0x1.486a2cp+0f, -0x1.47d866p-25f}, {0x1.4a32bp+0f, -0x1.e50584p-25f}, \
+        {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.4dcb2ap+0f, -0x1.8088bcp-26f}, {0x1.4f9b28p+0f, -0x1.2c5a6cp-25f}, \
+        {0x1.516daap+0f, 0x1.67b32p-27f}, {0x1.5342b6p+0f, -0x1.2c561p-25f}, {0x1.551a4cp+0f, 0x1.4bb242p-25f}, \
+        {0x1.56f474p+0f, -0x1.295b04p-25f}, {0x1.58d12ep+0f, -0x1.6d07p-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f}, \
+        {0x1.5c9268p+0f, 0x1.4b28d6p-25f}, {0x1.5e76f2p+0f, -0x1.4a5bd6p-25f}, {0x1.605e1cp+0f, -0x1.a248fep-26f}, \
+        {0x1.6247ecp+0f, -0x1.f8b55p-25f}, {0x1.643464p+0f, -0x1.66679cp-25f}, {0x1.662388p+0f, 0x1.2a9112p-27f}, \
+        {0x1.68155ep+0f, -0x1.766ad2p-25f}, {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}, {0x1.6c0128p+0f, -0x1.5e84a8p-25f}, \
+        {0x1.6dfb24p+0f, -0x1.cd72e8p-27f}, {0x1.6ff7ep+0f, -0x1.ab9aep-26f}, {0x1.71f75ep+0f, 0x1.1d8beep-25f}, \
+        {0x1.73f9a4p+0f, 0x1.14b02ep-25f}, {0x1.75feb6p+0f, -0x1.37b306p-25f}, {0x1.780694p+0f, 0x1.fbcba8p-25f}, \
+        {0x1.7a1148p+0f, -0x1.829fdp-25f}, {0x1.7c1edp+0f, 0x1.30c132p-28f}, {0x1.7e2f34p+0f, -0x1.261634p-25f}, \
+        {0x1.804276p+0f, -0x1.783cbep-25f}, {0x1.82589ap+0f, -0x1.accc7cp-26f}, {0x1.8471a4p+0f, 0x1.88f1ecp-26f}, \
+        {0x1.868d9ap+0f, -0x1.2edb44p-26f}, {0x1.88ac7ep+0f, -0x1.9d665ap-26f}, {0x1.8ace54p+0f, 0x1.15506ep-27f}, \
+        {0x1.8cf322p+0f, -0x1.29576ep-25f}, {0x1.8f1aeap+0f, -0x1.baa232p-26f}, {0x1.9145bp+0f, 0x1.723ff8p-25f}, \
+        {0x1.93737cp+0f, -0x1.e64744p-25f}, {0x1.95a44cp+0f, 0x1.790a42p-25f}, {0x1.97d82ap+0f, -0x1.0d8d84p-31f}, \
+        {0x1.9a0f18p+0f, -0x1.e6bf08p-25f}, {0x1.9c4918p+0f, 0x1.51f848p-27f}, {0x1.9e8632p+0f, -0x1.873738p-26f}, \
+        {0x1.a0c668p+0f, -0x1.2886a6p-26f}, {0x1.a309bep+0f, 0x1.8945a6p-25f}, {0x1.a5503cp+0f, -0x1.b83b54p-25f}, \
+        {0x1.a799e2p+0f, -0x1.99e994p-25f}, {0x1.a9e6b6p+0f, -0x1.50c048p-25f}, {0x1.ac36bcp+0f, -0x1.606432p-31f}, \
+        {0x1.ae89fap+0f, -0x1.a94b14p-26f}, {0x1.b0e072p+0f, 0x1.31b6ccp-25f}, {0x1.b33a2cp+0f, -0x1.ec3a82p-26f}, \
+        {0x1.b59728p+0f, 0x1.bcab28p-25f}, {0x1.b7f77p+0f, -0x1.a09438p-25f}, {0x1.ba5b04p+0f, -0x1.ebdf36p-25f}, \
+        {0x1.bcc1eap+0f, -0x1.f687c6p-25f}, {0x1.bf2c26p+0f, -0x1.0a387ep-26f}, {0x1.c199bep+0f, -0x1.3d56b2p-27f}, \
+        {0x1.c40ab6p+0f, -0x1.7c2c98p-39f}, {0x1.c67f12p+0f, 0x1.cafa2ap-25f}, {0x1.c8f6dap+0f, -0x1.7f230ap-25f}, \
+        {0x1.cb720ep+0f, -0x1.8837ccp-27f}, {0x1.cdf0b6p+0f, -0x1.54478p-25f}, {0x1.d072d4p+0f, 0x1.40f13p-25f}, \
+        {0x1.d2f87p+0f, 0x1.01b13ep-25f}, {0x1.d5818ep+0f, -0x1.822dbcp-27f}, {0x1.d80e32p+0f, -0x1.26cf8ep-25f}, \
+        {0x1.da9e6p+0f, 0x1.ed9942p-27f}, {0x1.dd322p+0f, -0x1.9fc974p-25f}, {0x1.dfc974p+0f, -0x1.908c94p-25f}, \
+        {0x1.e26462p+0f, -0x1.614bdap-25f}, {0x1.e502eep+0f, 0x1.e2cffep-26f}, {0x1.e7a52p+0f, -0x1.0e2cep-26f}, \
+        {0x1.ea4afap+0f, 0x1.52486cp-27f}, {0x1.ecf482p+0f, 0x1.b1ccfep-25f}, {0x1.efa1bep+0f, 0x1.cc2b44p-25f}, \
+        {0x1.f252b4p+0f, -0x1.1288aep-25f}, {0x1.f50766p+0f, -0x1.246ebp-26f}, {0x1.f7bfdap+0f, 0x1.b397c2p-25f}, \
+        {0x1.fa7c18p+0f, 0x1.9e90d8p-28f}, {0x1.fd3c22p+0f, 0x1.71ee3ep-25f}                                   \
     }
 
 SPEC_HD float bits_float(int b) {
@@ -61,52 +86,59 @@ SPEC_HD float bits_float(int b) {
 #endif
 }
 
+SPEC_HD int float_bits(float f) {
+#ifdef __CUDA_ARCH__
+    return __float_as_int(f);
+#else
+    int b;
+    memcpy(&b, &f, 4);
+    return b;
+#endif
+}
+
 // What turns a row's logits into weights: the row maximum m, c = log2(e) / T as a pair, U.
 struct Scale {
     float m;
     float ch, cl;
-    int U;  // units of 2^-U; U + bits(V) <= 62, so that a row's sum stays below 2^63
+    int U;  // units of 2^-U; U + bits(V) <= 62, so that a row's sum stays below 2^63, and U <= 48 (fixed_weight)
 };
 
-SPEC_HD unsigned long long fixed_weight(float l, const Scale &s, const float2 *pow2) {
+// Branch-free, so that a vector's logits go through it side by side.
+SPEC_HD unsigned long long fixed_weight(float logit, const Scale &s, const float2 *pow2) {
+    const bool some = (logit - s.m) * s.ch > -60.f;  // else below half a unit for every U; also logit = -inf
+    const float l = some ? logit : s.m;
     const float dh = l - s.m;
     const float ph = dh * s.ch;
-    if (!(ph > -60.f)) return 0ull;  // below half a unit for every U; also l = -inf
     const float bb = dh - l;
     const float dl = (l - (dh - bb)) + (-s.m - bb);
     float pl = fmaf(dh, s.ch, -ph);
     pl = fmaf(dh, s.cl, pl);
     pl = fmaf(dl, s.ch, pl);
-    const float jf = rintf(ph * 32.f);
-    const int j = static_cast<int>(jf);
-    const float gx = fmaf(jf, -0.03125f, ph);  // exact: both are multiples of ph's last place
-    const float g = gx + pl;                   // |pl| reaches 2^-18: left apart, y^3/6 would miss it
+    const float shifted = fmaf(ph, 128.f, 0x1.8p23f);  // its last bits are the nearest whole number to 128 ph
+    const int j = float_bits(shifted) - 0x4b400000;
+    const float gx = fmaf(shifted - 0x1.8p23f, -0x1p-7f, ph);  // exact: both are multiples of ph's last place
+    const float g = gx + pl;                                   // |pl| reaches 2^-18: left apart, y^3/6 would miss it
     const float gl = pl - (g - gx);
     constexpr float kLn2h = 0x1.62e430p-1f, kLn2l = -0x1.05c610p-29f;
     const float yh = g * kLn2h;
     float yl = fmaf(g, kLn2h, -yh);
     yl = fmaf(g, kLn2l, yl);
     yl = fmaf(gl, kLn2h, yl);
-    const float sh = yh * yh;
-    const float sl = fmaf(yh, yh, -sh);
-    const float c3 = sh * yh * fmaf(yh, fmaf(yh, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f);
-    const float h = 0.5f * sh;
-    const float eh = yh + h;
-    const float el = (h - (eh - yh)) + (fmaf(0.5f, sl, yl) + fmaf(yh, yl, c3));
+    const float el = fmaf(yh * yh, fmaf(yh, 1.f / 6.f, 0.5f), yl);
     const float2 T = pow2[j & (kPow2Steps - 1)];
-    const float qh = T.x * eh;
-    const float ql = fmaf(T.x, el, fmaf(T.x, eh, -qh)) + T.y * eh;
+    const float qh = T.x * yh;
+    const float ql = fmaf(T.x, el, fmaf(T.y, yh, fmaf(T.x, yh, -qh)));
     const float wh = T.x + qh;
     const float wl = (qh - (wh - T.x)) + (T.y + ql);
     // wh + wl in units of 2^-U as (whole multiple of 2^22) + rest: scaled by a power of two, so exactly
-    const int e = (j >> 5) + s.U - 22;                   // 2^e units of 2^(22 - U); e in [-41, 30]
-    if (e < -24) return 0ull;                            // below half a unit
+    const int e = (j >> kPow2Bits) + s.U - 22;                 // in [-41, 26]: |wl| < 2^-17 keeps lo below 2^31
     const float up = bits_float((e + 127) << 23);
     const float t = wh * up;
     const uint32_t hi = static_cast<uint32_t>(t);
     const float rest = (t - static_cast<float>(hi)) + wl * up;  // exact, then one rounding
     const int lo = static_cast<int>(rintf(rest * 0x1p22f));
-    return (static_cast<unsigned long long>(hi) << 22) + static_cast<long long>(lo);
+    const unsigned long long v = (static_cast<unsigned long long>(hi) << 22) + static_cast<long long>(lo);
+    return some ? v : 0ull;
 }
 
 // floor(W * f) for f in [0, 1), and whether f * W is no whole number, exactly.

@@ -2,7 +2,7 @@
 
 Tokens, ids and values must be equal: the inputs' draws lie further than
 2^-36 from every border of the distribution (asserted; the kernel's weights
-are right to about 2^-43), so no tolerance is needed.
+are right to about 2^-38), so no tolerance is needed.
 """
 import numpy as np
 import pytest
