@@ -387,7 +387,7 @@ SPEC_API spec_status spec_top_logits(const void *logits, spec_dtype dtype, int B
  *   row_weight [N] fp32 or NULL (1): a row of weight 0 is ignored: its logits and
  *              its teacher are not read, its loss, statistics and gradient are 0.
  * Outputs:
- *   loss  [N] fp32;  stats [N, 2] fp32: the row's largest logit and
+ *   loss  [N] fp32;  stats [N, 2] fp32 (8-byte aligned): the row's largest logit and
  *         sum_v exp((s_v - largest) / T), for spec_distill_backward.
  *   grad  [N, V] of the logits' type, or NULL: the gradient of the sum of the
  *         losses, overwritten; it may be student_logits itself (in place).

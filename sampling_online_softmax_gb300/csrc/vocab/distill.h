@@ -9,6 +9,7 @@ namespace spec {
 namespace vocab {
 
 constexpr int kDThreads = 256;
+constexpr int kPartBytes = 64 * 1024;  // of a row, at most, in a CTA's shared memory (loss and gradient)
 
 struct DistillArgs {
     const unsigned char *student, *student_end;  // [N, V] logits
@@ -28,7 +29,8 @@ struct DistillArgs {
 
 enum DistillForm : int { kLoss = 0, kLossGrad = 1, kBackward = 2 };
 
-spec_status launch_distill(DistillArgs a, int eb, int form, cudaStream_t stream);
+template <int EB>
+spec_status launch_distill(const DistillArgs &a, int form, cudaStream_t stream);
 
 }  // namespace vocab
 }  // namespace spec

@@ -4,10 +4,40 @@
 // of a neighbouring row (read as -inf).  Bytes outside the tensor are never read.
 #pragma once
 
+#include "../ptx.cuh"
 #include "cluster.cuh"
 
 namespace spec {
 namespace vocab {
+
+// Pairs of floats in one instruction each.
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(unsigned long long p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 template <int EB>
 struct Part {
@@ -37,12 +67,21 @@ struct Part {
     __device__ __forceinline__ bool edge(int i) const { return first + i == 0 || first + i == total - 1; }
     __device__ __forceinline__ bool inside(int i) const { return at(i) >= base && at(i) + 16 <= end; }
 
-    __device__ __forceinline__ void copy(uint4 *buf, int i) const {
-        if (inside(i)) copy16(smem_u32(buf + i), at(i));
+    // This thread's vectors (i = tid, tid + step, ...) to shared memory, asynchronously; then the row's
+    // first and last, which may hold a neighbour's logits or lie across the tensor's end, by the threads
+    // that own them.
+    __device__ __forceinline__ void copy_all(uint4 *buf, int tid, int step) const {
+        if (n <= 0) return;
+        const int from = inside(0) ? 0 : 1, upto = inside(n - 1) ? n : n - 1;
+        const unsigned char *src = at(tid);
+        uint32_t dst = smem_u32(buf + tid);
+        for (int i = tid; i < upto; i += step, src += 16 * step, dst += 16 * step)
+            if (i >= from) copy16(dst, src);
     }
-    // After the copy: an edge vector's logits outside the row become -inf.
-    __device__ __forceinline__ void mend(uint4 *buf, int i) const {
-        if (edge(i)) buf[i] = by_logit(at(i), index(i, 0), V);
+    __device__ __forceinline__ void mend_all(uint4 *buf, int tid, int step) const {
+        if (n <= 0) return;
+        if (tid == 0 && edge(0)) buf[0] = by_logit(at(0), index(0, 0), V);
+        if (tid == (n - 1) % step && edge(n - 1)) buf[n - 1] = by_logit(at(n - 1), index(n - 1, 0), V);
     }
     // Vector `at`, whose first element is logit x0 of the row, element by element.
     static __device__ __noinline__ uint4 by_logit(const unsigned char *at, int x0, int V) {
@@ -78,6 +117,19 @@ struct Part {
                 l[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
             }
         }
+    }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    // The largest logit of a vector, NaN if it holds one.
+    static __device__ __forceinline__ float vector_max(const uint4 &v) {
+        if (EB == 2) {
+            const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+            return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+        }
+        return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
     static __device__ __forceinline__ float logit(const void *p, int i) {
         return EB == 4 ? reinterpret_cast<const float *>(p)[i]

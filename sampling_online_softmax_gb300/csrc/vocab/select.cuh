@@ -19,7 +19,6 @@
 // choose.  Few rows: a cluster shares a row through distributed shared memory.
 #pragma once
 
-#include "../ptx.cuh"
 #include "part.cuh"
 #include "rows.h"
 #include "weight.cuh"
@@ -91,12 +90,6 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v, in
     }
     return v;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 // Sum over the block of v.
 __device__ __forceinline__ unsigned long long block_sum(unsigned long long v, unsigned long long *red, int lane, int warp) {
     v = warp_sum(v);
@@ -107,24 +100,6 @@ __device__ __forceinline__ unsigned long long block_sum(unsigned long long v, un
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) v += red[w];
     return v;
-}
-
-// Pairs of floats in one instruction each.
-__device__ __forceinline__ unsigned long long pair(float a, float b) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void split(unsigned long long p, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 template <int EB>
@@ -155,19 +130,7 @@ struct Row {
             cluster_sync();
     }
 
-    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
-        uint32_t r;
-        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
-    // The largest logit of a vector, NaN if it holds one.
-    static __device__ __forceinline__ float vector_max(const uint4 &v) {
-        if (EB == 2) {
-            const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
-            return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-        }
-        return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
-    }
+    static __device__ __forceinline__ float vector_max(const uint4 &v) { return P::vector_max(v); }
     // 2^(l c - q) of two logits; adds weight times exponent to `b`.
     template <bool BOUND>
     static __device__ __forceinline__ unsigned long long exp_pair(float l0, float l1, unsigned long long c2, unsigned long long q2,

@@ -127,12 +127,14 @@ extern "C" spec_status spec_distill(const void *student_logits, spec_dtype dtype
     spec_status st = distill_args(&a, student_logits, dtype, N, V, top_ids, top_logits, K, top_lse, temperature, row_weight, dev_status);
     if (st != SPEC_OK || N == 0) return st;
     if (!loss || !stats) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
-    if (!aligned(loss, 4) || !aligned(stats, 4) || !aligned(grad, elt_bytes(dtype)))
+    if (!aligned(loss, 4) || !aligned(stats, 8) || !aligned(grad, elt_bytes(dtype)))
         return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
     a.loss = loss;
     a.stats = stats;
     a.grad = static_cast<unsigned char *>(grad);
-    return launch_distill(a, elt_bytes(dtype), grad ? kLossGrad : kLoss, static_cast<cudaStream_t>(stream));
+    const int form = grad ? kLossGrad : kLoss;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == SPEC_F32 ? launch_distill<4>(a, form, s) : launch_distill<2>(a, form, s);
 }
 
 extern "C" spec_status spec_distill_backward(const void *student_logits, spec_dtype dtype, int N, int V, const int32_t *top_ids,
@@ -144,10 +146,11 @@ extern "C" spec_status spec_distill_backward(const void *student_logits, spec_dt
     spec_status st = distill_args(&a, student_logits, dtype, N, V, top_ids, top_logits, K, top_lse, temperature, row_weight, dev_status);
     if (st != SPEC_OK || N == 0) return st;
     if (!stats || !grad_loss || !grad) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
-    if (!aligned(stats, 4) || !aligned(grad_loss, 4) || !aligned(grad, elt_bytes(dtype)))
+    if (!aligned(stats, 8) || !aligned(grad_loss, 4) || !aligned(grad, elt_bytes(dtype)))
         return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
     a.stats = const_cast<float *>(stats);
     a.grad_loss = grad_loss;
     a.grad = static_cast<unsigned char *>(grad);
-    return launch_distill(a, elt_bytes(dtype), kBackward, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == SPEC_F32 ? launch_distill<4>(a, kBackward, s) : launch_distill<2>(a, kBackward, s);
 }
