@@ -6,7 +6,9 @@
 //
 // HBM bounds all three forms.  Loss and gradient in one call read each logit once:
 // a cluster keeps the row in its CTAs' shared memory between the exp-sum and the
-// gradient.  A CTA writes its share of P q_v densely and then, after a block
+// gradient, and goes on to another row: as a thread takes a vector for the
+// gradient, it sends for the next row's into its place, so that memory is read
+// while the gradient is written and the next teacher weighed.  A CTA writes its share of P q_v densely and then, after a block
 // barrier, the columns of its own teacher entries over it; an entry's column
 // is written by one thread (the first slot that names it), which adds the slots
 // that name it too in their order, so the gradient does not depend on timing.
@@ -29,9 +31,10 @@ template <int SLOTS>
 struct alignas(16) DistillShared {
     int32_t id[SLOTS * kDThreads];  // teacher entries in this CTA's part (-1: none, elsewhere, or out of range)
     float p[SLOTS * kDThreads];
-    float red[5][kDWarps];
-    float4 slot[kMaxCluster];       // of each CTA: its maximum, exp-sum, sum of p (log p - (s - m) / T), sum of p
-    int twice;                      // some column is named by two entries
+    float2 part[kDWarps];           // each warp's share of the teacher's normaliser: a maximum and a sum
+    float2 slot[2][kMaxCluster * kDWarps];  // of each warp of the row: its maximum and exp-sum
+    float loss[2][kMaxCluster * kDWarps];   // and (rank 0) its share of the loss
+    int twice[2];                   // some column is named by two entries
 };
 
 __device__ __forceinline__ float warp_add(float v) {
@@ -47,6 +50,13 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // Beyond it a maximum's product with c is taken for overflowing, and (l - m) c is computed as that.
 constexpr float kHuge = 1e38f;
+// 2^((l - m) c) of two logits: as l c - q, q the rounded m c (PLAIN), or as it stands.
+template <bool PLAIN>
+__device__ __forceinline__ unsigned long long exp2_pair(float l0, float l1, float c, float m, float q) {
+    float x, y;
+    split(PLAIN ? fma2(pair(l0, l1), pair(c, c), pair(-q, -q)) : mul2(add2(pair(l0, l1), pair(-m, -m)), pair(c, c)), x, y);
+    return pair(ptx::ex2(x), ptx::ex2(y));
+}
 
 template <int EB, int SLOTS>
 struct Distill {
@@ -62,49 +72,37 @@ struct Distill {
     float t[SLOTS];   // the teacher's logits, then log p
 
     __device__ __forceinline__ Distill(const DistillArgs &a_, DistillShared<SLOTS> *s, int row, uint32_t rank) : a(a_), sh(s) {
-        b = row;
         tid = threadIdx.x;
         lane = tid & 31;
         warp = tid >> 5;
         c = kLog2ef / a.T;
         invT = 1.f / a.T;
+        place(row, rank);
+    }
+    __device__ __forceinline__ void place(int row, uint32_t rank) {
+        b = row;
         part.place(a.student, a.student_end, a.V, b, rank, a.part);
     }
-    template <class F>
-    __device__ __forceinline__ float block(float v, float none, int which, F join) {
-        if (lane == 0) sh->red[which][warp] = v;
-        __syncthreads();
-        v = none;
-#pragma unroll
-        for (int i = 0; i < kDWarps; ++i) v = join(v, sh->red[which][i]);
-        return v;
-    }
-    __device__ __forceinline__ float block_add(float v, int which) {
-        return block(warp_add(v), 0.f, which, [](float x, float y) { return x + y; });
-    }
-    __device__ __forceinline__ float block_max(float v, int which) {
-        return block(warp_max(v), -INFINITY, which, [](float x, float y) { return fmaxf(x, y); });
-    }
-
     // The teacher's entries, on their way while the copies of the logits are issued.
-    __device__ __forceinline__ void ask_teacher() {
-        const size_t at = static_cast<size_t>(b) * a.K;
+    __device__ __forceinline__ void ask_teacher(int row, int32_t (&ids)[SLOTS], float (&logits)[SLOTS]) const {
+        const size_t at = static_cast<size_t>(row) * a.K;
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
             const int k = tid + j * kDThreads;
-            id[j] = -1;
-            t[j] = -INFINITY;
+            ids[j] = -1;
+            logits[j] = -INFINITY;
             if (k < a.K) {
-                id[j] = __ldg(a.ids + at + k);
-                t[j] = __ldg(a.top + at + k);
+                ids[j] = __ldg(a.ids + at + k);
+                logits[j] = __ldg(a.top + at + k);
             }
         }
     }
-    // Every CTA of a row weighs all K entries (P has to be the same everywhere) and keeps those in its
-    // part, marked in a bitmap, one bit a logit; sh->twice: a column was marked before.  `bits` has been
-    // cleared, a block barrier ago.
-    __device__ __forceinline__ void teacher(uint32_t *bits) {
-        float top = -INFINITY;
+    // Every CTA of a row weighs all K entries (P has to be the same everywhere).  First each warp's share
+    // of the normaliser, then, after a block barrier, log p and p, which it keeps for the entries in its
+    // part.  Their columns are marked in a bitmap, one bit a logit, cleared before; sh->twice[turn]: a
+    // column was marked before.
+    __device__ __forceinline__ void teacher_share() {
+        float top = -INFINITY, s = 0.f;
         bool wrong = false, off = false;
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
@@ -113,65 +111,128 @@ struct Distill {
             if (!(t[j] < INFINITY)) wrong = true;
             top = fmaxf(top, t[j]);
         }
-        float norm;  // log p = (t - top) / T - norm
+        if (off) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
         if (a.lse) {
-            top = 0.f;
-            norm = __ldg(a.lse + b);
-            if (!(fabsf(norm) < INFINITY)) wrong = true;
-        } else {
-            top = block_max(top, 0);
-            float s = 0.f;
+            top = 0.f;  // log p = t / T - lse
+            const float z = __ldg(a.lse + b);
+            if (!(fabsf(z) < INFINITY)) wrong = true;
 #pragma unroll
-            for (int j = 0; j < SLOTS; ++j)
-                if (t[j] > -INFINITY) s += expf((t[j] - top) * invT);
-            s = block_add(s, 1);
-            norm = s > 0.f ? logf(s) : 0.f;
+            for (int j = 0; j < SLOTS; ++j) {
+                const bool any = t[j] > -INFINITY;
+                t[j] = any ? t[j] * invT - z : -INFINITY;
+                s += any ? expf(t[j]) : 0.f;
+            }
+        } else if (__any_sync(kAllLanes, top > -INFINITY)) {
+            top = warp_max(top);
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) s += t[j] > -INFINITY ? expf((t[j] - top) * invT) : 0.f;
         }
-        float sum = 0.f;
+        if (wrong) s = NAN;
+        if (__any_sync(kAllLanes, s != 0.f)) s = warp_add(s);
+        if (lane == 0) sh->part[warp] = make_float2(top, s);
+    }
+    __device__ __forceinline__ void teacher_finish(uint32_t *bits, int turn) {
+        float top = -INFINITY, s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kDWarps; ++i) top = fmaxf(top, sh->part[i].x);
+#pragma unroll
+        for (int i = 0; i < kDWarps; ++i) {
+            const float2 v = sh->part[i];
+            s += a.lse ? v.y : v.y == 0.f ? 0.f : v.y * expf((v.x - top) * invT);
+        }
+        sum_p = a.lse || !(s > 0.f) ? s : 1.f;  // (NaN stays)
+        const float norm = !a.lse && s > 0.f ? logf(s) : 0.f;
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
             const bool any = t[j] > -INFINITY;
-            t[j] = any ? (t[j] - top) * invT - norm : 0.f;
+            if (!a.lse) t[j] = any ? (t[j] - top) * invT - norm : 0.f;
             const float p = any ? expf(t[j]) : 0.f;
-            sum += p;
             const int k = tid + j * kDThreads;
             const int o = id[j] >= 0 ? part.offset(id[j]) : -1;
             if (o < 0 || o >= part.n * kPer) id[j] = -1;
             sh->id[k] = id[j];
             sh->p[k] = p;
-            if (bits && id[j] >= 0 && (atomicOr(&bits[o >> 5], 1u << (o & 31)) >> (o & 31) & 1u)) sh->twice = 1;
+            if (bits && id[j] >= 0 && (atomicOr(&bits[o >> 5], 1u << (o & 31)) >> (o & 31) & 1u)) sh->twice[turn] = 1;
         }
-        if (off) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
-        sum_p = block_add(wrong ? NAN : sum, 2);
     }
     __device__ __forceinline__ void clear(uint32_t *bits) {
-        for (int i = tid; i < (part.n * kPer + 31) / 32; i += kDThreads) bits[i] = 0;
-        if (tid == 0) sh->twice = 0;
+        for (int i = tid; i < (a.part * kPer + 31) / 32; i += kDThreads) bits[i] = 0;
     }
 
-    __device__ __forceinline__ void store(int i, const float (&v)[kPer], bool same) const {
-        unsigned char *d = a.grad + (part.at(i) - a.student);
-        if (same && !part.edge(i)) {
-            uint4 o;
-            if (EB == 4) {
-                o = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-            } else {
-                uint32_t w[4];
+    // The vectors of the part that lie in the row alone: [first, end).  The others, at most the row's
+    // first and last, are written by logit, as all are where the tensors' vectors do not lie alike.
+    __device__ __forceinline__ int whole_from() const { return part.n > 0 && part.edge(0) ? 1 : 0; }
+    __device__ __forceinline__ int whole_upto() const { return part.n > 0 && part.edge(part.n - 1) ? part.n - 1 : part.n; }
+    static __device__ __forceinline__ uint4 packed(const float (&v)[kPer]) {
+        uint32_t w[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[q]) : "f"(v[(2 * q + 1) % kPer]), "f"(v[(2 * q) % kPer]));
-                o = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            *reinterpret_cast<uint4 *>(d) = o;
-        } else {
-            store_each(i, v);
+        for (int q = 0; q < 4; ++q) {
+            if (EB == 4)
+                w[q] = __float_as_uint(v[q]);
+            else
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[q]) : "f"(v[(2 * q + 1) % kPer]), "f"(v[(2 * q) % kPer]));
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // The gradients make(load(i), floats) of every vector i, into whole vectors' places or by logit.  A
+    // batch of loads goes before its stores: grad may be student, so the compiler would keep their order
+    // and wait for each load alone.
+    static constexpr int kBatch = 4;
+    // The whole vectors' first batch for write(), loaded ahead of what it waits for.
+    template <class L>
+    __device__ __forceinline__ void ask_first(L load, uint4 (&v)[kBatch]) const {
+        const int upto = whole_upto(), i = tid < whole_from() ? tid + kDThreads : tid;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (i + j * kDThreads < upto) v[j] = load(i + j * kDThreads);
         }
     }
-    __device__ __forceinline__ void store_each(int i, const float (&v)[kPer]) const {
+    template <class L, class F>
+    __device__ __forceinline__ void write(L load, F make, const uint4 (*ahead)[kBatch] = nullptr) const {
+        const bool alike = ((reinterpret_cast<uintptr_t>(a.grad) ^ reinterpret_cast<uintptr_t>(a.student)) & 15) == 0;
+        const int from = alike ? whole_from() : 0, upto = alike ? whole_upto() : 0;
+        int i = tid < from ? tid + kDThreads : tid;
+        unsigned char *dst = a.grad + (part.at(0) - a.student) + static_cast<size_t>(i) * 16;
+        auto put = [](unsigned char *at, const uint4 &v) {
+            asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(__cvta_generic_to_global(at)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+        };
+        if (ahead && alike) {
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) {
-            const int x = part.index(i, q);
-            if (x >= 0 && x < a.V) store_one(x, v[q]);
+            for (int j = 0; j < kBatch; ++j) {
+                if (i + j * kDThreads >= upto) break;
+                float l[kPer];
+                make((*ahead)[j], l);
+                put(dst + 16 * j * kDThreads, packed(l));
+            }
+            i += kBatch * kDThreads;
+            dst += 16 * kBatch * kDThreads;
+        }
+        for (; i + (kBatch - 1) * kDThreads < upto; i += kBatch * kDThreads, dst += 16 * kBatch * kDThreads) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) v[j] = load(i + j * kDThreads);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                float l[kPer];
+                make(v[j], l);
+                put(dst + 16 * j * kDThreads, packed(l));
+            }
+        }
+        for (; i < upto; i += kDThreads, dst += 16 * kDThreads) {
+            float l[kPer];
+            make(load(i), l);
+            put(dst, packed(l));
+        }
+        for (int j = tid; j < part.n; j += kDThreads) {
+            if (j >= from && j < upto) continue;
+            float l[kPer];
+            make(load(j), l);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+                const int x = part.index(j, q);
+                if (x >= 0 && x < a.V) store_one(x, l[q]);
+            }
         }
     }
     __device__ __forceinline__ void store_one(int x, float v) const {
@@ -181,46 +242,44 @@ struct Distill {
         else
             reinterpret_cast<__nv_bfloat16 *>(a.grad)[e] = __float2bfloat16_rn(v);
     }
-    // The two tensors' vectors lie alike, so a vector of logits gives a vector of gradients.
-    __device__ __forceinline__ bool alike() const {
-        return ((reinterpret_cast<uintptr_t>(a.grad) ^ reinterpret_cast<uintptr_t>(a.student)) & 15) == 0;
-    }
-    __device__ __forceinline__ void fill(float v) const {
-        float g[kPer];
+    __device__ __forceinline__ void fill(float g) const {
+        write([](int) { return make_uint4(0, 0, 0, 0); },
+              [&](const uint4 &, float(&v)[kPer]) {
 #pragma unroll
-        for (int q = 0; q < kPer; ++q) g[q] = v;
-        const bool same = alike();
-        for (int i = tid; i < part.n; i += kDThreads) store(i, g, same);
+                  for (int q = 0; q < kPer; ++q) v[q] = g;
+              });
     }
-    // (w / T) P q_v for every column of the part (logits from `get`), then the teacher's columns.
-    // g: w / T; m, S: the row's maximum and exp-sum.
-    template <class G, class L>
-    __device__ __forceinline__ void gradient(float g, float m, float S, G get, L logit_at) {
+    template <bool PLAIN, class G>
+    __device__ __forceinline__ void dense(float m, float q, float A, G get, const uint4 (*ahead)[kBatch]) const {
+        write(
+            get,
+            [&](const uint4 &v, float(&l)[kPer]) {
+                P::unpack(v, l);
+#pragma unroll
+                for (int e = 0; e < kPer; e += 2) split(mul2(exp2_pair<PLAIN>(l[e], l[e + 1], c, m, q), pair(A, A)), l[e], l[e + 1]);
+            },
+            ahead);
+    }
+    // The logits of this thread's entries.
+    template <class L>
+    __device__ __forceinline__ void own_logits(L logit_at, float (&own)[SLOTS]) const {
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) own[j] = id[j] >= 0 ? logit_at(id[j]) : 0.f;
+    }
+    // (w / T) P q_v for every column of the part (logits from `get`), then, after a block barrier, the
+    // teacher's columns over it.  g: w / T; m, S: the row's maximum and exp-sum; own: read before
+    // anything is written, as grad may be student.
+    template <class G>
+    __device__ __forceinline__ void gradient(float g, float m, float S, const float (&own)[SLOTS], int turn, G get,
+                                             const uint4 (*ahead)[kBatch] = nullptr) {
         // exponents as l c - q, q the rounded m c, whose rounding goes into the factor
         const float q = m * c, A = g * sum_p / S;
-        const bool plain = fabsf(q) < kHuge;
-        const float A_ = plain ? A * (1.f - 0.6931471805599453f * fmaf(-m, c, q)) : A;
-        const bool same = alike();
-        float own[SLOTS];
-#pragma unroll
-        for (int j = 0; j < SLOTS; ++j) own[j] = id[j] >= 0 ? logit_at(id[j]) : 0.f;  // before anything is written: grad may be student
+        if (fabsf(q) < kHuge)
+            dense<true>(m, q, A * (1.f - 0.6931471805599453f * fmaf(-m, c, q)), get, ahead);
+        else
+            dense<false>(m, q, A, get, ahead);
         __syncthreads();
-        const bool twice = sh->twice != 0;
-        const unsigned long long A2 = pair(A_, A_), c2 = pair(c, c), q2 = pair(-q, -q);
-#pragma unroll 4
-        for (int i = tid; i < part.n; i += kDThreads) {
-            float l[kPer];
-            P::unpack(get(i), l);
-#pragma unroll
-            for (int e = 0; e < kPer; e += 2) {
-                float x, y;
-                const unsigned long long two = pair(l[e], l[e + 1]);
-                split(plain ? fma2(two, c2, q2) : mul2(add2(two, pair(-m, -m)), c2), x, y);
-                split(mul2(pair(ptx::ex2(x), ptx::ex2(y)), A2), l[e], l[e + 1]);
-            }
-            store(i, l, same);
-        }
-        __syncthreads();
+        const bool twice = sh->twice[turn] != 0;
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
             const int x = id[j];
@@ -262,8 +321,13 @@ struct Running {
             q = to;
         }
         if (m == -INFINITY) return;  // masked so far
-        const bool plain = fabsf(q) < kHuge;
-        const unsigned long long c2 = pair(c, c), q2 = pair(-q, -q);
+        if (fabsf(q) < kHuge)
+            weigh<true>(v, c);
+        else
+            weigh<false>(v, c);
+    }
+    template <bool PLAIN, int N>
+    __device__ __forceinline__ void weigh(const uint4 (&v)[N], float c) {
         unsigned long long sum = 0;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -271,12 +335,7 @@ struct Running {
             P::unpack(v[j], l);
             unsigned long long e[P::kPer / 2];
 #pragma unroll
-            for (int i = 0; i < P::kPer / 2; ++i) {
-                float x, y;
-                const unsigned long long two = pair(l[2 * i], l[2 * i + 1]);
-                split(plain ? fma2(two, c2, q2) : mul2(add2(two, pair(-m, -m)), c2), x, y);
-                e[i] = pair(ptx::ex2(x), ptx::ex2(y));
-            }
+            for (int i = 0; i < P::kPer / 2; ++i) e[i] = exp2_pair<PLAIN>(l[2 * i], l[2 * i + 1], c, m, q);
 #pragma unroll
             for (int h = P::kPer / 4; h; h >>= 1)
 #pragma unroll
@@ -285,6 +344,33 @@ struct Running {
         }
         s = add2(s, sum);
     }
+    // A thread's vectors of the part, from global memory; meanwhile() runs while the first are on their way.
+    template <class F>
+    __device__ __forceinline__ void stream(const P &part, int tid, float c, F meanwhile) {
+        constexpr int kBatch = 4;
+        const int n = part.n;
+        uint4 v[kBatch];
+        auto load = [&](int i) {
+            if (i > 0 && i + (kBatch - 1) * kDThreads < n - 1) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(part.at(i));
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) v[j] = src[j * kDThreads];
+            } else {  // (-inf beyond the end)
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    v[j] = P::nothing();
+                    if (i + j * kDThreads < n) v[j] = part.fetch(i + j * kDThreads);
+                }
+            }
+        };
+        load(tid);
+        meanwhile();
+        for (int i = tid; i < n;) {
+            add(v, c);
+            i += kBatch * kDThreads;
+            if (i < n) load(i);
+        }
+    }
     __device__ __forceinline__ float sum(float c) const {
         float x, y;
         split(s, x, y);
@@ -292,42 +378,145 @@ struct Running {
     }
 };
 
-// Loss and row statistics, and with GRAD the gradient: a cluster per row.
-template <int EB, int SLOTS, bool GRAD>
-__global__ void __launch_bounds__(kDThreads, 4) distill_kernel(const DistillArgs a) {
+// A warp's maximum and exp-sum, to every CTA of the row; row_sums() after the row's barrier.
+template <int EB, int SLOTS>
+__device__ __forceinline__ void post_sums(Distill<EB, SLOTS> &d, const Running<EB> &r, uint32_t rank, int turn) {
+    const float m = warp_max(r.m);  // (NaN passes through the sums)
+    const float s = warp_add(r.m == -INFINITY ? 0.f : r.sum(d.c) * ptx::ex2((r.m - m) * d.c));
+    if (d.lane < d.a.cluster) st_peer(peer(&d.sh->slot[turn][rank * kDWarps + d.warp], d.lane), pair(m, s));
+}
+template <int EB, int SLOTS>
+__device__ __forceinline__ void row_sums(const Distill<EB, SLOTS> &d, int turn, float *row_m, float *row_s) {
+    constexpr int kEach = (kMaxCluster * kDWarps + 31) / 32;
+    float2 v[kEach];
+    float m = -INFINITY, s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int g = i * 32 + d.lane;
+        v[i] = g < d.a.cluster * kDWarps ? d.sh->slot[turn][g] : make_float2(-INFINITY, 0.f);
+        m = fmaxf(m, v[i].x);
+    }
+    m = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) s += v[i].x == -INFINITY ? v[i].y : v[i].y * ptx::ex2((v[i].x - m) * d.c);  // (masked: 0, or NaN)
+    *row_m = m;
+    *row_s = warp_add(s);
+}
+// This warp's share of the row's loss, to the CTA of rank 0: sum of p (log p - log q).
+template <int EB, int SLOTS>
+__device__ __forceinline__ void post_loss(Distill<EB, SLOTS> &d, const float (&own)[SLOTS], float m, float s, uint32_t rank, int turn) {
+    const float log_s = logf(s);
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < SLOTS; ++j) {
+        const float p = d.id[j] >= 0 ? d.sh->p[d.tid + j * kDThreads] : 0.f;
+        // a masked token that the teacher wants: +inf
+        if (p != 0.f) v += p * (d.t[j] - (own[j] == -INFINITY ? own[j] : (own[j] - m) * d.invT) + log_s);
+    }
+    if (__any_sync(kAllLanes, v != 0.f)) v = warp_add(v);
+    if (d.lane == 0) st_peer(peer(&d.sh->loss[turn][rank * kDWarps + d.warp], 0), __float_as_uint(v));
+}
+// A row's loss and statistics, by a warp of rank 0 after the barrier that follows post_loss.
+template <int EB, int SLOTS>
+__device__ __forceinline__ void write_row(const Distill<EB, SLOTS> &d, int row, float w, bool sound, float m, float s, int turn) {
+    float v = 0.f;
+    for (int g = d.lane; g < d.a.cluster * kDWarps; g += 32) v += d.sh->loss[turn][g];
+    v = warp_add(v);
+    if (d.lane == 0) {
+        d.a.loss[row] = sound ? w * v : NAN;
+        reinterpret_cast<float2 *>(d.a.stats)[row] = sound ? make_float2(m, s) : make_float2(NAN, NAN);
+        if (!sound) atomicOr(d.a.status, SPEC_DEV_NONFINITE);
+    }
+}
+template <int EB, int SLOTS>
+__device__ __forceinline__ bool row_sound(const Distill<EB, SLOTS> &d, float m, float s) {  // not: NaN, +inf, or nothing but -inf
+    return d.sum_p == d.sum_p && m < INFINITY && s > 0.f && s < INFINITY;
+}
+template <int EB, int SLOTS>
+__device__ __forceinline__ void ignored(const Distill<EB, SLOTS> &d, uint32_t rank) {
+    if (rank == 0 && d.tid == 0) {
+        d.a.loss[d.b] = 0.f;
+        reinterpret_cast<float2 *>(d.a.stats)[d.b] = make_float2(0.f, 0.f);
+    }
+}
+
+// Loss and row statistics: a cluster per row.
+template <int EB, int SLOTS>
+__global__ void __launch_bounds__(kDThreads, 4) distill_loss_kernel(const DistillArgs a) {
     extern __shared__ uint4 dyn[];
-    DistillShared<SLOTS> *sh = reinterpret_cast<DistillShared<SLOTS> *>(dyn);
-    uint4 *buf = dyn + sizeof(DistillShared<SLOTS>) / 16;
-    uint32_t *bits = GRAD ? reinterpret_cast<uint32_t *>(buf + a.part) : nullptr;
     const uint32_t rank = cluster_rank();
-    const int b = blockIdx.x / a.cluster;
-    Distill<EB, SLOTS> d(a, sh, b, rank);
-    const int tid = d.tid;
-    const float w = a.weight ? __ldg(a.weight + b) : 1.f;
-    if (w == 0.f) {  // an ignored row: its logits are not read
-        if (GRAD) d.fill(0.f);
-        if (rank == 0 && tid == 0) {
-            a.loss[b] = 0.f;
-            a.stats[2 * static_cast<size_t>(b)] = 0.f;
-            a.stats[2 * static_cast<size_t>(b) + 1] = 0.f;
-        }
+    Distill<EB, SLOTS> d(a, reinterpret_cast<DistillShared<SLOTS> *>(dyn), blockIdx.x / a.cluster, rank);
+    const float w = a.weight ? __ldg(a.weight + d.b) : 1.f;
+    if (w == 0.f) {  // its logits are not read
+        ignored(d, rank);
         return;
     }
     cluster_arrive();
-    d.ask_teacher();
-    const int n = d.part.n;
-    if (GRAD) {
-        d.part.copy_all(buf, tid, kDThreads);
-        copies_commit();
-        d.clear(bits);
-        __syncthreads();
-    }
-    d.teacher(bits);
+    d.ask_teacher(d.b, d.id, d.t);
     Running<EB> r;
-    if (GRAD) {
+    r.stream(d.part, d.tid, d.c, [&]() { d.teacher_share(); });
+    cluster_wait();  // the peers have started
+    post_sums(d, r, rank, 0);
+    cluster_sync();
+    float m, s, own[SLOTS];
+    row_sums(d, 0, &m, &s);
+    d.teacher_finish(nullptr, 0);
+    d.own_logits([&](int x) { return Part<EB>::logit(a.student + (static_cast<size_t>(d.b) * a.V + x) * EB, 0); }, own);
+    post_loss(d, own, m, s, rank, 0);
+    cluster_sync();
+    if (rank == 0 && d.warp == 0) write_row(d, d.b, w, row_sound(d, m, s), m, s, 0);
+}
+
+// Loss, statistics and gradient: a cluster takes every gridDim-th row.  A row has one cluster barrier,
+// between its sums and its gradient, which also carries the loss of the row before.
+template <int EB, int SLOTS>
+__global__ void __launch_bounds__(kDThreads, kTrainCtas) distill_kernel(const DistillArgs a) {
+    extern __shared__ uint4 dyn[];
+    DistillShared<SLOTS> *sh = reinterpret_cast<DistillShared<SLOTS> *>(dyn);
+    uint4 *buf = dyn + sizeof(DistillShared<SLOTS>) / 16;
+    uint32_t *bits = reinterpret_cast<uint32_t *>(buf + a.part);
+    const uint32_t rank = cluster_rank();
+    const int step = static_cast<int>(gridDim.x) / a.cluster;
+    Distill<EB, SLOTS> d(a, sh, static_cast<int>(blockIdx.x) / a.cluster, rank);
+    const int tid = d.tid;
+    cluster_arrive();
+    auto weight = [&](int row) { return row < a.N && a.weight ? __ldg(a.weight + row) : 1.f; };
+    // the first row of weight other than 0 from `row` on; those before it get their zeros
+    auto live = [&](int row, float &w) {
+        while (row < a.N && w == 0.f) {
+            Distill<EB, SLOTS> z(a, sh, row, rank);
+            z.fill(0.f);
+            ignored(z, rank);
+            row += step;
+            w = weight(row);
+        }
+        return row;
+    };
+    float w = weight(d.b);
+    int row = live(d.b, w);
+    if (row >= a.N) {
+        cluster_wait();
+        return;
+    }
+    d.place(row, rank);
+    d.ask_teacher(row, d.id, d.t);
+    d.part.copy_all(buf, tid, kDThreads);
+    copies_commit();
+    d.clear(bits);
+    if (tid < 2) sh->twice[tid] = 0;
+    struct {
+        int row = -1;
+        float w, m, s;
+        bool sound;
+    } last;  // the row before, whose loss is on its way
+    for (int turn = 0, first = 1;; turn ^= 1, first = 0) {
+        float next_w = weight(row + step);
+        d.teacher_share();
         copies_wait<0>();
         d.part.mend_all(buf, tid, kDThreads);
+        Running<EB> r;
         int i = tid;
+        const int n = d.part.n;
         for (; i + kDThreads < n; i += 2 * kDThreads) {
             const uint4 v[2] = {buf[i], buf[i + kDThreads]};
             r.add(v, d.c);
@@ -336,81 +525,66 @@ __global__ void __launch_bounds__(kDThreads, 4) distill_kernel(const DistillArgs
             const uint4 v[1] = {buf[i]};
             r.add(v, d.c);
         }
-    } else {
-        int i = tid;
-        for (; i + 3 * kDThreads < n; i += 4 * kDThreads) {
-            uint4 v[4];
-            if (i > 0 && i + 3 * kDThreads < n - 1) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(d.part.at(i));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = __ldg(src + j * kDThreads);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = d.part.fetch(i + j * kDThreads);
-            }
-            r.add(v, d.c);
+        if (first) cluster_wait();  // the peers have started
+        post_sums(d, r, rank, turn);
+        cluster_sync();
+        if (last.row >= 0 && rank == 0 && d.warp == 0) write_row(d, last.row, last.w, last.sound, last.m, last.s, turn ^ 1);
+        float m, s, own[SLOTS];
+        row_sums(d, turn, &m, &s);
+        d.teacher_finish(bits, turn);
+        d.own_logits([&](int x) { return Part<EB>::logit(buf, d.part.offset(x)); }, own);
+        const bool sound = row_sound(d, m, s);
+        post_loss(d, own, m, s, rank, turn);
+        const int next = live(row + step, next_w);
+        // the next row's vectors into the places of those taken
+        Part<EB> ahead;
+        int from = 0, upto = 0;
+        int32_t ids[SLOTS];
+        float logits[SLOTS];
+        if (next < a.N) {
+            d.ask_teacher(next, ids, logits);
+            ahead.place(a.student, a.student_end, a.V, next, rank, a.part);
+            from = ahead.copy_from();
+            upto = ahead.copy_upto();
         }
-        for (; i < n; i += kDThreads) {
-            const uint4 v[1] = {d.part.fetch(i)};
-            r.add(v, d.c);
+        auto take = [&](int j) {
+            const uint4 v = buf[j];
+            // (an address that waits for v: the copy must not overtake the read)
+            if (j >= from && j < upto) copy16(smem_u32(buf + j) + (v.w & a.zero), ahead.at(j));
+            return v;
+        };
+        __syncthreads();  // the entries' logits have been read, the bitmap is complete
+        if (sound) {
+            d.gradient(w * d.invT, m, s, own, turn, take);
+        } else {
+            d.fill(NAN);
+            for (int j = tid; j < n; j += kDThreads) take(j);
+            __syncthreads();
+        }
+        last.row = row;
+        last.w = w;
+        last.m = m;
+        last.s = s;
+        last.sound = sound;
+        if (next >= a.N) {
+            cluster_sync();
+            if (rank == 0 && d.warp == 0) write_row(d, last.row, last.w, last.sound, last.m, last.s, turn);
+            return;
+        }
+        for (int j = tid; j < upto; j += kDThreads)
+            if (j >= n) copy16(smem_u32(buf + j), ahead.at(j));
+        copies_commit();
+        d.clear(bits);  // (marked after the next barrier)
+        if (tid == 0) sh->twice[turn ^ 1] = 0;
+        row = next;
+        w = next_w;
+        d.place(row, rank);
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            d.id[j] = ids[j];
+            d.t[j] = logits[j];
         }
     }
-    // the block's, then the cluster's.  NaN passes through the sums.
-    const float bm = d.block_max(r.m, 3);
-    float s = r.m == -INFINITY ? 0.f : r.sum(d.c) * ptx::ex2((r.m - bm) * d.c);
-    // (after that barrier the part is in shared memory for every thread)
-    auto logit_at = [&](int x) {
-        return GRAD ? Part<EB>::logit(buf, d.part.offset(x)) : Part<EB>::logit(a.student + (static_cast<size_t>(b) * a.V + x) * EB, 0);
-    };
-    float dot = 0.f, ps = 0.f;
-#pragma unroll
-    for (int j = 0; j < SLOTS; ++j) {
-        const float p = d.id[j] >= 0 ? sh->p[tid + j * kDThreads] : 0.f;
-        if (p == 0.f) continue;
-        const float l = logit_at(d.id[j]);
-        dot += p * (d.t[j] - (l == -INFINITY ? l : (l - bm) * d.invT));  // a masked token the teacher wants: +inf
-        ps += p;
-    }
-    s = warp_add(s);
-    dot = warp_add(dot);
-    ps = warp_add(ps);
-    if (d.lane == 0) {
-        sh->red[0][d.warp] = s;
-        sh->red[1][d.warp] = dot;
-        sh->red[4][d.warp] = ps;
-    }
-    __syncthreads();
-    s = dot = ps = 0.f;
-#pragma unroll
-    for (int i = 0; i < kDWarps; ++i) {
-        s += sh->red[0][i];
-        dot += sh->red[1][i];
-        ps += sh->red[4][i];
-    }
-    cluster_wait();
-    if (tid < a.cluster) st_peer(peer(&sh->slot[rank], tid), make_float4(bm, s, dot, ps));
-    cluster_sync();
-    float m = -INFINITY;
-    for (int i = 0; i < a.cluster; ++i) m = fmaxf(m, sh->slot[i].x);
-    s = 0.f;
-    dot = 0.f;
-    for (int i = 0; i < a.cluster; ++i) {
-        const float4 v = sh->slot[i];
-        s += v.x == -INFINITY ? v.y : v.y * ptx::ex2((v.x - m) * d.c);  // a part of masked logits has sum 0 (or NaN)
-        if (v.w != 0.f) dot += v.z + v.w * ((m - v.x) * d.invT);
-    }
-    const bool bad = !(d.sum_p == d.sum_p) || !(m < INFINITY && s > 0.f && s < INFINITY);  // NaN, +inf, or nothing but -inf
-    if (rank == 0 && tid == 0) {
-        a.loss[b] = bad ? NAN : d.sum_p > 0.f ? w * (dot + d.sum_p * logf(s)) : 0.f;
-        a.stats[2 * static_cast<size_t>(b)] = bad ? NAN : m;
-        a.stats[2 * static_cast<size_t>(b) + 1] = bad ? NAN : s;
-        if (bad) atomicOr(a.status, SPEC_DEV_NONFINITE);
-    }
-    if (!GRAD) return;
-    if (bad)
-        d.fill(NAN);
-    else
-        d.gradient(w * d.invT, m, s, [&](int i) { return buf[i]; }, logit_at);
 }
 
 // The gradient alone, from the logits and a forward call's statistics: a CTA per part of a row.
@@ -426,18 +600,25 @@ __global__ void __launch_bounds__(kDThreads, 4) distill_backward_kernel(const Di
         d.fill(0.f);
         return;
     }
-    d.ask_teacher();
+    auto fetch = [&](int i) { return d.part.fetch(i); };
+    uint4 first[Distill<EB, SLOTS>::kBatch];
+    d.ask_teacher(b, d.id, d.t);
+    d.ask_first(fetch, first);
     const float2 ms = __ldg(reinterpret_cast<const float2 *>(a.stats) + b);
     d.clear(bits);
+    if (d.tid == 0) sh->twice[0] = 0;
+    d.teacher_share();
     __syncthreads();
-    d.teacher(bits);
-    if (!(d.sum_p == d.sum_p) || !(fabsf(ms.x) < INFINITY && ms.y > 0.f && ms.y < INFINITY)) {
+    d.teacher_finish(bits, 0);
+    if (!row_sound(d, fabsf(ms.x) < INFINITY ? ms.x : INFINITY, ms.y)) {
         if (d.tid == 0) atomicOr(a.status, SPEC_DEV_NONFINITE);
         d.fill(NAN);
         return;
     }
-    d.gradient(up * d.invT, ms.x, ms.y, [&](int i) { return d.part.fetch(i); },
-               [&](int x) { return Part<EB>::logit(a.student + (static_cast<size_t>(b) * a.V + x) * EB, 0); });
+    float own[SLOTS];
+    d.own_logits([&](int x) { return Part<EB>::logit(a.student + (static_cast<size_t>(b) * a.V + x) * EB, 0); }, own);
+    __syncthreads();
+    d.gradient(up * d.invT, ms.x, ms.y, own, 0, fetch, &first);
 }
 
 template <class Kernel>
@@ -449,10 +630,10 @@ spec_status go(Kernel kernel, DistillArgs a, int eb, int slots, int form, cudaSt
     st = allow_max_dyn_smem(dev, reinterpret_cast<const void *>(kernel), &di);
     if (st != SPEC_OK) return st;
     const long long vecs = (static_cast<long long>(a.V) * eb + 14) / 16 + 1;  // at the worst alignment
-    const long long most = (form == kLossGrad ? kPartBytes : 48 * 1024);
+    const long long most = form == kLossGrad ? kPartBytes : form == kLoss ? kLossBytes : kBackwardBytes;
     const long long limit = form == kBackward ? 1 << 20 : kMaxCluster;
     long long cs = std::min(limit, (vecs * 16 + most - 1) / most);
-    while (2 * cs <= kMaxCluster && a.N * cs < 2 * di.sms && vecs / cs > 2 * kDThreads) cs *= 2;
+    while (2 * cs <= kMaxCluster && a.N * cs < kWaves * di.sms && vecs / cs > 2 * kDThreads) cs *= 2;
     a.cluster = static_cast<int>(cs);
     a.part = static_cast<int>((vecs + cs - 1) / cs);
     const size_t fixed = slots == 1 ? sizeof(DistillShared<1>) : sizeof(DistillShared<4>);
@@ -472,6 +653,10 @@ spec_status go(Kernel kernel, DistillArgs a, int eb, int slots, int form, cudaSt
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = form == kBackward ? 0 : 1;
+    if (form == kLossGrad) {  // as many rows under way as there are clusters at a time
+        const int most_rows = resident_clusters(dev, reinterpret_cast<const void *>(kernel), cfg);
+        if (most_rows > 0 && most_rows < a.N) cfg.gridDim = dim3(static_cast<unsigned>(most_rows * cs));
+    }
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess)
@@ -482,12 +667,12 @@ spec_status go(Kernel kernel, DistillArgs a, int eb, int slots, int form, cudaSt
 template <int EB>
 spec_status launch_distill(const DistillArgs &a, int form, cudaStream_t stream) {
     if (a.K <= kDThreads) {
-        if (form == kLoss) return go(distill_kernel<EB, 1, false>, a, EB, 1, form, stream);
-        if (form == kLossGrad) return go(distill_kernel<EB, 1, true>, a, EB, 1, form, stream);
+        if (form == kLoss) return go(distill_loss_kernel<EB, 1>, a, EB, 1, form, stream);
+        if (form == kLossGrad) return go(distill_kernel<EB, 1>, a, EB, 1, form, stream);
         return go(distill_backward_kernel<EB, 1>, a, EB, 1, form, stream);
     }
-    if (form == kLoss) return go(distill_kernel<EB, 4, false>, a, EB, 4, form, stream);
-    if (form == kLossGrad) return go(distill_kernel<EB, 4, true>, a, EB, 4, form, stream);
+    if (form == kLoss) return go(distill_loss_kernel<EB, 4>, a, EB, 4, form, stream);
+    if (form == kLossGrad) return go(distill_kernel<EB, 4>, a, EB, 4, form, stream);
     return go(distill_backward_kernel<EB, 4>, a, EB, 4, form, stream);
 }
 

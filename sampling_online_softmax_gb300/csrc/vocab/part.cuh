@@ -67,17 +67,19 @@ struct Part {
     __device__ __forceinline__ bool edge(int i) const { return first + i == 0 || first + i == total - 1; }
     __device__ __forceinline__ bool inside(int i) const { return at(i) >= base && at(i) + 16 <= end; }
 
-    // This thread's vectors (i = tid, tid + step, ...) to shared memory, asynchronously; then the row's
-    // first and last, which may hold a neighbour's logits or lie across the tensor's end, by the threads
-    // that own them.
+    // The vectors that can be read whole: all but one that lies across the tensor's first or last byte.
+    __device__ __forceinline__ int copy_from() const { return n > 0 && !inside(0) ? 1 : 0; }
+    __device__ __forceinline__ int copy_upto() const { return n > 0 && !inside(n - 1) ? n - 1 : n; }
+    // This thread's vectors (i = tid, tid + step, ...) to shared memory, asynchronously.
     __device__ __forceinline__ void copy_all(uint4 *buf, int tid, int step) const {
-        if (n <= 0) return;
-        const int from = inside(0) ? 0 : 1, upto = inside(n - 1) ? n : n - 1;
+        const int from = copy_from(), upto = copy_upto();
         const unsigned char *src = at(tid);
         uint32_t dst = smem_u32(buf + tid);
         for (int i = tid; i < upto; i += step, src += 16 * step, dst += 16 * step)
             if (i >= from) copy16(dst, src);
     }
+    // After the copies: the row's first and last vector, which may hold a neighbour's logits or lie
+    // across the tensor's end, by the threads that own them.
     __device__ __forceinline__ void mend_all(uint4 *buf, int tid, int step) const {
         if (n <= 0) return;
         if (tid == 0 && edge(0)) buf[0] = by_logit(at(0), index(0, 0), V);
@@ -130,6 +132,11 @@ struct Part {
             return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
         }
         return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+    // A vector of -inf.
+    static __device__ __forceinline__ uint4 nothing() {
+        const uint32_t w = EB == 2 ? 0xff80ff80u : 0xff800000u;
+        return make_uint4(w, w, w, w);
     }
     static __device__ __forceinline__ float logit(const void *p, int i) {
         return EB == 4 ? reinterpret_cast<const float *>(p)[i]

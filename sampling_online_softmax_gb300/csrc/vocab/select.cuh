@@ -366,10 +366,7 @@ struct Row {
         return false;
     }
 
-    static __device__ __forceinline__ uint4 nothing() {
-        const uint32_t w = EB == 2 ? 0xff80ff80u : 0xff800000u;
-        return make_uint4(w, w, w, w);
-    }
+    static __device__ __forceinline__ uint4 nothing() { return P::nothing(); }
     // f(vectors, number) for the vectors of the groups whose maximum reaches `low`, spread over all
     // threads, kGather at a time, whole warps together; number(j) is vector j's (-1: none).
     static constexpr int kGather = 8;

@@ -3,6 +3,9 @@
 // dispatch.
 #include <climits>
 #include <cmath>
+#include <map>
+#include <mutex>
+#include <tuple>
 
 #include "distill.h"
 
@@ -64,7 +67,25 @@ spec_status rows_args(RowArgs *a, const void *logits, spec_dtype dtype, int B, i
     return SPEC_OK;
 }
 
+std::mutex g_clusters_mutex;
+std::map<std::tuple<int, const void *, size_t, unsigned>, int> g_clusters;
+
 }  // namespace
+
+int resident_clusters(int dev, const void *kernel, const cudaLaunchConfig_t &cfg) {
+    const auto key = std::make_tuple(dev, kernel, cfg.dynamicSmemBytes, cfg.attrs[0].val.clusterDim.x);
+    std::lock_guard<std::mutex> lock(g_clusters_mutex);
+    const auto it = g_clusters.find(key);
+    if (it != g_clusters.end()) return it->second;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    g_clusters[key] = n;
+    return n;
+}
+
 }  // namespace vocab
 }  // namespace spec
 
