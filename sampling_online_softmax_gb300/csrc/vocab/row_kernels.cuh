@@ -192,8 +192,8 @@ constexpr uint32_t kOpen = 1;  // in place of a cut's key (keys are larger): the
 
 // Where the kept tokens, in the order of falling logits, reach COUNT: the k-th; else: p times
 // their weight.  False: fewer than k, or (with near sums) open.
-//   1  a histogram of counts over 2048 equal steps below the maximum.  A bin's weight lies between
-//      its edges', 2 % apart, so its running sums bracket the cut's bin (COUNT: find it).
+//   1  a histogram of counts over 512 equal steps below the maximum.  A bin's weight lies between
+//      its edges', 7 % apart at most, so its running sums bracket the cut's bin (COUNT: find it).
 //   2  the weights above the bracket and in all, and a histogram of the bracket's inside.
 //   3  the weights between, and the tokens of the narrowed bracket: a few, or equal ones, which one
 //      CTA sorts and weighs.
@@ -213,26 +213,40 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
     const W_ weigh(sc, sh->pow2, had);
     // 48 steps of two hold every weight that counts; narrower rows get finer bins
     const float span = fminf(48.f / sc.ch, 2.f * (sc.m - r.least_maximum()));
-    const float scale = (kBins - 1) / fmaxf(span, 1e-30f);
-    auto place = [&](float l) { return fminf((sc.m - l) * scale, 0x1.fffffep10f); };  // in bins below the maximum; < kBins
+    const float scale = (kCutBins - 1) / fmaxf(span, 1e-30f);
+    auto place = [&](float l) { return fminf((sc.m - l) * scale, 0x1.fffffep8f); };  // in bins below the maximum; < kCutBins
     auto clear = [&]() {
         r.sync();  // the histogram before this one has been read, by the peers too
-        for (int i = tid; i < kBins; i += kThreads) sh->count[i] = 0;
-        if (tid == 0) sh->cross_bin = kAll, sh->cross_last = kBins - 1;
+        for (int i = tid; i < kCutBins; i += kThreads) sh->count[i] = 0;
+        if (tid == 0) sh->cross_bin = kAll, sh->cross_last = kCutBins - 1;
         __syncthreads();
     };
-    // weights of a bin whose edge lies `at` bins below the maximum, in units of 2^-40
-    auto edge = [&](float at, float slack) { return static_cast<unsigned long long>(ptx::ex2(-at / scale * sc.ch) * slack * 0x1p40f); };
-    unsigned long long v[kBinsPerThread];
-    const int first = tid * kBinsPerThread;
+    unsigned long long v[kCutPerThread];
+    const int first = tid * kCutPerThread;
+    const float per_bin = sc.ch / scale;
+    // the weight of a logit that lies `at` bins below the maximum, in units of 2^-40
+    auto edge = [&](float at) { return __float2ull_rn(ptx::ex2(-at * per_bin) * 0x1p40f); };
+    // this thread's bins' weights at most and at least, their counts times their edges' give or take 2^-slack;
+    // a last bin without end: 0
+    auto weights = [&](float at, float step, int slack, bool endless, unsigned long long (&lo)[kCutPerThread],
+                       unsigned long long (&hi)[kCutPerThread]) {
+        unsigned long long e = edge(at);
+#pragma unroll
+        for (int i = 0; i < kCutPerThread; ++i) {
+            const unsigned long long below = edge(at + static_cast<float>(i + 1) * step);
+            hi[i] = v[i] * (e + (e >> slack) + 1);
+            lo[i] = endless && tid == kThreads - 1 && i == kCutPerThread - 1 ? 0ull : v[i] * (below - (below >> slack));
+            e = below;
+        }
+    };
     // the bin of the histogram in which the count from `over` on reaches `goal`
     auto counted = [&](unsigned long long over, unsigned long long goal) {
         unsigned long long mine = 0;
 #pragma unroll
-        for (int i = 0; i < kBinsPerThread; ++i) mine += v[i];
+        for (int i = 0; i < kCutPerThread; ++i) mine += v[i];
         unsigned long long run = over + r.sum_before(mine);
 #pragma unroll
-        for (int i = 0; i < kBinsPerThread; ++i) {
+        for (int i = 0; i < kCutPerThread; ++i) {
             if (run < goal && run + v[i] >= goal) {
                 sh->cross_bin = first + i;
                 sh->above = run;
@@ -245,16 +259,17 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
     clear();
     uint32_t deep = 0;  // in the last bin, which may hold most of a cold row
     r.vectors([&](const uint4(&vec)[Row<EB>::kBatch], int i0) {
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < Row<EB>::kBatch; ++j) {
-            if (!(Row<EB>::vector_max(vec[j]) >= weigh.floor)) continue;
+            const uint4 one = Row<EB>::pick(vec, j);
+            if (!(Row<EB>::vector_max(one) >= weigh.floor)) continue;
             float l[kPer];
-            Row<EB>::unpack(vec[j], l);
+            Row<EB>::unpack(one, l);
 #pragma unroll
             for (int q = 0; q < kPer; ++q) {
                 if (!weigh.kept(l[q], r.index(i0 + j * kThreads, q))) continue;
                 const int y = static_cast<int>(place(l[q]));
-                if (y == kBins - 1)
+                if (y == kCutBins - 1)
                     ++deep;
                 else
                     atomicAdd(&sh->count[y], 1u);
@@ -262,9 +277,9 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
         }
     });
     deep = __reduce_add_sync(kAll, deep);
-    if (r.lane == 0 && deep) atomicAdd(&sh->count[kBins - 1], deep);
+    if (r.lane == 0 && deep) atomicAdd(&sh->count[kCutBins - 1], deep);
     r.sync();
-    r.template bins<true>(v);
+    r.cut_bins(v);
     uint32_t b0, b1;              // the cut's bin is in [b0, b1]
     unsigned long long A = 0;     // what lies above b0
     if (COUNT) {
@@ -273,19 +288,14 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
         if (b0 == kAll) return false;
         A = sh->above;
     } else {
-        unsigned long long lo[kBinsPerThread], hi[kBinsPerThread], low = 0, high = 0, all_l, all_h;
+        unsigned long long lo[kCutPerThread], hi[kCutPerThread], low = 0, high = 0, all_l, all_h;
+        weights(static_cast<float>(first), 1.f, 12, true, lo, hi);
 #pragma unroll
-        for (int i = 0; i < kBinsPerThread; ++i) {
-            const float at = static_cast<float>(first + i);
-            hi[i] = v[i] ? v[i] * (edge(at, 1.001f) + 1) : 0ull;
-            lo[i] = v[i] && first + i < kBins - 1 ? v[i] * edge(at + 1.f, 0.999f) : 0ull;
-            low += lo[i];
-            high += hi[i];
-        }
+        for (int i = 0; i < kCutPerThread; ++i) low += lo[i], high += hi[i];
         unsigned long long run_l = r.sum_before(low, &all_l), run_h = r.sum_before(high, &all_h);
         const unsigned long long t0 = share_of(all_l, p), t1 = share_of(all_h, p);
 #pragma unroll
-        for (int i = 0; i < kBinsPerThread; ++i) {
+        for (int i = 0; i < kCutPerThread; ++i) {
             if (run_h < t0 && run_h + hi[i] >= t0) sh->cross_bin = first + i;
             if (run_l < t1 && run_l + lo[i] >= t1) sh->cross_last = first + i;
             run_h += hi[i];
@@ -294,25 +304,26 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
         __syncthreads();
         b0 = sh->cross_bin == kAll ? 0u : sh->cross_bin;
         b1 = sh->cross_last;
-        exact |= edge(static_cast<float>(b1), 1.f) < all_l >> 14;
+        exact |= edge(static_cast<float>(b1)) < all_l >> 14;
     }
 
     const float from = static_cast<float>(b0), upto = static_cast<float>(b1 + 1);
-    const float fine = kBins / (upto - from);
-    auto sub = [&](float at) { return min(kBins - 1, static_cast<int>((at - from) * fine)); };
+    const float fine = kCutBins / (upto - from);
+    auto sub = [&](float at) { return min(kCutBins - 1, static_cast<int>((at - from) * fine)); };
     // no logit of the bracket lies below (the last bin has no end)
-    const float edge_l = b1 == kBins - 1 ? -FLT_MAX : sc.m - upto / scale - (fabsf(sc.m) + span) * 0x1p-20f;
+    const float edge_l = b1 == kCutBins - 1 ? -FLT_MAX : sc.m - upto / scale - (fabsf(sc.m) + span) * 0x1p-20f;
     unsigned long long W = 0, B = 0, target = static_cast<unsigned long long>(k);
     float b = 0.f;
     int vectors = 0;
     clear();
     r.vectors([&](const uint4(&vec)[Row<EB>::kBatch], int i0) {
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < Row<EB>::kBatch; ++j) {
-            const float top = Row<EB>::vector_max(vec[j]);
+            const uint4 one = Row<EB>::pick(vec, j);
+            const float top = Row<EB>::vector_max(one);
             if (!(top >= (COUNT ? fmaxf(weigh.floor, edge_l) : weigh.floor))) continue;
             float l[kPer], s = 0.f, a = 0.f;
-            Row<EB>::unpack(vec[j], l);
+            Row<EB>::unpack(one, l);
 #pragma unroll
             for (int q = 0; q < kPer; ++q) {
                 const bool in = weigh.kept(l[q], r.index(i0 + j * kThreads, q));
@@ -345,7 +356,7 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
         if (!exact) B = r.sum(W_::bound(b * 2.f, 2 * vectors));  // (sums in a row, not a tree: 7 2^-24 more)
         target = share_of(W, p);
     }
-    r.template bins<true>(v);
+    r.cut_bins(v);
     uint32_t s0, s1;
     if (COUNT) {
         counted(A, target);
@@ -355,19 +366,14 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
         const float step = 1.f / fine;
         const int drop = exact ? sc.U - 40 : 0;  // from the sums' units to 2^-40
         const unsigned long long unit = A >> drop, aim = target >> drop, slack = B + 1;
-        unsigned long long lo[kBinsPerThread], hi[kBinsPerThread], low = 0, high = 0;
+        unsigned long long lo[kCutPerThread], hi[kCutPerThread], low = 0, high = 0;
+        weights(from + static_cast<float>(first) * step, step, 14, b1 == kCutBins - 1, lo, hi);
 #pragma unroll
-        for (int i = 0; i < kBinsPerThread; ++i) {
-            const float at = from + static_cast<float>(first + i) * step;
-            hi[i] = v[i] ? v[i] * (edge(at, 1.00005f) + 1) : 0ull;
-            lo[i] = v[i] && !(b1 == kBins - 1 && first + i == kBins - 1) ? v[i] * edge(at + step, 0.99995f) : 0ull;
-            low += lo[i];
-            high += hi[i];
-        }
+        for (int i = 0; i < kCutPerThread; ++i) low += lo[i], high += hi[i];
         unsigned long long run_h = unit + slack + r.sum_before(high);
         unsigned long long run_l = unit + r.sum_before(low);
 #pragma unroll
-        for (int i = 0; i < kBinsPerThread; ++i) {
+        for (int i = 0; i < kCutPerThread; ++i) {
             if (run_h < aim && run_h + hi[i] >= aim) sh->cross_bin = first + i;
             if (run_l < aim + slack && run_l + lo[i] >= aim + slack) sh->cross_last = first + i;
             run_h += hi[i];
@@ -383,12 +389,13 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
     unsigned long long between = 0;
     r.vectors([&](const uint4(&vec)[Row<EB>::kBatch], int i0) {
         unsigned long long bits = 0;
-#pragma unroll
+#pragma unroll 1
         for (int j = 0; j < Row<EB>::kBatch; ++j) {
-            const float top = Row<EB>::vector_max(vec[j]);
+            const uint4 one = Row<EB>::pick(vec, j);
+            const float top = Row<EB>::vector_max(one);
             if (!(top >= fmaxf(weigh.floor, edge_l))) continue;
             float l[kPer], s = 0.f;
-            Row<EB>::unpack(vec[j], l);
+            Row<EB>::unpack(one, l);
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 const float at = place(l[e]);
@@ -694,10 +701,10 @@ __device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) 
                 float e = 0.f;
                 int vectors = 0;
                 r.vectors([&](const uint4(&v)[Row<EB>::kBatch], int) {
-#pragma unroll
+#pragma unroll 1
                     for (int j = 0; j < Row<EB>::kBatch; ++j) {
                         float l[Row<EB>::kPer], s = 0.f;
-                        Row<EB>::unpack(v[j], l);
+                        Row<EB>::unpack(Row<EB>::pick(v, j), l);
 #pragma unroll
                         for (int x = 0; x < Row<EB>::kPer; ++x) s += l[x] >= low || l[x] == -INFINITY ? 0.f : weigh.near(l[x], &e);
                         rest += __float2ull_rn(s * 0x1p40f);

@@ -30,6 +30,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBinBits = 11;
 constexpr int kBins = 1 << kBinBits;
 constexpr int kBinsPerThread = kBins / kThreads;
+constexpr int kCutBins = 512;                    // bins of cut_row's histograms
+constexpr int kCutPerThread = kCutBins / kThreads;
 constexpr int kGroups = kMaxCluster * kThreads;  // groups of a row's logits, whatever the cluster's size
 constexpr int kKeysPerThread = kGroups / kThreads;
 constexpr int kWhole = 128;                      // rows up to this long are listed whole
@@ -476,15 +478,16 @@ struct Row {
         }
         __syncwarp();
     }
+    // v[j], for loops that are not unrolled.
+    static __device__ __forceinline__ uint4 pick(const uint4 (&v)[kBatch], int j) { return j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3]; }
     // f(logit, index) for every logit of the part (and for some -inf of no index).
     template <class F>
     __device__ __forceinline__ void each(F f) const {
         vectors([&](const uint4(&v)[kBatch], int i0) {
 #pragma unroll 1
             for (int j = 0; j < kBatch; ++j) {
-                const uint4 w = j == 0 ? v[0] : j == 1 ? v[1] : j == 2 ? v[2] : v[3];
                 float l[kPer];
-                unpack(w, l);
+                unpack(pick(v, j), l);
 #pragma unroll
                 for (int q = 0; q < kPer; ++q) f(l[q], index(i0 + j * kThreads, q));
             }
@@ -548,6 +551,17 @@ struct Row {
                     v[2 * h + 1] += c.z | static_cast<unsigned long long>(c.w) << 32;
                 }
             }
+        }
+    }
+    // The same of cut_row's.
+    __device__ __forceinline__ void cut_bins(unsigned long long (&v)[kCutPerThread]) const {
+        static_assert(kCutPerThread == 2, "read as a pair");
+        v[0] = v[1] = 0;
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) {
+            if (r >= cs) break;
+            const uint2 c = ld_peer2(peer(&sh->count[2 * tid], r));
+            v[0] += c.x, v[1] += c.y;
         }
     }
     // The block's running sum before this thread's v, and its whole sum.
@@ -638,8 +652,8 @@ struct Row {
                     w[j] = nothing();
                     if (i0 + 32 * j < s1) w[j] = part.fetch(i0 + 32 * j);
                 }
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) v += weigh(w[j], i0 + 32 * j);
+#pragma unroll 1
+                for (int j = 0; j < kBatch; ++j) v += weigh(pick(w, j), i0 + 32 * j);
             }
             return warp_sum(v);
         };
@@ -647,17 +661,19 @@ struct Row {
         const unsigned long long mine = run_sum(min(n, warp * run), min(n, (warp + 1) * run));
         if (lane < static_cast<int>(cs)) st_peer(peer(&sh->seg[turn][rank * kWarps + warp], lane), mine);
         sync();
-        unsigned long long total = 0;
-        for (uint32_t g = lane; g < cs * kWarps; g += 32) total += sh->seg[turn][g];
-        const unsigned long long target = aim(warp_sum(total));
-        unsigned long long before = 0;
-        uint32_t g = 0;
-        for (; g < cs * kWarps; ++g) {
-            const unsigned long long x = sh->seg[turn][g];
-            if (before + x >= target) break;
-            before += x;
-        }
+        // the runs' sums, two to a lane in order
+        static_assert(kMaxCluster * kWarps == 64, "two runs a lane");
+        const uint32_t g0 = 2 * lane;
+        const unsigned long long a0 = g0 < cs * kWarps ? sh->seg[turn][g0] : 0ull, a1 = g0 + 1 < cs * kWarps ? sh->seg[turn][g0 + 1] : 0ull;
+        const unsigned long long incl = warp_scan(a0 + a1, lane);
         turn ^= 1;
+        const unsigned long long target = aim(__shfl_sync(kAll, incl, 31));
+        const uint32_t hits = __ballot_sync(kAll, incl >= target);
+        if (!hits) return;  // (no row that aims within its sum)
+        const int owner = __ffs(hits) - 1;
+        const bool second = incl - a1 < target;
+        const uint32_t g = __shfl_sync(kAll, g0 + second, owner);
+        unsigned long long before = __shfl_sync(kAll, incl - a1 - (second ? 0ull : a0), owner);
         if (g / kWarps != rank) return;  // the whole CTA
         int s0 = min(n, static_cast<int>(g % kWarps) * run), s1 = min(n, s0 + run);
         const int piece = (s1 - s0 + kWarps - 1) / kWarps;

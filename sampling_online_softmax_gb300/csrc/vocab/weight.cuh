@@ -141,20 +141,25 @@ SPEC_HD unsigned long long fixed_weight(float logit, const Scale &s, const float
     return some ? v : 0ull;
 }
 
-// floor(W * f) for f in [0, 1), and whether f * W is no whole number, exactly.
+// floor(W * f) for W < 2^63 and f in [0, 1), and whether f * W is no whole number, exactly.
 SPEC_HD unsigned long long scaled_floor(unsigned long long W, float f, bool *rest) {
     int e = 0;
     const float fr = frexpf(f, &e);  // f = fr 2^e, fr in [0.5, 1), e <= 0
     const unsigned long long M = static_cast<unsigned long long>(fr * 16777216.f);
-    const unsigned __int128 P = static_cast<unsigned __int128>(W) * M;
-    const int s = 24 - e;  // >= 24
-    if (s >= 128) {
-        *rest = P != 0;
+    const int s = 24 - e;  // >= 24; the product W M, above and below 2^32:
+    const unsigned long long low = (W & 0xffffffffull) * M, A = (W >> 32) * M + (low >> 32);
+    const uint32_t r = static_cast<uint32_t>(low);
+    if (s < 32) {
+        *rest = (r & ((1u << s) - 1)) != 0;
+        return (A << (32 - s)) + (r >> s);
+    }
+    if (s >= 96) {
+        *rest = W != 0 && M != 0;
         return 0ull;
     }
-    const unsigned __int128 q = P >> s;
-    *rest = (q << s) != P;
-    return static_cast<unsigned long long>(q);
+    const unsigned long long q = A >> (s - 32);
+    *rest = r != 0 || (q << (s - 32)) != A;
+    return q;
 }
 
 }  // namespace vocab
