@@ -507,8 +507,8 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
                 for (int e = 0; e < kPer; ++e) c += weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc, q.min_p);
                 return c;
             },
-            [](unsigned long long) { return 1ull; },
-            [&](const uint4 &v, int i, unsigned long long, unsigned long long) {
+            []() { return 0ull; }, [](unsigned long long) { return 1ull; },
+            [&](const uint4 &v, int i, unsigned long long, unsigned long long, unsigned long long, unsigned long long) {
                 float l[kPer];
                 Row<EB>::unpack(v, l);
                 int x = -1;
@@ -523,11 +523,11 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
         bool rest;
         return scaled_floor(W, q.u, &rest) + 1;
     };
-    // first by near sums: the draw is sure where u's place is further from the token's ends than the
-    // sums' error (the same 2^-20 of the whole)
+    // First by near sums.  u's place is u W - C_v: the errors of what lies up to v count (1 - u) times,
+    // of what lies behind u times.  The draw is sure where it is further than that from the token's ends.
     float b = 0.f;
     int vectors = 0;
-    if (r.tid == 0) sh->slack = 0;
+    if (r.tid == 0) sh->drawn = kAll;
     __syncthreads();
     bool counting = true;
     r.locate(
@@ -537,40 +537,33 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
             if (counting) b += more, ++vectors;
             return w;
         },
-        [&](unsigned long long W) {
+        [&]() {
             counting = false;
-            return aim(W);
+            return Weigh<EB>::bound(b, vectors);
         },
-        [&](const uint4 &v, int i, unsigned long long before, unsigned long long target) {
+        aim,
+        [&](const uint4 &v, int i, unsigned long long before, unsigned long long target, unsigned long long b_upto, unsigned long long b_from) {
             float l[kPer], none = 0.f;
             Row<EB>::unpack(v, l);
+            const unsigned long long off = __float2ull_ru(((1.f - q.u) * static_cast<float>(b_upto) + q.u * static_cast<float>(b_from)) * 1.001f) + kPer + 2;
             unsigned long long run = before;
             uint32_t x = kAll;
-            long long left = 0, right = 0;
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 const bool in = weigh.kept(l[e], r.index(i, e));
                 const unsigned long long w = in ? __float2ull_rn(weigh.near(l[e], &none) * 0x1p40f) : 0ull;
-                if (x == kAll && run < target && run + w >= target) {
-                    x = static_cast<uint32_t>(r.index(i, e));
-                    left = static_cast<long long>(target - 1 - run);
-                    right = static_cast<long long>(run + w - target);
-                }
+                if (run < target && run + w >= target && target > run + off && run + w > target + off) x = static_cast<uint32_t>(r.index(i, e));
                 run += w;
             }
-            if (x != kAll)
-                for (uint32_t c = 0; c < r.cs; ++c) {
-                    st_peer(peer(&sh->drawn, c), x);
-                    st_peer(peer(&sh->slack, c), static_cast<unsigned long long>(min(left, right)));
-                }
+            for (uint32_t c = 0; c < r.cs; ++c) st_peer(peer(&sh->drawn, c), x);
         });
-    const unsigned long long B = r.sum(Weigh<EB>::bound(b, vectors)) + kPer + 2;
-    if (sh->slack > B) {
+    r.sync();
+    if (sh->drawn != kAll) {
         if (r.rank == 0 && r.tid == 0) *token = static_cast<int32_t>(sh->drawn);
         return;
     }
-    r.locate([&](const uint4 &v, int i) { return weigh.exact_sum(r, v, i); }, aim,
-             [&](const uint4 &v, int i, unsigned long long before, unsigned long long target) {
+    r.locate([&](const uint4 &v, int i) { return weigh.exact_sum(r, v, i); }, []() { return 0ull; }, aim,
+             [&](const uint4 &v, int i, unsigned long long before, unsigned long long target, unsigned long long, unsigned long long) {
                  float l[kPer];
                  Row<EB>::unpack(v, l);
 #pragma unroll
@@ -818,12 +811,15 @@ __global__ void __launch_bounds__(kThreads, kRowCtas) row_kernel(const RowArgs a
         top_row<EB>(a, r, b);
 }
 
-// CTAs per row and vectors per CTA: one CTA a row where that gives every SM two rows, else enough
-// to do so, as long as a CTA has at least two vectors a thread.
-inline void row_split(RowArgs *a, int EB, int sms) {
+// CTAs per row and vectors per CTA: one CTA a row where that gives every SM two rows, else enough to do
+// so, as long as a CTA has four vectors a thread.  (64 rows of 152064 bf16 logits, microseconds with 1, 2,
+// 4, 8 CTAs a row: short way 16.1, 15.1, 14.8, 16.7; unfiltered 127, 73, 46, 38.  512 rows, short way:
+// 62, 67, 92, 166.  The long way's passes want more CTAs: four an SM where no filter is given at all.)
+inline void row_split(RowArgs *a, int EB, int sms, bool unfiltered) {
     const long long vecs = (static_cast<long long>(a->V) * EB + 14) / 16 + 1;  // at the worst alignment
+    const long long want = (unfiltered && vecs > 8192 ? 4ll : 2ll) * sms;
     int cs = 1;
-    while (cs < kMaxCluster && static_cast<long long>(a->B) * cs < 2 * sms && vecs / cs > 2 * kThreads) cs *= 2;
+    while (cs < kMaxCluster && a->B * static_cast<long long>(cs) < want && vecs / cs > 4 * kThreads) cs *= 2;
     a->cluster = cs;
     a->part = static_cast<int>((vecs + cs - 1) / cs);
 }
@@ -838,7 +834,7 @@ spec_status launch_rows(const RowArgs &a0, cudaStream_t stream) {
     auto kernel = row_kernel<EB, OP>;
     st = allow_max_dyn_smem(dev, reinterpret_cast<const void *>(kernel), &di);
     if (st != SPEC_OK) return st;
-    row_split(&a, EB, di.sms);
+    row_split(&a, EB, di.sms, OP == kSampleRows && !a.top_k && !a.top_p && !a.min_p);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.cluster);
     cfg.blockDim = dim3(kThreads);

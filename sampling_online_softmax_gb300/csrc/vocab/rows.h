@@ -12,7 +12,7 @@ namespace spec {
 namespace vocab {
 
 constexpr int kThreads = 256;
-constexpr int kRowCtas = 4;       // CTAs of a row kernel per SM
+constexpr int kRowCtas = 3;       // CTAs of a row kernel per SM
 constexpr int kMaxCluster = 8;    // CTAs per row (the portable limit)
 constexpr int kMaxList = 2048;    // entries of a cluster's list
 

@@ -73,8 +73,7 @@ struct alignas(16) SelectShared {
     uint32_t tie_index;
     uint32_t cut[2];                           // a cut's key and index
     uint32_t verdict;
-    uint32_t drawn;                            // a near draw and how far u is from its token's ends
-    unsigned long long slack;
+    uint32_t drawn;                            // a sure draw by near sums (kAll: none)
     uint32_t steps[kSteps];
     float2 pow2[kPow2Steps];
 };
@@ -638,11 +637,11 @@ struct Row {
     }
 
     // Where, in index order, the running sum of weigh(vector, number) reaches aim(the row's sum):
-    // found(vector, number, the sum before it, target) is called by the one thread of the row that has
-    // it.  By warps over runs of the row, then by the warps of the CTA that has it over parts of that
+    // found(vector, number, the sum before it, target, ...) is called by the one thread of the row that
+    // has it; with it the sums of off(), a thread's after its weights, over the runs up to and from its.  By warps over runs of the row, then by the warps of the CTA that has it over parts of that
     // run, then by one warp.
-    template <class F, class A, class G>
-    __device__ __forceinline__ void locate(F weigh, A aim, G found) {
+    template <class F, class O, class A, class G>
+    __device__ __forceinline__ void locate(F weigh, O off, A aim, G found) {
         auto run_sum = [&](int s0, int s1) {
             unsigned long long v = 0;
             for (int i0 = s0 + lane; i0 - lane < s1; i0 += kBatch * 32) {
@@ -659,18 +658,25 @@ struct Row {
         };
         const int run = (n + kWarps - 1) / kWarps;
         const unsigned long long mine = run_sum(min(n, warp * run), min(n, (warp + 1) * run));
-        if (lane < static_cast<int>(cs)) st_peer(peer(&sh->seg[turn][rank * kWarps + warp], lane), mine);
+        const unsigned long long bound = warp_sum(off());
+        if (lane < static_cast<int>(cs)) {
+            st_peer(peer(&sh->seg[turn][rank * kWarps + warp], lane), mine);
+            st_peer(peer(&sh->seg2[turn][rank * kWarps + warp], lane), bound);
+        }
         sync();
         // the runs' sums, two to a lane in order
         static_assert(kMaxCluster * kWarps == 64, "two runs a lane");
         const uint32_t g0 = 2 * lane;
         const unsigned long long a0 = g0 < cs * kWarps ? sh->seg[turn][g0] : 0ull, a1 = g0 + 1 < cs * kWarps ? sh->seg[turn][g0 + 1] : 0ull;
-        const unsigned long long incl = warp_scan(a0 + a1, lane);
+        const unsigned long long b = (g0 < cs * kWarps ? sh->seg2[turn][g0] : 0ull) + (g0 + 1 < cs * kWarps ? sh->seg2[turn][g0 + 1] : 0ull);
+        const unsigned long long incl = warp_scan(a0 + a1, lane), b_incl = warp_scan(b, lane);
         turn ^= 1;
         const unsigned long long target = aim(__shfl_sync(kAll, incl, 31));
         const uint32_t hits = __ballot_sync(kAll, incl >= target);
         if (!hits) return;  // (no row that aims within its sum)
         const int owner = __ffs(hits) - 1;
+        const unsigned long long b_upto = __shfl_sync(kAll, b_incl, owner);
+        const unsigned long long b_from = __shfl_sync(kAll, b_incl, 31) - __shfl_sync(kAll, b_incl - b, owner);
         const bool second = incl - a1 < target;
         const uint32_t g = __shfl_sync(kAll, g0 + second, owner);
         unsigned long long before = __shfl_sync(kAll, incl - a1 - (second ? 0ull : a0), owner);
@@ -696,7 +702,7 @@ struct Row {
             const unsigned long long x = weigh(v, i), incl = before + warp_scan(x, lane);
             const uint32_t hit = __ballot_sync(kAll, incl >= target);
             if (hit) {
-                if (lane == __ffs(hit) - 1) found(v, i, incl - x, target);
+                if (lane == __ffs(hit) - 1) found(v, i, incl - x, target, b_upto, b_from);
                 return;
             }
             before = __shfl_sync(kAll, incl, 31);
@@ -716,8 +722,8 @@ struct Row {
                 for (int q = 0; q < kPer; ++q) c += is(l[q], index(i, q));
                 return c;
             },
-            [&](unsigned long long) { return r; },
-            [&](const uint4 &v, int i, unsigned long long before, unsigned long long target) {
+            []() { return 0ull; }, [&](unsigned long long) { return r; },
+            [&](const uint4 &v, int i, unsigned long long before, unsigned long long target, unsigned long long, unsigned long long) {
                 float l[kPer];
                 unpack(v, l);
 #pragma unroll
