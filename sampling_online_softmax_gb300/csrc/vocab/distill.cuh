@@ -184,8 +184,9 @@ struct Distill {
         const int upto = whole_upto(), i = tid < whole_from() ? tid + kDThreads : tid;
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            v[j] = make_uint4(0, 0, 0, 0);
-            if (i + j * kDThreads < upto) v[j] = load(i + j * kDThreads);
+            uint4 one[1] = {make_uint4(0, 0, 0, 0)};
+            if (i + j * kDThreads < upto) load(i + j * kDThreads, one);
+            v[j] = one[0];
         }
     }
     template <class L, class F>
@@ -210,8 +211,7 @@ struct Distill {
         }
         for (; i + (kBatch - 1) * kDThreads < upto; i += kBatch * kDThreads, dst += 16 * kBatch * kDThreads) {
             uint4 v[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) v[j] = load(i + j * kDThreads);
+            load(i, v);
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
                 float l[kPer];
@@ -219,15 +219,19 @@ struct Distill {
                 put(dst + 16 * j * kDThreads, packed(l));
             }
         }
+        uint4 v[1];
         for (; i < upto; i += kDThreads, dst += 16 * kDThreads) {
             float l[kPer];
-            make(load(i), l);
+            load(i, v);
+            make(v[0], l);
             put(dst, packed(l));
         }
-        for (int j = tid; j < part.n; j += kDThreads) {
-            if (j >= from && j < upto) continue;
+        // the rest: vector 0 before `from`, and those from `upto` on
+        for (int j = tid < from || upto == 0 ? tid : upto + (tid + kDThreads - upto % kDThreads) % kDThreads; j < part.n;
+             j = j < from && upto > 0 ? upto + (tid + kDThreads - upto % kDThreads) % kDThreads : j + kDThreads) {
             float l[kPer];
-            make(load(j), l);
+            load(j, v);
+            make(v[0], l);
 #pragma unroll
             for (int q = 0; q < kPer; ++q) {
                 const int x = part.index(j, q);
@@ -243,7 +247,7 @@ struct Distill {
             reinterpret_cast<__nv_bfloat16 *>(a.grad)[e] = __float2bfloat16_rn(v);
     }
     __device__ __forceinline__ void fill(float g) const {
-        write([](int) { return make_uint4(0, 0, 0, 0); },
+        write([](int, auto &v) { v[0] = make_uint4(0, 0, 0, 0); },
               [&](const uint4 &, float(&v)[kPer]) {
 #pragma unroll
                   for (int q = 0; q < kPer; ++q) v[q] = g;
@@ -310,9 +314,7 @@ struct Running {
 
     template <int N>
     __device__ __forceinline__ void add(const uint4 (&v)[N], float c) {
-        float top = P::vector_max(v[0]);  // NaN if there is one
-#pragma unroll
-        for (int j = 1; j < N; ++j) top = max_nan(top, P::vector_max(v[j]));
+        const float top = P::vectors_max(v);  // NaN if there is one
         if (!(top <= m) && m == m) {      // (a NaN stays)
             const float to = top * c;
             const float f = m > -INFINITY ? ptx::ex2(fabsf(to) < kHuge ? q - to : (m - top) * c) : 0.f;
@@ -517,11 +519,11 @@ __global__ void __launch_bounds__(kDThreads, kTrainCtas) distill_kernel(const Di
         Running<EB> r;
         int i = tid;
         const int n = d.part.n;
-        for (; i + kDThreads < n; i += 2 * kDThreads) {
-            const uint4 v[2] = {buf[i], buf[i + kDThreads]};
+        for (; i + 3 * kDThreads < n; i += 4 * kDThreads) {
+            const uint4 v[4] = {buf[i], buf[i + kDThreads], buf[i + 2 * kDThreads], buf[i + 3 * kDThreads]};
             r.add(v, d.c);
         }
-        if (i < n) {
+        for (; i < n; i += kDThreads) {
             const uint4 v[1] = {buf[i]};
             r.add(v, d.c);
         }
@@ -547,18 +549,30 @@ __global__ void __launch_bounds__(kDThreads, kTrainCtas) distill_kernel(const Di
             from = ahead.copy_from();
             upto = ahead.copy_upto();
         }
-        auto take = [&](int j) {
-            const uint4 v = buf[j];
+        auto take = [&](int j, auto &v) {
+            constexpr int N = static_cast<int>(sizeof(v) / sizeof(uint4));
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[e] = buf[j + e * kDThreads];
             // (an address that waits for v: the copy must not overtake the read)
-            if (j >= from && j < upto) copy16(smem_u32(buf + j) + (v.w & a.zero), ahead.at(j));
-            return v;
+            const uint32_t dst = smem_u32(buf + j);
+            const unsigned char *src = ahead.at(j);
+            if (j >= from && j + (N - 1) * kDThreads < upto) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) copy16(dst + 16 * e * kDThreads + (v[e].w & a.zero), src + 16 * e * kDThreads);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (j + e * kDThreads >= from && j + e * kDThreads < upto)
+                        copy16(dst + 16 * e * kDThreads + (v[e].w & a.zero), src + 16 * e * kDThreads);
+            }
         };
         __syncthreads();  // the entries' logits have been read, the bitmap is complete
         if (sound) {
             d.gradient(w * d.invT, m, s, own, turn, take);
         } else {
             d.fill(NAN);
-            for (int j = tid; j < n; j += kDThreads) take(j);
+            uint4 v[1];
+            for (int j = tid; j < n; j += kDThreads) take(j, v);
             __syncthreads();
         }
         last.row = row;
@@ -578,7 +592,8 @@ __global__ void __launch_bounds__(kDThreads, kTrainCtas) distill_kernel(const Di
         if (tid == 0) sh->twice[turn ^ 1] = 0;
         row = next;
         w = next_w;
-        d.place(row, rank);
+        d.b = next;
+        d.part = ahead;
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
             d.id[j] = ids[j];
@@ -600,7 +615,10 @@ __global__ void __launch_bounds__(kDThreads, 4) distill_backward_kernel(const Di
         d.fill(0.f);
         return;
     }
-    auto fetch = [&](int i) { return d.part.fetch(i); };
+    auto fetch = [&](int i, auto &v) {
+#pragma unroll
+        for (int j = 0; j < static_cast<int>(sizeof(v) / sizeof(uint4)); ++j) v[j] = d.part.fetch(i + j * kDThreads);
+    };
     uint4 first[Distill<EB, SLOTS>::kBatch];
     d.ask_teacher(b, d.id, d.t);
     d.ask_first(fetch, first);

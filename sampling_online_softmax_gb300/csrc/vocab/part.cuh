@@ -133,6 +133,24 @@ struct Part {
         }
         return max_nan(max_nan(__uint_as_float(v.x), __uint_as_float(v.y)), max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
+    // The largest logit of N vectors.
+    template <int N>
+    static __device__ __forceinline__ float vectors_max(const uint4 (&v)[N]) {
+        if (EB == 2) {
+            uint32_t m[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) m[j] = max2(max2(v[j].x, v[j].y), max2(v[j].z, v[j].w));
+#pragma unroll
+            for (int h = N / 2; h; h >>= 1)
+#pragma unroll
+                for (int j = 0; j < h; ++j) m[j] = max2(m[j], m[j + h]);
+            return max_nan(__uint_as_float(m[0] << 16), __uint_as_float(m[0] & 0xffff0000u));
+        }
+        float m = vector_max(v[0]);
+#pragma unroll
+        for (int j = 1; j < N; ++j) m = max_nan(m, vector_max(v[j]));
+        return m;
+    }
     // A vector of -inf.
     static __device__ __forceinline__ uint4 nothing() {
         const uint32_t w = EB == 2 ? 0xff80ff80u : 0xff800000u;
