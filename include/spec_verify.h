@@ -390,7 +390,8 @@ SPEC_API spec_status spec_top_logits(const void *logits, spec_dtype dtype, int B
  *   loss  [N] fp32;  stats [N, 2] fp32 (8-byte aligned): the row's largest logit and
  *         sum_v exp((s_v - largest) / T), for spec_distill_backward.
  *   grad  [N, V] of the logits' type, or NULL: the gradient of the sum of the
- *         losses, overwritten; it may be student_logits itself (in place).
+ *         losses, overwritten; it may be student_logits itself (in place), and
+ *         must not overlap it otherwise.
  *         With it the logits are read once for both.
  *   dev_status  SPEC_DEV_BAD_TOKEN; SPEC_DEV_NONFINITE: a row of weight other
  *         than 0 with NaN or +inf among its logits or its teacher's, or nothing

@@ -542,7 +542,7 @@ def _launch(fn, args, tensors, dev, stream):
         _check(st)
     if stream is not None and stream != torch.cuda.current_stream(dev):
         for t in tensors:
-            if t is not None:
+            if isinstance(t, torch.Tensor):
                 t.record_stream(stream)
 
 

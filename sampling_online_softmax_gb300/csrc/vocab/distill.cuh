@@ -115,10 +115,11 @@ struct Distill {
         if (a.lse) {
             top = 0.f;  // log p = t / T - lse
             const float z = __ldg(a.lse + b);
-            if (!(fabsf(z) < INFINITY)) wrong = true;
+            if (!(z < INFINITY)) wrong = true;
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
                 const bool any = t[j] > -INFINITY;
+                if (any && z == -INFINITY) wrong = true;  // (a masked row's teacher has no entries)
                 t[j] = any ? t[j] * invT - z : -INFINITY;
                 s += any ? expf(t[j]) : 0.f;
             }

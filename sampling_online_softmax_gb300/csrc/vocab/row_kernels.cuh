@@ -30,8 +30,9 @@ __device__ __forceinline__ unsigned long long share_of(unsigned long long W, flo
     return max(t + (rest ? 1ull : 0ull), 1ull);
 }
 
-// The first kept token, whatever its weight: what u = 0 draws.  A weight that is 0 in 64 bits
-// (below 2^-1074) is not drawn.
+// u = 0 draws the first kept token, whatever its weight: also one below half a unit, which the whole
+// numbers have as 0, and which min-p asks about in its own place.  A weight that is 0 in 64 bits (below
+// 2^-1074) is not drawn.
 __device__ __forceinline__ bool drawn_at_zero(float l, const Scale &sc, float min_p) {
     const float x = (l - sc.m) * sc.ch;
     return x > -1074.f && (min_p == 0.f || x >= log2f(min_p));
@@ -78,7 +79,7 @@ __device__ __forceinline__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, c
             if (a != b) return kWeigh;
             nk = a;
         }
-        nk = min(nk, static_cast<int>(c >> 32));
+        if (q.u > 0.f) nk = min(nk, static_cast<int>(c >> 32));  // (u = 0: see drawn_at_zero)
     }
     if (nk == 1) {
         if (tid == 0) *token = static_cast<int32_t>(index(0));
@@ -492,7 +493,7 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
         for (int again = 0; again < 2; ++again)
             if (cut_row<false>(r, sc, 0, q.p, again, &cut)) break;
     }
-    if (q.least) {
+    if (q.least && q.u > 0.f) {  // (u = 0: see drawn_at_zero)
         const uint32_t x = least_key(r, sc, q.least);
         if (x > cut.key) cut = {x, INT_MAX};
     }

@@ -380,15 +380,15 @@ struct Row {
             if (sh->maxima[(rank * per + j) * kThreads + tid] >= bound) sh->hit[atomicAdd(&sh->hit_n, 1u)] = static_cast<uint16_t>(j * kThreads + tid);
         __syncthreads();
         // (group, round) pairs, the rounds padded to a power of two: no division in number()
-        const int rounds = ((n + kThreads - 1) / kThreads + per - 1) / per;  // vectors of a group, at most
-        const int sh2 = 32 - __clz(rounds - 1);
-        const int total = static_cast<int>(sh->hit_n) << sh2;
+        const int rounds = max(1, ((n + kThreads - 1) / kThreads + per - 1) / per);  // vectors of a group, at most
+        const int bits = 32 - __clz(rounds - 1);
+        const int total = static_cast<int>(sh->hit_n) << bits;
         for (int e0 = tid; e0 - lane < total; e0 += kGather * kThreads) {
             auto number = [&](int j) {
                 const int e = e0 + j * kThreads;
                 if (e >= total) return -1;
-                const int group = sh->hit[e >> sh2];
-                const int i = ((e & ((1 << sh2) - 1)) * per + group / kThreads) * kThreads + group % kThreads;
+                const int group = sh->hit[e >> bits];
+                const int i = ((e & ((1 << bits) - 1)) * per + group / kThreads) * kThreads + group % kThreads;
                 return i < n ? i : -1;
             };
             uint4 v[kGather];

@@ -72,7 +72,7 @@ std::map<std::tuple<int, const void *, size_t, unsigned>, int> g_clusters;
 
 }  // namespace
 
-int resident_clusters(int dev, const void *kernel, const cudaLaunchConfig_t &cfg) {
+int resident_clusters(int dev, const void *kernel, const cudaLaunchConfig_t &cfg) try {
     const auto key = std::make_tuple(dev, kernel, cfg.dynamicSmemBytes, cfg.attrs[0].val.clusterDim.x);
     std::lock_guard<std::mutex> lock(g_clusters_mutex);
     const auto it = g_clusters.find(key);
@@ -84,6 +84,8 @@ int resident_clusters(int dev, const void *kernel, const cudaLaunchConfig_t &cfg
     }
     g_clusters[key] = n;
     return n;
+} catch (...) {  // (no exception leaves the C ABI)
+    return 0;
 }
 
 }  // namespace vocab

@@ -262,3 +262,39 @@ def test_offsets_past_32_bits():
     r = sv.spec_distill(x, ids, t, row_weight=w, grad=True, out=out)
     check(last, i, v, None, 1.0, None, dict(loss=r["loss"][-1:], stats=r["stats"][-1:]), x[-1:])
     assert (r["loss"][:-1] == 0).all() and not x[:-1].any()
+
+
+def test_a_masked_teacher_row_and_the_longest_rows():
+    """spec_top_logits of a masked row is a teacher without tokens: (-1, -inf, lse -inf)."""
+    for dtype, V in ((torch.float32, 262144), (torch.bfloat16, 524288), (torch.bfloat16, 3001)):
+        x, _, _, _ = inputs(3, V, 4, dtype, 9)
+        teacher = (x + 0.5).clone()
+        teacher[1] = float("-inf")
+        top = sv.spec_top_logits(teacher, 40, lse=True, temperature=0.9)
+        r = sv.spec_distill(x, top["ids"], top["values"], 0.9, top_lse=top["lse"], grad=True)
+        back = sv.spec_distill_backward(x, top["ids"], top["values"], r["stats"], torch.ones(3, device=DEV), 0.9, top_lse=top["lse"])["grad"]
+        assert int(r["status"][0]) == 0
+        assert float(r["loss"][1]) == 0 and not r["grad"][1].any() and not back[1].any()
+        for b in (0, 2):
+            sub = slice(b, b + 1)
+            check(x[sub], top["ids"][sub], top["values"][sub], top["lse"][sub], 0.9, None, dict(loss=r["loss"][sub], stats=r["stats"][sub]), r["grad"][sub])
+            check(x[sub], top["ids"][sub], top["values"][sub], top["lse"][sub], 0.9, None, None, back[sub], torch.ones(1))
+
+
+@pytest.mark.parametrize("N,V,dtype", [(700, 33000, torch.bfloat16), (1300, 2051, torch.float32), (260, 70001, torch.bfloat16)])
+def test_many_rows_with_ignored_ones_between(N, V, dtype):
+    """More rows than clusters are resident: each takes several, skipping ignored ones; odd rows, so that
+    neighbours share vectors; in place."""
+    x, ids, t, lse = inputs(N, V, 12, dtype, N, tail=True)
+    w = (torch.rand(N, generator=torch.Generator().manual_seed(1)) < 0.6).float().to(DEV) * 0.5
+    w[-3:] = 0
+    y = x.clone()
+    r = sv.spec_distill(x, ids, t, top_lse=lse, row_weight=w, grad=True)
+    out = dict(loss=torch.empty(N, device=DEV), stats=torch.empty((N, 2), device=DEV), grad=y)
+    sv.spec_distill(y, ids, t, top_lse=lse, row_weight=w, grad=True, out=out)
+    assert torch.equal(y, r["grad"]) and torch.equal(out["loss"], r["loss"]) and torch.equal(out["stats"], r["stats"])
+    pick = [int(b) for b in np.random.RandomState(0).choice(N, 25, replace=False)] + [0, 1, N - 4, N - 1]
+    i = torch.tensor(pick, device=DEV)
+    check(x[i], ids[i], t[i], lse[i], 1.0, w[i], dict(loss=r["loss"][i], stats=r["stats"][i]), r["grad"][i])
+    # every row's gradient sums to w (P - P) = 0 but for rounding: at most 2^-8 of the summed sizes, 2 w = 1
+    assert r["grad"].float().sum(1).abs().max() <= 2.0 ** -8

@@ -272,3 +272,54 @@ def test_magnitudes(scale):
         v, i, z = ref.top_logits(host(x[b]), 20)
         assert np.array_equal(r["ids"][b].cpu().numpy(), i) and np.array_equal(host(r["values"][b]), v)
         assert abs(float(r["lse"][b]) - z) <= 2.0 ** -20 + 2.0 ** -22 * abs(z)
+
+
+def test_a_zero_uniform_draws_the_first_kept_token():
+    """u = 0 under each filter, with weights below half a unit among the kept (2^-60 and 2^-100 of the largest)."""
+    for V in (300, 6000):
+        x = torch.full((4, V), -50.0 * 0.6931, device=DEV)
+        x[:, V - 1] = 0.0
+        x[:, 3] = -60.0 * 0.6931
+        x[:, 1] = -100.0 * 0.6931
+        u = torch.zeros(4, device=DEV)
+        for q in (dict(), dict(mp=(1e-20,)), dict(mp=(1e-25,)), dict(k=(V - 1,)), dict(mp=(1e-16,)), dict(k=(100,), mp=(1e-25,)), dict(k=(5000,), mp=(1e-25,)),
+                  dict(mp=(0.5,)), dict(p=(0.5,))):
+            q = params(4, 0, **q)
+            r = sv.spec_sample_filtered(x, u, **q)
+            want = [ref.sample_filtered(host(x[b]), 0.0, 1.0, int(q["top_k"][b]), float(q["top_p"][b]), float(q["min_p"][b]))[0] for b in range(4)]
+            assert r["tokens"].tolist() == want
+
+
+def test_the_first_call_may_be_captured():
+    """In a process of its own: each operator's first call inside a graph capture."""
+    import subprocess
+    import sys
+    code = """
+import torch, sampling_online_softmax_gb300 as sv
+x = torch.randn((6, 5003), device="cuda:0")
+u, T = torch.rand(6, device="cuda:0"), torch.ones(6, device="cuda:0")
+status = torch.zeros(1, dtype=torch.int32, device="cuda:0")
+o1 = dict(tokens=torch.zeros(6, dtype=torch.int32, device="cuda:0"))
+o2 = dict(values=torch.zeros((6, 9), device="cuda:0"), ids=torch.zeros((6, 9), dtype=torch.int32, device="cuda:0"))
+o3 = dict(loss=torch.zeros(6, device="cuda:0"), stats=torch.zeros((6, 2), device="cuda:0"), grad=torch.zeros_like(x))
+g3 = torch.zeros_like(x)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    sv.spec_sample_filtered(x, u, T, out=o1, status=status)
+    sv.spec_top_logits(x, 9, out=o2, status=status)
+    sv.spec_distill(x, o2["ids"], o2["values"], grad=True, out=o3, status=status)
+    sv.spec_distill_backward(x, o2["ids"], o2["values"], o3["stats"], T, out=g3, status=status)
+g.replay()
+torch.cuda.synchronize()
+a = sv.spec_sample_filtered(x, u, T)["tokens"]
+b = sv.spec_top_logits(x, 9)
+c = sv.spec_distill(x, b["ids"], b["values"], grad=True)
+torch.cuda.synchronize()
+assert torch.equal(a, o1["tokens"]) and torch.equal(b["ids"], o2["ids"]) and torch.equal(c["grad"], o3["grad"]) and int(status[0]) == 0
+assert (g3 - o3["grad"]).abs().max() < 1e-5
+print("ok")
+"""
+    import os
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
