@@ -183,6 +183,10 @@ struct Distill {
     template <class L>
     __device__ __forceinline__ void ask_first(L load, uint4 (&v)[kBatch]) const {
         const int upto = whole_upto(), i = tid < whole_from() ? tid + kDThreads : tid;
+        if (i + (kBatch - 1) * kDThreads < upto) {
+            load(i, v);
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
             uint4 one[1] = {make_uint4(0, 0, 0, 0)};
@@ -617,8 +621,13 @@ __global__ void __launch_bounds__(kDThreads, 4) distill_backward_kernel(const Di
         return;
     }
     auto fetch = [&](int i, auto &v) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(d.part.at(i));
+        if (sizeof(v) > sizeof(uint4) || !d.part.edge(i)) {  // (a batch is of whole vectors)
 #pragma unroll
-        for (int j = 0; j < static_cast<int>(sizeof(v) / sizeof(uint4)); ++j) v[j] = d.part.fetch(i + j * kDThreads);
+            for (int j = 0; j < static_cast<int>(sizeof(v) / sizeof(uint4)); ++j) v[j] = src[j * kDThreads];
+        } else {
+            v[0] = d.part.fetch(i);
+        }
     };
     uint4 first[Distill<EB, SLOTS>::kBatch];
     d.ask_teacher(b, d.id, d.t);
