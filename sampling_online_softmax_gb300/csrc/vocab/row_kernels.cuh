@@ -643,8 +643,9 @@ __device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) 
     // The short way: the list holds the logits from `low` on; all: that is every token.
     float low = -FLT_MAX;
     bool all = true;
-    int attempts = sums ? 2 : 1;
+    int attempts = sums ? kGoals : 1;
     unsigned long long W0 = 0, W1 = 0;
+    float need = 0.f;  // what a list has to weigh for top-p
     if (a.V > kWhole) {
         if (sums) {  // bounds of the row's weight
             float Q, off, s = r.exp_total(&Q, &off);
@@ -656,24 +657,25 @@ __device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) 
             const unsigned long long w = __float2ull_rn(sound ? s * unit : 0.f), e = __float2ull_ru(sound ? s * off * unit : 0.f);
             W0 = sound ? w - e : 1ull;
             W1 = sound ? w + e : 1ull << 62;
+            need = sound ? q.p * s : 0.f;
         }
         if (q.k > kMaxGoal || (q.k == 0 && !share && q.min_p == 0.f)) {
             attempts = 0;
-        } else if (q.k > 0 || share) {  // too few groups for it: few tokens that are not masked
-            all = !r.threshold(sc.m, q.k > 0 ? q.k : kFirstGoal, &low);
-        } else {  // from a little below what min-p asks for
+        } else if (q.k > 0) {  // too few groups for it: few tokens that are not masked
+            all = !r.threshold(sc.m, q.k, &low);
+        } else if (!share) {   // from a little below what min-p asks for
             const float x = log2f(q.min_p) / sc.ch;
             low = sc.m + x - (fabsf(x) + fabsf(sc.m)) * 0x1p-18f;
             all = false;
         }
     }
     for (int attempt = 0; attempt < attempts; ++attempt) {
-        // a list of the largest n logits weighs at most n, and about what its groups' maxima do
-        const float need = sums ? q.p * static_cast<float>(W0) * exp2f(static_cast<float>(-sc.U)) : 0.f;
-        if (sums && need > (attempt ? static_cast<float>(kMaxList) : 2.f * kFirstGoal)) continue;
-        if (attempt == 1) {
-            all = !r.threshold(sc.m, kMaxGoal, &low);
-            if (!all && 2.f * r.weight_of_maxima(sc.m, sc.ch, low) < need) break;
+        if (sums) {
+            const int goal = attempt == 0 ? kGoal0 : attempt == 1 ? kGoal1 : kMaxGoal;
+            // a list of the largest n logits weighs at most n, and a little more than its groups' maxima
+            if (need > 2.f * static_cast<float>(goal)) continue;
+            all = !r.threshold(sc.m, goal, &low);
+            if (!all && 1.15f * r.weight_of_maxima(sc.m, sc.ch, low) < need) continue;
         }
         if (all) low = -FLT_MAX;
         const uint32_t n = r.collect(low, attempt);

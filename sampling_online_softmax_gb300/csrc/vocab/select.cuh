@@ -35,8 +35,8 @@ constexpr int kCutPerThread = kCutBins / kThreads;
 constexpr int kGroups = kMaxCluster * kThreads;  // groups of a row's logits, whatever the cluster's size
 constexpr int kKeysPerThread = kGroups / kThreads;
 constexpr int kWhole = 128;                      // rows up to this long are listed whole
-constexpr int kFirstGoal = 64;                   // candidates asked for at first where top-p alone limits,
-constexpr int kMaxGoal = 1024;                   // and at most
+constexpr int kGoal0 = 64, kGoal1 = 256;         // candidates asked for where top-p alone limits, one after the
+constexpr int kMaxGoal = 1024, kGoals = 3;       // other (64 sort in a third of the time that 256 take), at most
 constexpr int kSteps = kThreads;                 // bins of the groups' maxima
 constexpr uint32_t kAll = 0xffffffffu;
 static_assert(kBinsPerThread % 4 == 0, "a thread reads its bins of a peer in 16-byte vectors");
@@ -64,11 +64,11 @@ struct alignas(16) SelectShared {
     };
     uint32_t maxima[kGroups];                  // keys of the groups' maxima, the whole row's
     unsigned long long seg[2][kMaxCluster * kWarps], seg2[2][kMaxCluster * kWarps];
-    uint32_t hits[2][kMaxCluster * kWarps];    // candidates of each warp of the cluster
+    uint32_t hits[kGoals][kMaxCluster * kWarps];    // candidates of each warp of the cluster
     unsigned long long red[kWarps];
     unsigned long long above;                  // a crossing: what lies above its bin,
     uint32_t cross_bin, cross_last;            // and the bin (kAll: none), or the last it may be in
-    uint32_t list_n[2];
+    uint32_t list_n[kGoals];
     uint32_t hit_n;
     uint32_t tie_index;
     uint32_t cut[2];                           // a cut's key and index
@@ -873,7 +873,7 @@ __device__ __forceinline__ Row<EB> row_setup(const RowArgs &a, SelectShared *sh,
     sh->steps[r.tid] = 0;
     if (r.tid == 0) sh->cross_bin = kAll;
     if (r.tid < kPow2Steps) sh->pow2[r.tid] = pow2[r.tid];
-    if (r.tid < 2) sh->list_n[r.tid] = 0;
+    if (r.tid < kGoals) sh->list_n[r.tid] = 0;
     r.part.place(a.base, a.end, a.V, b, static_cast<int>(r.rank), a.part);
     r.n = r.part.n;
     return r;
