@@ -814,15 +814,24 @@ __global__ void __launch_bounds__(kThreads, kRowCtas) row_kernel(const RowArgs a
         top_row<EB>(a, r, b);
 }
 
-// CTAs per row and vectors per CTA: one CTA a row where that gives every SM two rows, else enough to do
-// so, as long as a CTA has four vectors a thread.  (64 rows of 152064 bf16 logits, microseconds with 1, 2,
-// 4, 8 CTAs a row: short way 16.1, 15.1, 14.8, 16.7; unfiltered 127, 73, 46, 38.  512 rows, short way:
-// 62, 67, 92, 166.  The long way's passes want more CTAs: four an SM where no filter is given at all.)
-inline void row_split(RowArgs *a, int EB, int sms, bool unfiltered) {
+// CTAs per row and vectors per CTA.  The largest logits: the row is shared while all CTAs run at once
+// and each has 64 KB of it (16 KB where a long list is to be gathered).  64 rows of 32000 fp32, us with
+// 1, 2, 4, 8 CTAs a row: 8.6, 9.1, 9.0, 15.2; 1 row of 152064 bf16: 15.5, 14.1, 12.6, 12.4; the 777
+// largest of 12 rows of 50257 bf16: 20.8, 16.7, 14.9, 14.2.
+// Sampling, whose long way is passes over the row: shared while that leaves fewer than two CTAs an SM
+// (four where no filter is given at all) and each has four vectors a thread.  64 rows of 152064 bf16:
+// short way 16.1, 15.1, 14.8, 16.7, unfiltered 127, 73, 46, 38; 512 rows, short way: 62, 67, 92, 166.
+inline void row_split(RowArgs *a, int EB, int sms, bool top) {
     const long long vecs = (static_cast<long long>(a->V) * EB + 14) / 16 + 1;  // at the worst alignment
-    const long long want = (unfiltered && vecs > 8192 ? 4ll : 2ll) * sms;
+    const long long B = a->B;
     int cs = 1;
-    while (cs < kMaxCluster && a->B * static_cast<long long>(cs) < want && vecs / cs > 4 * kThreads) cs *= 2;
+    if (top) {
+        while (cs < kMaxCluster && 2 * cs * B <= kRowCtas * sms && vecs / cs > (a->K > 256 ? 1024 : 4096)) cs *= 2;
+    } else {
+        const bool unfiltered = !a->top_k && !a->top_p && !a->min_p;
+        const long long want = (unfiltered && vecs > 8192 ? 4ll : 2ll) * sms;
+        while (cs < kMaxCluster && B * cs < want && vecs / cs > 4 * kThreads) cs *= 2;
+    }
     a->cluster = cs;
     a->part = static_cast<int>((vecs + cs - 1) / cs);
 }
@@ -837,7 +846,7 @@ spec_status launch_rows(const RowArgs &a0, cudaStream_t stream) {
     auto kernel = row_kernel<EB, OP>;
     st = allow_max_dyn_smem(dev, reinterpret_cast<const void *>(kernel), &di);
     if (st != SPEC_OK) return st;
-    row_split(&a, EB, di.sms, OP == kSampleRows && !a.top_k && !a.top_p && !a.min_p);
+    row_split(&a, EB, di.sms, OP == kTopRows);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.B) * a.cluster);
     cfg.blockDim = dim3(kThreads);
