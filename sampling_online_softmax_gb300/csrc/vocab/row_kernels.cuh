@@ -580,6 +580,8 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
 template <int EB>
 __device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) {
     SelectShared *sh = r.sh;
+    uint4 first[Row<EB>::kStream];
+    r.load(r.tid, first);
     Request q;
     q.u = a.u[b];
     float T = a.temperature[b];
@@ -610,7 +612,7 @@ __device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) 
     }
     const bool share = q.p < 1.f && q.k == 0;  // top-p is a share of the whole row
     const bool sums = share && a.V > kWhole && !one;
-    sc.m = sums ? r.template stream<Row<EB>::kBounded>(sc.ch) : r.template stream<Row<EB>::kNone>(sc.ch);
+    sc.m = sums ? r.template stream<Row<EB>::kBounded>(sc.ch, first) : r.template stream<Row<EB>::kNone>(sc.ch, first);
     if (!(fabsf(sc.m) < INFINITY)) {  // NaN, +inf, or nothing but -inf
         if (r.rank == 0 && r.tid == 0) {
             a.tokens[b] = -1;
@@ -728,7 +730,9 @@ template <int EB>
 __device__ __forceinline__ void top_row(const RowArgs &a, Row<EB> &r, int b) {
     SelectShared *sh = r.sh;
     const float c = kLog2e / a.temp;
-    const float m = a.lse ? r.template stream<Row<EB>::kSum>(c) : r.template stream<Row<EB>::kNone>(c);
+    uint4 first[Row<EB>::kStream];
+    r.load(r.tid, first);
+    const float m = a.lse ? r.template stream<Row<EB>::kSum>(c, first) : r.template stream<Row<EB>::kNone>(c, first);
     const size_t out = static_cast<size_t>(b) * a.K;
     if (!(m < INFINITY)) {  // NaN or +inf
         if (r.rank == 0) {
@@ -815,7 +819,7 @@ __global__ void __launch_bounds__(kThreads, kRowCtas) row_kernel(const RowArgs a
 }
 
 // CTAs per row and vectors per CTA.  The largest logits: the row is shared while all CTAs run at once
-// and each has 64 KB of it (16 KB where a long list is to be gathered).  64 rows of 32000 fp32, us with
+// and each has 64 KB of it (16 KB where a long list is to be gathered, or the rows are few).  64 rows of 32000 fp32, us with
 // 1, 2, 4, 8 CTAs a row: 8.6, 9.1, 9.0, 15.2; 1 row of 152064 bf16: 15.5, 14.1, 12.6, 12.4; the 777
 // largest of 12 rows of 50257 bf16: 20.8, 16.7, 14.9, 14.2.
 // Sampling, whose long way is passes over the row: shared while that leaves fewer than two CTAs an SM
@@ -826,7 +830,7 @@ inline void row_split(RowArgs *a, int EB, int sms, bool top) {
     const long long B = a->B;
     int cs = 1;
     if (top) {
-        while (cs < kMaxCluster && 2 * cs * B <= kRowCtas * sms && vecs / cs > (a->K > 256 ? 1024 : 4096)) cs *= 2;
+        while (cs < kMaxCluster && 2 * cs * B <= kRowCtas * sms && vecs / cs > (a->K > 256 || 4 * cs * B <= sms ? 1024 : 4096)) cs *= 2;
     } else {
         const bool unfiltered = !a->top_k && !a->top_p && !a->min_p;
         const long long want = (unfiltered && vecs > 8192 ? 4ll : 2ll) * sms;

@@ -160,9 +160,25 @@ struct Row {
     // (ex2) relative; rebasing a sum to a larger q by (6 + |change|) 2^-24, which counts as 4 more of
     // |x|; and the sums by 2 + 3 (trees), 2 (pairs of floats), 5 + 5 levels of 2^-24.
     enum Sums : int { kNone = 0, kSum = 1, kBounded = 2 };  // kBounded: b too
+    static constexpr int kStream = 8;  // vectors of a batch: one of each group
+    __device__ __forceinline__ void load(int i0, uint4 (&v)[kStream]) const {
+        if (i0 > 0 && i0 + (kStream - 1) * kThreads < n - 1) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(part.at(i0));
+#pragma unroll
+            for (int j = 0; j < kStream; ++j) v[j] = __ldg(p + j * kThreads);
+        } else {  // the row's first and last vectors may hold a neighbour's logits
+#pragma unroll
+            for (int j = 0; j < kStream; ++j) {
+                const int i = i0 + j * kThreads;
+                v[j] = nothing();
+                if (i < n) v[j] = part.fetch(i);
+            }
+        }
+    }
+    // v: load(tid), ahead of what the caller waits for.
     template <int SUM>
-    __device__ __forceinline__ float stream(float c) {
-        constexpr int kBatch = 8;
+    __device__ __forceinline__ float stream(float c, uint4 (&v)[kStream]) {
+        constexpr int kBatch = kStream;
         static_assert(kBatch == kMaxCluster, "a batch's vectors are one of each group");
         float g[kBatch];
 #pragma unroll
@@ -204,21 +220,10 @@ struct Row {
                 }
             }
         };
-        for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
-            uint4 v[kBatch];
-            if (i0 > 0 && i0 + (kBatch - 1) * kThreads < n - 1) {
-                const uint4 *p = reinterpret_cast<const uint4 *>(part.at(i0));
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) v[j] = __ldg(p + j * kThreads);
-            } else {  // the row's first and last vectors may hold a neighbour's logits
-                const uint32_t none = EB == 2 ? 0xff80ff80u : 0xff800000u;
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const int i = i0 + j * kThreads;
-                    v[j] = i < n ? part.fetch(i) : make_uint4(none, none, none, none);
-                }
-            }
+        for (int i0 = tid; i0 < n;) {
             take(v);
+            i0 += kBatch * kThreads;
+            if (i0 < n) load(i0, v);
         }
         if (per <= 4) {
 #pragma unroll
