@@ -529,10 +529,26 @@ def _raw_stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _capturing(stream):
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _launch(fn, args, tensors, dev, stream):
     """Calls the library on `stream` (the device's current one where it is None), with the tensors'
-    device current; a stream that is not the current one keeps the tensors' memory until it is done."""
-    h = _raw_stream(dev.index) if stream is None else stream.cuda_stream
+    device current.  A stream that is not the current one first waits for it, where the tensors were
+    made (not into or out of a graph capture: there the caller orders), and keeps their memory until
+    it is done."""
+    current = None
+    if stream is None:
+        h = _raw_stream(dev.index)
+    else:
+        h = stream.cuda_stream
+        current = torch.cuda.current_stream(dev)
+        if stream == current:
+            current = None
+        elif not (_capturing(stream) or _capturing(current)):
+            stream.wait_stream(current)
     if dev.index == torch.cuda.current_device():
         st = fn(*args, h)
     else:
@@ -540,7 +556,7 @@ def _launch(fn, args, tensors, dev, stream):
             st = fn(*args, h)
     if st != SPEC_OK:
         _check(st)
-    if stream is not None and stream != torch.cuda.current_stream(dev):
+    if current is not None:
         for t in tensors:
             if isinstance(t, torch.Tensor):
                 t.record_stream(stream)

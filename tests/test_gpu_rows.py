@@ -13,6 +13,14 @@ import sampling_online_softmax_gb300 as sv
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def memory_given_back():
+    """What these tests keep cached (gigabytes) goes back to the device."""
+    yield
+    torch.cuda.empty_cache()
+
 NEAR = 2.0 ** -36
 
 
@@ -323,3 +331,27 @@ print("ok")
     import os
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
+
+
+def test_another_stream_waits_for_the_inputs():
+    """Inputs still being made on the current stream when the call goes to another one, and freed after it."""
+    side = torch.cuda.Stream()
+    big = torch.zeros((2048, 131072), device=DEV)
+    want = None
+    for _ in range(3):
+        for _ in range(20):
+            big.add_(1.0)                        # a millisecond or two before the logits are written
+        x = torch.zeros((64, 9001), device=DEV)
+        x[torch.arange(64, device=DEV), torch.arange(64, device=DEV) * 100 + 7] = 30.0
+        u, T = torch.full((64,), 0.5, device=DEV), torch.ones(64, device=DEV)
+        top = sv.spec_top_logits(x, 3, stream=side)
+        tok = sv.spec_sample_filtered(x, u, T, stream=side)
+        with torch.cuda.stream(side):
+            r = sv.spec_distill(x, top["ids"], top["values"], grad=True)
+        x.record_stream(side)
+        del x, u, T
+        junk = torch.full((64, 9001), 9.0, device=DEV)
+        torch.cuda.synchronize()
+        want = torch.arange(64, device=DEV, dtype=torch.int32) * 100 + 7
+        assert torch.equal(tok["tokens"], want) and torch.equal(top["ids"][:, 0], want) and torch.isfinite(r["loss"]).all()
+        del junk

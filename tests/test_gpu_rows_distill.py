@@ -21,6 +21,14 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
 
+@pytest.fixture(scope="module", autouse=True)
+def memory_given_back():
+    """What these tests keep cached (gigabytes) goes back to the device."""
+    yield
+    torch.cuda.empty_cache()
+
+
+
 def host(t):
     return t.detach().float().cpu().numpy().astype(np.float64)
 
