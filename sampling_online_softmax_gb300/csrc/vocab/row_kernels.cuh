@@ -803,7 +803,7 @@ __device__ __forceinline__ void top_row(const RowArgs &a, Row<EB> &r, int b) {
 }
 
 template <int EB, int OP>
-__global__ void __launch_bounds__(kThreads, OP == kTopRows ? kTopCtas : kSampleCtas) row_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kThreads, kRowCtas) row_kernel(const RowArgs a) {
     extern __shared__ uint4 dyn[];
     SelectShared *sh = reinterpret_cast<SelectShared *>(dyn);
     const int b = blockIdx.x / a.cluster;
@@ -830,7 +830,7 @@ inline void row_split(RowArgs *a, int EB, int sms, bool top) {
     const long long B = a->B;
     int cs = 1;
     if (top) {
-        while (cs < kMaxCluster && 2 * cs * B <= kTopCtas * sms && vecs / cs > (a->K > 256 || 4 * cs * B <= sms ? 1024 : 4096)) cs *= 2;
+        while (cs < kMaxCluster && 2 * cs * B <= kRowCtas * sms && vecs / cs > (a->K > 256 || 4 * cs * B <= sms ? 1024 : 4096)) cs *= 2;
     } else {
         const bool unfiltered = !a->top_k && !a->top_p && !a->min_p;
         const long long want = (unfiltered && vecs > 8192 ? 4ll : 2ll) * sms;

@@ -12,10 +12,10 @@ namespace spec {
 namespace vocab {
 
 constexpr int kThreads = 256;
-// CTAs per SM.  Sampling: with 3 its long way spills less (48 flat rows of 50257 fp32: 72 us against 78, 512
-// rows on top-p alone: 62 against 59); the largest logits: 4 hide more of each other's tails (1293 rows of
-// 2695 bf16: 19.9 us against 20.6).
-constexpr int kSampleCtas = 3, kTopCtas = 4;
+// CTAs of a row kernel per SM.  With 3 (80 registers) little is spilled: 48 flat rows of 50257 fp32 take
+// 65 us against 79 with 4, the 64 largest of 2304 rows of 129280 bf16 134 against 140; 4 hide more of each
+// other's tails where rows are short (1293 rows of 2695 bf16: 19.9 us against 20.6).
+constexpr int kRowCtas = 3;
 constexpr int kMaxCluster = 8;    // CTAs per row (the portable limit)
 constexpr int kMaxList = 2048;    // entries of a cluster's list
 
