@@ -479,7 +479,7 @@ def spec_sample_rows(logits, u, temperature, *, status=None, out=None, workspace
 # take the quick way first: one look at each tensor, and the named refusal only where it fails.
 def _need(t, name, dtype, shape, dev, index):
     """`t` is on the device, contiguous, and of this type and shape; returns its address."""
-    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()):  # (a CPU tensor's: -1)
         _cuda(t, name, dtype, dev)
         if tuple(t.shape) != tuple(shape):
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
