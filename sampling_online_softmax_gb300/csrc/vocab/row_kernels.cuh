@@ -30,12 +30,15 @@ __device__ __forceinline__ unsigned long long share_of(unsigned long long W, flo
     return max(t + (rest ? 1ull : 0ull), 1ull);
 }
 
+// Whether weights in units tell exactly which tokens min-p keeps: its own weight is 2^24 units or more,
+// or the draw is of a weight's place in a sum (u > 0), where fewer units weigh nothing.
+__device__ __forceinline__ bool by_weight(const Request &q) { return q.u > 0.f || q.least >> 24; }
 // u = 0 draws the first kept token, whatever its weight: also one below half a unit, which the whole
-// numbers have as 0, and which min-p asks about in its own place.  A weight that is 0 in 64 bits (below
-// 2^-1074) is not drawn.
-__device__ __forceinline__ bool drawn_at_zero(float l, const Scale &sc, float min_p) {
+// numbers have as 0; a min-p of so few units is asked about by its logarithm.  A weight that is 0 in
+// 64 bits (below 2^-1074) is not drawn.
+__device__ __forceinline__ bool drawn_at_zero(float l, const Scale &sc, const Request &q) {
     const float x = (l - sc.m) * sc.ch;
-    return x > -1074.f && (min_p == 0.f || x >= log2f(min_p));
+    return x > -1074.f && (!q.least || by_weight(q) || x >= log2f(q.min_p));
 }
 
 // The leader's part of a row whose kept tokens are among the n entries of its list, which holds the
@@ -79,7 +82,7 @@ __device__ __forceinline__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, c
             if (a != b) return kWeigh;
             nk = a;
         }
-        if (q.u > 0.f) nk = min(nk, static_cast<int>(c >> 32));  // (u = 0: see drawn_at_zero)
+        if (by_weight(q)) nk = min(nk, static_cast<int>(c >> 32));
     }
     if (nk == 1) {
         if (tid == 0) *token = static_cast<int32_t>(index(0));
@@ -88,7 +91,7 @@ __device__ __forceinline__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, c
     if (q.u == 0.f) {
         uint32_t x = kAll;
         for (int i = tid; i < nk; i += kThreads)
-            if (drawn_at_zero(value(i), sc, q.min_p)) x = min(x, index(i));
+            if (drawn_at_zero(value(i), sc, q)) x = min(x, index(i));
         x = __reduce_min_sync(kAll, x);
         __syncthreads();
         if (lane == 0) sh->red[warp] = x;
@@ -493,7 +496,7 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
         for (int again = 0; again < 2; ++again)
             if (cut_row<false>(r, sc, 0, q.p, again, &cut)) break;
     }
-    if (q.least && q.u > 0.f) {  // (u = 0: see drawn_at_zero)
+    if (q.least && by_weight(q)) {
         const uint32_t x = least_key(r, sc, q.least);
         if (x > cut.key) cut = {x, INT_MAX};
     }
@@ -505,7 +508,7 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
                 Row<EB>::unpack(v, l);
                 unsigned long long c = 0;
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) c += weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc, q.min_p);
+                for (int e = 0; e < kPer; ++e) c += weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc, q);
                 return c;
             },
             []() { return 0ull; }, [](unsigned long long) { return 1ull; },
@@ -515,7 +518,7 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
                 int x = -1;
 #pragma unroll
                 for (int e = kPer - 1; e >= 0; --e)
-                    if (weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc, q.min_p)) x = r.index(i, e);
+                    if (weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc, q)) x = r.index(i, e);
                 *token = x;
             });
         return;

@@ -355,3 +355,34 @@ def test_another_stream_waits_for_the_inputs():
         want = torch.arange(64, device=DEV, dtype=torch.int32) * 100 + 7
         assert torch.equal(tok["tokens"], want) and torch.equal(top["ids"][:, 0], want) and torch.isfinite(r["loss"]).all()
         del junk
+
+
+@pytest.mark.parametrize("V", [2, 300, 5003])
+def test_min_p_at_its_border_with_a_zero_uniform(V):
+    """Tokens whose weight lies within one fp32 step of min-p: the first token of each row is kept or
+    not by 2^-26 to 2^-24 of its weight, which 64 bits (and whole-number weights, right to 2^-38) tell
+    and fp32 logarithms do not.  At u = 0 the draw is that token where it is kept, else a later one."""
+    B = 64
+    g = torch.Generator().manual_seed(57)
+    x = torch.full((B, V), -30.0)
+    x[:, V - 1] = 0.0
+    x[:, 0] = -torch.rand((B,), generator=g) * 6.0
+    w = np.exp(x[:, 0].numpy().astype(np.float64))
+    mp = w.astype(np.float32)  # the nearest fp32, above the weight or below it
+    far = np.abs(mp.astype(np.float64) / w - 1)
+    assert (far > NEAR).all() and ((mp > w).sum() > 8) and ((mp < w).sum() > 8)
+    x = x.to(DEV)
+    one = torch.ones(B, device=DEV)
+    for u in (0.0, 1e-12):
+        r = sv.spec_sample_filtered(x, one * u, one, min_p=torch.tensor(mp, device=DEV))
+        assert int(r["status"][0]) == 0
+        assert r["tokens"].tolist() == [0 if a <= b else V - 1 for a, b in zip(mp.astype(np.float64), w)]
+    # the long way: nothing but min-p of a long flat row's tail
+    V = 60001
+    x = torch.zeros((B, V), device=DEV)
+    x[:, 0] = torch.tensor(np.log(w), dtype=torch.float32)
+    w = np.exp(x[:, 0].cpu().numpy().astype(np.float64))
+    mp = w.astype(np.float32)
+    assert (np.abs(mp.astype(np.float64) / w - 1) > NEAR).all()
+    r = sv.spec_sample_filtered(x, one * 0.0, one, min_p=torch.tensor(mp, device=DEV))
+    assert r["tokens"].tolist() == [0 if a <= b else 1 for a, b in zip(mp.astype(np.float64), w)]
