@@ -44,13 +44,19 @@ __device__ __forceinline__ bool drawn_at_zero(float l, const Scale &sc, const Re
 // The leader's part of a row whose kept tokens are among the n entries of its list, which holds the
 // row's n largest logits: sorts them, cuts, draws.  W0, W1: bounds of the weight of all tokens that
 // top-p is a share of, in units of 2^-U; 0: the list's own first k.  kWeigh: the bounds leave the
-// cut open; kMore: the cut lies past the list.
+// cut open; kMore: the cut lies past the list.  need: what it has to weigh, nearly
+// (0: not known); again: the list is sorted and weighed, its bounds are new.
 template <int EB>
 __device__ __forceinline__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, const Request &q, int n, unsigned long long W0, unsigned long long W1,
-                                  int32_t *token) {
+                                  float need, bool again, int32_t *token) {
     SelectShared *sh = r.sh;
     const int tid = r.tid, lane = r.lane, warp = r.warp;
-    sort_list(sh->list, n, sh->scratch, sh->red, tid);
+    if (need > 0.f) {
+        float s = 0.f;
+        for (int i = tid; i < n; i += kThreads) s += ptx::ex2((key_value(~static_cast<uint32_t>(sh->list[i] >> 32)) - sc.m) * sc.ch);
+        if (static_cast<float>(block_sum(__float2ull_rn(s * 0x1p24f), sh->red, lane, warp)) * (1.001f * 0x1p-24f) < need) return kMore;
+    }
+    if (!again) sort_list(sh->list, n, sh->scratch, sh->red, tid);
     int nk = q.k > 0 ? min(n, q.k) : n;
     auto value = [&](int i) { return key_value(~static_cast<uint32_t>(sh->list[i] >> 32)); };
     auto index = [&](int i) { return static_cast<uint32_t>(sh->list[i]); };
@@ -59,14 +65,16 @@ __device__ __forceinline__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, c
     // running sums of the sorted weights, a run of entries per thread
     const int per = (nk + kThreads - 1) / kThreads;
     const int i0 = min(nk, tid * per), i1 = min(nk, i0 + per);
-    unsigned long long mine = 0;
-    for (int i = i0; i < i1; ++i) {
-        mine += fixed_weight(value(i), sc, sh->pow2);
-        sh->cum[i] = mine;
+    if (!again) {
+        unsigned long long mine = 0;
+        for (int i = i0; i < i1; ++i) {
+            mine += fixed_weight(value(i), sc, sh->pow2);
+            sh->cum[i] = mine;
+        }
+        const unsigned long long before = r.sum_before(mine);
+        for (int i = i0; i < i1; ++i) sh->cum[i] += before;
+        __syncthreads();
     }
-    const unsigned long long before = r.sum_before(mine);
-    for (int i = i0; i < i1; ++i) sh->cum[i] += before;
-    __syncthreads();
 
     if (q.p < 1.f || q.least) {
         const unsigned long long total = sh->cum[nk - 1];
@@ -141,12 +149,12 @@ struct Cut {
 };
 
 // Weights of a vector's kept tokens.  Near: 2^((l - m) c) by ex2, off by at most
-//   3 2^-24 |x| ln 2 (difference, product and c round) + 2^-22 (ex2) + 3 2^-24 (sums of eight)
+//   3.25 2^-24 |x| ln 2 (difference, product, c and its log2 e round) + 2^-22 (ex2) + 3 2^-24 (sums of eight)
 // relative, which bound() adds up; in units of 2^-40.  Exact: fixed_weight, in units of 2^-U.
 template <int EB>
 struct Weigh {
     static constexpr int kPer = Row<EB>::kPer;
-    static constexpr float kPerBit = 2.1f * 0x1p-24f, kFlat = 7.5f * 0x1p-24f;
+    static constexpr float kPerBit = 2.3f * 0x1p-24f, kFlat = 7.5f * 0x1p-24f;
     const Scale &sc;
     const float2 *pow2;
     float floor;
@@ -162,16 +170,20 @@ struct Weigh {
         *b = fmaf(w, fmaf(-x, kPerBit, kFlat), *b);
         return w;
     }
+    // The sum of a vector's weights, three roundings deep.  (Sums over the row that share their tokens'
+    // errors are off from one another by no more than the whole's: the cut compares A with p W.)
+    static __device__ __forceinline__ float tree(const float (&w)[kPer]) {
+        const float s = (w[0] + w[1]) + (w[2] + w[3]);
+        return kPer == 4 ? s : s + ((w[4 % kPer] + w[5 % kPer]) + (w[6 % kPer] + w[7 % kPer]));
+    }
     // The kept weights of a vector, and in *b their error's bound.
     __device__ __forceinline__ unsigned long long near_sum(const Row<EB> &r, const uint4 &v, int i, float *b) const {
         if (!(Row<EB>::vector_max(v) >= floor)) return 0ull;
-        float l[kPer], s = 0.f;
+        float l[kPer];
         Row<EB>::unpack(v, l);
 #pragma unroll
         for (int q = 0; q < kPer; ++q) l[q] = kept(l[q], r.index(i, q)) ? near(l[q], b) : 0.f;
-#pragma unroll
-        for (int q = 0; q < kPer; q += 2) s += l[q] + l[q + 1];
-        return __float2ull_rn(s * 0x1p40f);
+        return __float2ull_rn(tree(l) * 0x1p40f);
     }
     __device__ __forceinline__ unsigned long long exact(float l, int x) const {
         const unsigned long long w = fixed_weight(l, sc, pow2);
@@ -297,16 +309,22 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
 #pragma unroll
         for (int i = 0; i < kCutPerThread; ++i) low += lo[i], high += hi[i];
         unsigned long long run_l = r.sum_before(low, &all_l), run_h = r.sum_before(high, &all_h);
-        const unsigned long long t0 = share_of(all_l, p), t1 = share_of(all_h, p);
+        // a bin's end lies at or past the cut where (1 - p) of what lies up to it is at least p of what lies
+        // behind it (closer than its share of a sum that is known to 7 %): perhaps, and for certain
+        const float rest = 1.f - p;
+        uint32_t maybe = kCutBins - 1, sure = kCutBins - 1;
 #pragma unroll
         for (int i = 0; i < kCutPerThread; ++i) {
-            if (run_h < t0 && run_h + hi[i] >= t0) sh->cross_bin = first + i;
-            if (run_l < t1 && run_l + lo[i] >= t1) sh->cross_last = first + i;
             run_h += hi[i];
             run_l += lo[i];
+            if (share_of(run_h, rest) >= share_of(all_l - run_l, p)) maybe = min(maybe, first + i);
+            if (share_of(run_l, rest) >= share_of(all_h - run_h, p)) sure = min(sure, first + i);
         }
+        maybe = __reduce_min_sync(kAll, maybe);
+        sure = __reduce_min_sync(kAll, sure);
+        if (r.lane == 0) atomicMin(&sh->cross_bin, maybe), atomicMin(&sh->cross_last, sure);
         __syncthreads();
-        b0 = sh->cross_bin == kAll ? 0u : sh->cross_bin;
+        b0 = sh->cross_bin;
         b1 = sh->cross_last;
         exact |= edge(static_cast<float>(b1)) < all_l >> 14;
     }
@@ -326,16 +344,15 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
             const uint4 one = Row<EB>::pick(vec, j);
             const float top = Row<EB>::vector_max(one);
             if (!(top >= (COUNT ? fmaxf(weigh.floor, edge_l) : weigh.floor))) continue;
-            float l[kPer], s = 0.f, a = 0.f;
+            float l[kPer], w[kPer], a[kPer];
             Row<EB>::unpack(one, l);
 #pragma unroll
             for (int q = 0; q < kPer; ++q) {
                 const bool in = weigh.kept(l[q], r.index(i0 + j * kThreads, q));
                 const float at = place(l[q]);
                 if (!COUNT && !exact) {
-                    const float w = in ? weigh.near(l[q], &b) : 0.f;
-                    s += w;
-                    a += at < from ? w : 0.f;
+                    w[q] = in ? weigh.near(l[q], &b) : 0.f;
+                    a[q] = at < from ? w[q] : 0.f;
                 }
                 if (in && at >= from && at < upto) atomicAdd(&sh->count[sub(at)], 1u);
             }
@@ -347,8 +364,8 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
                     A += place(l[q]) < from ? w : 0ull;
                 }
             } else if (!COUNT) {
-                W += __float2ull_rn(s * 0x1p40f);
-                A += __float2ull_rn(a * 0x1p40f);
+                W += __float2ull_rn(W_::tree(w) * 0x1p40f);
+                A += __float2ull_rn(W_::tree(a) * 0x1p40f);
                 ++vectors;
             }
         }
@@ -357,7 +374,7 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
         r.sync();
     } else {
         r.sum2(W, A);
-        if (!exact) B = r.sum(W_::bound(b * 2.f, 2 * vectors));  // (sums in a row, not a tree: 7 2^-24 more)
+        if (!exact) B = r.sum(W_::bound(b, 2 * vectors));
         target = share_of(W, p);
     }
     r.cut_bins(v);
@@ -398,21 +415,22 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
             const uint4 one = Row<EB>::pick(vec, j);
             const float top = Row<EB>::vector_max(one);
             if (!(top >= fmaxf(weigh.floor, edge_l))) continue;
-            float l[kPer], s = 0.f;
+            float l[kPer], w[kPer];
             Row<EB>::unpack(one, l);
 #pragma unroll
             for (int e = 0; e < kPer; ++e) {
                 const float at = place(l[e]);
+                w[e] = 0.f;
                 if (!(at >= from && at < upto) || !weigh.kept(l[e], r.index(i0 + j * kThreads, e))) continue;
                 const int y = sub(at);
                 if (y < static_cast<int>(s0)) {
-                    if (!COUNT && !exact) s += weigh.near(l[e], &b);
+                    if (!COUNT && !exact) w[e] = weigh.near(l[e], &b);
                     if (!COUNT && exact) between += fixed_weight(l[e], sc, weigh.pow2);
                 } else if (y <= static_cast<int>(s1)) {
                     bits |= 1ull << (j * kPer + e);
                 }
             }
-            if (!COUNT && s > 0.f) between += __float2ull_rn(s * 0x1p40f);
+            if (!COUNT && !exact) between += __float2ull_rn(W_::tree(w) * 0x1p40f);
         }
         found += r.append(bits, 1, [&](int j) { return i0 + j * kThreads; });
     });
@@ -683,13 +701,14 @@ __device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) 
             if (!all && 1.15f * r.weight_of_maxima(sc.m, sc.ch, low) < need) continue;
         }
         if (all) low = -FLT_MAX;
+        const bool part = share && !all;
         const uint32_t n = r.collect(low, attempt);
         if (n > kMaxList) break;
-        const bool part = share && !all;
         uint32_t v = kDone;
         for (int weighed = 0; weighed < 3; ++weighed) {
             if (r.rank == 0) {
-                v = draw_from_list(r, sc, q, n, part ? W0 : 0ull, part ? W1 : 0ull, a.tokens + b);
+                v = draw_from_list(r, sc, q, n, part ? W0 : 0ull, part ? W1 : 0ull, part && n > kThreads / 2 && weighed == 0 ? need : 0.f,
+                                   weighed > 0, a.tokens + b);
                 if (part && r.tid < static_cast<int>(r.cs)) st_peer(peer(&sh->verdict, r.tid), v);
             }
             if (!part) return;
@@ -704,15 +723,15 @@ __device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) 
                 r.vectors([&](const uint4(&v)[Row<EB>::kBatch], int) {
 #pragma unroll 1
                     for (int j = 0; j < Row<EB>::kBatch; ++j) {
-                        float l[Row<EB>::kPer], s = 0.f;
+                        float l[Row<EB>::kPer];
                         Row<EB>::unpack(Row<EB>::pick(v, j), l);
 #pragma unroll
-                        for (int x = 0; x < Row<EB>::kPer; ++x) s += l[x] >= low || l[x] == -INFINITY ? 0.f : weigh.near(l[x], &e);
-                        rest += __float2ull_rn(s * 0x1p40f);
+                        for (int x = 0; x < Row<EB>::kPer; ++x) l[x] = l[x] >= low || l[x] == -INFINITY ? 0.f : weigh.near(l[x], &e);
+                        rest += __float2ull_rn(Weigh<EB>::tree(l) * 0x1p40f);
                         ++vectors;
                     }
                 });
-                bound = Weigh<EB>::bound(2.f * e, vectors);  // (in a row, not a tree)
+                bound = Weigh<EB>::bound(e, vectors);
                 r.sum2(rest, bound);
                 const unsigned long long listed = sh->cum[n - 1];
                 W0 = listed + ((rest - min(rest, bound)) << (sc.U - 40));

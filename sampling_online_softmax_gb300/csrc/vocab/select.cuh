@@ -164,7 +164,7 @@ struct Row {
     // Reads the part; then the largest logit of the row (returned; NaN if there is one), the keys of
     // the groups' maxima in sh->maxima of every CTA, and with kSum what exp_total() takes: a sum s of
     // 2^x, x = l c - q, for every warp, its q, and (kBounded) b, the sum of 2^x |x|, for the error.  q is a rounded
-    // maximum times c and counts as exact, so a term is off by 2 |x| 2^-24 ln 2 (x and c round) + 2^-22
+    // maximum times c and counts as exact, so a term is off by 2.25 |x| 2^-24 ln 2 (x, c and its log2 e round) + 2^-22
     // (ex2) relative; rebasing a sum to a larger q by (6 + |change|) 2^-24, which counts as 4 more of
     // |x|; and the sums by 2 + 3 (trees), 2 (pairs of floats), 5 + 5 levels of 2^-24.
     enum Sums : int { kNone = 0, kSum = 1, kBounded = 2 };  // kBounded: b too
@@ -317,7 +317,7 @@ struct Row {
             b += __shfl_xor_sync(kAll, b, o);
         }
         *q = Q;
-        *off = (1.5f * (b / s) + 24.f) * (1.01f * 0x1p-24f);
+        *off = (1.6f * (b / s) + 24.f) * (1.01f * 0x1p-24f);
         return s;
     }
     // The smallest of the groups' maxima that is finite (the row's largest if there is no other).
