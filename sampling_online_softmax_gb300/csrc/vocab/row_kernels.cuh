@@ -484,6 +484,121 @@ __device__ __forceinline__ bool cut_row(Row<EB> &r, const Scale &sc, int k, floa
     return true;
 }
 
+// The same cut by top-p for bf16 rows, whose logits are few different ones (128 in each power of two): one
+// histogram of their keys and one exact weight a key, not a token.  Its 4096 bins are the keys from the
+// maximum's downwards, but for those of the 2 `skip` magnitudes next to 0 where the bins would not
+// reach to weights that count.  The few tokens of these, and those below the last bin, are weighed one by
+// one.  False where the cut is among them.  One row of 128256 in 8 CTAs: 10 us for the histogram, which the
+// shared atomics bound (a lane a clock), 6 to merge, weigh and find, 8 for the tie; by cut_row with exact
+// weights 45.
+__device__ __forceinline__ bool cut_by_keys(Row<2> &r, const Scale &sc, float p, Cut *cut) {
+    constexpr int kPer = Row<2>::kPer;
+    SelectShared *sh = r.sh;
+    const int tid = r.tid;
+    const Cut had = *cut;
+    const Weigh<2> weigh(sc, sh->pow2, had);
+    const float span = fminf(48.f / sc.ch, 2.f * (sc.m - r.least_maximum()));
+    const int top = static_cast<int>(Row<2>::key(sc.m)), end = static_cast<int>(Row<2>::key(fmaxf(sc.m - span, -FLT_MAX)));
+    int skip = 0;  // magnitudes (as bf16's bits) below it, where the bins lie on both sides of 0
+    if (top >= 0x8000 && end < 0x8000) {
+        skip = max(0, (top - end + 2 - kTally + 1) / 2);
+        if (top - 0x8000 < skip) return false;
+    }
+    const int last = top - 0x8000 - skip;  // the last bin above 0
+    r.sync();  // the histogram before this one has been read, by the peers too
+    for (int i = tid; i < kTally; i += kThreads) sh->tally[i] = 0;
+    if (tid == 0) sh->cross_bin = kAll;
+    __syncthreads();
+    unsigned long long near = 0, deep = 0;  // the weights next to 0, and below the last bin
+    r.vectors([&](const uint4(&vec)[Row<2>::kBatch], int i0) {
+#pragma unroll 1
+        for (int j = 0; j < Row<2>::kBatch; ++j) {
+            uint4 one = Row<2>::pick(vec, j);
+            if (!(Row<2>::vector_max(one) >= weigh.floor)) continue;
+            uint32_t rest = 0;
+#pragma unroll 1  // (the atomics set the pace)
+            for (int e = 0; e < kPer; e += 2) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float l = __uint_as_float(h ? one.x & 0xffff0000u : one.x << 16);
+                    const int k = static_cast<int>(Row<2>::key(l));
+                    const int d = top - k - (k < 0x8000 - skip ? 2 * skip : 0);
+                    const bool in = weigh.kept(l, r.index(i0 + j * kThreads, e + h)), out = d >= kTally || (k >= 0x8000 - skip && k < 0x8000 + skip);
+                    if (in && !out) atomicAdd(&sh->tally[d], 1u);
+                    if (in && out && (l - sc.m) * sc.ch > -60.f) rest |= 1u << (e + h);
+                }
+                one.x = one.y, one.y = one.z, one.z = one.w;
+            }
+            for (; rest; rest &= rest - 1) {
+                const float x = Part<2>::logit(r.part.at(i0 + j * kThreads), __ffs(rest) - 1);
+                const unsigned long long w = fixed_weight(x, sc, weigh.pow2);
+                if (top - static_cast<int>(Row<2>::key(x)) - 2 * skip >= kTally)
+                    deep += w;
+                else
+                    near += w;
+            }
+        }
+    });
+    r.sum2(near, deep);
+    // Each CTA sums and weighs its share of the bins; the one that has the cut tells it to the others.
+    const int per = kTally / kThreads / static_cast<int>(r.cs), base = static_cast<int>(r.rank) * per * kThreads;
+    uint32_t *whole = sh->whole + tid * per;
+    const int first = base + tid * per;
+    for (int h = 0; h < per; h += 2) {
+        uint2 v = make_uint2(0, 0);
+#pragma unroll
+        for (uint32_t c = 0; c < kMaxCluster; ++c) {
+            if (c >= r.cs) break;
+            const uint2 x = ld_peer2(peer(&sh->tally[first + h], c));
+            v.x += x.x, v.y += x.y;
+        }
+        *reinterpret_cast<uint2 *>(whole + h) = v;
+    }
+    auto key_of = [&](int d) { return static_cast<uint32_t>(top - d - (d > last ? 2 * skip : 0)); };
+    auto weight = [&](int d) {
+        const uint32_t c = whole[d - first];
+        return c ? c * fixed_weight(Row<2>::value(key_of(d)), sc, weigh.pow2) : 0ull;
+    };
+    unsigned long long mine = 0, all;
+#pragma unroll 1
+    for (int d = first; d < first + per; ++d) mine += weight(d);
+    unsigned long long run = r.sum_before(mine, &all);
+    if (tid < static_cast<int>(r.cs)) st_peer(peer(&sh->seg[r.turn][r.rank], tid), all);
+    r.sync();
+    all = near + deep;
+    for (uint32_t c = 0; c < r.cs; ++c) {
+        const unsigned long long x = sh->seg[r.turn][c];
+        if (c < r.rank) run += x;
+        all += x;
+    }
+    r.turn ^= 1;
+    const unsigned long long target = share_of(all, p);
+    if (run < target && run + mine + near >= target) {
+#pragma unroll 1
+        for (int d = first; d < first + per; ++d) {
+            const unsigned long long w = weight(d), before = run + (d > last ? near : 0ull);
+            if (before < target && before + w >= target) {
+                for (uint32_t c = 0; c < r.cs; ++c) {
+                    st_peer(peer(&sh->cross_bin, c), static_cast<uint32_t>(d));
+                    st_peer(peer(&sh->cross_last, c), whole[d - first]);
+                    st_peer(peer(&sh->above, c), target - before);
+                }
+            }
+            run += w;
+        }
+    }
+    r.sync();
+    const uint32_t d = sh->cross_bin, count = sh->cross_last;
+    if (d == kAll) return false;
+    const uint32_t key = key_of(d);
+    const unsigned long long w = fixed_weight(Row<2>::value(key), sc, weigh.pow2), kept = (sh->above + w - 1) / w;
+    cut->index = key == had.key ? had.index : INT_MAX;
+    if (kept < count) cut->index = r.tie_index(key, kept, cut->index);
+    cut->key = key;
+    return true;
+}
+__device__ __forceinline__ bool cut_by_keys(Row<4> &, const Scale &, float, Cut *) { return false; }
+
 // The key of the least logit whose weight is at least `least`; a warp's lanes try 32 keys at a time.
 template <int EB>
 __device__ __forceinline__ uint32_t least_key(const Row<EB> &r, const Scale &sc, unsigned long long least) {
@@ -510,7 +625,7 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
     SelectShared *sh = r.sh;
     Cut cut = {Row<EB>::kLowest, INT_MAX};
     if (q.k > 0) cut_row<true>(r, sc, q.k, 1.f, false, &cut);
-    if (q.p < 1.f) {
+    if (q.p < 1.f && !cut_by_keys(r, sc, q.p, &cut)) {
         for (int again = 0; again < 2; ++again)
             if (cut_row<false>(r, sc, 0, q.p, again, &cut)) break;
     }

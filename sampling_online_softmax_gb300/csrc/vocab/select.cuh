@@ -40,6 +40,7 @@ constexpr int kBins = 1 << kBinBits;
 constexpr int kBinsPerThread = kBins / kThreads;
 constexpr int kCutBins = 512;                    // bins of cut_row's histograms
 constexpr int kCutPerThread = kCutBins / kThreads;
+constexpr int kTally = 4096;                     // bins of cut_by_keys' histogram, a bf16 key each
 constexpr int kGroups = kMaxCluster * kThreads;  // groups of a row's logits, whatever the cluster's size
 constexpr int kKeysPerThread = kGroups / kThreads;
 constexpr int kWhole = 128;                      // rows up to this long are listed whole
@@ -63,12 +64,14 @@ struct alignas(16) SelectShared {
     union {                                    // the long way's histogram, or the leader's list:
         unsigned long long mass[kBins];
         uint32_t count[kBins];
+        uint32_t tally[kTally];
         unsigned long long list[kMaxList];     // (~key << 32) | index
     };
     union {
         unsigned long long cum[kMaxList];      // the leader's: running sums of the sorted list's weights
         uint16_t hit[kGroups];                 // this CTA's groups that reach a bound
         uint32_t scratch[kBins];               // sort_list's
+        uint32_t whole[kTally];                // the row's tally
     };
     uint32_t maxima[kGroups];                  // keys of the groups' maxima, the whole row's
     unsigned long long seg[2][kMaxCluster * kWarps], seg2[2][kMaxCluster * kWarps];
@@ -726,11 +729,15 @@ struct Row {
     // of the row.
     __device__ __forceinline__ int tie_index(uint32_t k, unsigned long long r, int last) {
         auto is = [&](float l, int x) { return key(l) == k && x <= last; };
+        const uint32_t twin = EB == 2 ? (__float_as_uint(value(k)) >> 16) * 0x10001u : 0u;
         locate(
             [&](const uint4 &v, int i) {
+                unsigned long long c = 0;
+                // (few vectors hold one: bf16 pairs are compared with it first, but for the two zeros)
+                if (EB == 2 && k != 0x8000u && !(__vcmpeq2(v.x, twin) | __vcmpeq2(v.y, twin) | __vcmpeq2(v.z, twin) | __vcmpeq2(v.w, twin)))
+                    return c;
                 float l[kPer];
                 unpack(v, l);
-                unsigned long long c = 0;
 #pragma unroll
                 for (int q = 0; q < kPer; ++q) c += is(l[q], index(i, q));
                 return c;

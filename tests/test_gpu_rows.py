@@ -386,3 +386,45 @@ def test_min_p_at_its_border_with_a_zero_uniform(V):
     assert (np.abs(mp.astype(np.float64) / w - 1) > NEAR).all()
     r = sv.spec_sample_filtered(x, one * 0.0, one, min_p=torch.tensor(mp, device=DEV))
     assert r["tokens"].tolist() == [0 if a <= b else 1 for a, b in zip(mp.astype(np.float64), w)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift,scale,T,k", [
+    (0.0, 2.0, 1.2, 0),         # both sides of 0
+    (40.0, 2.0, 1.5, 0),        # all above it
+    (-40.0, 2.0, 1.5, 0),       # all below it
+    (0.0, 0.01, 0.006, 0),      # around 0 on a small scale
+    (0.3, 0.001, 1.0, 0),       # few different bf16 values: thousands of equal logits at the cut
+    (-0.001, 1e-6, 1.0, 0),     # one value in bf16, next to 0
+    (0.0, 3000.0, 1500.0, 0),   # wide
+    (0.0, 1e30, 5e5, 0),        # next to nothing but the maximum
+    (0.0, 2.0, 1.2, 3001),      # top-p of the first k, k past a list's reach
+    (-3.0, 0.01, 1.0, 2999),
+])
+def test_the_cut_of_long_rows_wherever_their_logits_lie(shift, scale, T, k, dtype):
+    B, V = 5, 20011
+    g = torch.Generator().manual_seed(91)
+    x = (torch.randn((B, V), generator=g) * scale + shift).to(dtype).to(DEV)
+    x[1, ::3] = float("-inf")
+    x[2, 7] = x[2].max() + 0.5 * scale
+    u = torch.tensor([0.11, 0.37, 0.52, 0.71, 0.93], device=DEV)
+    for p in (0.3, 0.9, 0.999):
+        check_sample(x, u, params(B, 0, T=(T,), k=(k,), p=(p,)))
+
+
+@pytest.mark.parametrize("B", [1, 3, 200])
+def test_the_cut_among_logits_next_to_zero(B):
+    """Most of the weight on tokens a millionth from 0, between logits of both signs: bf16 keys that no
+    histogram of a few thousand bins has beside those of the others."""
+    V = 30001
+    g = torch.Generator().manual_seed(92)
+    x = torch.randn((B, V), generator=g) * 1e-6
+    x[:, ::10] = torch.randn((B, (V + 9) // 10), generator=g) * 2 - 8
+    x[:, 5] = 3.0
+    x = x.to(torch.bfloat16).to(DEV)
+    u = torch.rand((B,), generator=g).to(DEV)
+    n = min(B, 3)  # (the oracle's time)
+    r = sv.spec_sample_filtered(x, u, torch.ones(B, device=DEV), top_p=torch.full((B,), 0.6, device=DEV))
+    check_sample(x[:n].contiguous(), u[:n].contiguous(), params(n, 0, T=(1.0,), p=(0.6,)))
+    assert r["tokens"][:n].tolist() == sv.spec_sample_filtered(
+        x[:n].contiguous(), u[:n].contiguous(), torch.ones(n, device=DEV), top_p=torch.full((n,), 0.6, device=DEV))["tokens"].tolist()
