@@ -957,11 +957,13 @@ __global__ void __launch_bounds__(kThreads, kRowCtas) row_kernel(const RowArgs a
 
 // CTAs per row and vectors per CTA.  The largest logits: the row is shared while all CTAs run at once
 // and each has 64 KB of it (16 KB where a long list is to be gathered, or the rows are few).  64 rows of 32000 fp32, us with
-// 1, 2, 4, 8 CTAs a row: 8.6, 9.1, 9.0, 15.2; 1 row of 152064 bf16: 15.5, 14.1, 12.6, 12.4; the 777
-// largest of 12 rows of 50257 bf16: 20.8, 16.7, 14.9, 14.2.
+// 1, 2, 4, 8 CTAs a row: 8.5, 8.8, 8.7, 14.8; 1 row of 152064 bf16: 15.2, 11.7, 10.0, 9.3; the 777
+// largest of 12 rows of 50257 bf16: 20.2, 16.3, 14.9, 14.3.
 // Sampling, whose long way is passes over the row: shared while that leaves fewer than two CTAs an SM
-// (four where no filter is given at all) and each has four vectors a thread.  64 rows of 152064 bf16:
-// short way 16.1, 15.1, 14.8, 16.7, unfiltered 127, 73, 46, 38; 512 rows, short way: 62, 67, 92, 166.
+// (four where no filter is given at all) and each has four vectors a thread, by 8 only where all run at
+// once (a tenth of the places lie where no cluster of 8 fits).  64 rows of 152064 bf16: short way 14.1, 13.8,
+// 13.8, 21.7, unfiltered 128, 74, 46, 46; 48 flat rows of 50257 fp32, all the long way: 186, 108, 75, 61; 512
+// rows of 152064, short way: 61, 70, 95, 173.
 inline void row_split(RowArgs *a, int EB, int sms, bool top) {
     const long long vecs = (static_cast<long long>(a->V) * EB + 14) / 16 + 1;  // at the worst alignment
     const long long B = a->B;
@@ -971,7 +973,7 @@ inline void row_split(RowArgs *a, int EB, int sms, bool top) {
     } else {
         const bool unfiltered = !a->top_k && !a->top_p && !a->min_p;
         const long long want = (unfiltered && vecs > 8192 ? 4ll : 2ll) * sms;
-        while (cs < kMaxCluster && B * cs < want && vecs / cs > 4 * kThreads) cs *= 2;
+        while (cs < kMaxCluster && B * cs < want && vecs / cs > 4 * kThreads && (cs < 4 || 10 * 2 * cs * B <= 9 * kRowCtas * sms)) cs *= 2;
     }
     a->cluster = cs;
     a->part = static_cast<int>((vecs + cs - 1) / cs);

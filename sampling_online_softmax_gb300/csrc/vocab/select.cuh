@@ -13,7 +13,8 @@
 //
 // The long way, for rows of which thousands of tokens are kept: passes over the
 // row in L2.  A histogram of counts brackets the cut, a second one narrows it,
-// and the few tokens left are sorted; see cut_row.
+// and the few tokens left are sorted; see cut_row.  In bf16 one histogram of the
+// keys is enough; see cut_by_keys.
 //
 // Many rows: one CTA each, several to an SM, so that some stream while others
 // choose.  Few rows: a cluster shares a row through distributed shared memory.
@@ -22,9 +23,9 @@
 // trip to L2, a short sort: 8 to 10 us a row on a busy SM, 6 alone), hidden where an
 // SM has other rows to stream.  Measured (kernel alone, GB300): the 64 largest of 2304
 // rows of 129280 bf16 134 us, 4.4 TB/s of logits; top-p over 512 such rows of 152064
-// 62 us, 2.5 TB/s (all rows under way at once: stream 25 us, then tails); one row of
-// 32000 fp32 10 us.  The long way is bound by instructions (about 200 a token): 48
-// flat rows of 50257 fp32, 17000 tokens kept, 65 us.
+// 60 us, 2.6 TB/s (all rows under way at once: stream 25 us, then tails); one row of
+// 32000 fp32 10.7 us.  The long way is bound by instructions (450 a token in all) and by
+// its passes' barriers: 48 flat rows of 50257 fp32, 17000 tokens kept, 61 us.
 #pragma once
 
 #include "part.cuh"
