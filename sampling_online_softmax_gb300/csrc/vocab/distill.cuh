@@ -296,7 +296,7 @@ struct Distill {
         // exponents as l c - q, q the rounded m c, whose rounding goes into the factor
         const float q = m * c, A = g * sum_p / S;
         if (fabsf(q) < kHuge)
-            dense<true>(m, q, A * (1.f - 0.6931471805599453f * fmaf(-m, c, q)), get, ahead);
+            dense<true>(m, q, A * (1.f + 0.6931471805599453f * fmaf(-m, c, q)), get, ahead);
         else
             dense<false>(m, q, A, get, ahead);
         __syncthreads();

@@ -306,3 +306,23 @@ def test_many_rows_with_ignored_ones_between(N, V, dtype):
     check(x[i], ids[i], t[i], lse[i], 1.0, w[i], dict(loss=r["loss"][i], stats=r["stats"][i]), r["grad"][i])
     # every row's gradient sums to w (P - P) = 0 but for rounding: at most 2^-8 of the summed sizes, 2 w = 1
     assert r["grad"].float().sum(1).abs().max() <= 2.0 ** -8
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_gradient_of_large_logits(split):
+    """Logits around 200, where the maximum times log2 e rounds by up to 2^-16: the columns without a
+    teacher's entry, against 64 bits.  Those within 4 octaves of the maximum are off by at most 4 |x|
+    halves of 2^-23 ln 2 (l c, its c) and 4 of 2^-24 (ex2.approx) in the weight, as much in the
+    exp-sum, and 6 more of 2^-24 in sums and products: 32 of 2^-24 in all."""
+    V, K = 1501, 3
+    g = torch.Generator().manual_seed(33)
+    x = (torch.rand((8, V), generator=g) * 2.5 + 198.7).to("cuda:0")
+    ids = torch.randint(0, V, (8, K), generator=g, dtype=torch.int32).to("cuda:0")
+    t = torch.randn((8, K), generator=g).to("cuda:0")
+    r = sv.spec_distill(x, ids, t, grad=not split)
+    grad = r["grad"] if not split else sv.spec_distill_backward(x, ids, t, r["stats"], torch.ones(8, device="cuda:0"))["grad"]
+    q = torch.softmax(x.double(), 1)
+    q.scatter_(1, ids.long(), 0.0)
+    grad = grad.double().scatter_(1, ids.long(), 0.0)
+    off = ((grad - q).abs() / q.clamp(min=1e-30)).max().item()
+    assert off < 32 * 2.0 ** -24, off / 2.0 ** -24
