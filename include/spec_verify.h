@@ -101,7 +101,7 @@ typedef enum spec_dtype {
 #define SPEC_DEV_BAD_PARAM    64u  /* spec_sample_filtered: a row's parameter out of range (token -1) */
 
 /* Limits of the operators on rows of logits (spec_sample_filtered,
- * spec_top_logits, spec_distill: a row is kept in shared memory). */
+ * spec_top_logits, spec_distill, which keeps a row in a cluster's shared memory). */
 #define SPEC_MAX_ROW_BYTES (1 << 20) /* V * element size: 262144 fp32 or 524288 bf16 logits */
 #define SPEC_MAX_TOP       1024      /* K of spec_top_logits and spec_distill */
 

@@ -24,8 +24,8 @@
 // SM has other rows to stream.  Measured (kernel alone, GB300): the 64 largest of 2304
 // rows of 129280 bf16 134 us, 4.4 TB/s of logits; top-p over 512 such rows of 152064
 // 60 us, 2.6 TB/s (all rows under way at once: stream 25 us, then tails); one row of
-// 32000 fp32 10.7 us.  The long way is bound by instructions (450 a token in all) and by
-// its passes' barriers: 48 flat rows of 50257 fp32, 17000 tokens kept, 61 us.
+// 32000 fp32 10.7 us.  The long way is bound by instructions (430 a token in all), by
+// their fetching and by its passes' barriers: 48 flat rows of 50257 fp32, 17000 tokens kept, 61 us.
 #pragma once
 
 #include "part.cuh"
