@@ -60,9 +60,13 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-// Beyond it a maximum's product with c is taken for overflowing, and (l - m) c is computed as that.
-constexpr float kHuge = 1e38f;
-// 2^((l - m) c) of two logits: as l c - q, q the rounded m c (PLAIN), or as it stands.
+// Exponents (l - m) c are formed as l c - q, q the rounded m c, in one operation a pair, where |q| is below
+// this: q is then off by 2^-13 at most, which is made up for to the first order (the second: 2^-28).
+// Beyond it (finite masks, small temperatures) they are computed as they stand: q could be off by
+// many octaves, and a row's weights or their sum would overflow or vanish.
+constexpr float kPlainLimit = 4096.f;
+__device__ __forceinline__ bool plain(float q) { return fabsf(q) < kPlainLimit; }
+// 2^((l - m) c) of two logits: as l c - q (PLAIN), or as it stands.
 template <bool PLAIN>
 __device__ __forceinline__ unsigned long long exp2_pair(float l0, float l1, float c, float m, float q) {
     float x, y;
@@ -293,9 +297,9 @@ struct Distill {
     template <class G>
     __device__ __forceinline__ void gradient(float g, float m, float S, const float (&own)[SLOTS], int turn, G get,
                                              const uint4 (*ahead)[kBatch] = nullptr) {
-        // exponents as l c - q, q the rounded m c, whose rounding goes into the factor
+        // where exponents are l c - q, q's rounding goes into the factor
         const float q = m * c, A = g * sum_p / S;
-        if (fabsf(q) < kHuge)
+        if (plain(q))
             dense<true>(m, q, A * (1.f + 0.6931471805599453f * fmaf(-m, c, q)), get, ahead);
         else
             dense<false>(m, q, A, get, ahead);
@@ -321,8 +325,8 @@ struct Distill {
     }
 };
 
-// A thread's running maximum m and sum of 2^((l - m) c): as 2^(l c - q), q the rounded m c, one fused
-// operation a pair; at the end the rounding of q goes into the sum.
+// A thread's running maximum m and sum of 2^((l - m) c), or, where plain(q), of 2^(l c - q); at the end
+// the rounding of q goes into the sum.
 template <int EB>
 struct Running {
     using P = Part<EB>;
@@ -334,13 +338,15 @@ struct Running {
         const float top = P::vectors_max(v);  // NaN if there is one
         if (!(top <= m) && m == m) {      // (a NaN stays)
             const float to = top * c;
-            const float f = m > -INFINITY ? ptx::ex2(fabsf(to) < kHuge ? q - to : (m - top) * c) : 0.f;
+            // from the old maximum's form to the new one's
+            const float x = plain(q) ? (plain(to) ? q - to : fmaf(-top, c, q)) : plain(to) ? fmaf(m, c, -to) : (m - top) * c;
+            const float f = m > -INFINITY ? ptx::ex2(x) : 0.f;
             s = mul2(s, pair(f, f));
             m = top;
             q = to;
         }
         if (m == -INFINITY) return;  // masked so far
-        if (fabsf(q) < kHuge)
+        if (plain(q))
             weigh<true>(v, c);
         else
             weigh<false>(v, c);
@@ -393,7 +399,7 @@ struct Running {
     __device__ __forceinline__ float sum(float c) const {
         float x, y;
         split(s, x, y);
-        return (x + y) * (fabsf(q) < kHuge ? 1.f + 0.6931471805599453f * fmaf(-m, c, q) : 1.f);
+        return (x + y) * (plain(q) ? 1.f + 0.6931471805599453f * fmaf(-m, c, q) : 1.f);
     }
 };
 
