@@ -802,8 +802,7 @@ __device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) 
         } else if (q.k > 0) {  // too few groups for it: few tokens that are not masked
             all = !r.threshold(sc.m, q.k, &low);
         } else if (!share) {   // from a little below what min-p asks for
-            const float x = log2f(q.min_p) / sc.ch;
-            low = sc.m + x - (fabsf(x) + fabsf(sc.m)) * 0x1p-18f;
+            low = logit_under(sc.m, -log2f(q.min_p) / sc.ch);
             all = false;
         }
     }

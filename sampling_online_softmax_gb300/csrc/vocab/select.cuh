@@ -386,7 +386,8 @@ struct Row {
 
     static __device__ __forceinline__ uint4 nothing() { return P::nothing(); }
     // f(vectors, number) for the vectors of the groups whose maximum reaches `low`, spread over all
-    // threads, kGather at a time, whole warps together; number(j) is vector j's (-1: none).
+    // threads, kGather at a time, whole warps together; number(j) is vector j's (-1: none, a vector of -inf).
+    // `low` is finite.
     static constexpr int kGather = 8;
     template <class F>
     __device__ __forceinline__ void gather(float low, F f) {
@@ -421,7 +422,7 @@ struct Row {
         }
         __syncwarp();
     }
-    // One bit for each logit of a vector that is at least `low`.
+    // One bit for each logit of a vector that is at least `low` (finite: elements outside the row are -inf).
     static __device__ __forceinline__ uint32_t reaching(const uint4 &v, float low) {
         if (!(vector_max(v) >= low)) return 0;
         float l[kPer];

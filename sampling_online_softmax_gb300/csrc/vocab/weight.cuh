@@ -15,6 +15,8 @@
 // in fp32 (below 2^-18, so its rounding is below 2^-42; y^4/24 is below 2^-38).
 #pragma once
 
+#include <cfloat>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -140,6 +142,10 @@ SPEC_HD unsigned long long fixed_weight(float logit, const Scale &s, const float
     const unsigned long long v = (static_cast<unsigned long long>(hi) << 22) + static_cast<long long>(lo);
     return some ? v : 0ull;
 }
+
+// A finite logit below every one that lies at most `depth` under the largest, m: below the difference's own
+// error.  (Not -inf, which masked tokens and the padding of a row's vectors reach.)
+SPEC_HD float logit_under(float m, float depth) { return fmaxf(m - depth - (fabsf(depth) + fabsf(m)) * 0x1p-18f, -FLT_MAX); }
 
 // floor(W * f) for W < 2^63 and f in [0, 1), and whether f * W is no whole number, exactly.
 SPEC_HD unsigned long long scaled_floor(unsigned long long W, float f, bool *rest) {

@@ -428,3 +428,22 @@ def test_the_cut_among_logits_next_to_zero(B):
     check_sample(x[:n].contiguous(), u[:n].contiguous(), params(n, 0, T=(1.0,), p=(0.6,)))
     assert r["tokens"][:n].tolist() == sv.spec_sample_filtered(
         x[:n].contiguous(), u[:n].contiguous(), torch.ones(n, device=DEV), top_p=torch.full((n,), 0.6, device=DEV))["tokens"].tolist()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [129, 1000, 5003])
+def test_min_p_over_rows_of_the_lowest_value(V, dtype):
+    """Rows masked by the type's lowest value, whole, mixed with -inf, and near it; min-p alone and beside the others."""
+    low = torch.finfo(dtype).min
+    x = torch.full((6, V), low, dtype=dtype, device=DEV)
+    x[1, ::2] = float("-inf")
+    x[2] = float("-inf")
+    x[2, V - 1] = low
+    x[3, V // 2] = low * (1 - 2.0 ** -7)
+    x[4, 3] = 1.0
+    x[5, : V // 3] = -1.0
+    u = torch.tensor([0.11, 0.37, 0.52, 0.71, 0.93, 0.23], device=DEV)
+    for q in (dict(mp=(0.05,)), dict(mp=(1.0,)), dict(mp=(1e-30,)), dict(mp=(0.05,), T=(1e6,)), dict(mp=(0.05,), T=(1e-6,)),
+              dict(mp=(0.05,), p=(0.7,)), dict(mp=(0.05,), k=(40,)), dict(mp=(0.05,), k=(3,), p=(0.5,))):
+        check_sample(x, u, params(6, 0, **q))
+    check_sample(x, torch.zeros_like(u), params(6, 0, mp=(0.05,)))

@@ -62,3 +62,40 @@ def test_weights_against_long_doubles(tmp_path):
     subprocess.run(["g++", "-O2", "-ffp-contract=off", "-x", "c++", "-I", CSRC, "-o", str(tmp_path / "w"), str(src)], check=True, capture_output=True)
     worst = float(subprocess.run([str(tmp_path / "w")], capture_output=True, text=True, check=True).stdout)
     assert worst <= 8.0, "a weight is %.3f * 2^-40 off" % worst
+
+
+UNDER = r"""
+#include <cmath>
+#include <cstdio>
+#include <random>
+struct float2 { float x, y; };
+#include "weight.cuh"
+using namespace spec::vocab;
+int main() {
+    std::mt19937 gen(2);
+    std::uniform_real_distribution<float> draw(-1, 1);
+    int wrong = 0;
+    const float sizes[] = {0.f, 1e-38f, 1.f, 30.f, 1e9f, 3e37f, 3.3895314e38f, 3.4028e38f, FLT_MAX}, depths[] = {0.f, 1e-6f, 4.f, 150.f, 1e8f, 1e38f, INFINITY};
+    for (float m : sizes)
+        for (float d : depths)
+            for (int i = 0; i < 1000; ++i) {
+                const float top = i < 2 ? (i ? m : -m) : m * draw(gen), depth = i % 3 ? d : d * fabsf(draw(gen));
+                const float low = logit_under(top, depth);
+                // finite, and not above top - depth where that is a logit
+                if (!(low >= -FLT_MAX) || (double)low > fmax((double)top - (double)depth, -(double)FLT_MAX)) ++wrong;
+            }
+    printf("%d\n", wrong);
+    return 0;
+}
+"""
+
+
+def test_the_bound_under_the_largest_logit_is_finite(tmp_path):
+    """Also where the largest is the type's lowest value, as in a row masked by it: -inf would be reached by masked tokens
+    and by the padding of a row's vectors, which lie outside the tensor."""
+    if shutil.which("g++") is None:
+        pytest.skip("no g++")
+    src = tmp_path / "u.cpp"
+    src.write_text(UNDER)
+    subprocess.run(["g++", "-O2", "-ffp-contract=off", "-x", "c++", "-I", CSRC, "-o", str(tmp_path / "u"), str(src)], check=True, capture_output=True)
+    assert int(subprocess.run([str(tmp_path / "u")], capture_output=True, text=True, check=True).stdout) == 0
