@@ -18,7 +18,8 @@ enum Verdict : uint32_t { kDone = 0, kWeigh = 1, kMore = 2 };
 // One row's request, after the checks.
 struct Request {
     float p, min_p, u;
-    unsigned long long least;  // the weight that min-p asks for (0: none)
+    unsigned long long least;  // the weight that min-p asks for (0: none),
+    uint32_t min_key;          // or, where by_weight() is false, the least key that has it
     int k;                     // 0: no limit
 };
 
@@ -30,16 +31,13 @@ __device__ __forceinline__ unsigned long long share_of(unsigned long long W, flo
     return max(t + (rest ? 1ull : 0ull), 1ull);
 }
 
-// Whether weights in units tell exactly which tokens min-p keeps: its own weight is 2^24 units or more,
-// or the draw is of a weight's place in a sum (u > 0), where fewer units weigh nothing.
-__device__ __forceinline__ bool by_weight(const Request &q) { return q.u > 0.f || q.least >> 24; }
+// Whether whole units tell which tokens min-p keeps as well as weights are known: half of one is 2^-37 of
+// its weight or less.  (Smaller ones are asked about by key: rows of equal logits next to min-p would be
+// kept or not by a unit's rounding, all of them alike.)
+__device__ __forceinline__ bool by_weight(const Request &q) { return q.least >> 36; }
 // u = 0 draws the first kept token, whatever its weight: also one below half a unit, which the whole
-// numbers have as 0; a min-p of so few units is asked about by its logarithm.  A weight that is 0 in
-// 64 bits (below 2^-1074) is not drawn.
-__device__ __forceinline__ bool drawn_at_zero(float l, const Scale &sc, const Request &q) {
-    const float x = (l - sc.m) * sc.ch;
-    return x > -1074.f && (!q.least || by_weight(q) || x >= log2f(q.min_p));
-}
+// numbers have as 0.  A weight that is 0 in 64 bits (below 2^-1074) is not drawn.
+__device__ __forceinline__ bool drawn_at_zero(float l, const Scale &sc) { return (l - sc.m) * sc.ch > -1074.f; }
 
 // The leader's part of a row whose kept tokens are among the n entries of its list, which holds the
 // row's n largest logits: sorts them, cuts, draws.  W0, W1: bounds of the weight of all tokens that
@@ -77,12 +75,13 @@ __device__ __forceinline__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, c
     }
 
     if (q.p < 1.f || q.least) {
+        const bool weighed = by_weight(q);
         const unsigned long long total = sh->cum[nk - 1];
         const unsigned long long t0 = share_of(W0 ? W0 : total, q.p), t1 = share_of(W1 ? W1 : total, q.p);
         unsigned long long c = 0;  // entries below the two cuts of top-p, and entries that min-p keeps
         for (int i = i0; i < i1; ++i)
             c += static_cast<unsigned long long>(sh->cum[i] < t0) | static_cast<unsigned long long>(sh->cum[i] < t1) << 16 |
-                 static_cast<unsigned long long>(weight(i) >= q.least) << 32;
+                 static_cast<unsigned long long>(weighed ? weight(i) >= q.least : Row<EB>::key(value(i)) >= q.min_key) << 32;
         c = block_sum(c, sh->red, lane, warp);
         if (q.p < 1.f) {
             const int a = static_cast<int>(c & 0xffff) + 1, b = static_cast<int>((c >> 16) & 0xffff) + 1;
@@ -90,7 +89,7 @@ __device__ __forceinline__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, c
             if (a != b) return kWeigh;
             nk = a;
         }
-        if (by_weight(q)) nk = min(nk, static_cast<int>(c >> 32));
+        nk = min(nk, static_cast<int>(c >> 32));
     }
     if (nk == 1) {
         if (tid == 0) *token = static_cast<int32_t>(index(0));
@@ -99,7 +98,7 @@ __device__ __forceinline__ Verdict draw_from_list(Row<EB> &r, const Scale &sc, c
     if (q.u == 0.f) {
         uint32_t x = kAll;
         for (int i = tid; i < nk; i += kThreads)
-            if (drawn_at_zero(value(i), sc, q)) x = min(x, index(i));
+            if (drawn_at_zero(value(i), sc)) x = min(x, index(i));
         x = __reduce_min_sync(kAll, x);
         __syncthreads();
         if (lane == 0) sh->red[warp] = x;
@@ -599,13 +598,15 @@ __device__ __forceinline__ bool cut_by_keys(Row<2> &r, const Scale &sc, float p,
 }
 __device__ __forceinline__ bool cut_by_keys(Row<4> &, const Scale &, float, Cut *) { return false; }
 
-// The key of the least logit whose weight is at least `least`; a warp's lanes try 32 keys at a time.
+// The key of the least logit whose weight is at least min_p; a warp's lanes try 32 keys at a time.
+// (Out of line and without the Row: rarely called, and the rest's registers and code are as without it.)
 template <int EB>
-__device__ __forceinline__ uint32_t least_key(const Row<EB> &r, const Scale &sc, unsigned long long least) {
+__device__ __noinline__ uint32_t least_key(const Scale sc, const float2 *pow2, float min_p) {
     uint32_t lo = Row<EB>::kLowest, hi = Row<EB>::key(sc.m);  // hi's weight suffices; the answer is in [lo, hi]
+    const uint32_t lane = threadIdx.x & 31;
     while (lo < hi) {
-        const uint32_t step = (hi - lo) / 32 + 1, k = min(hi, lo + r.lane * step);
-        const uint32_t ok = __ballot_sync(kAll, fixed_weight(Row<EB>::value(k), sc, r.sh->pow2) >= least);
+        const uint32_t step = (hi - lo) / 32 + 1, k = min(hi, lo + lane * step);
+        const uint32_t ok = __ballot_sync(kAll, weight_reaches(Row<EB>::value(k), sc, min_p, pow2));
         if (!ok) {  // above the last key tried
             lo = min(hi, lo + 31 * step + 1);
             continue;
@@ -629,8 +630,8 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
         for (int again = 0; again < 2; ++again)
             if (cut_row<false>(r, sc, 0, q.p, again, &cut)) break;
     }
-    if (q.least && by_weight(q)) {
-        const uint32_t x = least_key(r, sc, q.least);
+    if (q.least) {
+        const uint32_t x = by_weight(q) ? least_key<EB>(sc, sh->pow2, q.min_p) : q.min_key;
         if (x > cut.key) cut = {x, INT_MAX};
     }
     const Weigh<EB> weigh(sc, sh->pow2, cut);
@@ -641,7 +642,7 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
                 Row<EB>::unpack(v, l);
                 unsigned long long c = 0;
 #pragma unroll
-                for (int e = 0; e < kPer; ++e) c += weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc, q);
+                for (int e = 0; e < kPer; ++e) c += weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc);
                 return c;
             },
             []() { return 0ull; }, [](unsigned long long) { return 1ull; },
@@ -651,7 +652,7 @@ __device__ __forceinline__ void draw_from_row(Row<EB> &r, const Scale &sc, const
                 int x = -1;
 #pragma unroll
                 for (int e = kPer - 1; e >= 0; --e)
-                    if (weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc, q)) x = r.index(i, e);
+                    if (weigh.kept(l[e], r.index(i, e)) && drawn_at_zero(l[e], sc)) x = r.index(i, e);
                 *token = x;
             });
         return;
@@ -725,6 +726,7 @@ __device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) 
     q.p = a.top_p ? a.top_p[b] : 1.f;
     q.min_p = a.min_p ? a.min_p[b] : 0.f;
     q.least = 0;
+    q.min_key = 0;
     const bool greedy = T == 0.f;
     const bool bad = !(greedy || (T >= kMinTemperature && T <= kMaxTemperature)) ||
                      !(greedy || (q.p >= 0.f && q.p <= 1.f && q.min_p >= 0.f && q.min_p <= 1.f && q.u >= 0.f && q.u < 1.f));
@@ -776,7 +778,10 @@ __device__ __forceinline__ void sample_row(const RowArgs &a, Row<EB> &r, int b) 
         }
         return;
     }
-    if (q.min_p > 0.f) q.least = share_of(1ull << sc.U, q.min_p);
+    if (q.min_p > 0.f) {
+        q.least = share_of(1ull << sc.U, q.min_p);
+        if (!by_weight(q)) q.min_key = least_key<EB>(sc, sh->pow2, q.min_p);
+    }
 
     // The short way: the list holds the logits from `low` on; all: that is every token.
     float low = -FLT_MAX;

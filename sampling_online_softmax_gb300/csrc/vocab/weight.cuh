@@ -105,9 +105,10 @@ struct Scale {
     int U;  // units of 2^-U; U + bits(V) <= 62, so that a row's sum stays below 2^63, and U <= 48 (fixed_weight)
 };
 
-// Branch-free, so that a vector's logits go through it side by side.
-SPEC_HD unsigned long long fixed_weight(float logit, const Scale &s, const float2 *pow2) {
-    const bool some = (logit - s.m) * s.ch > -60.f;  // else below half a unit for every U; also logit = -inf
+// Branch-free, so that a vector's logits go through it side by side.  Weights below 2^least are 0 (-60: below
+// half a unit for every U of a row); least + U > -100, so that the scale is a normal number.
+SPEC_HD unsigned long long fixed_weight(float logit, const Scale &s, const float2 *pow2, float least = -60.f) {
+    const bool some = (logit - s.m) * s.ch > least;  // not: logit = -inf
     const float l = some ? logit : s.m;
     const float dh = l - s.m;
     const float ph = dh * s.ch;
@@ -141,6 +142,19 @@ SPEC_HD unsigned long long fixed_weight(float logit, const Scale &s, const float
     const int lo = static_cast<int>(rintf(rest * 0x1p22f));
     const unsigned long long v = (static_cast<unsigned long long>(hi) << 22) + static_cast<long long>(lo);
     return some ? v : 0ull;
+}
+
+// Whether a logit's weight is at least f, in (0, 1]: in units of 2^-40 of f's own size, so right to 2^-37 of f
+// however small it is.
+SPEC_HD bool weight_reaches(float l, const Scale &s, float f, const float2 *pow2) {
+    int k = 0;
+    const float fr = frexpf(f, &k);  // f = fr 2^k, fr in [0.5, 1)
+    const float x = (l - s.m) * s.ch, size = static_cast<float>(k);
+    if (!(x > size - 2.f)) return false;
+    if (x > size + 1.f) return true;
+    Scale near = s;
+    near.U = 40 - k;
+    return fixed_weight(l, near, pow2, size - 3.f) >= static_cast<unsigned long long>(fr * 16777216.f) << 16;
 }
 
 // A finite logit below every one that lies at most `depth` under the largest, m: below the difference's own

@@ -1,0 +1,62 @@
+"""Filtered sampling at borders that whole units of weight are too coarse for."""
+import numpy as np
+import pytest
+import torch
+
+import sampling_online_softmax_gb300 as sv
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.mark.parametrize("V,k,u", [(1000, 0, 1 - 2.0 ** -24), (262144, 0, 0.99999), (262144, 1000, 1 - 2.0 ** -24), (262144, 5000, 1 - 2.0 ** -22)])
+def test_min_p_next_to_a_long_tail(V, k, u):
+    """One token ahead of a tail of equal ones whose weight, 10^-10 of its own, lies 2^-13 of itself above
+    or below min-p: kept, the tail has the mass that u asks for; else the draw is the first token's."""
+    B = 64
+    g = torch.Generator().manual_seed(V + k)
+    low = -(22.5 + torch.rand((B,), generator=g))
+    w = np.exp(low.numpy().astype(np.float64))
+    kept = np.arange(B) % 2 == 0
+    mp = (w * np.where(kept, 1 - 2.0 ** -13, 1 + 2.0 ** -13)).astype(np.float32)
+    assert ((mp <= w) == kept).all()
+    x = low.unsqueeze(1).repeat(1, V)
+    x[:, 7] = 0.0
+    tail = (k or V) - 1
+    # u W > 1 (token 7, which 7 of the tail's come before) where the tail is kept; the token is then well inside the tail
+    t = float(np.float32(u)) * (1 + tail * w)
+    assert ((t - 1) / w > 8).all()
+    c = np.floor((t - 1) / w).astype(np.int64)  # tail tokens before the drawn one
+    far = (t - 1) / w - c
+    x = x.to(DEV)
+    one = torch.ones(B, device=DEV)
+    top_k = torch.full((B,), k, dtype=torch.int32, device=DEV)
+    got = sv.spec_sample_filtered(x, one * u, one, top_k=top_k, min_p=torch.tensor(mp, device=DEV))["tokens"].tolist()
+    for b in range(B):
+        if not kept[b]:
+            assert got[b] == 7, (b, got[b])
+        else:  # whole units of the tail's weights are off by 0.8 each: a place in the tail by that share of its length
+            units = w[b] * 2.0 ** min(48, 62 - (V - 1).bit_length())
+            assert abs(got[b] - (c[b] + 1 + far[b])) <= 2 + tail * 0.8 / units, (b, got[b], c[b])
+
+
+@pytest.mark.parametrize("V", [300, 6000, 60001])
+@pytest.mark.parametrize("top", [30.0, 60.0, 85.0])
+def test_min_p_far_below_the_largest(V, top):
+    """The same at u = 0, down to weights of 10^-37: the first token is drawn where its weight reaches min-p."""
+    B = 64
+    g = torch.Generator().manual_seed(V)
+    low = -(top + torch.rand((B,), generator=g))
+    w = np.exp(low.numpy().astype(np.float64))
+    mp = w.astype(np.float32)  # the nearest fp32, above the weight or below it
+    keep = mp <= w
+    assert (np.abs(mp / w - 1) > 2.0 ** -35).all() and keep.sum() > 8 and (~keep).sum() > 8
+    x = torch.full((B, V), -200.0)
+    x[:, 0] = low
+    x[:, V // 2] = 0.0
+    x = x.to(DEV)
+    one = torch.ones(B, device=DEV)
+    for kw in (dict(), dict(top_k=torch.full((B,), 5, dtype=torch.int32, device=DEV)), dict(top_k=torch.full((B,), 2000, dtype=torch.int32, device=DEV))):
+        r = sv.spec_sample_filtered(x, one * 0.0, one, min_p=torch.tensor(mp, device=DEV), **kw)
+        assert int(r["status"][0]) == 0
+        assert r["tokens"].tolist() == [0 if a else V // 2 for a in keep]

@@ -99,3 +99,55 @@ def test_the_bound_under_the_largest_logit_is_finite(tmp_path):
     src.write_text(UNDER)
     subprocess.run(["g++", "-O2", "-ffp-contract=off", "-x", "c++", "-I", CSRC, "-o", str(tmp_path / "u"), str(src)], check=True, capture_output=True)
     assert int(subprocess.run([str(tmp_path / "u")], capture_output=True, text=True, check=True).stdout) == 0
+
+
+REACHES = r"""
+#include <cmath>
+#include <cstdio>
+#include <random>
+struct float2 { float x, y; };
+#include "weight.cuh"
+using namespace spec::vocab;
+static const float2 table[kPow2Steps] = SPEC_POW2_TABLE;
+int main() {
+    std::mt19937 gen(3);
+    std::uniform_real_distribution<float> draw(0, 1);
+    int wrong = 0, near = 0;
+    for (int i = 0; i < 1000000; ++i) {
+        Scale s;
+        s.m = (draw(gen) - 0.5f) * (i % 3 ? 60.f : 1.f);
+        const float T = i % 5 ? 0.3f + draw(gen) : exp2f(i % 30 - 15);
+        constexpr float kH = 0x1.715476p+0f, kL = 0x1.4ae0c0p-26f;
+        s.ch = kH / T;
+        s.cl = (fmaf(-s.ch, T, kH) + kL) / T;
+        s.U = 43;
+        const float l = s.m - draw(gen) * 103.f * T;
+        const long double w = expl(((long double)l - (long double)s.m) / (long double)T);
+        float f = (float)w;  // within 2^-24 of the weight, or (below 2^-126) 2^-150; and some further off
+        if (i % 7 == 0) f *= 1.f + (draw(gen) - 0.5f) * 0x1p-10f;
+        if (i % 11 == 0) f *= 8.f * draw(gen);
+        if (i % 13 == 0) f = draw(gen);
+        if (!(f > 0.f && f <= 1.f)) continue;
+        const long double off = fabsl((long double)f / w - 1);
+        if (off <= exp2l(-37)) continue;
+        near += off < exp2l(-24);
+        wrong += weight_reaches(l, s, f, table) != (w >= (long double)f);
+    }
+    Scale s = {3.f, 1.f, 0.f, 48};
+    if (!weight_reaches(3.f, s, 1.f, table) || weight_reaches(-INFINITY, s, 0x1p-149f, table) || !weight_reaches(-146.f, s, 0x1p-149f, table)) ++wrong;
+    if (weight_reaches(-146.00002f, s, 0x1p-149f, table) || weight_reaches(-3e38f, s, 0x1p-149f, table)) ++wrong;
+    printf("%d %d\n", wrong, near);
+    return 0;
+}
+"""
+
+
+def test_which_weights_reach_a_bound_of_any_size(tmp_path):
+    """Against 80-bit exponentials, for every bound further than 2^-37 from the weight, down to fp32's smallest."""
+    if shutil.which("g++") is None:
+        pytest.skip("no g++")
+    src = tmp_path / "r.cpp"
+    src.write_text(REACHES)
+    subprocess.run(["g++", "-O2", "-ffp-contract=off", "-x", "c++", "-I", CSRC, "-o", str(tmp_path / "r"), str(src)], check=True, capture_output=True)
+    wrong, near = map(int, subprocess.run([str(tmp_path / "r")], capture_output=True, text=True, check=True).stdout.split())
+    assert wrong == 0 and near > 100000
