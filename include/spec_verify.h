@@ -409,8 +409,9 @@ SPEC_API spec_status spec_distill(const void *student_logits, spec_dtype dtype, 
  * The gradient alone, for losses whose upstream gradients are known only later:
  * grad[n, v] = grad_loss[n] * d loss[n] / d s_v, from spec_distill's stats of the
  * same logits, teacher, temperature and weights.  Arguments as there; stats and
- * grad_loss [N] fp32 are inputs.  A row with row_weight * grad_loss = 0 is not
- * read and its gradient is 0.  grad may be student_logits itself.
+ * grad_loss [N] fp32 are inputs.  A row whose row_weight or grad_loss is 0 (or
+ * their product) is not read and its gradient is 0, whatever the other is.
+ * grad may be student_logits itself.
  */
 SPEC_API spec_status spec_distill_backward(const void *student_logits, spec_dtype dtype, int N, int V, const int32_t *top_ids,
                                            const float *top_logits, int K, const float *top_lse, float temperature,

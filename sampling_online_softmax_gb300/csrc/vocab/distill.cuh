@@ -633,8 +633,8 @@ __global__ void __launch_bounds__(kDThreads, 4) distill_backward_kernel(const Di
     uint32_t *bits = reinterpret_cast<uint32_t *>(dyn + sizeof(DistillShared<SLOTS>) / 16);
     const int b = blockIdx.x / a.cluster;
     Distill<EB, SLOTS> d(a, sh, b, blockIdx.x % a.cluster);
-    const float up = (a.weight ? __ldg(a.weight + b) : 1.f) * __ldg(a.grad_loss + b);
-    if (up == 0.f) {
+    const float w = a.weight ? __ldg(a.weight + b) : 1.f, grad_loss = __ldg(a.grad_loss + b), up = w * grad_loss;
+    if (w == 0.f || grad_loss == 0.f || up == 0.f) {  // (0 times an infinite factor is not 0)
         d.fill(0.f);
         return;
     }

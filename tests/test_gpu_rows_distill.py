@@ -326,3 +326,26 @@ def test_gradient_of_large_logits(split):
     grad = grad.double().scatter_(1, ids.long(), 0.0)
     off = ((grad - q).abs() / q.clamp(min=1e-30)).max().item()
     assert off < 32 * 2.0 ** -24, off / 2.0 ** -24
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_an_ignored_row_whatever_its_upstream_gradient(dtype):
+    """Padding rows (weight 0) under a loss scale that overflowed; and a zero upstream gradient of any weight."""
+    N, V, K = 9, 3001, 12
+    x, ids, t, lse = inputs(N, V, K, dtype, 31, tail=True)
+    x[1], t[2], lse[3] = float("nan"), float("nan"), float("inf")
+    w = torch.ones(N, device=DEV)
+    w[[1, 2, 3, 4]] = 0.0
+    w[4] = -0.0
+    up = torch.ones(N, device=DEV)
+    up[1], up[2], up[3], up[4] = float("inf"), float("nan"), float("-inf"), float("nan")
+    up[6], w[7], up[7] = 0.0, float("inf"), 0.0
+    finite = torch.where(torch.isfinite(w), w, 1.0)
+    r = sv.spec_distill(x, ids, t, top_lse=lse, row_weight=finite)
+    assert int(r["status"][0]) == 0
+    back = sv.spec_distill_backward(x, ids, t, r["stats"], up, top_lse=lse, row_weight=w)
+    assert int(back["status"][0]) == 0
+    assert not back["grad"][[1, 2, 3, 4, 6, 7]].any()
+    for b in (0, 5, 8):
+        sub = slice(b, b + 1)
+        check(x[sub], ids[sub], t[sub], lse[sub], 1.0, None, None, back["grad"][sub], up[sub])
