@@ -298,7 +298,7 @@ struct Distill {
     __device__ __forceinline__ void gradient(float g, float m, float S, const float (&own)[SLOTS], int turn, G get,
                                              const uint4 (*ahead)[kBatch] = nullptr) {
         // where exponents are l c - q, q's rounding goes into the factor
-        const float q = m * c, A = g * sum_p / S;
+        const float q = __fmul_rn(m, c), A = g * sum_p / S;
         if (plain(q))
             dense<true>(m, q, A * (1.f + 0.6931471805599453f * fmaf(-m, c, q)), get, ahead);
         else
@@ -337,7 +337,7 @@ struct Running {
     __device__ __forceinline__ void add(const uint4 (&v)[N], float c) {
         const float top = P::vectors_max(v);  // NaN if there is one
         if (!(top <= m) && m == m) {      // (a NaN stays)
-            const float to = top * c;
+            const float to = __fmul_rn(top, c);  // (rounded, as weigh() subtracts it: not to be fused into q - to)
             // from the old maximum's form to the new one's
             const float x = plain(q) ? (plain(to) ? q - to : fmaf(-top, c, q)) : plain(to) ? fmaf(m, c, -to) : (m - top) * c;
             const float f = m > -INFINITY ? ptx::ex2(x) : 0.f;

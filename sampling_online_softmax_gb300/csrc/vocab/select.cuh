@@ -208,7 +208,8 @@ struct Row {
             }
             if (SUM) {
                 if (m > top) {
-                    const float to = m * c, f = top > -INFINITY ? ptx::ex2(q - to) : 0.f, d = top > -INFINITY ? q - to - 4.f : 0.f;
+                    // (the rounded product, as it is subtracted below: not to be fused into q - to)
+                    const float to = __fmul_rn(m, c), f = top > -INFINITY ? ptx::ex2(q - to) : 0.f, d = top > -INFINITY ? q - to - 4.f : 0.f;
                     const unsigned long long none = pair(0.f, 0.f), f2 = pair(f, f);
                     if (SUM == kBounded) b = fma2(fma2(s, pair(d, d), b), f2, none);
                     s = fma2(s, f2, none);

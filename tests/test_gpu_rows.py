@@ -447,3 +447,17 @@ def test_min_p_over_rows_of_the_lowest_value(V, dtype):
               dict(mp=(0.05,), p=(0.7,)), dict(mp=(0.05,), k=(40,)), dict(mp=(0.05,), k=(3,), p=(0.5,))):
         check_sample(x, u, params(6, 0, **q))
     check_sample(x, torch.zeros_like(u), params(6, 0, mp=(0.05,)))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size", [200.0, 1000.0, 3000.0, -3000.0])
+def test_top_p_of_rows_far_from_zero(size, dtype):
+    """Logits over T around 10^4, where the maximum times log2(e) / T rounds by 2^-10: the bounds of the
+    row's weight that the short list's cut goes by hold all the same."""
+    B, V, T = 24, 20011, 0.1
+    g = torch.Generator().manual_seed(14)
+    x = (size + torch.randn((B, V), generator=g) * (0.35 if dtype == torch.float32 else 8.0)).to(dtype).to(DEV)
+    T = T if dtype == torch.float32 else 2.3
+    u = torch.rand(B, generator=g).to(DEV)
+    for p in (0.2, 0.5, 0.9):
+        check_sample(x, u, params(B, 0, T=(T,), p=(p,)))

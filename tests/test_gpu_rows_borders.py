@@ -60,3 +60,21 @@ def test_min_p_far_below_the_largest(V, top):
         r = sv.spec_sample_filtered(x, one * 0.0, one, min_p=torch.tensor(mp, device=DEV), **kw)
         assert int(r["status"][0]) == 0
         assert r["tokens"].tolist() == [0 if a else V // 2 for a in keep]
+
+
+@pytest.mark.parametrize("n,p", [(64, 0.5), (64, 0.25), (40, 0.625), (200, 0.5), (1000, 0.75), (3000, 0.5)])
+@pytest.mark.parametrize("T", [1e-6, 1e-4, 0.01])
+def test_top_p_on_the_border_between_equal_logits(T, n, p):
+    """n equal tokens, of which top-p keeps n p exactly, at maxima over T of up to 10^9: the last kept one is drawn
+    only if the bounds of the row's weight hold to their last place."""
+    B, V = 96, 9001
+    g = torch.Generator().manual_seed(n)
+    m = torch.logspace(-2, 3, B)
+    x = -torch.rand((B, V), generator=g) * 1000 - 100 - 2 * m.unsqueeze(1)
+    at = torch.stack([torch.randperm(V, generator=g)[:n].sort().values for _ in range(B)])
+    x.scatter_(1, at, m.unsqueeze(1).expand(B, n))
+    x = x.to(DEV)
+    one = torch.ones(B, device=DEV)
+    r = sv.spec_sample_filtered(x, one * (1 - 2.0 ** -24), one * T, top_p=one * p)
+    assert int(r["status"][0]) == 0
+    assert r["tokens"].tolist() == at[:, int(n * p) - 1].tolist()
