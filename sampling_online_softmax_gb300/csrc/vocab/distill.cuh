@@ -132,11 +132,14 @@ struct Distill {
             top = 0.f;  // log p = t / T - lse
             const float z = __ldg(a.lse + b);
             if (!(z < INFINITY)) wrong = true;
+            const float rest = fmaf(-invT, a.T, 1.f) * invT;  // 1 / T - invT
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
                 const bool any = t[j] > -INFINITY;
                 if (any && z == -INFINITY) wrong = true;  // (a masked row's teacher has no entries)
-                t[j] = any ? t[j] * invT - z : -INFINITY;
+                // t / T as a pair: it may be far larger than its difference from lse
+                const float h = __fmul_rn(t[j], invT), l = fabsf(h) < 1e30f ? fmaf(t[j], rest, fmaf(t[j], invT, -h)) : 0.f;
+                t[j] = any ? (h - z) + l : -INFINITY;
                 s += any ? expf(t[j]) : 0.f;
             }
         } else if (__any_sync(kAllLanes, top > -INFINITY)) {

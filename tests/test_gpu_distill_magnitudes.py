@@ -151,3 +151,17 @@ def test_running_maxima_across_sizes():
     x = torch.stack(rows).to(DEV)
     ids, t = teacher(x, 9, 1.0, 7)
     check(x, ids, t)
+
+
+@pytest.mark.parametrize("T", [1e-6, 1e-4, 1e-2, 0.3, 1e6])
+def test_a_log_normaliser_of_large_logits(T):
+    """p = exp(t / T - lse) where t / T is large and the difference a few units."""
+    V, K = 5003, 40
+    g = torch.Generator().manual_seed(12)
+    step = max(float(np.float32(T)), 2.0 ** -19)
+    x = (19.7 - step * torch.randint(0, 7, (6, V), generator=g)).to(DEV)
+    ids, t = teacher(x, K, T, 13)
+    t[:, 7] = torch.finfo(torch.float32).min  # (over T, nothing or -inf)
+    whole = torch.logsumexp(t.double() / float(np.float32(T)), 1)
+    lse = (whole + 0.3).float()
+    check(x, ids, t, lse=lse, T=T)
