@@ -599,6 +599,12 @@ def spec_top_logits(logits, k, *, temperature=1.0, lse=False, status=None, out=N
     return out
 
 
+def _overwritten(grad):
+    """A gradient written into the caller's tensor, the logits' own perhaps: autograd, which sees only the
+    address change hands, refuses a graph that saved what was there."""
+    torch.autograd.graph.increment_version(grad)
+
+
 def _distill_inputs(student, top_ids, top_logits, top_lse, row_weight, temperature):
     """Checks the inputs of a distillation; returns (N, V, device, its index, the call's first arguments)."""
     N, V, dev, i, code = _logits_2d(student, "student")
@@ -619,7 +625,8 @@ def spec_distill(student, top_ids, top_logits, temperature=1.0, *, top_lse=None,
     int32, top_logits [N, K] float32, and with top_lse [N] float32 its log-normaliser; as
     spec_top_logits returns them): returns dict(loss [N], stats [N, 2], status), and with grad=True
     also grad [N, V], the gradient of the summed losses in student's dtype (out["grad"] may be
-    student itself).  row_weight [N] scales each row; a row of weight 0 is not read.
+    student itself: autograd then refuses a graph that saved the logits).  row_weight [N] scales
+    each row; a row of weight 0 is not read.
 
     No autograd graph is recorded: pass the gradient on with student.backward(r["grad"]), or keep
     stats for spec_distill_backward."""
@@ -628,9 +635,12 @@ def spec_distill(student, top_ids, top_logits, temperature=1.0, *, top_lse=None,
     shapes = {"loss": ((N,), torch.float32), "stats": ((N, 2), torch.float32)}
     if grad:
         shapes["grad"] = ((N, V), student.dtype)
+    given = grad and out is not None
     out, at, st = _results(out, shapes, status, dev, i, stream)
     _launch(lib.spec_distill, (*args, at[0], at[1], at[2] if grad else None, st),
             (student, top_ids, top_logits, top_lse, row_weight, *out.values()), dev, stream)
+    if given:
+        _overwritten(out["grad"])
     return out
 
 
@@ -647,6 +657,8 @@ def spec_distill_backward(student, top_ids, top_logits, stats, grad_loss, temper
     r, (g,), st = _results(None if out is None else dict(grad=out), {"grad": ((N, V), student.dtype)}, status, dev, i, stream)
     _launch(lib.spec_distill_backward, (*args, *more, g, st),
             (student, top_ids, top_logits, top_lse, row_weight, stats, grad_loss, *r.values()), dev, stream)
+    if out is not None:
+        _overwritten(out)
     return r
 
 

@@ -202,3 +202,23 @@ def test_the_distillation_reference_on_a_worked_row():
             h[v] = 1e-6
             d = (ref.distill(x + h, ids, t, lse, 0.5, 2.0)[0] - ref.distill(x - h, ids, t, lse, 0.5, 2.0)[0]) / 2e-6
             assert abs(d - g[v]) < 1e-7
+
+
+def test_a_gradient_over_saved_logits_is_refused_by_autograd(fake):
+    """exp saves its result: a gradient written over it, by either call, makes the graph's backward an error, not a
+    wrong gradient."""
+    N, K = 4, 6
+    ids, t, n = torch.zeros((N, K), dtype=i32), torch.zeros((N, K)), torch.zeros(N)
+    for call in (lambda y: sv.spec_distill(y, ids, t, grad=True, out=dict(loss=n.clone(), stats=torch.zeros((N, 2)), grad=y)),
+                 lambda y: sv.spec_distill_backward(y, ids, t, torch.zeros((N, 2)), n, out=y)):
+        leaf = torch.zeros((N, V), requires_grad=True)
+        y = leaf.exp()
+        call(y.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+        y = leaf.exp()
+        sv.spec_distill(y.detach(), ids, t, grad=True, out=dict(loss=n.clone(), stats=torch.zeros((N, 2)), grad=torch.zeros((N, V))))
+        sv.spec_distill_backward(y.detach(), ids, t, torch.zeros((N, 2)), n)
+        y.sum().backward()
+        with torch.inference_mode():
+            call(torch.zeros((N, V)))
