@@ -337,9 +337,13 @@ SPEC_API spec_status spec_mtp_plug(const int32_t *in_tokens, int B, int K, const
  *   dev_status  SPEC_DEV_BAD_PARAM: a row's parameter is out of range or NaN;
  *               SPEC_DEV_NONFINITE: a row holds NaN or +inf, or every token of
  *               it is masked.  Such a row's token is -1; the others are drawn.
- * Weights and their sums are whole numbers in units of at most 2^-42, right to
- * about 2^-38 relative, so the token is the definition's unless u
- * lies that near a border, and a call gives the same token every time.
+ * Weights are whole numbers in units of 2^-U, U = min(48, 62 - ceil(log2 V))
+ * (43 for the longest rows, 47 for 32000 logits), each right to 2^-37 of itself
+ * and 0.8 units; their sums are exact.  So with W the sum over the N tokens that
+ * a filter or the draw looks at, the token is the definition's unless u W, or
+ * top-p's share, lies within 2^-37 W + 0.8 N 2^-U of a border; a tail of many
+ * tokens below half a unit weighs nothing.  Which tokens min-p keeps is right to 2^-36 of
+ * min-p, whatever its size.  A call gives the same token every time.
  * Rows of at most SPEC_MAX_ROW_BYTES bytes (SPEC_ERR_UNSUPPORTED above).
  * No workspace; one launch.
  */

@@ -1,12 +1,15 @@
 // weight.cuh -- softmax weights as whole numbers: 2^((l - m) c) in units of
-// 2^-U, right to about 38 bits, in fp32 arithmetic alone.
+// 2^-U, each right to 2^-37 of itself and 0.8 units, in fp32 arithmetic alone.
 //
 // A draw picks the token at a border of a sum over the whole row, and top-p cuts
 // the order at another, so a weight's error moves the choice wherever tokens are
 // small: with 10^4 tokens in play, weights right to 2^-22 (one ex2.approx) would
 // pick another token than the definition for about one row in a hundred.  GB300's
 // FP64 pipe issues two FMAs a clock per SM, so an exp in double costs a row of
-// 150 k logits over a millisecond; pairs of floats take about 60 fp32 operations.  Sums of whole numbers do not depend on their order.
+// 150 k logits over a millisecond; pairs of floats take about 75 instructions.  Sums of whole numbers do not
+// depend on their order.  A row's sum stays below 2^63, so its length sets U: a sum over N tokens may be
+// off by 0.8 N units (2^-24 of the largest weight for 524288 tokens, 2^-32 for 32000), all in one
+// direction where the tokens are equal.
 //
 // x = (l - m) c is kept as a pair (TwoSum of l and -m, products with their FMA
 // remainders), x = n + t/128 + g with |g| <= 1/256, and

@@ -78,3 +78,33 @@ def test_top_p_on_the_border_between_equal_logits(T, n, p):
     r = sv.spec_sample_filtered(x, one * (1 - 2.0 ** -24), one * T, top_p=one * p)
     assert int(r["status"][0]) == 0
     assert r["tokens"].tolist() == at[:, int(n * p) - 1].tolist()
+
+
+@pytest.mark.parametrize("dtype,V", [(torch.bfloat16, 524288), (torch.float32, 262144), (torch.bfloat16, 131072), (torch.float32, 32000)])
+def test_a_long_tail_of_equal_tokens(V, dtype):
+    """One token far ahead of a tail of equal ones, down to a unit of weight each, whose rounding adds up:
+    the drawn token's interval holds u W to within 2^-37 W + 0.8 V units of 2^-U."""
+    bits = (V - 1).bit_length()
+    unit = 2.0 ** -min(48, 62 - bits)
+    low = [float(torch.tensor(l).to(dtype)) for l in (np.log(1.49 * unit), np.log(1.51 * unit), np.log(0.6 * unit), np.log(30.3 * unit), -21.0, -14.0, -9.3)]
+    x = torch.tensor(low).unsqueeze(1).repeat(1, V)
+    ahead = V // 3
+    x[:, ahead] = 0.0
+    x = x.to(dtype).to(DEV)
+    w = np.exp(np.array(low))
+    B = len(low)
+    one = torch.ones(B, device=DEV)
+    for u in (1 - 2.0 ** -24, 1 - 2.0 ** -23, 1 - 2.0 ** -18, 0.6, 2.0 ** -26, 2.0 ** -40):
+        for kw in (dict(), dict(top_p=one * (1 - 2.0 ** -24))):
+            r = sv.spec_sample_filtered(x, one * u, one, **kw)
+            assert int(r["status"][0]) == 0
+            for b, tok in enumerate(r["tokens"].tolist()):
+                n, off = V - 1, 2.0 ** -37 * (1 + (V - 1) * w[b]) + 0.8 * V * unit
+                if kw:  # the token ahead and the first n others, the fewest with that share; n may be a token and `off` off
+                    n = max(0, int(np.ceil(((1 - 2.0 ** -24) * (1 + n * w[b]) - 1) / w[b])))
+                    off = 2 * off + 2 * w[b]
+                W = 1 + n * w[b]
+                start = tok * w[b] if tok < ahead else min(n, ahead) * w[b] if tok == ahead else (tok - 1) * w[b] + 1
+                end = start + (1.0 if tok == ahead else w[b])
+                t = float(np.float32(u)) * W
+                assert start - off <= t <= end + off, (b, u, bool(kw), tok, start, t, end, off)
