@@ -343,7 +343,8 @@ SPEC_API spec_status spec_mtp_plug(const int32_t *in_tokens, int B, int K, const
  * a filter or the draw looks at, the token is the definition's unless u W, or
  * top-p's share, lies within 2^-37 W + 0.8 N 2^-U of a border; a tail of many
  * tokens below half a unit weighs nothing.  Which tokens min-p keeps is right to 2^-36 of
- * min-p, whatever its size.  A call gives the same token every time.
+ * min-p, whatever its size.  At u = 0 a weight counts that is not 0 in 64 bits
+ * (2^-1075 and above), units or not.  A call gives the same token every time.
  * Rows of at most SPEC_MAX_ROW_BYTES bytes (SPEC_ERR_UNSUPPORTED above).
  * No workspace; one launch.
  */

@@ -36,8 +36,8 @@ __device__ __forceinline__ unsigned long long share_of(unsigned long long W, flo
 // kept or not by a unit's rounding, all of them alike.)
 __device__ __forceinline__ bool by_weight(const Request &q) { return q.least >> 36; }
 // u = 0 draws the first kept token, whatever its weight: also one below half a unit, which the whole
-// numbers have as 0.  A weight that is 0 in 64 bits (below 2^-1074) is not drawn.
-__device__ __forceinline__ bool drawn_at_zero(float l, const Scale &sc) { return (l - sc.m) * sc.ch > -1074.f; }
+// numbers have as 0.  A weight that is 0 in 64 bits (below 2^-1075, which rounds to 0) is not drawn.
+__device__ __forceinline__ bool drawn_at_zero(float l, const Scale &sc) { return (l - sc.m) * sc.ch > -1075.f; }
 
 // The leader's part of a row whose kept tokens are among the n entries of its list, which holds the
 // row's n largest logits: sorts them, cuts, draws.  W0, W1: bounds of the weight of all tokens that

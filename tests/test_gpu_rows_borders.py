@@ -108,3 +108,17 @@ def test_a_long_tail_of_equal_tokens(V, dtype):
                 end = start + (1.0 if tok == ahead else w[b])
                 t = float(np.float32(u)) * W
                 assert start - off <= t <= end + off, (b, u, bool(kw), tok, start, t, end, off)
+
+
+@pytest.mark.parametrize("V", [100, 5000, 70001])
+def test_the_smallest_weights_at_a_zero_uniform(V):
+    """Weights of 2^-1075 to 2^-1074 are not 0 in 64 bits, smaller ones are: the first that is not is drawn."""
+    low = np.float32([-744.5, -744.8, -745.0, -745.1, -745.2, -746.0, -800.0])
+    x = torch.zeros((len(low), V))
+    x[:, 0] = torch.tensor(low)
+    one = torch.ones(len(low), device=DEV)
+    x = x.to(DEV)
+    want = [0 if w > 0 else 1 for w in np.exp(low.astype(np.float64))]
+    assert want == [0, 0, 0, 0, 1, 1, 1]
+    for kw in (dict(), dict(top_p=one * 0.999999), dict(top_k=torch.full((len(low),), V, dtype=torch.int32, device=DEV))):
+        assert sv.spec_sample_filtered(x, one * 0.0, one, **{n: v for n, v in kw.items() if n != "top_p"})["tokens"].tolist() == want
