@@ -55,7 +55,7 @@
  *     context); it never deadlocks waiting for a CTA that cannot start.
  *   - Apart from a per-thread copy of the last error message, the library keeps
  *     only caches filled once per device and guarded by locks (a kernel's
- *     occupancy and shared-memory limit, the static workspace's address); the
+ *     occupancy, in blocks or clusters, and shared-memory limit, the static workspace's address); the
  *     functions may be called from several host threads.
  */
 #ifndef SPEC_VERIFY_H
@@ -325,6 +325,10 @@ SPEC_API spec_status spec_mtp_plug(const int32_t *in_tokens, int B, int K, const
  *   min-p   of those, the ones with w_v >= min_p.
  * Each leaves a prefix of the order.  The token is the first v, in index order,
  * whose running sum of kept weights exceeds u * (their sum).
+ * Not for draft tokens that spec_verify_linear is to test, where a filter limits
+ * or rows differ in T: it takes q for the whole draft row's softmax at one T, and
+ * what it emits follows the target only if the draft was drawn from that
+ * (spec_sample_rows, or this call without filters at that T).
  *
  *   logits      [B, V]  fp32 or bf16; -inf masks a token (it is never kept).
  *   temperature [B] fp32: 0 (the lowest-index argmax; the row's other
@@ -381,6 +385,11 @@ SPEC_API spec_status spec_top_logits(const void *logits, spec_dtype dtype, int B
  *   loss = w * sum_k p_k (log p_k - log q[id_k])
  *   d loss / d s_v = (w / T) * (P q_v - sum of p_k over the entries with id_k = v)
  * The teacher is a constant: it gets no gradient.
+ * The mass that top_lse leaves outside the K entries, 1 - P, enters neither loss
+ * nor gradient: with it the gradient is P times the one without it (the least
+ * loss is at q = p / P on the entries, 0 elsewhere, either way), so it weighs
+ * each row by how much of the teacher its entries hold.  The loss is then a
+ * divergence only at P = 1; below it may be negative.
  *
  *   student_logits [N, V] fp32 or bf16; -inf masks a token (a masked token that
  *                  the teacher gives weight makes the loss +inf).

@@ -566,7 +566,10 @@ def spec_sample_filtered(logits, u, temperature, *, top_k=None, top_p=None, min_
                          stream=None):
     """One token per row of logits [B, V] under temperature [B] (float32; 0: the argmax), top_k [B]
     (int32; <= 0: no limit), top_p [B] and min_p [B] (float32), at u [B] (float32, in [0, 1)); a
-    filter left None does not limit.  Returns dict(tokens [B], status)."""
+    filter left None does not limit.  Returns dict(tokens [B], status).
+
+    Draft tokens for spec_verify_linear come from spec_sample_rows, or from this without filters at
+    the verify's temperature: it tests them against the whole draft row's softmax."""
     lib = load_library()
     B, V, dev, i, code = _logits_2d(logits, "logits")
     if u is None or temperature is None:
@@ -622,7 +625,8 @@ def _distill_inputs(student, top_ids, top_logits, top_lse, row_weight, temperatu
 def spec_distill(student, top_ids, top_logits, temperature=1.0, *, top_lse=None, row_weight=None, grad=False,
                  status=None, out=None, stream=None):
     """Distillation loss of student logits [N, V] against a teacher's largest logits (top_ids [N, K]
-    int32, top_logits [N, K] float32, and with top_lse [N] float32 its log-normaliser; as
+    int32, top_logits [N, K] float32, and with top_lse [N] float32 its log-normaliser, which weighs
+    a row by the mass P of its entries, the rest of the teacher entering nothing; as
     spec_top_logits returns them): returns dict(loss [N], stats [N, 2], status), and with grad=True
     also grad [N, V], the gradient of the summed losses in student's dtype (out["grad"] may be
     student itself: autograd then refuses a graph that saved the logits).  row_weight [N] scales
