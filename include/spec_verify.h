@@ -405,7 +405,7 @@ SPEC_API spec_status spec_top_logits(const void *logits, spec_dtype dtype, int B
  *         sum_v exp((s_v - largest) / T), for spec_distill_backward.
  *   grad  [N, V] of the logits' type, or NULL: the gradient of the sum of the
  *         losses, overwritten; it may be student_logits itself (in place), and
- *         must not overlap it otherwise.
+ *         must not overlap it otherwise (SPEC_ERR_INVALID_ARG).
  *         With it the logits are read once for both.
  *   dev_status  SPEC_DEV_BAD_TOKEN; SPEC_DEV_NONFINITE: a row of weight other
  *         than 0 with NaN or +inf among its logits or its teacher's, or nothing

@@ -12,7 +12,7 @@ namespace spec {
 namespace vocab {
 
 constexpr int kThreads = 256;
-// CTAs of a row kernel per SM.  With 3 (80 registers) sampling spills 80 words in bf16 and
+// CTAs of a row kernel per SM.  With 3 (80 registers) sampling spills 78 words in bf16 and
 // 14 in fp32, the largest logits none: 48 flat rows of 50257 fp32 take
 // 61 us against 65 with 4, the 64 largest of 2304 rows of 129280 bf16 134 against 141, top-p alone over 64
 // rows of 128256 bf16 58 against 71, one row 10.7 against 11.7; 4 hide more of each other's tails where rows are

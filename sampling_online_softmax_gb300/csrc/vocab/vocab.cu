@@ -49,6 +49,17 @@ spec_status distill_args(DistillArgs *a, const void *student, spec_dtype dtype, 
     return SPEC_OK;
 }
 
+// The gradient lies over the logits each on its own, or beside them: shifted, it would overwrite others unread.
+spec_status place_grad(DistillArgs *a, void *grad, spec_dtype dtype) {
+    if (!aligned(grad, elt_bytes(dtype))) return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    a->grad = static_cast<unsigned char *>(grad);
+    const uintptr_t g = reinterpret_cast<uintptr_t>(grad), s = reinterpret_cast<uintptr_t>(a->student);
+    const size_t bytes = static_cast<size_t>(a->student_end - a->student);
+    if (grad && g != s && (g > s ? g - s : s - g) < bytes)
+        return fail(SPEC_ERR_INVALID_ARG, "grad overlaps student_logits in part");
+    return SPEC_OK;
+}
+
 // The checks every operator on [B, V] logits shares, and their fields of the parameter block.
 spec_status rows_args(RowArgs *a, const void *logits, spec_dtype dtype, int B, int V, uint32_t *dev_status) {
     const int eb = elt_bytes(dtype);
@@ -150,11 +161,11 @@ extern "C" spec_status spec_distill(const void *student_logits, spec_dtype dtype
     spec_status st = distill_args(&a, student_logits, dtype, N, V, top_ids, top_logits, K, top_lse, temperature, row_weight, dev_status);
     if (st != SPEC_OK || N == 0) return st;
     if (!loss || !stats) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
-    if (!aligned(loss, 4) || !aligned(stats, 8) || !aligned(grad, elt_bytes(dtype)))
-        return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    if (!aligned(loss, 4) || !aligned(stats, 8)) return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    st = place_grad(&a, grad, dtype);
+    if (st != SPEC_OK) return st;
     a.loss = loss;
     a.stats = stats;
-    a.grad = static_cast<unsigned char *>(grad);
     const int form = grad ? kLossGrad : kLoss;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == SPEC_F32 ? launch_distill<4>(a, form, s) : launch_distill<2>(a, form, s);
@@ -169,11 +180,11 @@ extern "C" spec_status spec_distill_backward(const void *student_logits, spec_dt
     spec_status st = distill_args(&a, student_logits, dtype, N, V, top_ids, top_logits, K, top_lse, temperature, row_weight, dev_status);
     if (st != SPEC_OK || N == 0) return st;
     if (!stats || !grad_loss || !grad) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
-    if (!aligned(stats, 8) || !aligned(grad_loss, 4) || !aligned(grad, elt_bytes(dtype)))
-        return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    if (!aligned(stats, 8) || !aligned(grad_loss, 4)) return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    st = place_grad(&a, grad, dtype);
+    if (st != SPEC_OK) return st;
     a.stats = const_cast<float *>(stats);
     a.grad_loss = grad_loss;
-    a.grad = static_cast<unsigned char *>(grad);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == SPEC_F32 ? launch_distill<4>(a, kBackward, s) : launch_distill<2>(a, kBackward, s);
 }

@@ -222,3 +222,12 @@ def test_a_gradient_over_saved_logits_is_refused_by_autograd(fake):
         y.sum().backward()
         with torch.inference_mode():
             call(torch.zeros((N, V)))
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_a_gradient_that_overlaps_the_logits_in_part_is_refused(lib, dtype):
+    """Over them or beside them, not shifted: by an element, a row, all but an element."""
+    size = 2 * 100 * (4 if dtype == 0 else 2)
+    for off in (4, size // 2, size - 4, -4, -size // 2, 4 - size):
+        assert _distill(lib, dtype=dtype, grad=ctypes.c_void_p(0x10000 + off)) == (sv.SPEC_ERR_INVALID_ARG,) * 2
+        assert "overlap" in lib.spec_last_error().decode()
