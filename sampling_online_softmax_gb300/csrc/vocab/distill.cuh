@@ -9,7 +9,7 @@
 // between the exp-sum and the gradient, and goes on to another row: as a thread
 // takes a vector for the gradient, it sends for the next row's into its place, so
 // that memory is read while the gradient is written and the next teacher weighed.
-// A row has one cluster barrier.  2048 rows of 128256 bf16 take 212 us (4.7 TB/s of
+// A row has one cluster barrier.  2048 rows of 128256 bf16 take 214 us (4.7 TB/s of
 // reads and writes; 147 at the copy rate).  What holds it back is the row's own chain
 // (exp-sum 2.8 us, barrier and merging 4, gradient 3.6: 11 us a row, in which an SM
 // moves 384 KB) and steady write-back.  Tried and slower: no prefetch (223 us), one
