@@ -86,19 +86,26 @@ typedef enum spec_status {
 
 typedef enum spec_dtype {
     SPEC_F32 = 0,  /* IEEE binary32 logits */
-    SPEC_BF16 = 1  /* bfloat16 logits (upper half of an IEEE binary32) */
+    SPEC_BF16 = 1, /* bfloat16 logits (upper half of an IEEE binary32) */
+    SPEC_F16 = 2,  /* IEEE binary16: queries, keys and values alone */
+    SPEC_E4M3 = 3  /* 8-bit floats (4 bits of exponent, 3 of mantissa), a cache's alone, with a power of two a row */
 } spec_dtype;
 
 /* Bits OR-ed into *dev_status by the kernels. */
 #define SPEC_DEV_BAD_TOKEN     1u  /* a draft token outside [0, V): treated as rejected;
-                                      spec_distill: a teacher's token outside [-1, V): left out */
+                                      spec_distill: a teacher's token outside [-1, V): left out;
+                                      spec_adjust_logits: any token outside [-1, V): left out */
 #define SPEC_DEV_NONFINITE     2u  /* a row whose max or exp-sum is not finite; outputs unspecified */
 #define SPEC_DEV_TIMEOUT       4u  /* a bounded wait (a copy, or a value another warp publishes) gave up; outputs unspecified, workspace cleared */
 #define SPEC_DEV_ZERO_RESIDUAL 8u  /* residual weight W == 0 at a rejection: drew from p_j instead */
 #define SPEC_DEV_BAD_TREE     16u  /* parents[] not topological (0 <= parents[c] < c): edge ignored */
 #define SPEC_DEV_BAD_LENGTH   32u  /* spec_sample_bonus: accept_len[b] outside [0, K] (token -1);
-                                      spec_mtp_plug: num_emitted[b] outside [0, K+1] */
-#define SPEC_DEV_BAD_PARAM    64u  /* spec_sample_filtered: a row's parameter out of range (token -1) */
+                                      spec_mtp_plug: num_emitted[b] outside [0, K+1];
+                                      the cache's calls: a position behind the page table's end, or a length that
+                                      its call excludes; spec_adjust_logits: a length outside the history */
+#define SPEC_DEV_BAD_PARAM    64u  /* spec_sample_filtered: a row's parameter out of range (token -1);
+                                      spec_adjust_logits: a penalty out of range (taken as none) */
+#define SPEC_DEV_BAD_PAGE    128u  /* the cache's calls: a page table entry outside [0, pages) that a call needs */
 
 /* Limits of the operators on rows of logits (spec_sample_filtered,
  * spec_top_logits, spec_distill, which keeps a row in a cluster's shared memory). */
@@ -431,6 +438,137 @@ SPEC_API spec_status spec_distill_backward(const void *student_logits, spec_dtyp
                                            const float *top_logits, int K, const float *top_lse, float temperature,
                                            const float *row_weight, const float *stats, const float *grad_loss, void *grad,
                                            uint32_t *dev_status, void *stream);
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on the logits that a
+ * verify or a draw then takes.  Row n of sequence b scores what follows node n
+ * of the draft, so it counts the sequence's history and the drafted tokens on
+ * node n's own path, which differ from row to row:
+ *   x = logits[b, n, t] in fp32, then in this order, each step rounded to fp32:
+ *   bias        x += the sum of the bias values whose id is t (in slot order)
+ *   repetition  if t is in the history or on the path: x = x > 0 ? x / r : x * r
+ *   frequency   x -= f * c,  c = how often t is among the generated tokens and on the path
+ *   presence    x -= p  if c > 0
+ *   mask        x = -inf  if t's bit in allowed is 0 (whatever x is, NaN too)
+ * and out[b, n, t] = x in the logits' type.
+ *   logits [B, N, V] fp32 or bf16: a verify's target rows.  A linear draft of K
+ *          tokens has N = K + 1 and mask NULL; rows without a draft have N = 1.
+ *   tokens [B, L] int32: the history, prompt first; -1 is no token.  NULL with L = 0: none.
+ *   prompt_len, total_len [B] int32: tokens[b, 0 .. prompt_len) are the prompt's, up to
+ *          total_len the generated ones, the token that the step started from (the
+ *          root) among them.  NULL: 0, and L.
+ *   node_tokens [B, N] int32: column 0 (the root) is ignored, -1 is no token; row b of
+ *          spec_mtp_plug's in_tokens has this form.  NULL: no drafted tokens.
+ *   mask   [N, ceil(N/32)]: node n's path as spec_tree_mask gives it (bit 0 is
+ *          ignored); NULL: a chain, nodes 1 .. n.
+ *   repetition r > 0, frequency f, presence p: [B] fp32, finite, or NULL (1, 0, 0).
+ *          A sequence with r = 1 and f = p = 0 has its history left unread.
+ *   bias_ids, bias [B, M]: int32 (-1: an empty slot), fp32.  NULL with M = 0: none.
+ *   allowed [B, N, ceil(V/32)] uint32: bit (t % 32) of word t / 32 of a row; NULL: all.
+ *   out    [B, N, V]: it may be logits itself (then only what changes is written), and
+ *          must not overlap it otherwise (SPEC_ERR_INVALID_ARG).
+ *   dev_status  SPEC_DEV_BAD_TOKEN, SPEC_DEV_BAD_LENGTH (taken as the nearest length
+ *          in [0, L], the prompt's at most total_len), SPEC_DEV_BAD_PARAM.
+ * 1 <= N <= SPEC_MAX_NODES, 0 <= M <= SPEC_MAX_BIASES, 0 <= L < 2^24.  No workspace; one
+ * launch; the same result every time.
+ */
+SPEC_API spec_status spec_adjust_logits(const void *logits, spec_dtype dtype, int B, int N, int V, const int32_t *tokens, int L,
+                                        const int32_t *prompt_len, const int32_t *total_len, const int32_t *node_tokens,
+                                        const uint32_t *mask, const float *repetition, const float *frequency,
+                                        const float *presence, const int32_t *bias_ids, const float *bias, int M,
+                                        const uint32_t *allowed, void *out, uint32_t *dev_status, void *stream);
+#define SPEC_MAX_NODES  1024 /* N of spec_adjust_logits and spec_tree_attention */
+#define SPEC_MAX_BIASES 1024 /* M of spec_adjust_logits */
+
+/*
+ * A paged cache of keys and values, as the three calls below take it (a HOST
+ * struct, read during the call; its pointers are device memory).  A token at
+ * position i of sequence b lies in page page_table[b, i / page_size], in slot
+ * i % page_size of every head.  In 8 bits each (token, head) row of D values x has
+ * one power of two 2^e, kept as the byte e + 127: with e the least whole number
+ * such that max |x| <= 448 * 2^e, -110 <= e <= 120 (in fp16 also e >= -24), the values
+ * are x / 2^e rounded to e4m3, to nearest even (fp16 values beyond 63488 are kept as
+ * 61440, which fp16 can give back).  A row with an infinity or a NaN has byte 255 and reads as NaN.
+ * Powers of two lose nothing in a floating format and make what is read back exact.
+ */
+typedef struct spec_cache {
+    void *k, *v;               /* [pages, kv_heads, page_size, head_dim], 16-byte aligned */
+    uint8_t *k_scale, *v_scale; /* [pages, kv_heads, page_size] with SPEC_E4M3, else NULL */
+    const int32_t *page_table; /* [B, table_width] */
+    spec_dtype dtype;          /* SPEC_E4M3, or the type of the keys and values themselves */
+    int pages, page_size;      /* page_size 16, 32, 64, 128 or 256 */
+    int kv_heads, head_dim;    /* head_dim 64 or 128 */
+    int table_width;
+} spec_cache;
+
+/*
+ * Writes keys and values of a batch into the cache: what a prompt, a step, or the
+ * accepted path of a verified draft adds to each sequence's context.
+ *   k, v     [B, N, kv_heads, head_dim] of `dtype` (SPEC_BF16 or SPEC_F16); strides (host, 4
+ *            entries: k's batch and token strides in elements, then v's; multiples of 8) or
+ *            NULL for contiguous; 16-byte aligned.
+ *   select   [B, S] int32: row i of sequence b is token select[b, i] (spec_verify_tree's
+ *            path_nodes with S = max_depth + 1); a negative entry writes nothing.  NULL: S = N, row i is token i.
+ *   start    [B] int32: row i goes to position start[b] + i; a sequence with a negative start is left out.
+ *   count    [B] int32: only rows i < count[b] (above S: S, below 0: none); NULL: all S.
+ *            spec_verify_linear's num_emitted, when u_bonus was given, counts the accepted rows (the root's among them).
+ * No length is advanced: the layers of a model call this with the same start.
+ * Two rows that name one slot leave either's value.  dev_status: SPEC_DEV_BAD_LENGTH (a
+ * position behind the table, or an entry of select not below N), SPEC_DEV_BAD_PAGE; such a row
+ * is not written.  No workspace; one launch.
+ */
+SPEC_API spec_status spec_cache_append(const void *k, const void *v, spec_dtype dtype, int B, int N, const long long *strides,
+                                       const int32_t *select, int S, const int32_t *start, const int32_t *count,
+                                       const spec_cache *cache, uint32_t *dev_status, void *stream);
+
+/*
+ * Reads positions start[b] .. start[b] + count[b] - 1 of every sequence back:
+ *   k, v [B, S, kv_heads, head_dim] of `dtype` (output, contiguous, 16-byte aligned): row i is
+ *        position start[b] + i; rows from count[b] on are left as they were.  With SPEC_E4M3
+ *        each value is q * 2^e, rounded to `dtype` (exactly, but for fp16 below 2^-14).
+ *   start, count, dev_status as in spec_cache_append (such a row is left as it was).
+ */
+SPEC_API spec_status spec_cache_read(const spec_cache *cache, int B, int S, const int32_t *start, const int32_t *count, void *k,
+                                     void *v, spec_dtype dtype, uint32_t *dev_status, void *stream);
+
+/*
+ * Attention of drafted tokens: the N nodes of each sequence's draft (N = 1: plain
+ * decoding) attend to the sequence's cached context and to the nodes on their own
+ * path ("Speculative-Decoding / Medusa" blog, section 三: the tree is verified in
+ * one target pass under a mask that keeps its paths apart), for query head h of key head
+ * g = h / (heads / kv_heads):
+ *   s_j = scale * q[b, n, h] . k_j,   out[b, n, h] = sum_j exp(s_j) v_j / sum_j exp(s_j)
+ * over the positions j < context_lens[b] of the cache and the nodes m with bit m set in mask
+ * row n.  A row that sees nothing gives 0, and lse -inf.  A key or value that a row does not
+ * see has no part in it, whatever it holds.
+ *   q [B, N, heads, head_dim], k, v [B, N, kv_heads, head_dim] of `dtype` (SPEC_BF16 or
+ *          SPEC_F16): the nodes' own, not in the cache yet (spec_cache_append adds the accepted
+ *          ones); strides (host, 6 entries: q's batch and token strides in elements, k's, v's;
+ *          multiples of 8) or NULL for contiguous; 16-byte aligned.
+ *   cache  of `dtype` or SPEC_E4M3.  Positions may differ in their key heads' scales.
+ *   context_lens [B] int32; a sequence with a negative length is left out, its rows of out
+ *          and lse as they were.
+ *   shared_len  the first shared_len positions hold the same keys and values in every
+ *          sequence (a common prompt): they are read through sequence 0's page table, once for
+ *          the whole batch.  0: nothing is shared.  Every context_lens[b] >= 0 is then at least
+ *          shared_len (SPEC_DEV_BAD_LENGTH where it is not, and that sequence's rows are unspecified).
+ *   mask   [N, ceil(N/32)] as spec_tree_mask gives it; NULL: a chain, nodes 0 .. n.
+ *   scale  finite, > 0.
+ *   out    [B, N, heads, head_dim] of `dtype`, contiguous, 16-byte aligned.
+ *   lse    [B, N, heads] fp32 or NULL: log sum_j exp(s_j).
+ *   dev_status  SPEC_DEV_BAD_LENGTH, SPEC_DEV_BAD_PAGE: that sequence's rows are unspecified;
+ *          SPEC_DEV_TIMEOUT.
+ *   workspace  spec_workspace_bytes_attention() bytes, 16-byte aligned; its content before a
+ *          call does not matter.
+ * Scores, sums and the weighted sums are fp32; exp(s_j - m), the weight of v_j in the matrix
+ * product, is rounded to `dtype` (2^-9 of itself in bf16, with errors that the sum averages).
+ * 1 <= N <= SPEC_MAX_NODES; heads a multiple of kv_heads.  The same result every time.
+ */
+SPEC_API size_t spec_workspace_bytes_attention(int B, int N, int heads, int kv_heads, int head_dim, int shared_len);
+SPEC_API spec_status spec_tree_attention(const void *q, const void *k, const void *v, spec_dtype dtype, int B, int N, int heads,
+                                         const long long *strides, const spec_cache *cache, const int32_t *context_lens,
+                                         int shared_len, const uint32_t *mask, float scale, void *out, float *lse,
+                                         uint32_t *dev_status, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * spec_verify_linear with the library's own workspace.  The pages describe no

@@ -24,6 +24,12 @@ Entry points (same names as the C ABI):
                        outputs, and the advanced lengths, on the device
                        ("Beschleunigung von Sonar durch Spekulation", sections
                        "MTP" and "MTP-Zeitplan für ein einzelnes Token")
+  spec_sample_filtered, spec_top_logits, spec_distill, spec_distill_backward
+                       operators on rows of logits
+  spec_adjust_logits   penalties, biases and grammar masks on a verify's rows
+  spec_tree_attention, spec_cache_append, spec_cache_read
+                       attention of drafted tokens over a paged cache, which is
+                       written and read back in 8 bits or as it is
 """
 from __future__ import annotations
 
@@ -45,6 +51,8 @@ SPEC_ERR_WORKSPACE = 4
 
 SPEC_F32 = 0
 SPEC_BF16 = 1
+SPEC_F16 = 2
+SPEC_E4M3 = 3
 
 DEV_BAD_TOKEN = 1
 DEV_NONFINITE = 2
@@ -53,15 +61,26 @@ DEV_ZERO_RESIDUAL = 8
 DEV_BAD_TREE = 16
 DEV_BAD_LENGTH = 32
 DEV_BAD_PARAM = 64
+DEV_BAD_PAGE = 128
 
 MAX_ROW_BYTES = 1 << 20  # SPEC_MAX_ROW_BYTES
 MAX_TOP = 1024           # SPEC_MAX_TOP
+MAX_NODES = 1024         # SPEC_MAX_NODES
+MAX_BIASES = 1024        # SPEC_MAX_BIASES
+PAGE_SIZES = (16, 32, 64, 128, 256)
 
 
 class SpecError(RuntimeError):
     def __init__(self, status: int, detail: str):
         super().__init__("%s (%s)" % (detail, _status_name(status)))
         self.status = status
+
+
+class _Cache(ctypes.Structure):
+    """spec_cache of the C ABI."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("dtype", ctypes.c_int), ("pages", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("table_width", ctypes.c_int)]
 
 
 _lock = threading.Lock()
@@ -115,6 +134,16 @@ def load_library():
         lib.spec_distill.restype = i32
         lib.spec_distill_backward.argtypes = [P, i32, i32, i32, P, P, i32, P, f32, P, P, P, P, P, P]
         lib.spec_distill_backward.restype = i32
+        lib.spec_adjust_logits.argtypes = [P, i32, i32, i32, i32, P, i32, P, P, P, P, P, P, P, P, P, i32, P, P, P, P]
+        lib.spec_adjust_logits.restype = i32
+        lib.spec_cache_append.argtypes = [P, P, i32, i32, i32, P, P, i32, P, P, P, P, P]
+        lib.spec_cache_append.restype = i32
+        lib.spec_cache_read.argtypes = [P, i32, i32, P, P, P, P, i32, P, P]
+        lib.spec_cache_read.restype = i32
+        lib.spec_workspace_bytes_attention.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.spec_workspace_bytes_attention.restype = u64
+        lib.spec_tree_attention.argtypes = [P, P, P, i32, i32, i32, i32, P, P, P, i32, P, f32, P, P, P, P, u64, P]
+        lib.spec_tree_attention.restype = i32
         lib.spec_status_string.argtypes = [i32]
         lib.spec_status_string.restype = ctypes.c_char_p
         lib.spec_last_error.argtypes = []
@@ -664,6 +693,228 @@ def spec_distill_backward(student, top_ids, top_logits, stats, grad_loss, temper
     if out is not None:
         _overwritten(out)
     return r
+
+
+def spec_adjust_logits(logits, *, tokens=None, prompt_len=None, total_len=None, node_tokens=None, mask=None, repetition=None,
+                       frequency=None, presence=None, bias_ids=None, bias=None, allowed=None, out=None, status=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks on logits [B, N, V] (a verify's target rows: N = K + 1 for a
+    linear draft, the tree's nodes, or 1 without a draft): returns dict(logits [B, N, V], status).
+
+    tokens [B, L] int32 is the history (prompt_len [B], total_len [B]: where the prompt and the history end; -1 is no token),
+    node_tokens [B, N] int32 the drafted tokens (column 0, the root, ignored), mask [N, ceil(N/32)] their paths as
+    spec_tree_mask gives them (None: a chain).  A row counts the history and its own path: repetition (divides or
+    multiplies), frequency (a count) and presence [B] float32.  bias_ids, bias [B, M] add to tokens; allowed
+    [B, N, ceil(V/32)] int32 holds a bit a token, 0 for -inf.  out=dict(logits=logits) works in place (autograd then
+    refuses a graph that saved the logits)."""
+    lib = load_library()
+    if not (logits.is_cuda and logits.is_contiguous()):
+        _cuda(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, N, V]")
+    B, N, V = logits.shape
+    dev = logits.device
+    i, code, i32, f32 = dev.index, _dtype_code(logits), torch.int32, torch.float32
+    if N < 1 or V < 1:
+        raise ValueError("logits must have at least one row and one token")
+    L = M = 0
+    if tokens is not None:
+        if tokens.dim() != 2:
+            raise ValueError("tokens must be [B, L]")
+        L = tokens.shape[1]
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    if bias_ids is not None:
+        if bias_ids.dim() != 2:
+            raise ValueError("bias_ids must be [B, M]")
+        M = bias_ids.shape[1]
+    row = (B,)
+    args = (_may(tokens, "tokens", i32, (B, L), dev, i), L, _may(prompt_len, "prompt_len", i32, row, dev, i),
+            _may(total_len, "total_len", i32, row, dev, i), _may(node_tokens, "node_tokens", i32, (B, N), dev, i),
+            _may(mask, "mask", i32, (N, (N + 31) // 32), dev, i), _may(repetition, "repetition", f32, row, dev, i),
+            _may(frequency, "frequency", f32, row, dev, i), _may(presence, "presence", f32, row, dev, i),
+            _may(bias_ids, "bias_ids", i32, (B, M), dev, i), _may(bias, "bias", f32, (B, M), dev, i), M,
+            _may(allowed, "allowed", i32, (B, N, (V + 31) // 32), dev, i))
+    given = out is not None
+    out, (at,), st = _results(out, {"logits": ((B, N, V), logits.dtype)}, status, dev, i, stream)
+    _launch(lib.spec_adjust_logits, (logits.data_ptr(), code, B, N, V, *args, at, st),
+            (logits, tokens, prompt_len, total_len, node_tokens, mask, repetition, frequency, presence, bias_ids, bias, allowed,
+             *out.values()), dev, stream)
+    if given:
+        _overwritten(out["logits"])
+    return out
+
+
+_CODES = {torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+
+
+def _cache_arg(k_cache, v_cache, page_table, k_scale, v_scale, B, heads, dim, dtype, dev, i):
+    """Checks a paged cache for keys and values of `heads` heads of `dim`; returns the C struct."""
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim]")
+    pages, kv, page, d = k_cache.shape
+    if (kv, d) != (heads, dim):
+        raise ValueError("k_cache must have %d heads of %d, got %d of %d" % (heads, dim, kv, d))
+    q8 = k_cache.dtype is torch.float8_e4m3fn
+    if not q8 and k_cache.dtype is not dtype:
+        raise TypeError("k_cache must be %s or torch.float8_e4m3fn, got %s" % (dtype, k_cache.dtype))
+    if q8 != (k_scale is not None) or q8 != (v_scale is not None):
+        raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache, and it needs both")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, width]")
+    shape = (pages, kv, page)
+    return _Cache(_need(k_cache, "k_cache", k_cache.dtype, (*shape, d), dev, i), _need(v_cache, "v_cache", k_cache.dtype, (*shape, d), dev, i),
+                  _may(k_scale, "k_scale", torch.uint8, shape, dev, i), _may(v_scale, "v_scale", torch.uint8, shape, dev, i),
+                  _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev, i),
+                  SPEC_E4M3 if q8 else _CODES[dtype], pages, page, kv, d, page_table.shape[1])
+
+
+def _token_rows(t, name, shape, dtype, dev, index):
+    """Checks [B, N, heads, dim], whose heads lie together while its tokens may be strided; returns (address, batch and token strides)."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    B, N, heads, dim = shape
+    sb, sn, sh, sd = t.stride()
+    if t.numel() and ((dim > 1 and sd != 1) or (heads > 1 and sh != dim)):
+        raise ValueError("%s must have its heads next to each other (strides %s)" % (name, t.stride()))
+    sn = sn if N > 1 else heads * dim  # (an axis of one entry has any stride)
+    sb = sb if B > 1 else N * heads * dim
+    if sb % 8 or sn % 8 or sb < 0 or sn < 0 or t.data_ptr() % 16:
+        raise ValueError("%s must start on a 16-byte boundary with strides of whole 16 bytes (strides %s)" % (name, t.stride()))
+    return t.data_ptr(), sb, sn
+
+
+def _new_tokens(t, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dim() != 4:
+        raise ValueError("%s must be [B, N, heads, head_dim]" % name)
+    if t.dtype not in _CODES:
+        raise TypeError("%s must be bfloat16 or float16, got %s" % (name, t.dtype))
+    return t.shape, t.dtype, t.device, t.device.index
+
+
+def _status_at(status, dev, index, stream):
+    """The status word alone, a new one where it is None."""
+    return _results({}, {}, status, dev, index, stream)[::2]
+
+
+def spec_cache_append(k, v, k_cache, v_cache, page_table, start, *, count=None, select=None, k_scale=None, v_scale=None, status=None,
+                      stream=None):
+    """Writes k, v [B, N, kv_heads, head_dim] (bfloat16 or float16; tokens may be strided) into a paged cache
+    [pages, kv_heads, page_size, head_dim] of their type, or of float8_e4m3fn with k_scale, v_scale
+    [pages, kv_heads, page_size] uint8 (a power of two a row): row i of sequence b goes to position start[b] + i, which
+    page_table [B, width] int32 places.  select [B, S] int32 picks the rows (spec_verify_tree's path_nodes; -1: none);
+    count [B] int32 limits them; a negative start leaves a sequence out.  Returns dict(status)."""
+    lib = load_library()
+    shape, dtype, dev, i = _new_tokens(k, "k")
+    B, N, heads, dim = shape
+    at, sk = _token_rows(k, "k", shape, dtype, dev, i), _token_rows(v, "v", shape, dtype, dev, i)
+    cache = _cache_arg(k_cache, v_cache, page_table, k_scale, v_scale, B, heads, dim, dtype, dev, i)
+    if select is not None and select.dim() != 2:
+        raise ValueError("select must be [B, S]")
+    S = N if select is None else select.shape[1]
+    i32 = torch.int32
+    args = (_may(select, "select", i32, (B, S), dev, i), S, _need(start, "start", i32, (B,), dev, i), _may(count, "count", i32, (B,), dev, i))
+    out, st = _status_at(status, dev, i, stream)
+    strides = (ctypes.c_longlong * 4)(at[1], at[2], sk[1], sk[2])
+    _launch(lib.spec_cache_append, (at[0], sk[0], _CODES[dtype], B, N, strides, *args, ctypes.byref(cache), st),
+            (k, v, k_cache, v_cache, page_table, start, count, select, k_scale, v_scale, *out.values()), dev, stream)
+    for t in (k_cache, v_cache, k_scale, v_scale):
+        if t is not None:
+            _overwritten(t)
+    return out
+
+
+def spec_cache_read(k_cache, v_cache, page_table, start, n, *, count=None, k_scale=None, v_scale=None, dtype=torch.bfloat16, status=None,
+                    out=None, stream=None):
+    """Reads n positions of every sequence, from start[b] on, out of a paged cache as spec_cache_append writes it: returns
+    dict(k, v [B, n, kv_heads, head_dim], status), of the cache's type, or of `dtype` (bfloat16, float16) where the
+    cache is float8_e4m3fn.  Rows from count[b] on are left as they were (new ones: 0)."""
+    lib = load_library()
+    if not k_cache.is_cuda:
+        raise ValueError("k_cache must be a CUDA tensor")
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim]")
+    _, heads, _, dim = k_cache.shape
+    dev, n = k_cache.device, int(n)
+    i = dev.index
+    if k_cache.dtype in _CODES:
+        dtype = k_cache.dtype
+    if dtype not in _CODES:
+        raise TypeError("dtype must be bfloat16 or float16, got %s" % dtype)
+    if n < 0:
+        raise ValueError("n must be >= 0")
+    if start is None or start.dim() != 1:
+        raise ValueError("start must be [B]")
+    B = start.shape[0]
+    cache = _cache_arg(k_cache, v_cache, page_table, k_scale, v_scale, B, heads, dim, dtype, dev, i)
+    args = (_need(start, "start", torch.int32, (B,), dev, i), _may(count, "count", torch.int32, (B,), dev, i))
+    shape, given = (B, n, heads, dim), out is not None
+    if not given:
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            out = {x: torch.zeros(shape, dtype=dtype, device=dev) for x in ("k", "v")}
+    out, at, st = _results(out, {"k": (shape, dtype), "v": (shape, dtype)}, status, dev, i, stream)
+    _launch(lib.spec_cache_read, (ctypes.byref(cache), B, n, *args, *at, _CODES[dtype], st),
+            (k_cache, v_cache, page_table, start, count, k_scale, v_scale, *out.values()), dev, stream)
+    if given:
+        _overwritten(out["k"])
+        _overwritten(out["v"])
+    return out
+
+
+def spec_workspace_bytes_attention(B: int, N: int, heads: int, kv_heads: int, head_dim: int, shared_len: int = 0) -> int:
+    return int(load_library().spec_workspace_bytes_attention(int(B), int(N), int(heads), int(kv_heads), int(head_dim), int(shared_len)))
+
+
+def spec_tree_attention(q, k, v, k_cache, v_cache, page_table, context_lens, *, mask=None, shared_len=0, scale=None, k_scale=None,
+                        v_scale=None, lse=False, status=None, out=None, workspace=None, stream=None):
+    """Attention of the N drafted nodes of each sequence over its cached context and their own paths: q [B, N, heads,
+    head_dim], k, v [B, N, kv_heads, head_dim] (bfloat16 or float16; tokens may be strided; not in the cache yet) and a paged
+    cache as spec_cache_append writes it, of which sequence b holds context_lens[b] positions (int32; negative: left out).
+    mask [N, ceil(N/32)] int32 as spec_tree_mask gives it (None: a chain, nodes 0 .. n; N = 1 is plain decoding).  The
+    first shared_len positions are the same in every sequence and are read once, through page_table[0].  scale
+    is 1 / sqrt(head_dim) where it is None.  Returns dict(out [B, N, heads, head_dim], status), with lse=True also
+    lse [B, N, heads] float32, the log of the softmax's sum."""
+    lib = load_library()
+    qs, dtype, dev, i = _new_tokens(q, "q")
+    B, N, heads, dim = qs
+    if k.dim() != 4:
+        raise ValueError("k must be [B, N, kv_heads, head_dim]")
+    kv = k.shape[2]
+    if N < 1 or kv < 1 or heads < 1 or heads % kv:
+        raise ValueError("need N >= 1 and heads a multiple of kv_heads, got %d and %d of %d" % (N, heads, kv))
+    ks = (B, N, kv, dim)
+    at = [_token_rows(q, "q", qs, dtype, dev, i), _token_rows(k, "k", ks, dtype, dev, i), _token_rows(v, "v", ks, dtype, dev, i)]
+    cache = _cache_arg(k_cache, v_cache, page_table, k_scale, v_scale, B, kv, dim, dtype, dev, i)
+    shared_len = int(shared_len)
+    args = (_need(context_lens, "context_lens", torch.int32, (B,), dev, i), shared_len, _may(mask, "mask", torch.int32, (N, (N + 31) // 32), dev, i),
+            float(scale) if scale is not None else dim ** -0.5)
+    shapes = {"out": (qs, dtype)}
+    if lse:
+        shapes["lse"] = ((B, N, heads), torch.float32)
+    given = out is not None
+    out, to, st = _results(out, shapes, status, dev, i, stream)
+    nbytes = lib.spec_workspace_bytes_attention(B, N, heads, kv, dim, shared_len)
+    if workspace is None:  # (of the stream's own memory, or of the graph that is being captured)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    else:
+        _cuda(workspace, "workspace", None, dev)
+    room = workspace.numel() * workspace.element_size()
+    strides = (ctypes.c_longlong * 6)(*(x for a in at for x in a[1:]))
+    _launch(lib.spec_tree_attention, (at[0][0], at[1][0], at[2][0], _CODES[dtype], B, N, heads, strides, ctypes.byref(cache), *args,
+                                      to[0], to[1] if lse else None, st, workspace.data_ptr(), room),
+            (q, k, v, k_cache, v_cache, page_table, context_lens, mask, k_scale, v_scale, workspace, *out.values()), dev, stream)
+    if given:
+        for x in shapes:
+            _overwritten(out[x])
+    return out
 
 
 def spec_tree_mask(parents, *, status=None, out=None, stream=None):

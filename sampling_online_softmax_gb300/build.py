@@ -2,7 +2,8 @@
 
 The kernel's modes live in separate translation units (csrc/kern_*.cu), which
 are compiled in parallel and linked with the host side (csrc/spec_verify.cu,
-csrc/tree_build.cpp); the operators on rows of logits live in csrc/vocab/.
+csrc/tree_build.cpp); the operators on rows of logits live in csrc/vocab/, those on
+the paged cache in csrc/context/.
 """
 from __future__ import annotations
 
@@ -17,11 +18,11 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libspecverify.so")
-VOCAB = os.path.join(CSRC, "vocab")
+FOLDERS = (CSRC, os.path.join(CSRC, "vocab"), os.path.join(CSRC, "context"))
 
 
 def _files(pattern):
-    return sorted(glob.glob(os.path.join(CSRC, pattern)) + glob.glob(os.path.join(VOCAB, pattern)))
+    return sorted(f for folder in FOLDERS for f in glob.glob(os.path.join(folder, pattern)))
 
 
 SOURCES = _files("*.cu") + _files("*.cpp")

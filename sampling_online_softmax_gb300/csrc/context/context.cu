@@ -1,0 +1,190 @@
+// context.cu -- host side of the operators on the paged cache (spec_cache_append, spec_cache_read,
+// spec_tree_attention): argument checks and dispatch.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "attention.h"
+#include "cache.cuh"
+
+namespace spec {
+
+extern thread_local char g_last_error[512];
+
+namespace context {
+namespace {
+
+bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// The checks that every call on a cache shares; `dtype` is the keys' and values' own.
+spec_status cache_args(CacheView *v, const spec_cache *c, spec_dtype dtype) {
+    if (dtype != SPEC_BF16 && dtype != SPEC_F16) return fail(SPEC_ERR_INVALID_ARG, "keys and values of dtype %d", (int)dtype);
+    if (!c) return fail(SPEC_ERR_INVALID_ARG, "cache is null");
+    if (c->dtype != dtype && c->dtype != SPEC_E4M3) return fail(SPEC_ERR_INVALID_ARG, "a cache of dtype %d", (int)c->dtype);
+    if (c->pages < 0 || c->kv_heads < 1 || c->table_width < 0) return fail(SPEC_ERR_INVALID_ARG, "need pages >= 0, kv_heads >= 1, table_width >= 0");
+    if (c->head_dim != 64 && c->head_dim != 128) return fail(SPEC_ERR_UNSUPPORTED, "head_dim = %d: 64 or 128", c->head_dim);
+    int bits = 4;
+    while (bits < 8 && 1 << bits != c->page_size) ++bits;
+    if (1 << bits != c->page_size) return fail(SPEC_ERR_UNSUPPORTED, "page_size = %d: 16, 32, 64, 128 or 256", c->page_size);
+    if (c->table_width > INT_MAX >> bits) return fail(SPEC_ERR_UNSUPPORTED, "table_width = %d: positions below 2^31", c->table_width);
+    if (c->kv_heads > 1024) return fail(SPEC_ERR_UNSUPPORTED, "kv_heads = %d > 1024", c->kv_heads);
+    if (c->pages && (!c->k || !c->v)) return fail(SPEC_ERR_INVALID_ARG, "the cache's k or v is null");
+    if (c->table_width && !c->page_table) return fail(SPEC_ERR_INVALID_ARG, "page_table is null");
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4)) return fail(SPEC_ERR_INVALID_ARG, "the cache is misaligned");
+    if (c->dtype == SPEC_E4M3 && c->pages && (!c->k_scale || !c->v_scale)) return fail(SPEC_ERR_INVALID_ARG, "an e4m3 cache needs k_scale and v_scale");
+    *v = CacheView{{static_cast<unsigned char *>(c->k), static_cast<unsigned char *>(c->v)}, {c->k_scale, c->v_scale},
+                   c->page_table, c->pages, bits, c->kv_heads, c->table_width};
+    return SPEC_OK;
+}
+
+// Strides in elements of `n` tensors (batch, token), contiguous where `given` is null.
+spec_status strides_of(long long *to, const long long *given, int n, long long N, const long long *token) {
+    for (int i = 0; i < n; ++i) {
+        to[2 * i] = given ? given[2 * i] : N * token[i];
+        to[2 * i + 1] = given ? given[2 * i + 1] : token[i];
+        if (to[2 * i] % 8 || to[2 * i + 1] % 8 || to[2 * i] < 0 || to[2 * i + 1] < 0)
+            return fail(SPEC_ERR_INVALID_ARG, "strides must be multiples of 8 elements, and not negative");
+    }
+    return SPEC_OK;
+}
+
+enum CacheOp { kAppend, kRead };
+
+template <typename T, int D, bool Q8>
+spec_status launch_cache(CacheOp op, const CacheRowsArgs &a, cudaStream_t stream) {
+    DeviceInfo di;
+    int dev = 0;
+    spec_status st = device_info(&di, &dev);
+    if (st != SPEC_OK) return st;
+    constexpr int kRows = kCacheThreads / (D / 8);  // rows of a CTA at once
+    const long long rows = 2ll * a.B * a.S * a.cache.kv_heads;
+    const long long grid = std::min<long long>((rows + kRows - 1) / kRows, 8ll * di.sms);
+    if (op == kAppend) cache_append_kernel<T, D, Q8><<<static_cast<unsigned>(grid), kCacheThreads, 0, stream>>>(a);
+    else cache_read_kernel<T, D, Q8><<<static_cast<unsigned>(grid), kCacheThreads, 0, stream>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "cache launch: %s", cudaGetErrorString(e));
+}
+
+template <typename T>
+spec_status dispatch_cache(CacheOp op, const CacheRowsArgs &a, int D, bool q8, cudaStream_t s) {
+    if (D == 64) return q8 ? launch_cache<T, 64, true>(op, a, s) : launch_cache<T, 64, false>(op, a, s);
+    return q8 ? launch_cache<T, 128, true>(op, a, s) : launch_cache<T, 128, false>(op, a, s);
+}
+
+template <typename T>
+spec_status dispatch_attention(const AttentionArgs &a, int D, bool q8, cudaStream_t s) {
+    if (D == 64) return q8 ? launch_attention<T, 64, true>(a, s) : launch_attention<T, 64, false>(a, s);
+    return q8 ? launch_attention<T, 128, true>(a, s) : launch_attention<T, 128, false>(a, s);
+}
+
+}  // namespace
+}  // namespace context
+}  // namespace spec
+
+using namespace spec;
+using namespace spec::context;
+
+extern "C" spec_status spec_cache_append(const void *k, const void *v, spec_dtype dtype, int B, int N, const long long *strides,
+                                         const int32_t *select, int S, const int32_t *start, const int32_t *count,
+                                         const spec_cache *cache, uint32_t *dev_status, void *stream) try {
+    g_last_error[0] = '\0';
+    CacheRowsArgs a = {};
+    spec_status st = cache_args(&a.cache, cache, dtype);
+    if (st != SPEC_OK) return st;
+    if (B < 0 || N < 0 || S < 0 || (!select && S != N)) return fail(SPEC_ERR_INVALID_ARG, "need B >= 0, N >= 0, S >= 0, and S == N without select");
+    if (B == 0 || S == 0) return SPEC_OK;
+    if ((N && (!k || !v)) || !start || !dev_status) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
+    if (!aligned(k, 16) || !aligned(v, 16)) return fail(SPEC_ERR_INVALID_ARG, "k or v misaligned (16 bytes)");
+    if (!aligned(select, 4) || !aligned(start, 4) || !aligned(count, 4) || !aligned(dev_status, 4))
+        return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    const long long token = static_cast<long long>(cache->kv_heads) * cache->head_dim, tokens[2] = {token, token};
+    long long to[4];
+    st = strides_of(to, strides, 2, N, tokens);
+    if (st != SPEC_OK) return st;
+    for (int i = 0; i < 2; ++i) a.batch_stride[i] = to[2 * i], a.token_stride[i] = to[2 * i + 1];
+    a.src[0] = static_cast<const unsigned char *>(k);
+    a.src[1] = static_cast<const unsigned char *>(v);
+    a.select = select, a.start = start, a.count = count;
+    a.B = B, a.N = N, a.S = S;
+    a.status = dev_status;
+    const bool q8 = cache->dtype == SPEC_E4M3;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == SPEC_BF16 ? dispatch_cache<__nv_bfloat16>(kAppend, a, cache->head_dim, q8, s)
+                              : dispatch_cache<__half>(kAppend, a, cache->head_dim, q8, s);
+} catch (...) {  // (no exception leaves the C ABI)
+    return fail(SPEC_ERR_CUDA, "spec_cache_append: a host allocation failed");
+}
+
+extern "C" spec_status spec_cache_read(const spec_cache *cache, int B, int S, const int32_t *start, const int32_t *count, void *k,
+                                       void *v, spec_dtype dtype, uint32_t *dev_status, void *stream) try {
+    g_last_error[0] = '\0';
+    CacheRowsArgs a = {};
+    spec_status st = cache_args(&a.cache, cache, dtype);
+    if (st != SPEC_OK) return st;
+    if (B < 0 || S < 0) return fail(SPEC_ERR_INVALID_ARG, "need B >= 0, S >= 0");
+    if (B == 0 || S == 0) return SPEC_OK;
+    if (!k || !v || !start || !dev_status) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
+    if (!aligned(k, 16) || !aligned(v, 16)) return fail(SPEC_ERR_INVALID_ARG, "k or v misaligned (16 bytes)");
+    if (!aligned(start, 4) || !aligned(count, 4) || !aligned(dev_status, 4)) return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    a.dst[0] = static_cast<unsigned char *>(k);
+    a.dst[1] = static_cast<unsigned char *>(v);
+    a.start = start, a.count = count;
+    a.B = B, a.S = S;
+    a.status = dev_status;
+    const bool q8 = cache->dtype == SPEC_E4M3;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == SPEC_BF16 ? dispatch_cache<__nv_bfloat16>(kRead, a, cache->head_dim, q8, s)
+                              : dispatch_cache<__half>(kRead, a, cache->head_dim, q8, s);
+} catch (...) {
+    return fail(SPEC_ERR_CUDA, "spec_cache_read: a host allocation failed");
+}
+
+extern "C" size_t spec_workspace_bytes_attention(int B, int N, int heads, int kv_heads, int head_dim, int shared_len) {
+    if (B <= 0 || N < 1 || N > SPEC_MAX_NODES || kv_heads < 1 || heads < 1 || heads % kv_heads || (head_dim != 64 && head_dim != 128) || shared_len < 0)
+        return 0;
+    return 16;
+}
+
+extern "C" spec_status spec_tree_attention(const void *q, const void *k, const void *v, spec_dtype dtype, int B, int N, int heads,
+                                           const long long *strides, const spec_cache *cache, const int32_t *context_lens,
+                                           int shared_len, const uint32_t *mask, float scale, void *out, float *lse,
+                                           uint32_t *dev_status, void *workspace, size_t workspace_bytes, void *stream) try {
+    g_last_error[0] = '\0';
+    AttentionArgs a = {};
+    spec_status st = cache_args(&a.cache, cache, dtype);
+    if (st != SPEC_OK) return st;
+    const int kv = cache->kv_heads, D = cache->head_dim;
+    if (B < 0 || N < 1 || heads < 1 || heads % kv) return fail(SPEC_ERR_INVALID_ARG, "need B >= 0, N >= 1, heads a multiple of kv_heads");
+    if (N > SPEC_MAX_NODES) return fail(SPEC_ERR_UNSUPPORTED, "N = %d > %d", N, SPEC_MAX_NODES);
+    if (shared_len < 0 || shared_len > cache->table_width * cache->page_size)
+        return fail(SPEC_ERR_INVALID_ARG, "shared_len = %d: within the page table", shared_len);
+    if (!(scale > 0.0f && scale < INFINITY)) return fail(SPEC_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (B == 0) return SPEC_OK;
+    if (static_cast<long long>(B) * N * heads > INT_MAX / 2) return fail(SPEC_ERR_UNSUPPORTED, "too many rows (B=%d, N=%d, heads=%d)", B, N, heads);
+    if (!q || !k || !v || !context_lens || !out || !dev_status) return fail(SPEC_ERR_INVALID_ARG, "a pointer is null");
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16))
+        return fail(SPEC_ERR_INVALID_ARG, "q, k, v or out misaligned (16 bytes)");
+    if (!aligned(context_lens, 4) || !aligned(mask, 4) || !aligned(lse, 4) || !aligned(dev_status, 4))
+        return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
+    const size_t need = spec_workspace_bytes_attention(B, N, heads, kv, D, shared_len);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
+        return fail(SPEC_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, needed (got %zu)", need, workspace_bytes);
+    const long long tokens[3] = {static_cast<long long>(heads) * D, static_cast<long long>(kv) * D, static_cast<long long>(kv) * D};
+    st = strides_of(a.stride, strides, 3, N, tokens);
+    if (st != SPEC_OK) return st;
+    a.q = static_cast<const unsigned char *>(q);
+    a.k = static_cast<const unsigned char *>(k);
+    a.v = static_cast<const unsigned char *>(v);
+    a.lens = context_lens;
+    a.mask = mask;
+    a.out = static_cast<unsigned char *>(out);
+    a.lse = lse;
+    a.status = dev_status;
+    a.B = B, a.N = N, a.heads = heads, a.shared_len = shared_len;
+    a.scale = scale;
+    const bool q8 = cache->dtype == SPEC_E4M3;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == SPEC_BF16 ? dispatch_attention<__nv_bfloat16>(a, D, q8, s) : dispatch_attention<__half>(a, D, q8, s);
+} catch (...) {
+    return fail(SPEC_ERR_CUDA, "spec_tree_attention: a host allocation failed");
+}
