@@ -487,8 +487,8 @@ SPEC_API spec_status spec_adjust_logits(const void *logits, spec_dtype dtype, in
  * i % page_size of every head.  In 8 bits each (token, head) row of D values x has
  * one power of two 2^e, kept as the byte e + 127: with e the least whole number
  * such that max |x| <= 448 * 2^e, -110 <= e <= 120 (in fp16 also e >= -24), the values
- * are x / 2^e rounded to e4m3, to nearest even (fp16 values beyond 63488 are kept as
- * 61440, which fp16 can give back).  A row with an infinity or a NaN has byte 255 and reads as NaN.
+ * are x / 2^e rounded to e4m3, to nearest even (at the type's end, e = 120 and
+ * in fp16 e = 8, at most 240, since 256 * 2^e would be read back as an infinity).  A row with an infinity or a NaN has byte 255 and reads as NaN.
  * Powers of two lose nothing in a floating format and make what is read back exact.
  */
 typedef struct spec_cache {

@@ -768,11 +768,15 @@ def _cache_arg(k_cache, v_cache, page_table, k_scale, v_scale, B, heads, dim, dt
                   SPEC_E4M3 if q8 else _CODES[dtype], pages, page, kv, d, page_table.shape[1])
 
 
-def _token_rows(t, name, shape, dtype, dev, index):
-    """Checks [B, N, heads, dim], whose heads lie together while its tokens may be strided; returns (address, batch and token strides)."""
+def _on_gpu(t, name):
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.get_device() != index:
+
+
+def _token_rows(t, name, shape, dtype, dev):
+    """Checks [B, N, heads, dim], whose heads lie together while its tokens may be strided; returns (address, batch and token strides)."""
+    _on_gpu(t, name)
+    if t.device != dev:
         raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
     if t.dtype is not dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
@@ -790,8 +794,7 @@ def _token_rows(t, name, shape, dtype, dev, index):
 
 
 def _new_tokens(t, name):
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
+    _on_gpu(t, name)
     if t.dim() != 4:
         raise ValueError("%s must be [B, N, heads, head_dim]" % name)
     if t.dtype not in _CODES:
@@ -814,7 +817,7 @@ def spec_cache_append(k, v, k_cache, v_cache, page_table, start, *, count=None, 
     lib = load_library()
     shape, dtype, dev, i = _new_tokens(k, "k")
     B, N, heads, dim = shape
-    at, sk = _token_rows(k, "k", shape, dtype, dev, i), _token_rows(v, "v", shape, dtype, dev, i)
+    at, sk = _token_rows(k, "k", shape, dtype, dev), _token_rows(v, "v", shape, dtype, dev)
     cache = _cache_arg(k_cache, v_cache, page_table, k_scale, v_scale, B, heads, dim, dtype, dev, i)
     if select is not None and select.dim() != 2:
         raise ValueError("select must be [B, S]")
@@ -837,8 +840,7 @@ def spec_cache_read(k_cache, v_cache, page_table, start, n, *, count=None, k_sca
     dict(k, v [B, n, kv_heads, head_dim], status), of the cache's type, or of `dtype` (bfloat16, float16) where the
     cache is float8_e4m3fn.  Rows from count[b] on are left as they were (new ones: 0)."""
     lib = load_library()
-    if not k_cache.is_cuda:
-        raise ValueError("k_cache must be a CUDA tensor")
+    _on_gpu(k_cache, "k_cache")
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages, kv_heads, page_size, head_dim]")
     _, heads, _, dim = k_cache.shape
@@ -890,7 +892,7 @@ def spec_tree_attention(q, k, v, k_cache, v_cache, page_table, context_lens, *, 
     if N < 1 or kv < 1 or heads < 1 or heads % kv:
         raise ValueError("need N >= 1 and heads a multiple of kv_heads, got %d and %d of %d" % (N, heads, kv))
     ks = (B, N, kv, dim)
-    at = [_token_rows(q, "q", qs, dtype, dev, i), _token_rows(k, "k", ks, dtype, dev, i), _token_rows(v, "v", ks, dtype, dev, i)]
+    at = [_token_rows(q, "q", qs, dtype, dev), _token_rows(k, "k", ks, dtype, dev), _token_rows(v, "v", ks, dtype, dev)]
     cache = _cache_arg(k_cache, v_cache, page_table, k_scale, v_scale, B, kv, dim, dtype, dev, i)
     shared_len = int(shared_len)
     args = (_need(context_lens, "context_lens", torch.int32, (B,), dev, i), shared_len, _may(mask, "mask", torch.int32, (N, (N + 31) // 32), dev, i),

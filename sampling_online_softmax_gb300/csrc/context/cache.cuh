@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_append_kernel(const Cache
         const uint32_t bits = __float_as_uint(most);
         const int e = max(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), Elt<T>::kLeastExp);
         const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const float top = Elt<T>::kTopExp >= 0 && e >= Elt<T>::kTopExp ? 240.0f : 448.0f;  // fp16: 2^8 * 256 would not come back
+        const float top = e >= Elt<T>::kTopExp ? 240.0f : 448.0f;  // 256 2^e would not come back
         uint32_t q[2] = {0, 0};
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {

@@ -17,7 +17,7 @@ namespace {
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // The checks that every call on a cache shares; `dtype` is the keys' and values' own.
-spec_status cache_args(CacheView *v, const spec_cache *c, spec_dtype dtype) {
+spec_status cache_args(CacheView *v, const spec_cache *c, spec_dtype dtype, int B) {
     if (dtype != SPEC_BF16 && dtype != SPEC_F16) return fail(SPEC_ERR_INVALID_ARG, "keys and values of dtype %d", (int)dtype);
     if (!c) return fail(SPEC_ERR_INVALID_ARG, "cache is null");
     if (c->dtype != dtype && c->dtype != SPEC_E4M3) return fail(SPEC_ERR_INVALID_ARG, "a cache of dtype %d", (int)c->dtype);
@@ -28,10 +28,10 @@ spec_status cache_args(CacheView *v, const spec_cache *c, spec_dtype dtype) {
     if (1 << bits != c->page_size) return fail(SPEC_ERR_UNSUPPORTED, "page_size = %d: 16, 32, 64, 128 or 256", c->page_size);
     if (c->table_width > INT_MAX >> bits) return fail(SPEC_ERR_UNSUPPORTED, "table_width = %d: positions below 2^31", c->table_width);
     if (c->kv_heads > 1024) return fail(SPEC_ERR_UNSUPPORTED, "kv_heads = %d > 1024", c->kv_heads);
-    if (c->pages && (!c->k || !c->v)) return fail(SPEC_ERR_INVALID_ARG, "the cache's k or v is null");
-    if (c->table_width && !c->page_table) return fail(SPEC_ERR_INVALID_ARG, "page_table is null");
+    if (B > 0 && c->pages && (!c->k || !c->v)) return fail(SPEC_ERR_INVALID_ARG, "the cache's k or v is null");
+    if (B > 0 && c->table_width && !c->page_table) return fail(SPEC_ERR_INVALID_ARG, "page_table is null");
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->page_table, 4)) return fail(SPEC_ERR_INVALID_ARG, "the cache is misaligned");
-    if (c->dtype == SPEC_E4M3 && c->pages && (!c->k_scale || !c->v_scale)) return fail(SPEC_ERR_INVALID_ARG, "an e4m3 cache needs k_scale and v_scale");
+    if (B > 0 && c->dtype == SPEC_E4M3 && c->pages && (!c->k_scale || !c->v_scale)) return fail(SPEC_ERR_INVALID_ARG, "an e4m3 cache needs k_scale and v_scale");
     *v = CacheView{{static_cast<unsigned char *>(c->k), static_cast<unsigned char *>(c->v)}, {c->k_scale, c->v_scale},
                    c->page_table, c->pages, bits, c->kv_heads, c->table_width};
     return SPEC_OK;
@@ -89,7 +89,7 @@ extern "C" spec_status spec_cache_append(const void *k, const void *v, spec_dtyp
                                          const spec_cache *cache, uint32_t *dev_status, void *stream) try {
     g_last_error[0] = '\0';
     CacheRowsArgs a = {};
-    spec_status st = cache_args(&a.cache, cache, dtype);
+    spec_status st = cache_args(&a.cache, cache, dtype, B);
     if (st != SPEC_OK) return st;
     if (B < 0 || N < 0 || S < 0 || (!select && S != N)) return fail(SPEC_ERR_INVALID_ARG, "need B >= 0, N >= 0, S >= 0, and S == N without select");
     if (B == 0 || S == 0) return SPEC_OK;
@@ -119,7 +119,7 @@ extern "C" spec_status spec_cache_read(const spec_cache *cache, int B, int S, co
                                        void *v, spec_dtype dtype, uint32_t *dev_status, void *stream) try {
     g_last_error[0] = '\0';
     CacheRowsArgs a = {};
-    spec_status st = cache_args(&a.cache, cache, dtype);
+    spec_status st = cache_args(&a.cache, cache, dtype, B);
     if (st != SPEC_OK) return st;
     if (B < 0 || S < 0) return fail(SPEC_ERR_INVALID_ARG, "need B >= 0, S >= 0");
     if (B == 0 || S == 0) return SPEC_OK;
@@ -151,7 +151,7 @@ extern "C" spec_status spec_tree_attention(const void *q, const void *k, const v
                                            uint32_t *dev_status, void *workspace, size_t workspace_bytes, void *stream) try {
     g_last_error[0] = '\0';
     AttentionArgs a = {};
-    spec_status st = cache_args(&a.cache, cache, dtype);
+    spec_status st = cache_args(&a.cache, cache, dtype, B);
     if (st != SPEC_OK) return st;
     const int kv = cache->kv_heads, D = cache->head_dim;
     if (B < 0 || N < 1 || heads < 1 || heads % kv) return fail(SPEC_ERR_INVALID_ARG, "need B >= 0, N >= 1, heads a multiple of kv_heads");

@@ -16,7 +16,7 @@ struct Elt;
 template <>
 struct Elt<__nv_bfloat16> {
     static constexpr int kLeastExp = -110;  // of a row's power of two: 2^e and q 2^e stay normal
-    static constexpr int kTopExp = -1;      // no limit (e <= 120)
+    static constexpr int kTopExp = 120;     // where a row's largest q 2^e could be 2^128, past bf16's range
     static __device__ __forceinline__ float2 to_float2(uint32_t x) {
         return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
     }
