@@ -1,77 +1,913 @@
-// attention.cuh -- attention of drafted tokens over the paged cache and their own tree.
+// attention.cuh -- attention of drafted tokens over the paged cache and their own tree, on the
+// fifth-generation tensor cores.
 //
-// One warp a row (b, n, h): it goes over the keys one by one, each lane holding D / 32 values of the
-// query and of the weighted sum, with a running maximum and sum.
+// The rows of a block are (node, query head) pairs that share a key head, so a tile of keys is read
+// once for all of them.  Scores S = Q K^T and weighted sums O += P V are tcgen05 products of 128 rows:
+//   Q, K, V   shared memory, in swizzled rows of 128 bytes (K and V as TMA lays them)
+//   S, O      tensor memory, a row a lane; P, the weights in the element type, over S's columns
+// Two products are under way at once, each with a warpgroup of its own for the softmax: blocks of more
+// than 128 rows have two halves, which share each tile; smaller ones take their tiles in turn, and the
+// two sums are joined at the end.  While one warpgroup computes weights, the other's products run.
+//
+//   warps 0-3, 4-7   softmax of product 0, 1: a thread a row
+//   warps 8-11       loads by plain instructions: Q, the nodes' keys and values, 8-bit tiles widened,
+//                    last tiles of values (what lies behind a sequence's end must be 0: 0 * NaN is NaN)
+//   warp 12          TMA
+//   warp 13          tcgen05.mma
+//
+// The softmax keeps a row's running maximum as it was until a tile's exceeds it by 2^8: weights up to 2^8
+// lose nothing in a float format, and O is rescaled almost never.
 #pragma once
 
-#include "cache.cuh"
+#include <type_traits>
+
 #include "attention.h"
+#include "cache.cuh"
+#include "tensor.cuh"
 
 namespace spec {
 namespace context {
 
-template <typename T, int D, bool Q8>
-__global__ void __launch_bounds__(128) attention_kernel(const AttentionArgs a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= static_cast<long long>(a.B) * a.N * a.heads) return;
-    const int h = static_cast<int>(row % a.heads), n = static_cast<int>(row / a.heads % a.N), b = static_cast<int>(row / a.heads / a.N);
-    const int g = h / (a.heads / a.cache.kv_heads);
-    int len = __ldg(a.lens + b);
-    if (len < 0) return;
-    bool bad_page = false;
-    if (len < a.shared_len || len > a.cache.table_width << a.cache.page_bits) {
-        if (lane == 0) atomicOr(a.status, SPEC_DEV_BAD_LENGTH);
-        len = min(max(len, a.shared_len), a.cache.table_width << a.cache.page_bits);
-    }
-    float q[E], o[E], m = -INFINITY, l = 0.0f;
-    const T *qr = reinterpret_cast<const T *>(a.q) + b * a.stride[0] + n * a.stride[1] + static_cast<size_t>(h) * D + lane * E;
-    for (int e = 0; e < E; ++e) q[e] = static_cast<float>(qr[e]) * a.scale, o[e] = 0.0f;
-    auto key = [&](const float *k, const float *v) {
-        float s = 0.0f;
-        for (int e = 0; e < E; ++e) s += q[e] * k[e];
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        const float top = fmaxf(m, s);
-        const float was = m == -INFINITY ? 0.0f : expf(m - top), p = s == -INFINITY ? 0.0f : expf(s - top);
-        l = l * was + p;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * was + p * v[e];
-        m = top;
-    };
-    for (int j = 0; j < len; ++j) {
-        const int owner = j < a.shared_len ? 0 : b;
-        const int page = __ldg(a.cache.table + static_cast<size_t>(owner) * a.cache.table_width + (j >> a.cache.page_bits));
-        if (page < 0 || page >= a.cache.pages) {
-            bad_page = true;
-            continue;
+constexpr int kAttentionThreads = 512;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+template <int D, bool Q8>
+struct Layout {
+    static constexpr int kQ = kTile * D * 2;     // bytes of 128 rows of queries, keys or values
+    static constexpr int kRing = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    static constexpr int kStage = Q8 ? kTile * D : 0;
+    static constexpr int kStages = Q8 ? (D == 128 ? 4 : 8) : 0;
+    static constexpr int kBytes = 2 * kQ + kRing * kQ + kStages * kStage;
+};
+
+struct Control {  // behind the tiles in shared memory
+    uint64_t full[8], empty[8];    // ring of tiles
+    uint64_t staged[8], free_[8];  // ring of 8-bit tiles
+    uint64_t q_full[2], q_empty[2];
+    uint64_t scores[2], weights[2], sums[2];  // of the two products
+    uint64_t joined[2];            // both warpgroups: statistics there, sums read
+    uint64_t drained;
+    uint32_t tmem;
+    int gave_up;
+    int odd[8];                    // a value of the piece's nodes is not finite (by piece, in turn)
+    int scan[16];
+    int total, b, before;          // tiles in all; the sequence a CTA begins in and the tiles before it
+    float2 stats[2][kTile];
+};
+
+// A CTA's pieces of the list, in order.
+struct Piece {
+    bool shared, two;    // of the prefix; two products a tile
+    int b, g, first, rows;
+    int t0, t1, tiles;   // the piece's tiles, of the block's
+    int len, context;    // own: the sequence's length, its context's tiles
+};
+
+struct Walk {
+    const AttentionArgs &a;
+    int left, item, t, b, tiles, context, len, per_seq, shared_items, shared_tiles;
+    bool shared;
+
+    __device__ Walk(const AttentionArgs &a_, const Control *c) : a(a_) {
+        const int lo = static_cast<int>(static_cast<long long>(blockIdx.x) * c->total / a.ctas);
+        left = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * c->total / a.ctas) - lo;
+        shared_tiles = tiles_of(a.shared_len);
+        shared_items = shared_tiles ? a.cache.kv_heads * a.shared_blocks : 0;
+        per_seq = a.cache.kv_heads * a.blocks;
+        b = -1;
+        shared = lo < shared_items * shared_tiles;
+        if (shared) {
+            item = lo / shared_tiles;
+            t = lo % shared_tiles;
+        } else if (left > 0) {
+            sequence(c->b);
+            item = (lo - c->before) / tiles;
+            t = (lo - c->before) % tiles;
         }
-        const size_t at = cache_row(a.cache, (static_cast<long long>(page) << a.cache.page_bits) + (j & ((1 << a.cache.page_bits) - 1)), g);
-        float x[2][E];
-        for (int w = 0; w < 2; ++w) {
-            const float s = Q8 ? scale_of(a.cache.scale[w][at]) : 1.0f;
-            for (int e = 0; e < E; ++e) {
-                if (Q8) x[w][e] = Elt<T>::clamp(e4m3x2(a.cache.data[w][at * D + lane * E + e]).x * s);
-                else x[w][e] = static_cast<float>(reinterpret_cast<const T *>(a.cache.data[w])[at * D + lane * E + e]);
+    }
+    __device__ void sequence(int to) {
+        b = to;
+        const int room = a.cache.table_width << a.cache.page_bits;
+        len = __ldg(a.lens + b);
+        if (len >= 0) len = min(max(len, a.shared_len), room);
+        context = len > a.shared_len ? tiles_of(len) - a.shared_len / kTile : 0;
+        tiles = len < 0 ? 0 : context + tiles_of(a.N);
+        item = 0;
+    }
+    __device__ bool next(Piece *p) {
+        if (left <= 0) return false;
+        if (shared && item == shared_items) shared = false;
+        if (!shared)
+            while (b < 0 || tiles == 0 || item == per_seq) sequence(b + 1);
+        const int blocks = shared ? a.shared_blocks : a.blocks, rows = shared ? a.shared_rows : a.block_rows;
+        const int all = shared ? a.B * a.N * a.group : a.N * a.group;
+        const int block = item % blocks;
+        p->shared = shared;
+        p->two = rows > kTile;
+        p->b = shared ? 0 : b;
+        p->g = item / blocks;
+        p->first = block * rows;
+        p->rows = min(rows, all - p->first);
+        p->tiles = shared ? shared_tiles : tiles;
+        p->t0 = t;
+        p->t1 = min(p->tiles, t + left);
+        p->len = shared ? a.shared_len : len;
+        p->context = shared ? shared_tiles : context;
+        left -= p->t1 - p->t0;
+        t = p->t1;
+        if (t == p->tiles) {
+            t = 0;
+            ++item;
+        }
+        return true;
+    }
+};
+
+// A ring's next slot, and the parity of its round.
+struct Cursor {
+    int slot = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void step(int n) {
+        if (++slot == n) {
+            slot = 0;
+            round ^= 1;
+        }
+    }
+};
+
+// The row of the batch that row `r` (of all the rows of piece p's kind) is.
+struct RowId {
+    int b, n, h;
+};
+__device__ __forceinline__ RowId row_id(const AttentionArgs &a, const Piece &p, int r) {
+    const int i = (p.first + r) / a.group, h = (p.first + r) % a.group;
+    return RowId{p.shared ? i / a.N : p.b, p.shared ? i % a.N : i, p.g * a.group + h};
+}
+
+// Sixteen e4m3 values, times 2^(byte - 127), as 16 elements.
+template <typename T>
+struct Widen;
+template <>
+struct Widen<__nv_bfloat16> {
+    uint32_t m1, m2;
+    bool twice;
+    // An e4m3 value's bits, moved into bf16's places, read as 2^-120 of it (subnormal ones too), so
+    // it is a product with 2^(120 + e), in two steps where that is past bf16.
+    __device__ __forceinline__ void scale(uint32_t byte) {
+        const int e = static_cast<int>(byte) - 127, e1 = min(e + 120, 127);
+        uint32_t s1 = static_cast<uint32_t>(max(e1 + 127, 1)) << 7;
+        const uint32_t s2 = static_cast<uint32_t>(127 + e + 120 - e1) << 7;
+        if (byte == 255) s1 = 0x7fff;
+        m1 = s1 | s1 << 16;
+        m2 = s2 | s2 << 16;
+        twice = e > 7;
+    }
+    __device__ __forceinline__ void zero() { m1 = 0, twice = false; }
+    static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    __device__ __forceinline__ uint2 four(uint32_t w) const {
+        const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+        uint32_t x = times((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), m1), y = times((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), m1);
+        if (twice) x = times(x, m2), y = times(y, m2);
+        return make_uint2(x, y);
+    }
+};
+template <>
+struct Widen<__half> {
+    uint32_t m;
+    __device__ __forceinline__ void scale(uint32_t byte) {
+        const int e = min(max(static_cast<int>(byte) - 127, -24), 15);
+        uint32_t s = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 1u << (e + 24);
+        if (byte == 255) s = 0x7fff;
+        m = s | s << 16;
+    }
+    __device__ __forceinline__ void zero() { m = 0; }
+    static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    __device__ __forceinline__ uint2 four(uint32_t w) const {
+        const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffff), __NV_E4M3);
+        const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
+        return make_uint2(times(*reinterpret_cast<const uint32_t *>(&x), m), times(*reinterpret_cast<const uint32_t *>(&y), m));
+    }
+};
+
+// Where a tile's 16-byte chunk c of row r lies: 64 columns (8 chunks) a sub-tile of 128 rows, swizzled.
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return static_cast<uint32_t>((c >> 3) * (kTile * 128) + r * 128 + ((c & 7) ^ (r & 7)) * 16);
+}
+__device__ __forceinline__ void store16(uint32_t at, const uint4 &x) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+__device__ __forceinline__ uint4 load16(uint32_t at) {
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at) : "memory");
+    return x;
+}
+
+// Packed fp32 arithmetic.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)), "l"(*reinterpret_cast<uint64_t *>(&c)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
+// ------------------------------------------------------------------ the four kinds of warps
+template <typename T, int D, bool Q8>
+struct Attention {
+    using L = Layout<D, Q8>;
+    static constexpr bool kHalf = std::is_same<T, __half>::value;
+    static constexpr uint32_t kType = kHalf ? 0 : 1;
+    static constexpr uint32_t kScoresInstr = instruction(kType, kTile, false), kSumsInstr = instruction(kType, D, true);
+    static constexpr uint32_t kScores = 0, kSums = 256;  // columns of tensor memory; 128 a product
+    // fp16 weights: up to 2^15 instead of 2^8, since they stop at 2^-25
+    static constexpr float kShift = kHalf ? 7.0f : 0.0f;
+
+    const AttentionArgs &a;
+    Control *c;
+    uint32_t tiles, stages;  // shared-memory addresses: queries, then the ring; 8-bit tiles
+    int lane, warp;
+
+    __device__ __forceinline__ bool wait(const uint64_t *bar, uint32_t parity) {
+        return wait_phase(ptx::smem_addr(bar), parity, &c->gave_up, a.status);
+    }
+    __device__ __forceinline__ uint32_t ring(int slot) const { return tiles + 2 * L::kQ + slot * L::kQ; }
+    // Whether entry (tile t of piece p; keys or values) comes by TMA straight into the ring.
+    __device__ __forceinline__ bool by_tma(const Piece &p, int t, bool values) const {
+        if (Q8 || t >= p.context) return false;
+        return !values || (first_tile(p) + t + 1) * kTile <= p.len;
+    }
+    __device__ __forceinline__ int first_tile(const Piece &p) const { return p.shared ? 0 : a.shared_len / kTile; }
+    __device__ __forceinline__ int begin(const Piece &p) const { return p.shared ? 0 : a.shared_len; }  // the piece's first position
+
+    // ---- TMA
+    __device__ void load_tiles(const CUtensorMap *k_map, const CUtensorMap *v_map) {
+        Walk walk(a, c);
+        Piece p;
+        Cursor at;
+        // tiles that one block takes are read once; where several blocks take them, L2 may keep them
+        const uint64_t first = ptx::policy_evict_first(), normal = policy_evict_normal();
+        const int box = min(1 << a.cache.page_bits, kTile), boxes = kTile / box;
+        bool bad = false, ok = true;
+        Cursor last = at;
+        int issued = 0;
+        const int slots = Q8 ? L::kStages : L::kRing;
+        while (ok && walk.next(&p)) {
+            const int32_t *table = a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width;
+            const uint64_t policy = (p.shared ? a.shared_blocks : a.blocks) == 1 ? first : normal;
+            for (int t = p.t0; ok && t < p.t1; ++t) {
+                // lane i: the tile's i-th box of keys
+                const long long pos = static_cast<long long>(first_tile(p) + t) * kTile + lane * box;
+                int page = a.cache.pages;  // outside: zeros
+                if (t < p.context && lane < boxes && pos < p.len && pos + box > begin(p)) {
+                    const int entry = __ldg(table + (pos >> a.cache.page_bits));
+                    if (entry < 0 || entry >= a.cache.pages) bad = true;
+                    else page = entry;
+                }
+                for (int w = 0; w < 2; ++w) {
+                    const bool mine = Q8 ? t < p.context : by_tma(p, t, w);
+                    if (!Q8 && !mine) at.step(slots);
+                    if (!mine) continue;
+                    const uint64_t *full = Q8 ? &c->staged[at.slot] : &c->full[at.slot], *empty = Q8 ? &c->free_[at.slot] : &c->empty[at.slot];
+                    if (!(ok = wait(empty, at.round ^ 1))) break;
+                    const uint32_t bar = ptx::smem_addr(full), to = Q8 ? stages + at.slot * L::kStage : ring(at.slot);
+                    if (lane == 0) {
+                        if (!Q8) arrive(bar, 3);
+                        ptx::mbar_arrive_expect_tx(bar, Q8 ? L::kStage : L::kQ);
+                    }
+                    __syncwarp();
+                    if (lane < boxes) {
+                        const int y = (p.g << a.cache.page_bits) + static_cast<int>(pos & ((1 << a.cache.page_bits) - 1));
+                        if (Q8) tma_load3(to + lane * box * D, w ? v_map : k_map, 0, y, page, bar, policy);
+                        else
+                            for (int x = 0; x < D; x += 64) tma_load3(to + (x / 64) * (kTile * 128) + lane * box * 128, w ? v_map : k_map, x, y, page, bar, policy);
+                    }
+                    last = at;
+                    ++issued;
+                    at.step(slots);
+                }
             }
         }
-        key(x[0], x[1]);
-    }
-    const int words = (a.N + 31) / 32;
-    for (int j = 0; j < a.N; ++j) {
-        const bool on = a.mask ? (a.mask[static_cast<size_t>(n) * words + (j >> 5)] >> (j & 31)) & 1 : j <= n;
-        if (!on) continue;
-        float x[2][E];
-        for (int e = 0; e < E; ++e) {
-            x[0][e] = static_cast<float>((reinterpret_cast<const T *>(a.k) + b * a.stride[2] + j * a.stride[3] + static_cast<size_t>(g) * D)[lane * E + e]);
-            x[1][e] = static_cast<float>((reinterpret_cast<const T *>(a.v) + b * a.stride[4] + j * a.stride[5] + static_cast<size_t>(g) * D)[lane * E + e]);
+        if (bad) atomicOr(a.status, SPEC_DEV_BAD_PAGE);
+        // No copy is in flight when the CTA ends: where a wait gave up, each slot's last one is waited for.
+        if (!ok) {
+            for (int i = 0; i < min(issued, slots); ++i) {
+                const uint32_t bar = ptx::smem_addr(Q8 ? &c->staged[last.slot] : &c->full[last.slot]);
+                bool done = false;
+                for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(bar, last.round);
+                if (last.slot-- == 0) {
+                    last.slot = slots - 1;
+                    last.round ^= 1;
+                }
+            }
         }
-        key(x[0], x[1]);
     }
-    if (bad_page && lane == 0) atomicOr(a.status, SPEC_DEV_BAD_PAGE);
-    T *out = reinterpret_cast<T *>(a.out) + row * D + lane * E;
+
+    // ---- tcgen05.mma
+    struct Pending {
+        bool any, add, release, final;
+        int slot;
+        uint32_t round;
+    };
+    __device__ bool add_values(Pending &w, int s, uint32_t &weights_round) {
+        w.any = false;
+        if (!wait(&c->full[w.slot], w.round) || !wait(&c->weights[s], weights_round)) return false;
+        weights_round ^= 1;
+        fence_after();
+        if (lane == 0) {
+            const uint32_t v = ring(w.slot), d = c->tmem + kSums + s * 128, p = c->tmem + kScores + s * 128;
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k) mma_tmem(d, p + k * 8, operand(v + k * 16 * 128, kTile * 128), kSumsInstr, w.add || k > 0);
+            if (w.release) mma_commit(ptx::smem_addr(&c->empty[w.slot]));
+            if (w.final) mma_commit(ptx::smem_addr(&c->sums[s]));
+        }
+        __syncwarp();
+        return true;
+    }
+    __device__ void multiply() {
+        Walk walk(a, c);
+        Piece p;
+        Cursor at;
+        Pending pending[2] = {};
+        uint32_t weights_round[2] = {0, 0}, q_round[2] = {0, 0};
+        int half = 0;
+        bool ok = true;
+        while (ok && walk.next(&p)) {
+            const int n = p.t1 - p.t0;
+            if (p.two) half = 0;
+            for (int h = 0; ok && h < 2; ++h)
+                if (p.two || h == half) {
+                    ok = wait(&c->q_full[h], q_round[h]);
+                    q_round[h] ^= 1;
+                }
+            for (int i = 0; ok && i < n; ++i) {
+                const Cursor keys = at;
+                at.step(L::kRing);
+                const Cursor values = at;
+                at.step(L::kRing);
+                for (int x = 0; ok && x < (p.two ? 2 : 1); ++x) {
+                    const int s = p.two ? x : i & 1;
+                    if (pending[s].any && !(ok = add_values(pending[s], s, weights_round[s]))) break;
+                    if (x == 0 && !(ok = wait(&c->full[keys.slot], keys.round))) break;
+                    fence_after();
+                    if (lane == 0) {
+                        const uint32_t q = tiles + (p.two ? x : half) * L::kQ, k = ring(keys.slot), d = c->tmem + kScores + s * 128;
+#pragma unroll
+                        for (int e = 0; e < D / 16; ++e) {
+                            const uint32_t off = (e / 4) * (kTile * 128) + (e % 4) * 32;
+                            mma(d, operand(q + off, 16), operand(k + off, 16), kScoresInstr, e > 0);
+                        }
+                        mma_commit(ptx::smem_addr(&c->scores[s]));
+                        if (x == (p.two ? 1 : 0)) mma_commit(ptx::smem_addr(&c->empty[keys.slot]));
+                        if (i == n - 1) {
+                            if (p.two) mma_commit(ptx::smem_addr(&c->q_empty[x]));
+                            else mma_commit(ptx::smem_addr(&c->q_empty[half]));
+                        }
+                    }
+                    __syncwarp();
+                    pending[s] = Pending{true, p.two ? i > 0 : i > 1, !p.two || x == 1, p.two ? i == n - 1 : i >= n - 2, values.slot, values.round};
+                }
+            }
+            // the piece's last weights: the earlier product's first
+            for (int x = 0; ok && x < 2; ++x) {
+                const int s = p.two ? x : (n + x) & 1;
+                if (pending[s].any) ok = add_values(pending[s], s, weights_round[s]);
+            }
+            if (!p.two) half ^= 1;
+        }
+        // Every product done before tensor memory is freed, also where a wait gave up.
+        if (lane == 0) mma_commit(ptx::smem_addr(&c->drained));
+        __syncwarp();
+        bool done = false;
+        for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(ptx::smem_addr(&c->drained), 0);
+    }
+
+    // ---- plain loads: a row of D elements by D / 8 lanes
+    // Rows of queries; those the block lacks are 0.
+    __device__ void load_queries(const Piece &p, int half, int from, int tid) {
+        constexpr int kLanes = D / 8;
+#pragma unroll 4
+        for (int i = tid; i < kTile * kLanes; i += 128) {
+            const int r = i / kLanes, x = i % kLanes;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (from + r < p.rows) {
+                const RowId id = row_id(a, p, from + r);
+                v = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(a.q) + id.b * a.stride[0] + id.n * a.stride[1] + id.h * D) + x);
+            }
+            store16(tiles + half * L::kQ + chunk_at(r, x), v);
+        }
+    }
+    __device__ __forceinline__ static bool odd_pair(uint32_t x) {  // an infinity or NaN among two elements
+        constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
+        return (x & e) == e || (x >> 16 & e) == e;
+    }
+    // Keys or values of the nodes; rows past the last are 0, and so are values that are not finite: a row
+    // that does not see them would get 0 * NaN.  Those that do are given them at the end.
+    __device__ bool load_nodes(const Piece &p, int t, bool values, uint32_t to, int tid) {
+        constexpr int kLanes = D / 8;
+        const int m0 = (t - p.context) * kTile;
+        const T *src = reinterpret_cast<const T *>(values ? a.v : a.k) + p.b * a.stride[values ? 4 : 2] + p.g * D;
+        const long long step = a.stride[values ? 5 : 3];
+        bool odd = false;
+#pragma unroll 4
+        for (int i = tid; i < kTile * kLanes; i += 128) {
+            const int r = i / kLanes, x = i % kLanes;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (m0 + r < a.N) v = __ldg(reinterpret_cast<const uint4 *>(src + (m0 + r) * step) + x);
+            if (values && (odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w))) {
+                odd = true;
+                uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+                constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if ((w[k] & e) == e) w[k] &= 0xffff0000u;
+                    if ((w[k] >> 16 & e) == e) w[k] &= 0xffffu;
+                }
+            }
+            store16(to + chunk_at(r, x), v);
+        }
+        return odd;
+    }
+    // A last tile of values of the cache, 0 from the sequence's end on.
+    __device__ void load_last_values(const Piece &p, int t, uint32_t to, int tid) {
+        constexpr int kLanes = D / 8;
+        const int32_t *table = a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width;
+#pragma unroll 4
+        for (int i = tid; i < kTile * kLanes; i += 128) {
+            const int r = i / kLanes, x = i % kLanes;
+            const int pos = (first_tile(p) + t) * kTile + r;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (pos < p.len && pos >= begin(p)) {
+                const int page = __ldg(table + (pos >> a.cache.page_bits));
+                if (page >= 0 && page < a.cache.pages) {
+                    const size_t row = cache_row(a.cache, (static_cast<long long>(page) << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1)), p.g);
+                    v = __ldg(reinterpret_cast<const uint4 *>(a.cache.data[1] + row * D * 2) + x);
+                }
+            }
+            store16(to + chunk_at(r, x), v);
+        }
+    }
+    // An 8-bit tile, widened: a thread a row; the chunks in turned order, so that eight rows' meet different banks.
+    __device__ void widen(uint32_t from, uint32_t to, int r, const Widen<T> &w) {
+        constexpr int kChunks = D / 16;
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j) {
+            const int x = D == 128 ? (j + r) & 7 : (j + (r >> 1)) & 3;
+            const uint4 v = load16(from + r * D + x * 16);
+            const uint2 b0 = w.four(v.x), b1 = w.four(v.y), b2 = w.four(v.z), b3 = w.four(v.w);
+            store16(to + chunk_at(r, 2 * x), make_uint4(b0.x, b0.y, b1.x, b1.y));
+            store16(to + chunk_at(r, 2 * x + 1), make_uint4(b2.x, b2.y, b3.x, b3.y));
+        }
+    }
+    __device__ void load_rows(int tid) {
+        Walk walk(a, c);
+        Piece p;
+        Cursor at, staged;
+        uint32_t q_round[2] = {0, 0};
+        int half = 0, count = 0;
+        bool ok = true;
+        while (ok && walk.next(&p)) {
+            if (p.two) half = 0;
+            for (int h = 0; ok && h < 2; ++h) {
+                if (!p.two && h != half) continue;
+                if (!(ok = wait(&c->q_empty[h], q_round[h] ^ 1))) break;
+                q_round[h] ^= 1;
+                // (the piece four on: none is read that far back, nor loaded that far ahead)
+                if (tid == 0) *const_cast<volatile int *>(&c->odd[(count + 4) & 7]) = 0;
+                load_queries(p, h, p.two ? h * kTile : 0, tid);
+                fence_async();
+                __syncwarp();
+                if (lane == 0) arrive(ptx::smem_addr(&c->q_full[h]));
+            }
+            for (int t = p.t0; ok && t < p.t1; ++t) {
+                uint32_t byte[2] = {0, 0};
+                bool live = false;
+                if (Q8 && t < p.context) {  // this thread's row: the scales of its keys and values
+                    const int pos = (first_tile(p) + t) * kTile + tid;
+                    if (pos < p.len && pos >= begin(p)) {
+                        const int page = __ldg(a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width + (pos >> a.cache.page_bits));
+                        if (page >= 0 && page < a.cache.pages) {
+                            const size_t row = cache_row(a.cache, (static_cast<long long>(page) << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1)), p.g);
+                            byte[0] = __ldg(a.cache.scale[0] + row);
+                            byte[1] = __ldg(a.cache.scale[1] + row);
+                            live = true;
+                        }
+                    }
+                }
+                for (int w = 0; ok && w < 2; ++w, at.step(L::kRing)) {
+                    if (by_tma(p, t, w)) continue;
+                    if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
+                    const uint32_t to = ring(at.slot);
+                    if (t >= p.context) {
+                        if (load_nodes(p, t, w, to, tid)) *const_cast<volatile int *>(&c->odd[count & 7]) = 1;
+                    } else if (!Q8) {
+                        load_last_values(p, t, to, tid);
+                    } else {
+                        if (!(ok = wait(&c->staged[staged.slot], staged.round))) break;
+                        Widen<T> x;
+                        if (live) x.scale(byte[w]);
+                        else x.zero();
+                        widen(stages + staged.slot * L::kStage, to, tid, x);
+                        __syncwarp();
+                        if (lane == 0) arrive(ptx::smem_addr(&c->free_[staged.slot]));
+                        staged.step(L::kStages > 0 ? L::kStages : 1);
+                    }
+                    fence_async();
+                    __syncwarp();
+                    if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
+                }
+            }
+            ++count;
+            if (!p.two) half ^= 1;
+        }
+    }
+
+    // ---- softmax
+    // The 128 columns of a tile that row `r` does not see are masked; `words`: a bit a column.
+    __device__ void seen_words(const Piece &p, int t, int n, uint32_t (&words)[4]) const {
+        if (t < p.context) {
+            const int base = (first_tile(p) + t) * kTile;
+            const int lo = p.shared ? 0 : max(0, a.shared_len - base), hi = min(kTile, p.len - base);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int from = min(max(lo - 32 * k, 0), 32), to = min(max(hi - 32 * k, 0), 32);
+                const uint32_t below_to = to == 32 ? ~0u : (1u << to) - 1, below_from = from == 32 ? ~0u : (1u << from) - 1;
+                words[k] = below_to & ~below_from;
+            }
+            return;
+        }
+        const int m0 = (t - p.context) * kTile, all = (a.N + 31) / 32;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int m = m0 + 32 * k;
+            uint32_t w = 0;
+            if (m < a.N) {
+                if (a.mask) w = __ldg(a.mask + static_cast<size_t>(n) * all + m / 32);
+                else if (n >= m) w = n - m >= 31 ? ~0u : (2u << (n - m)) - 1;
+                if (a.N - m < 32) w &= (1u << (a.N - m)) - 1;
+            }
+            words[k] = w;
+        }
+    }
+    template <bool MASKED>
+    __device__ void tile_weights(uint32_t s_at, uint32_t o_at, const uint32_t (&words)[4], float scale, bool first, float &m, float &l) {
+        uint32_t x[32];
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            tmem_load32(x, s_at + 32 * k);
+            wait_loads();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const float v = __uint_as_float(x[j]);
+                top = fmaxf(top, MASKED && !((words[k] >> j) & 1) ? -INFINITY : v);
+            }
+        }
+        top = top * scale;
+        // `m` is what the exponents subtract; -inf while the row has seen nothing
+        const float want = top - kShift;
+        const bool moves = m == -INFINITY ? want > -INFINITY : want > m + 8.0f;
+        if (__any_sync(0xffffffffu, moves)) {
+            const float f = moves ? (m == -INFINITY ? 0.0f : ptx::ex2(m - want)) : 1.0f;
+            l *= f;
+            if (moves) m = want;
+            if (!first) {
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    tmem_load32(x, o_at + k);
+                    wait_loads();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+                    tmem_store32(o_at + k, x);
+                }
+                wait_stores();
+            }
+        }
+        const float sub = m == -INFINITY ? 0.0f : -m;
+        const float2 c2 = make_float2(scale, scale), s2 = make_float2(sub, sub);
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            tmem_load32(x, s_at + 32 * k);
+            wait_loads();
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+                float2 e = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), c2, s2);
+                e.x = ptx::ex2(e.x);
+                e.y = ptx::ex2(e.y);
+                if (MASKED) {
+                    if (!((words[k] >> j) & 1)) e.x = 0.0f;
+                    if (!((words[k] >> (j + 1)) & 1)) e.y = 0.0f;
+                }
+                sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
+                w[j / 2] = Elt<T>::from_float2(e.x, e.y);
+            }
+            tmem_store16(s_at + 16 * k, w);
+        }
+        const float2 both = add2(sum[0], sum[1]);
+        l += both.x + both.y;
+        wait_stores();
+    }
+    // Rows of a piece that see a value of a node which is not finite get it: 32 columns from column d0.
+    __device__ void add_odd(const Piece &p, const RowId &id, int d0, uint32_t (&x)[32]) const {
+        for (int t = max(p.t0, p.context); t < p.t1; ++t) {
+            uint32_t words[4];
+            seen_words(p, t, id.n, words);
+            for (int k = 0; k < 4; ++k)
+                for (uint32_t w = words[k]; w; w &= w - 1) {
+                    const int node = (t - p.context) * kTile + 32 * k + __ffs(w) - 1;
+                    const T *v = reinterpret_cast<const T *>(a.v) + p.b * a.stride[4] + node * a.stride[5] + p.g * D + d0;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float y = static_cast<float>(v[j]);
+                        if (!isfinite(y)) x[j] = __float_as_uint(__uint_as_float(x[j]) + y);
+                    }
+                }
+        }
+    }
+    // Columns [d0, d1) of the block's row r: f0 * product 0's sums + f1 * product 1's, to where the piece's go.
+    __device__ void write_sums(const Piece &p, int r, int d0, int d1, bool use0, bool use1, float f0, float f1, float m, float l, bool odd) {
+        const uint32_t lanes = c->tmem + (static_cast<uint32_t>(warp & 3) << 21) + kSums;
+        const bool live = r < p.rows;
+        const RowId id = row_id(a, p, live ? r : 0);
+        const size_t row = (static_cast<size_t>(id.b) * a.N + id.n) * a.heads + id.h;
+        const bool whole = p.t0 == 0 && p.t1 == p.tiles;
+        const bool final = whole && a.shared_len == 0;
+        float *to = nullptr;
+        if (!final) {
+            float2 *stats;
+            if (whole) {
+                const size_t i = (p.shared ? static_cast<size_t>(a.B) * a.N * a.heads : 0) + row;
+                to = a.row_sums + i * D;
+                stats = a.row_stats + i;
+            } else {
+                const size_t i = (static_cast<size_t>(blockIdx.x) * 2 + (p.t0 == 0 ? 1 : 0)) * kBlockRows + r;
+                to = a.cut_sums + i * D;
+                stats = a.cut_stats + i;
+            }
+            if (live && d0 == 0) *stats = make_float2(m, l);
+        } else if (live && d0 == 0 && a.lse) {
+            a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+        }
+        const float inv = final ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+        for (int d = d0; d < d1; d += 32) {
+            uint32_t x[32], y[32];
+            if (use0) {
+                tmem_load32(x, lanes + d);
+                wait_loads();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f0);
+            }
+            if (use1) {
+                tmem_load32(y, lanes + 128 + d);
+                wait_loads();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(use0 ? fmaf(__uint_as_float(y[j]), f1, __uint_as_float(x[j])) : __uint_as_float(y[j]) * f1);
+            }
+            if (live && odd) add_odd(p, id, d, x);
+            if (live && final) {
+                uint4 *out = reinterpret_cast<uint4 *>(a.out + (row * D + d) * 2);
+#pragma unroll
+                for (int j = 0; j < 32; j += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[j + e]) * inv;
+                    out[j / 8] = pack8<T>(v);
+                }
+            } else if (live) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                    *reinterpret_cast<float4 *>(to + d + j) =
+                        make_float4(__uint_as_float(x[j]), __uint_as_float(x[j + 1]), __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+            }
+            __syncwarp();  // (the next load takes the whole warp)
+        }
+    }
+    __device__ void softmax(int s, int tid) {
+        Walk walk(a, c);
+        Piece p;
+        uint32_t scores_round = 0, sums_round = 0, joined_round = 0;
+        int count = 0;
+        bool ok = true;
+        const float scale = a.scale * kLog2e;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, at bit 16
+        while (ok && walk.next(&p)) {
+            const uint32_t s_at = c->tmem + lanes + kScores + s * 128, o_at = c->tmem + lanes + kSums + s * 128;
+            const int r = tid + (p.two ? s * kTile : 0);  // this thread's row of the block
+            const bool idle = (r & ~31) >= p.rows;        // the warp has none
+            const int n = row_id(a, p, min(r, p.rows - 1)).n;
+            float m = -INFINITY, l = 0.0f;
+            bool first = true;
+            for (int t = p.t0 + (p.two ? 0 : s); t < p.t1; t += p.two ? 1 : 2) {
+                if (!(ok = wait(&c->scores[s], scores_round))) break;
+                scores_round ^= 1;
+                fence_after();
+                if (!idle) {
+                    const int base = (first_tile(p) + t) * kTile;
+                    const bool masked = t >= p.context || base + kTile > p.len || (!p.shared && base < a.shared_len);
+                    uint32_t words[4];
+                    if (masked) {
+                        seen_words(p, t, n, words);
+                        tile_weights<true>(s_at, o_at, words, scale, first, m, l);
+                    } else {
+                        tile_weights<false>(s_at, o_at, words, scale, first, m, l);
+                    }
+                }
+                first = false;
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(ptx::smem_addr(&c->weights[s]));
+            }
+            if (!ok) break;
+            const int any = p.two ? 2 : min(2, p.t1 - p.t0);  // products with sums
+            if (p.two || s < any) {
+                if (!(ok = wait(&c->sums[s], sums_round))) break;
+                sums_round ^= 1;
+                fence_after();
+            }
+            const bool odd = *const_cast<volatile int *>(&c->odd[count & 7]) != 0 && !p.shared && p.t1 > p.context;
+            if (p.two) {
+                if (!idle) write_sums(p, r, 0, D, s == 0, s == 1, 1.0f, 1.0f, m, l, odd);
+                fence_before();
+            } else {
+                // Both products' sums: each warpgroup writes half the columns.
+                c->stats[s][tid] = make_float2(m, l);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(ptx::smem_addr(&c->joined[0]));
+                if (!(ok = wait(&c->joined[0], joined_round))) break;
+                fence_after();
+                const float2 x = c->stats[0][tid], y = any == 2 ? c->stats[1][tid] : make_float2(-INFINITY, 0.0f);
+                const float top = fmaxf(x.x, y.x);
+                const float f0 = x.x == -INFINITY ? 0.0f : ptx::ex2(x.x - top), f1 = y.x == -INFINITY ? 0.0f : ptx::ex2(y.x - top);
+                if (!idle) write_sums(p, tid, s * (D / 2), (s + 1) * (D / 2), true, any == 2, f0, f1, top, x.y * f0 + y.y * f1, odd);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) arrive(ptx::smem_addr(&c->joined[1]));
+                if (!(ok = wait(&c->joined[1], joined_round))) break;
+                joined_round ^= 1;
+                fence_after();
+            }
+            ++count;
+        }
+    }
+};
+
+template <typename T, int D, bool Q8>
+__global__ void __launch_bounds__(kAttentionThreads, 1)
+    attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using L = Layout<D, Q8>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    Control *c = reinterpret_cast<Control *>(smem + L::kBytes);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // Every CTA counts the tiles before each sequence: a thread some sequences, then a scan over threads.
+    const int per = (a.B + kAttentionThreads - 1) / kAttentionThreads;
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    const int room = a.cache.table_width << a.cache.page_bits, nodes = tiles_of(a.N), per_seq = a.cache.kv_heads * a.blocks;
+    const int shared_tiles = tiles_of(a.shared_len) * a.cache.kv_heads * a.shared_blocks;
+    int mine = 0;
+    bool bad = false;
+    const auto tiles = [&](int b) {
+        int len = __ldg(a.lens + b);
+        if (len < 0) return 0;
+        bad |= len < a.shared_len || len > room;
+        len = min(max(len, a.shared_len), room);
+        return ((len > a.shared_len ? tiles_of(len) - a.shared_len / kTile : 0) + nodes) * per_seq;
+    };
+    for (int b = b0; b < b1; ++b) mine += tiles(b);
+    if (bad && blockIdx.x == 0) atomicOr(a.status, SPEC_DEV_BAD_LENGTH);
+    int sum = mine;
+    for (int x = 1; x < 32; x *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, x);
+        if (lane >= x) sum += y;
+    }
+    if (lane == 31) c->scan[warp] = sum;
+    if (tid == 0) {
+        c->gave_up = 0;
+        for (int i = 0; i < 8; ++i) c->odd[i] = 0;
+        for (int i = 0; i < 8; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&c->full[i]), 4);
+            ptx::mbar_init(ptx::smem_addr(&c->empty[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&c->staged[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&c->free_[i]), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&c->q_full[i]), 4);
+            ptx::mbar_init(ptx::smem_addr(&c->q_empty[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&c->scores[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&c->weights[i]), 4);
+            ptx::mbar_init(ptx::smem_addr(&c->sums[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&c->joined[i]), 8);
+        }
+        ptx::mbar_init(ptx::smem_addr(&c->drained), 1);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    int before = shared_tiles + sum - mine;
+    for (int i = 0; i < warp; ++i) before += c->scan[i];
+    if (tid == kAttentionThreads - 1) c->total = before + mine;
+    __syncthreads();
+    const int total = c->total;
+    const int lo = static_cast<int>(static_cast<long long>(blockIdx.x) * total / a.ctas);
+    const int hi = static_cast<int>(static_cast<long long>(blockIdx.x + 1) * total / a.ctas);
+    for (int b = b0; b < b1; ++b) {
+        if (blockIdx.x == 0) a.starts[b] = before;
+        const int n = tiles(b);
+        if (lo >= before && lo < before + n) c->b = b, c->before = before;
+        before += n;
+    }
+    if (blockIdx.x == 0 && tid == kAttentionThreads - 1) a.starts[a.B] = total;
+    if (lo >= hi) return;  // the whole CTA
+    if (warp == 13) tmem_alloc(ptx::smem_addr(&c->tmem), 512);
+    __syncthreads();
+    fence_after();
+
+    Attention<T, D, Q8> x{a, c, ptx::smem_addr(smem), ptx::smem_addr(smem) + 2 * L::kQ + L::kRing * L::kQ, lane, warp};
+    if (warp < 8) x.softmax(warp >> 2, tid & 127);
+    else if (warp < 12) x.load_rows(tid - 256);
+    else if (warp == 12) x.load_tiles(&k_map, &v_map);
+    else if (warp == 13) x.multiply();
+
+    fence_before();
+    __syncthreads();
+    if (warp == 13) tmem_free(c->tmem, 512);
+}
+
+// ------------------------------------------------------------------ joining
+// A warp a row: the partial sums of the blocks that hold it, in the order of their keys.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attention_join_kernel(const AttentionArgs a) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const long long rows = static_cast<long long>(a.B) * a.N * a.heads;
+    if (row >= rows) return;
+    const int h = static_cast<int>(row % a.heads), n = static_cast<int>(row / a.heads % a.N), b = static_cast<int>(row / a.heads / a.N);
+    const int total = a.starts[a.B], start = a.starts[b], tiles = (a.starts[b + 1] - start) / (a.cache.kv_heads * a.blocks);
+    if (tiles == 0) return;  // left out
+    const int g = h / a.group, in_seq = n * a.group + h % a.group;
+    const auto owner = [&](int t) { return static_cast<int>(((t + 1ll) * a.ctas - 1) / total); };
+
+    float m = -INFINITY, l = 0.0f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.0f;
+    const auto take = [&](const float *sums, float2 s) {
+        if (s.x == -INFINITY && s.y == 0.0f) return;
+        float x[E];
+        if (E == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(sums + lane * E);
+        else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(sums + lane * E);
+        const float top = fmaxf(m, s.x), was = m == -INFINITY ? 0.0f : ptx::ex2(m - top), now = ptx::ex2(s.x - top);
+        l = l * was + s.y * now;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = o[e] * was + x[e] * now;
+        m = top;
+    };
+    for (int kind = a.shared_len ? 0 : 1; kind < 2; ++kind) {  // the prefix, then the sequence's own
+        int t0, n_tiles, r;
+        if (kind == 0) {
+            const int all = b * a.N * a.group + in_seq;
+            n_tiles = tiles_of(a.shared_len);
+            t0 = (g * a.shared_blocks + all / a.shared_rows) * n_tiles;
+            r = all % a.shared_rows;
+        } else {
+            n_tiles = tiles;
+            t0 = start + (g * a.blocks + in_seq / a.block_rows) * tiles;
+            r = in_seq % a.block_rows;
+        }
+        const int c0 = owner(t0), c1 = owner(t0 + n_tiles - 1);
+        if (c0 == c1) {
+            if (!a.shared_len) return;  // written already
+            const size_t i = static_cast<size_t>(kind == 0 ? rows : 0) + row;
+            take(a.row_sums + i * D, a.row_stats[i]);
+            continue;
+        }
+        for (int c = c0; c <= c1; ++c) {
+            const int lo = static_cast<int>(static_cast<long long>(c) * total / a.ctas);
+            if (lo == static_cast<int>((c + 1ll) * total / a.ctas)) continue;  // a CTA without tiles
+            const size_t i = (static_cast<size_t>(c) * 2 + (t0 < lo ? 0 : 1)) * kBlockRows + r;
+            take(a.cut_sums + i * D, a.cut_stats[i]);
+        }
+    }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    for (int e = 0; e < E; ++e) out[e] = static_cast<T>(o[e] * inv);
-    if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : m + logf(l);
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) w[e / 2] = Elt<T>::from_float2(o[e] * inv, o[e + 1] * inv);
+    uint32_t *out = reinterpret_cast<uint32_t *>(a.out) + row * (D / 2) + lane * (E / 2);
+    if (E == 4) *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[E / 2 - 1]);
+    else out[0] = w[0];
+    if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 }  // namespace context

@@ -1,10 +1,23 @@
-// attention.h -- the parameter block of the attention and its launchers.
+// attention.h -- what the host and the kernels of the attention share: tiles, the split of the work, the
+// parameter block.
+//
+// The work is a list of tiles of 128 keys.  First the shared prefix: for each key head and block of up to
+// 256 rows of the whole batch, its tiles.  Then sequence by sequence, key head by key head, block by
+// block of up to 256 of the sequence's rows, the tiles of its own context and of its nodes.  A CTA takes
+// an equal run of the list, wherever that begins and ends, so the split balances to a tile whatever
+// the lengths; a block that several CTAs share leaves partial sums, which a second kernel joins.
 #pragma once
+
+#include <cuda.h>
 
 #include "context.h"
 
 namespace spec {
 namespace context {
+
+constexpr int kTile = 128;       // keys of a tile, rows of a matrix product
+constexpr int kBlockRows = 256;  // rows of a block: two products share a tile of keys
+constexpr int kMaxCtas = 160;    // one an SM
 
 struct AttentionArgs {
     CacheView cache;
@@ -17,7 +30,25 @@ struct AttentionArgs {
     uint32_t *status;
     int B, N, heads, shared_len;
     float scale;
+    // the split
+    int group;                        // query heads a key head
+    int blocks, block_rows;           // of a sequence's N * group rows
+    int shared_blocks, shared_rows;   // of the batch's B * N * group rows
+    int ctas;
+    // the workspace
+    int32_t *starts;   // [B + 1] tiles before each sequence's
+    float *cut_sums;   // [ctas][2][kBlockRows][D]: blocks cut at a CTA's begin and at its end
+    float2 *cut_stats; // ... their rows' (maximum in units of log 2, sum)
+    float *row_sums;   // [2][B * N * heads][D], with a shared prefix: blocks that one CTA took whole, the sequence's own and the prefix's
+    float2 *row_stats;
 };
+
+// The driver's encoder of tensor maps (null where the driver has none).
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled();
+
+__host__ __device__ inline int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 
 template <typename T, int D, bool Q8>
 spec_status launch_attention(const AttentionArgs &a, cudaStream_t stream);

@@ -1,6 +1,7 @@
 // attention_launch.cuh -- the launcher of the attention, instantiated one element type a unit.
 #pragma once
 
+#include <algorithm>
 #include <climits>
 
 #include "attention.cuh"
@@ -8,12 +9,48 @@
 namespace spec {
 namespace context {
 
+// The cache's keys or values [pages][kv_heads * page_size][D] in boxes of up to 128 rows of a page: 16-bit ones in
+// halves of 64 columns, swizzled as the products take them; 8-bit ones whole, to be widened.
+template <int D, bool Q8>
+spec_status tensor_map(CUtensorMap *map, const AttentionArgs &a, void *base, CUtensorMapDataType type) {
+    const EncodeTiled encode = encode_tiled();
+    if (!encode) return fail(SPEC_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    const cuuint64_t rows = static_cast<cuuint64_t>(a.cache.kv_heads) << a.cache.page_bits, row = D * (Q8 ? 1 : 2);
+    const cuuint64_t dims[3] = {D, rows, static_cast<cuuint64_t>(std::max(a.cache.pages, 1))}, strides[2] = {row, rows * row};
+    const cuuint32_t box[3] = {Q8 ? D : 64, static_cast<cuuint32_t>(std::min(1 << a.cache.page_bits, kTile)), 1}, each[3] = {1, 1, 1};
+    const CUresult r = encode(map, type, 3, base, dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              Q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SPEC_OK : fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
+}
+
 template <typename T, int D, bool Q8>
-spec_status launch_attention(const AttentionArgs &a, cudaStream_t stream) {
+spec_status launch_attention(const AttentionArgs &a0, cudaStream_t stream) {
+    DeviceInfo di;
+    int dev = 0;
+    spec_status st = device_info(&di, &dev);
+    if (st != SPEC_OK) return st;
+    auto kernel = attention_kernel<T, D, Q8>;
+    st = allow_max_dyn_smem(dev, reinterpret_cast<const void *>(kernel), &di);
+    if (st != SPEC_OK) return st;
+    constexpr size_t smem = Layout<D, Q8>::kBytes + sizeof(Control);
+    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
+    if (smem > di.max_dyn) return fail(SPEC_ERR_UNSUPPORTED, "%zu bytes of shared memory needed, %zu there", smem, di.max_dyn);
+    AttentionArgs a = a0;
+    a.ctas = std::min(di.sms, kMaxCtas);
+    const CUtensorMapDataType type = Q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                        : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    CUtensorMap maps[2];
+    for (int i = 0; i < 2; ++i) {  // (a cache without pages is not read: any address does)
+        st = tensor_map<D, Q8>(&maps[i], a, a.cache.pages ? a.cache.data[i] : a.out, type);
+        if (st != SPEC_OK) return st;
+    }
+    kernel<<<a.ctas, kAttentionThreads, smem, stream>>>(a, maps[0], maps[1]);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
     const long long rows = static_cast<long long>(a.B) * a.N * a.heads;
-    attention_kernel<T, D, Q8><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
+    attention_join_kernel<T, D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "join launch: %s", cudaGetErrorString(e));
 }
 
 }  // namespace context

@@ -12,6 +12,21 @@ namespace spec {
 extern thread_local char g_last_error[512];
 
 namespace context {
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled f = []() -> EncodeTiled {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
 namespace {
 
 bool aligned(const void *p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -26,7 +41,7 @@ spec_status cache_args(CacheView *v, const spec_cache *c, spec_dtype dtype, int 
     int bits = 4;
     while (bits < 8 && 1 << bits != c->page_size) ++bits;
     if (1 << bits != c->page_size) return fail(SPEC_ERR_UNSUPPORTED, "page_size = %d: 16, 32, 64, 128 or 256", c->page_size);
-    if (c->table_width > INT_MAX >> bits) return fail(SPEC_ERR_UNSUPPORTED, "table_width = %d: positions below 2^31", c->table_width);
+    if (c->table_width > 1 << (30 - bits)) return fail(SPEC_ERR_UNSUPPORTED, "table_width = %d: positions below 2^30", c->table_width);
     if (c->kv_heads > 1024) return fail(SPEC_ERR_UNSUPPORTED, "kv_heads = %d > 1024", c->kv_heads);
     if (B > 0 && c->pages && (!c->k || !c->v)) return fail(SPEC_ERR_INVALID_ARG, "the cache's k or v is null");
     if (B > 0 && c->table_width && !c->page_table) return fail(SPEC_ERR_INVALID_ARG, "page_table is null");
@@ -69,6 +84,26 @@ template <typename T>
 spec_status dispatch_cache(CacheOp op, const CacheRowsArgs &a, int D, bool q8, cudaStream_t s) {
     if (D == 64) return q8 ? launch_cache<T, 64, true>(op, a, s) : launch_cache<T, 64, false>(op, a, s);
     return q8 ? launch_cache<T, 128, true>(op, a, s) : launch_cache<T, 128, false>(op, a, s);
+}
+
+// The workspace: tiles before each sequence, then the partial sums (see AttentionArgs), each part on 16 bytes.
+size_t attention_layout(AttentionArgs *a, int B, int N, int heads, int D, int shared_len, unsigned char *base) {
+    size_t at = 0;
+    const auto part = [&](size_t bytes) {
+        unsigned char *p = base + at;
+        at += (bytes + 15) / 16 * 16;
+        return p;
+    };
+    const size_t cut = static_cast<size_t>(kMaxCtas) * 2 * kBlockRows, rows = shared_len ? 2 * static_cast<size_t>(B) * N * heads : 0;
+    unsigned char *p[5] = {part(4 * (static_cast<size_t>(B) + 1)), part(cut * D * 4), part(cut * 8), part(rows * D * 4), part(rows * 8)};
+    if (a) {
+        a->starts = reinterpret_cast<int32_t *>(p[0]);
+        a->cut_sums = reinterpret_cast<float *>(p[1]);
+        a->cut_stats = reinterpret_cast<float2 *>(p[2]);
+        a->row_sums = reinterpret_cast<float *>(p[3]);
+        a->row_stats = reinterpret_cast<float2 *>(p[4]);
+    }
+    return at;
 }
 
 template <typename T>
@@ -142,7 +177,7 @@ extern "C" spec_status spec_cache_read(const spec_cache *cache, int B, int S, co
 extern "C" size_t spec_workspace_bytes_attention(int B, int N, int heads, int kv_heads, int head_dim, int shared_len) {
     if (B <= 0 || N < 1 || N > SPEC_MAX_NODES || kv_heads < 1 || heads < 1 || heads % kv_heads || (head_dim != 64 && head_dim != 128) || shared_len < 0)
         return 0;
-    return 16;
+    return attention_layout(nullptr, B, N, heads, head_dim, shared_len, nullptr);
 }
 
 extern "C" spec_status spec_tree_attention(const void *q, const void *k, const void *v, spec_dtype dtype, int B, int N, int heads,
@@ -156,7 +191,7 @@ extern "C" spec_status spec_tree_attention(const void *q, const void *k, const v
     const int kv = cache->kv_heads, D = cache->head_dim;
     if (B < 0 || N < 1 || heads < 1 || heads % kv) return fail(SPEC_ERR_INVALID_ARG, "need B >= 0, N >= 1, heads a multiple of kv_heads");
     if (N > SPEC_MAX_NODES) return fail(SPEC_ERR_UNSUPPORTED, "N = %d > %d", N, SPEC_MAX_NODES);
-    if (shared_len < 0 || shared_len > cache->table_width * cache->page_size)
+    if (shared_len < 0 || shared_len > cache->table_width * cache->page_size || (shared_len && !cache->pages))
         return fail(SPEC_ERR_INVALID_ARG, "shared_len = %d: within the page table", shared_len);
     if (!(scale > 0.0f && scale < INFINITY)) return fail(SPEC_ERR_INVALID_ARG, "scale must be finite and > 0");
     if (B == 0) return SPEC_OK;
@@ -182,6 +217,18 @@ extern "C" spec_status spec_tree_attention(const void *q, const void *k, const v
     a.status = dev_status;
     a.B = B, a.N = N, a.heads = heads, a.shared_len = shared_len;
     a.scale = scale;
+    if (a.cache.pages == 0) a.cache.table_width = 0;  // no position is there
+    attention_layout(&a, B, N, heads, D, shared_len, static_cast<unsigned char *>(workspace));
+    // Blocks of at most 256 rows, as equal as they can be.
+    a.group = heads / kv;
+    const int rows = N * a.group, all = B * rows;
+    a.blocks = (rows + kBlockRows - 1) / kBlockRows;
+    a.block_rows = (rows + a.blocks - 1) / a.blocks;
+    a.shared_blocks = (all + kBlockRows - 1) / kBlockRows;
+    a.shared_rows = (all + a.shared_blocks - 1) / a.shared_blocks;
+    const long long tiles = static_cast<long long>(kv) * (static_cast<long long>(B) * a.blocks * (tiles_of(cache->table_width * cache->page_size) + tiles_of(N)) +
+                                                          static_cast<long long>(a.shared_blocks) * tiles_of(shared_len));
+    if (tiles > INT_MAX) return fail(SPEC_ERR_UNSUPPORTED, "too much work: %lld tiles of %d keys", tiles, kTile);
     const bool q8 = cache->dtype == SPEC_E4M3;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == SPEC_BF16 ? dispatch_attention<__nv_bfloat16>(a, D, q8, s) : dispatch_attention<__half>(a, D, q8, s);
