@@ -259,8 +259,7 @@ struct Attention {
         const uint64_t first = ptx::policy_evict_first(), normal = policy_evict_normal();
         const int box = min(1 << a.cache.page_bits, kTile), boxes = kTile / box;
         bool bad = false, ok = true;
-        Cursor last = at;
-        int issued = 0;
+        uint32_t issued = 0, rounds = 0;  // a bit a slot: it was loaded into; the parity of the last such round
         const int slots = Q8 ? L::kStages : L::kRing;
         while (ok && walk.next(&p)) {
             const int32_t *table = a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width;
@@ -276,10 +275,15 @@ struct Attention {
                 }
                 for (int w = 0; w < 2; ++w) {
                     const bool mine = Q8 ? t < p.context : by_tma(p, t, w);
-                    if (!Q8 && !mine) at.step(slots);
-                    if (!mine) continue;
+                    if (Q8 && !mine) continue;
                     const uint64_t *full = Q8 ? &c->staged[at.slot] : &c->full[at.slot], *empty = Q8 ? &c->free_[at.slot] : &c->empty[at.slot];
+                    // Each round of each slot is waited for, also where another warp fills it: a parity tells
+                    // a round from the next, not from the one after.
                     if (!(ok = wait(empty, at.round ^ 1))) break;
+                    if (!mine) {
+                        at.step(slots);
+                        continue;
+                    }
                     const uint32_t bar = ptx::smem_addr(full), to = Q8 ? stages + at.slot * L::kStage : ring(at.slot);
                     if (lane == 0) {
                         if (!Q8) arrive(bar, 3);
@@ -292,8 +296,8 @@ struct Attention {
                         else
                             for (int x = 0; x < D; x += 64) tma_load3(to + (x / 64) * (kTile * 128) + lane * box * 128, w ? v_map : k_map, x, y, page, bar, policy);
                     }
-                    last = at;
-                    ++issued;
+                    issued |= 1u << at.slot;
+                    rounds = (rounds & ~(1u << at.slot)) | at.round << at.slot;
                     at.step(slots);
                 }
             }
@@ -301,14 +305,10 @@ struct Attention {
         if (bad) atomicOr(a.status, SPEC_DEV_BAD_PAGE);
         // No copy is in flight when the CTA ends: where a wait gave up, each slot's last one is waited for.
         if (!ok) {
-            for (int i = 0; i < min(issued, slots); ++i) {
-                const uint32_t bar = ptx::smem_addr(Q8 ? &c->staged[last.slot] : &c->full[last.slot]);
-                bool done = false;
-                for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(bar, last.round);
-                if (last.slot-- == 0) {
-                    last.slot = slots - 1;
-                    last.round ^= 1;
-                }
+            for (int i = 0; i < slots; ++i) {
+                const uint32_t bar = ptx::smem_addr(Q8 ? &c->staged[i] : &c->full[i]);
+                bool done = !(issued >> i & 1);
+                for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(bar, rounds >> i & 1);
             }
         }
     }
@@ -505,8 +505,8 @@ struct Attention {
                     }
                 }
                 for (int w = 0; ok && w < 2; ++w, at.step(L::kRing)) {
+                    if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;  // (also a tile that TMA loads: see there)
                     if (by_tma(p, t, w)) continue;
-                    if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
                     const uint32_t to = ring(at.slot);
                     if (t >= p.context) {
                         if (load_nodes(p, t, w, to, tid)) *const_cast<volatile int *>(&c->odd[count & 7]) = 1;

@@ -113,6 +113,17 @@ def test_many_sequences_and_long_contexts():
     check_all(problem(2, 80, 8, 2, 128, 64, [3000, 2900], BF, True, seed=7))
 
 
+@pytest.mark.parametrize("q8", [False, True])
+def test_long_contexts_behind_each_other(q8):
+    """Many rounds of the ring of tiles between the ones that plain loads bring (the ends of contexts, the nodes), and many of
+    the latter between the others."""
+    for s in (problem(16, 64, 8, 2, 128, 32, [1500 - 60 * b for b in range(16)], BF, q8, seed=11),
+              problem(40, 3, 8, 4, 128, 64, [(2000 * b) % 1777 + 1 for b in range(40)], BF, q8, seed=12),
+              problem(12, 40, 8, 2, 64, 16, [1300 - 100 * b for b in range(12)], F16, q8, seed=13),
+              problem(3, 1024, 1, 1, 128, 64, [900, 1100, 300], BF, q8, seed=14)):
+        check(call(s), s)
+
+
 def test_masks():
     """Rows that see no node, none that sees itself, all nodes; a chain without a mask; rows that see nothing at all."""
     N = 40
