@@ -834,11 +834,11 @@ def spec_cache_append(k, v, k_cache, v_cache, page_table, start, *, count=None, 
     return out
 
 
-def spec_cache_read(k_cache, v_cache, page_table, start, n, *, count=None, k_scale=None, v_scale=None, dtype=torch.bfloat16, status=None,
+def spec_cache_read(k_cache, v_cache, page_table, start, n, *, count=None, k_scale=None, v_scale=None, dtype=None, status=None,
                     out=None, stream=None):
     """Reads n positions of every sequence, from start[b] on, out of a paged cache as spec_cache_append writes it: returns
-    dict(k, v [B, n, kv_heads, head_dim], status), of the cache's type, or of `dtype` (bfloat16, float16) where the
-    cache is float8_e4m3fn.  Rows from count[b] on are left as they were (new ones: 0)."""
+    dict(k, v [B, n, kv_heads, head_dim], status), of the cache's type, or of `dtype` (bfloat16, float16; None: out's,
+    or bfloat16) where the cache is float8_e4m3fn.  Rows from count[b] on are left as they were (new ones: 0)."""
     lib = load_library()
     _on_gpu(k_cache, "k_cache")
     if k_cache.dim() != 4:
@@ -848,6 +848,8 @@ def spec_cache_read(k_cache, v_cache, page_table, start, n, *, count=None, k_sca
     i = dev.index
     if k_cache.dtype in _CODES:
         dtype = k_cache.dtype
+    elif dtype is None:
+        dtype = torch.bfloat16 if out is None or out.get("k") is None else out["k"].dtype
     if dtype not in _CODES:
         raise TypeError("dtype must be bfloat16 or float16, got %s" % dtype)
     if n < 0:

@@ -42,6 +42,7 @@ struct Layout {
 
 struct Control {  // behind the tiles in shared memory
     uint64_t full[8], empty[8];    // ring of tiles
+    uint64_t copied[8];            // a slot's values are there, to be cleared in part
     uint64_t staged[8], free_[8];  // ring of 8-bit tiles
     uint64_t q_full[2], q_empty[2];
     uint64_t scores[2], weights[2], sums[2];  // of the two products
@@ -162,21 +163,23 @@ struct Widen<__nv_bfloat16> {
         m2 = s2 | s2 << 16;
         twice = e > 7;
     }
-    __device__ __forceinline__ void zero() { m1 = 0, twice = false; }
+    __device__ __forceinline__ void zero() { m1 = m2 = 0, twice = false; }
     static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
         uint32_t r;
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
     }
+    template <bool TWICE>
     __device__ __forceinline__ uint2 four(uint32_t w) const {
         const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
         uint32_t x = times((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), m1), y = times((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), m1);
-        if (twice) x = times(x, m2), y = times(y, m2);
+        if (TWICE) x = times(x, m2), y = times(y, m2);
         return make_uint2(x, y);
     }
 };
 template <>
 struct Widen<__half> {
+    static constexpr bool twice = false;
     uint32_t m;
     __device__ __forceinline__ void scale(uint32_t byte) {
         const int e = min(max(static_cast<int>(byte) - 127, -24), 15);
@@ -190,6 +193,7 @@ struct Widen<__half> {
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
     }
+    template <bool>
     __device__ __forceinline__ uint2 four(uint32_t w) const {
         const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffff), __NV_E4M3);
         const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
@@ -222,6 +226,27 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return *reinterpret_cast<float2 *>(&r);
 }
 
+// Where a piece leaves its rows' sums, column by column (a warp's rows lie next to each other), and (maximum, sum).
+struct Part {
+    float *sums;    // [D][rows]
+    float2 *stats;  // [rows]
+    int rows;
+};
+// A block that a CTA does not hold whole: at the CTA's begin (its block began in an earlier one) or its end.
+template <int D>
+__device__ __forceinline__ Part cut_part(const AttentionArgs &a, int cta, bool at_end) {
+    const size_t i = static_cast<size_t>(cta) * 2 + (at_end ? 1 : 0);
+    return Part{a.cut_sums + i * kBlockRows * D, a.cut_stats + i * kBlockRows, kBlockRows};
+}
+// A whole block, beside a prefix: of sequence b's rows, or of the batch's (`first`: its first row of them).
+template <int D>
+__device__ __forceinline__ Part whole_part(const AttentionArgs &a, bool shared, int b, int g, int first) {
+    const size_t per_seq = static_cast<size_t>(a.N) * a.group, all = per_seq * a.B;
+    const size_t row = shared ? (a.cache.kv_heads + g) * all + first : g * all + b * per_seq + first;
+    const int rows = shared ? min(static_cast<int>(all) - first, a.shared_rows) : min(static_cast<int>(per_seq) - first, a.block_rows);
+    return Part{a.row_sums + row * D, a.row_stats + row, rows};
+}
+
 // ------------------------------------------------------------------ the four kinds of warps
 template <typename T, int D, bool Q8>
 struct Attention {
@@ -236,16 +261,17 @@ struct Attention {
     const AttentionArgs &a;
     Control *c;
     uint32_t tiles, stages;  // shared-memory addresses: queries, then the ring; 8-bit tiles
+    uint32_t tmem;
     int lane, warp;
 
     __device__ __forceinline__ bool wait(const uint64_t *bar, uint32_t parity) {
         return wait_phase(ptx::smem_addr(bar), parity, &c->gave_up, a.status);
     }
     __device__ __forceinline__ uint32_t ring(int slot) const { return tiles + 2 * L::kQ + slot * L::kQ; }
-    // Whether entry (tile t of piece p; keys or values) comes by TMA straight into the ring.
-    __device__ __forceinline__ bool by_tma(const Piece &p, int t, bool values) const {
-        if (Q8 || t >= p.context) return false;
-        return !values || (first_tile(p) + t + 1) * kTile <= p.len;
+    // Whether a piece's tile t of the context ends behind the sequence, or begins before what is its own.
+    __device__ __forceinline__ bool ragged(const Piece &p, int t) const {
+        const int at = (first_tile(p) + t) * kTile;
+        return at + kTile > p.len || at < begin(p);
     }
     __device__ __forceinline__ int first_tile(const Piece &p) const { return p.shared ? 0 : a.shared_len / kTile; }
     __device__ __forceinline__ int begin(const Piece &p) const { return p.shared ? 0 : a.shared_len; }  // the piece's first position
@@ -259,7 +285,7 @@ struct Attention {
         const uint64_t first = ptx::policy_evict_first(), normal = policy_evict_normal();
         const int box = min(1 << a.cache.page_bits, kTile), boxes = kTile / box;
         bool bad = false, ok = true;
-        uint32_t issued = 0, rounds = 0;  // a bit a slot: it was loaded into; the parity of the last such round
+        uint32_t issued = 0, rounds = 0, copies = 0;  // a bit a slot: it was loaded into; the parity of the last such round, of copies
         const int slots = Q8 ? L::kStages : L::kRing;
         while (ok && walk.next(&p)) {
             const int32_t *table = a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width;
@@ -274,21 +300,24 @@ struct Attention {
                     else page = entry;
                 }
                 for (int w = 0; w < 2; ++w) {
-                    const bool mine = Q8 ? t < p.context : by_tma(p, t, w);
+                    const bool mine = t < p.context;
                     if (Q8 && !mine) continue;
                     const uint64_t *full = Q8 ? &c->staged[at.slot] : &c->full[at.slot], *empty = Q8 ? &c->free_[at.slot] : &c->empty[at.slot];
-                    // Each round of each slot is waited for, also where another warp fills it: a parity tells
-                    // a round from the next, not from the one after.
+                    // Each round of each slot is waited for and arrived at by this warp and by the four that load
+                    // rows, whichever fills it: a parity tells a round from its neighbours alone, so none may
+                    // run ahead of the ring by more than a round, or fall behind it.
                     if (!(ok = wait(empty, at.round ^ 1))) break;
                     if (!mine) {
+                        if (lane == 0) arrive(ptx::smem_addr(full));
+                        __syncwarp();
                         at.step(slots);
                         continue;
                     }
-                    const uint32_t bar = ptx::smem_addr(full), to = Q8 ? stages + at.slot * L::kStage : ring(at.slot);
-                    if (lane == 0) {
-                        if (!Q8) arrive(bar, 3);
-                        ptx::mbar_arrive_expect_tx(bar, Q8 ? L::kStage : L::kQ);
-                    }
+                    // (values whose other rows are to be cleared: their copy is waited for by those who do that)
+                    const bool cleared = !Q8 && w && ragged(p, t);
+                    if (cleared && lane == 0) arrive(ptx::smem_addr(full));
+                    const uint32_t bar = ptx::smem_addr(cleared ? &c->copied[at.slot] : full), to = Q8 ? stages + at.slot * L::kStage : ring(at.slot);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, Q8 ? L::kStage : L::kQ);
                     __syncwarp();
                     if (lane < boxes) {
                         const int y = (p.g << a.cache.page_bits) + static_cast<int>(pos & ((1 << a.cache.page_bits) - 1));
@@ -298,6 +327,7 @@ struct Attention {
                     }
                     issued |= 1u << at.slot;
                     rounds = (rounds & ~(1u << at.slot)) | at.round << at.slot;
+                    if (cleared) copies ^= 1u << at.slot;
                     at.step(slots);
                 }
             }
@@ -309,6 +339,8 @@ struct Attention {
                 const uint32_t bar = ptx::smem_addr(Q8 ? &c->staged[i] : &c->full[i]);
                 bool done = !(issued >> i & 1);
                 for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(bar, rounds >> i & 1);
+                done = Q8 || !(issued >> i & 1);
+                for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(ptx::smem_addr(&c->copied[i]), (copies >> i & 1) ^ 1);
             }
         }
     }
@@ -319,15 +351,17 @@ struct Attention {
         int slot;
         uint32_t round;
     };
+    // The same in every lane, said so that the compiler keeps it in a uniform register, as the mma wants it.
+    static __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
     __device__ bool add_values(Pending &w, int s, uint32_t &weights_round) {
         w.any = false;
         if (!wait(&c->full[w.slot], w.round) || !wait(&c->weights[s], weights_round)) return false;
         weights_round ^= 1;
         fence_after();
-        if (lane == 0) {
-            const uint32_t v = ring(w.slot), d = c->tmem + kSums + s * 128, p = c->tmem + kScores + s * 128;
+        const uint32_t v = uniform(operand(ring(w.slot), kTile * 128)), d = uniform(tmem + kSums + s * 128), p = uniform(tmem + kScores + s * 128);
+        if (elect()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) mma_tmem(d, p + k * 8, operand(v + k * 16 * 128, kTile * 128), kSumsInstr, w.add || k > 0);
+            for (int k = 0; k < kTile / 16; ++k) mma_tmem(d, p + k * 8, descriptor(v + k * 16 * 128 / 16), kSumsInstr, w.add || k > 0);
             if (w.release) mma_commit(ptx::smem_addr(&c->empty[w.slot]));
             if (w.final) mma_commit(ptx::smem_addr(&c->sums[s]));
         }
@@ -360,12 +394,13 @@ struct Attention {
                     if (pending[s].any && !(ok = add_values(pending[s], s, weights_round[s]))) break;
                     if (x == 0 && !(ok = wait(&c->full[keys.slot], keys.round))) break;
                     fence_after();
-                    if (lane == 0) {
-                        const uint32_t q = tiles + (p.two ? x : half) * L::kQ, k = ring(keys.slot), d = c->tmem + kScores + s * 128;
+                    const uint32_t q = uniform(operand(tiles + (p.two ? x : half) * L::kQ, 16)), k = uniform(operand(ring(keys.slot), 16));
+                    const uint32_t d = uniform(tmem + kScores + s * 128);
+                    if (elect()) {
 #pragma unroll
                         for (int e = 0; e < D / 16; ++e) {
-                            const uint32_t off = (e / 4) * (kTile * 128) + (e % 4) * 32;
-                            mma(d, operand(q + off, 16), operand(k + off, 16), kScoresInstr, e > 0);
+                            const uint32_t off = ((e / 4) * (kTile * 128) + (e % 4) * 32) / 16;
+                            mma(d, descriptor(q + off), descriptor(k + off), kScoresInstr, e > 0);
                         }
                         mma_commit(ptx::smem_addr(&c->scores[s]));
                         if (x == (p.two ? 1 : 0)) mma_commit(ptx::smem_addr(&c->empty[keys.slot]));
@@ -386,146 +421,181 @@ struct Attention {
             if (!p.two) half ^= 1;
         }
         // Every product done before tensor memory is freed, also where a wait gave up.
-        if (lane == 0) mma_commit(ptx::smem_addr(&c->drained));
+        if (elect()) mma_commit(ptx::smem_addr(&c->drained));
         __syncwarp();
         bool done = false;
         for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(ptx::smem_addr(&c->drained), 0);
     }
 
-    // ---- plain loads: a row of D elements by D / 8 lanes
+    // ---- plain loads: a row of D elements by D / 8 lanes, a tile's all under way at once; they are issued
+    // before the warp waits for the place in shared memory that they go to
+    static constexpr int kLanes = D / 8, kLoads = kTile * kLanes / 128;  // lanes a row, 16-byte loads a thread
+    struct Loaded {
+        uint4 v[kLoads];
+    };
+    __device__ __forceinline__ void place(const Loaded &x, uint32_t to, int tid) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) store16(to + chunk_at(tid / kLanes + i * (128 / kLanes), tid % kLanes), x.v[i]);
+    }
     // Rows of queries; those the block lacks are 0.
-    __device__ void load_queries(const Piece &p, int half, int from, int tid) {
-        constexpr int kLanes = D / 8;
-#pragma unroll 4
-        for (int i = tid; i < kTile * kLanes; i += 128) {
-            const int r = i / kLanes, x = i % kLanes;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (from + r < p.rows) {
-                const RowId id = row_id(a, p, from + r);
-                v = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(a.q) + id.b * a.stride[0] + id.n * a.stride[1] + id.h * D) + x);
-            }
-            store16(tiles + half * L::kQ + chunk_at(r, x), v);
+    __device__ __forceinline__ void load_queries(const Piece &p, int from, int tid, Loaded &x) const {
+        constexpr int kStep = 128 / kLanes;  // rows from one load of a thread to its next
+        int r = from + tid / kLanes;
+        RowId id = row_id(a, p, r);
+        const int h0 = p.g * a.group, more_n = kStep / a.group, more_h = kStep % a.group;
+        const T *q = reinterpret_cast<const T *>(a.q) + tid % kLanes * 8;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            x.v[i] = make_uint4(0, 0, 0, 0);
+            if (r < p.rows) x.v[i] = __ldg(reinterpret_cast<const uint4 *>(q + id.b * a.stride[0] + id.n * a.stride[1] + id.h * D));
+            r += kStep;
+            id.n += more_n;
+            id.h += more_h;
+            if (id.h >= h0 + a.group) id.h -= a.group, ++id.n;
+            while (p.shared && id.n >= a.N) id.n -= a.N, ++id.b;
         }
     }
     __device__ __forceinline__ static bool odd_pair(uint32_t x) {  // an infinity or NaN among two elements
         constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
         return (x & e) == e || (x >> 16 & e) == e;
     }
-    // Keys or values of the nodes; rows past the last are 0, and so are values that are not finite: a row
-    // that does not see them would get 0 * NaN.  Those that do are given them at the end.
-    __device__ bool load_nodes(const Piece &p, int t, bool values, uint32_t to, int tid) {
-        constexpr int kLanes = D / 8;
+    // Keys or values of the nodes; rows past the last are 0.
+    __device__ __forceinline__ void load_nodes(const Piece &p, int t, bool values, int tid, Loaded &x) const {
         const int m0 = (t - p.context) * kTile;
         const T *src = reinterpret_cast<const T *>(values ? a.v : a.k) + p.b * a.stride[values ? 4 : 2] + p.g * D;
         const long long step = a.stride[values ? 5 : 3];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int m = m0 + tid / kLanes + i * (128 / kLanes);
+            x.v[i] = make_uint4(0, 0, 0, 0);
+            if (m < a.N) x.v[i] = __ldg(reinterpret_cast<const uint4 *>(src + m * step) + tid % kLanes);
+        }
+    }
+    // Values that are not finite become 0 (true: there were some): a row that does not see them would get
+    // 0 * NaN.  The rows that do are given them at the end.
+    __device__ __forceinline__ bool take_odd(Loaded &x) const {
         bool odd = false;
-#pragma unroll 4
-        for (int i = tid; i < kTile * kLanes; i += 128) {
-            const int r = i / kLanes, x = i % kLanes;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (m0 + r < a.N) v = __ldg(reinterpret_cast<const uint4 *>(src + (m0 + r) * step) + x);
-            if (values && (odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w))) {
-                odd = true;
-                uint32_t *w = reinterpret_cast<uint32_t *>(&v);
-                constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) odd |= odd_pair(x.v[i].x) || odd_pair(x.v[i].y) || odd_pair(x.v[i].z) || odd_pair(x.v[i].w);
+        if (odd) {
+            constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(&x.v[i]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if ((w[k] & e) == e) w[k] &= 0xffff0000u;
                     if ((w[k] >> 16 & e) == e) w[k] &= 0xffffu;
                 }
             }
-            store16(to + chunk_at(r, x), v);
         }
         return odd;
     }
-    // A last tile of values of the cache, 0 from the sequence's end on.
-    __device__ void load_last_values(const Piece &p, int t, uint32_t to, int tid) {
-        constexpr int kLanes = D / 8;
-        const int32_t *table = a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width;
-#pragma unroll 4
-        for (int i = tid; i < kTile * kLanes; i += 128) {
-            const int r = i / kLanes, x = i % kLanes;
-            const int pos = (first_tile(p) + t) * kTile + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (pos < p.len && pos >= begin(p)) {
-                const int page = __ldg(table + (pos >> a.cache.page_bits));
-                if (page >= 0 && page < a.cache.pages) {
-                    const size_t row = cache_row(a.cache, (static_cast<long long>(page) << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1)), p.g);
-                    v = __ldg(reinterpret_cast<const uint4 *>(a.cache.data[1] + row * D * 2) + x);
-                }
-            }
-            store16(to + chunk_at(r, x), v);
-        }
+    // The page of this thread's row of a piece's tile t, -1 where there is none; the scales of its keys and values.
+    __device__ __forceinline__ int row_page(const Piece &p, int t, int tid) const {
+        const int pos = (first_tile(p) + t) * kTile + tid;
+        if (t >= min(p.t1, p.context) || pos >= p.len || pos < begin(p)) return -1;
+        const int page = __ldg(a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width + (pos >> a.cache.page_bits));
+        return page < a.cache.pages ? page : -1;
+    }
+    __device__ __forceinline__ int row_scales(const Piece &p, int t, int tid, int page) const {  // keys', values' << 8; -1: no row
+        if (page < 0) return -1;
+        const int pos = (first_tile(p) + t) * kTile + tid;
+        const size_t row = cache_row(a.cache, (static_cast<long long>(page) << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1)), p.g);
+        return __ldg(a.cache.scale[0] + row) | __ldg(a.cache.scale[1] + row) << 8;
     }
     // An 8-bit tile, widened: a thread a row; the chunks in turned order, so that eight rows' meet different banks.
-    __device__ void widen(uint32_t from, uint32_t to, int r, const Widen<T> &w) {
-        constexpr int kChunks = D / 16;
+    template <bool TWICE>
+    __device__ __forceinline__ void widen(uint32_t from, uint32_t to, int r, const Widen<T> &w) const {
+        constexpr int kChunks = D / 16, kAhead = 4;
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            const int x = D == 128 ? (j + r) & 7 : (j + (r >> 1)) & 3;
-            const uint4 v = load16(from + r * D + x * 16);
-            const uint2 b0 = w.four(v.x), b1 = w.four(v.y), b2 = w.four(v.z), b3 = w.four(v.w);
-            store16(to + chunk_at(r, 2 * x), make_uint4(b0.x, b0.y, b1.x, b1.y));
-            store16(to + chunk_at(r, 2 * x + 1), make_uint4(b2.x, b2.y, b3.x, b3.y));
+        for (int j0 = 0; j0 < kChunks; j0 += kAhead) {
+            uint4 v[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) v[j] = load16(from + r * D + turned(j0 + j, r) * 16);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int x = turned(j0 + j, r);
+                const uint2 b0 = w.template four<TWICE>(v[j].x), b1 = w.template four<TWICE>(v[j].y);
+                store16(to + chunk_at(r, 2 * x), make_uint4(b0.x, b0.y, b1.x, b1.y));
+                const uint2 b2 = w.template four<TWICE>(v[j].z), b3 = w.template four<TWICE>(v[j].w);
+                store16(to + chunk_at(r, 2 * x + 1), make_uint4(b2.x, b2.y, b3.x, b3.y));
+            }
         }
+    }
+    static __device__ __forceinline__ int turned(int j, int r) { return D == 128 ? (j + r) & 7 : (j + (r >> 1)) & 3; }
+    // The rows of a tile of values outside [from, to) become 0.
+    __device__ __forceinline__ void clear_rows(uint32_t at, int r, int from, int to) const {
+        if (r >= from && r < to) return;
+#pragma unroll 4
+        for (int x = 0; x < kLanes; ++x) store16(at + chunk_at(r, x), make_uint4(0, 0, 0, 0));
     }
     __device__ void load_rows(int tid) {
         Walk walk(a, c);
         Piece p;
         Cursor at, staged;
-        uint32_t q_round[2] = {0, 0};
+        uint32_t q_round[2] = {0, 0}, copies = 0;  // the parity of each slot's next copy to clear
         int half = 0, count = 0;
         bool ok = true;
         while (ok && walk.next(&p)) {
+            int scales = -1, next_page = -1;  // of the tile at hand; of the one after it
+            if (Q8) {
+                scales = row_scales(p, p.t0, tid, row_page(p, p.t0, tid));
+                next_page = row_page(p, p.t0 + 1, tid);
+            }
             if (p.two) half = 0;
             for (int h = 0; ok && h < 2; ++h) {
                 if (!p.two && h != half) continue;
+                Loaded x;
+                load_queries(p, p.two ? h * kTile : 0, tid, x);
                 if (!(ok = wait(&c->q_empty[h], q_round[h] ^ 1))) break;
                 q_round[h] ^= 1;
                 // (the piece four on: none is read that far back, nor loaded that far ahead)
                 if (tid == 0) *const_cast<volatile int *>(&c->odd[(count + 4) & 7]) = 0;
-                load_queries(p, h, p.two ? h * kTile : 0, tid);
+                place(x, tiles + h * L::kQ, tid);
                 fence_async();
                 __syncwarp();
                 if (lane == 0) arrive(ptx::smem_addr(&c->q_full[h]));
             }
             for (int t = p.t0; ok && t < p.t1; ++t) {
-                uint32_t byte[2] = {0, 0};
-                bool live = false;
-                if (Q8 && t < p.context) {  // this thread's row: the scales of its keys and values
-                    const int pos = (first_tile(p) + t) * kTile + tid;
-                    if (pos < p.len && pos >= begin(p)) {
-                        const int page = __ldg(a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width + (pos >> a.cache.page_bits));
-                        if (page >= 0 && page < a.cache.pages) {
-                            const size_t row = cache_row(a.cache, (static_cast<long long>(page) << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1)), p.g);
-                            byte[0] = __ldg(a.cache.scale[0] + row);
-                            byte[1] = __ldg(a.cache.scale[1] + row);
-                            live = true;
-                        }
-                    }
+                int next_scales = -1;
+                if (Q8) {  // two dependent loads, each issued a tile ahead of its use
+                    next_scales = row_scales(p, t + 1, tid, next_page);
+                    next_page = row_page(p, t + 2, tid);
                 }
                 for (int w = 0; ok && w < 2; ++w, at.step(L::kRing)) {
-                    if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;  // (also a tile that TMA loads: see there)
-                    if (by_tma(p, t, w)) continue;
                     const uint32_t to = ring(at.slot);
-                    if (t >= p.context) {
-                        if (load_nodes(p, t, w, to, tid)) *const_cast<volatile int *>(&c->odd[count & 7]) = 1;
-                    } else if (!Q8) {
-                        load_last_values(p, t, to, tid);
-                    } else {
-                        if (!(ok = wait(&c->staged[staged.slot], staged.round))) break;
+                    if (Q8 && t < p.context) {
                         Widen<T> x;
-                        if (live) x.scale(byte[w]);
+                        if (scales >= 0) x.scale(scales >> (8 * w) & 255);
                         else x.zero();
-                        widen(stages + staged.slot * L::kStage, to, tid, x);
+                        if (!(ok = wait(&c->empty[at.slot], at.round ^ 1) && wait(&c->staged[staged.slot], staged.round))) break;
+                        const uint32_t from = stages + staged.slot * L::kStage;
+                        if (__any_sync(0xffffffffu, x.twice)) widen<true>(from, to, tid, x);
+                        else widen<false>(from, to, tid, x);
                         __syncwarp();
                         if (lane == 0) arrive(ptx::smem_addr(&c->free_[staged.slot]));
                         staged.step(L::kStages > 0 ? L::kStages : 1);
+                    } else if (t < p.context) {
+                        if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
+                        if (w && ragged(p, t)) {
+                            if (!(ok = wait(&c->copied[at.slot], copies >> at.slot & 1))) break;
+                            copies ^= 1u << at.slot;
+                            const int base = (first_tile(p) + t) * kTile;
+                            clear_rows(to, tid, begin(p) - base, p.len - base);
+                        }
+                    } else {
+                        Loaded x;
+                        load_nodes(p, t, w, tid, x);
+                        if (w && take_odd(x)) *const_cast<volatile int *>(&c->odd[count & 7]) = 1;
+                        if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
+                        place(x, to, tid);
                     }
                     fence_async();
                     __syncwarp();
                     if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
                 }
+                scales = next_scales;
             }
             ++count;
             if (!p.two) half ^= 1;
@@ -533,45 +603,63 @@ struct Attention {
     }
 
     // ---- softmax
-    // The 128 columns of a tile that row `r` does not see are masked; `words`: a bit a column.
-    __device__ void seen_words(const Piece &p, int t, int n, uint32_t (&words)[4]) const {
+    // Which of a tile's columns 32 k .. 32 k + 31 a row of node n sees: a bit a column.
+    __device__ __forceinline__ uint32_t seen(const Piece &p, int t, int n, int k) const {
         if (t < p.context) {
-            const int base = (first_tile(p) + t) * kTile;
-            const int lo = p.shared ? 0 : max(0, a.shared_len - base), hi = min(kTile, p.len - base);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int from = min(max(lo - 32 * k, 0), 32), to = min(max(hi - 32 * k, 0), 32);
-                const uint32_t below_to = to == 32 ? ~0u : (1u << to) - 1, below_from = from == 32 ? ~0u : (1u << from) - 1;
-                words[k] = below_to & ~below_from;
-            }
-            return;
+            const int at = (first_tile(p) + t) * kTile + 32 * k;
+            const int from = min(max(begin(p) - at, 0), 32), to = min(max(p.len - at, 0), 32);
+            return static_cast<uint32_t>((1ull << to) - 1) & ~static_cast<uint32_t>((1ull << from) - 1);
         }
-        const int m0 = (t - p.context) * kTile, all = (a.N + 31) / 32;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int m = m0 + 32 * k;
-            uint32_t w = 0;
-            if (m < a.N) {
-                if (a.mask) w = __ldg(a.mask + static_cast<size_t>(n) * all + m / 32);
-                else if (n >= m) w = n - m >= 31 ? ~0u : (2u << (n - m)) - 1;
-                if (a.N - m < 32) w &= (1u << (a.N - m)) - 1;
-            }
-            words[k] = w;
-        }
+        const int m = (t - p.context) * kTile + 32 * k;
+        if (m >= a.N) return 0;
+        uint32_t w = a.N - m < 32 ? (1u << (a.N - m)) - 1 : ~0u;
+        if (a.mask) w &= __ldg(a.mask + static_cast<size_t>(n) * ((a.N + 31) / 32) + m / 32);
+        else w &= static_cast<uint32_t>((1ull << min(max(n - m + 1, 0), 32)) - 1);
+        return w;
     }
     template <bool MASKED>
-    __device__ void tile_weights(uint32_t s_at, uint32_t o_at, const uint32_t (&words)[4], float scale, bool first, float &m, float &l) {
-        uint32_t x[32];
-        float top = -INFINITY;
+    static __device__ __forceinline__ float largest(const uint32_t (&x)[32], uint32_t w) {
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            tmem_load32(x, s_at + 32 * k);
-            wait_loads();
+        for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], MASKED && !((w >> j) & 1) ? -INFINITY : __uint_as_float(x[j]));
+        return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+    }
+    // Weights of 32 columns into tensor memory; their sum is added to `sum`.
+    template <bool MASKED>
+    static __device__ __forceinline__ void weigh(const uint32_t (&x)[32], uint32_t w, float2 scale, float2 sub, float2 (&sum)[2], uint32_t to) {
+        uint32_t y[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const float v = __uint_as_float(x[j]);
-                top = fmaxf(top, MASKED && !((words[k] >> j) & 1) ? -INFINITY : v);
+        for (int j = 0; j < 32; j += 2) {
+            float2 e = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), scale, sub);
+            e.x = ptx::ex2(e.x);
+            e.y = ptx::ex2(e.y);
+            if (MASKED) {
+                if (!((w >> j) & 1)) e.x = 0.0f;
+                if (!((w >> (j + 1)) & 1)) e.y = 0.0f;
             }
+            sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
+            y[j / 2] = Elt<T>::from_float2(e.x, e.y);
+        }
+        tmem_store16(to, y);
+    }
+    // A tile's scores into weights, in two passes over tensor memory (the row's maximum, then the weights), 32 columns
+    // at a time, the next ones under way.  The loops stay loops: every unrolled copy is fetched cold in each launch.
+    template <bool MASKED>
+    __device__ __forceinline__ void tile_weights(const Piece &p, int t, int n, uint32_t s_at, uint32_t o_at, float scale, bool first, float &m, float &l) {
+        uint32_t x[32], y[32];
+        float top = -INFINITY;
+        __syncwarp();  // tensor memory's loads and stores take the warp as one: here and below, behind what parts it
+        tmem_load32(x, s_at);
+#pragma unroll 1
+        for (int k = 0; k < 4; k += 2) {
+            const uint32_t w0 = MASKED ? seen(p, t, n, k) : 0, w1 = MASKED ? seen(p, t, n, k + 1) : 0;
+            if (MASKED) __syncwarp();
+            wait_loads(x);
+            tmem_load32(y, s_at + 32 * k + 32);
+            top = fmaxf(top, largest<MASKED>(x, w0));
+            wait_loads(y);
+            tmem_load32(x, s_at + ((32 * k + 64) & 127));  // (the last: the first columns again, for the second pass)
+            top = fmaxf(top, largest<MASKED>(y, w1));
         }
         top = top * scale;
         // `m` is what the exponents subtract; -inf while the row has seen nothing
@@ -581,39 +669,33 @@ struct Attention {
             const float f = moves ? (m == -INFINITY ? 0.0f : ptx::ex2(m - want)) : 1.0f;
             l *= f;
             if (moves) m = want;
+            __syncwarp();
             if (!first) {
+                wait_loads(x);
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
-                    tmem_load32(x, o_at + k);
-                    wait_loads();
+                    tmem_load32(y, o_at + k);
+                    wait_loads(y);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-                    tmem_store32(o_at + k, x);
+                    for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                    tmem_store32(o_at + k, y);
                 }
-                wait_stores();
             }
         }
         const float sub = m == -INFINITY ? 0.0f : -m;
         const float2 c2 = make_float2(scale, scale), s2 = make_float2(sub, sub);
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            tmem_load32(x, s_at + 32 * k);
-            wait_loads();
-            uint32_t w[16];
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-                float2 e = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), c2, s2);
-                e.x = ptx::ex2(e.x);
-                e.y = ptx::ex2(e.y);
-                if (MASKED) {
-                    if (!((words[k] >> j) & 1)) e.x = 0.0f;
-                    if (!((words[k] >> (j + 1)) & 1)) e.y = 0.0f;
-                }
-                sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
-                w[j / 2] = Elt<T>::from_float2(e.x, e.y);
-            }
-            tmem_store16(s_at + 16 * k, w);
+        __syncwarp();
+#pragma unroll 1
+        for (int k = 0; k < 4; k += 2) {
+            const uint32_t w0 = MASKED ? seen(p, t, n, k) : 0, w1 = MASKED ? seen(p, t, n, k + 1) : 0;
+            if (MASKED) __syncwarp();
+            wait_loads(x);
+            tmem_load32(y, s_at + 32 * k + 32);
+            weigh<MASKED>(x, w0, c2, s2, sum, s_at + 16 * k);
+            wait_loads(y);
+            if (k == 0) tmem_load32(x, s_at + 64);
+            weigh<MASKED>(y, w1, c2, s2, sum, s_at + 16 * k + 16);
         }
         const float2 both = add2(sum[0], sum[1]);
         l += both.x + both.y;
@@ -622,10 +704,8 @@ struct Attention {
     // Rows of a piece that see a value of a node which is not finite get it: 32 columns from column d0.
     __device__ void add_odd(const Piece &p, const RowId &id, int d0, uint32_t (&x)[32]) const {
         for (int t = max(p.t0, p.context); t < p.t1; ++t) {
-            uint32_t words[4];
-            seen_words(p, t, id.n, words);
             for (int k = 0; k < 4; ++k)
-                for (uint32_t w = words[k]; w; w &= w - 1) {
+                for (uint32_t w = seen(p, t, id.n, k); w; w &= w - 1) {
                     const int node = (t - p.context) * kTile + 32 * k + __ffs(w) - 1;
                     const T *v = reinterpret_cast<const T *>(a.v) + p.b * a.stride[4] + node * a.stride[5] + p.g * D + d0;
 #pragma unroll
@@ -638,42 +718,37 @@ struct Attention {
     }
     // Columns [d0, d1) of the block's row r: f0 * product 0's sums + f1 * product 1's, to where the piece's go.
     __device__ void write_sums(const Piece &p, int r, int d0, int d1, bool use0, bool use1, float f0, float f1, float m, float l, bool odd) {
-        const uint32_t lanes = c->tmem + (static_cast<uint32_t>(warp & 3) << 21) + kSums;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kSums;
         const bool live = r < p.rows;
         const RowId id = row_id(a, p, live ? r : 0);
         const size_t row = (static_cast<size_t>(id.b) * a.N + id.n) * a.heads + id.h;
         const bool whole = p.t0 == 0 && p.t1 == p.tiles;
         const bool final = whole && a.shared_len == 0;
-        float *to = nullptr;
-        if (!final) {
-            float2 *stats;
-            if (whole) {
-                const size_t i = (p.shared ? static_cast<size_t>(a.B) * a.N * a.heads : 0) + row;
-                to = a.row_sums + i * D;
-                stats = a.row_stats + i;
-            } else {
-                const size_t i = (static_cast<size_t>(blockIdx.x) * 2 + (p.t0 == 0 ? 1 : 0)) * kBlockRows + r;
-                to = a.cut_sums + i * D;
-                stats = a.cut_stats + i;
-            }
-            if (live && d0 == 0) *stats = make_float2(m, l);
-        } else if (live && d0 == 0 && a.lse) {
-            a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+        const Part to = whole ? whole_part<D>(a, p.shared, p.b, p.g, p.first) : cut_part<D>(a, blockIdx.x, p.t0 == 0);
+        if (live && d0 == 0) {
+            if (!final) to.stats[r] = make_float2(m, l);
+            else if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
         }
         const float inv = final ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+#pragma unroll 1
         for (int d = d0; d < d1; d += 32) {
-            uint32_t x[32], y[32];
+            uint32_t x[32];
+            __syncwarp();
             if (use0) {
                 tmem_load32(x, lanes + d);
-                wait_loads();
+                wait_loads(x);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f0);
             }
             if (use1) {
-                tmem_load32(y, lanes + 128 + d);
-                wait_loads();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(use0 ? fmaf(__uint_as_float(y[j]), f1, __uint_as_float(x[j])) : __uint_as_float(y[j]) * f1);
+                for (int h = 0; h < 32; h += 16) {
+                    uint32_t y[16];
+                    tmem_load16(y, lanes + 128 + d + h);
+                    wait_loads(y);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) x[h + j] = __float_as_uint(use0 ? fmaf(__uint_as_float(y[j]), f1, __uint_as_float(x[h + j])) : __uint_as_float(y[j]) * f1);
+                }
             }
             if (live && odd) add_odd(p, id, d, x);
             if (live && final) {
@@ -687,11 +762,8 @@ struct Attention {
                 }
             } else if (live) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                    *reinterpret_cast<float4 *>(to + d + j) =
-                        make_float4(__uint_as_float(x[j]), __uint_as_float(x[j + 1]), __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+                for (int j = 0; j < 32; ++j) to.sums[static_cast<size_t>(d + j) * to.rows + r] = __uint_as_float(x[j]);
             }
-            __syncwarp();  // (the next load takes the whole warp)
         }
     }
     __device__ void softmax(int s, int tid) {
@@ -703,7 +775,7 @@ struct Attention {
         const float scale = a.scale * kLog2e;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, at bit 16
         while (ok && walk.next(&p)) {
-            const uint32_t s_at = c->tmem + lanes + kScores + s * 128, o_at = c->tmem + lanes + kSums + s * 128;
+            const uint32_t s_at = tmem + lanes + kScores + s * 128, o_at = tmem + lanes + kSums + s * 128;
             const int r = tid + (p.two ? s * kTile : 0);  // this thread's row of the block
             const bool idle = (r & ~31) >= p.rows;        // the warp has none
             const int n = row_id(a, p, min(r, p.rows - 1)).n;
@@ -714,15 +786,9 @@ struct Attention {
                 scores_round ^= 1;
                 fence_after();
                 if (!idle) {
-                    const int base = (first_tile(p) + t) * kTile;
-                    const bool masked = t >= p.context || base + kTile > p.len || (!p.shared && base < a.shared_len);
-                    uint32_t words[4];
-                    if (masked) {
-                        seen_words(p, t, n, words);
-                        tile_weights<true>(s_at, o_at, words, scale, first, m, l);
-                    } else {
-                        tile_weights<false>(s_at, o_at, words, scale, first, m, l);
-                    }
+                    const bool masked = t >= p.context || ragged(p, t);
+                    if (masked) tile_weights<true>(p, t, n, s_at, o_at, scale, first, m, l);
+                    else tile_weights<false>(p, t, n, s_at, o_at, scale, first, m, l);
                 }
                 first = false;
                 fence_before();
@@ -798,8 +864,9 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         c->gave_up = 0;
         for (int i = 0; i < 8; ++i) c->odd[i] = 0;
         for (int i = 0; i < 8; ++i) {
-            ptx::mbar_init(ptx::smem_addr(&c->full[i]), 4);
+            ptx::mbar_init(ptx::smem_addr(&c->full[i]), Q8 ? 4 : 5);
             ptx::mbar_init(ptx::smem_addr(&c->empty[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&c->copied[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&c->staged[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&c->free_[i]), 4);
         }
@@ -834,11 +901,17 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     __syncthreads();
     fence_after();
 
-    Attention<T, D, Q8> x{a, c, ptx::smem_addr(smem), ptx::smem_addr(smem) + 2 * L::kQ + L::kRing * L::kQ, lane, warp};
-    if (warp < 8) x.softmax(warp >> 2, tid & 127);
-    else if (warp < 12) x.load_rows(tid - 256);
-    else if (warp == 12) x.load_tiles(&k_map, &v_map);
-    else if (warp == 13) x.multiply();
+    Attention<T, D, Q8> x{a, c, ptx::smem_addr(smem), ptx::smem_addr(smem) + 2 * L::kQ + L::kRing * L::kQ, c->tmem, lane, warp};
+    // Registers of a thread: 2 * 128 * 160 + 2 * 128 * 96 is what the launch has, 512 * 128.
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        x.softmax(warp >> 2, tid & 127);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp < 12) x.load_rows(tid - 256);
+        else if (warp == 12) x.load_tiles(&k_map, &v_map);
+        else if (warp == 13) x.multiply();
+    }
 
     fence_before();
     __syncthreads();
@@ -846,68 +919,67 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
 }
 
 // ------------------------------------------------------------------ joining
-// A warp a row: the partial sums of the blocks that hold it, in the order of their keys.
+// 32 rows of a block, a lane each, D / 8 columns a warp: the partial sums of the pieces that hold them, in the order
+// of their keys, and the result through shared memory, so that it is written in whole lines.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) attention_join_kernel(const AttentionArgs a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const long long rows = static_cast<long long>(a.B) * a.N * a.heads;
-    if (row >= rows) return;
-    const int h = static_cast<int>(row % a.heads), n = static_cast<int>(row / a.heads % a.N), b = static_cast<int>(row / a.heads / a.N);
+__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttentionArgs a) {
+    constexpr int E = D / 8;
+    __shared__ uint32_t result[32][D / 2 + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int chunks = (a.block_rows + 31) / 32;
+    const int first = blockIdx.x % chunks * 32, item = blockIdx.x / chunks;
+    const int block = item % a.blocks, g = item / a.blocks % a.cache.kv_heads, b = item / a.blocks / a.cache.kv_heads;
     const int total = a.starts[a.B], start = a.starts[b], tiles = (a.starts[b + 1] - start) / (a.cache.kv_heads * a.blocks);
     if (tiles == 0) return;  // left out
-    const int g = h / a.group, in_seq = n * a.group + h % a.group;
     const auto owner = [&](int t) { return static_cast<int>(((t + 1ll) * a.ctas - 1) / total); };
+    const int own0 = start + (g * a.blocks + block) * tiles, c0 = owner(own0), c1 = owner(own0 + tiles - 1);
+    if (c0 == c1 && !a.shared_len) return;  // written already
+    const int rows = min(a.block_rows, a.N * a.group - block * a.block_rows);  // of the block
+    const int r = min(first + lane, rows - 1), in_seq = block * a.block_rows + r;
+    const bool live = first + lane < rows;
 
     float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    const auto take = [&](const float *sums, float2 s) {
-        if (s.x == -INFINITY && s.y == 0.0f) return;
+    const auto take = [&](const Part &p, int at) {
+        const float2 s = p.stats[at];
         float x[E];
-        if (E == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(sums + lane * E);
-        else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(sums + lane * E);
-        const float top = fmaxf(m, s.x), was = m == -INFINITY ? 0.0f : ptx::ex2(m - top), now = ptx::ex2(s.x - top);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = p.sums[static_cast<size_t>(warp * E + e) * p.rows + at];
+        const float top = fmaxf(m, s.x), was = m == -INFINITY ? 0.0f : ptx::ex2(m - top), now = s.x == -INFINITY ? 0.0f : ptx::ex2(s.x - top);
         l = l * was + s.y * now;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = o[e] * was + x[e] * now;
         m = top;
     };
-    for (int kind = a.shared_len ? 0 : 1; kind < 2; ++kind) {  // the prefix, then the sequence's own
-        int t0, n_tiles, r;
-        if (kind == 0) {
-            const int all = b * a.N * a.group + in_seq;
-            n_tiles = tiles_of(a.shared_len);
-            t0 = (g * a.shared_blocks + all / a.shared_rows) * n_tiles;
-            r = all % a.shared_rows;
-        } else {
-            n_tiles = tiles;
-            t0 = start + (g * a.blocks + in_seq / a.block_rows) * tiles;
-            r = in_seq % a.block_rows;
-        }
-        const int c0 = owner(t0), c1 = owner(t0 + n_tiles - 1);
-        if (c0 == c1) {
-            if (!a.shared_len) return;  // written already
-            const size_t i = static_cast<size_t>(kind == 0 ? rows : 0) + row;
-            take(a.row_sums + i * D, a.row_stats[i]);
-            continue;
-        }
-        for (int c = c0; c <= c1; ++c) {
+    const auto pieces = [&](int t0, int from, int to, int at) {  // of a block whose tiles begin at t0
+        for (int c = from; c <= to; ++c) {
             const int lo = static_cast<int>(static_cast<long long>(c) * total / a.ctas);
             if (lo == static_cast<int>((c + 1ll) * total / a.ctas)) continue;  // a CTA without tiles
-            const size_t i = (static_cast<size_t>(c) * 2 + (t0 < lo ? 0 : 1)) * kBlockRows + r;
-            take(a.cut_sums + i * D, a.cut_stats[i]);
+            take(cut_part<D>(a, c, t0 >= lo), at);
         }
+    };
+    if (a.shared_len) {  // the prefix comes first; the rows of a block may lie in two of its blocks
+        const int all = b * a.N * a.group + in_seq, at = all % a.shared_rows, part = all / a.shared_rows, n = tiles_of(a.shared_len);
+        const int t0 = (g * a.shared_blocks + part) * n, s0 = owner(t0), s1 = owner(t0 + n - 1);
+        if (s0 == s1) take(whole_part<D>(a, true, 0, g, part * a.shared_rows), at);
+        else pieces(t0, s0, s1, at);
     }
+    if (c0 == c1) take(whole_part<D>(a, false, b, g, block * a.block_rows), r);
+    else pieces(own0, c0, c1, r);
+
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint32_t w[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) w[e / 2] = Elt<T>::from_float2(o[e] * inv, o[e + 1] * inv);
-    uint32_t *out = reinterpret_cast<uint32_t *>(a.out) + row * (D / 2) + lane * (E / 2);
-    if (E == 4) *reinterpret_cast<uint2 *>(out) = make_uint2(w[0], w[E / 2 - 1]);
-    else out[0] = w[0];
-    if (a.lse && lane == 0) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+    for (int e = 0; e < E; e += 2) result[lane][(warp * E + e) / 2] = Elt<T>::from_float2(o[e] * inv, o[e + 1] * inv);
+    const size_t row = (static_cast<size_t>(b) * a.N + in_seq / a.group) * a.heads + g * a.group + in_seq % a.group;
+    if (a.lse && warp == 0 && live) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+    __syncthreads();
+    for (int i = threadIdx.x; i < 32 * (D / 2); i += 256) {
+        const int k = i / (D / 2), x = i % (D / 2), s = block * a.block_rows + first + k;
+        if (first + k >= rows) break;
+        const size_t to = (static_cast<size_t>(b) * a.N + s / a.group) * a.heads + g * a.group + s % a.group;
+        reinterpret_cast<uint32_t *>(a.out)[to * (D / 2) + x] = result[k][x];
+    }
 }
 
 }  // namespace context

@@ -37,9 +37,9 @@ struct AttentionArgs {
     int ctas;
     // the workspace
     int32_t *starts;   // [B + 1] tiles before each sequence's
-    float *cut_sums;   // [ctas][2][kBlockRows][D]: blocks cut at a CTA's begin and at its end
+    float *cut_sums;   // [ctas][2][D][kBlockRows]: blocks cut at a CTA's begin and at its end
     float2 *cut_stats; // ... their rows' (maximum in units of log 2, sum)
-    float *row_sums;   // [2][B * N * heads][D], with a shared prefix: blocks that one CTA took whole, the sequence's own and the prefix's
+    float *row_sums;   // [2][kv_heads][blocks' rows, D columns a block], with a prefix: whole blocks, the sequences' own and the prefix's
     float2 *row_stats;
 };
 

@@ -47,8 +47,8 @@ spec_status launch_attention(const AttentionArgs &a0, cudaStream_t stream) {
     kernel<<<a.ctas, kAttentionThreads, smem, stream>>>(a, maps[0], maps[1]);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
-    const long long rows = static_cast<long long>(a.B) * a.N * a.heads;
-    attention_join_kernel<T, D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, stream>>>(a);
+    const long long join = static_cast<long long>(a.B) * a.cache.kv_heads * a.blocks * ((a.block_rows + 31) / 32);
+    attention_join_kernel<T, D><<<static_cast<unsigned>(join), 256, 0, stream>>>(a);
     e = cudaGetLastError();
     return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "join launch: %s", cudaGetErrorString(e));
 }

@@ -22,7 +22,23 @@ __device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The warp's loads are done; `r` is named so that nothing that uses it moves ahead of this.
+__device__ __forceinline__ void wait_loads(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), 
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), 
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), 
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void wait_loads(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), 
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 columns of the warp's 32 lanes, a lane a thread.
@@ -34,6 +50,13 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t at) {
           "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
           "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
           "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(at));
 }
 __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
@@ -55,11 +78,18 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16
 }
 
 // ---- tcgen05.mma, kind::f16, one CTA: D[128 x n] (fp32, tensor memory) (+)= A[128 x 16] B[16 x n]
-// A shared-memory operand in rows of 128 bytes, swizzled over 8 rows (1024 bytes); `lead`: bytes
-// between groups of 64 columns of an operand whose rows run along the product's inner axis.
-__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t lead) {
-    return static_cast<uint64_t>((at & 0x3ffff) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 | static_cast<uint64_t>(1024 >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
+// The low word of a shared-memory operand in rows of 128 bytes, swizzled over 8 rows (1024 bytes); `lead`: bytes
+// between groups of 64 columns of an operand whose rows run along the product's inner axis.  A step of
+// 16 bytes is 1.
+__device__ __forceinline__ uint32_t operand(uint32_t at, uint32_t lead) { return (at & 0x3ffff) >> 4 | lead >> 4 << 16; }
+__device__ __forceinline__ uint64_t descriptor(uint32_t low) {
+    constexpr uint32_t kHigh = 1024 >> 4 | 1u << 14 | 2u << 29;  // 1024 bytes between groups of 8 rows; version; swizzle
+    return static_cast<uint64_t>(kHigh) << 32 | low;
+}
+__device__ __forceinline__ bool elect() {  // one lane of a whole warp
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 // `type`: 0 fp16, 1 bf16; `rows_inner`: B's rows run along the inner axis (its columns are contiguous).
 constexpr uint32_t instruction(uint32_t type, uint32_t n, bool rows_inner) {

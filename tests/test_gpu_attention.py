@@ -106,7 +106,10 @@ def test_a_shared_prefix(q8, B, N, H, kv, D, page, shared, lens):
 
 def test_many_sequences_and_long_contexts():
     """More work than CTAs, and contexts that many CTAs share."""
-    check_all = lambda s: check(call(s), s)  # noqa: E731
+    def check_all(s):
+        r = call(s)
+        assert int(r["status"][0]) == 0
+        check(r, s)
     check_all(problem(120, 2, 4, 2, 64, 16, [(37 * b) % 300 for b in range(120)], BF, True, seed=4))
     check_all(problem(1, 2, 2, 1, 128, 128, [40000], BF, False, seed=5))
     check_all(problem(2, 3, 8, 4, 64, 64, [9000, 5], F16, True, seed=6))
@@ -121,7 +124,9 @@ def test_long_contexts_behind_each_other(q8):
               problem(40, 3, 8, 4, 128, 64, [(2000 * b) % 1777 + 1 for b in range(40)], BF, q8, seed=12),
               problem(12, 40, 8, 2, 64, 16, [1300 - 100 * b for b in range(12)], F16, q8, seed=13),
               problem(3, 1024, 1, 1, 128, 64, [900, 1100, 300], BF, q8, seed=14)):
-        check(call(s), s)
+        r = call(s)
+        assert int(r["status"][0]) == 0
+        check(r, s)
 
 
 def test_masks():
