@@ -10,10 +10,9 @@
 // two sums are joined at the end.  While one warpgroup computes weights, the other's products run.
 //
 //   warps 0-3, 4-7   softmax of product 0, 1: a thread a row
-//   warps 8-11       loads by plain instructions: Q, the nodes' keys and values, 8-bit tiles widened,
-//                    last tiles of values (what lies behind a sequence's end must be 0: 0 * NaN is NaN)
-//   warp 12          TMA
-//   warp 13          tcgen05.mma
+//   four warps       values whose other rows must be 0 (what lies behind a sequence's end, nodes that are
+//                    not finite: 0 * NaN is NaN); eight of them where 8-bit tiles are widened too
+//   one warp each    TMA of tiles; tcgen05.mma; TMA of queries; TMA of 8-bit tiles
 //
 // The softmax keeps a row's running maximum as it was until a tile's exceeds it by 2^8: weights up to 2^8
 // lose nothing in a float format, and O is rescaled almost never.
@@ -28,15 +27,19 @@
 namespace spec {
 namespace context {
 
-constexpr int kAttentionThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D, bool Q8>
 struct Layout {
     static constexpr int kQ = kTile * D * 2;     // bytes of 128 rows of queries, keys or values
-    static constexpr int kRing = Q8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    static constexpr int kRing = Q8 ? (D == 128 ? 4 : 6) : (D == 128 ? 5 : 8);
     static constexpr int kStage = Q8 ? kTile * D : 0;
-    static constexpr int kStages = Q8 ? (D == 128 ? 4 : 8) : 0;
+    static constexpr int kStages = Q8 ? (D == 128 ? 2 : 8) : 0;
+    static constexpr int kWorkers = Q8 ? 8 : 4;              // warps that clear and widen
+    static constexpr int kThreads = (8 + kWorkers + 4) * 32;
+    // Registers of a thread after the start: the sum over the warps is what the launch has (65536 at 512
+    // threads, 640 * 96 at 640).
+    static constexpr int kSoftmaxRegs = Q8 ? 152 : 192, kOtherRegs = Q8 ? 56 : 64;
     static constexpr int kBytes = 2 * kQ + kRing * kQ + kStages * kStage;
 };
 
@@ -51,7 +54,7 @@ struct Control {  // behind the tiles in shared memory
     uint32_t tmem;
     int gave_up;
     int odd[8];                    // a value of the piece's nodes is not finite (by piece, in turn)
-    int scan[16];
+    int scan[20];
     int total, b, before;          // tiles in all; the sequence a CTA begins in and the tiles before it
     float2 stats[2][kTile];
 };
@@ -104,7 +107,7 @@ struct Walk {
         const int all = shared ? a.B * a.N * a.group : a.N * a.group;
         const int block = item % blocks;
         p->shared = shared;
-        p->two = rows > kTile;
+        p->two = rows > a.half_nodes * a.group;
         p->b = shared ? 0 : b;
         p->g = item / blocks;
         p->first = block * rows;
@@ -277,72 +280,134 @@ struct Attention {
     __device__ __forceinline__ int begin(const Piece &p) const { return p.shared ? 0 : a.shared_len; }  // the piece's first position
 
     // ---- TMA
-    __device__ void load_tiles(const CUtensorMap *k_map, const CUtensorMap *v_map) {
+    // The keys and values of one tile of the context, in boxes of at most a page: lane i the i-th.
+    struct Boxes {
+        int page, y;
+    };
+    __device__ __forceinline__ Boxes boxes_of(const Piece &p, int t, int box, bool &bad) const {
+        const long long pos = static_cast<long long>(first_tile(p) + t) * kTile + lane * box;
+        Boxes b{a.cache.pages, (p.g << a.cache.page_bits) + static_cast<int>(pos & ((1 << a.cache.page_bits) - 1))};  // outside: zeros
+        if (lane < kTile / box && pos < p.len && pos + box > begin(p)) {
+            const int entry = __ldg(a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width + (pos >> a.cache.page_bits));
+            if (entry < 0 || entry >= a.cache.pages) bad = true;
+            else b.page = entry;
+        }
+        return b;
+    }
+    __device__ __forceinline__ int box_rows() const { return min(1 << a.cache.page_bits, kTile); }
+    // No copy is in flight when the CTA ends: where a wait gave up, the last one into each of the n slots is waited for
+    // (`rounds`: the parities of their barriers' phases).
+    __device__ void drain(const uint64_t *bars, int n, uint32_t issued, uint32_t rounds) {
+        for (int i = 0; i < n; ++i) {
+            bool done = !(issued >> i & 1);
+            for (int k = 0; !done && k < kWaitTries; ++k) done = ptx::mbar_try_wait(ptx::smem_addr(bars + i), rounds >> i & 1);
+        }
+    }
+    // Tiles into the ring: of a 16-bit cache, and of the nodes.  Each round of each slot is waited for and
+    // arrived at by this warp and by the workers, whichever fills it: a parity tells a round from its
+    // neighbours alone, so none may run ahead of the ring by more than a round, or fall behind it.
+    __device__ void load_tiles(const Maps &maps) {
         Walk walk(a, c);
         Piece p;
         Cursor at;
         // tiles that one block takes are read once; where several blocks take them, L2 may keep them
-        const uint64_t first = ptx::policy_evict_first(), normal = policy_evict_normal();
-        const int box = min(1 << a.cache.page_bits, kTile), boxes = kTile / box;
+        const uint64_t once = ptx::policy_evict_first(), normal = policy_evict_normal();
+        const int box = box_rows();
         bool bad = false, ok = true;
-        uint32_t issued = 0, rounds = 0, copies = 0;  // a bit a slot: it was loaded into; the parity of the last such round, of copies
-        const int slots = Q8 ? L::kStages : L::kRing;
+        uint32_t issued = 0, rounds = 0, copied = 0, copies = 0;  // a bit a slot: loaded; its last phase's parity; the same of `copied`
         while (ok && walk.next(&p)) {
-            const int32_t *table = a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width;
-            const uint64_t policy = (p.shared ? a.shared_blocks : a.blocks) == 1 ? first : normal;
+            const uint64_t policy = (p.shared ? a.shared_blocks : a.blocks) == 1 ? once : normal;
             for (int t = p.t0; ok && t < p.t1; ++t) {
-                // lane i: the tile's i-th box of keys
-                const long long pos = static_cast<long long>(first_tile(p) + t) * kTile + lane * box;
-                int page = a.cache.pages;  // outside: zeros
-                if (t < p.context && lane < boxes && pos < p.len && pos + box > begin(p)) {
-                    const int entry = __ldg(table + (pos >> a.cache.page_bits));
-                    if (entry < 0 || entry >= a.cache.pages) bad = true;
-                    else page = entry;
-                }
-                for (int w = 0; w < 2; ++w) {
-                    const bool mine = t < p.context;
-                    if (Q8 && !mine) continue;
-                    const uint64_t *full = Q8 ? &c->staged[at.slot] : &c->full[at.slot], *empty = Q8 ? &c->free_[at.slot] : &c->empty[at.slot];
-                    // Each round of each slot is waited for and arrived at by this warp and by the four that load
-                    // rows, whichever fills it: a parity tells a round from its neighbours alone, so none may
-                    // run ahead of the ring by more than a round, or fall behind it.
-                    if (!(ok = wait(empty, at.round ^ 1))) break;
-                    if (!mine) {
-                        if (lane == 0) arrive(ptx::smem_addr(full));
+                Boxes boxes;
+                if (!Q8 && t < p.context) boxes = boxes_of(p, t, box, bad);
+                for (int w = 0; w < 2; ++w, at.step(L::kRing)) {
+                    if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
+                    const uint32_t full = ptx::smem_addr(&c->full[at.slot]), to = ring(at.slot), bit = 1u << at.slot;
+                    if (Q8 && t < p.context) {
+                        if (lane == 0) arrive(full);
                         __syncwarp();
-                        at.step(slots);
                         continue;
                     }
-                    // (values whose other rows are to be cleared: their copy is waited for by those who do that)
-                    const bool cleared = !Q8 && w && ragged(p, t);
-                    if (cleared && lane == 0) arrive(ptx::smem_addr(full));
-                    const uint32_t bar = ptx::smem_addr(cleared ? &c->copied[at.slot] : full), to = Q8 ? stages + at.slot * L::kStage : ring(at.slot);
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, Q8 ? L::kStage : L::kQ);
-                    __syncwarp();
-                    if (lane < boxes) {
-                        const int y = (p.g << a.cache.page_bits) + static_cast<int>(pos & ((1 << a.cache.page_bits) - 1));
-                        if (Q8) tma_load3(to + lane * box * D, w ? v_map : k_map, 0, y, page, bar, policy);
-                        else
-                            for (int x = 0; x < D; x += 64) tma_load3(to + (x / 64) * (kTile * 128) + lane * box * 128, w ? v_map : k_map, x, y, page, bar, policy);
+                    // Values that the workers look through first: their copy is waited for there.
+                    const bool checked = w && (t >= p.context || ragged(p, t));
+                    const uint32_t bar = checked ? ptx::smem_addr(&c->copied[at.slot]) : full;
+                    if (lane == 0) {
+                        if (checked) arrive(full);
+                        ptx::mbar_arrive_expect_tx(bar, L::kQ);
                     }
-                    issued |= 1u << at.slot;
-                    rounds = (rounds & ~(1u << at.slot)) | at.round << at.slot;
-                    if (cleared) copies ^= 1u << at.slot;
-                    at.step(slots);
+                    __syncwarp();
+                    if (t >= p.context) {
+                        if (lane < D / 64) tma_load4(to + lane * (kTile * 128), w ? &maps.v_nodes : &maps.k_nodes, lane * 64, p.g, (t - p.context) * kTile, p.b, bar, normal);
+                    } else if (lane < kTile / box) {
+                        for (int x = 0; x < D; x += 64) tma_load3(to + (x / 64) * (kTile * 128) + lane * box * 128, w ? &maps.v : &maps.k, x, boxes.y, boxes.page, bar, policy);
+                    }
+                    if (checked) copied |= bit, copies ^= bit;
+                    else issued |= bit, rounds = (rounds & ~bit) | at.round << at.slot;
                 }
             }
         }
         if (bad) atomicOr(a.status, SPEC_DEV_BAD_PAGE);
-        // No copy is in flight when the CTA ends: where a wait gave up, each slot's last one is waited for.
         if (!ok) {
-            for (int i = 0; i < slots; ++i) {
-                const uint32_t bar = ptx::smem_addr(Q8 ? &c->staged[i] : &c->full[i]);
-                bool done = !(issued >> i & 1);
-                for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(bar, rounds >> i & 1);
-                done = Q8 || !(issued >> i & 1);
-                for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(ptx::smem_addr(&c->copied[i]), (copies >> i & 1) ^ 1);
+            drain(c->full, L::kRing, issued, rounds);
+            drain(c->copied, L::kRing, copied, ~copies);
+        }
+    }
+    // 8-bit tiles, to be widened.
+    __device__ void load_stages(const Maps &maps) {
+        Walk walk(a, c);
+        Piece p;
+        Cursor at;
+        const uint64_t once = ptx::policy_evict_first(), normal = policy_evict_normal();
+        const int box = box_rows();
+        bool bad = false, ok = true;
+        uint32_t issued = 0, rounds = 0;
+        while (ok && walk.next(&p)) {
+            const uint64_t policy = (p.shared ? a.shared_blocks : a.blocks) == 1 ? once : normal;
+            for (int t = p.t0; ok && t < min(p.t1, p.context); ++t) {
+                const Boxes boxes = boxes_of(p, t, box, bad);
+                for (int w = 0; w < 2; ++w) {
+                    if (!(ok = wait(&c->free_[at.slot], at.round ^ 1))) break;
+                    const uint32_t bar = ptx::smem_addr(&c->staged[at.slot]);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStage);
+                    __syncwarp();
+                    if (lane < kTile / box) tma_load3(stages + at.slot * L::kStage + lane * box * D, w ? &maps.v : &maps.k, 0, boxes.y, boxes.page, bar, policy);
+                    issued |= 1u << at.slot;
+                    rounds = (rounds & ~(1u << at.slot)) | at.round << at.slot;
+                    at.step(L::kStages > 0 ? L::kStages : 1);
+                }
             }
         }
+        if (bad) atomicOr(a.status, SPEC_DEV_BAD_PAGE);
+        if (!ok) drain(c->staged, L::kStages, issued, rounds);
+    }
+    // Queries: a half holds a.half_nodes nodes, whose heads of the group lie next to each other.
+    __device__ void load_queries(const Maps &maps) {
+        Walk walk(a, c);
+        Piece p;
+        const uint64_t normal = policy_evict_normal();
+        uint32_t round = 0, issued = 0;  // a bit a half
+        int half = 0, count = 0;
+        bool ok = true;
+        while (ok && walk.next(&p)) {
+            if (p.two) half = 0;
+            for (int h = 0; ok && h < 2; ++h) {
+                if (!p.two && h != half) continue;
+                if (!(ok = wait(&c->q_empty[h], (round >> h & 1) ^ 1))) break;
+                round ^= 1u << h;
+                issued |= 1u << h;
+                // (the piece four on: none is read that far back, nor loaded that far ahead)
+                if (lane == 0) *const_cast<volatile int *>(&c->odd[(count + 4) & 7]) = 0;
+                const uint32_t bar = ptx::smem_addr(&c->q_full[h]);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, a.q_nodes * a.group * D * 2);
+                __syncwarp();
+                const int node = p.first / a.group + (p.two ? h * a.half_nodes : 0);
+                const int z = a.q_merged && !p.shared ? p.b * a.N + node : node, b = a.q_merged ? 0 : p.b;
+                if (lane < D / 64) tma_load4(tiles + h * L::kQ + lane * (kTile * 128), &maps.q, lane * 64, p.g * a.group, z, b, bar, normal);
+            }
+            ++count;
+            if (!p.two) half ^= 1;
+        }
+        if (!ok) drain(c->q_full, 2, issued, ~round);
     }
 
     // ---- tcgen05.mma
@@ -427,178 +492,128 @@ struct Attention {
         for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(ptx::smem_addr(&c->drained), 0);
     }
 
-    // ---- plain loads: a row of D elements by D / 8 lanes, a tile's all under way at once; they are issued
-    // before the warp waits for the place in shared memory that they go to
-    static constexpr int kLanes = D / 8, kLoads = kTile * kLanes / 128;  // lanes a row, 16-byte loads a thread
-    struct Loaded {
-        uint4 v[kLoads];
-    };
-    __device__ __forceinline__ void place(const Loaded &x, uint32_t to, int tid) const {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) store16(to + chunk_at(tid / kLanes + i * (128 / kLanes), tid % kLanes), x.v[i]);
-    }
-    // Rows of queries; those the block lacks are 0.
-    __device__ __forceinline__ void load_queries(const Piece &p, int from, int tid, Loaded &x) const {
-        constexpr int kStep = 128 / kLanes;  // rows from one load of a thread to its next
-        int r = from + tid / kLanes;
-        RowId id = row_id(a, p, r);
-        const int h0 = p.g * a.group, more_n = kStep / a.group, more_h = kStep % a.group;
-        const T *q = reinterpret_cast<const T *>(a.q) + tid % kLanes * 8;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            x.v[i] = make_uint4(0, 0, 0, 0);
-            if (r < p.rows) x.v[i] = __ldg(reinterpret_cast<const uint4 *>(q + id.b * a.stride[0] + id.n * a.stride[1] + id.h * D));
-            r += kStep;
-            id.n += more_n;
-            id.h += more_h;
-            if (id.h >= h0 + a.group) id.h -= a.group, ++id.n;
-            while (p.shared && id.n >= a.N) id.n -= a.N, ++id.b;
-        }
-    }
+    // ---- workers: a thread a row, or two threads where there are eight warps
+    static constexpr int kLanes = D / 8, kSplit = L::kWorkers / 4, kShare = kLanes / kSplit;  // 16-byte chunks of a row; of a thread
     __device__ __forceinline__ static bool odd_pair(uint32_t x) {  // an infinity or NaN among two elements
         constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
         return (x & e) == e || (x >> 16 & e) == e;
     }
-    // Keys or values of the nodes; rows past the last are 0.
-    __device__ __forceinline__ void load_nodes(const Piece &p, int t, bool values, int tid, Loaded &x) const {
-        const int m0 = (t - p.context) * kTile;
-        const T *src = reinterpret_cast<const T *>(values ? a.v : a.k) + p.b * a.stride[values ? 4 : 2] + p.g * D;
-        const long long step = a.stride[values ? 5 : 3];
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int m = m0 + tid / kLanes + i * (128 / kLanes);
-            x.v[i] = make_uint4(0, 0, 0, 0);
-            if (m < a.N) x.v[i] = __ldg(reinterpret_cast<const uint4 *>(src + m * step) + tid % kLanes);
-        }
+    // The rows of a tile of values outside [from, to) become 0.
+    __device__ __forceinline__ void clear_rows(uint32_t at, int tid, int from, int to) const {
+        const int r = tid & 127;
+        if (r >= from && r < to) return;
+#pragma unroll 4
+        for (int x = 0; x < kShare; ++x) store16(at + chunk_at(r, (tid >> 7) * kShare + x), make_uint4(0, 0, 0, 0));
     }
-    // Values that are not finite become 0 (true: there were some): a row that does not see them would get
-    // 0 * NaN.  The rows that do are given them at the end.
-    __device__ __forceinline__ bool take_odd(Loaded &x) const {
+    // Values of nodes that are not finite become 0 (true: there were some): a row that does not see them would
+    // get 0 * NaN.  The rows that do are given them at the end.
+    __device__ __forceinline__ bool take_odd(uint32_t at, int tid) const {
         bool odd = false;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) odd |= odd_pair(x.v[i].x) || odd_pair(x.v[i].y) || odd_pair(x.v[i].z) || odd_pair(x.v[i].w);
-        if (odd) {
-            constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
-#pragma unroll
-            for (int i = 0; i < kLoads; ++i) {
-                uint32_t *w = reinterpret_cast<uint32_t *>(&x.v[i]);
+#pragma unroll 4
+        for (int i = 0; i < kShare; ++i) {
+            const uint32_t to = at + chunk_at(tid & 127, (tid >> 7) * kShare + i);
+            uint4 v = load16(to);
+            if (odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w)) {
+                constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
+                uint32_t *w = reinterpret_cast<uint32_t *>(&v);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if ((w[k] & e) == e) w[k] &= 0xffff0000u;
                     if ((w[k] >> 16 & e) == e) w[k] &= 0xffffu;
                 }
+                store16(to, v);
+                odd = true;
             }
         }
         return odd;
     }
     // The page of this thread's row of a piece's tile t, -1 where there is none; the scales of its keys and values.
-    __device__ __forceinline__ int row_page(const Piece &p, int t, int tid) const {
-        const int pos = (first_tile(p) + t) * kTile + tid;
+    __device__ __forceinline__ int row_page(const Piece &p, int t, int r) const {
+        const int pos = (first_tile(p) + t) * kTile + r;
         if (t >= min(p.t1, p.context) || pos >= p.len || pos < begin(p)) return -1;
         const int page = __ldg(a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width + (pos >> a.cache.page_bits));
         return page < a.cache.pages ? page : -1;
     }
-    __device__ __forceinline__ int row_scales(const Piece &p, int t, int tid, int page) const {  // keys', values' << 8; -1: no row
+    __device__ __forceinline__ int row_scales(const Piece &p, int t, int r, int page) const {  // keys', values' << 8; -1: no row
         if (page < 0) return -1;
-        const int pos = (first_tile(p) + t) * kTile + tid;
+        const int pos = (first_tile(p) + t) * kTile + r;
         const size_t row = cache_row(a.cache, (static_cast<long long>(page) << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1)), p.g);
         return __ldg(a.cache.scale[0] + row) | __ldg(a.cache.scale[1] + row) << 8;
     }
-    // An 8-bit tile, widened: a thread a row; the chunks in turned order, so that eight rows' meet different banks.
+    // An 8-bit tile, widened: half a row a thread; the chunks in turned order, so that eight rows' meet different banks.
     template <bool TWICE>
-    __device__ __forceinline__ void widen(uint32_t from, uint32_t to, int r, const Widen<T> &w) const {
-        constexpr int kChunks = D / 16, kAhead = 4;
+    __device__ __forceinline__ void widen(uint32_t from, uint32_t to, int tid, const Widen<T> &w) const {
+        constexpr int kChunks = D / 32;
+        const int r = tid & 127;
+        uint4 v[kChunks];
 #pragma unroll
-        for (int j0 = 0; j0 < kChunks; j0 += kAhead) {
-            uint4 v[kAhead];
+        for (int j = 0; j < kChunks; ++j) v[j] = load16(from + r * D + turned(j, tid) * 16);
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) v[j] = load16(from + r * D + turned(j0 + j, r) * 16);
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int x = turned(j0 + j, r);
-                const uint2 b0 = w.template four<TWICE>(v[j].x), b1 = w.template four<TWICE>(v[j].y);
-                store16(to + chunk_at(r, 2 * x), make_uint4(b0.x, b0.y, b1.x, b1.y));
-                const uint2 b2 = w.template four<TWICE>(v[j].z), b3 = w.template four<TWICE>(v[j].w);
-                store16(to + chunk_at(r, 2 * x + 1), make_uint4(b2.x, b2.y, b3.x, b3.y));
-            }
+        for (int j = 0; j < kChunks; ++j) {
+            const int x = turned(j, tid);
+            const uint2 b0 = w.template four<TWICE>(v[j].x), b1 = w.template four<TWICE>(v[j].y);
+            store16(to + chunk_at(r, 2 * x), make_uint4(b0.x, b0.y, b1.x, b1.y));
+            const uint2 b2 = w.template four<TWICE>(v[j].z), b3 = w.template four<TWICE>(v[j].w);
+            store16(to + chunk_at(r, 2 * x + 1), make_uint4(b2.x, b2.y, b3.x, b3.y));
         }
     }
-    static __device__ __forceinline__ int turned(int j, int r) { return D == 128 ? (j + r) & 7 : (j + (r >> 1)) & 3; }
-    // The rows of a tile of values outside [from, to) become 0.
-    __device__ __forceinline__ void clear_rows(uint32_t at, int r, int from, int to) const {
-        if (r >= from && r < to) return;
-#pragma unroll 4
-        for (int x = 0; x < kLanes; ++x) store16(at + chunk_at(r, x), make_uint4(0, 0, 0, 0));
+    // The j-th chunk of thread tid's half row: of 16 bytes, eight rows' in one step lie in eight places modulo 128 bytes.
+    static __device__ __forceinline__ int turned(int j, int tid) {
+        const int k = j + (tid >> 7) * (D / 32);
+        return D == 128 ? (k + tid) & 7 : (k + (tid >> 1)) & 3;
     }
-    __device__ void load_rows(int tid) {
+    __device__ void work(int tid) {
         Walk walk(a, c);
         Piece p;
         Cursor at, staged;
-        uint32_t q_round[2] = {0, 0}, copies = 0;  // the parity of each slot's next copy to clear
-        int half = 0, count = 0;
+        uint32_t copies = 0;  // the parity of each slot's next copy to look through
+        int count = 0;
         bool ok = true;
+        const int r = tid & 127;
         while (ok && walk.next(&p)) {
             int scales = -1, next_page = -1;  // of the tile at hand; of the one after it
             if (Q8) {
-                scales = row_scales(p, p.t0, tid, row_page(p, p.t0, tid));
-                next_page = row_page(p, p.t0 + 1, tid);
-            }
-            if (p.two) half = 0;
-            for (int h = 0; ok && h < 2; ++h) {
-                if (!p.two && h != half) continue;
-                Loaded x;
-                load_queries(p, p.two ? h * kTile : 0, tid, x);
-                if (!(ok = wait(&c->q_empty[h], q_round[h] ^ 1))) break;
-                q_round[h] ^= 1;
-                // (the piece four on: none is read that far back, nor loaded that far ahead)
-                if (tid == 0) *const_cast<volatile int *>(&c->odd[(count + 4) & 7]) = 0;
-                place(x, tiles + h * L::kQ, tid);
-                fence_async();
-                __syncwarp();
-                if (lane == 0) arrive(ptx::smem_addr(&c->q_full[h]));
+                scales = row_scales(p, p.t0, r, row_page(p, p.t0, r));
+                next_page = row_page(p, p.t0 + 1, r);
             }
             for (int t = p.t0; ok && t < p.t1; ++t) {
                 int next_scales = -1;
                 if (Q8) {  // two dependent loads, each issued a tile ahead of its use
-                    next_scales = row_scales(p, t + 1, tid, next_page);
-                    next_page = row_page(p, t + 2, tid);
+                    next_scales = row_scales(p, t + 1, r, next_page);
+                    next_page = row_page(p, t + 2, r);
                 }
                 for (int w = 0; ok && w < 2; ++w, at.step(L::kRing)) {
                     const uint32_t to = ring(at.slot);
+                    if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
                     if (Q8 && t < p.context) {
+                        if (!(ok = wait(&c->staged[staged.slot], staged.round))) break;
                         Widen<T> x;
                         if (scales >= 0) x.scale(scales >> (8 * w) & 255);
                         else x.zero();
-                        if (!(ok = wait(&c->empty[at.slot], at.round ^ 1) && wait(&c->staged[staged.slot], staged.round))) break;
                         const uint32_t from = stages + staged.slot * L::kStage;
                         if (__any_sync(0xffffffffu, x.twice)) widen<true>(from, to, tid, x);
                         else widen<false>(from, to, tid, x);
                         __syncwarp();
                         if (lane == 0) arrive(ptx::smem_addr(&c->free_[staged.slot]));
                         staged.step(L::kStages > 0 ? L::kStages : 1);
-                    } else if (t < p.context) {
-                        if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
-                        if (w && ragged(p, t)) {
-                            if (!(ok = wait(&c->copied[at.slot], copies >> at.slot & 1))) break;
-                            copies ^= 1u << at.slot;
+                        fence_async();
+                    } else if (w && (t >= p.context || ragged(p, t))) {
+                        if (!(ok = wait(&c->copied[at.slot], copies >> at.slot & 1))) break;
+                        copies ^= 1u << at.slot;
+                        if (t < p.context) {
                             const int base = (first_tile(p) + t) * kTile;
                             clear_rows(to, tid, begin(p) - base, p.len - base);
+                        } else if (take_odd(to, tid)) {
+                            *const_cast<volatile int *>(&c->odd[count & 7]) = 1;
                         }
-                    } else {
-                        Loaded x;
-                        load_nodes(p, t, w, tid, x);
-                        if (w && take_odd(x)) *const_cast<volatile int *>(&c->odd[count & 7]) = 1;
-                        if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
-                        place(x, to, tid);
+                        fence_async();
                     }
-                    fence_async();
                     __syncwarp();
                     if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
                 }
                 scales = next_scales;
             }
             ++count;
-            if (!p.two) half ^= 1;
         }
     }
 
@@ -776,8 +791,8 @@ struct Attention {
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, at bit 16
         while (ok && walk.next(&p)) {
             const uint32_t s_at = tmem + lanes + kScores + s * 128, o_at = tmem + lanes + kSums + s * 128;
-            const int r = tid + (p.two ? s * kTile : 0);  // this thread's row of the block
-            const bool idle = (r & ~31) >= p.rows;        // the warp has none
+            const int own = tid < a.half_nodes * a.group ? tid : kBlockRows, r = own + (p.two ? s * a.half_nodes * a.group : 0);  // this thread's row of the block
+            const bool idle = __all_sync(0xffffffffu, r >= p.rows);  // the warp has none
             const int n = row_id(a, p, min(r, p.rows - 1)).n;
             float m = -INFINITY, l = 0.0f;
             bool first = true;
@@ -817,7 +832,7 @@ struct Attention {
                 const float2 x = c->stats[0][tid], y = any == 2 ? c->stats[1][tid] : make_float2(-INFINITY, 0.0f);
                 const float top = fmaxf(x.x, y.x);
                 const float f0 = x.x == -INFINITY ? 0.0f : ptx::ex2(x.x - top), f1 = y.x == -INFINITY ? 0.0f : ptx::ex2(y.x - top);
-                if (!idle) write_sums(p, tid, s * (D / 2), (s + 1) * (D / 2), true, any == 2, f0, f1, top, x.y * f0 + y.y * f1, odd);
+                if (!idle) write_sums(p, r, s * (D / 2), (s + 1) * (D / 2), true, any == 2, f0, f1, top, x.y * f0 + y.y * f1, odd);
                 fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(ptx::smem_addr(&c->joined[1]));
@@ -831,15 +846,15 @@ struct Attention {
 };
 
 template <typename T, int D, bool Q8>
-__global__ void __launch_bounds__(kAttentionThreads, 1)
-    attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+__global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Maps maps) {
     using L = Layout<D, Q8>;
+    constexpr int kThreads = L::kThreads;
     extern __shared__ __align__(1024) unsigned char smem[];
     Control *c = reinterpret_cast<Control *>(smem + L::kBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     // Every CTA counts the tiles before each sequence: a thread some sequences, then a scan over threads.
-    const int per = (a.B + kAttentionThreads - 1) / kAttentionThreads;
+    const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     const int room = a.cache.table_width << a.cache.page_bits, nodes = tiles_of(a.N), per_seq = a.cache.kv_heads * a.blocks;
     const int shared_tiles = tiles_of(a.shared_len) * a.cache.kv_heads * a.shared_blocks;
@@ -864,14 +879,14 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         c->gave_up = 0;
         for (int i = 0; i < 8; ++i) c->odd[i] = 0;
         for (int i = 0; i < 8; ++i) {
-            ptx::mbar_init(ptx::smem_addr(&c->full[i]), Q8 ? 4 : 5);
+            ptx::mbar_init(ptx::smem_addr(&c->full[i]), L::kWorkers + 1);
             ptx::mbar_init(ptx::smem_addr(&c->empty[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&c->copied[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&c->staged[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&c->free_[i]), 4);
+            ptx::mbar_init(ptx::smem_addr(&c->free_[i]), L::kWorkers);
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(ptx::smem_addr(&c->q_full[i]), 4);
+            ptx::mbar_init(ptx::smem_addr(&c->q_full[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&c->q_empty[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&c->scores[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&c->weights[i]), 4);
@@ -884,7 +899,7 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
     __syncthreads();
     int before = shared_tiles + sum - mine;
     for (int i = 0; i < warp; ++i) before += c->scan[i];
-    if (tid == kAttentionThreads - 1) c->total = before + mine;
+    if (tid == kThreads - 1) c->total = before + mine;
     __syncthreads();
     const int total = c->total;
     const int lo = static_cast<int>(static_cast<long long>(blockIdx.x) * total / a.ctas);
@@ -895,27 +910,29 @@ __global__ void __launch_bounds__(kAttentionThreads, 1)
         if (lo >= before && lo < before + n) c->b = b, c->before = before;
         before += n;
     }
-    if (blockIdx.x == 0 && tid == kAttentionThreads - 1) a.starts[a.B] = total;
+    if (blockIdx.x == 0 && tid == kThreads - 1) a.starts[a.B] = total;
     if (lo >= hi) return;  // the whole CTA
-    if (warp == 13) tmem_alloc(ptx::smem_addr(&c->tmem), 512);
+    constexpr int kFirst = 8 + L::kWorkers;  // of the four single warps
+    if (warp == kFirst + 1) tmem_alloc(ptx::smem_addr(&c->tmem), 512);
     __syncthreads();
     fence_after();
 
     Attention<T, D, Q8> x{a, c, ptx::smem_addr(smem), ptx::smem_addr(smem) + 2 * L::kQ + L::kRing * L::kQ, c->tmem, lane, warp};
-    // Registers of a thread: 2 * 128 * 160 + 2 * 128 * 96 is what the launch has, 512 * 128.
     if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftmaxRegs));
         x.softmax(warp >> 2, tid & 127);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-        if (warp < 12) x.load_rows(tid - 256);
-        else if (warp == 12) x.load_tiles(&k_map, &v_map);
-        else if (warp == 13) x.multiply();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
+        if (warp < kFirst) x.work(tid - 256);
+        else if (warp == kFirst) x.load_tiles(maps);
+        else if (warp == kFirst + 1) x.multiply();
+        else if (warp == kFirst + 2) x.load_queries(maps);
+        else if (Q8) x.load_stages(maps);
     }
 
     fence_before();
     __syncthreads();
-    if (warp == 13) tmem_free(c->tmem, 512);
+    if (warp == kFirst + 1) tmem_free(c->tmem, 512);
 }
 
 // ------------------------------------------------------------------ joining

@@ -32,8 +32,11 @@ struct AttentionArgs {
     float scale;
     // the split
     int group;                        // query heads a key head
-    int blocks, block_rows;           // of a sequence's N * group rows
+    int half_nodes;                   // whole nodes of a product's 128 rows
+    int blocks, block_rows;           // of a sequence's N * group rows: whole nodes, two halves at most
     int shared_blocks, shared_rows;   // of the batch's B * N * group rows
+    int q_nodes;                      // nodes that a copy of queries brings
+    int q_merged;                     // the batch's nodes are evenly spaced: one axis
     int ctas;
     // the workspace
     int32_t *starts;   // [B + 1] tiles before each sequence's
@@ -47,6 +50,11 @@ struct AttentionArgs {
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiled encode_tiled();
+
+// Tensor maps: the cache's keys and values, the queries, the nodes' keys and values.
+struct Maps {
+    CUtensorMap k, v, q, k_nodes, v_nodes;
+};
 
 __host__ __device__ inline int tiles_of(int keys) { return (keys + kTile - 1) / kTile; }
 

@@ -9,18 +9,36 @@
 namespace spec {
 namespace context {
 
+inline spec_status encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
+                          const cuuint32_t *box, bool swizzled) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return fail(SPEC_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+    const cuuint32_t each[4] = {1, 1, 1, 1};
+    const CUresult r = f(map, type, rank, const_cast<void *>(base), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? SPEC_OK : fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
+}
+
 // The cache's keys or values [pages][kv_heads * page_size][D] in boxes of up to 128 rows of a page: 16-bit ones in
 // halves of 64 columns, swizzled as the products take them; 8-bit ones whole, to be widened.
 template <int D, bool Q8>
-spec_status tensor_map(CUtensorMap *map, const AttentionArgs &a, void *base, CUtensorMapDataType type) {
-    const EncodeTiled encode = encode_tiled();
-    if (!encode) return fail(SPEC_ERR_CUDA, "the driver has no cuTensorMapEncodeTiled");
+spec_status cache_map(CUtensorMap *map, const AttentionArgs &a, int i, CUtensorMapDataType type) {
     const cuuint64_t rows = static_cast<cuuint64_t>(a.cache.kv_heads) << a.cache.page_bits, row = D * (Q8 ? 1 : 2);
     const cuuint64_t dims[3] = {D, rows, static_cast<cuuint64_t>(std::max(a.cache.pages, 1))}, strides[2] = {row, rows * row};
-    const cuuint32_t box[3] = {Q8 ? D : 64, static_cast<cuuint32_t>(std::min(1 << a.cache.page_bits, kTile)), 1}, each[3] = {1, 1, 1};
-    const CUresult r = encode(map, type, 3, base, dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              Q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? SPEC_OK : fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", (int)r);
+    const cuuint32_t box[3] = {Q8 ? D : 64, static_cast<cuuint32_t>(std::min(1 << a.cache.page_bits, kTile)), 1};
+    // (a cache without pages is not read: any address does)
+    return encode(map, Q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type, 3, a.cache.pages ? a.cache.data[i] : a.out, dims, strides, box, !Q8);
+}
+
+// [batch][nodes][heads][D] in boxes of `heads` heads of `nodes` nodes, 64 columns, swizzled; the batch's nodes on one
+// axis where `merged`.
+inline spec_status nodes_map(CUtensorMap *map, const AttentionArgs &a, const void *base, int D, int heads, const long long *stride, bool merged, int box_heads,
+                             int box_nodes, CUtensorMapDataType type) {
+    const cuuint64_t B = a.B, N = a.N, token = stride[1] * 2, batch = merged ? token : stride[0] * 2;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), merged ? B * N : N, merged ? 1 : B};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(D) * 2, token, batch};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_nodes), 1};
+    return encode(map, type, 4, base, dims, strides, box, true);
 }
 
 template <typename T, int D, bool Q8>
@@ -37,14 +55,15 @@ spec_status launch_attention(const AttentionArgs &a0, cudaStream_t stream) {
     if (smem > di.max_dyn) return fail(SPEC_ERR_UNSUPPORTED, "%zu bytes of shared memory needed, %zu there", smem, di.max_dyn);
     AttentionArgs a = a0;
     a.ctas = std::min(di.sms, kMaxCtas);
-    const CUtensorMapDataType type = Q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                        : std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    CUtensorMap maps[2];
-    for (int i = 0; i < 2; ++i) {  // (a cache without pages is not read: any address does)
-        st = tensor_map<D, Q8>(&maps[i], a, a.cache.pages ? a.cache.data[i] : a.out, type);
-        if (st != SPEC_OK) return st;
-    }
-    kernel<<<a.ctas, kAttentionThreads, smem, stream>>>(a, maps[0], maps[1]);
+    const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int kv = a.cache.kv_heads;
+    Maps maps;
+    if ((st = cache_map<D, Q8>(&maps.k, a, 0, type)) != SPEC_OK || (st = cache_map<D, Q8>(&maps.v, a, 1, type)) != SPEC_OK ||
+        (st = nodes_map(&maps.q, a, a.q, D, a.heads, a.stride, a.q_merged, a.group, a.q_nodes, type)) != SPEC_OK ||
+        (st = nodes_map(&maps.k_nodes, a, a.k, D, kv, a.stride + 2, false, 1, kTile, type)) != SPEC_OK ||
+        (st = nodes_map(&maps.v_nodes, a, a.v, D, kv, a.stride + 4, false, 1, kTile, type)) != SPEC_OK)
+        return st;
+    kernel<<<a.ctas, Layout<D, Q8>::kThreads, smem, stream>>>(a, maps);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
     const long long join = static_cast<long long>(a.B) * a.cache.kv_heads * a.blocks * ((a.block_rows + 31) / 32);

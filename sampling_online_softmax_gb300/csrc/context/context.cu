@@ -191,6 +191,7 @@ extern "C" spec_status spec_tree_attention(const void *q, const void *k, const v
     const int kv = cache->kv_heads, D = cache->head_dim;
     if (B < 0 || N < 1 || heads < 1 || heads % kv) return fail(SPEC_ERR_INVALID_ARG, "need B >= 0, N >= 1, heads a multiple of kv_heads");
     if (N > SPEC_MAX_NODES) return fail(SPEC_ERR_UNSUPPORTED, "N = %d > %d", N, SPEC_MAX_NODES);
+    if (heads / kv > kTile) return fail(SPEC_ERR_UNSUPPORTED, "%d query heads a key head: at most %d", heads / kv, kTile);
     if (shared_len < 0 || shared_len > cache->table_width * cache->page_size || (shared_len && !cache->pages))
         return fail(SPEC_ERR_INVALID_ARG, "shared_len = %d: within the page table", shared_len);
     if (!(scale > 0.0f && scale < INFINITY)) return fail(SPEC_ERR_INVALID_ARG, "scale must be finite and > 0");
@@ -207,6 +208,8 @@ extern "C" spec_status spec_tree_attention(const void *q, const void *k, const v
     const long long tokens[3] = {static_cast<long long>(heads) * D, static_cast<long long>(kv) * D, static_cast<long long>(kv) * D};
     st = strides_of(a.stride, strides, 3, N, tokens);
     if (st != SPEC_OK) return st;
+    for (const long long x : a.stride)
+        if (x == 0 || x >= 1ll << 38) return fail(SPEC_ERR_INVALID_ARG, "strides must be above 0 and below 2^38 elements");
     a.q = static_cast<const unsigned char *>(q);
     a.k = static_cast<const unsigned char *>(k);
     a.v = static_cast<const unsigned char *>(v);
@@ -219,13 +222,19 @@ extern "C" spec_status spec_tree_attention(const void *q, const void *k, const v
     a.scale = scale;
     if (a.cache.pages == 0) a.cache.table_width = 0;  // no position is there
     attention_layout(&a, B, N, heads, D, shared_len, static_cast<unsigned char *>(workspace));
-    // Blocks of at most 256 rows, as equal as they can be.
+    // Blocks of two halves of up to 128 rows, whole nodes each, as equal as they can be.
     a.group = heads / kv;
-    const int rows = N * a.group, all = B * rows;
-    a.blocks = (rows + kBlockRows - 1) / kBlockRows;
-    a.block_rows = (rows + a.blocks - 1) / a.blocks;
-    a.shared_blocks = (all + kBlockRows - 1) / kBlockRows;
-    a.shared_rows = (all + a.shared_blocks - 1) / a.shared_blocks;
+    a.half_nodes = kTile / a.group;
+    const auto split = [&](int nodes, int *blocks, int *block_rows) {
+        *blocks = (nodes + 2 * a.half_nodes - 1) / (2 * a.half_nodes);
+        const int each = (nodes + *blocks - 1) / *blocks;
+        *block_rows = each * a.group;
+        a.q_nodes = std::max(a.q_nodes, std::min(each, a.half_nodes));
+    };
+    split(N, &a.blocks, &a.block_rows);
+    split(shared_len ? B * N : N, &a.shared_blocks, &a.shared_rows);
+    a.q_merged = B == 1 || a.stride[0] == N * a.stride[1];
+    if (shared_len && !a.q_merged) return fail(SPEC_ERR_UNSUPPORTED, "with shared_len, q's batch stride is N times its token stride");
     const long long tiles = static_cast<long long>(kv) * (static_cast<long long>(B) * a.blocks * (tiles_of(cache->table_width * cache->page_size) + tiles_of(N)) +
                                                           static_cast<long long>(a.shared_blocks) * tiles_of(shared_len));
     if (tiles > INT_MAX) return fail(SPEC_ERR_UNSUPPORTED, "too much work: %lld tiles of %d keys", tiles, kTile);
