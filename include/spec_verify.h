@@ -525,7 +525,8 @@ SPEC_API spec_status spec_cache_append(const void *k, const void *v, spec_dtype 
  * Reads positions start[b] .. start[b] + count[b] - 1 of every sequence back:
  *   k, v [B, S, kv_heads, head_dim] of `dtype` (output, contiguous, 16-byte aligned): row i is
  *        position start[b] + i; rows from count[b] on are left as they were.  With SPEC_E4M3
- *        each value is q * 2^e, rounded to `dtype` (exactly, but for fp16 below 2^-14).
+ *        each value is q * 2^e, rounded to `dtype` (exactly, but for fp16 below 2^-14, and past fp16's
+ *        range where the cache was written from bf16: an infinity).
  *   start, count, dev_status as in spec_cache_append (such a row is left as it was).
  */
 SPEC_API spec_status spec_cache_read(const spec_cache *cache, int B, int S, const int32_t *start, const int32_t *count, void *k,

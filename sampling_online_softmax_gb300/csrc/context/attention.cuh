@@ -12,12 +12,14 @@
 //   warps 0-3, 4-7   softmax of product 0, 1: a thread a row
 //   four warps       values whose other rows must be 0 (what lies behind a sequence's end, nodes that are
 //                    not finite: 0 * NaN is NaN); eight of them where 8-bit tiles are widened too
-//   one warp each    TMA of tiles; tcgen05.mma; TMA of queries; TMA of 8-bit tiles
+//   a lane each      tcgen05.mma of product 0, of product 1
+//   one or two warps the list of work, TMA of queries and of tiles; with 8-bit tiles one more for their TMA
 //
 // The softmax keeps a row's running maximum as it was until a tile's exceeds it by 2^8: weights up to 2^8
 // lose nothing in a float format, and O is rescaled almost never.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attention.h"
@@ -31,42 +33,61 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 template <int D, bool Q8>
 struct Layout {
-    static constexpr int kQ = kTile * D * 2;     // bytes of 128 rows of queries, keys or values
-    static constexpr int kRing = Q8 ? (D == 128 ? 4 : 6) : (D == 128 ? 5 : 8);
-    static constexpr int kStage = Q8 ? kTile * D : 0;
-    static constexpr int kStages = Q8 ? (D == 128 ? 2 : 8) : 0;
-    static constexpr int kWorkers = Q8 ? 8 : 4;              // warps that clear and widen
+    static constexpr int kTileBytes = kTile * D * 2;         // of 128 rows of keys or values
+    static constexpr int kStageBytes = Q8 ? kTile * D : 0;   // of an 8-bit tile
+    static constexpr int kWorkers = Q8 ? 8 : 4;              // warps that clear and widen: in 8 bits four for keys, four for values
     static constexpr int kThreads = (8 + kWorkers + 4) * 32;
-    // Registers of a thread after the start: the sum over the warps is what the launch has (65536 at 512
-    // threads, 640 * 96 at 640).
-    static constexpr int kSoftmaxRegs = Q8 ? 152 : 192, kOtherRegs = Q8 ? 56 : 64;
-    static constexpr int kBytes = 2 * kQ + kRing * kQ + kStages * kStage;
+    // Registers of a thread after the start, by role: over the warpgroups they sum to what the launch has, 512 at 512
+    // threads (128 each), 480 at 640 (96 each).
+    static constexpr int kSoftmaxRegs = Q8 ? 144 : 160, kWorkerRegs = Q8 ? 48 : 64;  // (the single warps keep the launch's)
 };
 
+// How shared memory is shared out: two halves of queries, as many rows of each as a launch has (a product reads 128 rows
+// all the same; what the others hold goes nowhere), then the ring of tiles and 8-bit tiles.  Four tiles of the ring
+// keep both products fed where 8-bit ones are widened into it; the rest holds copies under way.
+template <int D, bool Q8>
+inline void share_out(AttentionArgs *a, int room) {
+    using L = Layout<D, Q8>;
+    a->q_sub = (a->q_nodes * a->group + 7) / 8 * 1024;
+    int left = room - 2 * a->q_sub * (D / 64);
+    a->ring = Q8 ? (D == 128 ? 4 : 8) : std::min(8, left / L::kTileBytes);
+    left -= a->ring * L::kTileBytes;
+    a->stages = Q8 ? std::min(8, left / L::kStageBytes) & ~1 : 0;  // (ring and stages even: each group of workers sees its own slots)
+}
+
+// A CTA's run of the list, cut at the blocks' borders.
+struct Piece {
+    int shared, two;     // of the prefix; two products a tile
+    int b, g, first, rows;
+    int t0, t1, tiles;   // the piece's tiles, of the block's
+    int context;         // own: the context's tiles; the nodes' follow
+    int plain0, plain1;  // tiles of the context that begin and end inside it: every row sees every key
+    int at, from, to;    // tile 0's first position; the positions that are the piece's
+    int turn;            // one product a tile: tile t0 is product `turn`'s, and so on in turn
+    int last;            // no piece: the run is over
+    int odd;             // a value of its nodes is not finite
+};
+constexpr int kPieces = 4;
+
 struct Control {  // behind the tiles in shared memory
+    Piece pieces[kPieces];
+    uint64_t piece_there[kPieces], piece_done[kPieces];
     uint64_t full[8], empty[8];    // ring of tiles
     uint64_t copied[8];            // a slot's values are there, to be cleared in part
     uint64_t staged[8], free_[8];  // ring of 8-bit tiles
     uint64_t q_full[2], q_empty[2];
-    uint64_t scores[2], weights[2], sums[2];  // of the two products
+    uint64_t scores[2], weights[2][2], sums[2];  // of the two products; weights of a tile's first and second 64 keys
     uint64_t joined[2];            // both warpgroups: statistics there, sums read
+    uint64_t turn[2];              // a warpgroup's weights of a tile are done
     uint64_t drained;
     uint32_t tmem;
     int gave_up;
-    int odd[8];                    // a value of the piece's nodes is not finite (by piece, in turn)
     int scan[20];
     int total, b, before;          // tiles in all; the sequence a CTA begins in and the tiles before it
     float2 stats[2][kTile];
 };
 
-// A CTA's pieces of the list, in order.
-struct Piece {
-    bool shared, two;    // of the prefix; two products a tile
-    int b, g, first, rows;
-    int t0, t1, tiles;   // the piece's tiles, of the block's
-    int len, context;    // own: the sequence's length, its context's tiles
-};
-
+// The pieces of a CTA, in order.
 struct Walk {
     const AttentionArgs &a;
     int left, item, t, b, tiles, context, len, per_seq, shared_items, shared_tiles;
@@ -106,6 +127,7 @@ struct Walk {
         const int blocks = shared ? a.shared_blocks : a.blocks, rows = shared ? a.shared_rows : a.block_rows;
         const int all = shared ? a.B * a.N * a.group : a.N * a.group;
         const int block = item % blocks;
+        p->last = 0;
         p->shared = shared;
         p->two = rows > a.half_nodes * a.group;
         p->b = shared ? 0 : b;
@@ -115,8 +137,12 @@ struct Walk {
         p->tiles = shared ? shared_tiles : tiles;
         p->t0 = t;
         p->t1 = min(p->tiles, t + left);
-        p->len = shared ? a.shared_len : len;
         p->context = shared ? shared_tiles : context;
+        p->at = shared ? 0 : a.shared_len / kTile * kTile;
+        p->from = shared ? 0 : a.shared_len;
+        p->to = shared ? a.shared_len : len;
+        p->plain0 = (p->from - p->at + kTile - 1) / kTile;
+        p->plain1 = (p->to - p->at) / kTile;
         left -= p->t1 - p->t0;
         t = p->t1;
         if (t == p->tiles) {
@@ -139,7 +165,7 @@ struct Cursor {
     }
 };
 
-// The row of the batch that row `r` (of all the rows of piece p's kind) is.
+// The row of the batch that row r of a piece is.
 struct RowId {
     int b, n, h;
 };
@@ -148,41 +174,21 @@ __device__ __forceinline__ RowId row_id(const AttentionArgs &a, const Piece &p, 
     return RowId{p.shared ? i / a.N : p.b, p.shared ? i % a.N : i, p.g * a.group + h};
 }
 
-// Sixteen e4m3 values, times 2^(byte - 127), as 16 elements.
+// e4m3 values times 2^(byte - 127), four at a time: exact steps, by the conversions that there are (of which each
+// takes less than moving the bits by shifts and masks, or by multiplications).
 template <typename T>
 struct Widen;
 template <>
 struct Widen<__nv_bfloat16> {
-    uint32_t m1, m2;
-    bool twice;
-    // An e4m3 value's bits, moved into bf16's places, read as 2^-120 of it (subnormal ones too), so
-    // it is a product with 2^(120 + e), in two steps where that is past bf16.
-    __device__ __forceinline__ void scale(uint32_t byte) {
-        const int e = static_cast<int>(byte) - 127, e1 = min(e + 120, 127);
-        uint32_t s1 = static_cast<uint32_t>(max(e1 + 127, 1)) << 7;
-        const uint32_t s2 = static_cast<uint32_t>(127 + e + 120 - e1) << 7;
-        if (byte == 255) s1 = 0x7fff;
-        m1 = s1 | s1 << 16;
-        m2 = s2 | s2 << 16;
-        twice = e > 7;
-    }
-    __device__ __forceinline__ void zero() { m1 = m2 = 0, twice = false; }
-    static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
-        uint32_t r;
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
-    template <bool TWICE>
+    float m;
+    __device__ __forceinline__ void scale(uint32_t byte) { m = scale_of(byte); }
     __device__ __forceinline__ uint2 four(uint32_t w) const {
-        const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-        uint32_t x = times((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), m1), y = times((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), m1);
-        if (TWICE) x = times(x, m2), y = times(y, m2);
-        return make_uint2(x, y);
+        const float2 a = e4m3x2(w), b = e4m3x2(w >> 16);
+        return make_uint2(Elt<__nv_bfloat16>::from_float2(a.x * m, a.y * m), Elt<__nv_bfloat16>::from_float2(b.x * m, b.y * m));
     }
 };
 template <>
 struct Widen<__half> {
-    static constexpr bool twice = false;
     uint32_t m;
     __device__ __forceinline__ void scale(uint32_t byte) {
         const int e = min(max(static_cast<int>(byte) - 127, -24), 15);
@@ -190,13 +196,11 @@ struct Widen<__half> {
         if (byte == 255) s = 0x7fff;
         m = s | s << 16;
     }
-    __device__ __forceinline__ void zero() { m = 0; }
     static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
         uint32_t r;
         asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
     }
-    template <bool>
     __device__ __forceinline__ uint2 four(uint32_t w) const {
         const __half2_raw x = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffff), __NV_E4M3);
         const __half2_raw y = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
@@ -229,9 +233,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return *reinterpret_cast<float2 *>(&r);
 }
 
-// Where a piece leaves its rows' sums, column by column (a warp's rows lie next to each other), and (maximum, sum).
+// Where a piece leaves its rows' sums, four columns at a time (a warp's rows lie next to each other), and (maximum, sum).
 struct Part {
-    float *sums;    // [D][rows]
+    float *sums;    // [D / 4][rows][4]
     float2 *stats;  // [rows]
     int rows;
 };
@@ -250,7 +254,23 @@ __device__ __forceinline__ Part whole_part(const AttentionArgs &a, bool shared, 
     return Part{a.row_sums + row * D, a.row_stats + row, rows};
 }
 
-// ------------------------------------------------------------------ the four kinds of warps
+// Values of nodes m0 .. m1 - 1 that are not finite, to a row of node n that sees them: its columns [d0, d1), already
+// written, four next to each other and `step` from there to the next four.  Out of line: it is hardly ever called, and inlined it would keep registers from what is.
+template <typename T, typename X>
+__device__ __noinline__ void add_odd(const AttentionArgs &a, int b, int g, int n, int m0, int m1, int d0, int d1, int D, X *to, int step) {
+    for (int m = m0; m < m1; ++m) {
+        const bool on = a.mask ? a.mask[static_cast<size_t>(n) * ((a.N + 31) / 32) + m / 32] >> (m & 31) & 1 : m <= n;
+        if (!on) continue;
+        const T *v = reinterpret_cast<const T *>(a.v) + b * a.stride[4] + m * a.stride[5] + g * D;
+        for (int d = d0; d < d1; ++d) {
+            const float y = static_cast<float>(v[d]);
+            X &x = to[static_cast<size_t>(d / 4) * step + d % 4];
+            if (!isfinite(y)) x = static_cast<X>(static_cast<float>(x) + y);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the kinds of warps
 template <typename T, int D, bool Q8>
 struct Attention {
     using L = Layout<D, Q8>;
@@ -263,21 +283,93 @@ struct Attention {
 
     const AttentionArgs &a;
     Control *c;
-    uint32_t tiles, stages;  // shared-memory addresses: queries, then the ring; 8-bit tiles
+    uint32_t queries, tiles, stages;  // shared-memory addresses: of queries, of the ring, of 8-bit tiles
     uint32_t tmem;
     int lane, warp;
+    int piece_at = 0;
+    uint32_t piece_round = 0;
 
     __device__ __forceinline__ bool wait(const uint64_t *bar, uint32_t parity) {
-        return wait_phase(ptx::smem_addr(bar), parity, &c->gave_up, a.status);
+        return wait_phase<false>(ptx::smem_addr(bar), parity, &c->gave_up, a.status);
     }
-    __device__ __forceinline__ uint32_t ring(int slot) const { return tiles + 2 * L::kQ + slot * L::kQ; }
-    // Whether a piece's tile t of the context ends behind the sequence, or begins before what is its own.
-    __device__ __forceinline__ bool ragged(const Piece &p, int t) const {
-        const int at = (first_tile(p) + t) * kTile;
-        return at + kTile > p.len || at < begin(p);
+    __device__ __forceinline__ bool hurry(const uint64_t *bar, uint32_t parity) {
+        return wait_phase<true>(ptx::smem_addr(bar), parity, &c->gave_up, a.status);
     }
-    __device__ __forceinline__ int first_tile(const Piece &p) const { return p.shared ? 0 : a.shared_len / kTile; }
-    __device__ __forceinline__ int begin(const Piece &p) const { return p.shared ? 0 : a.shared_len; }  // the piece's first position
+    __device__ __forceinline__ bool wait1(const uint64_t *bar, uint32_t parity) {
+        return wait_alone(ptx::smem_addr(bar), parity, &c->gave_up, a.status);
+    }
+    __device__ __forceinline__ uint32_t ring(int slot) const { return tiles + slot * L::kTileBytes; }
+    __device__ __forceinline__ uint32_t query_half(int h) const { return queries + h * (D / 64) * a.q_sub; }
+
+    // ---- pieces: one warp walks the list; the others take them in turn, and say when they are done with one
+    __device__ __forceinline__ const Piece *piece() const { return c->pieces[piece_at].last ? nullptr : &c->pieces[piece_at]; }
+    __device__ __forceinline__ const Piece *next_piece() { return wait(&c->piece_there[piece_at], piece_round) ? piece() : nullptr; }
+    __device__ __forceinline__ const Piece *next_piece1() { return wait1(&c->piece_there[piece_at], piece_round) ? piece() : nullptr; }
+    __device__ __forceinline__ void done_piece1() {
+        arrive(ptx::smem_addr(&c->piece_done[piece_at]));
+        if (++piece_at == kPieces) piece_at = 0, piece_round ^= 1;
+    }
+    __device__ __forceinline__ void done_piece() {
+        __syncwarp();
+        if (lane == 0) arrive(ptx::smem_addr(&c->piece_done[piece_at]));
+        if (++piece_at == kPieces) piece_at = 0, piece_round ^= 1;
+    }
+    // Whether values of a tile are to be looked through: the context's ends, and the nodes.
+    static __device__ __forceinline__ bool plain(const Piece &p, int t) { return t >= p.plain0 && t < p.plain1; }
+
+    __device__ __forceinline__ bool announce(const Piece &p) {
+        if (!wait(&c->piece_done[piece_at], piece_round ^ 1)) return false;
+        if (lane == 0) {
+            c->pieces[piece_at] = p;
+            arrive(ptx::smem_addr(&c->piece_there[piece_at]));
+        }
+        __syncwarp();
+        if (++piece_at == kPieces) piece_at = 0, piece_round ^= 1;
+        return true;
+    }
+    // 8 bits: the products take the ring's tiles in turn across pieces, so that each has slots of its own there (the
+    // ring's are a multiple of four) and need not see the other's, which the workers may be late with.
+    static __device__ __forceinline__ bool next_of(Walk &walk, Piece *p, int &tiles) {
+        const bool more = walk.next(p);
+        p->last = !more;
+        p->odd = 0;
+        p->turn = Q8 ? tiles & 1 : 0;
+        tiles += p->t1 - p->t0;
+        return more;
+    }
+    // The queries of a piece: a half holds a.half_nodes nodes, whose heads of the group lie next to each other.
+    struct Queries {
+        uint32_t round = 0, issued = 0;  // a bit a half
+        int half = 0;
+    };
+    __device__ __forceinline__ bool load_queries(const Piece &p, const Maps &maps, Queries &q) {
+        if (p.two) q.half = 0;
+        for (int h = 0; h < 2; ++h) {
+            if (!p.two && h != q.half) continue;
+            if (!wait(&c->q_empty[h], (q.round >> h & 1) ^ 1)) return false;
+            q.round ^= 1u << h;
+            q.issued |= 1u << h;
+            const uint32_t bar = ptx::smem_addr(&c->q_full[h]);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar, a.q_nodes * a.group * D * 2);
+            __syncwarp();
+            const int node = p.first / a.group + (p.two ? h * a.half_nodes : 0);
+            const int z = a.q_merged && !p.shared ? p.b * a.N + node : node, b = a.q_merged ? 0 : p.b;
+            if (lane < D / 64) tma_load4(query_half(h) + lane * a.q_sub, &maps.q, lane * 64, p.g * a.group, z, b, bar, policy_evict_normal());
+        }
+        if (!p.two) q.half ^= 1;
+        return true;
+    }
+    __device__ void lead(const Maps &maps) {
+        Walk walk(a, c);
+        Piece p;
+        Queries q;
+        int tiles = 0;
+        while (true) {
+            const bool more = next_of(walk, &p, tiles);
+            if (!announce(p) || !more || !load_queries(p, maps, q)) break;
+        }
+        if (c->gave_up) drain(c->q_full, 2, q.issued, ~q.round);
+    }
 
     // ---- TMA
     // The keys and values of one tile of the context, in boxes of at most a page: lane i the i-th.
@@ -285,9 +377,9 @@ struct Attention {
         int page, y;
     };
     __device__ __forceinline__ Boxes boxes_of(const Piece &p, int t, int box, bool &bad) const {
-        const long long pos = static_cast<long long>(first_tile(p) + t) * kTile + lane * box;
+        const long long pos = static_cast<long long>(p.at) + t * kTile + lane * box;
         Boxes b{a.cache.pages, (p.g << a.cache.page_bits) + static_cast<int>(pos & ((1 << a.cache.page_bits) - 1))};  // outside: zeros
-        if (lane < kTile / box && pos < p.len && pos + box > begin(p)) {
+        if (lane < kTile / box && pos < p.to && pos + box > p.from) {
             const int entry = __ldg(a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width + (pos >> a.cache.page_bits));
             if (entry < 0 || entry >= a.cache.pages) bad = true;
             else b.page = entry;
@@ -306,212 +398,202 @@ struct Attention {
     // Tiles into the ring: of a 16-bit cache, and of the nodes.  Each round of each slot is waited for and
     // arrived at by this warp and by the workers, whichever fills it: a parity tells a round from its
     // neighbours alone, so none may run ahead of the ring by more than a round, or fall behind it.
-    __device__ void load_tiles(const Maps &maps) {
-        Walk walk(a, c);
-        Piece p;
+    struct Tiles {
         Cursor at;
-        // tiles that one block takes are read once; where several blocks take them, L2 may keep them
-        const uint64_t once = ptx::policy_evict_first(), normal = policy_evict_normal();
-        const int box = box_rows();
-        bool bad = false, ok = true;
+        bool bad = false;
         uint32_t issued = 0, rounds = 0, copied = 0, copies = 0;  // a bit a slot: loaded; its last phase's parity; the same of `copied`
-        while (ok && walk.next(&p)) {
-            const uint64_t policy = (p.shared ? a.shared_blocks : a.blocks) == 1 ? once : normal;
-            for (int t = p.t0; ok && t < p.t1; ++t) {
-                Boxes boxes;
-                if (!Q8 && t < p.context) boxes = boxes_of(p, t, box, bad);
-                for (int w = 0; w < 2; ++w, at.step(L::kRing)) {
-                    if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
-                    const uint32_t full = ptx::smem_addr(&c->full[at.slot]), to = ring(at.slot), bit = 1u << at.slot;
-                    if (Q8 && t < p.context) {
-                        if (lane == 0) arrive(full);
-                        __syncwarp();
-                        continue;
-                    }
-                    // Values that the workers look through first: their copy is waited for there.
-                    const bool checked = w && (t >= p.context || ragged(p, t));
-                    const uint32_t bar = checked ? ptx::smem_addr(&c->copied[at.slot]) : full;
-                    if (lane == 0) {
-                        if (checked) arrive(full);
-                        ptx::mbar_arrive_expect_tx(bar, L::kQ);
-                    }
+    };
+    __device__ __forceinline__ bool load_tiles(const Piece &p, const Maps &maps, Tiles &s) {
+        const int box = box_rows();
+        const uint64_t normal = policy_evict_normal();
+        // tiles that one block takes are read once; where several blocks take them, L2 may keep them
+        const uint64_t policy = (p.shared ? a.shared_blocks : a.blocks) == 1 ? ptx::policy_evict_first() : normal;
+        for (int t = p.t0; t < p.t1; ++t) {
+            Boxes boxes;
+            if (!Q8 && t < p.context) boxes = boxes_of(p, t, box, s.bad);
+            for (int w = 0; w < 2; ++w, s.at.step(a.ring)) {
+                if (!wait(&c->empty[s.at.slot], s.at.round ^ 1)) return false;
+                const uint32_t full = ptx::smem_addr(&c->full[s.at.slot]), to = ring(s.at.slot), bit = 1u << s.at.slot;
+                if (Q8 && t < p.context) {
+                    if (lane == 0) arrive(full);
                     __syncwarp();
-                    if (t >= p.context) {
-                        if (lane < D / 64) tma_load4(to + lane * (kTile * 128), w ? &maps.v_nodes : &maps.k_nodes, lane * 64, p.g, (t - p.context) * kTile, p.b, bar, normal);
-                    } else if (lane < kTile / box) {
-                        for (int x = 0; x < D; x += 64) tma_load3(to + (x / 64) * (kTile * 128) + lane * box * 128, w ? &maps.v : &maps.k, x, boxes.y, boxes.page, bar, policy);
-                    }
-                    if (checked) copied |= bit, copies ^= bit;
-                    else issued |= bit, rounds = (rounds & ~bit) | at.round << at.slot;
+                    continue;
                 }
+                // Values that the workers look through first: their copy is waited for there.
+                const bool checked = w && !plain(p, t);
+                const uint32_t bar = checked ? ptx::smem_addr(&c->copied[s.at.slot]) : full;
+                if (lane == 0) {
+                    if (checked) arrive(full);
+                    ptx::mbar_arrive_expect_tx(bar, L::kTileBytes);
+                }
+                __syncwarp();
+                if (t >= p.context) {
+                    if (lane < D / 64) tma_load4(to + lane * (kTile * 128), w ? &maps.v_nodes : &maps.k_nodes, lane * 64, p.g, (t - p.context) * kTile, p.b, bar, normal);
+                } else if (lane < kTile / box) {
+                    for (int x = 0; x < D; x += 64) tma_load3(to + (x / 64) * (kTile * 128) + lane * box * 128, w ? &maps.v : &maps.k, x, boxes.y, boxes.page, bar, policy);
+                }
+                if (checked) s.copied |= bit, s.copies ^= bit;
+                else s.issued |= bit, s.rounds = (s.rounds & ~bit) | s.at.round << s.at.slot;
             }
         }
-        if (bad) atomicOr(a.status, SPEC_DEV_BAD_PAGE);
-        if (!ok) {
-            drain(c->full, L::kRing, issued, rounds);
-            drain(c->copied, L::kRing, copied, ~copies);
+        return true;
+    }
+    __device__ __forceinline__ void end_tiles(const Tiles &s) {
+        if (s.bad) atomicOr(a.status, SPEC_DEV_BAD_PAGE);
+        if (!c->gave_up) return;
+        drain(c->full, a.ring, s.issued, s.rounds);
+        drain(c->copied, a.ring, s.copied, ~s.copies);
+    }
+    __device__ void load_tiles(const Maps &maps) {
+        Tiles s;
+        for (const Piece *p; (p = next_piece()) && load_tiles(*p, maps, s);) done_piece();
+        end_tiles(s);
+    }
+    // The list, the queries and the ring by one warp, which has the next piece announced before a piece's tiles.
+    __device__ void lead_tiles(const Maps &maps) {
+        Walk walk(a, c);
+        Piece p, next;
+        Queries q;
+        Tiles s;
+        int tiles = 0;
+        bool more = next_of(walk, &p, tiles), ok = announce(p);
+        while (ok && more) {
+            more = next_of(walk, &next, tiles);
+            ok = announce(next) && load_queries(p, maps, q) && load_tiles(p, maps, s);
+            p = next;
         }
+        end_tiles(s);
+        if (c->gave_up) drain(c->q_full, 2, q.issued, ~q.round);
     }
     // 8-bit tiles, to be widened.
     __device__ void load_stages(const Maps &maps) {
-        Walk walk(a, c);
-        Piece p;
         Cursor at;
         const uint64_t once = ptx::policy_evict_first(), normal = policy_evict_normal();
         const int box = box_rows();
         bool bad = false, ok = true;
         uint32_t issued = 0, rounds = 0;
-        while (ok && walk.next(&p)) {
+        for (const Piece *pp; ok && (pp = next_piece()); done_piece()) {
+            const Piece &p = *pp;
             const uint64_t policy = (p.shared ? a.shared_blocks : a.blocks) == 1 ? once : normal;
-            for (int t = p.t0; ok && t < min(p.t1, p.context); ++t) {
+            const int t1 = min(p.t1, p.context);
+            for (int t = p.t0; ok && t < t1; ++t) {
                 const Boxes boxes = boxes_of(p, t, box, bad);
                 for (int w = 0; w < 2; ++w) {
                     if (!(ok = wait(&c->free_[at.slot], at.round ^ 1))) break;
                     const uint32_t bar = ptx::smem_addr(&c->staged[at.slot]);
-                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStage);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, L::kStageBytes);
                     __syncwarp();
-                    if (lane < kTile / box) tma_load3(stages + at.slot * L::kStage + lane * box * D, w ? &maps.v : &maps.k, 0, boxes.y, boxes.page, bar, policy);
+                    if (lane < kTile / box) tma_load3(stages + at.slot * L::kStageBytes + lane * box * D, w ? &maps.v : &maps.k, 0, boxes.y, boxes.page, bar, policy);
                     issued |= 1u << at.slot;
                     rounds = (rounds & ~(1u << at.slot)) | at.round << at.slot;
-                    at.step(L::kStages > 0 ? L::kStages : 1);
+                    at.step(a.stages);
                 }
             }
         }
         if (bad) atomicOr(a.status, SPEC_DEV_BAD_PAGE);
-        if (!ok) drain(c->staged, L::kStages, issued, rounds);
-    }
-    // Queries: a half holds a.half_nodes nodes, whose heads of the group lie next to each other.
-    __device__ void load_queries(const Maps &maps) {
-        Walk walk(a, c);
-        Piece p;
-        const uint64_t normal = policy_evict_normal();
-        uint32_t round = 0, issued = 0;  // a bit a half
-        int half = 0, count = 0;
-        bool ok = true;
-        while (ok && walk.next(&p)) {
-            if (p.two) half = 0;
-            for (int h = 0; ok && h < 2; ++h) {
-                if (!p.two && h != half) continue;
-                if (!(ok = wait(&c->q_empty[h], (round >> h & 1) ^ 1))) break;
-                round ^= 1u << h;
-                issued |= 1u << h;
-                // (the piece four on: none is read that far back, nor loaded that far ahead)
-                if (lane == 0) *const_cast<volatile int *>(&c->odd[(count + 4) & 7]) = 0;
-                const uint32_t bar = ptx::smem_addr(&c->q_full[h]);
-                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, a.q_nodes * a.group * D * 2);
-                __syncwarp();
-                const int node = p.first / a.group + (p.two ? h * a.half_nodes : 0);
-                const int z = a.q_merged && !p.shared ? p.b * a.N + node : node, b = a.q_merged ? 0 : p.b;
-                if (lane < D / 64) tma_load4(tiles + h * L::kQ + lane * (kTile * 128), &maps.q, lane * 64, p.g * a.group, z, b, bar, normal);
-            }
-            ++count;
-            if (!p.two) half ^= 1;
-        }
-        if (!ok) drain(c->q_full, 2, issued, ~round);
+        if (c->gave_up) drain(c->staged, a.stages, issued, rounds);
     }
 
-    // ---- tcgen05.mma
-    struct Pending {
-        bool any, add, release, final;
-        int slot;
-        uint32_t round;
-    };
-    // The same in every lane, said so that the compiler keeps it in a uniform register, as the mma wants it.
-    static __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-    __device__ bool add_values(Pending &w, int s, uint32_t &weights_round) {
-        w.any = false;
-        if (!wait(&c->full[w.slot], w.round) || !wait(&c->weights[s], weights_round)) return false;
-        weights_round ^= 1;
+    // ---- tcgen05.mma: a lane a product.  The tensor cores hold few products ahead, so what a lane does between
+    // its own is hidden behind the other's.  A slot of the ring is free after two arrivals: one of each lane, used or
+    // not; 8 bits, one product a tile: both of the lane that uses it.
+    __device__ __forceinline__ bool add_values(int s, const Cursor &values, uint32_t round, bool add, bool last, bool alone) {
+        const uint32_t d = tmem + kSums + s * 128, x = tmem + kScores + s * 128, v = operand(ring(values.slot), kTile * 128);
+        if (!wait1(&c->full[values.slot], values.round) || !wait1(&c->weights[s][0], round)) return false;
         fence_after();
-        const uint32_t v = uniform(operand(ring(w.slot), kTile * 128)), d = uniform(tmem + kSums + s * 128), p = uniform(tmem + kScores + s * 128);
-        if (elect()) {
 #pragma unroll
-            for (int k = 0; k < kTile / 16; ++k) mma_tmem(d, p + k * 8, descriptor(v + k * 16 * 128 / 16), kSumsInstr, w.add || k > 0);
-            if (w.release) mma_commit(ptx::smem_addr(&c->empty[w.slot]));
-            if (w.final) mma_commit(ptx::smem_addr(&c->sums[s]));
-        }
-        __syncwarp();
+        for (int k = 0; k < kTile / 32; ++k) mma_tmem(d, x + k * 8, descriptor(v + k * 128), kSumsInstr, add || k > 0);
+        if (!wait1(&c->weights[s][1], round)) return false;
+        fence_after();
+#pragma unroll
+        for (int k = kTile / 32; k < kTile / 16; ++k) mma_tmem(d, x + k * 8, descriptor(v + k * 128), kSumsInstr, true);
+        mma_commit(ptx::smem_addr(&c->empty[values.slot]));
+        if (alone) mma_commit(ptx::smem_addr(&c->empty[values.slot]));
+        if (last) mma_commit(ptx::smem_addr(&c->sums[s]));
         return true;
     }
-    __device__ void multiply() {
-        Walk walk(a, c);
-        Piece p;
+    __device__ void multiply(int s) {
         Cursor at;
-        Pending pending[2] = {};
-        uint32_t weights_round[2] = {0, 0}, q_round[2] = {0, 0};
+        uint32_t round = 0, q_round = 0;  // of the weights; a bit a half
+        const uint32_t sub = a.q_sub / 16, x = tmem + kScores + s * 128;
         int half = 0;
         bool ok = true;
-        while (ok && walk.next(&p)) {
-            const int n = p.t1 - p.t0;
-            if (p.two) half = 0;
-            for (int h = 0; ok && h < 2; ++h)
-                if (p.two || h == half) {
-                    ok = wait(&c->q_full[h], q_round[h]);
-                    q_round[h] ^= 1;
-                }
+        for (const Piece *p; ok && (p = next_piece1()); done_piece1()) {
+            const int n = p->t1 - p->t0;
+            const bool two = p->two;
+            if (two) half = 0;
+            for (int h = 0; ok && h < 2; ++h) {
+                if (!two && h != half) continue;
+                ok = wait1(&c->q_full[h], q_round >> h & 1);
+                q_round ^= 1u << h;
+            }
+            if (!ok) break;
+            const int own = two ? s : half, turn = p->turn ^ s, used = two ? n : (n - turn + 1) / 2;
+            const bool alone = Q8 && !two;
+            if (two) arrive(ptx::smem_addr(&c->q_empty[1 - s]));
+            else if (used == 0) arrive(ptx::smem_addr(&c->q_empty[half]));
+            const uint32_t q = operand(query_half(own), 16);
+            Cursor values;
+            int done = 0;  // own tiles whose scores are under way
             for (int i = 0; ok && i < n; ++i) {
                 const Cursor keys = at;
-                at.step(L::kRing);
-                const Cursor values = at;
-                at.step(L::kRing);
-                for (int x = 0; ok && x < (p.two ? 2 : 1); ++x) {
-                    const int s = p.two ? x : i & 1;
-                    if (pending[s].any && !(ok = add_values(pending[s], s, weights_round[s]))) break;
-                    if (x == 0 && !(ok = wait(&c->full[keys.slot], keys.round))) break;
-                    fence_after();
-                    const uint32_t q = uniform(operand(tiles + (p.two ? x : half) * L::kQ, 16)), k = uniform(operand(ring(keys.slot), 16));
-                    const uint32_t d = uniform(tmem + kScores + s * 128);
-                    if (elect()) {
-#pragma unroll
-                        for (int e = 0; e < D / 16; ++e) {
-                            const uint32_t off = ((e / 4) * (kTile * 128) + (e % 4) * 32) / 16;
-                            mma(d, descriptor(q + off), descriptor(k + off), kScoresInstr, e > 0);
-                        }
-                        mma_commit(ptx::smem_addr(&c->scores[s]));
-                        if (x == (p.two ? 1 : 0)) mma_commit(ptx::smem_addr(&c->empty[keys.slot]));
-                        if (i == n - 1) {
-                            if (p.two) mma_commit(ptx::smem_addr(&c->q_empty[x]));
-                            else mma_commit(ptx::smem_addr(&c->q_empty[half]));
-                        }
-                    }
-                    __syncwarp();
-                    pending[s] = Pending{true, p.two ? i > 0 : i > 1, !p.two || x == 1, p.two ? i == n - 1 : i >= n - 2, values.slot, values.round};
+                at.step(a.ring);
+                const Cursor next = at;
+                at.step(a.ring);
+                if (!two && (i & 1) != turn) {
+                    if (alone) continue;
+                    if (!(ok = wait1(&c->full[keys.slot], keys.round))) break;
+                    arrive(ptx::smem_addr(&c->empty[keys.slot]));
+                    if (!(ok = wait1(&c->full[next.slot], next.round))) break;
+                    arrive(ptx::smem_addr(&c->empty[next.slot]));
+                    continue;
                 }
+                if (done) {
+                    if (!(ok = add_values(s, values, round, done > 1, false, alone))) break;
+                    round ^= 1;
+                }
+                if (!(ok = wait1(&c->full[keys.slot], keys.round))) break;
+                fence_after();
+                const uint32_t k = operand(ring(keys.slot), 16);
+#pragma unroll
+                for (int e = 0; e < D / 16; ++e) mma(x, descriptor(q + (e / 4) * sub + (e % 4) * 2), descriptor(k + (e / 4) * (kTile * 128 / 16) + (e % 4) * 2), kScoresInstr, e > 0);
+                mma_commit(ptx::smem_addr(&c->scores[s]));
+                mma_commit(ptx::smem_addr(&c->empty[keys.slot]));
+                if (alone) mma_commit(ptx::smem_addr(&c->empty[keys.slot]));
+                if (++done == used) mma_commit(ptx::smem_addr(&c->q_empty[own]));
+                values = next;
             }
-            // the piece's last weights: the earlier product's first
-            for (int x = 0; ok && x < 2; ++x) {
-                const int s = p.two ? x : (n + x) & 1;
-                if (pending[s].any) ok = add_values(pending[s], s, weights_round[s]);
+            if (ok && used) {
+                ok = add_values(s, values, round, done > 1, true, alone);
+                round ^= 1;
             }
-            if (!p.two) half ^= 1;
+            if (!two) half ^= 1;
         }
         // Every product done before tensor memory is freed, also where a wait gave up.
-        if (elect()) mma_commit(ptx::smem_addr(&c->drained));
-        __syncwarp();
+        mma_commit(ptx::smem_addr(&c->drained));
         bool done = false;
         for (int n = 0; !done && n < kWaitTries; ++n) done = ptx::mbar_try_wait(ptx::smem_addr(&c->drained), 0);
     }
 
-    // ---- workers: a thread a row, or two threads where there are eight warps
-    static constexpr int kLanes = D / 8, kSplit = L::kWorkers / 4, kShare = kLanes / kSplit;  // 16-byte chunks of a row; of a thread
+    // ---- workers: a thread a row
+    static constexpr int kLanes = D / 8;  // 16-byte chunks of a row
     __device__ __forceinline__ static bool odd_pair(uint32_t x) {  // an infinity or NaN among two elements
         constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
         return (x & e) == e || (x >> 16 & e) == e;
     }
     // The rows of a tile of values outside [from, to) become 0.
-    __device__ __forceinline__ void clear_rows(uint32_t at, int tid, int from, int to) const {
-        const int r = tid & 127;
+    __device__ __forceinline__ void clear_rows(uint32_t at, int r, int from, int to) const {
         if (r >= from && r < to) return;
 #pragma unroll 4
-        for (int x = 0; x < kShare; ++x) store16(at + chunk_at(r, (tid >> 7) * kShare + x), make_uint4(0, 0, 0, 0));
+        for (int x = 0; x < kLanes; ++x) store16(at + chunk_at(r, x), make_uint4(0, 0, 0, 0));
     }
     // Values of nodes that are not finite become 0 (true: there were some): a row that does not see them would
     // get 0 * NaN.  The rows that do are given them at the end.
-    __device__ __forceinline__ bool take_odd(uint32_t at, int tid) const {
+    __device__ __forceinline__ bool take_odd(uint32_t at, int r) const {
         bool odd = false;
 #pragma unroll 4
-        for (int i = 0; i < kShare; ++i) {
-            const uint32_t to = at + chunk_at(tid & 127, (tid >> 7) * kShare + i);
+        for (int i = 0; i < kLanes; ++i) {
+            const uint32_t to = at + chunk_at(r, i);
             uint4 v = load16(to);
             if (odd_pair(v.x) || odd_pair(v.y) || odd_pair(v.z) || odd_pair(v.w)) {
                 constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
@@ -527,93 +609,109 @@ struct Attention {
         }
         return odd;
     }
-    // The page of this thread's row of a piece's tile t, -1 where there is none; the scales of its keys and values.
+    // Row r of a piece's tile t: whether there is one; its page as the table has it (0 where there is none); its row of the cache.
+    __device__ __forceinline__ bool is_row(const Piece &p, int t, int r) const {
+        const int pos = p.at + t * kTile + r;
+        return t < min(p.t1, p.context) && pos < p.to && pos >= p.from;
+    }
     __device__ __forceinline__ int row_page(const Piece &p, int t, int r) const {
-        const int pos = (first_tile(p) + t) * kTile + r;
-        if (t >= min(p.t1, p.context) || pos >= p.len || pos < begin(p)) return -1;
-        const int page = __ldg(a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width + (pos >> a.cache.page_bits));
-        return page < a.cache.pages ? page : -1;
+        return is_row(p, t, r) ? __ldg(a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width + ((p.at + t * kTile + r) >> a.cache.page_bits)) : -1;
     }
-    __device__ __forceinline__ int row_scales(const Piece &p, int t, int r, int page) const {  // keys', values' << 8; -1: no row
-        if (page < 0) return -1;
-        const int pos = (first_tile(p) + t) * kTile + r;
-        const size_t row = cache_row(a.cache, (static_cast<long long>(page) << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1)), p.g);
-        return __ldg(a.cache.scale[0] + row) | __ldg(a.cache.scale[1] + row) << 8;
+    __device__ __forceinline__ uint32_t row_scale(const Piece &p, int t, int r, int page, int w) const {
+        if (page < 0 || page >= a.cache.pages) return kNoRow;
+        const int pos = p.at + t * kTile + r;
+        return __ldg(a.cache.scale[w] + cache_row(a.cache, (static_cast<long long>(page) << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1)), p.g));
     }
-    // An 8-bit tile, widened: half a row a thread; the chunks in turned order, so that eight rows' meet different banks.
-    template <bool TWICE>
-    __device__ __forceinline__ void widen(uint32_t from, uint32_t to, int tid, const Widen<T> &w) const {
-        constexpr int kChunks = D / 32;
-        const int r = tid & 127;
-        uint4 v[kChunks];
+    static constexpr uint32_t kNoRow = 256;
+    // An 8-bit tile, widened: the chunks of 16 in turned order, so that eight rows' meet different banks.
+    __device__ __forceinline__ void widen(uint32_t from, uint32_t to, int r, const Widen<T> &w) const {
+        constexpr int kChunks = D / 16, kAhead = 4;
+#pragma unroll 1
+        for (int j0 = 0; j0 < kChunks; j0 += kAhead) {
+            uint4 v[kAhead];
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) v[j] = load16(from + r * D + turned(j, tid) * 16);
+            for (int j = 0; j < kAhead; ++j) v[j] = load16(from + r * D + turned(j0 + j, r) * 16);
 #pragma unroll
-        for (int j = 0; j < kChunks; ++j) {
-            const int x = turned(j, tid);
-            const uint2 b0 = w.template four<TWICE>(v[j].x), b1 = w.template four<TWICE>(v[j].y);
-            store16(to + chunk_at(r, 2 * x), make_uint4(b0.x, b0.y, b1.x, b1.y));
-            const uint2 b2 = w.template four<TWICE>(v[j].z), b3 = w.template four<TWICE>(v[j].w);
-            store16(to + chunk_at(r, 2 * x + 1), make_uint4(b2.x, b2.y, b3.x, b3.y));
+            for (int j = 0; j < kAhead; ++j) {
+                const int x = turned(j0 + j, r);
+                const uint2 b0 = w.four(v[j].x), b1 = w.four(v[j].y);
+                store16(to + chunk_at(r, 2 * x), make_uint4(b0.x, b0.y, b1.x, b1.y));
+                const uint2 b2 = w.four(v[j].z), b3 = w.four(v[j].w);
+                store16(to + chunk_at(r, 2 * x + 1), make_uint4(b2.x, b2.y, b3.x, b3.y));
+            }
         }
     }
-    // The j-th chunk of thread tid's half row: of 16 bytes, eight rows' in one step lie in eight places modulo 128 bytes.
-    static __device__ __forceinline__ int turned(int j, int tid) {
-        const int k = j + (tid >> 7) * (D / 32);
-        return D == 128 ? (k + tid) & 7 : (k + (tid >> 1)) & 3;
-    }
-    __device__ void work(int tid) {
-        Walk walk(a, c);
-        Piece p;
+    static __device__ __forceinline__ int turned(int j, int r) { return D == 128 ? (j + r) & 7 : (j + (r >> 1)) & 3; }
+    // 8 bits: this warpgroup's keys (w = 0) or values (w = 1), widened; values of nodes looked through.
+    __device__ void work8(int w, int r) {
         Cursor at, staged;
-        uint32_t copies = 0;  // the parity of each slot's next copy to look through
-        int count = 0;
+        if (w) at.step(a.ring), staged.step(a.stages);
+        uint32_t copies = 0;
         bool ok = true;
-        const int r = tid & 127;
-        while (ok && walk.next(&p)) {
-            int scales = -1, next_page = -1;  // of the tile at hand; of the one after it
-            if (Q8) {
-                scales = row_scales(p, p.t0, r, row_page(p, p.t0, r));
-                next_page = row_page(p, p.t0 + 1, r);
-            }
+        for (const Piece *pp; ok && (pp = next_piece()); done_piece()) {
+            const Piece &p = *pp;
+            // Two dependent loads, each issued a tile ahead of its use.
+            uint32_t byte = row_scale(p, p.t0, r, row_page(p, p.t0, r), w);
+            int next_page = row_page(p, p.t0 + 1, r);
             for (int t = p.t0; ok && t < p.t1; ++t) {
-                int next_scales = -1;
-                if (Q8) {  // two dependent loads, each issued a tile ahead of its use
-                    next_scales = row_scales(p, t + 1, r, next_page);
-                    next_page = row_page(p, t + 2, r);
+                const uint32_t next_byte = row_scale(p, t + 1, r, next_page, w);
+                next_page = row_page(p, t + 2, r);
+                const uint32_t to = ring(at.slot);
+                if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
+                if (t < p.context) {
+                    if (!(ok = wait(&c->staged[staged.slot], staged.round))) break;
+                    if (byte != kNoRow) {
+                        Widen<T> x;
+                        x.scale(byte);
+                        widen(stages + staged.slot * L::kStageBytes, to, r, x);
+                    } else {
+                        clear_rows(to, r, 0, 0);
+                    }
+                    __syncwarp();
+                    if (lane == 0) arrive(ptx::smem_addr(&c->free_[staged.slot]));
+                    staged.step(a.stages);
+                    staged.step(a.stages);
+                    fence_async();
+                } else if (w) {
+                    if (!(ok = look_through(p, at.slot, to, r, copies))) break;
                 }
-                for (int w = 0; ok && w < 2; ++w, at.step(L::kRing)) {
+                __syncwarp();
+                if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
+                at.step(a.ring);
+                at.step(a.ring);
+                byte = next_byte;
+            }
+        }
+    }
+    __device__ __forceinline__ bool look_through(const Piece &p, int slot, uint32_t to, int r, uint32_t &copies) {
+        if (!wait(&c->copied[slot], copies >> slot & 1)) return false;
+        copies ^= 1u << slot;
+        if (take_odd(to, r)) *const_cast<volatile int *>(&c->pieces[piece_at].odd) = 1;
+        fence_async();
+        return true;
+    }
+    __device__ void work(int r) {
+        Cursor at;
+        uint32_t copies = 0;  // the parity of each slot's next copy to look through
+        bool ok = true;
+        for (const Piece *pp; ok && (pp = next_piece()); done_piece()) {
+            const Piece &p = *pp;
+            for (int t = p.t0; ok && t < p.t1; ++t)
+                for (int w = 0; ok && w < 2; ++w, at.step(a.ring)) {
                     const uint32_t to = ring(at.slot);
                     if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
-                    if (Q8 && t < p.context) {
-                        if (!(ok = wait(&c->staged[staged.slot], staged.round))) break;
-                        Widen<T> x;
-                        if (scales >= 0) x.scale(scales >> (8 * w) & 255);
-                        else x.zero();
-                        const uint32_t from = stages + staged.slot * L::kStage;
-                        if (__any_sync(0xffffffffu, x.twice)) widen<true>(from, to, tid, x);
-                        else widen<false>(from, to, tid, x);
-                        __syncwarp();
-                        if (lane == 0) arrive(ptx::smem_addr(&c->free_[staged.slot]));
-                        staged.step(L::kStages > 0 ? L::kStages : 1);
-                        fence_async();
-                    } else if (w && (t >= p.context || ragged(p, t))) {
+                    if (w && t >= p.context) {
+                        if (!(ok = look_through(p, at.slot, to, r, copies))) break;
+                    } else if (w && !plain(p, t)) {
                         if (!(ok = wait(&c->copied[at.slot], copies >> at.slot & 1))) break;
                         copies ^= 1u << at.slot;
-                        if (t < p.context) {
-                            const int base = (first_tile(p) + t) * kTile;
-                            clear_rows(to, tid, begin(p) - base, p.len - base);
-                        } else if (take_odd(to, tid)) {
-                            *const_cast<volatile int *>(&c->odd[count & 7]) = 1;
-                        }
+                        const int base = p.at + t * kTile;
+                        clear_rows(to, r, p.from - base, p.to - base);
                         fence_async();
                     }
                     __syncwarp();
                     if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
                 }
-                scales = next_scales;
-            }
-            ++count;
         }
     }
 
@@ -621,8 +719,8 @@ struct Attention {
     // Which of a tile's columns 32 k .. 32 k + 31 a row of node n sees: a bit a column.
     __device__ __forceinline__ uint32_t seen(const Piece &p, int t, int n, int k) const {
         if (t < p.context) {
-            const int at = (first_tile(p) + t) * kTile + 32 * k;
-            const int from = min(max(begin(p) - at, 0), 32), to = min(max(p.len - at, 0), 32);
+            const int at = p.at + t * kTile + 32 * k;
+            const int from = min(max(p.from - at, 0), 32), to = min(max(p.to - at, 0), 32);
             return static_cast<uint32_t>((1ull << to) - 1) & ~static_cast<uint32_t>((1ull << from) - 1);
         }
         const int m = (t - p.context) * kTile + 32 * k;
@@ -657,82 +755,74 @@ struct Attention {
         }
         tmem_store16(to, y);
     }
-    // A tile's scores into weights, in two passes over tensor memory (the row's maximum, then the weights), 32 columns
-    // at a time, the next ones under way.  The loops stay loops: every unrolled copy is fetched cold in each launch.
+    // A row's maximum and sum move on to what `top`, the largest score of a tile, asks for; the sums are scaled along.
+    // `m` is what the exponents subtract, in units of log 2; -inf while the row has seen nothing.
+    __device__ __forceinline__ void move_on(float top, uint32_t o_at, bool first, float &m, float &l) const {
+        const float want = top - kShift;
+        const bool moves = m == -INFINITY ? want > -INFINITY : want > m + 8.0f;
+        if (!__any_sync(0xffffffffu, moves)) return;
+        const float f = moves ? (m == -INFINITY ? 0.0f : ptx::ex2(m - want)) : 1.0f;
+        l *= f;
+        if (moves) m = want;
+        __syncwarp();  // tensor memory's loads and stores take the warp as one: here and below, behind what parts it
+        if (first) return;
+#pragma unroll 1
+        for (int k = 0; k < D; k += 16) {
+            uint32_t y[16];
+            tmem_load16(y, o_at + k);
+            wait_loads(y);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+            tmem_store16(o_at + k, y);
+        }
+    }
+    __device__ __forceinline__ void weights_there(int s, int h, uint32_t arrivals) {
+        wait_stores();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive(ptx::smem_addr(&c->weights[s][h]), arrivals);
+    }
+    // A tile's scores into weights, whose halves the products may take one after the other: two passes over tensor
+    // memory (the row's maximum, then the weights), 32 columns at a time, the next ones under way.  The loops stay
+    // loops: the kinds of warps share the instruction caches, which their unrolled bodies would overflow.
     template <bool MASKED>
-    __device__ __forceinline__ void tile_weights(const Piece &p, int t, int n, uint32_t s_at, uint32_t o_at, float scale, bool first, float &m, float &l) {
+    __device__ __forceinline__ void tile_weights(int s, uint32_t arrivals, const uint32_t (&w)[4], uint32_t s_at, uint32_t o_at, float scale, bool first, float &m, float &l) {
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float2 c2 = make_float2(scale, scale);
         uint32_t x[32], y[32];
         float top = -INFINITY;
-        __syncwarp();  // tensor memory's loads and stores take the warp as one: here and below, behind what parts it
+        __syncwarp();
         tmem_load32(x, s_at);
 #pragma unroll 1
         for (int k = 0; k < 4; k += 2) {
-            const uint32_t w0 = MASKED ? seen(p, t, n, k) : 0, w1 = MASKED ? seen(p, t, n, k + 1) : 0;
-            if (MASKED) __syncwarp();
             wait_loads(x);
             tmem_load32(y, s_at + 32 * k + 32);
-            top = fmaxf(top, largest<MASKED>(x, w0));
+            top = fmaxf(top, largest<MASKED>(x, k ? w[2] : w[0]));
             wait_loads(y);
             tmem_load32(x, s_at + ((32 * k + 64) & 127));  // (the last: the first columns again, for the second pass)
-            top = fmaxf(top, largest<MASKED>(y, w1));
+            top = fmaxf(top, largest<MASKED>(y, k ? w[3] : w[1]));
         }
-        top = top * scale;
-        // `m` is what the exponents subtract; -inf while the row has seen nothing
-        const float want = top - kShift;
-        const bool moves = m == -INFINITY ? want > -INFINITY : want > m + 8.0f;
-        if (__any_sync(0xffffffffu, moves)) {
-            const float f = moves ? (m == -INFINITY ? 0.0f : ptx::ex2(m - want)) : 1.0f;
-            l *= f;
-            if (moves) m = want;
-            __syncwarp();
-            if (!first) {
-                wait_loads(x);
-#pragma unroll 1
-                for (int k = 0; k < D; k += 32) {
-                    tmem_load32(y, o_at + k);
-                    wait_loads(y);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                    tmem_store32(o_at + k, y);
-                }
-            }
-        }
+        wait_loads(x);
+        move_on(top * scale, o_at, first, m, l);
         const float sub = m == -INFINITY ? 0.0f : -m;
-        const float2 c2 = make_float2(scale, scale), s2 = make_float2(sub, sub);
-        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float2 s2 = make_float2(sub, sub);
         __syncwarp();
 #pragma unroll 1
         for (int k = 0; k < 4; k += 2) {
-            const uint32_t w0 = MASKED ? seen(p, t, n, k) : 0, w1 = MASKED ? seen(p, t, n, k + 1) : 0;
-            if (MASKED) __syncwarp();
-            wait_loads(x);
             tmem_load32(y, s_at + 32 * k + 32);
-            weigh<MASKED>(x, w0, c2, s2, sum, s_at + 16 * k);
+            weigh<MASKED>(x, k ? w[2] : w[0], c2, s2, sum, s_at + 16 * k);
             wait_loads(y);
             if (k == 0) tmem_load32(x, s_at + 64);
-            weigh<MASKED>(y, w1, c2, s2, sum, s_at + 16 * k + 16);
+            weigh<MASKED>(y, k ? w[3] : w[1], c2, s2, sum, s_at + 16 * k + 16);
+            weights_there(s, k / 2, arrivals);
+            if (k == 0) wait_loads(x);
         }
         const float2 both = add2(sum[0], sum[1]);
         l += both.x + both.y;
-        wait_stores();
     }
-    // Rows of a piece that see a value of a node which is not finite get it: 32 columns from column d0.
-    __device__ void add_odd(const Piece &p, const RowId &id, int d0, uint32_t (&x)[32]) const {
-        for (int t = max(p.t0, p.context); t < p.t1; ++t) {
-            for (int k = 0; k < 4; ++k)
-                for (uint32_t w = seen(p, t, id.n, k); w; w &= w - 1) {
-                    const int node = (t - p.context) * kTile + 32 * k + __ffs(w) - 1;
-                    const T *v = reinterpret_cast<const T *>(a.v) + p.b * a.stride[4] + node * a.stride[5] + p.g * D + d0;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float y = static_cast<float>(v[j]);
-                        if (!isfinite(y)) x[j] = __float_as_uint(__uint_as_float(x[j]) + y);
-                    }
-                }
-        }
-    }
+
     // Columns [d0, d1) of the block's row r: f0 * product 0's sums + f1 * product 1's, to where the piece's go.
-    __device__ void write_sums(const Piece &p, int r, int d0, int d1, bool use0, bool use1, float f0, float f1, float m, float l, bool odd) {
+    __device__ void write_sums(const Piece &p, int r, int d0, int d1, bool use0, bool use1, float f0, float f1, float m, float l) {
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21) + kSums;
         const bool live = r < p.rows;
         const RowId id = row_id(a, p, live ? r : 0);
@@ -745,6 +835,8 @@ struct Attention {
             else if (a.lse) a.lse[row] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
         }
         const float inv = final ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+        f0 *= inv;
+        f1 *= inv;
 #pragma unroll 1
         for (int d = d0; d < d1; d += 32) {
             uint32_t x[32];
@@ -765,82 +857,105 @@ struct Attention {
                     for (int j = 0; j < 16; ++j) x[h + j] = __float_as_uint(use0 ? fmaf(__uint_as_float(y[j]), f1, __uint_as_float(x[h + j])) : __uint_as_float(y[j]) * f1);
                 }
             }
-            if (live && odd) add_odd(p, id, d, x);
             if (live && final) {
                 uint4 *out = reinterpret_cast<uint4 *>(a.out + (row * D + d) * 2);
 #pragma unroll
                 for (int j = 0; j < 32; j += 8) {
                     float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[j + e]) * inv;
+                    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(x[j + e]);
                     out[j / 8] = pack8<T>(v);
                 }
             } else if (live) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) to.sums[static_cast<size_t>(d + j) * to.rows + r] = __uint_as_float(x[j]);
+                for (int j = 0; j < 32; j += 4)
+                    reinterpret_cast<float4 *>(to.sums)[(d + j) / 4 * to.rows + r] =
+                        make_float4(__uint_as_float(x[j]), __uint_as_float(x[j + 1]), __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
             }
+        }
+        if (*const_cast<volatile const int *>(&p.odd) && live) {
+            const int m0 = max(p.t0 - p.context, 0) * kTile, m1 = min((p.t1 - p.context) * kTile, a.N);
+            if (final) add_odd<T>(a, p.b, p.g, id.n, m0, m1, d0, d1, D, reinterpret_cast<T *>(a.out) + row * D, 4);
+            else add_odd<T>(a, p.b, p.g, id.n, m0, m1, d0, d1, D, to.sums + 4 * r, 4 * to.rows);
         }
     }
     __device__ void softmax(int s, int tid) {
-        Walk walk(a, c);
-        Piece p;
-        uint32_t scores_round = 0, sums_round = 0, joined_round = 0;
-        int count = 0;
+        uint32_t scores_round = 0, sums_round = 0, joined_round = 0, turn_round = 0;
         bool ok = true;
         const float scale = a.scale * kLog2e;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, at bit 16
-        while (ok && walk.next(&p)) {
-            const uint32_t s_at = tmem + lanes + kScores + s * 128, o_at = tmem + lanes + kSums + s * 128;
-            const int own = tid < a.half_nodes * a.group ? tid : kBlockRows, r = own + (p.two ? s * a.half_nodes * a.group : 0);  // this thread's row of the block
-            const bool idle = __all_sync(0xffffffffu, r >= p.rows);  // the warp has none
-            const int n = row_id(a, p, min(r, p.rows - 1)).n;
+        const uint32_t s_at = tmem + lanes + kScores + s * 128, o_at = tmem + lanes + kSums + s * 128;
+        const int half_rows = a.half_nodes * a.group;
+        for (const Piece *p; ok && (p = next_piece()); done_piece()) {
+            const bool two = p->two;
+            const int r = (tid < half_rows ? tid : kBlockRows) + (two ? s * half_rows : 0);  // this thread's row of the block
+            const bool idle = (warp & 3) != 0 && __all_sync(0xffffffffu, r >= p->rows);  // the warp has none: it only counts
+            // The first warp arrives for those that are idle.  (A last block may have no rows for product 1.)
+            const int live = max(1, (min(half_rows, p->rows - (two ? s * half_rows : 0)) + 31) / 32);
+            const uint32_t arrivals = (warp & 3) == 0 ? 5 - live : 1;
+            const int t0 = p->t0, t1 = p->t1, plain0 = p->plain0, plain1 = p->plain1, n = row_id(a, *p, min(r, p->rows - 1)).n;
             float m = -INFINITY, l = 0.0f;
             bool first = true;
-            for (int t = p.t0 + (p.two ? 0 : s); t < p.t1; t += p.two ? 1 : 2) {
-                if (!(ok = wait(&c->scores[s], scores_round))) break;
+            const int turn = p->turn ^ s;
+            for (int t = idle ? t1 : t0 + (two ? 0 : turn); t < t1; t += two ? 1 : 2) {
+                const bool masked = t < plain0 || t >= plain1;
+                uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+                if (masked)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] = seen(*p, t, n, k);
+                if (!(ok = hurry(&c->scores[s], scores_round))) break;
                 scores_round ^= 1;
-                fence_after();
-                if (!idle) {
-                    const bool masked = t >= p.context || ragged(p, t);
-                    if (masked) tile_weights<true>(p, t, n, s_at, o_at, scale, first, m, l);
-                    else tile_weights<false>(p, t, n, s_at, o_at, scale, first, m, l);
+                // Two products a tile: the warpgroups take turns, so that one's products run behind the other's weights.
+                if (two && (s || !first)) {
+                    if (!(ok = hurry(&c->turn[1 - s], turn_round))) break;
+                    turn_round ^= 1;
                 }
+                fence_after();
+                if (masked) tile_weights<true>(s, arrivals, w, s_at, o_at, scale, first, m, l);
+                else tile_weights<false>(s, arrivals, w, s_at, o_at, scale, first, m, l);
                 first = false;
-                fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(ptx::smem_addr(&c->weights[s]));
+                if (two && (s == 0 || t + 1 < t1)) {
+                    __syncwarp();
+                    if (lane == 0) arrive(ptx::smem_addr(&c->turn[s]), arrivals);
+                }
             }
             if (!ok) break;
-            const int any = p.two ? 2 : min(2, p.t1 - p.t0);  // products with sums
-            if (p.two || s < any) {
-                if (!(ok = wait(&c->sums[s], sums_round))) break;
+            if (two || t0 + turn < t1) {  // the product has sums
+                if (!(ok = idle ? wait(&c->sums[s], sums_round) : hurry(&c->sums[s], sums_round))) break;
                 sums_round ^= 1;
                 fence_after();
             }
-            const bool odd = *const_cast<volatile int *>(&c->odd[count & 7]) != 0 && !p.shared && p.t1 > p.context;
-            if (p.two) {
-                if (!idle) write_sums(p, r, 0, D, s == 0, s == 1, 1.0f, 1.0f, m, l, odd);
-                fence_before();
-            } else {
-                // Both products' sums: each warpgroup writes half the columns.
+            if (idle) {  // the rounds that went by
+                const int n = two ? t1 - t0 : (t1 - t0 - turn + 1) / 2;
+                scores_round ^= n & 1;
+                if (two) turn_round ^= (s ? n : n - 1) & 1;
+            }
+            // Two products a tile: each warpgroup writes its rows.  One: both products' sums are joined, and each
+            // warpgroup writes half the columns.
+            bool use0 = s == 0, use1 = s == 1;
+            float f0 = 1.0f, f1 = 1.0f;
+            if (!two) {
                 c->stats[s][tid] = make_float2(m, l);
                 fence_before();
                 __syncwarp();
                 if (lane == 0) arrive(ptx::smem_addr(&c->joined[0]));
-                if (!(ok = wait(&c->joined[0], joined_round))) break;
+                if (!idle && !(ok = hurry(&c->joined[0], joined_round))) break;
                 fence_after();
-                const float2 x = c->stats[0][tid], y = any == 2 ? c->stats[1][tid] : make_float2(-INFINITY, 0.0f);
-                const float top = fmaxf(x.x, y.x);
-                const float f0 = x.x == -INFINITY ? 0.0f : ptx::ex2(x.x - top), f1 = y.x == -INFINITY ? 0.0f : ptx::ex2(y.x - top);
-                if (!idle) write_sums(p, r, s * (D / 2), (s + 1) * (D / 2), true, any == 2, f0, f1, top, x.y * f0 + y.y * f1, odd);
-                fence_before();
+                const float2 x = c->stats[0][tid], y = c->stats[1][tid];
+                use0 = t1 - t0 > 1 || p->turn == 0, use1 = t1 - t0 > 1 || p->turn == 1;
+                m = fmaxf(x.x, y.x);
+                f0 = x.x == -INFINITY ? 0.0f : ptx::ex2(x.x - m), f1 = y.x == -INFINITY ? 0.0f : ptx::ex2(y.x - m);
+                l = x.y * f0 + y.y * f1;
+            }
+            if (!idle) write_sums(*p, r, two ? 0 : s * (D / 2), two ? D : (s + 1) * (D / 2), use0, use1, f0, f1, m, l);
+            fence_before();
+            if (!two) {
                 __syncwarp();
                 if (lane == 0) arrive(ptx::smem_addr(&c->joined[1]));
                 if (!(ok = wait(&c->joined[1], joined_round))) break;
                 joined_round ^= 1;
                 fence_after();
             }
-            ++count;
         }
     }
 };
@@ -850,7 +965,7 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attention_kernel(c
     using L = Layout<D, Q8>;
     constexpr int kThreads = L::kThreads;
     extern __shared__ __align__(1024) unsigned char smem[];
-    Control *c = reinterpret_cast<Control *>(smem + L::kBytes);
+    Control *c = reinterpret_cast<Control *>(smem + a.control);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     // Every CTA counts the tiles before each sequence: a thread some sequences, then a scan over threads.
@@ -877,23 +992,28 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attention_kernel(c
     if (lane == 31) c->scan[warp] = sum;
     if (tid == 0) {
         c->gave_up = 0;
-        for (int i = 0; i < 8; ++i) c->odd[i] = 0;
+        for (int i = 0; i < kPieces; ++i) {
+            ptx::mbar_init(ptx::smem_addr(&c->piece_there[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&c->piece_done[i]), 8 + L::kWorkers + 3);
+        }
         for (int i = 0; i < 8; ++i) {
-            ptx::mbar_init(ptx::smem_addr(&c->full[i]), L::kWorkers + 1);
-            ptx::mbar_init(ptx::smem_addr(&c->empty[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&c->full[i]), 4 + 1);
+            ptx::mbar_init(ptx::smem_addr(&c->empty[i]), 2);
             ptx::mbar_init(ptx::smem_addr(&c->copied[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&c->staged[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&c->free_[i]), L::kWorkers);
+            ptx::mbar_init(ptx::smem_addr(&c->free_[i]), 4);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_addr(&c->q_full[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&c->q_empty[i]), 1);
+            ptx::mbar_init(ptx::smem_addr(&c->q_empty[i]), 2);
             ptx::mbar_init(ptx::smem_addr(&c->scores[i]), 1);
-            ptx::mbar_init(ptx::smem_addr(&c->weights[i]), 4);
+            ptx::mbar_init(ptx::smem_addr(&c->weights[i][0]), 4);
+            ptx::mbar_init(ptx::smem_addr(&c->weights[i][1]), 4);
             ptx::mbar_init(ptx::smem_addr(&c->sums[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&c->joined[i]), 8);
+            ptx::mbar_init(ptx::smem_addr(&c->turn[i]), 4);
         }
-        ptx::mbar_init(ptx::smem_addr(&c->drained), 1);
+        ptx::mbar_init(ptx::smem_addr(&c->drained), 2);
         ptx::fence_mbar_init();
     }
     __syncthreads();
@@ -917,17 +1037,26 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attention_kernel(c
     __syncthreads();
     fence_after();
 
-    Attention<T, D, Q8> x{a, c, ptx::smem_addr(smem), ptx::smem_addr(smem) + 2 * L::kQ + L::kRing * L::kQ, c->tmem, lane, warp};
+    const uint32_t queries = ptx::smem_addr(smem), tiles_at = queries + 2 * (D / 64) * a.q_sub;
+    Attention<T, D, Q8> x{a, c, queries, tiles_at, tiles_at + a.ring * L::kTileBytes, c->tmem, lane, warp};
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftmaxRegs));
         x.softmax(warp >> 2, tid & 127);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
-        if (warp < kFirst) x.work(tid - 256);
-        else if (warp == kFirst) x.load_tiles(maps);
-        else if (warp == kFirst + 1) x.multiply();
-        else if (warp == kFirst + 2) x.load_queries(maps);
-        else if (Q8) x.load_stages(maps);
+        if (warp < kFirst) {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kWorkerRegs));
+            if (Q8) x.work8(warp >= 12, tid & 127);
+            else x.work(tid & 127);
+        } else if (warp == kFirst + 1 || warp == kFirst + 2) {
+            if (lane == 0) x.multiply(warp - kFirst - 1);
+            __syncwarp();
+        } else if (warp == kFirst) {
+            if (Q8) x.lead_tiles(maps);
+            else x.load_tiles(maps);
+        } else {
+            if (Q8) x.load_stages(maps);
+            else x.lead(maps);
+        }
     }
 
     fence_before();
@@ -960,9 +1089,10 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
     const auto take = [&](const Part &p, int at) {
         const float2 s = p.stats[at];
-        float x[E];
+        alignas(16) float x[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = p.sums[static_cast<size_t>(warp * E + e) * p.rows + at];
+        for (int e = 0; e < E; e += 4)
+            *reinterpret_cast<float4 *>(x + e) = reinterpret_cast<const float4 *>(p.sums)[(warp * E + e) / 4 * p.rows + at];
         const float top = fmaxf(m, s.x), was = m == -INFINITY ? 0.0f : ptx::ex2(m - top), now = s.x == -INFINITY ? 0.0f : ptx::ex2(s.x - top);
         l = l * was + s.y * now;
 #pragma unroll

@@ -38,6 +38,8 @@ struct AttentionArgs {
     int q_nodes;                      // nodes that a copy of queries brings
     int q_merged;                     // the batch's nodes are evenly spaced: one axis
     int ctas;
+    // shared memory: bytes of 64 columns of a half's queries, tiles in the ring, 8-bit tiles, where Control begins
+    int q_sub, ring, stages, control;
     // the workspace
     int32_t *starts;   // [B + 1] tiles before each sequence's
     float *cut_sums;   // [ctas][2][D][kBlockRows]: blocks cut at a CTA's begin and at its end

@@ -50,11 +50,13 @@ spec_status launch_attention(const AttentionArgs &a0, cudaStream_t stream) {
     auto kernel = attention_kernel<T, D, Q8>;
     st = allow_max_dyn_smem(dev, reinterpret_cast<const void *>(kernel), &di);
     if (st != SPEC_OK) return st;
-    constexpr size_t smem = Layout<D, Q8>::kBytes + sizeof(Control);
-    static_assert(smem <= 227 * 1024, "shared memory of a CTA");
-    if (smem > di.max_dyn) return fail(SPEC_ERR_UNSUPPORTED, "%zu bytes of shared memory needed, %zu there", smem, di.max_dyn);
     AttentionArgs a = a0;
     a.ctas = std::min(di.sms, kMaxCtas);
+    // All the shared memory there is, so that one CTA is on an SM: each takes all of its tensor memory.
+    a.control = static_cast<int>((di.max_dyn - sizeof(Control)) / 1024 * 1024);
+    share_out<D, Q8>(&a, a.control);
+    const size_t smem = a.control + sizeof(Control);
+    if (a.ring < 4 || (Q8 && a.stages < 2)) return fail(SPEC_ERR_UNSUPPORTED, "%zu bytes of shared memory a CTA do not do", di.max_dyn);
     const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int kv = a.cache.kv_heads;
     Maps maps;

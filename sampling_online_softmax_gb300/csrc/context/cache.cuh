@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheRo
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
                 const float2 f = e4m3x2((k < 4 ? q.x : q.y) >> (k % 4 * 8));
-                v[k] = Elt<T>::clamp(f.x * s);
-                v[k + 1] = Elt<T>::clamp(f.y * s);
+                v[k] = f.x * s;
+                v[k + 1] = f.y * s;
             }
             x = pack8<T>(v);
         }

@@ -24,7 +24,6 @@ struct Elt<__nv_bfloat16> {
         const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&v);
     }
-    static __device__ __forceinline__ float clamp(float x) { return x; }
 };
 
 template <>
@@ -36,8 +35,6 @@ struct Elt<__half> {
         const __half2 v = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&v);
     }
-    // A cache written from bf16 may hold more than fp16 does: the largest finite value then (NaN stays).
-    static __device__ __forceinline__ float clamp(float x) { return x > 65504.0f ? 65504.0f : x < -65504.0f ? -65504.0f : x; }
 };
 
 template <typename T>

@@ -86,13 +86,8 @@ __device__ __forceinline__ uint64_t descriptor(uint32_t low) {
     constexpr uint32_t kHigh = 1024 >> 4 | 1u << 14 | 2u << 29;  // 1024 bytes between groups of 8 rows; version; swizzle
     return static_cast<uint64_t>(kHigh) << 32 | low;
 }
-__device__ __forceinline__ bool elect() {  // one lane of a whole warp
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
 // `type`: 0 fp16, 1 bf16; `rows_inner`: B's rows run along the inner axis (its columns are contiguous).
-constexpr uint32_t instruction(uint32_t type, uint32_t n, bool rows_inner) {
+__host__ __device__ constexpr uint32_t instruction(uint32_t type, uint32_t n, bool rows_inner) {
     return 1u << 4 | type << 7 | type << 10 | (rows_inner ? 1u << 16 : 0u) | n >> 3 << 17 | 128u >> 4 << 24;
 }
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, bool add) {
@@ -138,14 +133,32 @@ __device__ __forceinline__ void arrive(uint32_t bar, uint32_t n = 1) {
 // What generic stores wrote to shared memory is there for the tensor cores and TMA.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-constexpr int kWaitTries = 1 << 20;  // each suspends the warp for a while: far beyond any wait that ends
+constexpr int kWaitTries = 1 << 20;  // each suspends the thread for a while: far beyond any wait that ends
 
-// A whole warp waits for a barrier's phase; false after kWaitTries, or once another warp of the CTA
-// has given up.  Nothing spins for ever: on false the caller leaves its loop.
+// (mbar_try_wait takes no hint of a time to suspend for: with one of a microsecond the thread slept past the phase's end.)
+
+// A thread waits for a barrier's phase; false after kWaitTries, or once another of the CTA has given up.  Nothing spins
+// for ever: on false the caller leaves its loop.
+__device__ __forceinline__ bool wait_alone(uint32_t bar, uint32_t parity, volatile int *gave_up, uint32_t *status) {
+    bool done = ptx::mbar_try_wait(bar, parity);
+    for (int i = 1; !done && i < kWaitTries; ++i) {
+        if ((i & 63) == 0 && *gave_up) return false;
+        done = ptx::mbar_try_wait(bar, parity);
+    }
+    if (!done) {
+        *gave_up = 1;
+        atomicOr(status, SPEC_DEV_TIMEOUT);
+    }
+    return done;
+}
+// The same for a whole warp, which sleeps between its tries where it is not in a hurry: warps that ask all the time
+// take shared memory's ports from those that work.
+template <bool HURRY>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *gave_up, uint32_t *status) {
     bool done = ptx::mbar_try_wait(bar, parity);
     for (int i = 1; !done && i < kWaitTries; ++i) {
         if ((i & 63) == 0 && *gave_up) break;
+        if (!HURRY) __nanosleep(100);
         done = ptx::mbar_try_wait(bar, parity);
     }
     done = __all_sync(0xffffffffu, done);
