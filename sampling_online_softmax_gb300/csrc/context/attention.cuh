@@ -11,7 +11,7 @@
 //
 //   warps 0-3, 4-7   softmax of product 0, 1: a thread a row
 //   four warps       values whose other rows must be 0 (what lies behind a sequence's end, nodes that are
-//                    not finite: 0 * NaN is NaN); eight of them where 8-bit tiles are widened too
+//                    not finite: 0 * NaN is NaN); 8-bit tiles, widened
 //   a lane each      tcgen05.mma of product 0, of product 1
 //   one or two warps the list of work, TMA of queries and of tiles; with 8-bit tiles one more for their TMA
 //
@@ -35,11 +35,10 @@ template <int D, bool Q8>
 struct Layout {
     static constexpr int kTileBytes = kTile * D * 2;         // of 128 rows of keys or values
     static constexpr int kStageBytes = Q8 ? kTile * D : 0;   // of an 8-bit tile
-    static constexpr int kWorkers = Q8 ? 8 : 4;              // warps that clear and widen: in 8 bits four for keys, four for values
+    static constexpr int kWorkers = 4;                       // warps that clear and widen
     static constexpr int kThreads = (8 + kWorkers + 4) * 32;
-    // Registers of a thread after the start, by role: over the warpgroups they sum to what the launch has, 512 at 512
-    // threads (128 each), 480 at 640 (96 each).
-    static constexpr int kSoftmaxRegs = Q8 ? 144 : 160, kWorkerRegs = Q8 ? 48 : 64;  // (the single warps keep the launch's)
+    // Registers of a thread after the start, by role: over the four warpgroups they sum to what the launch has, 4 * 128.
+    static constexpr int kSoftmaxRegs = 176, kWorkerRegs = 64, kSingleRegs = 96;
 };
 
 // How shared memory is shared out: two halves of queries, as many rows of each as a launch has (a product reads 128 rows
@@ -52,7 +51,7 @@ inline void share_out(AttentionArgs *a, int room) {
     int left = room - 2 * a->q_sub * (D / 64);
     a->ring = Q8 ? (D == 128 ? 4 : 8) : std::min(8, left / L::kTileBytes);
     left -= a->ring * L::kTileBytes;
-    a->stages = Q8 ? std::min(8, left / L::kStageBytes) & ~1 : 0;  // (ring and stages even: each group of workers sees its own slots)
+    a->stages = Q8 ? std::min(8, left / L::kStageBytes) : 0;
 }
 
 // A CTA's run of the list, cut at the blocks' borders.
@@ -78,11 +77,11 @@ struct Control {  // behind the tiles in shared memory
     uint64_t q_full[2], q_empty[2];
     uint64_t scores[2], weights[2][2], sums[2];  // of the two products; weights of a tile's first and second 64 keys
     uint64_t joined[2];            // both warpgroups: statistics there, sums read
-    uint64_t turn[2];              // a warpgroup's weights of a tile are done
+    uint64_t turn[2];              // a warpgroup's weights of a tile are worked out
     uint64_t drained;
     uint32_t tmem;
     int gave_up;
-    int scan[20];
+    int scan[16];
     int total, b, before;          // tiles in all; the sequence a CTA begins in and the tiles before it
     float2 stats[2][kTile];
 };
@@ -609,18 +608,18 @@ struct Attention {
         }
         return odd;
     }
-    // Row r of a piece's tile t: whether there is one; its page as the table has it (0 where there is none); its row of the cache.
-    __device__ __forceinline__ bool is_row(const Piece &p, int t, int r) const {
-        const int pos = p.at + t * kTile + r;
-        return t < min(p.t1, p.context) && pos < p.to && pos >= p.from;
+    // The row of a thread at position `pos` of a piece: its page as the table has it (-1: no such row), and the scale of its
+    // keys (w = 0) or values, from a page.
+    __device__ __forceinline__ int row_page(const int32_t *table, int pos, int from, int to) const {
+        return pos >= from && pos < to ? __ldg(table + (pos >> a.cache.page_bits)) : -1;
     }
-    __device__ __forceinline__ int row_page(const Piece &p, int t, int r) const {
-        return is_row(p, t, r) ? __ldg(a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width + ((p.at + t * kTile + r) >> a.cache.page_bits)) : -1;
-    }
-    __device__ __forceinline__ uint32_t row_scale(const Piece &p, int t, int r, int page, int w) const {
-        if (page < 0 || page >= a.cache.pages) return kNoRow;
-        const int pos = p.at + t * kTile + r;
-        return __ldg(a.cache.scale[w] + cache_row(a.cache, (static_cast<long long>(page) << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1)), p.g));
+    __device__ __forceinline__ void row_scales(int page, int pos, int g, uint32_t &key, uint32_t &value) const {
+        key = value = kNoRow;
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.cache.pages)) return;
+        const int in_page = (g << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1));
+        const size_t row = static_cast<size_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(a.cache.kv_heads << a.cache.page_bits) + in_page;
+        key = __ldg(a.cache.scale[0] + row);
+        value = __ldg(a.cache.scale[1] + row);
     }
     static constexpr uint32_t kNoRow = 256;
     // An 8-bit tile, widened: the chunks of 16 in turned order, so that eight rows' meet different banks.
@@ -642,44 +641,47 @@ struct Attention {
         }
     }
     static __device__ __forceinline__ int turned(int j, int r) { return D == 128 ? (j + r) & 7 : (j + (r >> 1)) & 3; }
-    // 8 bits: this warpgroup's keys (w = 0) or values (w = 1), widened; values of nodes looked through.
-    __device__ void work8(int w, int r) {
+    // 8 bits: keys and values widened, values of nodes looked through.
+    __device__ void work8(int r) {
         Cursor at, staged;
-        if (w) at.step(a.ring), staged.step(a.stages);
         uint32_t copies = 0;
         bool ok = true;
         for (const Piece *pp; ok && (pp = next_piece()); done_piece()) {
             const Piece &p = *pp;
             // Two dependent loads, each issued a tile ahead of its use.
-            uint32_t byte = row_scale(p, p.t0, r, row_page(p, p.t0, r), w);
-            int next_page = row_page(p, p.t0 + 1, r);
-            for (int t = p.t0; ok && t < p.t1; ++t) {
-                const uint32_t next_byte = row_scale(p, t + 1, r, next_page, w);
-                next_page = row_page(p, t + 2, r);
-                const uint32_t to = ring(at.slot);
-                if (!(ok = wait(&c->empty[at.slot], at.round ^ 1))) break;
-                if (t < p.context) {
-                    if (!(ok = wait(&c->staged[staged.slot], staged.round))) break;
-                    if (byte != kNoRow) {
-                        Widen<T> x;
-                        x.scale(byte);
-                        widen(stages + staged.slot * L::kStageBytes, to, r, x);
-                    } else {
-                        clear_rows(to, r, 0, 0);
+            const int32_t *table = a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width;
+            const int from = p.from, end = min(p.to, p.at + p.t1 * kTile), context = p.context, t1 = p.t1, g = p.g;
+            int pos = p.at + p.t0 * kTile + r;
+            uint32_t next_key, next_value;
+            row_scales(row_page(table, pos, from, end), pos, g, next_key, next_value);
+            int next_page = row_page(table, pos + kTile, from, end);
+            for (int t = p.t0; ok && t < t1; ++t, pos += kTile) {
+                const uint32_t key = next_key, value = next_value;
+                row_scales(next_page, pos + kTile, g, next_key, next_value);
+                next_page = row_page(table, pos + 2 * kTile, from, end);
+#pragma unroll 1
+                for (int w = 0; w < 2; ++w, at.step(a.ring)) {
+                    const uint32_t to = ring(at.slot), byte = w ? value : key;
+                    if (!(ok = hurry(&c->empty[at.slot], at.round ^ 1))) break;
+                    if (t < context) {
+                        if (!(ok = hurry(&c->staged[staged.slot], staged.round))) break;
+                        if (byte != kNoRow) {
+                            Widen<T> x;
+                            x.scale(byte);
+                            widen(stages + staged.slot * L::kStageBytes, to, r, x);
+                        } else {
+                            clear_rows(to, r, 0, 0);
+                        }
+                        __syncwarp();
+                        if (lane == 0) arrive(ptx::smem_addr(&c->free_[staged.slot]));
+                        staged.step(a.stages);
+                        fence_async();
+                    } else if (w) {
+                        if (!(ok = look_through(p, at.slot, to, r, copies))) break;
                     }
                     __syncwarp();
-                    if (lane == 0) arrive(ptx::smem_addr(&c->free_[staged.slot]));
-                    staged.step(a.stages);
-                    staged.step(a.stages);
-                    fence_async();
-                } else if (w) {
-                    if (!(ok = look_through(p, at.slot, to, r, copies))) break;
+                    if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
                 }
-                __syncwarp();
-                if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
-                at.step(a.ring);
-                at.step(a.ring);
-                byte = next_byte;
             }
         }
     }
@@ -730,15 +732,13 @@ struct Attention {
         else w &= static_cast<uint32_t>((1ull << min(max(n - m + 1, 0), 32)) - 1);
         return w;
     }
-    template <bool MASKED>
     static __device__ __forceinline__ float largest(const uint32_t (&x)[32], uint32_t w) {
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], MASKED && !((w >> j) & 1) ? -INFINITY : __uint_as_float(x[j]));
+        for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], !((w >> j) & 1) ? -INFINITY : __uint_as_float(x[j]));
         return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     }
     // Weights of 32 columns into tensor memory; their sum is added to `sum`.
-    template <bool MASKED>
     static __device__ __forceinline__ void weigh(const uint32_t (&x)[32], uint32_t w, float2 scale, float2 sub, float2 (&sum)[2], uint32_t to) {
         uint32_t y[16];
 #pragma unroll
@@ -746,10 +746,8 @@ struct Attention {
             float2 e = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), scale, sub);
             e.x = ptx::ex2(e.x);
             e.y = ptx::ex2(e.y);
-            if (MASKED) {
-                if (!((w >> j) & 1)) e.x = 0.0f;
-                if (!((w >> (j + 1)) & 1)) e.y = 0.0f;
-            }
+            if (!((w >> j) & 1)) e.x = 0.0f;
+            if (!((w >> (j + 1)) & 1)) e.y = 0.0f;
             sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
             y[j / 2] = Elt<T>::from_float2(e.x, e.y);
         }
@@ -757,9 +755,9 @@ struct Attention {
     }
     // A row's maximum and sum move on to what `top`, the largest score of a tile, asks for; the sums are scaled along.
     // `m` is what the exponents subtract, in units of log 2; -inf while the row has seen nothing.
-    __device__ __forceinline__ void move_on(float top, uint32_t o_at, bool first, float &m, float &l) const {
+    __device__ __forceinline__ void move_on(float top, bool live, uint32_t o_at, bool first, float &m, float &l) const {
         const float want = top - kShift;
-        const bool moves = m == -INFINITY ? want > -INFINITY : want > m + 8.0f;
+        const bool moves = live && (m == -INFINITY ? want > -INFINITY : want > m + 8.0f);
         if (!__any_sync(0xffffffffu, moves)) return;
         const float f = moves ? (m == -INFINITY ? 0.0f : ptx::ex2(m - want)) : 1.0f;
         l *= f;
@@ -782,11 +780,51 @@ struct Attention {
         __syncwarp();
         if (lane == 0) arrive(ptx::smem_addr(&c->weights[s][h]), arrivals);
     }
+    // A tile's scores into weights in one pass, against the maximum as it stands: false, and nothing done, where a row's
+    // has to move on (or the row has seen nothing yet).  Every key is seen.
+    __device__ __forceinline__ bool quick_weights(int s, uint32_t arrivals, bool live, const uint64_t *turn, uint32_t s_at, float scale, float m, float &l) {
+        uint32_t x[32], y[32], p0[32], p1[32];
+        float top = -INFINITY;
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float2 c2 = make_float2(scale, scale), s2 = make_float2(-m, -m);
+        __syncwarp();
+        tmem_load32(x, s_at);
+        wait_loads(x);
+        tmem_load32(y, s_at + 32);
+        weigh_into(x, c2, s2, sum, top, p0, 0);
+        wait_loads(y);
+        tmem_load32(x, s_at + 64);
+        weigh_into(y, c2, s2, sum, top, p0, 16);
+        wait_loads(x);
+        tmem_load32(y, s_at + 96);
+        weigh_into(x, c2, s2, sum, top, p1, 0);
+        wait_loads(y);
+        weigh_into(y, c2, s2, sum, top, p1, 16);
+        if (turn && lane == 0) arrive(ptx::smem_addr(turn), arrivals);  // the arithmetic is done
+        if (__any_sync(0xffffffffu, live && !(top * scale - kShift <= m + 8.0f))) return false;  // (also where either is NaN)
+        tmem_store32(s_at, p0);
+        weights_there(s, 0, arrivals);
+        tmem_store32(s_at + 32, p1);
+        weights_there(s, 1, arrivals);
+        const float2 both = add2(sum[0], sum[1]);
+        l += both.x + both.y;
+        return true;
+    }
+    static __device__ __forceinline__ void weigh_into(const uint32_t (&x)[32], float2 scale, float2 sub, float2 (&sum)[2], float &top, uint32_t (&to)[32], int at) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            top = fmaxf(top, fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
+            float2 e = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), scale, sub);
+            e.x = ptx::ex2(e.x);
+            e.y = ptx::ex2(e.y);
+            sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
+            to[at + j / 2] = Elt<T>::from_float2(e.x, e.y);
+        }
+    }
     // A tile's scores into weights, whose halves the products may take one after the other: two passes over tensor
     // memory (the row's maximum, then the weights), 32 columns at a time, the next ones under way.  The loops stay
     // loops: the kinds of warps share the instruction caches, which their unrolled bodies would overflow.
-    template <bool MASKED>
-    __device__ __forceinline__ void tile_weights(int s, uint32_t arrivals, const uint32_t (&w)[4], uint32_t s_at, uint32_t o_at, float scale, bool first, float &m, float &l) {
+    __device__ __forceinline__ void tile_weights(int s, uint32_t arrivals, bool live, const uint32_t (&w)[4], uint32_t s_at, uint32_t o_at, float scale, bool first, float &m, float &l) {
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         const float2 c2 = make_float2(scale, scale);
         uint32_t x[32], y[32];
@@ -797,23 +835,23 @@ struct Attention {
         for (int k = 0; k < 4; k += 2) {
             wait_loads(x);
             tmem_load32(y, s_at + 32 * k + 32);
-            top = fmaxf(top, largest<MASKED>(x, k ? w[2] : w[0]));
+            top = fmaxf(top, largest(x, k ? w[2] : w[0]));
             wait_loads(y);
             tmem_load32(x, s_at + ((32 * k + 64) & 127));  // (the last: the first columns again, for the second pass)
-            top = fmaxf(top, largest<MASKED>(y, k ? w[3] : w[1]));
+            top = fmaxf(top, largest(y, k ? w[3] : w[1]));
         }
         wait_loads(x);
-        move_on(top * scale, o_at, first, m, l);
+        move_on(top * scale, live, o_at, first, m, l);
         const float sub = m == -INFINITY ? 0.0f : -m;
         const float2 s2 = make_float2(sub, sub);
         __syncwarp();
 #pragma unroll 1
         for (int k = 0; k < 4; k += 2) {
             tmem_load32(y, s_at + 32 * k + 32);
-            weigh<MASKED>(x, k ? w[2] : w[0], c2, s2, sum, s_at + 16 * k);
+            weigh(x, k ? w[2] : w[0], c2, s2, sum, s_at + 16 * k);
             wait_loads(y);
             if (k == 0) tmem_load32(x, s_at + 64);
-            weigh<MASKED>(y, k ? w[3] : w[1], c2, s2, sum, s_at + 16 * k + 16);
+            weigh(y, k ? w[3] : w[1], c2, s2, sum, s_at + 16 * k + 16);
             weights_there(s, k / 2, arrivals);
             if (k == 0) wait_loads(x);
         }
@@ -891,6 +929,7 @@ struct Attention {
             const int r = (tid < half_rows ? tid : kBlockRows) + (two ? s * half_rows : 0);  // this thread's row of the block
             const bool idle = (warp & 3) != 0 && __all_sync(0xffffffffu, r >= p->rows);  // the warp has none: it only counts
             // The first warp arrives for those that are idle.  (A last block may have no rows for product 1.)
+            const bool has_row = r < p->rows;
             const int live = max(1, (min(half_rows, p->rows - (two ? s * half_rows : 0)) + 31) / 32);
             const uint32_t arrivals = (warp & 3) == 0 ? 5 - live : 1;
             const int t0 = p->t0, t1 = p->t1, plain0 = p->plain0, plain1 = p->plain1, n = row_id(a, *p, min(r, p->rows - 1)).n;
@@ -906,18 +945,18 @@ struct Attention {
                 if (!(ok = hurry(&c->scores[s], scores_round))) break;
                 scores_round ^= 1;
                 // Two products a tile: the warpgroups take turns, so that one's products run behind the other's weights.
+                const uint64_t *pass = two && (s == 0 || t + 1 < t1) ? &c->turn[s] : nullptr;
                 if (two && (s || !first)) {
                     if (!(ok = hurry(&c->turn[1 - s], turn_round))) break;
                     turn_round ^= 1;
                 }
                 fence_after();
-                if (masked) tile_weights<true>(s, arrivals, w, s_at, o_at, scale, first, m, l);
-                else tile_weights<false>(s, arrivals, w, s_at, o_at, scale, first, m, l);
-                first = false;
-                if (two && (s == 0 || t + 1 < t1)) {
-                    __syncwarp();
-                    if (lane == 0) arrive(ptx::smem_addr(&c->turn[s]), arrivals);
+                const bool slow = masked || first;
+                if (slow || !quick_weights(s, arrivals, has_row, pass, s_at, scale, m, l)) {
+                    tile_weights(s, arrivals, has_row, w, s_at, o_at, scale, first, m, l);
+                    if (slow && pass && lane == 0) arrive(ptx::smem_addr(pass), arrivals);
                 }
+                first = false;
             }
             if (!ok) break;
             if (two || t0 + turn < t1) {  // the product has sums
@@ -1043,9 +1082,10 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attention_kernel(c
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftmaxRegs));
         x.softmax(warp >> 2, tid & 127);
     } else {
+        if (warp < kFirst) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kWorkerRegs));
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kSingleRegs));
         if (warp < kFirst) {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kWorkerRegs));
-            if (Q8) x.work8(warp >= 12, tid & 127);
+            if (Q8) x.work8(tid & 127);
             else x.work(tid & 127);
         } else if (warp == kFirst + 1 || warp == kFirst + 2) {
             if (lane == 0) x.multiply(warp - kFirst - 1);
