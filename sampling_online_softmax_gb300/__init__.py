@@ -761,11 +761,10 @@ def _cache_arg(k_cache, v_cache, page_table, k_scale, v_scale, B, heads, dim, dt
         raise ValueError("k_scale and v_scale belong to a float8_e4m3fn cache, and it needs both")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, width]")
-    shape = (pages, kv, page)
-    return _Cache(_need(k_cache, "k_cache", k_cache.dtype, (*shape, d), dev, i), _need(v_cache, "v_cache", k_cache.dtype, (*shape, d), dev, i),
+    shape, width = (pages, kv, page), page_table.shape[1]
+    return _Cache(_need(k_cache, "k_cache", k_cache.dtype, (pages, kv, page, d), dev, i), _need(v_cache, "v_cache", k_cache.dtype, (pages, kv, page, d), dev, i),
                   _may(k_scale, "k_scale", torch.uint8, shape, dev, i), _may(v_scale, "v_scale", torch.uint8, shape, dev, i),
-                  _need(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev, i),
-                  SPEC_E4M3 if q8 else _CODES[dtype], pages, page, kv, d, page_table.shape[1])
+                  _need(page_table, "page_table", torch.int32, (B, width), dev, i), SPEC_E4M3 if q8 else _CODES[dtype], pages, page, kv, d, width)
 
 
 def _on_gpu(t, name):

@@ -22,20 +22,21 @@ spec_status launch_adjust(AdjustArgs a, cudaStream_t stream) {
     auto kernel = adjust_kernel<EB, VEC, INPLACE>;
     st = allow_max_dyn_smem(dev, reinterpret_cast<const void *>(kernel), &di);
     if (st != SPEC_OK) return st;
-    // Each CTA reads its sequence's whole history, so slices are long and a CTA takes all rows of
-    // its sequence, unless that leaves SMs idle: then shorter slices, and then fewer rows.
-    const long long want = 4ll * di.sms;
+    // Each CTA reads its sequence's whole history, so slices are long and a CTA takes all rows of its
+    // sequence, unless that leaves SMs idle (the slices of the common tokens have most of the listed ones, so
+    // a few CTAs an SM): then fewer rows, and then shorter slices.
+    const long long want = 8ll * di.sms;
     const auto slices = [&](int n) { return (a.V + n - 1) / n; };
     a.slice = kMaxSlice;
-    while (a.slice > kMinSlice && static_cast<long long>(a.B) * slices(a.slice) < want) a.slice /= 2;
     a.slices = slices(a.slice);
-    const long long per_row = static_cast<long long>(a.B) * a.slices;
-    a.groups = static_cast<int>(std::min<long long>(a.N, std::max<long long>(1, want / per_row)));
+    const int most = (a.N + kAdjustRows - 1) / kAdjustRows;  // groups of rows
+    a.groups = static_cast<int>(std::min<long long>(most, std::max<long long>(1, want / (static_cast<long long>(a.B) * a.slices))));
     a.rows = (a.N + a.groups - 1) / a.groups;
     a.groups = (a.N + a.rows - 1) / a.rows;
+    while (a.slice > kMinSlice && static_cast<long long>(a.B) * a.groups * a.slices < want) a.slice /= 2, a.slices = slices(a.slice);
+    const long long per_row = static_cast<long long>(a.B) * a.slices;
     if (per_row * a.groups > INT_MAX) return fail(SPEC_ERR_UNSUPPORTED, "too many rows (B=%d, N=%d, V=%d)", a.B, a.N, a.V);
-    const bool counts = a.repetition || a.frequency || a.presence;
-    const size_t smem = 4 * (a.slice / 32 + 1 + static_cast<size_t>(a.slice) * ((counts ? 1 : 0) + (a.M ? 1 : 0)));
+    const size_t smem = 4 * static_cast<size_t>(AdjustShared(a).words);
     kernel<<<static_cast<unsigned>(per_row * a.groups), kAdjustThreads, smem, stream>>>(a);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "adjust launch: %s", cudaGetErrorString(e));

@@ -1,15 +1,16 @@
 // adjust.cuh -- penalties for repeated tokens, biases and grammar masks on rows of logits.
 //
 // A CTA takes one slice of the vocabulary of one sequence and some of its rows.  It counts the
-// history once into a table of the slice in shared memory (one word a token: bit 31 says that the
-// prompt holds it, the rest count the generated occurrences), with a bit a token that anything may
-// change.  Then it streams the slice of its rows: a 16-byte vector without such a bit is copied
-// under its mask bits, the others are computed token by token.  The drafted tokens of a row's own
-// path are added to the table before the row and taken out behind it, by integer atomics on shared
-// memory, whose order changes nothing.
+// history once into a table of the slice in shared memory (a word a token: bit 31 says that the prompt
+// holds it, the rest count the generated occurrences) and lists the tokens that anything may change.
+// Then, a few rows at a time, it streams the slice under the mask bits, 16 bytes a load, and computes the
+// listed tokens over what it streamed.  In text these are a tenth of the tokens here and there: computed
+// in the stream they would cost each warp that holds one the whole arithmetic (16 sequences of 64 rows of 32000
+// fp32: 156 us, against 63 us so).  The drafted tokens of a row's own path are found through a chain of
+// drafted tokens at each listed token.
 //
 // Bound by HBM: each logit read and written once, a bit of mask a logit.  A vector whose mask lets
-// nothing through is not read; in place, only vectors that change are touched at all.
+// nothing through is not read; in place, only what changes is touched.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -23,6 +24,7 @@ namespace vocab {
 
 constexpr int kAdjustThreads = 256;
 constexpr int kMinSlice = 1024, kMaxSlice = 8192;  // tokens of a CTA
+constexpr int kAdjustRows = 4;                     // rows streamed before their listed tokens are computed
 
 struct AdjustArgs {
     const unsigned char *in;
@@ -39,6 +41,20 @@ struct AdjustArgs {
     uint32_t *status;
 };
 
+// Where the parts of a CTA's shared memory begin, in words; those that a call has no use for are empty.
+struct AdjustShared {
+    int count, bias, list, chain, before, words;
+    __host__ __device__ explicit AdjustShared(const AdjustArgs &a) {
+        const bool counts = a.repetition || a.frequency || a.presence, lists = counts || a.M, paths = counts && a.nodes && a.N > 1;
+        count = lists ? a.slice / 32 : 0;
+        bias = count + (counts ? a.slice : 0);
+        list = bias + (a.M ? a.slice : 0);
+        chain = list + (lists ? a.slice / 2 : 0);
+        before = chain + (paths ? a.slice / 2 : 0);
+        words = before + (paths ? (a.N + 1) / 2 : 0);
+    }
+};
+
 template <int EB>
 __device__ __forceinline__ float load_one(const unsigned char *p) {
     if (EB == 4) return *reinterpret_cast<const float *>(p);
@@ -49,18 +65,13 @@ __device__ __forceinline__ void store_one(unsigned char *p, float x) {
     if (EB == 4) *reinterpret_cast<float *>(p) = x;
     else *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(x);
 }
-// EPV bits from bit `at` of a bit array that has one word to spare behind them.
-template <int EPV>
-__device__ __forceinline__ uint32_t bits_at(const uint32_t *words, int at) {
-    return __funnelshift_r(words[at >> 5], words[(at >> 5) + 1], at & 31) & ((1u << EPV) - 1);
-}
-
 template <int EB, bool VEC, bool INPLACE>
 __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs a) {
     constexpr int EPV = VEC ? 16 / EB : 1;  // tokens of a vector
     constexpr uint32_t kAll = (1u << EPV) - 1;
     constexpr int kBatch = 4;               // vectors of a thread under way at once
     extern __shared__ uint32_t smem[];
+    __shared__ int listed;
     const int tid = threadIdx.x;
     const int s = blockIdx.x % a.slices;
     const int group = blockIdx.x / a.slices % a.groups;
@@ -77,16 +88,23 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
     const bool counts = r != 1.0f || f != 0.0f || p != 0.0f;
     const bool paths = counts && a.nodes && a.N > 1;
 
-    uint32_t *touched = smem;                                       // slice bits and one spare word
-    uint32_t *count = touched + a.slice / 32 + 1;                   // [slice], where a penalty is given
-    float *bias = reinterpret_cast<float *>(count + (a.repetition || a.frequency || a.presence ? a.slice : 0));  // [slice], where M > 0
-    for (int i = tid; i <= a.slice / 32; i += kAdjustThreads) touched[i] = 0;
-    if (counts)
-        for (int i = tid; i < len; i += kAdjustThreads) count[i] = 0;
-    if (a.M)
-        for (int i = tid; i < len; i += kAdjustThreads) bias[i] = 0.0f;
-    __syncthreads();
-
+    const AdjustShared at(a);
+    uint32_t *touched = smem, *count = smem + at.count;  // a bit a token; a word a token
+    float *bias = reinterpret_cast<float *>(smem + at.bias);
+    uint16_t *list = reinterpret_cast<uint16_t *>(smem + at.list);    // the tokens that are touched
+    uint16_t *chain = reinterpret_cast<uint16_t *>(smem + at.chain);  // a token's last drafted node
+    uint16_t *before = reinterpret_cast<uint16_t *>(smem + at.before);  // a node's predecessor in its token's chain (0: none)
+    if (counts || a.M) {
+        for (int i = tid; i < a.slice / 32; i += kAdjustThreads) touched[i] = 0;
+        if (counts)
+            for (int i = tid; i < len; i += kAdjustThreads) count[i] = 0;
+        if (paths)
+            for (int i = tid; i < (len + 1) / 2; i += kAdjustThreads) reinterpret_cast<uint32_t *>(chain)[i] = 0;
+        if (a.M)
+            for (int i = tid; i < len; i += kAdjustThreads) bias[i] = 0.0f;
+        if (tid == 0) listed = 0;
+        __syncthreads();
+    }
     const int32_t *nodes = a.nodes ? a.nodes + static_cast<size_t>(b) * a.N : nullptr;
     if (counts) {
         int total = a.total_len ? a.total_len[b] : a.L, prompt = a.prompt_len ? a.prompt_len[b] : 0;
@@ -111,11 +129,19 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
                 }
             }
         }
-        if (paths)
-            for (int m = 1 + tid; m < a.N; m += kAdjustThreads) {
-                const int t = nodes[m];
+        if (paths && tid < 32)  // (one warp, node by node, so that a chain is never entered twice at once)
+            for (int m0 = 1; m0 < a.N; m0 += 32) {
+                const int m = m0 + tid, t = m < a.N ? nodes[m] : -1;
                 odd |= t < -1 || t >= a.V;
-                if (t >= t0 && t < t0 + len) atomicOr(&touched[(t - t0) >> 5], 1u << ((t - t0) & 31));
+                const bool mine = t >= t0 && t < t0 + len;
+                for (uint32_t left = __ballot_sync(0xffffffffu, mine); left; left &= left - 1) {
+                    if (tid == __ffs(left) - 1) {
+                        before[m] = chain[t - t0];
+                        chain[t - t0] = static_cast<uint16_t>(m);
+                        atomicOr(&touched[(t - t0) >> 5], 1u << ((t - t0) & 31));
+                    }
+                    __syncwarp();
+                }
             }
         if (s == 0) {
             if (odd) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
@@ -138,115 +164,115 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
         bias[t - t0] = sum;
         atomicOr(&touched[(t - t0) >> 5], 1u << ((t - t0) & 31));
     }
-    __syncthreads();
-
-    auto adjusted = [&](float x, int u) {
-        if (a.M) x = __fadd_rn(x, bias[u]);
-        if (counts) {
-            const uint32_t c = count[u], made = c & 0x7fffffffu;
-            if (c) x = x > 0.0f ? __fdiv_rn(x, r) : __fmul_rn(x, r);
-            if (made) x = __fsub_rn(__fsub_rn(x, __fmul_rn(f, static_cast<float>(made))), p);
+    int n_listed = 0;
+    if (counts || a.M) {
+        __syncthreads();
+        for (int i = tid; i < (len + 31) / 32; i += kAdjustThreads) {
+            uint32_t w = touched[i];
+            if (!w) continue;
+            for (int to = atomicAdd(&listed, __popc(w)); w; w &= w - 1) list[to++] = static_cast<uint16_t>(32 * i + __ffs(w) - 1);
         }
-        return x;
-    };
-    // The path's tokens of row n into the table (by 1) or out of it (by -1).
-    auto path = [&](int n, uint32_t by) {
-        const int words = (a.N + 31) / 32;
-        for (int m = 1 + tid; m < a.N; m += kAdjustThreads) {
-            const bool on = a.mask ? (__ldg(a.mask + static_cast<size_t>(n) * words + (m >> 5)) >> (m & 31)) & 1 : m <= n;
-            const int t = nodes[m];
-            if (on && t >= t0 && t < t0 + len) atomicAdd(&count[t - t0], by);
-        }
-    };
+        __syncthreads();
+        n_listed = listed;
+    }
 
-    const int words = (a.V + 31) / 32;
+    const int words = (a.V + 31) / 32, mask_words = (a.N + 31) / 32;
     const int n_end = min(a.N, (group + 1) * a.rows);
-    for (int n = group * a.rows; n < n_end; ++n) {
-        const size_t row = static_cast<size_t>(b) * a.N + n;
-        if (paths) {
-            if (n > group * a.rows) {
-                __syncthreads();
-                path(n - 1, ~0u);
-            }
-            path(n, 1u);
-            __syncthreads();
-        }
-        const size_t first = (row * a.V + t0) * EB;  // the slice's first byte
-        const int off = VEC ? static_cast<int>(reinterpret_cast<uintptr_t>(a.in + first) % 16) / EB : 0;
-        const int vectors = (len + off + EPV - 1) / EPV;
-        const uint32_t *allowed = a.allowed ? a.allowed + row * words : nullptr;
-        for (int j0 = tid; j0 < vectors; j0 += kBatch * kAdjustThreads) {
-            uint32_t ok[kBatch], hit[kBatch];
-            uint4 v[kBatch];
+    for (int n0 = group * a.rows; n0 < n_end; n0 += kAdjustRows) {
+        const int n1 = min(n_end, n0 + kAdjustRows);
+        // The stream.  In place and without a mask nothing is copied.
+        for (int n = n0; (!INPLACE || a.allowed) && n < n1; ++n) {
+            const size_t row = static_cast<size_t>(b) * a.N + n;
+            const size_t first = (row * a.V + t0) * EB;  // the slice's first byte
+            const int off = VEC ? static_cast<int>(reinterpret_cast<uintptr_t>(a.in + first) % 16) / EB : 0;
+            const int vectors = (len + off + EPV - 1) / EPV;
+            const uint32_t *allowed = a.allowed ? a.allowed + row * words : nullptr;
+            for (int j0 = tid; j0 < vectors; j0 += kBatch * kAdjustThreads) {
+                uint32_t ok[kBatch];
+                uint4 v[kBatch];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int u = (j0 + k * kAdjustThreads) * EPV - off;  // the vector's first token in the slice
-                ok[k] = kAll;
-                hit[k] = 0;
-                if (u < 0 || u + EPV > len) continue;
-                hit[k] = bits_at<EPV>(touched, u);
-                if (allowed) {
+                for (int k = 0; k < kBatch; ++k) {
+                    const int u = (j0 + k * kAdjustThreads) * EPV - off;  // the vector's first token in the slice
+                    ok[k] = kAll;
+                    if (!allowed || u < 0 || u + EPV > len) continue;
                     const int t = t0 + u, w = t >> 5;
                     const uint32_t low = __ldg(allowed + w), high = (t & 31) + EPV > 32 ? __ldg(allowed + w + 1) : 0;
                     ok[k] = __funnelshift_r(low, high, t & 31) & kAll;
                 }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int u = (j0 + k * kAdjustThreads) * EPV - off;
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (u < 0 || u + EPV > len || ok[k] == 0 || (INPLACE && ok[k] == kAll)) continue;
+                    const unsigned char *from = a.in + first + static_cast<ptrdiff_t>(u) * EB;
+                    if (VEC) v[k] = *reinterpret_cast<const uint4 *>(from);
+                    else v[k].x = EB == 4 ? *reinterpret_cast<const uint32_t *>(from) : *reinterpret_cast<const uint16_t *>(from);
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int u = (j0 + k * kAdjustThreads) * EPV - off;
+                    if (u >= len) continue;
+                    unsigned char *to = a.out + first + static_cast<ptrdiff_t>(u) * EB;
+                    if (u < 0 || u + EPV > len) {  // a vector that the slice holds in part
+                        for (int e = max(0, -u); e < min(EPV, len - u); ++e) {
+                            const int t = t0 + u + e;
+                            const bool let = !allowed || (__ldg(allowed + (t >> 5)) >> (t & 31)) & 1;
+                            if (INPLACE && let) continue;
+                            store_one<EB>(to + e * EB, let ? load_one<EB>(a.in + first + static_cast<ptrdiff_t>(u + e) * EB) : -INFINITY);
+                        }
+                        continue;
+                    }
+                    if (INPLACE && ok[k] == kAll) continue;
+                    if (ok[k] != kAll) {
+                        uint32_t *x = reinterpret_cast<uint32_t *>(&v[k]);
+#pragma unroll
+                        for (int e = 0; e < EPV; ++e) {
+                            if ((ok[k] >> e) & 1) continue;
+                            if (EB == 4) x[e] = 0xff800000u;
+                            else x[e >> 1] = (e & 1) ? (x[e >> 1] & 0xffffu) | 0xff800000u : (x[e >> 1] & 0xffff0000u) | 0xff80u;
+                        }
+                    }
+                    if (VEC) *reinterpret_cast<uint4 *>(to) = v[k];
+                    else if (EB == 4) *reinterpret_cast<uint32_t *>(to) = v[k].x;
+                    else *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(v[k].x);
+                }
+            }
+        }
+        if (n_listed == 0) continue;
+        __syncthreads();  // what was streamed lies under what the listed tokens get
+        const int items = n_listed * (n1 - n0);
+        for (int i0 = tid; i0 < items; i0 += kBatch * kAdjustThreads) {
+            uint32_t let[kBatch];
+            float x[kBatch];
+            int u[kBatch], n[kBatch];
+            size_t at[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int i = i0 + k * kAdjustThreads;
+                let[k] = 0;
+                if (i >= items) continue;
+                n[k] = n0 + i / n_listed;
+                u[k] = list[i % n_listed];
+                const int t = t0 + u[k];
+                const size_t row = static_cast<size_t>(b) * a.N + n[k];
+                at[k] = (row * a.V + t) * EB;
+                let[k] = a.allowed ? __ldg(a.allowed + row * words + (t >> 5)) >> (t & 31) & 1 : 1;
+                x[k] = load_one<EB>(a.in + at[k]);
             }
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const int u = (j0 + k * kAdjustThreads) * EPV - off;
-                const bool whole = u >= 0 && u + EPV <= len;
-                const bool read = whole && ok[k] != 0 && !(INPLACE && hit[k] == 0 && ok[k] == kAll);
-                v[k] = make_uint4(0, 0, 0, 0);
-                if (!read) continue;
-                const unsigned char *at = a.in + first + static_cast<ptrdiff_t>(u) * EB;
-                if (VEC) v[k] = __ldcs(reinterpret_cast<const uint4 *>(at));
-                else v[k].x = EB == 4 ? *reinterpret_cast<const uint32_t *>(at) : *reinterpret_cast<const uint16_t *>(at);
-            }
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const int u = (j0 + k * kAdjustThreads) * EPV - off;
-                if (u >= len) continue;
-                unsigned char *to = a.out + first + static_cast<ptrdiff_t>(u) * EB;
-                if (u < 0 || u + EPV > len) {  // a vector that the slice holds in part
-                    for (int e = max(0, -u); e < min(EPV, len - u); ++e) {
-                        const int t = t0 + u + e;
-                        const bool let = !allowed || (__ldg(allowed + (t >> 5)) >> (t & 31)) & 1;
-                        const bool touch = (touched[(u + e) >> 5] >> ((u + e) & 31)) & 1;
-                        if (INPLACE && let && !touch) continue;
-                        float x = -INFINITY;
-                        if (let) {
-                            x = load_one<EB>(a.in + first + static_cast<ptrdiff_t>(u + e) * EB);
-                            if (touch) x = adjusted(x, u + e);
-                        }
-                        store_one<EB>(to + e * EB, x);
-                    }
-                    continue;
+                if (!let[k]) continue;
+                if (a.M) x[k] = __fadd_rn(x[k], bias[u[k]]);
+                if (counts) {
+                    const uint32_t c = count[u[k]];
+                    uint32_t made = c & 0x7fffffffu;
+                    if (paths)
+                        for (int m = chain[u[k]]; m; m = before[m])
+                            made += a.mask ? (__ldg(a.mask + static_cast<size_t>(n[k]) * mask_words + (m >> 5)) >> (m & 31)) & 1 : m <= n[k];
+                    if (made || c) x[k] = x[k] > 0.0f ? __fdiv_rn(x[k], r) : __fmul_rn(x[k], r);
+                    if (made) x[k] = __fsub_rn(__fsub_rn(x[k], __fmul_rn(f, static_cast<float>(made))), p);
                 }
-                if (INPLACE && hit[k] == 0 && ok[k] == kAll) continue;
-                union {
-                    uint4 q;
-                    uint32_t w[4];
-                } x;
-                x.q = v[k];
-                if (hit[k] != 0 || ok[k] != kAll) {
-#pragma unroll
-                    for (int e = 0; e < EPV; ++e) {
-                        const bool let = (ok[k] >> e) & 1, touch = (hit[k] >> e) & 1;
-                        if (EB == 4) {
-                            if (touch && let) x.w[e] = __float_as_uint(adjusted(__uint_as_float(x.w[e]), u + e));
-                            if (!let) x.w[e] = 0xff800000u;
-                        } else {
-                            const int sh = (e & 1) * 16;
-                            uint32_t h = (x.w[e >> 1] >> sh) & 0xffffu;
-                            if (touch && let) h = __bfloat16_as_ushort(__float2bfloat16_rn(adjusted(__uint_as_float(h << 16), u + e)));
-                            if (!let) h = 0xff80u;
-                            x.w[e >> 1] = (x.w[e >> 1] & ~(0xffffu << sh)) | h << sh;
-                        }
-                    }
-                }
-                if (VEC) *reinterpret_cast<uint4 *>(to) = x.q;
-                else if (EB == 4) *reinterpret_cast<uint32_t *>(to) = x.q.x;
-                else *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(x.q.x);
+                store_one<EB>(a.out + at[k], x[k]);
             }
         }
     }
