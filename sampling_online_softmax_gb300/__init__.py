@@ -90,6 +90,8 @@ _lib = None
 def load_library():
     """Load libspecverify.so; raises ImportError if it was not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -774,6 +776,10 @@ def _on_gpu(t, name):
 
 def _token_rows(t, name, shape, dtype, dev):
     """Checks [B, N, heads, dim], whose heads lie together while its tokens may be strided; returns (address, batch and token strides)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous():  # (a CPU tensor's: -1)
+        p = t.data_ptr()
+        if p % 16 == 0:
+            return p, shape[1] * shape[2] * shape[3], shape[2] * shape[3]
     _on_gpu(t, name)
     if t.device != dev:
         raise ValueError("%s is on %s, not on %s" % (name, t.device, dev))
@@ -801,9 +807,9 @@ def _new_tokens(t, name):
     return t.shape, t.dtype, t.device, t.device.index
 
 
-def _status_at(status, dev, index, stream):
-    """The status word alone, a new one where it is None."""
-    return _results({}, {}, status, dev, index, stream)[::2]
+def _strides(*rows):
+    """Batch and token strides of what _token_rows returned, as the C ABI takes them."""
+    return (ctypes.c_longlong * (2 * len(rows)))(*(x for r in rows for x in r[1:]))
 
 
 def spec_cache_append(k, v, k_cache, v_cache, page_table, start, *, count=None, select=None, k_scale=None, v_scale=None, status=None,
@@ -823,13 +829,10 @@ def spec_cache_append(k, v, k_cache, v_cache, page_table, start, *, count=None, 
     S = N if select is None else select.shape[1]
     i32 = torch.int32
     args = (_may(select, "select", i32, (B, S), dev, i), S, _need(start, "start", i32, (B,), dev, i), _may(count, "count", i32, (B,), dev, i))
-    out, st = _status_at(status, dev, i, stream)
-    strides = (ctypes.c_longlong * 4)(at[1], at[2], sk[1], sk[2])
-    _launch(lib.spec_cache_append, (at[0], sk[0], _CODES[dtype], B, N, strides, *args, ctypes.byref(cache), st),
+    out, _, st = _results({}, {}, status, dev, i, stream)
+    _launch(lib.spec_cache_append, (at[0], sk[0], _CODES[dtype], B, N, _strides(at, sk), *args, ctypes.byref(cache), st),
             (k, v, k_cache, v_cache, page_table, start, count, select, k_scale, v_scale, *out.values()), dev, stream)
-    for t in (k_cache, v_cache, k_scale, v_scale):
-        if t is not None:
-            _overwritten(t)
+    _overwritten((k_cache, v_cache) if k_scale is None else (k_cache, v_cache, k_scale, v_scale))
     return out
 
 
@@ -866,8 +869,7 @@ def spec_cache_read(k_cache, v_cache, page_table, start, n, *, count=None, k_sca
     _launch(lib.spec_cache_read, (ctypes.byref(cache), B, n, *args, *at, _CODES[dtype], st),
             (k_cache, v_cache, page_table, start, count, k_scale, v_scale, *out.values()), dev, stream)
     if given:
-        _overwritten(out["k"])
-        _overwritten(out["v"])
+        _overwritten((out["k"], out["v"]))
     return out
 
 
@@ -910,13 +912,11 @@ def spec_tree_attention(q, k, v, k_cache, v_cache, page_table, context_lens, *, 
     else:
         _cuda(workspace, "workspace", None, dev)
     room = workspace.numel() * workspace.element_size()
-    strides = (ctypes.c_longlong * 6)(*(x for a in at for x in a[1:]))
-    _launch(lib.spec_tree_attention, (at[0][0], at[1][0], at[2][0], _CODES[dtype], B, N, heads, strides, ctypes.byref(cache), *args,
+    _launch(lib.spec_tree_attention, (at[0][0], at[1][0], at[2][0], _CODES[dtype], B, N, heads, _strides(*at), ctypes.byref(cache), *args,
                                       to[0], to[1] if lse else None, st, workspace.data_ptr(), room),
             (q, k, v, k_cache, v_cache, page_table, context_lens, mask, k_scale, v_scale, workspace, *out.values()), dev, stream)
     if given:
-        for x in shapes:
-            _overwritten(out[x])
+        _overwritten([out[x] for x in shapes])
     return out
 
 

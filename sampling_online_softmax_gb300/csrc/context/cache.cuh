@@ -6,10 +6,12 @@
 // costs a floating format no precision and makes x / 2^e and q 2^e exact, so one rounding, to e4m3,
 // is all there is.
 //
-// A row is held by D / 8 lanes, 16 bytes of it each, so a warp's loads and stores are whole 128-byte
-// lines; the row's maximum takes log2(D / 8) shuffles.  Both kernels move bytes and are bound by HBM
-// where there are many rows, by launch and two dependent trips (table entry, then row) where there
-// are few.
+// A row is held by lanes with 16 bytes of it each (16 of its 8-bit values, where it is read back), so a
+// warp's loads are whole lines; the row's maximum takes log2 of the lanes' number shuffles.  A CTA's
+// threads take the rows of one token, or of a few, and two tokens at a time are under way: where a token
+// goes is worked out once for its keys and values.  Bound by HBM where there are many tokens (39950 of 8 heads
+// of 128: append and read together 72 us at the copy rate), by launch and three dependent trips (start,
+// page, row) where there are few.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -58,96 +60,148 @@ __device__ __forceinline__ size_t cache_row(const CacheView &c, long long place,
     return (static_cast<size_t>(page * c.kv_heads + g) << c.page_bits) + static_cast<size_t>(slot);
 }
 
-template <typename T, int D, bool Q8>
+// A thread's share of the rows of a token, `items` lanes of them in all: the same of its keys and its values.
+struct CacheShare {
+    int items, tokens, sub, rounds;  // tokens that the CTA takes at once, this thread's of them; rounds over a token's lanes
+    __device__ CacheShare(int kv_heads, int lanes) {
+        items = kv_heads * lanes;
+        tokens = max(1, kCacheThreads / items);
+        sub = items <= kCacheThreads ? threadIdx.x / items : 0;
+        rounds = (items + kCacheThreads - 1) / kCacheThreads;
+    }
+    __device__ int item(int round) const { return items <= kCacheThreads ? threadIdx.x % items : threadIdx.x + round * kCacheThreads; }
+};
+
+// kCacheTokens: under way at once; 2, or 1 where the tokens are few and a CTA each is there for them.
+template <typename T, int D, bool Q8, int kCacheTokens>
 __global__ void __launch_bounds__(kCacheThreads) cache_append_kernel(const CacheRowsArgs a) {
     constexpr int kLanes = D / 8;
-    const int part = threadIdx.x % kLanes;
-    const long long rows = 2ll * a.B * a.S * a.cache.kv_heads;  // k and v next to each other: (b, i, k/v, head)
-    const long long step = static_cast<long long>(gridDim.x) * (kCacheThreads / kLanes);
-    const long long first = static_cast<long long>(blockIdx.x) * (kCacheThreads / kLanes) + threadIdx.x / kLanes;
-    // (every lane of a warp goes round together: the shuffles below take all of them)
-    for (long long at = first; at - first % (32 / kLanes) < rows; at += step) {
-        const int g = static_cast<int>(at % a.cache.kv_heads);
-        const int which = static_cast<int>(at / a.cache.kv_heads & 1);
-        const long long token = at / (2 * a.cache.kv_heads);
-        const int b = static_cast<int>(token / a.S), i = static_cast<int>(token % a.S);
-        long long place = -1;
-        int from = i;
-        if (at < rows) {
-            if (a.select) from = __ldg(a.select + token);
+    const CacheShare my(a.cache.kv_heads, kLanes);
+    const int all = a.B * a.S, step = my.tokens * kCacheTokens;
+    for (int t0 = blockIdx.x * step; t0 < all; t0 += gridDim.x * step) {
+        long long place[kCacheTokens];
+        int batch[kCacheTokens], node[kCacheTokens];
+#pragma unroll
+        for (int k = 0; k < kCacheTokens; ++k) {
+            const int token = t0 + k * my.tokens + my.sub;
+            place[k] = -1;
+            batch[k] = node[k] = 0;
+            if (my.sub >= my.tokens || token >= all) continue;
+            const int b = token / a.S, i = token - b * a.S, from = a.select ? __ldg(a.select + token) : i;
             if (from >= a.N) atomicOr(a.status, SPEC_DEV_BAD_LENGTH);
-            else if (from >= 0) place = cache_place(a, b, i);
+            else if (from >= 0) place[k] = cache_place(a, b, i);
+            batch[k] = b;
+            node[k] = from;
         }
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (place >= 0) {
-            const T *row = reinterpret_cast<const T *>(a.src[which]) + b * a.batch_stride[which] + from * a.token_stride[which] + static_cast<size_t>(g) * D;
-            x = __ldg(reinterpret_cast<const uint4 *>(row) + part);
-        }
-        const size_t row = place >= 0 ? cache_row(a.cache, place, g) : 0;
-        if (!Q8) {
-            if (place >= 0) *reinterpret_cast<uint4 *>(a.cache.data[which] + (row * D + part * 8) * 2) = x;
-            continue;
-        }
-        float v[8], most = 0.0f;
-        unpack8<T>(x, v);
-        bool odd = false;
+        for (int round = 0; round < my.rounds; ++round) {  // (the whole CTA goes round together: the shuffles take whole warps)
+            const int item = my.item(round), g = item / kLanes, part = item % kLanes;
+            const size_t within = static_cast<size_t>(g) * D + part * 8;
+            uint4 loaded[2][kCacheTokens];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            most = fmaxf(most, fabsf(v[k]));
-            odd |= !isfinite(v[k]);
-        }
+            for (int w = 0; w < 2; ++w)
 #pragma unroll
-        for (int m = 1; m < kLanes; m *= 2) {
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
-            odd |= __shfl_xor_sync(0xffffffffu, static_cast<int>(odd), m) != 0;
-        }
-        // max = c 2^(E - 127), 1 <= c < 2 (a subnormal maximum has E = 0 and is far below the least e)
-        const uint32_t bits = __float_as_uint(most);
-        const int e = max(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), Elt<T>::kLeastExp);
-        const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const float top = e >= Elt<T>::kTopExp ? 240.0f : 448.0f;  // 256 2^e would not come back
-        uint32_t q[2] = {0, 0};
+                for (int k = 0; k < kCacheTokens; ++k) {
+                    loaded[w][k] = make_uint4(0, 0, 0, 0);
+                    if (place[k] >= 0 && item < my.items)
+                        loaded[w][k] = __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(a.src[w]) + batch[k] * a.batch_stride[w] + node[k] * a.token_stride[w] + within));
+                }
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) {
-            const float2 pair = make_float2(fminf(fmaxf(v[k] * inv, -top), top), fminf(fmaxf(v[k + 1] * inv, -top), top));
-            q[k / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(pair, __NV_SATFINITE, __NV_E4M3)) << (k % 4 * 8);
-        }
-        if (place >= 0) {
-            *reinterpret_cast<uint2 *>(a.cache.data[which] + row * D + part * 8) = make_uint2(q[0], q[1]);
-            if (part == 0) a.cache.scale[which][row] = odd ? 255 : static_cast<uint8_t>(e + 127);
+            for (int k = 0; k < kCacheTokens; ++k) {
+                const bool live = place[k] >= 0 && item < my.items;
+                const size_t to = live ? cache_row(a.cache, place[k], g) : 0;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint4 x = loaded[w][k];
+                    if (!Q8) {
+                        if (live) *reinterpret_cast<uint4 *>(a.cache.data[w] + (to * D + part * 8) * 2) = x;
+                        continue;
+                    }
+                    // The largest magnitude, as whole numbers: without their signs the elements are ordered as their
+                    // bits are, infinities above the finite ones and NaN above those.
+                    const uint32_t bits4[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t most = __vmaxu2(__vmaxu2(bits4[0] & 0x7fff7fffu, bits4[1] & 0x7fff7fffu), __vmaxu2(bits4[2] & 0x7fff7fffu, bits4[3] & 0x7fff7fffu));
+#pragma unroll
+                    for (int m = 1; m < kLanes; m *= 2) most = __vmaxu2(most, __shfl_xor_sync(0xffffffffu, most, m));
+                    const uint32_t largest = max(most & 0xffffu, most >> 16);
+                    // max = c 2^(E - 127), 1 <= c < 2 (a subnormal maximum has E = 0 and is far below the least e)
+                    const uint32_t bits = __float_as_uint(Elt<T>::to_float2(largest).x);
+                    const int e = min(max(static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), Elt<T>::kLeastExp), Elt<T>::kTopExp);
+                    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+                    float v[8];
+                    unpack8<T>(x, v);
+#pragma unroll
+                    for (int h = 0; h < 8; ++h) v[h] *= inv;
+                    if (e >= Elt<T>::kTopExp)  // 256 2^e would not come back
+#pragma unroll
+                        for (int h = 0; h < 8; ++h) v[h] = fminf(fmaxf(v[h], -240.0f), 240.0f);
+                    uint32_t q[2] = {0, 0};
+#pragma unroll
+                    for (int h = 0; h < 8; h += 2)
+                        q[h / 4] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(v[h], v[h + 1]), __NV_SATFINITE, __NV_E4M3)) << (h % 4 * 8);
+                    if (live) {
+                        *reinterpret_cast<uint2 *>(a.cache.data[w] + to * D + part * 8) = make_uint2(q[0], q[1]);
+                        if (part == 0) a.cache.scale[w][to] = largest >= Elt<T>::kInfinity ? 255 : static_cast<uint8_t>(e + 127);
+                    }
+                }
+            }
         }
     }
 }
 
-template <typename T, int D, bool Q8>
+template <typename T, int D, bool Q8, int kCacheTokens>
 __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheRowsArgs a) {
-    constexpr int kLanes = D / 8;
-    const int part = threadIdx.x % kLanes;
-    const long long rows = 2ll * a.B * a.S * a.cache.kv_heads;
-    const long long step = static_cast<long long>(gridDim.x) * (kCacheThreads / kLanes);
-    for (long long at = static_cast<long long>(blockIdx.x) * (kCacheThreads / kLanes) + threadIdx.x / kLanes; at < rows; at += step) {
-        const int g = static_cast<int>(at % a.cache.kv_heads);
-        const int which = static_cast<int>(at / a.cache.kv_heads & 1);
-        const long long token = at / (2 * a.cache.kv_heads);
-        const long long place = cache_place(a, static_cast<int>(token / a.S), static_cast<int>(token % a.S));
-        if (place < 0) continue;
-        const size_t row = cache_row(a.cache, place, g);
-        uint4 x;
-        if (!Q8) {
-            x = *reinterpret_cast<const uint4 *>(a.cache.data[which] + (row * D + part * 8) * 2);
-        } else {
-            const uint2 q = *reinterpret_cast<const uint2 *>(a.cache.data[which] + row * D + part * 8);
-            const float s = scale_of(a.cache.scale[which][row]);
-            float v[8];
+    constexpr int kEach = Q8 ? 16 : 8, kLanes = D / kEach;  // values of a lane
+    const CacheShare my(a.cache.kv_heads, kLanes);
+    const int all = a.B * a.S, step = my.tokens * kCacheTokens;
+    for (int t0 = blockIdx.x * step; t0 < all; t0 += gridDim.x * step) {
+        long long place[kCacheTokens];
 #pragma unroll
-            for (int k = 0; k < 8; k += 2) {
-                const float2 f = e4m3x2((k < 4 ? q.x : q.y) >> (k % 4 * 8));
-                v[k] = f.x * s;
-                v[k + 1] = f.y * s;
-            }
-            x = pack8<T>(v);
+        for (int k = 0; k < kCacheTokens; ++k) {
+            const int token = t0 + k * my.tokens + my.sub;
+            place[k] = my.sub < my.tokens && token < all ? cache_place(a, token / a.S, token % a.S) : -1;
         }
-        reinterpret_cast<uint4 *>(a.dst[which])[(static_cast<size_t>(token) * a.cache.kv_heads + g) * kLanes + part] = x;
+        for (int round = 0; round < my.rounds; ++round) {
+            const int item = my.item(round), g = item / kLanes, part = item % kLanes;
+            if (item >= my.items) continue;
+            uint4 x[2][kCacheTokens];
+            uint32_t scale[2][kCacheTokens];
+#pragma unroll
+            for (int k = 0; k < kCacheTokens; ++k) {
+                if (place[k] < 0) continue;
+                const size_t at = cache_row(a.cache, place[k], g);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    x[w][k] = *reinterpret_cast<const uint4 *>(a.cache.data[w] + (at * D + part * kEach) * (Q8 ? 1 : 2));
+                    if (Q8) scale[w][k] = a.cache.scale[w][at];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kCacheTokens; ++k) {
+                if (place[k] < 0) continue;
+                const size_t token = static_cast<size_t>(t0) + k * my.tokens + my.sub, at = (token * a.cache.kv_heads + g) * (D / 8) + part * (kEach / 8);
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    uint4 *to = reinterpret_cast<uint4 *>(a.dst[w]) + at;
+                    if (!Q8) {
+                        *to = x[w][k];
+                        continue;
+                    }
+                    const float s = scale_of(scale[w][k]);
+                    const uint32_t q[4] = {x[w][k].x, x[w][k].y, x[w][k].z, x[w][k].w};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e += 2) {
+                            const float2 f = e4m3x2(q[2 * h + e / 4] >> (e % 4 * 8));
+                            v[e] = f.x * s;
+                            v[e + 1] = f.y * s;
+                        }
+                        to[h] = pack8<T>(v);
+                    }
+                }
+            }
+        }
     }
 }
 

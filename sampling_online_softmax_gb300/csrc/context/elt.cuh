@@ -17,6 +17,7 @@ template <>
 struct Elt<__nv_bfloat16> {
     static constexpr int kLeastExp = -110;  // of a row's power of two: 2^e and q 2^e stay normal
     static constexpr int kTopExp = 120;     // where a row's largest q 2^e could be 2^128, past bf16's range
+    static constexpr uint32_t kInfinity = 0x7f80;
     static __device__ __forceinline__ float2 to_float2(uint32_t x) {
         return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
     }
@@ -30,6 +31,7 @@ template <>
 struct Elt<__half> {
     static constexpr int kLeastExp = -24;  // fp16 holds multiples of 2^-24 alone
     static constexpr int kTopExp = 8;      // where a row's largest q 2^e could be 2^16, past fp16's range
+    static constexpr uint32_t kInfinity = 0x7c00;
     static __device__ __forceinline__ float2 to_float2(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2 *>(&x)); }
     static __device__ __forceinline__ uint32_t from_float2(float a, float b) {
         const __half2 v = __floats2half2_rn(a, b);
