@@ -43,15 +43,19 @@ struct AdjustArgs {
 
 // Where the parts of a CTA's shared memory begin, in words; those that a call has no use for are empty.
 struct AdjustShared {
-    int count, bias, list, chain, before, words;
+    int count, bias, mine, list, chain, before, sums, words;
+    bool narrow;  // counts of 16 bits
     __host__ __device__ explicit AdjustShared(const AdjustArgs &a) {
         const bool counts = a.repetition || a.frequency || a.presence, lists = counts || a.M, paths = counts && a.nodes && a.N > 1;
         count = lists ? a.slice / 32 : 0;
-        bias = count + (counts ? a.slice : 0);
-        list = bias + (a.M ? a.slice : 0);
-        chain = list + (lists ? a.slice / 2 : 0);
-        before = chain + (paths ? a.slice / 2 : 0);
-        words = before + (paths ? (a.N + 1) / 2 : 0);
+        narrow = a.L + a.N < 1 << 15;
+        bias = count + (counts ? a.slice / (narrow ? 2 : 1) : 0);
+        chain = bias + (a.M ? a.slice / 2 : 0);
+        list = chain + (paths ? a.slice / 2 : 0);  // (up to here all is zeroed)
+        mine = list + (lists ? a.slice / 2 : 0);
+        before = mine + (a.M + 1) / 2;
+        sums = before + (paths ? (a.N + 1) / 2 : 0);
+        words = sums + a.M;
     }
 };
 
@@ -65,13 +69,80 @@ __device__ __forceinline__ void store_one(unsigned char *p, float x) {
     if (EB == 4) *reinterpret_cast<float *>(p) = x;
     else *reinterpret_cast<__nv_bfloat16 *>(p) = __float2bfloat16_rn(x);
 }
+// Vectors of a slice of a row: tid + j0 and every kAdjustThreads-th from there on.
+template <int EB, bool VEC, bool INPLACE, int COUNT>
+struct Vectors {
+    static constexpr int EPV = VEC ? 16 / EB : 1;  // tokens of a vector
+    static constexpr uint32_t kAll = (1u << EPV) - 1;
+    uint32_t ok[COUNT];  // a bit a token: allowed
+    uint4 v[COUNT];
+    size_t first;        // the slice's first byte
+    int u0;              // the first vector's first token in the slice
+    const uint32_t *allowed;
+
+    __device__ __forceinline__ int token(int k) const { return u0 + k * kAdjustThreads * EPV; }
+    __device__ __forceinline__ void masks(const AdjustArgs &a, size_t row, int t0, int len, int j0) {
+        first = (row * a.V + t0) * EB;
+        u0 = j0 * EPV - (VEC ? static_cast<int>(reinterpret_cast<uintptr_t>(a.in + first) % 16) / EB : 0);
+        allowed = a.allowed ? a.allowed + row * ((a.V + 31) / 32) : nullptr;
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k) {
+            const int u = token(k), t = t0 + u, w = t >> 5;
+            ok[k] = kAll;
+            if (!allowed || u < 0 || u + EPV > len) continue;
+            const uint32_t low = __ldg(allowed + w), high = (t & 31) + EPV > 32 ? __ldg(allowed + w + 1) : 0;
+            ok[k] = __funnelshift_r(low, high, t & 31) & kAll;
+        }
+    }
+    __device__ __forceinline__ void load(const AdjustArgs &a, int len) {
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k) {
+            const int u = token(k);
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (u < 0 || u + EPV > len || ok[k] == 0 || (INPLACE && ok[k] == kAll)) continue;
+            const unsigned char *from = a.in + first + static_cast<ptrdiff_t>(u) * EB;
+            if (VEC) v[k] = *reinterpret_cast<const uint4 *>(from);
+            else v[k].x = EB == 4 ? *reinterpret_cast<const uint32_t *>(from) : *reinterpret_cast<const uint16_t *>(from);
+        }
+    }
+    __device__ __forceinline__ void store(const AdjustArgs &a, int t0, int len) {
+#pragma unroll
+        for (int k = 0; k < COUNT; ++k) {
+            const int u = token(k);
+            if (u >= len) continue;
+            unsigned char *to = a.out + first + static_cast<ptrdiff_t>(u) * EB;
+            if (u < 0 || u + EPV > len) {  // a vector that the slice holds in part
+                for (int e = max(0, -u); e < min(EPV, len - u); ++e) {
+                    const int t = t0 + u + e;
+                    const bool let = !allowed || (__ldg(allowed + (t >> 5)) >> (t & 31)) & 1;
+                    if (INPLACE && let) continue;
+                    store_one<EB>(to + e * EB, let ? load_one<EB>(a.in + first + static_cast<ptrdiff_t>(u + e) * EB) : -INFINITY);
+                }
+                continue;
+            }
+            if (INPLACE && ok[k] == kAll) continue;
+            if (ok[k] != kAll) {
+                uint32_t *x = reinterpret_cast<uint32_t *>(&v[k]);
+#pragma unroll
+                for (int e = 0; e < EPV; ++e) {
+                    if ((ok[k] >> e) & 1) continue;
+                    if (EB == 4) x[e] = 0xff800000u;
+                    else x[e >> 1] = (e & 1) ? (x[e >> 1] & 0xffffu) | 0xff800000u : (x[e >> 1] & 0xffff0000u) | 0xff80u;
+                }
+            }
+            if (VEC) *reinterpret_cast<uint4 *>(to) = v[k];
+            else if (EB == 4) *reinterpret_cast<uint32_t *>(to) = v[k].x;
+            else *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(v[k].x);
+        }
+    }
+};
+
 template <int EB, bool VEC, bool INPLACE>
-__global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs a) {
+__global__ void __launch_bounds__(kAdjustThreads, 4) adjust_kernel(const AdjustArgs a) {
     constexpr int EPV = VEC ? 16 / EB : 1;  // tokens of a vector
-    constexpr uint32_t kAll = (1u << EPV) - 1;
-    constexpr int kBatch = 4;               // vectors of a thread under way at once
-    extern __shared__ uint32_t smem[];
-    __shared__ int listed;
+    constexpr int kBatch = 4, kFix = 2;     // vectors of a row, and listed tokens, of a thread under way at once
+    extern __shared__ __align__(16) uint32_t smem[];
+    __shared__ int listed, biased;
     const int tid = threadIdx.x;
     const int s = blockIdx.x % a.slices;
     const int group = blockIdx.x / a.slices % a.groups;
@@ -89,19 +160,17 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
     const bool paths = counts && a.nodes && a.N > 1;
 
     const AdjustShared at(a);
-    uint32_t *touched = smem, *count = smem + at.count;  // a bit a token; a word a token
-    float *bias = reinterpret_cast<float *>(smem + at.bias);
+    uint32_t *touched = smem, *count = smem + at.count;  // a bit a token; a count a token, of 16 or of 32 bits
+    uint16_t *bias = reinterpret_cast<uint16_t *>(smem + at.bias);    // 1 + where a token's bias is among `sums`
+    uint16_t *mine = reinterpret_cast<uint16_t *>(smem + at.mine);    // slots of biases of the slice's tokens
+    float *sums = reinterpret_cast<float *>(smem + at.sums);
+    const int half = at.narrow ? 1 : 0;
+    const uint32_t prompt_bit = at.narrow ? 0x8000u : 0x80000000u;
     uint16_t *list = reinterpret_cast<uint16_t *>(smem + at.list);    // the tokens that are touched
     uint16_t *chain = reinterpret_cast<uint16_t *>(smem + at.chain);  // a token's last drafted node
     uint16_t *before = reinterpret_cast<uint16_t *>(smem + at.before);  // a node's predecessor in its token's chain (0: none)
     if (counts || a.M) {
-        for (int i = tid; i < a.slice / 32; i += kAdjustThreads) touched[i] = 0;
-        if (counts)
-            for (int i = tid; i < len; i += kAdjustThreads) count[i] = 0;
-        if (paths)
-            for (int i = tid; i < (len + 1) / 2; i += kAdjustThreads) reinterpret_cast<uint32_t *>(chain)[i] = 0;
-        if (a.M)
-            for (int i = tid; i < len; i += kAdjustThreads) bias[i] = 0.0f;
+        for (int i = tid; i < at.list / 4; i += kAdjustThreads) reinterpret_cast<uint4 *>(smem)[i] = make_uint4(0, 0, 0, 0);
         if (tid == 0) listed = 0;
         __syncthreads();
     }
@@ -123,8 +192,9 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
                 const uint32_t u = static_cast<uint32_t>(t[k]) - t0;  // (a token below t0 wraps past the slice's end)
                 odd |= t[k] < -1 || t[k] >= a.V;
                 if (t[k] >= 0 && u < static_cast<uint32_t>(len)) {
-                    if (i + k * kAdjustThreads < prompt) atomicOr(&count[u], 0x80000000u);
-                    else atomicAdd(&count[u], 1u);
+                    const int sh = half ? (u & 1) * 16 : 0;
+                    if (i + k * kAdjustThreads < prompt) atomicOr(&count[u >> half], prompt_bit << sh);
+                    else atomicAdd(&count[u >> half], 1u << sh);
                     atomicOr(&touched[u >> 5], 1u << (u & 31));
                 }
             }
@@ -148,21 +218,36 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
             if (tid == 0 && (total != total_in || prompt != prompt_in)) atomicOr(a.status, SPEC_DEV_BAD_LENGTH);
         }
     }
-    // The first slot that names a token adds the later ones' values, in their order.
-    for (int i = tid; i < a.M; i += kAdjustThreads) {
+    if (a.M) {
+        // The slots that name a token of the slice, in order; the first that names one adds the later ones' values.
         const int32_t *ids = a.bias_ids + static_cast<size_t>(b) * a.M;
-        const int t = ids[i];
-        if (s == 0 && (t < -1 || t >= a.V)) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
-        if (t < t0 || t >= t0 + len) continue;
-        bool first = true;
-        for (int k = 0; k < i && first; ++k) first = ids[k] != t;
-        if (!first) continue;
         const float *values = a.bias + static_cast<size_t>(b) * a.M;
-        float sum = values[i];
-        for (int k = i + 1; k < a.M; ++k)
-            if (ids[k] == t) sum += values[k];
-        bias[t - t0] = sum;
-        atomicOr(&touched[(t - t0) >> 5], 1u << ((t - t0) & 31));
+        if (tid >= 32 && tid < 64) {
+            const int lane = tid - 32;
+            int n = 0;
+            for (int i0 = 0; i0 < a.M; i0 += 32) {
+                const int t = i0 + lane < a.M ? ids[i0 + lane] : -1;
+                if (s == 0 && (t < -1 || t >= a.V)) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
+                const bool in = t >= t0 && t < t0 + len;
+                const uint32_t all = __ballot_sync(0xffffffffu, in);
+                if (in) mine[n + __popc(all & ((1u << lane) - 1))] = static_cast<uint16_t>(i0 + lane);
+                n += __popc(all);
+            }
+            if (lane == 0) biased = n;
+        }
+        __syncthreads();
+        for (int x = tid; x < biased; x += kAdjustThreads) {
+            const int t = ids[mine[x]];
+            bool first = true;
+            for (int y = 0; y < x && first; ++y) first = ids[mine[y]] != t;
+            if (!first) continue;
+            float sum = values[mine[x]];
+            for (int y = x + 1; y < biased; ++y)
+                if (ids[mine[y]] == t) sum += values[mine[y]];
+            sums[x] = sum;
+            bias[t - t0] = static_cast<uint16_t>(x + 1);
+            atomicOr(&touched[(t - t0) >> 5], 1u << ((t - t0) & 31));
+        }
     }
     int n_listed = 0;
     if (counts || a.M) {
@@ -182,72 +267,24 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
         const int n1 = min(n_end, n0 + kAdjustRows);
         // The stream.  In place and without a mask nothing is copied.
         for (int n = n0; (!INPLACE || a.allowed) && n < n1; ++n) {
-            const size_t row = static_cast<size_t>(b) * a.N + n;
-            const size_t first = (row * a.V + t0) * EB;  // the slice's first byte
-            const int off = VEC ? static_cast<int>(reinterpret_cast<uintptr_t>(a.in + first) % 16) / EB : 0;
-            const int vectors = (len + off + EPV - 1) / EPV;
-            const uint32_t *allowed = a.allowed ? a.allowed + row * words : nullptr;
-            for (int j0 = tid; j0 < vectors; j0 += kBatch * kAdjustThreads) {
-                uint32_t ok[kBatch];
-                uint4 v[kBatch];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int u = (j0 + k * kAdjustThreads) * EPV - off;  // the vector's first token in the slice
-                    ok[k] = kAll;
-                    if (!allowed || u < 0 || u + EPV > len) continue;
-                    const int t = t0 + u, w = t >> 5;
-                    const uint32_t low = __ldg(allowed + w), high = (t & 31) + EPV > 32 ? __ldg(allowed + w + 1) : 0;
-                    ok[k] = __funnelshift_r(low, high, t & 31) & kAll;
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int u = (j0 + k * kAdjustThreads) * EPV - off;
-                    v[k] = make_uint4(0, 0, 0, 0);
-                    if (u < 0 || u + EPV > len || ok[k] == 0 || (INPLACE && ok[k] == kAll)) continue;
-                    const unsigned char *from = a.in + first + static_cast<ptrdiff_t>(u) * EB;
-                    if (VEC) v[k] = *reinterpret_cast<const uint4 *>(from);
-                    else v[k].x = EB == 4 ? *reinterpret_cast<const uint32_t *>(from) : *reinterpret_cast<const uint16_t *>(from);
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int u = (j0 + k * kAdjustThreads) * EPV - off;
-                    if (u >= len) continue;
-                    unsigned char *to = a.out + first + static_cast<ptrdiff_t>(u) * EB;
-                    if (u < 0 || u + EPV > len) {  // a vector that the slice holds in part
-                        for (int e = max(0, -u); e < min(EPV, len - u); ++e) {
-                            const int t = t0 + u + e;
-                            const bool let = !allowed || (__ldg(allowed + (t >> 5)) >> (t & 31)) & 1;
-                            if (INPLACE && let) continue;
-                            store_one<EB>(to + e * EB, let ? load_one<EB>(a.in + first + static_cast<ptrdiff_t>(u + e) * EB) : -INFINITY);
-                        }
-                        continue;
-                    }
-                    if (INPLACE && ok[k] == kAll) continue;
-                    if (ok[k] != kAll) {
-                        uint32_t *x = reinterpret_cast<uint32_t *>(&v[k]);
-#pragma unroll
-                        for (int e = 0; e < EPV; ++e) {
-                            if ((ok[k] >> e) & 1) continue;
-                            if (EB == 4) x[e] = 0xff800000u;
-                            else x[e >> 1] = (e & 1) ? (x[e >> 1] & 0xffffu) | 0xff800000u : (x[e >> 1] & 0xffff0000u) | 0xff80u;
-                        }
-                    }
-                    if (VEC) *reinterpret_cast<uint4 *>(to) = v[k];
-                    else if (EB == 4) *reinterpret_cast<uint32_t *>(to) = v[k].x;
-                    else *reinterpret_cast<uint16_t *>(to) = static_cast<uint16_t>(v[k].x);
-                }
+            const int most = (len + EPV - 1) / EPV + (VEC ? 1 : 0);  // vectors of a row, wherever it lies on the 16-byte grid
+            for (int j0 = tid; j0 < most; j0 += kBatch * kAdjustThreads) {
+                Vectors<EB, VEC, INPLACE, kBatch> x;
+                x.masks(a, static_cast<size_t>(b) * a.N + n, t0, len, j0);
+                x.load(a, len);
+                x.store(a, t0, len);
             }
         }
         if (n_listed == 0) continue;
         __syncthreads();  // what was streamed lies under what the listed tokens get
         const int items = n_listed * (n1 - n0);
-        for (int i0 = tid; i0 < items; i0 += kBatch * kAdjustThreads) {
-            uint32_t let[kBatch];
-            float x[kBatch];
-            int u[kBatch], n[kBatch];
-            size_t at[kBatch];
+        for (int i0 = tid; i0 < items; i0 += kFix * kAdjustThreads) {
+            uint32_t let[kFix];
+            float x[kFix];
+            int u[kFix], n[kFix];
+            size_t at[kFix];
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
+            for (int k = 0; k < kFix; ++k) {
                 const int i = i0 + k * kAdjustThreads;
                 let[k] = 0;
                 if (i >= items) continue;
@@ -260,12 +297,12 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustArgs
                 x[k] = load_one<EB>(a.in + at[k]);
             }
 #pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
+            for (int k = 0; k < kFix; ++k) {
                 if (!let[k]) continue;
-                if (a.M) x[k] = __fadd_rn(x[k], bias[u[k]]);
+                if (a.M && bias[u[k]]) x[k] = __fadd_rn(x[k], sums[bias[u[k]] - 1]);
                 if (counts) {
-                    const uint32_t c = count[u[k]];
-                    uint32_t made = c & 0x7fffffffu;
+                    const uint32_t c = half ? count[u[k] >> 1] >> ((u[k] & 1) * 16) & 0xffffu : count[u[k]];
+                    uint32_t made = c & (prompt_bit - 1);
                     if (paths)
                         for (int m = chain[u[k]]; m; m = before[m])
                             made += a.mask ? (__ldg(a.mask + static_cast<size_t>(n[k]) * mask_words + (m >> 5)) >> (m & 31)) & 1 : m <= n[k];
