@@ -77,7 +77,6 @@ struct Control {  // behind the tiles in shared memory
     uint64_t q_full[2], q_empty[2];
     uint64_t scores[2], weights[2][2], sums[2];  // of the two products; weights of a tile's first and second 64 keys
     uint64_t joined[2];            // both warpgroups: statistics there, sums read
-    uint64_t turn[2];              // a warpgroup's weights of a tile are worked out
     uint64_t drained;
     uint32_t tmem;
     int gave_up;
@@ -624,7 +623,7 @@ struct Attention {
     static constexpr uint32_t kNoRow = 256;
     // An 8-bit tile, widened: the chunks of 16 in turned order, so that eight rows' meet different banks.
     __device__ __forceinline__ void widen(uint32_t from, uint32_t to, int r, const Widen<T> &w) const {
-        constexpr int kChunks = D / 16, kAhead = 4;
+        constexpr int kChunks = D / 16, kAhead = 2;
 #pragma unroll 1
         for (int j0 = 0; j0 < kChunks; j0 += kAhead) {
             uint4 v[kAhead];
@@ -782,7 +781,7 @@ struct Attention {
     }
     // A tile's scores into weights in one pass, against the maximum as it stands: false, and nothing done, where a row's
     // has to move on (or the row has seen nothing yet).  Every key is seen.
-    __device__ __forceinline__ bool quick_weights(int s, uint32_t arrivals, bool live, const uint64_t *turn, uint32_t s_at, float scale, float m, float &l) {
+    __device__ __forceinline__ bool quick_weights(int s, uint32_t arrivals, bool live, uint32_t s_at, float scale, float m, float &l) {
         uint32_t x[32], y[32], p0[32], p1[32];
         float top = -INFINITY;
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
@@ -800,7 +799,6 @@ struct Attention {
         weigh_into(x, c2, s2, sum, top, p1, 0);
         wait_loads(y);
         weigh_into(y, c2, s2, sum, top, p1, 16);
-        if (turn && lane == 0) arrive(ptx::smem_addr(turn), arrivals);  // the arithmetic is done
         if (__any_sync(0xffffffffu, live && !(top * scale - kShift <= m + 8.0f))) return false;  // (also where either is NaN)
         tmem_store32(s_at, p0);
         weights_there(s, 0, arrivals);
@@ -918,7 +916,7 @@ struct Attention {
         }
     }
     __device__ void softmax(int s, int tid) {
-        uint32_t scores_round = 0, sums_round = 0, joined_round = 0, turn_round = 0;
+        uint32_t scores_round = 0, sums_round = 0, joined_round = 0;
         bool ok = true;
         const float scale = a.scale * kLog2e;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, at bit 16
@@ -944,18 +942,9 @@ struct Attention {
                     for (int k = 0; k < 4; ++k) w[k] = seen(*p, t, n, k);
                 if (!(ok = hurry(&c->scores[s], scores_round))) break;
                 scores_round ^= 1;
-                // Two products a tile: the warpgroups take turns, so that one's products run behind the other's weights.
-                const uint64_t *pass = two && (s == 0 || t + 1 < t1) ? &c->turn[s] : nullptr;
-                if (two && (s || !first)) {
-                    if (!(ok = hurry(&c->turn[1 - s], turn_round))) break;
-                    turn_round ^= 1;
-                }
                 fence_after();
-                const bool slow = masked || first;
-                if (slow || !quick_weights(s, arrivals, has_row, pass, s_at, scale, m, l)) {
+                if (masked || first || !quick_weights(s, arrivals, has_row, s_at, scale, m, l))
                     tile_weights(s, arrivals, has_row, w, s_at, o_at, scale, first, m, l);
-                    if (slow && pass && lane == 0) arrive(ptx::smem_addr(pass), arrivals);
-                }
                 first = false;
             }
             if (!ok) break;
@@ -967,7 +956,6 @@ struct Attention {
             if (idle) {  // the rounds that went by
                 const int n = two ? t1 - t0 : (t1 - t0 - turn + 1) / 2;
                 scores_round ^= n & 1;
-                if (two) turn_round ^= (s ? n : n - 1) & 1;
             }
             // Two products a tile: each warpgroup writes its rows.  One: both products' sums are joined, and each
             // warpgroup writes half the columns.
@@ -1050,7 +1038,6 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attention_kernel(c
             ptx::mbar_init(ptx::smem_addr(&c->weights[i][1]), 4);
             ptx::mbar_init(ptx::smem_addr(&c->sums[i]), 1);
             ptx::mbar_init(ptx::smem_addr(&c->joined[i]), 8);
-            ptx::mbar_init(ptx::smem_addr(&c->turn[i]), 4);
         }
         ptx::mbar_init(ptx::smem_addr(&c->drained), 2);
         ptx::fence_mbar_init();
