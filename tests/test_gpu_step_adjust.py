@@ -3,6 +3,7 @@
 A value passes through at most five roundings to fp32 (bias sums, bias, repetition, frequency's product and difference,
 presence) and one to the logits' type, each off by half a step of what it rounds: the bound below counts 2^-24 of the
 largest magnitude on the way for each of M + 6, and half a step of the type of the result."""
+import gc
 import math
 
 import pytest
@@ -13,6 +14,14 @@ import sampling_online_softmax_gb300 as sv
 
 pytestmark = pytest.mark.gpu
 i32, f32, BF = torch.int32, torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def memory_given_back():
+    """What these tests keep cached (gigabytes) goes back to the device."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
 
 
 def make(B, N, V, dtype, L=30, M=5, allowed=True, nodes=True, chain=False, seed=1, spread=6.0):

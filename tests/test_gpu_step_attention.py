@@ -6,6 +6,7 @@ Bounds, with u the half step of the type (2^-8 in bf16, 2^-11 in fp16):
   a weight is an exponential good to 2^-21, rounded to the type (u), the sums are fp32 sums of at most `keys` terms;
   so |out - exact| <= (u + 4 d + 2^-20 + keys 2^-24) sum p |v| + u |out|, the last for the result's rounding,
   and |lse - exact| <= 2 d + 2^-20 + keys 2^-24 + |lse| 2^-22."""
+import gc
 import math
 
 import pytest
@@ -13,10 +14,18 @@ import torch
 
 import context_reference as ref
 import sampling_online_softmax_gb300 as sv
-from test_gpu_cache import append, make
+from test_gpu_step_cache import append, make
 
 pytestmark = pytest.mark.gpu
 BF, F16, F8, i32 = torch.bfloat16, torch.float16, torch.float8_e4m3fn, torch.int32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def memory_given_back():
+    """What these tests keep cached (gigabytes) goes back to the device."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
 
 
 def problem(B, N, H, kv, D, page, lens, dtype, q8, seed=1, shared=0, chain=False, spread=1.5, seen=None, width=None):

@@ -1,4 +1,6 @@
 """spec_cache_append and spec_cache_read on the GPU against their definitions in 64 bits."""
+import gc
+
 import pytest
 import torch
 
@@ -7,6 +9,14 @@ import sampling_online_softmax_gb300 as sv
 
 pytestmark = pytest.mark.gpu
 BF, F16, F8, i32, u8 = torch.bfloat16, torch.float16, torch.float8_e4m3fn, torch.int32, torch.uint8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def memory_given_back():
+    """What these tests keep cached (gigabytes) goes back to the device."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
 
 
 def make(B, width, kv, D, page, dtype, q8, seed, spare=2):
