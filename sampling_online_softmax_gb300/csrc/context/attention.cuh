@@ -178,6 +178,7 @@ template <typename T>
 struct Widen;
 template <>
 struct Widen<__nv_bfloat16> {
+    static constexpr uint32_t again = 0;
     float m;
     __device__ __forceinline__ void scale(uint32_t byte) { m = scale_of(byte); }
     __device__ __forceinline__ uint2 four(uint32_t w) const {
@@ -187,12 +188,20 @@ struct Widen<__nv_bfloat16> {
 };
 template <>
 struct Widen<__half> {
-    uint32_t m;
+    // fp16 has the powers 2^-24 .. 2^15.  A row written from bf16 may have others: the row is multiplied by one of them,
+    // which is exact or overflows as the whole would, and then again by what is left (0: nothing).
+    uint32_t m, again;
+    static __device__ __forceinline__ uint32_t power(int e) {
+        const uint32_t s = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 1u << (e + 24);
+        return s | s << 16;
+    }
     __device__ __forceinline__ void scale(uint32_t byte) {
-        const int e = min(max(static_cast<int>(byte) - 127, -24), 15);
-        uint32_t s = e >= -14 ? static_cast<uint32_t>(e + 15) << 10 : 1u << (e + 24);
-        if (byte == 255) s = 0x7fff;
-        m = s | s << 16;
+        const int e = static_cast<int>(byte) - 127;
+        again = 0;
+        if (e > 15) m = power(15), again = power(min(e - 15, 15));
+        else if (e < -24) m = power(-15), again = power(max(e + 15, -24));  // (448 * 2^-39 rounds to 0, as any less does)
+        else m = power(e);
+        if (byte == 255) m = 0x7fff7fffu;
     }
     static __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
         uint32_t r;
@@ -639,6 +648,15 @@ struct Attention {
             }
         }
     }
+    // A widened row times w.again, where its power of two takes two steps.
+    __device__ __forceinline__ void widen_again(uint32_t to, int r, uint32_t m) const {
+#pragma unroll 1
+        for (int i = 0; i < kLanes; ++i) {
+            uint4 v = load16(to + chunk_at(r, i));
+            v.x = Widen<__half>::times(v.x, m), v.y = Widen<__half>::times(v.y, m), v.z = Widen<__half>::times(v.z, m), v.w = Widen<__half>::times(v.w, m);
+            store16(to + chunk_at(r, i), v);
+        }
+    }
     static __device__ __forceinline__ int turned(int j, int r) { return D == 128 ? (j + r) & 7 : (j + (r >> 1)) & 3; }
     // 8 bits: keys and values widened, values of nodes looked through.
     __device__ void work8(int r) {
@@ -668,6 +686,7 @@ struct Attention {
                             Widen<T> x;
                             x.scale(byte);
                             widen(stages + staged.slot * L::kStageBytes, to, r, x);
+                            if (kHalf && x.again) widen_again(to, r, x.again);
                         } else {
                             clear_rows(to, r, 0, 0);
                         }

@@ -87,6 +87,23 @@ def test_tree_attention_host_validation(lib, kw, expect):
     assert (lib.spec_last_error().decode() == "") == (expect == OK)
 
 
+FAR = dict(k=FAKE + (1 << 20), v=FAKE + (1 << 20), out=FAKE + (1 << 21))  # B = 2, N = 3, 4 query heads of 64 on 1 or 2
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(heads=129, cache=dict(kv_heads=1)), UNS), (dict(FAR, strides=[0, 256] + [768, 256] * 2), INV), (dict(FAR, strides=[768, 256, 768, 0, 768, 256]), INV),
+    (dict(FAR, strides=[1 << 38, 256] + [768, 256] * 2), INV), (dict(FAR, strides=[-768, 256] + [768, 256] * 2), INV),
+    (dict(FAR, shared=16, strides=[1024, 256] + [768, 256] * 2), UNS), (dict(cache=dict(table_width=(1 << 26) + 1)), UNS),
+    (dict(FAR, out=FAKE), INV), (dict(FAR, out=FAKE + 16), INV), (dict(FAR, out=FAR["k"] - 16), INV), (dict(FAR, out=FAR["v"] + 16), INV)])
+def test_tree_attention_limits(lib, kw, expect):
+    assert _attend(lib, **kw) == expect and lib.spec_last_error().decode()
+
+
+def test_cache_call_limits(lib):
+    assert _append(lib, B=1 << 20, N=64, S=64) == UNS and _read(lib, B=1 << 20, S=64) == UNS
+    assert _append(lib, cache=dict(table_width=(1 << 26) + 1)) == UNS and _read(lib, cache=dict(table_width=(1 << 26) + 1)) == UNS
+
+
 def test_attention_workspace_sizes(lib):
     size = sv.spec_workspace_bytes_attention
     assert size(4, 5, 8, 2, 128) > 0 and size(4, 5, 8, 2, 128, 1000) >= size(4, 5, 8, 2, 128)

@@ -8,6 +8,9 @@ Bounds, with u the half step of the type (2^-8 in bf16, 2^-11 in fp16):
   and |lse - exact| <= 2 d + 2^-20 + keys 2^-24 + |lse| 2^-22."""
 import gc
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -353,3 +356,80 @@ def test_empty_batch():
     c = s["c"]
     r = sv.spec_tree_attention(s["q"][:0], s["k"][:0], s["v"][:0], c["k_cache"], c["v_cache"], c["page_table"][:0], s["lens"][:0])
     assert r["out"].shape == (0, 3, 4, 64)
+
+
+def test_an_8_bit_cache_with_powers_that_fp16_lacks():
+    """Rows as bf16 ones leave them: powers of two below 2^-24 and above 2^15, whose products with the 8-bit values fp16 holds or rounds."""
+    lens, page, D = [200, 37], 16, 64
+    s = problem(2, 3, 4, 2, D, page, lens, F16, True, seed=31)
+    c, g = s["c"], torch.Generator().manual_seed(31)
+    for n, top in (("k", 16), ("v", 22)):
+        shape = c[n + "_cache"].shape
+        raw = torch.randint(0, 127, shape, generator=g)
+        raw[:, 1] = torch.randint(0, 8, shape, generator=g)[:, 1]  # multiples of 2^-9
+        raw = raw + 128 * torch.randint(0, 2, shape, generator=g)
+        e = torch.randint(-45, -19, shape[:3], generator=g)
+        e[:, 1] = torch.randint(10, top + 1, shape[:3], generator=g)[:, 1]
+        c[n + "_cache"].view(torch.uint8).copy_(raw.to(torch.uint8))
+        c[n + "_scale"].copy_((e + 127).to(torch.uint8))
+        x = torch.ldexp(raw.to(torch.uint8).view(F8).double(), e.unsqueeze(-1).double()).to(F16).double()
+        assert torch.isfinite(x).all()
+        at = [torch.arange(length) for length in lens]
+        table = c["page_table"].cpu().long()
+        s["keys" if n == "k" else "values"] = [x[table[b, i // page], :, i % page] for b, i in enumerate(at)]
+    s["v"].zero_()  # (the nodes' values would hide the context's)
+    r = call(s)
+    assert int(r["status"][0]) == 0
+    out, lse, weight, mass = ref.attention(s["q"], s["k"], s["v"], s["keys"], s["values"], lens, s["seen"], s["scale"])
+    d, count = ((D + 4) * 2.0 ** -24 + 2.0 ** -22) * mass, 203
+    tol = (2.0 ** -11 + 4 * d.unsqueeze(-1) + 2.0 ** -20 + count * 2.0 ** -24) * weight + 2.0 ** -11 * out.abs() + 2.0 ** -25  # (half of fp16's least step)
+    assert ((r["out"].double().cpu() - out).abs() <= tol).all()
+    assert ((r["lse"].double().cpu() - lse).abs() <= 2 * d + 2.0 ** -20 + count * 2.0 ** -24 + lse.abs() * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_tokens_before_sequences(q8):
+    """q, k, v laid out [N, B, heads, head_dim]: a sequence's stride is smaller than a token's."""
+    s = problem(3, 6, 8, 2, 64, 32, [90, 0, 200], BF, q8, seed=15)
+    want = call(s)
+    t = dict(s, **{n: s[n].transpose(0, 1).contiguous().transpose(0, 1) for n in ("q", "k", "v")})
+    r = call(t)
+    assert torch.equal(r["out"], want["out"]) and torch.equal(r["lse"], want["lse"])
+    t = dict(problem(3, 6, 8, 2, 64, 32, [90, 70, 200], BF, q8, seed=15, shared=64))
+    t["q"] = t["q"].transpose(0, 1).contiguous().transpose(0, 1)  # the batch's rows are then not on one axis
+    with pytest.raises(sv.SpecError):
+        call(t)
+
+
+FIRST_CALL_CAPTURED = """
+import torch, sampling_online_softmax_gb300 as sv
+torch.manual_seed(0)
+d, BF, F8, i32 = "cuda", torch.bfloat16, torch.float8_e4m3fn, torch.int32
+q, k, v = (torch.randn((2, 3, h, 64), device=d).to(BF) for h in (4, 2, 2))
+kc, vc = (torch.zeros((8, 2, 16, 64), device=d).to(F8) for _ in range(2))
+ks, vs = (torch.zeros((8, 2, 16), dtype=torch.uint8, device=d) for _ in range(2))
+table, start = torch.arange(8, dtype=i32, device=d).view(2, 4), torch.tensor([5, 20], dtype=i32, device=d)
+hist, logits = torch.randint(0, 100, (2, 9), device=d).to(i32), torch.randn((2, 3, 100), device=d)
+rep = torch.full((2,), 1.5, device=d)
+def step():
+    a = sv.spec_cache_append(k, v, kc, vc, table, start, k_scale=ks, v_scale=vs)
+    r = sv.spec_cache_read(kc, vc, table, start, 3, k_scale=ks, v_scale=vs)
+    t = sv.spec_tree_attention(q, k, v, kc, vc, table, start, k_scale=ks, v_scale=vs, lse=True)
+    j = sv.spec_adjust_logits(logits, tokens=hist, repetition=rep)
+    return [r["k"], r["v"], t["out"], t["lse"], j["logits"]], [a["status"], r["status"], t["status"], j["status"]]
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got, status = step()
+for _ in range(3):
+    graph.replay()
+torch.cuda.synchronize()
+want, _ = step()
+assert all(torch.equal(x, y) for x, y in zip(got, want)) and not any(int(s[0]) for s in status)
+print("captured")
+"""
+
+
+def test_a_first_call_that_is_captured():
+    """A process whose first calls are captured into a graph: kernels, their attributes and the driver's encoder are all first met there."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_CAPTURED], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))), capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
