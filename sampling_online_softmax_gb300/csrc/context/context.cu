@@ -74,7 +74,7 @@ spec_status launch_cache(CacheOp op, const CacheRowsArgs &a, cudaStream_t stream
     const int lanes = op == kRead && Q8 ? D / 16 : D / 8, tokens = std::max(1, kCacheThreads / (a.cache.kv_heads * lanes));
     const long long all = (static_cast<long long>(a.B) * a.S + tokens - 1) / tokens, resident = 8ll * di.sms;  // CTAs' worth; CTAs at once
     // One token under way a thread as long as the CTAs for that are all resident (384 accepted tokens of 8 heads of 128, append and
-    // read: 6.1 us against 7.2 with two), two beyond (39950 tokens: 114 us against 141 with one).
+    // read: 6.3 us against 7.7 with two), two beyond (39950 tokens: 114 us against 118 with one).
     if (all <= resident) {
         if (op == kAppend) cache_append_kernel<T, D, Q8, 1><<<static_cast<unsigned>(all), kCacheThreads, 0, stream>>>(a);
         else cache_read_kernel<T, D, Q8, 1><<<static_cast<unsigned>(all), kCacheThreads, 0, stream>>>(a);

@@ -23,17 +23,19 @@ spec_status launch_adjust(AdjustArgs a, cudaStream_t stream) {
     st = allow_max_dyn_smem(dev, reinterpret_cast<const void *>(kernel), &di);
     if (st != SPEC_OK) return st;
     // Each CTA reads its sequence's whole history, so slices are long and a CTA takes all rows of its
-    // sequence, unless that leaves SMs idle (the slices of the common tokens have most of the listed ones, so
-    // a few CTAs an SM): then fewer rows, and then shorter slices.
-    const long long want = 8ll * di.sms;
+    // sequence, unless that leaves CTAs fewer than are resident at once: then fewer rows, and then shorter slices.
+    // The longest are halved also where there would be fewer than two rounds of CTAs (64 x 5 rows of 128256 bf16: 1024 CTAs
+    // of 8192 tokens take 77 us, 2048 of 4096 71); shorter ones are not (16 x 5 rows: 1024 CTAs of 4096 tokens 21 us, 2048 of 2048 29).
+    const long long resident = kAdjustResident * static_cast<long long>(di.sms);
     const auto slices = [&](int n) { return (a.V + n - 1) / n; };
     a.slice = kMaxSlice;
     a.slices = slices(a.slice);
     const int most = (a.N + kAdjustRows - 1) / kAdjustRows;  // groups of rows
-    a.groups = static_cast<int>(std::min<long long>(most, std::max<long long>(1, want / (static_cast<long long>(a.B) * a.slices))));
+    a.groups = static_cast<int>(std::min<long long>(most, std::max<long long>(1, resident / (static_cast<long long>(a.B) * a.slices))));
     a.rows = (a.N + a.groups - 1) / a.groups;
     a.groups = (a.N + a.rows - 1) / a.rows;
-    while (a.slice > kMinSlice && static_cast<long long>(a.B) * a.groups * a.slices < want) a.slice /= 2, a.slices = slices(a.slice);
+    while (a.slice > kMinSlice && static_cast<long long>(a.B) * a.groups * a.slices < (a.slice == kMaxSlice ? 2 : 1) * resident)
+        a.slice /= 2, a.slices = slices(a.slice);
     const long long per_row = static_cast<long long>(a.B) * a.slices;
     if (per_row * a.groups > INT_MAX) return fail(SPEC_ERR_UNSUPPORTED, "too many rows (B=%d, N=%d, V=%d)", a.B, a.N, a.V);
     const size_t smem = 4 * static_cast<size_t>(AdjustShared(a).words);
