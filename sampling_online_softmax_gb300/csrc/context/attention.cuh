@@ -1111,6 +1111,12 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attention_kernel(c
 }
 
 // ------------------------------------------------------------------ joining
+// x * y / z for y <= kMaxCtas, in 32 bits where these do (all but lists of millions of tiles).
+__device__ __forceinline__ int share_of(int x, int y, int z) {
+    if (x < 1 << 24) return static_cast<int>(static_cast<uint32_t>(x) * static_cast<uint32_t>(y) / static_cast<uint32_t>(z));
+    return static_cast<int>(static_cast<long long>(x) * y / z);
+}
+
 // 32 rows of a block, a lane each, D / 8 columns a warp: the partial sums of the pieces that hold them, in the order
 // of their keys, and the result through shared memory, so that it is written in whole lines.
 template <typename T, int D>
@@ -1123,7 +1129,11 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     const int block = item % a.blocks, g = item / a.blocks % a.cache.kv_heads, b = item / a.blocks / a.cache.kv_heads;
     const int total = a.starts[a.B], start = a.starts[b], tiles = (a.starts[b + 1] - start) / (a.cache.kv_heads * a.blocks);
     if (tiles == 0) return;  // left out
-    const auto owner = [&](int t) { return static_cast<int>(((t + 1ll) * a.ctas - 1) / total); };
+    // The CTA whose run holds tile t: the least c with t < (c + 1) total / ctas, rounded down.
+    const auto owner = [&](int t) {
+        if (t < 1 << 24) return static_cast<int>(((t + 1u) * static_cast<uint32_t>(a.ctas) - 1) / static_cast<uint32_t>(total));
+        return static_cast<int>(((t + 1ll) * a.ctas - 1) / total);
+    };
     const int own0 = start + (g * a.blocks + block) * tiles, c0 = owner(own0), c1 = owner(own0 + tiles - 1);
     if (c0 == c1 && !a.shared_len) return;  // written already
     const int rows = min(a.block_rows, a.N * a.group - block * a.block_rows);  // of the block
@@ -1147,8 +1157,8 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     };
     const auto pieces = [&](int t0, int from, int to, int at) {  // of a block whose tiles begin at t0
         for (int c = from; c <= to; ++c) {
-            const int lo = static_cast<int>(static_cast<long long>(c) * total / a.ctas);
-            if (lo == static_cast<int>((c + 1ll) * total / a.ctas)) continue;  // a CTA without tiles
+            const int lo = share_of(total, c, a.ctas);
+            if (lo == share_of(total, c + 1, a.ctas)) continue;  // a CTA without tiles
             take(cut_part<D>(a, c, t0 >= lo), at);
         }
     };
