@@ -25,7 +25,9 @@
  *
  * Conventions shared by every entry point
  *   - Every pointer except `stream` is DEVICE memory owned by the caller; the
- *     library allocates nothing and keeps no pointer after the call returns.
+ *     library allocates nothing and keeps no pointer after the call returns
+ *     (spec_cache and the strides of the calls on a cache are host memory, read
+ *     during the call).
  *   - Logits are row-major with the vocabulary contiguous (row stride V
  *     elements), fp32 or bf16, aligned to their element size.
  *   - Calls are stream-ordered and asynchronous: they enqueue kernels on
@@ -47,6 +49,8 @@
  *     that reports SPEC_DEV_TIMEOUT: its last CTA then clears every byte the
  *     call used -- so one zeroing suffices for any number of calls, but one
  *     workspace must not be shared by calls that may run at the same time.
+ *     spec_tree_attention's workspace need not be cleared; it too must not be
+ *     shared by calls that may run at the same time, two captured graphs among them.
  *   - Residency: the verify kernel's warps wait (bounded) on values that
  *     warps of other CTAs publish, so it is launched cooperatively: all its
  *     CTAs (at most one per SM) are resident at once, or the launch fails and
@@ -55,8 +59,8 @@
  *     context); it never deadlocks waiting for a CTA that cannot start.
  *   - Apart from a per-thread copy of the last error message, the library keeps
  *     only caches filled once per device and guarded by locks (a kernel's
- *     occupancy, in blocks or clusters, and shared-memory limit, the static workspace's address); the
- *     functions may be called from several host threads.
+ *     occupancy, in blocks or clusters, and shared-memory limit, the static workspace's address, the
+ *     address of the driver's encoder of tensor maps); the functions may be called from several host threads.
  */
 #ifndef SPEC_VERIFY_H
 #define SPEC_VERIFY_H
@@ -513,9 +517,9 @@ typedef struct spec_cache {
  *   count    [B] int32: only rows i < count[b] (above S: S, below 0: none); NULL: all S.
  *            spec_verify_linear's num_emitted, when u_bonus was given, counts the accepted rows (the root's among them).
  * No length is advanced: the layers of a model call this with the same start.
- * Two rows that name one slot leave either's value.  dev_status: SPEC_DEV_BAD_LENGTH (a
+ * Two rows that name one slot leave either's value; k and v must not overlap the cache.  dev_status: SPEC_DEV_BAD_LENGTH (a
  * position behind the table, or an entry of select not below N), SPEC_DEV_BAD_PAGE; such a row
- * is not written.  No workspace; one launch.
+ * is not written.  B * S <= INT_MAX / 64; positions below 2^30; kv_heads <= 1024.  No workspace; one launch.
  */
 SPEC_API spec_status spec_cache_append(const void *k, const void *v, spec_dtype dtype, int B, int N, const long long *strides,
                                        const int32_t *select, int S, const int32_t *start, const int32_t *count,
@@ -545,7 +549,8 @@ SPEC_API spec_status spec_cache_read(const spec_cache *cache, int B, int S, cons
  *   q [B, N, heads, head_dim], k, v [B, N, kv_heads, head_dim] of `dtype` (SPEC_BF16 or
  *          SPEC_F16): the nodes' own, not in the cache yet (spec_cache_append adds the accepted
  *          ones); strides (host, 6 entries: q's batch and token strides in elements, k's, v's;
- *          multiples of 8) or NULL for contiguous; 16-byte aligned.
+ *          multiples of 8, above 0 and below 2^38) or NULL for contiguous; 16-byte aligned.  With
+ *          shared_len q's batch stride is N times its token stride, or B = 1 (else SPEC_ERR_UNSUPPORTED).
  *   cache  of `dtype` or SPEC_E4M3.  Positions may differ in their key heads' scales.
  *   context_lens [B] int32; a sequence with a negative length is left out, its rows of out
  *          and lse as they were.
@@ -555,7 +560,8 @@ SPEC_API spec_status spec_cache_read(const spec_cache *cache, int B, int S, cons
  *          shared_len (SPEC_DEV_BAD_LENGTH where it is not, and that sequence's rows are unspecified).
  *   mask   [N, ceil(N/32)] as spec_tree_mask gives it; NULL: a chain, nodes 0 .. n.
  *   scale  finite, > 0.
- *   out    [B, N, heads, head_dim] of `dtype`, contiguous, 16-byte aligned.
+ *   out    [B, N, heads, head_dim] of `dtype`, contiguous, 16-byte aligned; overlaps nothing that is read
+ *          (SPEC_ERR_INVALID_ARG for q, k and v).
  *   lse    [B, N, heads] fp32 or NULL: log sum_j exp(s_j).
  *   dev_status  SPEC_DEV_BAD_LENGTH, SPEC_DEV_BAD_PAGE: that sequence's rows are unspecified;
  *          SPEC_DEV_TIMEOUT.
@@ -563,7 +569,8 @@ SPEC_API spec_status spec_cache_read(const spec_cache *cache, int B, int S, cons
  *          call does not matter.
  * Scores, sums and the weighted sums are fp32; exp(s_j - m), the weight of v_j in the matrix
  * product, is rounded to `dtype` (2^-9 of itself in bf16, with errors that the sum averages).
- * 1 <= N <= SPEC_MAX_NODES; heads a multiple of kv_heads.  The same result every time.
+ * 1 <= N <= SPEC_MAX_NODES; heads a multiple of kv_heads, at most 128 times it.  Positions below 2^30, and at most
+ * INT_MAX tiles of 128 keys (by the table's width).  Two launches.  The same result every time.
  */
 SPEC_API size_t spec_workspace_bytes_attention(int B, int N, int heads, int kv_heads, int head_dim, int shared_len);
 SPEC_API spec_status spec_tree_attention(const void *q, const void *k, const void *v, spec_dtype dtype, int B, int N, int heads,

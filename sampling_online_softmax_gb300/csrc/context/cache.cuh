@@ -9,9 +9,10 @@
 // A row is held by lanes with 16 bytes of it each (16 of its 8-bit values, where it is read back), so a
 // warp's loads are whole lines; the row's maximum takes log2 of the lanes' number shuffles.  A CTA's
 // threads take the rows of one token, or of a few, and two tokens at a time are under way: where a token
-// goes is worked out once for its keys and values.  Bound by HBM where there are many tokens (39950 of 8 heads
-// of 128: append and read together 72 us at the copy rate), by launch and three dependent trips (start,
-// page, row) where there are few.
+// goes is worked out once for its keys and values.  Where there are many tokens (39950 of 8 heads of 128, from bf16 to
+// 8 bits and back: 72 us at the copy rate) writing takes 61 us and reading 53, 4 - 4.7 TB/s: the first is bound by its
+// arithmetic (issue slots 63 % busy: maxima, scaling, conversions), the second by loads under way.  Where there are few, by
+// launch and three dependent trips (start, page, row): 384 accepted tokens of 64 sequences, both ways, 6.3 us.
 #pragma once
 
 #include <cuda_fp8.h>
