@@ -564,6 +564,17 @@ def _raw_stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _alloc(nbytes, stream):
+    """Memory of the caching allocator for a stream (its handle) of the current device: the address.  (torch.empty takes 5 us
+    more beside a launch.)"""
+    return torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, stream)
+
+
+def _free(at):
+    """Gives memory of _alloc back: what the stream has enqueued keeps it, as it does a freed tensor's."""
+    torch._C._cuda_cudaCachingAllocator_raw_delete(at)
+
+
 def _capturing(stream):
     with torch.cuda.stream(stream):
         return torch.cuda.is_current_stream_capturing()
@@ -814,7 +825,10 @@ def _new_tokens(t, name):
 
 def _strides(shapes, rows):
     """Batch and token strides of what _token_rows returned, as the C ABI takes them (NULL: all contiguous; the array takes 1.3 us)."""
-    if all(r[1] is None for r in rows):
+    for r in rows:
+        if r[1] is not None:
+            break
+    else:
         return None
     each = [r[1] or (n * heads * dim, heads * dim) for (_, n, heads, dim), r in zip(shapes, rows)]
     return (ctypes.c_longlong * (2 * len(rows)))(*(x for e in each for x in e))
@@ -885,7 +899,9 @@ def spec_workspace_bytes_attention(B: int, N: int, heads: int, kv_heads: int, he
     return int(load_library().spec_workspace_bytes_attention(int(B), int(N), int(heads), int(kv_heads), int(head_dim), int(shared_len)))
 
 
-_attention_room = functools.lru_cache(maxsize=256)(spec_workspace_bytes_attention)  # (of the sizes alone)
+@functools.lru_cache(maxsize=256)
+def _attention_room(lib, *sizes):  # (of the sizes alone)
+    return lib.spec_workspace_bytes_attention(*sizes)
 
 
 def spec_tree_attention(q, k, v, k_cache, v_cache, page_table, context_lens, *, mask=None, shared_len=0, scale=None, k_scale=None,
@@ -916,16 +932,21 @@ def spec_tree_attention(q, k, v, k_cache, v_cache, page_table, context_lens, *, 
         shapes["lse"] = ((B, N, heads), torch.float32)
     given = out is not None
     out, to, st = _results(out, shapes, status, dev, i, stream)
-    if workspace is None:  # (of the stream's own memory, or of the graph that is being captured)
-        room = max(_attention_room(B, N, heads, kv, dim, shared_len), 16)
-        with _ON_CURRENT if stream is None else torch.cuda.stream(stream):
-            workspace = torch.empty(room, dtype=torch.uint8, device=dev)
+    own = None
+    if workspace is None:  # the stream's own memory, or of the graph that is being captured, given back once the call is enqueued
+        room = max(_attention_room(lib, B, N, heads, kv, dim, shared_len), 16)
+        with _ON_CURRENT if i == torch.cuda.current_device() else torch.cuda.device(dev):
+            at_ws = own = _alloc(room, _raw_stream(i) if stream is None else stream.cuda_stream)
     else:
         _cuda(workspace, "workspace", None, dev)
-        room = workspace.numel() * workspace.element_size()
-    _launch(lib.spec_tree_attention, (at[0][0], at[1][0], at[2][0], _CODES[dtype], B, N, heads, _strides((qs, ks, ks), at), ctypes.byref(cache), *args,
-                                      to[0], to[1] if lse else None, st, workspace.data_ptr(), room),
-            (q, k, v, k_cache, v_cache, page_table, context_lens, mask, k_scale, v_scale, workspace, *out.values()), dev, stream)
+        at_ws, room = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    try:
+        _launch(lib.spec_tree_attention, (at[0][0], at[1][0], at[2][0], _CODES[dtype], B, N, heads, _strides((qs, ks, ks), at), ctypes.byref(cache), *args,
+                                          to[0], to[1] if lse else None, st, at_ws, room),
+                (q, k, v, k_cache, v_cache, page_table, context_lens, mask, k_scale, v_scale, workspace, *out.values()), dev, stream)
+    finally:
+        if own is not None:
+            _free(own)
     if given:
         _overwritten([out[x] for x in shapes])
     return out

@@ -160,6 +160,8 @@ def fake(monkeypatch):
     monkeypatch.setattr(sv, "_on_gpu", lambda t, name: None)
     monkeypatch.setattr(sv, "_raw_stream", lambda index: 0)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(sv, "_alloc", lambda nbytes, stream: calls.append("alloc") or 256)
+    monkeypatch.setattr(sv, "_free", lambda at: calls.append("free"))
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     return calls
 
@@ -239,6 +241,15 @@ def test_tree_attention_binding(fake, monkeypatch):
         with pytest.raises(TypeError):
             call(base, **bad)
     assert fake.count("spec_tree_attention") == 2
+    # the workspace goes back, once for each it came, also where the call is refused
+    assert fake.count("alloc") == fake.count("free") == 2
+    monkeypatch.setattr(sv, "_launch", lambda *a: (_ for _ in ()).throw(RuntimeError("refused")))
+    with pytest.raises(RuntimeError):
+        call(s)
+    assert fake.count("alloc") == fake.count("free") == 3
+    with pytest.raises(RuntimeError):
+        call(s, workspace=torch.zeros(4096, dtype=torch.uint8))
+    assert fake.count("alloc") == 3
 
 
 def test_adjust_logits_binding(fake):
