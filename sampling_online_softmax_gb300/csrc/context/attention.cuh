@@ -22,10 +22,10 @@
 // What bounds it, by rows a block and the cache's type (128-wide heads, one CTA of 512 threads an SM):
 //   long contexts, few rows   HBM: 3 contexts of up to 131072, 9 nodes x 4 heads: 192 us, 6.5 TB/s, 96 % of a copy
 //   two full halves           the chain scores -> weights -> sums of two products, 4 - 4.9 thousand clocks a tile, of which the
-//                             tensor cores are at work 2.2: 48 sequences of 9 nodes behind 16384 shared tokens 195 us
-//                             (0.61 PFLOP/s), 64 nodes of 16 sequences over 4096 75 us, 15 of them the second kernel's
+//                             tensor cores are at work 2.2: 48 sequences of 9 nodes behind 16384 shared tokens 172 us
+//                             (0.69 PFLOP/s), 64 nodes of 16 sequences over 4096 73 us, 15 of them the second kernel's
 //   8-bit tiles               widening, 3.3 thousand clocks a tile of four warps, and shared memory, which the widening and the
-//                             products share: 64 sequences of 5 nodes over 8192 298 us, 2.5 TB/s (16 bits: 231 us, 6.3 TB/s)
+//                             products share: 64 sequences of 5 nodes over 8192 296 us, 2.5 TB/s (16 bits: 225 us, 6.4 TB/s)
 //   small calls               launches and the chain from the list to the first sums: one token over 700 18 us
 // More worker warps, the softmaxes in turn, and the second kernel launched early were each measured slower.
 #pragma once
@@ -767,9 +767,8 @@ struct Attention {
         for (int j = 0; j < 32; ++j) top[j & 3] = fmaxf(top[j & 3], !((w >> j) & 1) ? -INFINITY : __uint_as_float(x[j]));
         return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
     }
-    // Weights of 32 columns into tensor memory; their sum is added to `sum`.
-    static __device__ __forceinline__ void weigh(const uint32_t (&x)[32], uint32_t w, float2 scale, float2 sub, float2 (&sum)[2], uint32_t to) {
-        uint32_t y[16];
+    // Weights of 32 columns; their sum is added to `sum`.
+    static __device__ __forceinline__ void weigh(const uint32_t (&x)[32], uint32_t w, float2 scale, float2 sub, float2 (&sum)[2], uint32_t (&y)[16]) {
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
             float2 e = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), scale, sub);
@@ -780,7 +779,6 @@ struct Attention {
             sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
             y[j / 2] = Elt<T>::from_float2(e.x, e.y);
         }
-        tmem_store16(to, y);
     }
     // A row's maximum and sum move on to what `top`, the largest score of a tile, asks for; the sums are scaled along.
     // `m` is what the exponents subtract, in units of log 2; -inf while the row has seen nothing.
@@ -850,38 +848,45 @@ struct Attention {
         }
     }
     // A tile's scores into weights, whose halves the products may take one after the other: two passes over tensor
-    // memory (the row's maximum, then the weights), 32 columns at a time, the next ones under way.  The loops stay
-    // loops: the kinds of warps share the instruction caches, which their unrolled bodies would overflow.
-    __device__ __forceinline__ void tile_weights(int s, uint32_t arrivals, bool live, const uint32_t (&w)[4], uint32_t s_at, uint32_t o_at, float scale, bool first, float &m, float &l) {
+    // memory (the row's maximum, then the weights), 32 columns at a time.  Most columns are seen by every row or by none (a
+    // context's ends, few nodes): those go without looking at bits, or are skipped (48 x 9 nodes behind 16384 shared tokens: 195 us
+    // without that, 172 so).  The loops stay loops: the kinds of warps share the instruction caches, which their unrolled bodies
+    // would overflow.
+    __device__ __forceinline__ void tile_weights(int s, uint32_t arrivals, bool live, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t s_at, uint32_t o_at, float scale, bool first, float &m, float &l) {
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         const float2 c2 = make_float2(scale, scale);
-        uint32_t x[32], y[32];
         float top = -INFINITY;
-        __syncwarp();
-        tmem_load32(x, s_at);
 #pragma unroll 1
-        for (int k = 0; k < 4; k += 2) {
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t w = w0;
+            w0 = w1, w1 = w2, w2 = w3, w3 = w;
+            if (!__any_sync(0xffffffffu, w != 0)) continue;
+            uint32_t x[32];
+            tmem_load32(x, s_at + 32 * k);
             wait_loads(x);
-            tmem_load32(y, s_at + 32 * k + 32);
-            top = fmaxf(top, largest(x, k ? w[2] : w[0]));
-            wait_loads(y);
-            tmem_load32(x, s_at + ((32 * k + 64) & 127));  // (the last: the first columns again, for the second pass)
-            top = fmaxf(top, largest(y, k ? w[3] : w[1]));
+            top = fmaxf(top, __all_sync(0xffffffffu, w == ~0u) ? largest(x, ~0u) : largest(x, w));
         }
-        wait_loads(x);
         move_on(top * scale, live, o_at, first, m, l);
         const float sub = m == -INFINITY ? 0.0f : -m;
         const float2 s2 = make_float2(sub, sub);
         __syncwarp();
 #pragma unroll 1
-        for (int k = 0; k < 4; k += 2) {
-            tmem_load32(y, s_at + 32 * k + 32);
-            weigh(x, k ? w[2] : w[0], c2, s2, sum, s_at + 16 * k);
-            wait_loads(y);
-            if (k == 0) tmem_load32(x, s_at + 64);
-            weigh(y, k ? w[3] : w[1], c2, s2, sum, s_at + 16 * k + 16);
-            weights_there(s, k / 2, arrivals);
-            if (k == 0) wait_loads(x);
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t w = w0;
+            w0 = w1, w1 = w2, w2 = w3, w3 = w;
+            uint32_t y[16];
+            if (!__any_sync(0xffffffffu, w != 0)) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = 0;
+            } else {
+                uint32_t x[32];
+                tmem_load32(x, s_at + 32 * k);
+                wait_loads(x);
+                if (__all_sync(0xffffffffu, w == ~0u)) weigh(x, ~0u, c2, s2, sum, y);
+                else weigh(x, w, c2, s2, sum, y);
+            }
+            tmem_store16(s_at + 16 * k, y);
+            if (k & 1) weights_there(s, k >> 1, arrivals);
         }
         const float2 both = add2(sum[0], sum[1]);
         l += both.x + both.y;
@@ -974,7 +979,7 @@ struct Attention {
                 scores_round ^= 1;
                 fence_after();
                 if (masked || first || !quick_weights(s, arrivals, has_row, s_at, scale, m, l))
-                    tile_weights(s, arrivals, has_row, w, s_at, o_at, scale, first, m, l);
+                    tile_weights(s, arrivals, has_row, w[0], w[1], w[2], w[3], s_at, o_at, scale, first, m, l);
                 first = false;
             }
             if (!ok) break;
