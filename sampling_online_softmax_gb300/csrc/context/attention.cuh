@@ -16,16 +16,15 @@
 //   one or two warps the list of work, TMA of queries and of tiles; with 8-bit tiles one more for their TMA
 //
 // The softmax keeps a row's running maximum as it was until a tile's exceeds it by 2^8: weights up to 2^8
-// lose nothing in a float format, and O is rescaled almost never.  So a tile's weights come of one pass over its scores,
-// and a second pass is taken only where a maximum moves on or a mask cuts.
+// lose nothing in a float format, and O is rescaled almost never.
 //
 // What bounds it, by rows a block and the cache's type (128-wide heads, one CTA of 512 threads an SM):
 //   long contexts, few rows   HBM: 3 contexts of up to 131072, 9 nodes x 4 heads: 192 us, 6.5 TB/s, 96 % of a copy
 //   two full halves           the chain scores -> weights -> sums of two products, 4 - 4.9 thousand clocks a tile, of which the
-//                             tensor cores are at work 2.2: 48 sequences of 9 nodes behind 16384 shared tokens 172 us
-//                             (0.69 PFLOP/s), 64 nodes of 16 sequences over 4096 73 us, 15 of them the second kernel's
+//                             tensor cores are at work 2.2: 48 sequences of 9 nodes behind 16384 shared tokens 158 us
+//                             (0.75 PFLOP/s), 64 nodes of 16 sequences over 4096 73 us, 15 of them the second kernel's
 //   8-bit tiles               widening, 3.3 thousand clocks a tile of four warps, and shared memory, which the widening and the
-//                             products share: 64 sequences of 5 nodes over 8192 296 us, 2.5 TB/s (16 bits: 225 us, 6.4 TB/s)
+//                             products share: 64 sequences of 5 nodes over 8192 280 us, 2.6 TB/s (16 bits: 223 us, 6.5 TB/s)
 //   small calls               launches and the chain from the list to the first sums: one token over 700 18 us
 // More worker warps, the softmaxes in turn, and the second kernel launched early were each measured slower.
 #pragma once
@@ -807,64 +806,30 @@ struct Attention {
         __syncwarp();
         if (lane == 0) arrive(ptx::smem_addr(&c->weights[s][h]), arrivals);
     }
-    // A tile's scores into weights in one pass, against the maximum as it stands: false, and nothing done, where a row's
-    // has to move on (or the row has seen nothing yet).  Every key is seen.
-    __device__ __forceinline__ bool quick_weights(int s, uint32_t arrivals, bool live, uint32_t s_at, float scale, float m, float &l) {
-        uint32_t x[32], y[32], p0[32], p1[32];
-        float top = -INFINITY;
-        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        const float2 c2 = make_float2(scale, scale), s2 = make_float2(-m, -m);
-        __syncwarp();
-        tmem_load32(x, s_at);
-        wait_loads(x);
-        tmem_load32(y, s_at + 32);
-        weigh_into(x, c2, s2, sum, top, p0, 0);
-        wait_loads(y);
-        tmem_load32(x, s_at + 64);
-        weigh_into(y, c2, s2, sum, top, p0, 16);
-        wait_loads(x);
-        tmem_load32(y, s_at + 96);
-        weigh_into(x, c2, s2, sum, top, p1, 0);
-        wait_loads(y);
-        weigh_into(y, c2, s2, sum, top, p1, 16);
-        if (__any_sync(0xffffffffu, live && !(top * scale - kShift <= m + 8.0f))) return false;  // (also where either is NaN)
-        tmem_store32(s_at, p0);
-        weights_there(s, 0, arrivals);
-        tmem_store32(s_at + 32, p1);
-        weights_there(s, 1, arrivals);
-        const float2 both = add2(sum[0], sum[1]);
-        l += both.x + both.y;
-        return true;
-    }
-    static __device__ __forceinline__ void weigh_into(const uint32_t (&x)[32], float2 scale, float2 sub, float2 (&sum)[2], float &top, uint32_t (&to)[32], int at) {
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-            top = fmaxf(top, fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
-            float2 e = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), scale, sub);
-            e.x = ptx::ex2(e.x);
-            e.y = ptx::ex2(e.y);
-            sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
-            to[at + j / 2] = Elt<T>::from_float2(e.x, e.y);
-        }
-    }
-    // A tile's scores into weights, whose halves the products may take one after the other: two passes over tensor
-    // memory (the row's maximum, then the weights), 32 columns at a time.  Most columns are seen by every row or by none (a
-    // context's ends, few nodes): those go without looking at bits, or are skipped (48 x 9 nodes behind 16384 shared tokens: 195 us
-    // without that, 172 so).  The loops stay loops: the kinds of warps share the instruction caches, which their unrolled bodies
-    // would overflow.
-    __device__ __forceinline__ void tile_weights(int s, uint32_t arrivals, bool live, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, uint32_t s_at, uint32_t o_at, float scale, bool first, float &m, float &l) {
+    // A tile's scores into weights, whose halves the products may take one after the other: the row's maximum, then the
+    // weights, 32 columns at a time, in loops that read tensor memory twice.  Code counts here, since the kinds of warps share
+    // the instruction caches: with one reading, all 128 columns unrolled and their weights held until the maximum is known
+    // to stand, 48 x 9 nodes behind 16384 shared tokens take 172 us, in loops of 64 columns 162, in these 158.
+    // MASKED: a row sees some of the columns; those that no row sees (behind a context's end, beyond few nodes) are skipped.
+    template <bool MASKED>
+    __device__ __forceinline__ void tile_weights(int s, uint32_t arrivals, bool live, uint32_t (&w)[4], uint32_t s_at, uint32_t o_at, float scale, bool first, float &m, float &l) {
+        const auto next = [&] {
+            const uint32_t x = w[0];
+            w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = x;
+            return x;
+        };
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         const float2 c2 = make_float2(scale, scale);
         float top = -INFINITY;
+        __syncwarp();
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-            const uint32_t w = w0;
-            w0 = w1, w1 = w2, w2 = w3, w3 = w;
-            if (!__any_sync(0xffffffffu, w != 0)) continue;
+            const uint32_t seen = MASKED ? next() : ~0u;
+            if (MASKED && !__any_sync(0xffffffffu, seen != 0)) continue;
             uint32_t x[32];
             tmem_load32(x, s_at + 32 * k);
             wait_loads(x);
-            top = fmaxf(top, __all_sync(0xffffffffu, w == ~0u) ? largest(x, ~0u) : largest(x, w));
+            top = fmaxf(top, largest(x, seen));
         }
         move_on(top * scale, live, o_at, first, m, l);
         const float sub = m == -INFINITY ? 0.0f : -m;
@@ -872,20 +837,18 @@ struct Attention {
         __syncwarp();
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-            const uint32_t w = w0;
-            w0 = w1, w1 = w2, w2 = w3, w3 = w;
-            uint32_t y[16];
-            if (!__any_sync(0xffffffffu, w != 0)) {
+            const uint32_t seen = MASKED ? next() : ~0u;
+            uint32_t p[16];
+            if (MASKED && !__any_sync(0xffffffffu, seen != 0)) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = 0;
+                for (int j = 0; j < 16; ++j) p[j] = 0;
             } else {
                 uint32_t x[32];
                 tmem_load32(x, s_at + 32 * k);
                 wait_loads(x);
-                if (__all_sync(0xffffffffu, w == ~0u)) weigh(x, ~0u, c2, s2, sum, y);
-                else weigh(x, w, c2, s2, sum, y);
+                weigh(x, seen, c2, s2, sum, p);
             }
-            tmem_store16(s_at + 16 * k, y);
+            tmem_store16(s_at + 16 * k, p);
             if (k & 1) weights_there(s, k >> 1, arrivals);
         }
         const float2 both = add2(sum[0], sum[1]);
@@ -971,15 +934,15 @@ struct Attention {
             const int turn = p->turn ^ s;
             for (int t = idle ? t1 : t0 + (two ? 0 : turn); t < t1; t += two ? 1 : 2) {
                 const bool masked = t < plain0 || t >= plain1;
-                uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
+                uint32_t w[4] = {};
                 if (masked)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) w[k] = seen(*p, t, n, k);
                 if (!(ok = hurry(&c->scores[s], scores_round))) break;
                 scores_round ^= 1;
                 fence_after();
-                if (masked || first || !quick_weights(s, arrivals, has_row, s_at, scale, m, l))
-                    tile_weights(s, arrivals, has_row, w[0], w[1], w[2], w[3], s_at, o_at, scale, first, m, l);
+                if (masked) tile_weights<true>(s, arrivals, has_row, w, s_at, o_at, scale, first, m, l);
+                else tile_weights<false>(s, arrivals, has_row, w, s_at, o_at, scale, first, m, l);
                 first = false;
             }
             if (!ok) break;
