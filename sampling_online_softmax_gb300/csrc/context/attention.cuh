@@ -11,22 +11,24 @@
 //
 //   warps 0-3, 4-7   softmax of product 0, 1: a thread a row
 //   four warps       values whose other rows must be 0 (what lies behind a sequence's end, nodes that are
-//                    not finite: 0 * NaN is NaN); 8-bit tiles, widened
+//                    not finite: 0 * NaN is NaN); 8-bit tiles, widened: four for keys, four for values
 //   a lane each      tcgen05.mma of product 0, of product 1
 //   one or two warps the list of work, TMA of queries and of tiles; with 8-bit tiles one more for their TMA
 //
 // The softmax keeps a row's running maximum as it was until a tile's exceeds it by 2^8: weights up to 2^8
 // lose nothing in a float format, and O is rescaled almost never.
 //
-// What bounds it, by rows a block and the cache's type (128-wide heads, one CTA of 512 threads an SM):
+// What bounds it, by rows a block and the cache's type (128-wide heads, one CTA an SM):
 //   long contexts, few rows   HBM: 3 contexts of up to 131072, 9 nodes x 4 heads: 192 us, 6.5 TB/s, 96 % of a copy
 //   two full halves           the chain scores -> weights -> sums of two products, 4 - 4.9 thousand clocks a tile, of which the
 //                             tensor cores are at work 2.2: 48 sequences of 9 nodes behind 16384 shared tokens 158 us
 //                             (0.75 PFLOP/s), 64 nodes of 16 sequences over 4096 73 us, 15 of them the second kernel's
-//   8-bit tiles               widening, 3.3 thousand clocks a tile of four warps, and shared memory, which the widening and the
-//                             products share: 64 sequences of 5 nodes over 8192 280 us, 2.6 TB/s (16 bits: 223 us, 6.5 TB/s)
+//   8-bit tiles               widening, 1.6 thousand clocks a tile of two times four warps, and shared memory, which it and the
+//                             products share: 64 sequences of 5 nodes over 8192 233 us, 3.1 TB/s (16 bits: 223 us, 6.5 TB/s)
 //   small calls               launches and the chain from the list to the first sums: one token over 700 18 us
-// More worker warps, the softmaxes in turn, and the second kernel launched early were each measured slower.
+// With four warps for keys and values of 8 bits, in turn, the last took 280 us; with two halves of rows the eight are slower (64
+// query heads, 32 nodes: 436 us against 421), since the softmax has fewer registers and shares more, and stay all the same.
+// The softmaxes in turn, and the second kernel launched early, were each measured slower.
 #pragma once
 
 #include <algorithm>
@@ -45,10 +47,10 @@ template <int D, bool Q8>
 struct Layout {
     static constexpr int kTileBytes = kTile * D * 2;         // of 128 rows of keys or values
     static constexpr int kStageBytes = Q8 ? kTile * D : 0;   // of an 8-bit tile
-    static constexpr int kWorkers = 4;                       // warps that clear and widen
+    static constexpr int kWorkers = Q8 ? 8 : 4;              // warps that clear and widen: 8 bits, four for keys and four for values
     static constexpr int kThreads = (8 + kWorkers + 4) * 32;
-    // Registers of a thread after the start, by role: over the four warpgroups they sum to what the launch has, 4 * 128.
-    static constexpr int kSoftmaxRegs = 176, kWorkerRegs = 64, kSingleRegs = 96;
+    // Registers of a thread after the start, by role: over the warpgroups they sum to what the launch has, 4 * 128 or 5 * 96.
+    static constexpr int kLaunchRegs = Q8 ? 96 : 128, kSoftmaxRegs = Q8 ? 128 : 176, kWorkerRegs = 64, kSingleRegs = 96;
 };
 
 // How shared memory is shared out: two halves of queries, as many rows of each as a launch has (a product reads 128 rows
@@ -61,7 +63,7 @@ inline void share_out(AttentionArgs *a, int room) {
     int left = room - 2 * a->q_sub * (D / 64);
     a->ring = Q8 ? (D == 128 ? 4 : 8) : std::min(8, left / L::kTileBytes);
     left -= a->ring * L::kTileBytes;
-    a->stages = Q8 ? std::min(8, left / L::kStageBytes) : 0;
+    a->stages = Q8 ? std::min(8, left / L::kStageBytes) / 2 * 2 : 0;  // (even: keys and values have slots of their own)
 }
 
 // A CTA's run of the list, cut at the blocks' borders.
@@ -90,7 +92,7 @@ struct Control {  // behind the tiles in shared memory
     uint64_t drained;
     uint32_t tmem;
     int gave_up;
-    int scan[16];
+    int scan[20];
     int total, b, before;          // tiles in all; the sequence a CTA begins in and the tiles before it
     float2 stats[2][kTile];
 };
@@ -627,17 +629,15 @@ struct Attention {
         return odd;
     }
     // The row of a thread at position `pos` of a piece: its page as the table has it (-1: no such row), and the scale of its
-    // keys (w = 0) or values, from a page.
+    // keys (which = 0) or values, from a page.
     __device__ __forceinline__ int row_page(const int32_t *table, int pos, int from, int to) const {
         return pos >= from && pos < to ? __ldg(table + (pos >> a.cache.page_bits)) : -1;
     }
-    __device__ __forceinline__ void row_scales(int page, int pos, int g, uint32_t &key, uint32_t &value) const {
-        key = value = kNoRow;
-        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.cache.pages)) return;
+    __device__ __forceinline__ uint32_t row_scale(int page, int pos, int g, int which) const {
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(a.cache.pages)) return kNoRow;
         const int in_page = (g << a.cache.page_bits) + (pos & ((1 << a.cache.page_bits) - 1));
         const size_t row = static_cast<size_t>(static_cast<uint32_t>(page)) * static_cast<uint32_t>(a.cache.kv_heads << a.cache.page_bits) + in_page;
-        key = __ldg(a.cache.scale[0] + row);
-        value = __ldg(a.cache.scale[1] + row);
+        return __ldg(a.cache.scale[which] + row);
     }
     static constexpr uint32_t kNoRow = 256;
     // An 8-bit tile, widened: the chunks of 16 in turned order, so that eight rows' meet different banks.
@@ -668,9 +668,11 @@ struct Attention {
         }
     }
     static __device__ __forceinline__ int turned(int j, int r) { return D == 128 ? (j + r) & 7 : (j + (r >> 1)) & 3; }
-    // 8 bits: keys and values widened, values of nodes looked through.
-    __device__ void work8(int r) {
+    // 8 bits: keys (which = 0) or values (1) widened, values of nodes looked through.  Both rings have an even number of
+    // slots, so keys and values have slots of their own and neither's warps wait for the other's.
+    __device__ void work8(int r, int which) {
         Cursor at, staged;
+        at.slot = staged.slot = which;
         uint32_t copies = 0;
         bool ok = true;
         for (const Piece *pp; ok && (pp = next_piece()); done_piece()) {
@@ -679,37 +681,35 @@ struct Attention {
             const int32_t *table = a.cache.table + static_cast<size_t>(p.b) * a.cache.table_width;
             const int from = p.from, end = min(p.to, p.at + p.t1 * kTile), context = p.context, t1 = p.t1, g = p.g;
             int pos = p.at + p.t0 * kTile + r;
-            uint32_t next_key, next_value;
-            row_scales(row_page(table, pos, from, end), pos, g, next_key, next_value);
+            uint32_t next_byte = row_scale(row_page(table, pos, from, end), pos, g, which);
             int next_page = row_page(table, pos + kTile, from, end);
             for (int t = p.t0; ok && t < t1; ++t, pos += kTile) {
-                const uint32_t key = next_key, value = next_value;
-                row_scales(next_page, pos + kTile, g, next_key, next_value);
+                const uint32_t byte = next_byte, to = ring(at.slot);
+                next_byte = row_scale(next_page, pos + kTile, g, which);
                 next_page = row_page(table, pos + 2 * kTile, from, end);
-#pragma unroll 1
-                for (int w = 0; w < 2; ++w, at.step(a.ring)) {
-                    const uint32_t to = ring(at.slot), byte = w ? value : key;
-                    if (!(ok = hurry(&c->empty[at.slot], at.round ^ 1))) break;
-                    if (t < context) {
-                        if (!(ok = hurry(&c->staged[staged.slot], staged.round))) break;
-                        if (byte != kNoRow) {
-                            Widen<T> x;
-                            x.scale(byte);
-                            widen(stages + staged.slot * L::kStageBytes, to, r, x);
-                            if (kHalf && x.again) widen_again(to, r, x.again);
-                        } else {
-                            clear_rows(to, r, 0, 0);
-                        }
-                        __syncwarp();
-                        if (lane == 0) arrive(ptx::smem_addr(&c->free_[staged.slot]));
-                        staged.step(a.stages);
-                        fence_async();
-                    } else if (w) {
-                        if (!(ok = look_through(p, at.slot, to, r, copies))) break;
+                if (!(ok = hurry(&c->empty[at.slot], at.round ^ 1))) break;
+                if (t < context) {
+                    if (!(ok = hurry(&c->staged[staged.slot], staged.round))) break;
+                    if (byte != kNoRow) {
+                        Widen<T> x;
+                        x.scale(byte);
+                        widen(stages + staged.slot * L::kStageBytes, to, r, x);
+                        if (kHalf && x.again) widen_again(to, r, x.again);
+                    } else {
+                        clear_rows(to, r, 0, 0);
                     }
                     __syncwarp();
-                    if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
+                    if (lane == 0) arrive(ptx::smem_addr(&c->free_[staged.slot]));
+                    staged.step(a.stages);
+                    staged.step(a.stages);
+                    fence_async();
+                } else if (which) {
+                    if (!(ok = look_through(p, at.slot, to, r, copies))) break;
                 }
+                __syncwarp();
+                if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
+                at.step(a.ring);
+                at.step(a.ring);
             }
         }
     }
@@ -1068,9 +1068,9 @@ __global__ void __launch_bounds__(Layout<D, Q8>::kThreads, 1) attention_kernel(c
         x.softmax(warp >> 2, tid & 127);
     } else {
         if (warp < kFirst) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kWorkerRegs));
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kSingleRegs));
+        else if (L::kSingleRegs < L::kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kSingleRegs));
         if (warp < kFirst) {
-            if (Q8) x.work8(tid & 127);
+            if (Q8) x.work8(tid & 127, (warp - 8) >> 2);
             else x.work(tid & 127);
         } else if (warp == kFirst + 1 || warp == kFirst + 2) {
             if (lane == 0) x.multiply(warp - kFirst - 1);
