@@ -1097,9 +1097,10 @@ __device__ __forceinline__ int share_of(int x, int y, int z) {
 }
 
 // 32 rows of a block, a lane each, D / 8 columns a warp: the partial sums of the pieces that hold them, in the order
-// of their keys, and the result through shared memory, so that it is written in whole lines.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) attention_join_kernel(const __grid_constant__ AttentionArgs a) {
+// of their keys, and the result through shared memory, so that it is written in whole lines.  kAtOnce: pieces whose loads
+// are under way together.
+template <typename T, int D, int kAtOnce>
+__global__ void __launch_bounds__(256, kAtOnce == 1 ? 4 : 1) attention_join_kernel(const __grid_constant__ AttentionArgs a) {
     constexpr int E = D / 8;
     __shared__ uint32_t result[32][D / 2 + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1122,23 +1123,40 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const __grid_consta
     float m = -INFINITY, l = 0.0f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.0f;
-    const auto take = [&](const Part &p, int at) {
-        const float2 s = p.stats[at];
-        alignas(16) float x[E];
+    const auto load = [&](const Part &p, int at, float2 &stat, float (&x)[E]) {
+        stat = p.stats[at];
 #pragma unroll
         for (int e = 0; e < E; e += 4)
             *reinterpret_cast<float4 *>(x + e) = reinterpret_cast<const float4 *>(p.sums)[(warp * E + e) / 4 * p.rows + at];
+    };
+    const auto add = [&](const float2 &s, const float (&x)[E]) {
         const float top = fmaxf(m, s.x), was = m == -INFINITY ? 0.0f : ptx::ex2(m - top), now = s.x == -INFINITY ? 0.0f : ptx::ex2(s.x - top);
         l = l * was + s.y * now;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = o[e] * was + x[e] * now;
         m = top;
     };
-    const auto pieces = [&](int t0, int from, int to, int at) {  // of a block whose tiles begin at t0
-        for (int c = from; c <= to; ++c) {
-            const int lo = share_of(total, c, a.ctas);
-            if (lo == share_of(total, c + 1, a.ctas)) continue;  // a CTA without tiles
-            take(cut_part<D>(a, c, t0 >= lo), at);
+    const auto take = [&](const Part &p, int at) {
+        alignas(16) float x[E];
+        float2 stat;
+        load(p, at, stat, x);
+        add(stat, x);
+    };
+    // Of a block whose tiles begin at t0: kAtOnce pieces' loads under way together, and added in order.
+    const auto pieces = [&](int t0, int from, int to, int at) {
+        for (int c = from; c <= to; c += kAtOnce) {
+            alignas(16) float x[kAtOnce][E];
+            float2 stat[kAtOnce];
+            bool there[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int lo = share_of(total, c + k, a.ctas);
+                there[k] = c + k <= to && lo != share_of(total, c + k + 1, a.ctas);  // (not a CTA without tiles)
+                if (there[k]) load(cut_part<D>(a, c + k, t0 >= lo), at, stat[k], x[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                if (there[k]) add(stat[k], x[k]);
         }
     };
     if (a.shared_len) {  // the prefix comes first; the rows of a block may lie in two of its blocks

@@ -69,7 +69,11 @@ spec_status launch_attention(const AttentionArgs &a0, cudaStream_t stream) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(SPEC_ERR_CUDA, "attention launch: %s", cudaGetErrorString(e));
     const long long join = static_cast<long long>(a.B) * a.cache.kv_heads * a.blocks * ((a.block_rows + 31) / 32);
-    attention_join_kernel<T, D><<<static_cast<unsigned>(join), 256, 0, stream>>>(a);
+    // Few CTAs wait for each piece's loads: 4 pieces at once.  Many hide them behind one another, and then registers count:
+    // one at once, four CTAs an SM (3 contexts of 52105, 49 nodes x 4 heads of one key head, 21 CTAs: 68 us with one, 47 with
+    // four, 45 with eight; 64 nodes of 16 sequences of 8 key heads, 1024 CTAs: 73 and 77 with one and four).
+    if (join <= 2 * di.sms) attention_join_kernel<T, D, 4><<<static_cast<unsigned>(join), 256, 0, stream>>>(a);
+    else attention_join_kernel<T, D, 1><<<static_cast<unsigned>(join), 256, 0, stream>>>(a);
     e = cudaGetLastError();
     return e == cudaSuccess ? SPEC_OK : fail(SPEC_ERR_CUDA, "join launch: %s", cudaGetErrorString(e));
 }
