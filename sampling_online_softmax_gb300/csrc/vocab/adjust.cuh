@@ -6,7 +6,7 @@
 // Then, a few rows at a time, it streams the slice under the mask bits, 16 bytes a load, and computes the
 // listed tokens over what it streamed.  In text these are a tenth of the tokens here and there: computed
 // in the stream they would cost each warp that holds one the whole arithmetic (16 sequences of 64 rows of 32000
-// fp32: 156 us, against 77 us so).  The drafted tokens of a row's own path are found through a chain of
+// fp32: 156 us, against 76 us so).  The drafted tokens of a row's own path are found through a chain of
 // drafted tokens at each listed token.
 //
 // HBM is the floor: each logit read and written once, a bit of mask a logit.  A vector whose mask lets
@@ -46,7 +46,7 @@ struct AdjustArgs {
 
 // Where the parts of a CTA's shared memory begin, in words; those that a call has no use for are empty.
 struct AdjustShared {
-    int count, bias, mine, list, chain, before, sums, words;
+    int count, bias, list, chain, before, sums, words;
     bool narrow;  // counts of 16 bits
     __host__ __device__ explicit AdjustShared(const AdjustArgs &a) {
         const bool counts = a.repetition || a.frequency || a.presence, lists = counts || a.M, paths = counts && a.nodes && a.N > 1;
@@ -55,8 +55,7 @@ struct AdjustShared {
         bias = count + (counts ? a.slice / (narrow ? 2 : 1) : 0);
         chain = bias + (a.M ? a.slice / 2 : 0);
         list = chain + (paths ? a.slice / 2 : 0);  // (up to here all is zeroed)
-        mine = list + (lists ? a.slice / 2 : 0);
-        before = mine + (a.M + 1) / 2;
+        before = list + (lists ? a.slice / 2 : 0);
         sums = before + (paths ? (a.N + 1) / 2 : 0);
         words = sums + a.M;
     }
@@ -145,7 +144,8 @@ __global__ void __launch_bounds__(kAdjustThreads, kAdjustResident) adjust_kernel
     constexpr int EPV = VEC ? 16 / EB : 1;  // tokens of a vector
     constexpr int kBatch = 4, kFix = 2;     // vectors of a row, and listed tokens, of a thread under way at once
     extern __shared__ __align__(16) uint32_t smem[];
-    __shared__ int listed, biased;
+    __shared__ int listed;
+    __shared__ float slots[32];
     const int tid = threadIdx.x;
     const int s = blockIdx.x % a.slices;
     const int group = blockIdx.x / a.slices % a.groups;
@@ -165,7 +165,6 @@ __global__ void __launch_bounds__(kAdjustThreads, kAdjustResident) adjust_kernel
     const AdjustShared at(a);
     uint32_t *touched = smem, *count = smem + at.count;  // a bit a token; a count a token, of 16 or of 32 bits
     uint16_t *bias = reinterpret_cast<uint16_t *>(smem + at.bias);    // 1 + where a token's bias is among `sums`
-    uint16_t *mine = reinterpret_cast<uint16_t *>(smem + at.mine);    // slots of biases of the slice's tokens
     float *sums = reinterpret_cast<float *>(smem + at.sums);
     const int half = at.narrow ? 1 : 0;
     const uint32_t prompt_bit = at.narrow ? 0x8000u : 0x80000000u;
@@ -202,19 +201,20 @@ __global__ void __launch_bounds__(kAdjustThreads, kAdjustResident) adjust_kernel
                 }
             }
         }
-        if (paths && tid < 32)  // (one warp, node by node, so that a chain is never entered twice at once)
+        if (paths && tid < 32)  // one warp, 32 nodes at a time, in order: each node leads to the one before it of its token
             for (int m0 = 1; m0 < a.N; m0 += 32) {
                 const int m = m0 + tid, t = m < a.N ? nodes[m] : -1;
                 odd |= t < -1 || t >= a.V;
-                const bool mine = t >= t0 && t < t0 + len;
-                for (uint32_t left = __ballot_sync(0xffffffffu, mine); left; left &= left - 1) {
-                    if (tid == __ffs(left) - 1) {
-                        before[m] = chain[t - t0];
-                        chain[t - t0] = static_cast<uint16_t>(m);
-                        atomicOr(&touched[(t - t0) >> 5], 1u << ((t - t0) & 31));
-                    }
-                    __syncwarp();
+                const bool in = t >= t0 && t < t0 + len;
+                if (!__any_sync(0xffffffffu, in)) continue;
+                const uint32_t same = __match_any_sync(0xffffffffu, in ? t : -1), lower = same & ((1u << tid) - 1);
+                if (in) before[m] = lower ? static_cast<uint16_t>(m0 + 31 - __clz(lower)) : chain[t - t0];
+                __syncwarp();
+                if (in && same >> tid == 1) {  // the last of its token
+                    chain[t - t0] = static_cast<uint16_t>(m);
+                    atomicOr(&touched[(t - t0) >> 5], 1u << ((t - t0) & 31));
                 }
+                __syncwarp();
             }
         if (s == 0) {
             if (odd) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
@@ -222,34 +222,36 @@ __global__ void __launch_bounds__(kAdjustThreads, kAdjustResident) adjust_kernel
         }
     }
     if (a.M) {
-        // The slots that name a token of the slice, in order; the first that names one adds the later ones' values.
+        // One warp, 32 slots at a time: the first slot that names a token of the slice holds the sum, and the others' values are
+        // added in slot order.  (Each slot compared with all the others: 80 x 10 rows of
+        // 4797 bf16 with 89 biases 22 us, this 18.)
         const int32_t *ids = a.bias_ids + static_cast<size_t>(b) * a.M;
         const float *values = a.bias + static_cast<size_t>(b) * a.M;
         if (tid >= 32 && tid < 64) {
             const int lane = tid - 32;
-            int n = 0;
             for (int i0 = 0; i0 < a.M; i0 += 32) {
-                const int t = i0 + lane < a.M ? ids[i0 + lane] : -1;
+                const int i = i0 + lane, t = i < a.M ? ids[i] : -1;
                 if (s == 0 && (t < -1 || t >= a.V)) atomicOr(a.status, SPEC_DEV_BAD_TOKEN);
                 const bool in = t >= t0 && t < t0 + len;
-                const uint32_t all = __ballot_sync(0xffffffffu, in);
-                if (in) mine[n + __popc(all & ((1u << lane) - 1))] = static_cast<uint16_t>(i0 + lane);
-                n += __popc(all);
+                if (!__any_sync(0xffffffffu, in)) continue;
+                uint32_t same = __match_any_sync(0xffffffffu, in ? t : -1);
+                slots[lane] = in ? values[i] : 0.0f;
+                __syncwarp();
+                if (in && (same & ((1u << lane) - 1)) == 0) {
+                    int at_sum = bias[t - t0];
+                    if (at_sum == 0) {
+                        at_sum = i + 1;
+                        bias[t - t0] = static_cast<uint16_t>(at_sum);
+                        atomicOr(&touched[(t - t0) >> 5], 1u << ((t - t0) & 31));
+                        sums[i] = slots[lane];
+                        same &= same - 1;
+                    }
+                    float sum = sums[at_sum - 1];
+                    for (; same; same &= same - 1) sum += slots[__ffs(same) - 1];
+                    sums[at_sum - 1] = sum;
+                }
+                __syncwarp();
             }
-            if (lane == 0) biased = n;
-        }
-        __syncthreads();
-        for (int x = tid; x < biased; x += kAdjustThreads) {
-            const int t = ids[mine[x]];
-            bool first = true;
-            for (int y = 0; y < x && first; ++y) first = ids[mine[y]] != t;
-            if (!first) continue;
-            float sum = values[mine[x]];
-            for (int y = x + 1; y < biased; ++y)
-                if (ids[mine[y]] == t) sum += values[mine[y]];
-            sums[x] = sum;
-            bias[t - t0] = static_cast<uint16_t>(x + 1);
-            atomicOr(&touched[(t - t0) >> 5], 1u << ((t - t0) & 31));
         }
     }
     int n_listed = 0;
