@@ -56,7 +56,7 @@ spec_status launch_attention(const AttentionArgs &a0, cudaStream_t stream) {
     a.control = static_cast<int>((di.max_dyn - sizeof(Control)) / 1024 * 1024);
     share_out<D, Q8>(&a, a.control);
     const size_t smem = a.control + sizeof(Control);
-    static_assert(sizeof(Control) <= 3072, "two full halves of queries, four tiles and two 8-bit ones leave no more of 227 KB");
+    static_assert(sizeof(Control) <= 3 * 1024, "two full halves of queries, four tiles and two 8-bit ones leave no more of 227 KB");
     if (a.ring < 4 || (Q8 && a.stages < 2)) return fail(SPEC_ERR_UNSUPPORTED, "%zu bytes of shared memory a CTA do not do", di.max_dyn);
     const CUtensorMapDataType type = std::is_same<T, __half>::value ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int kv = a.cache.kv_heads;
