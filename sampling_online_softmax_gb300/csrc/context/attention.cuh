@@ -915,7 +915,7 @@ struct Attention {
     }
     __device__ void softmax(int s, int tid) {
         uint32_t scores_round = 0, sums_round = 0, joined_round = 0;
-        bool ok = true;
+        bool ok = true, after_two = false;  // the piece before had two products a tile
         const float scale = a.scale * kLog2e;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, at bit 16
         const uint32_t s_at = tmem + lanes + kScores + s * 128, o_at = tmem + lanes + kSums + s * 128;
@@ -924,14 +924,23 @@ struct Attention {
             const bool two = p->two;
             const int r = (tid < half_rows ? tid : kBlockRows) + (two ? s * half_rows : 0);  // this thread's row of the block
             const bool idle = (warp & 3) != 0 && __all_sync(0xffffffffu, r >= p->rows);  // the warp has none: it only counts
-            // The first warp arrives for those that are idle.  (A last block may have no rows for product 1.)
+            // The first warp arrives for those that are idle.  (A last block may have no rows for product 1.)  But behind a piece of
+            // two products, whose warps nothing else brings together, each arrives for itself at a product's first tile: a product must
+            // not write over sums that a warp, idle now, still reads, nor leave it behind by more than a phase of `sums`.
             const bool has_row = r < p->rows;
             const int live = max(1, (min(half_rows, p->rows - (two ? s * half_rows : 0)) + 31) / 32);
-            const uint32_t arrivals = (warp & 3) == 0 ? 5 - live : 1;
+            const uint32_t arrivals = (warp & 3) == 0 ? 5 - live : 1, first_arrivals = after_two ? 1 : arrivals;
             const int t0 = p->t0, t1 = p->t1, plain0 = p->plain0, plain1 = p->plain1, n = row_id(a, *p, min(r, p->rows - 1)).n;
             float m = -INFINITY, l = 0.0f;
             bool first = true;
             const int turn = p->turn ^ s;
+            const bool has_sums = two || t0 + turn < t1;  // (a product may have no tile of a piece)
+            if (idle && after_two && has_sums) {
+                fence_before();
+                __syncwarp();
+                if (lane < 2) arrive(ptx::smem_addr(&c->weights[s][lane]));
+            }
+            after_two = two;
             for (int t = idle ? t1 : t0 + (two ? 0 : turn); t < t1; t += two ? 1 : 2) {
                 const bool masked = t < plain0 || t >= plain1;
                 uint32_t w[4] = {};
@@ -941,12 +950,12 @@ struct Attention {
                 if (!(ok = hurry(&c->scores[s], scores_round))) break;
                 scores_round ^= 1;
                 fence_after();
-                if (masked) tile_weights<true>(s, arrivals, has_row, w, s_at, o_at, scale, first, m, l);
-                else tile_weights<false>(s, arrivals, has_row, w, s_at, o_at, scale, first, m, l);
+                if (masked) tile_weights<true>(s, first ? first_arrivals : arrivals, has_row, w, s_at, o_at, scale, first, m, l);
+                else tile_weights<false>(s, first ? first_arrivals : arrivals, has_row, w, s_at, o_at, scale, first, m, l);
                 first = false;
             }
             if (!ok) break;
-            if (two || t0 + turn < t1) {  // the product has sums
+            if (has_sums) {
                 if (!(ok = idle ? wait(&c->sums[s], sums_round) : hurry(&c->sums[s], sums_round))) break;
                 sums_round ^= 1;
                 fence_after();
