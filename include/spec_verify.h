@@ -509,8 +509,8 @@ typedef struct spec_cache {
  * Writes keys and values of a batch into the cache: what a prompt, a step, or the
  * accepted path of a verified draft adds to each sequence's context.
  *   k, v     [B, N, kv_heads, head_dim] of `dtype` (SPEC_BF16 or SPEC_F16); strides (host, 4
- *            entries: k's batch and token strides in elements, then v's; multiples of 8) or
- *            NULL for contiguous; 16-byte aligned.
+ *            entries: k's batch and token strides in elements, then v's; multiples of 8, an axis of one
+ *            entry's does not matter) or NULL for contiguous; 16-byte aligned.
  *   select   [B, S] int32: row i of sequence b is token select[b, i] (spec_verify_tree's
  *            path_nodes with S = max_depth + 1); a negative entry writes nothing.  NULL: S = N, row i is token i.
  *   start    [B] int32: row i goes to position start[b] + i; a sequence with a negative start is left out.
@@ -549,8 +549,9 @@ SPEC_API spec_status spec_cache_read(const spec_cache *cache, int B, int S, cons
  *   q [B, N, heads, head_dim], k, v [B, N, kv_heads, head_dim] of `dtype` (SPEC_BF16 or
  *          SPEC_F16): the nodes' own, not in the cache yet (spec_cache_append adds the accepted
  *          ones); strides (host, 6 entries: q's batch and token strides in elements, k's, v's;
- *          multiples of 8, above 0 and below 2^38) or NULL for contiguous; 16-byte aligned.  With
- *          shared_len q's batch stride is N times its token stride, or B = 1 (else SPEC_ERR_UNSUPPORTED).
+ *          multiples of 8, above 0 and below 2^38, an axis of one entry's does not matter) or NULL for contiguous;
+ *          16-byte aligned.  With shared_len q's batch stride is N times its token stride, or B or N is 1
+ *          (else SPEC_ERR_UNSUPPORTED).
  *   cache  of `dtype` or SPEC_E4M3.  Positions may differ in their key heads' scales.
  *   context_lens [B] int32; a sequence with a negative length is left out, its rows of out
  *          and lse as they were.

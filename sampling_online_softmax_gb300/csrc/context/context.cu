@@ -52,11 +52,14 @@ spec_status cache_args(CacheView *v, const spec_cache *c, spec_dtype dtype, int 
     return SPEC_OK;
 }
 
-// Strides in elements of `n` tensors (batch, token), contiguous where `given` is null.
-spec_status strides_of(long long *to, const long long *given, int n, long long N, const long long *token) {
+// Strides in elements of `n` tensors (batch, token), contiguous where `given` is null.  An axis of one entry takes the
+// other's: its own says nothing (one token of each sequence is then evenly spaced, wherever the sequences lie).
+spec_status strides_of(long long *to, const long long *given, int n, int B, long long N, const long long *token) {
     for (int i = 0; i < n; ++i) {
         to[2 * i] = given ? given[2 * i] : N * token[i];
         to[2 * i + 1] = given ? given[2 * i + 1] : token[i];
+        if (N == 1) to[2 * i + 1] = B == 1 ? token[i] : to[2 * i];
+        if (B == 1) to[2 * i] = to[2 * i + 1];
         if (to[2 * i] % 8 || to[2 * i + 1] % 8 || to[2 * i] < 0 || to[2 * i + 1] < 0)
             return fail(SPEC_ERR_INVALID_ARG, "strides must be multiples of 8 elements, and not negative");
     }
@@ -142,7 +145,7 @@ extern "C" spec_status spec_cache_append(const void *k, const void *v, spec_dtyp
         return fail(SPEC_ERR_INVALID_ARG, "a pointer is misaligned");
     const long long token = static_cast<long long>(cache->kv_heads) * cache->head_dim, tokens[2] = {token, token};
     long long to[4];
-    st = strides_of(to, strides, 2, N, tokens);
+    st = strides_of(to, strides, 2, B, N, tokens);
     if (st != SPEC_OK) return st;
     for (int i = 0; i < 2; ++i) a.batch_stride[i] = to[2 * i], a.token_stride[i] = to[2 * i + 1];
     a.src[0] = static_cast<const unsigned char *>(k);
@@ -215,7 +218,7 @@ extern "C" spec_status spec_tree_attention(const void *q, const void *k, const v
     if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
         return fail(SPEC_ERR_WORKSPACE, "workspace of %zu bytes, 16-byte aligned, needed (got %zu)", need, workspace_bytes);
     const long long tokens[3] = {static_cast<long long>(heads) * D, static_cast<long long>(kv) * D, static_cast<long long>(kv) * D};
-    st = strides_of(a.stride, strides, 3, N, tokens);
+    st = strides_of(a.stride, strides, 3, B, N, tokens);
     if (st != SPEC_OK) return st;
     for (const long long x : a.stride)
         if (x == 0 || x >= 1ll << 38) return fail(SPEC_ERR_INVALID_ARG, "strides must be above 0 and below 2^38 elements");

@@ -99,6 +99,21 @@ def test_tree_attention_limits(lib, kw, expect):
     assert _attend(lib, **kw) == expect and lib.spec_last_error().decode()
 
 
+LAST = dict(FAR, heads=1024, out=FAKE + (1 << 30), cache=dict(kv_heads=1024, table_width=1 << 26))  # (more tiles than a call takes: the last check)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(N=1, shared=16, strides=[3 << 16, 1 << 16] + [3 << 16, 1 << 16] * 2),  # slices of a fused projection, as the binding passes them
+    dict(N=1, shared=16, strides=[3 << 16, 3] + [3 << 16, 0] * 2), dict(N=1, shared=0, strides=[3 << 16, 1 << 50] * 3),
+    dict(B=1, N=2, shared=16, strides=[0, 1 << 16] + [7, 1 << 16] * 2), dict(B=1, N=2, shared=16, strides=[1 << 50, 1 << 20] * 3),
+    dict(B=1, N=1, shared=16, strides=[3, 5] * 3), dict(N=2, shared=16, strides=[2 << 16, 1 << 16] * 3)])
+def test_an_axis_of_one_entry_has_any_stride(lib, kw):
+    assert _attend(lib, **LAST, **kw) == UNS and "too much work" in lib.spec_last_error().decode()
+    if kw.get("B") != 1 and kw["N"] == 1:  # the other axis' stride still counts
+        for bad in (4, -8, 0, 1 << 38):
+            assert _attend(lib, **LAST, **{**kw, "strides": [bad, 1 << 16] * 3}) == INV
+
+
 def test_cache_call_limits(lib):
     assert _append(lib, B=1 << 20, N=64, S=64) == UNS and _read(lib, B=1 << 20, S=64) == UNS
     assert _append(lib, cache=dict(table_width=(1 << 26) + 1)) == UNS and _read(lib, cache=dict(table_width=(1 << 26) + 1)) == UNS
