@@ -512,7 +512,8 @@ typedef struct spec_cache {
  *            entries: k's batch and token strides in elements, then v's; multiples of 8, an axis of one
  *            entry's does not matter) or NULL for contiguous; 16-byte aligned.
  *   select   [B, S] int32: row i of sequence b is token select[b, i] (spec_verify_tree's
- *            path_nodes with S = max_depth + 1); a negative entry writes nothing.  NULL: S = N, row i is token i.
+ *            path_nodes with S = max_depth + 1); a negative entry writes nothing, and one that start or count
+ *            leaves out is not looked at.  NULL: S = N, row i is token i.
  *   start    [B] int32: row i goes to position start[b] + i; a sequence with a negative start is left out.
  *   count    [B] int32: only rows i < count[b] (above S: S, below 0: none); NULL: all S.
  *            spec_verify_linear's num_emitted, when u_bonus was given, counts the accepted rows (the root's among them).

@@ -37,10 +37,14 @@ struct CacheRowsArgs {
     uint32_t *status;
 };
 
-// Where row (b, i) lies: page * page_size + slot, or -1 where there is nothing to do.
-__device__ __forceinline__ long long cache_place(const CacheRowsArgs &a, int b, int i) {
+// Where row (b, i), token `from` of `tokens`, lies: page * page_size + slot, or -1 where there is nothing to do.
+__device__ __forceinline__ long long cache_place(const CacheRowsArgs &a, int b, int i, int from, int tokens) {
     const int start = __ldg(a.start + b);
-    if (start < 0 || (a.count && i >= __ldg(a.count + b))) return -1;
+    if (start < 0 || from < 0 || (a.count && i >= __ldg(a.count + b))) return -1;
+    if (from >= tokens) {
+        atomicOr(a.status, SPEC_DEV_BAD_LENGTH);
+        return -1;
+    }
     const long long pos = static_cast<long long>(start) + i;
     const int column = static_cast<int>(pos >> a.cache.page_bits);
     if (column >= a.cache.table_width) {
@@ -89,8 +93,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_append_kernel(const Cache
             batch[k] = node[k] = 0;
             if (my.sub >= my.tokens || token >= all) continue;
             const int b = token / a.S, i = token - b * a.S, from = a.select ? __ldg(a.select + token) : i;
-            if (from >= a.N) atomicOr(a.status, SPEC_DEV_BAD_LENGTH);
-            else if (from >= 0) place[k] = cache_place(a, b, i);
+            place[k] = cache_place(a, b, i, from, a.N);
             batch[k] = b;
             node[k] = from;
         }
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_read_kernel(const CacheRo
 #pragma unroll
         for (int k = 0; k < kCacheTokens; ++k) {
             const int token = t0 + k * my.tokens + my.sub;
-            place[k] = my.sub < my.tokens && token < all ? cache_place(a, token / a.S, token % a.S) : -1;
+            place[k] = my.sub < my.tokens && token < all ? cache_place(a, token / a.S, token % a.S, 0, 1) : -1;
         }
         for (int round = 0; round < my.rounds; ++round) {
             const int item = my.item(round), g = item / kLanes, part = item % kLanes;
