@@ -95,3 +95,37 @@ def test_unequal_blocks(dtype, q8, B, N, group, kv, D):
 ])
 def test_fewer_rows_behind_a_prefix(q8, B, N, group, kv, D, shared):
     same_every_time(att.problem(B, N, group * kv, kv, D, 16, [shared + (29 * b) % 210 for b in range(B)], BF, q8, seed=B, shared=shared))
+
+
+@pytest.mark.parametrize("seed", range(60))
+def test_random_calls(seed):
+    """Calls over the range of types, head layouts, lengths, prefixes, masks and strides; some with sequences left out, some
+    with a node that is not finite."""
+    g = torch.Generator().manual_seed(1000 + seed)
+    pick = lambda *x: x[int(torch.randint(0, len(x), (1,), generator=g))]  # noqa: E731
+    between = lambda a, b: int(torch.randint(a, b + 1, (1,), generator=g))  # noqa: E731
+    along = lambda a, b: int(a * (b / a) ** float(torch.rand(1, generator=g)))  # noqa: E731
+    dtype, q8, D, page = pick(BF, F16), pick(False, True), pick(64, 128), pick(16, 32, 64, 128, 256)
+    group, kv, N = pick(1, 2, 3, 4, 5, 7, 8, 12, 16, 24, 31, 64, 65, 100, 128), pick(1, 2, 3, 4, 5), along(1, 300)
+    shared, top = pick(0, 0, between(1, 700)), along(1, 2500)
+    B = max(1, min(along(1, 150), 60000 // (N * group * kv), 60000 // ((shared + top) * kv)))
+    lens = [shared + between(0, top) if b == 0 or pick(True, True, True, False) else pick(shared, -1) for b in range(B)]
+    seen = pick(None, torch.rand((N, N), generator=g) < 0.4)
+    s = att.problem(B, N, group * kv, kv, D, page, lens, dtype, q8, seed=seed, shared=shared, chain=pick(False, True), seen=seen)
+    if pick(False, True):  # slices of a fused projection's tokens
+        wide = torch.zeros((B, N, (group + 2) * kv, D), dtype=dtype, device="cuda")
+        cuts = dict(q=slice(0, group * kv), k=slice(group * kv, (group + 1) * kv), v=slice((group + 1) * kv, (group + 2) * kv))
+        for n, cut in cuts.items():
+            wide[:, :, cut] = s[n]
+            s[n] = wide[:, :, cut]
+    r = same_every_time(s, 2)
+    b, m = between(0, B - 1), between(0, N - 1)
+    if lens[b] < 0:
+        return
+    t = dict(s, v=s["v"].clone())
+    t["v"][b, m, kv - 1, 5] = float("nan")
+    got, hit = att.call(t)["out"], s["seen"][:, m].cuda()
+    live = torch.tensor([x >= 0 for x in lens], device="cuda").view(B, 1, 1, 1).expand_as(got).clone()
+    assert torch.isnan(got[b, hit, -group:, 5]).all()
+    live[b, hit, -group:, 5] = False
+    assert torch.equal(got[live], r["out"][live])
