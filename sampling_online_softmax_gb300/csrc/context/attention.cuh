@@ -320,6 +320,12 @@ struct Attention {
     __device__ __forceinline__ uint32_t ring(int slot) const { return tiles + slot * L::kTileBytes; }
     __device__ __forceinline__ uint32_t query_half(int h) const { return queries + h * (D / 64) * a.q_sub; }
 
+    // Test builds only: whether this CTA leaves out a worker's arrivals (0), the first softmax warp's (1), the list's (2).
+#ifdef SPEC_TEST_HOOKS
+    __device__ __forceinline__ bool withheld(int what) const { return a.withhold == static_cast<int>(blockIdx.x) * 4 + what; }
+#else
+    static __device__ __forceinline__ constexpr bool withheld(int) { return false; }
+#endif
     // ---- pieces: one warp walks the list; the others take them in turn, and say when they are done with one
     __device__ __forceinline__ const Piece *piece() const { return c->pieces[piece_at].last ? nullptr : &c->pieces[piece_at]; }
     __device__ __forceinline__ const Piece *next_piece() { return wait(&c->piece_there[piece_at], piece_round) ? piece() : nullptr; }
@@ -340,7 +346,7 @@ struct Attention {
         if (!wait(&c->piece_done[piece_at], piece_round ^ 1)) return false;
         if (lane == 0) {
             c->pieces[piece_at] = p;
-            arrive(ptx::smem_addr(&c->piece_there[piece_at]));
+            if (!withheld(2)) arrive(ptx::smem_addr(&c->piece_there[piece_at]));
         }
         __syncwarp();
         if (++piece_at == kPieces) piece_at = 0, piece_round ^= 1;
@@ -707,7 +713,7 @@ struct Attention {
                     if (!(ok = look_through(p, at.slot, to, r, copies))) break;
                 }
                 __syncwarp();
-                if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
+                if (lane == 0 && !(warp == 8 && withheld(0))) arrive(ptx::smem_addr(&c->full[at.slot]));
                 at.step(a.ring);
                 at.step(a.ring);
             }
@@ -740,7 +746,7 @@ struct Attention {
                         fence_async();
                     }
                     __syncwarp();
-                    if (lane == 0) arrive(ptx::smem_addr(&c->full[at.slot]));
+                    if (lane == 0 && !(warp == 8 && withheld(0))) arrive(ptx::smem_addr(&c->full[at.slot]));
                 }
         }
     }
@@ -804,7 +810,7 @@ struct Attention {
         wait_stores();
         fence_before();
         __syncwarp();
-        if (lane == 0) arrive(ptx::smem_addr(&c->weights[s][h]), arrivals);
+        if (lane == 0 && !(warp == 0 && withheld(1))) arrive(ptx::smem_addr(&c->weights[s][h]), arrivals);
     }
     // A tile's scores into weights, whose halves the products may take one after the other: the row's maximum, then the
     // weights, 32 columns at a time, in loops that read tensor memory twice.  Code counts here, since the kinds of warps share

@@ -46,6 +46,9 @@ struct AttentionArgs {
     float2 *cut_stats; // ... their rows' (maximum in units of log 2, sum)
     float *row_sums;   // [2][kv_heads][blocks' rows, D columns a block], with a prefix: whole blocks, the sequences' own and the prefix's
     float2 *row_stats;
+#ifdef SPEC_TEST_HOOKS
+    int withhold;  // 4 * CTA + what it leaves out, so that a wait runs out (below 0: nothing)
+#endif
 };
 
 // The driver's encoder of tensor maps (null where the driver has none).

@@ -7,6 +7,11 @@
 #include "attention.cuh"
 
 namespace spec {
+
+#ifdef SPEC_TEST_HOOKS
+int test_withhold_unit();  // test builds only
+#endif
+
 namespace context {
 
 inline spec_status encode(CUtensorMap *map, CUtensorMapDataType type, int rank, const void *base, const cuuint64_t *dims, const cuuint64_t *strides,
@@ -52,6 +57,9 @@ spec_status launch_attention(const AttentionArgs &a0, cudaStream_t stream) {
     if (st != SPEC_OK) return st;
     AttentionArgs a = a0;
     a.ctas = std::min(di.sms, kMaxCtas);
+#ifdef SPEC_TEST_HOOKS
+    a.withhold = test_withhold_unit();
+#endif
     // All the shared memory there is, so that one CTA is on an SM: each takes all of its tensor memory.
     a.control = static_cast<int>((di.max_dyn - sizeof(Control)) / 1024 * 1024);
     share_out<D, Q8>(&a, a.control);

@@ -133,7 +133,11 @@ __device__ __forceinline__ void arrive(uint32_t bar, uint32_t n = 1) {
 // What generic stores wrote to shared memory is there for the tensor cores and TMA.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-constexpr int kWaitTries = 1 << 20;  // each suspends the thread for a while: far beyond any wait that ends
+#ifdef SPEC_TEST_HOOKS
+constexpr int kWaitTries = SPEC_SPIN_LIMIT;  // test builds: 25 ms
+#else
+constexpr int kWaitTries = 1 << 20;  // each suspends the thread for 1.5 us: 1.6 s, far beyond any wait that ends
+#endif
 
 // (mbar_try_wait takes no hint of a time to suspend for: with one of a microsecond the thread slept past the phase's end.)
 
