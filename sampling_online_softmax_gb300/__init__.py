@@ -68,7 +68,6 @@ MAX_ROW_BYTES = 1 << 20  # SPEC_MAX_ROW_BYTES
 MAX_TOP = 1024           # SPEC_MAX_TOP
 MAX_NODES = 1024         # SPEC_MAX_NODES
 MAX_BIASES = 1024        # SPEC_MAX_BIASES
-PAGE_SIZES = (16, 32, 64, 128, 256)
 
 
 class SpecError(RuntimeError):
