@@ -474,7 +474,7 @@ SPEC_API spec_status spec_distill_backward(const void *student_logits, spec_dtyp
  *   dev_status  SPEC_DEV_BAD_TOKEN, SPEC_DEV_BAD_LENGTH (taken as the nearest length
  *          in [0, L], the prompt's at most total_len), SPEC_DEV_BAD_PARAM.
  * 1 <= N <= SPEC_MAX_NODES, 0 <= M <= SPEC_MAX_BIASES, 0 <= L < 2^24.  No workspace; one
- * launch; the same result every time.
+ * launch; the same result every time.  For inference: there is no call for its gradient.
  */
 SPEC_API spec_status spec_adjust_logits(const void *logits, spec_dtype dtype, int B, int N, int V, const int32_t *tokens, int L,
                                         const int32_t *prompt_len, const int32_t *total_len, const int32_t *node_tokens,
@@ -518,7 +518,8 @@ typedef struct spec_cache {
  *   count    [B] int32: only rows i < count[b] (above S: S, below 0: none); NULL: all S.
  *            spec_verify_linear's num_emitted, when u_bonus was given, counts the accepted rows (the root's among them).
  * No length is advanced: the layers of a model call this with the same start.
- * Two rows that name one slot leave either's value; k and v must not overlap the cache.  dev_status: SPEC_DEV_BAD_LENGTH (a
+ * Two rows that name one slot leave it unspecified, unless they are the same row (in 8 bits it may hold one's values and the
+ * other's power of two): a page that sequences share is not appended to.  k and v must not overlap the cache.  dev_status: SPEC_DEV_BAD_LENGTH (a
  * position behind the table, or an entry of select not below N), SPEC_DEV_BAD_PAGE; such a row
  * is not written.  B * S <= INT_MAX / 64; positions below 2^30; kv_heads <= 1024.  No workspace; one launch.
  */
@@ -558,19 +559,20 @@ SPEC_API spec_status spec_cache_read(const spec_cache *cache, int B, int S, cons
  *          and lse as they were.
  *   shared_len  the first shared_len positions hold the same keys and values in every
  *          sequence (a common prompt): they are read through sequence 0's page table, once for
- *          the whole batch.  0: nothing is shared.  Every context_lens[b] >= 0 is then at least
+ *          the whole batch, also where sequence 0 is left out.  0: nothing is shared.  Every context_lens[b] >= 0 is then at least
  *          shared_len (SPEC_DEV_BAD_LENGTH where it is not, and that sequence's rows are unspecified).
  *   mask   [N, ceil(N/32)] as spec_tree_mask gives it; NULL: a chain, nodes 0 .. n.
  *   scale  finite, > 0.
  *   out    [B, N, heads, head_dim] of `dtype`, contiguous, 16-byte aligned; overlaps nothing that is read
  *          (SPEC_ERR_INVALID_ARG for q, k and v).
  *   lse    [B, N, heads] fp32 or NULL: log sum_j exp(s_j).
- *   dev_status  SPEC_DEV_BAD_LENGTH, SPEC_DEV_BAD_PAGE: that sequence's rows are unspecified;
- *          SPEC_DEV_TIMEOUT.
- *   workspace  spec_workspace_bytes_attention() bytes, 16-byte aligned; its content before a
- *          call does not matter.
+ *   dev_status  SPEC_DEV_BAD_LENGTH, SPEC_DEV_BAD_PAGE: that sequence's rows are unspecified (a bad page
+ *          of the shared positions: all rows); SPEC_DEV_TIMEOUT.
+ *   workspace  spec_workspace_bytes_attention() bytes (43 MB with head_dim 128, 22 MB with 64, and with shared_len 8 bytes more
+ *          for each value of out), 16-byte aligned; its content before a call does not matter.
  * Scores, sums and the weighted sums are fp32; exp(s_j - m), the weight of v_j in the matrix
- * product, is rounded to `dtype` (2^-9 of itself in bf16, with errors that the sum averages).
+ * product, is rounded to `dtype` (off by up to 2^-8 of itself in bf16, 2^-11 in fp16, errors that the sum averages).
+ * For inference: there is no call for its gradient.
  * 1 <= N <= SPEC_MAX_NODES; heads a multiple of kv_heads, at most 128 times it.  Positions below 2^30, and at most
  * INT_MAX tiles of 128 keys (by the table's width).  Two launches.  The same result every time.
  */

@@ -721,7 +721,7 @@ def spec_adjust_logits(logits, *, tokens=None, prompt_len=None, total_len=None, 
     spec_tree_mask gives them (None: a chain).  A row counts the history and its own path: repetition (divides or
     multiplies), frequency (a count) and presence [B] float32.  bias_ids, bias [B, M] add to tokens; allowed
     [B, N, ceil(V/32)] int32 holds a bit a token, 0 for -inf.  out=dict(logits=logits) works in place (autograd then
-    refuses a graph that saved the logits)."""
+    refuses a graph that saved the logits).  No autograd graph is recorded."""
     lib = load_library()
     if not (logits.is_cuda and logits.is_contiguous()):
         _cuda(logits, "logits")
@@ -839,7 +839,8 @@ def spec_cache_append(k, v, k_cache, v_cache, page_table, start, *, count=None, 
     [pages, kv_heads, page_size, head_dim] of their type, or of float8_e4m3fn with k_scale, v_scale
     [pages, kv_heads, page_size] uint8 (a power of two a row): row i of sequence b goes to position start[b] + i, which
     page_table [B, width] int32 places.  select [B, S] int32 picks the rows (spec_verify_tree's path_nodes; -1: none);
-    count [B] int32 limits them; a negative start leaves a sequence out.  Returns dict(status)."""
+    count [B] int32 limits them; a negative start leaves a sequence out.  Two different rows must not go to one slot.
+    Returns dict(status)."""
     lib = load_library()
     shape, dtype, dev, i = _new_tokens(k, "k")
     B, N, heads, dim = shape
@@ -911,7 +912,7 @@ def spec_tree_attention(q, k, v, k_cache, v_cache, page_table, context_lens, *, 
     mask [N, ceil(N/32)] int32 as spec_tree_mask gives it (None: a chain, nodes 0 .. n; N = 1 is plain decoding).  The
     first shared_len positions are the same in every sequence and are read once, through page_table[0].  scale
     is 1 / sqrt(head_dim) where it is None.  Returns dict(out [B, N, heads, head_dim], status), with lse=True also
-    lse [B, N, heads] float32, the log of the softmax's sum."""
+    lse [B, N, heads] float32, the log of the softmax's sum.  No autograd graph is recorded."""
     lib = load_library()
     qs, dtype, dev, i = _new_tokens(q, "q")
     B, N, heads, dim = qs

@@ -20,14 +20,17 @@
 //
 // What bounds it, by rows a block and the cache's type (128-wide heads, one CTA an SM):
 //   long contexts, few rows   HBM: 3 contexts of up to 131072, 9 nodes x 4 heads: 190 us, 6.6 TB/s, 97 % of a copy
-//   two full halves           the chain scores -> weights -> sums of two products, about 3 us a tile, of which the tensor cores
-//                             are at work a third: 48 sequences of 9 nodes behind 16384 shared tokens 158 us
-//                             (0.75 PFLOP/s), 64 nodes of 16 sequences over 4096 74 us, 15 of them the second kernel's
+//   two full halves           the chain scores -> weights -> sums of two products, about 3 us a tile, of which its four products are
+//                             1.35 us and the exponentials of both halves 0.5 (32 a clock and SM, measured); a row's weights
+//                             come from eight loads of tensor memory, each waited for before what is computed from it: 48 sequences
+//                             of 9 nodes behind 16384 shared tokens 158 us (0.75 PFLOP/s; over an 8-bit cache 194), 64 nodes of 16
+//                             sequences over 4096 74 us, 15 of them the second kernel's (8 bits: 82)
 //   8-bit tiles               widening, 1.6 thousand clocks a tile of two times four warps, and shared memory, which it and the
-//                             products share: 64 sequences of 5 nodes over 8192 233 us, 3.1 TB/s (16 bits: 223 us, 6.5 TB/s)
+//                             products share: 64 sequences of 5 nodes over 8192 234 us, 3.1 TB/s (16 bits: 222 us, 6.5 TB/s)
 //   small calls               launches and the chain from the list to the first sums: one token over 700 16 us
 // With four warps for keys and values of 8 bits, in turn, the last took 280 us; with two halves of rows the eight are slower (64
-// query heads, 32 nodes: 436 us against 421), since the softmax has fewer registers and shares more, and stay all the same.
+// query heads, 32 nodes: 436 us against 421), since the softmax has fewer registers and shares more.  All 8-bit calls take eight: a form
+// with four for two halves alone would be four more kernels, for those 3 %.
 // The softmaxes in turn, and the second kernel launched early, were each measured slower.
 #pragma once
 

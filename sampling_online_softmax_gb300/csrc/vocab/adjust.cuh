@@ -1,8 +1,9 @@
 // adjust.cuh -- penalties for repeated tokens, biases and grammar masks on rows of logits.
 //
 // A CTA takes one slice of the vocabulary of one sequence and some of its rows.  It counts the
-// history once into a table of the slice in shared memory (a word a token: bit 31 says that the prompt
-// holds it, the rest count the generated occurrences) and lists the tokens that anything may change.
+// history once into a table of the slice in shared memory (16 bits a token where history and nodes are fewer than
+// 2^15, else 32: the top bit says that the prompt holds it, the rest count the generated occurrences) and lists
+// the tokens that anything may change.
 // Then, a few rows at a time, it streams the slice under the mask bits, 16 bytes a load, and computes the
 // listed tokens over what it streamed.  In text these are a tenth of the tokens here and there: computed
 // in the stream they would cost each warp that holds one the whole arithmetic (16 sequences of 64 rows of 32000
@@ -25,7 +26,7 @@
 namespace spec {
 namespace vocab {
 
-constexpr int kAdjustThreads = 256, kAdjustResident = 4;  // threads of a CTA, CTAs of an SM
+constexpr int kAdjustThreads = 256, kAdjustResident = 4;  // threads of a CTA; CTAs of an SM, by registers (with every argument and 8192 tokens, 66 KB, three)
 constexpr int kMinSlice = 1024, kMaxSlice = 8192;  // tokens of a CTA
 constexpr int kAdjustRows = 4;                     // rows streamed before their listed tokens are computed
 
